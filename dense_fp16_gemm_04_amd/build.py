@@ -1,6 +1,7 @@
 """Build the gfx950 libraries in this package directory: ``libgemm_nt_f16.so``
-(the GEMM kernels and their C ABI) and ``libpower_probe.so`` (the power
-probe, a measuring instrument that the GEMM path never loads).
+(the GEMM kernels and their C ABI), one library for each operator beside it
+(``OPERATORS``) and ``libpower_probe.so`` (the power probe, a measuring
+instrument that no product path loads).
 
 One hipcc invocation per library compiles it ahead of time for gfx950 only.  ``-Xclang -target-feature -Xclang -packed-fp32-ops`` keeps the
 compiler from emitting packed fp32 arithmetic (v_pk_*_f32); the host pass
@@ -22,6 +23,7 @@ import re
 import shutil
 import subprocess
 import sys
+from concurrent.futures import ThreadPoolExecutor
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -32,7 +34,15 @@ RESOURCES = os.path.join(HERE, "libgemm_nt_f16.resources.json")
 PROBE_SRC = os.path.join(HERE, "csrc", "power_probe.hip")
 PROBE_LIB = os.path.join(HERE, "libpower_probe.so")
 PROBE_RESOURCES = os.path.join(HERE, "libpower_probe.resources.json")
+# csrc/<name>.hip -> lib<name>.so, with the C ABI of include/<name>.h
+OPERATORS = ("gated_nt", "orthogonalize_ns", "gemv_w4")
 ARCH = "gfx950"
+
+
+def operator_paths(name: str):
+    """(source, library, resource record) of an operator's library."""
+    return (os.path.join(HERE, "csrc", name + ".hip"), os.path.join(HERE, "lib%s.so" % name),
+            os.path.join(HERE, "lib%s.resources.json" % name))
 
 
 def hipcc() -> str:
@@ -121,10 +131,13 @@ def compile_library(src: str, lib: str, resources: str, verbose: bool = False, e
 
 
 def build(verbose: bool = False, extra=()) -> str:
-    """Both libraries (`extra` flags for the GEMM library only); returns the
-    GEMM library's path."""
-    compile_library(SRC, LIB, RESOURCES, verbose, extra)
-    compile_library(PROBE_SRC, PROBE_LIB, PROBE_RESOURCES, verbose)
+    """Every library, compiled side by side (`extra` flags for the GEMM
+    library only); returns the GEMM library's path."""
+    jobs = [(SRC, LIB, RESOURCES, verbose, extra), (PROBE_SRC, PROBE_LIB, PROBE_RESOURCES, verbose)]
+    jobs += [(*operator_paths(name), verbose) for name in OPERATORS]
+    with ThreadPoolExecutor(max_workers=len(jobs)) as pool:
+        for done in [pool.submit(compile_library, *job) for job in jobs]:
+            done.result()
     return LIB
 
 

@@ -1,0 +1,449 @@
+// The gated linear layer H = act(X Wg^T) * (X Wu^T) and its backward pass for
+// gfx950: include/gated_nt.h.
+//
+// Forward: one NT product whose B tile is half rows of Wg and half rows of
+// Wu, arranged so that each wave's sub-tile holds, for the same columns of H,
+// g in its first half and u in its second; the epilogue then combines them
+// lane by lane and g and u never leave the registers.
+//
+// Backward: dG = dH * P and dU = dH * Q element by element from the saved P =
+// u act'(g) and Q = act(g), written row-major ([dG dU], T x 2F) and
+// transposed (2F x T); then dX = [dG dU] [Wg; Wu] is one product with 2F
+// terms to a sum, and dWg, dWu are two of one shape over T, all in NT form on
+// transposed copies of X and of the weights.
+#include "gated_nt.h"
+
+#include <algorithm>
+
+#include "abi.h"
+#include "nt_core.h"
+#include "relayout.h"
+
+namespace {
+
+using namespace nt;
+
+// act(g) = g * sigmoid(g * (c0 + c1 * g^2)): silu has c0 = 1, c1 = 0; the
+// tanh form of gelu has 0.5 g (1 + tanh y) = g sigmoid(2 y).
+struct Activation {
+    float c0, c1;
+};
+
+// One activation's value and derivative.  exp2 and rcp are the hardware's
+// (1 ulp): 2^-22 relative beside the 2^-12 of the narrowest result.  Where
+// exp2 overflows, rcp gives the limit 0.  The sigmoid's argument is taken of
+// g held within +-2^13, where it is 0 or 1 long since: an infinite g would
+// make 0 * inf of a zero c1, a large one overflow its square.
+__device__ __forceinline__ float bounded(float g) { return __builtin_amdgcn_fmed3f(g, -8192.0f, 8192.0f); }
+__device__ __forceinline__ float act_value(const Activation& c, float g, float& s)
+{
+    const float x = bounded(g);
+    const float z = x * __builtin_fmaf(c.c1 * x, x, c.c0);
+    s = __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-1.44269504f * z));
+    return g * s;
+}
+__device__ __forceinline__ float act_slope(const Activation& c, float g, float s)
+{
+    const float x = bounded(g);
+    const float dz = __builtin_fmaf(3.0f * c.c1 * x, x, c.c0);
+    return __builtin_fmaf(g * s * (1.0f - s), dz, s);
+}
+
+// `saved`: for four columns f .. f + 3 of row t, four values P then four Q
+// (32 bytes): a 16 x 16 block's row of one matrix core result is one whole
+// 128-byte line.
+__host__ __device__ __forceinline__ int64_t saved_pitch(int64_t F) { return (F + 3) / 4 * 8; }
+
+template <class E, bool SAVE>
+struct GatedOp {
+    const E *X, *Wg, *Wu;
+    E* H;
+    float* saved;
+    int M, F, K, lda, ldg, ldu, ldh, tiles_m, tiles_n, group_m, vec;
+    Activation act;
+
+    template <int BM, int BN>
+    __device__ __forceinline__ bool tile(int id, Tile& t) const
+    {
+        int tm, tn;
+        tile_of(id, tiles_m, tiles_n, group_m, tm, tn);
+        t.m0 = tm * BM;
+        t.n0 = tn * (BN / 2);
+        t.batch = 0;
+        return true;
+    }
+    __device__ __forceinline__ const E* a_rows(const Tile& t, int row, int& n) const
+    {
+        return rows_from(X, t.m0 + row, M, lda, n);
+    }
+    // Quarter q of the B tile: rows of Wg for even q, of Wu for odd q, the
+    // same BN / 4 rows for both of a pair; a wave's sub-tile (half of the
+    // tile's columns) is one pair.
+    template <int BN>
+    __device__ __forceinline__ const E* b_rows(const Tile& t, int row, int& n) const
+    {
+        const int q = row / (BN / 4);
+        return rows_from(q & 1 ? Wu : Wg, t.n0 + (q >> 1) * (BN / 4), F, q & 1 ? ldu : ldg, n);
+    }
+    __device__ __forceinline__ int b_pitch(int q) const { return q & 1 ? ldu : ldg; }
+    template <class T>
+    __device__ __forceinline__ void epilogue(const Tile& t, const Acc<T>& acc, int lane, int wm, int wn,
+                                             unsigned char*) const
+    {
+        constexpr int HF = T::FN / 2;
+#pragma unroll
+        for (int i = 0; i < T::FM; ++i) {
+            const int m = t.m0 + wm * T::WTM + i * 16 + (lane & 15);
+            if (m >= M) continue;
+#pragma unroll
+            for (int j = 0; j < HF; ++j) {
+                const int f = t.n0 + wn * (T::WTN / 2) + j * 16 + 4 * (lane >> 4);
+                f32x4 h, p, q;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const float g = acc[i][j][e], u = acc[i][j + HF][e];
+                    float s;
+                    q[e] = act_value(act, g, s);
+                    h[e] = q[e] * u;
+                    if constexpr (SAVE) p[e] = u * act_slope(act, g, s);
+                }
+                store4<E>(H + (int64_t)m * ldh, f, F, h, vec);
+                if constexpr (SAVE)
+                    if (f < F) {
+                        float* at = saved + m * saved_pitch(F) + f * 2;
+                        *(f32x4*)at = p;
+                        *(f32x4*)(at + 4) = q;
+                    }
+            }
+        }
+    }
+};
+
+// dG = dH * P, dU = dH * Q for a 64 x 64 tile: row-major into rows of dGU
+// (dG at column 0, dU at column Fp), transposed into dGT and dUT (pitch Tp).
+// Rows and columns past the end, up to multiples of eight, become zeros.
+// Bound by its bytes: 2 + 8 read, 8 written per element.
+template <class E>
+__global__ void __launch_bounds__(relayout::kThreads)
+gated_slopes(const E* __restrict__ dH, const float* __restrict__ saved, E* __restrict__ dGU, E* __restrict__ dGT,
+             E* __restrict__ dUT, int T, int F, int64_t lddh, int Fp, int Tp, int tiles_f, int vec)
+{
+    using x4 = typename Elem<E>::x4;
+    using namespace relayout;
+    __shared__ E tg[kTile * kPitch], tu[kTile * kPitch];
+    const int t0 = (int)(blockIdx.x / tiles_f) * kTile, f0 = (int)(blockIdx.x % tiles_f) * kTile;
+    const int x = threadIdx.x & 15, y = threadIdx.x >> 4;
+    const int f = f0 + x * 4;
+#pragma unroll
+    for (int it = 0; it < 4; ++it) {
+        const int r = it * 16 + y, t = t0 + r;
+        x4 vg = {}, vu = {};
+        if (t < T) {
+            if (f < F) {
+                const x4 d = load4(dH + (int64_t)t * lddh, f, F, vec);
+                const float* at = saved + t * saved_pitch(F) + f * 2;
+                const f32x4 p = *(const f32x4*)at, q = *(const f32x4*)(at + 4);
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    if (f + e < F) {
+                        vg[e] = (E)((float)d[e] * p[e]);
+                        vu[e] = (E)((float)d[e] * q[e]);
+                    }
+            }
+            if (f < Fp) {
+                E* row = dGU + (int64_t)t * 2 * Fp;
+                *(x4*)(row + f) = vg;
+                *(x4*)(row + Fp + f) = vu;
+            }
+        }
+        *(x4*)(tg + r * kPitch + x * 4) = vg;
+        *(x4*)(tu + r * kPitch + x * 4) = vu;
+    }
+    __syncthreads();
+    store_transposed(tg, dGT, Tp, t0, f0, Tp, F);
+    store_transposed(tu, dUT, Tp, t0, f0, Tp, F);
+}
+
+// ------------------------------------------------------------------ host --
+
+template <class E>
+using Tile128 = Shape<E, 128, 128, 3, 1>;
+template <class E>
+using Tile64 = Shape<E, 64, 64, 3, 2>;
+
+bool vec4(const void* p, int64_t ld) { return (uintptr_t)p % 8 == 0 && ld % 4 == 0; }
+bool vec8(const void* p, int64_t ld) { return (uintptr_t)p % 16 == 0 && ld % 8 == 0; }
+
+template <class T, class OP>
+int launch_tiles(OP op, int64_t rows, int64_t cols, int bn, int batch, hipStream_t stream)
+{
+    const int64_t tm = (rows + T::BM - 1) / T::BM, tn = (cols + bn - 1) / bn;
+    if (tm * tn * batch > abi::kMaxDim) return hipErrorInvalidValue;
+    op.tiles_m = (int)tm;
+    op.tiles_n = (int)tn;
+    op.group_m = 8;
+    hipLaunchKernelGGL((nt_tile<T, OP>), dim3((unsigned)(tm * tn * batch)), dim3(T::THREADS), 0, stream, op);
+    return (int)hipGetLastError();
+}
+
+template <class E, class OP>
+int launch_product(const OP& op, int64_t rows, int64_t cols, int split, int batch, hipStream_t stream)
+{
+    const int64_t big = ((rows + 127) / 128) * ((cols * split + 127) / 128) * batch;
+    if (big >= 128) return launch_tiles<Tile128<E>>(op, rows, cols, 128 / split, batch, stream);
+    return launch_tiles<Tile64<E>>(op, rows, cols, 64 / split, batch, stream);
+}
+
+template <class E>
+int launch_copy(const E* src, int64_t ld, E* dst, int64_t ldd, int64_t rows, int64_t cols, hipStream_t stream)
+{
+    const int64_t work = rows * (ldd / 4);
+    if (work == 0) return hipSuccess;
+    hipLaunchKernelGGL(relayout::copy_rows<E>, dim3((unsigned)std::min<int64_t>((work + 255) / 256, 65536)), dim3(256), 0,
+                       stream, src, ld, dst, ldd, rows, (int)cols);
+    return (int)hipGetLastError();
+}
+
+template <class E>
+int launch_transpose(const E* src, int64_t ld, E* dst, int64_t ldd, int64_t rows, int64_t cols, int64_t padded,
+                     hipStream_t stream)
+{
+    const int64_t tr = (padded + 63) / 64, tc = (cols + 63) / 64;
+    if (tr * tc == 0) return hipSuccess;
+    if (tr * tc > abi::kMaxDim) return hipErrorInvalidValue;
+    hipLaunchKernelGGL(relayout::transpose<E>, dim3((unsigned)(tr * tc)), dim3(256), 0, stream, src, ld, dst, ldd,
+                       (int)rows, (int)cols, (int)padded, (int)tc, (int)vec4(src, ld));
+    return (int)hipGetLastError();
+}
+
+// Copies of the operands that the kernels cannot read in place.
+template <class E>
+struct ForwardSpace {
+    E *x, *g, *u;  // null: read in place
+    int64_t bytes;
+    bool copy_x, copy_g, copy_u;
+    ForwardSpace(void* base, const void* X, const void* Wg, const void* Wu, int64_t T, int64_t D, int64_t F, int64_t ldx,
+                 int64_t ldg, int64_t ldu)
+    {
+        abi::Carve c(base);
+        // a row's last chunk is read whole: K % 8 == 0 as well
+        copy_x = D % 8 || !vec8(X, ldx);
+        copy_g = D % 8 || !vec8(Wg, ldg);
+        copy_u = D % 8 || !vec8(Wu, ldu);
+        const int64_t Dp = abi::up(D, 8);
+        x = copy_x ? c.take<E>(T * Dp) : nullptr;
+        g = copy_g ? c.take<E>(F * Dp) : nullptr;
+        u = copy_u ? c.take<E>(F * Dp) : nullptr;
+        bytes = c.used();
+    }
+};
+
+template <class E>
+struct BackwardSpace {
+    E *wt, *xt, *dgu, *dgt, *dut;
+    int64_t Tp, Fp, bytes;
+    BackwardSpace(void* base, int64_t T, int64_t D, int64_t F)
+    {
+        abi::Carve c(base);
+        Tp = abi::up(T, 8);
+        Fp = abi::up(F, 8);
+        wt = c.take<E>(D * 2 * Fp);
+        xt = c.take<E>(D * Tp);
+        dgu = c.take<E>(T * 2 * Fp);
+        dgt = c.take<E>(F * Tp);
+        dut = c.take<E>(F * Tp);
+        bytes = c.used();
+    }
+};
+
+Activation activation_of(int32_t a)
+{
+    if (a == GATED_NT_SILU) return {1.0f, 0.0f};
+    return {1.59576912f, 0.0713548163f};  // 2 sqrt(2 / pi), 0.044715 times that
+}
+
+bool good_sizes(int64_t T, int64_t D, int64_t F)
+{
+    // a row of [dG dU] has 2F elements (and padding)
+    return abi::good_dim(T) && D >= 0 && D <= abi::kMaxPitch - 8 && F >= 0 && 2 * F <= abi::kMaxPitch - 16 &&
+           T <= abi::kMaxDim - 256;
+}
+
+template <class E, bool SAVE>
+int forward(const E* X, const E* Wg, const E* Wu, E* H, float* saved, int64_t T, int64_t D, int64_t F, int64_t ldx,
+            int64_t ldg, int64_t ldu, int64_t ldh, int32_t activation, void* workspace, hipStream_t stream)
+{
+    const ForwardSpace<E> w(workspace, X, Wg, Wu, T, D, F, ldx, ldg, ldu);
+    const int64_t Dp = abi::up(D, 8);
+    int rc = hipSuccess;
+    GatedOp<E, SAVE> op = {};
+    op.X = X;
+    op.Wg = Wg;
+    op.Wu = Wu;
+    op.lda = (int)ldx;
+    op.ldg = (int)ldg;
+    op.ldu = (int)ldu;
+    op.K = (int)Dp;
+    if (w.copy_x) {
+        if ((rc = launch_copy(X, ldx, w.x, Dp, T, D, stream))) return rc;
+        op.X = w.x;
+        op.lda = (int)Dp;
+    }
+    if (w.copy_g) {
+        if ((rc = launch_copy(Wg, ldg, w.g, Dp, F, D, stream))) return rc;
+        op.Wg = w.g;
+        op.ldg = (int)Dp;
+    }
+    if (w.copy_u) {
+        if ((rc = launch_copy(Wu, ldu, w.u, Dp, F, D, stream))) return rc;
+        op.Wu = w.u;
+        op.ldu = (int)Dp;
+    }
+    op.H = H;
+    op.saved = saved;
+    op.M = (int)T;
+    op.F = (int)F;
+    op.ldh = (int)ldh;
+    op.vec = vec4(H, ldh);
+    op.act = activation_of(activation);
+    return launch_product<E>(op, T, F, 2, 1, stream);
+}
+
+template <class E>
+int backward(const E* dH, const E* X, const E* Wg, const E* Wu, const float* saved, E* dX, E* dWg, E* dWu, int64_t T,
+             int64_t D, int64_t F, int64_t lddh, int64_t ldx, int64_t ldg, int64_t ldu, int64_t lddx, int64_t lddg,
+             int64_t lddu, void* workspace, hipStream_t stream)
+{
+    const BackwardSpace<E> w(workspace, T, D, F);
+    int rc;
+    const int64_t tt = (w.Tp + 63) / 64, tf = (w.Fp + 63) / 64;
+    if (tt * tf > abi::kMaxDim) return hipErrorInvalidValue;
+    if (tt * tf > 0) {
+        hipLaunchKernelGGL(gated_slopes<E>, dim3((unsigned)(tt * tf)), dim3(256), 0, stream, dH, saved, w.dgu, w.dgt,
+                           w.dut, (int)T, (int)F, lddh, (int)w.Fp, (int)w.Tp, (int)tf, (int)vec4(dH, lddh));
+        if ((rc = (int)hipGetLastError())) return rc;
+    }
+    if (T > 0 && D > 0) {
+        // [Wg; Wu]^T, D x 2 Fp, zeros between the two
+        if ((rc = launch_transpose(Wg, ldg, w.wt, 2 * w.Fp, F, D, w.Fp, stream))) return rc;
+        if ((rc = launch_transpose(Wu, ldu, w.wt + w.Fp, 2 * w.Fp, F, D, w.Fp, stream))) return rc;
+        StoreOp<E> op = {};
+        op.A = w.dgu;
+        op.B = w.wt;
+        op.C[0] = dX;
+        op.M = (int)T;
+        op.N = (int)D;
+        op.K = op.lda = op.ldb = (int)(2 * w.Fp);
+        op.ldc = (int)lddx;
+        op.vec = vec4(dX, lddx);
+        if ((rc = launch_product<E>(op, T, D, 1, 1, stream))) return rc;
+    }
+    if (F > 0 && D > 0) {
+        if ((rc = launch_transpose(X, ldx, w.xt, w.Tp, T, D, w.Tp, stream))) return rc;
+        for (int i = 0; i < 2; ++i) {
+            StoreOp<E> op = {};
+            op.A = i ? w.dut : w.dgt;
+            op.B = w.xt;
+            op.C[0] = i ? dWu : dWg;
+            op.M = (int)F;
+            op.N = (int)D;
+            op.K = op.lda = op.ldb = (int)w.Tp;
+            op.ldc = (int)(i ? lddu : lddg);
+            op.vec = vec4(op.C[0], op.ldc);
+            if ((rc = launch_product<E>(op, F, D, 1, 1, stream))) return rc;
+        }
+    }
+    return hipSuccess;
+}
+
+}  // namespace
+
+extern "C" {
+
+int gated_nt_version(void) { return GATED_NT_VERSION; }
+
+int64_t gated_nt_saved_bytes(int64_t T, int64_t F)
+{
+    if (!good_sizes(T, 0, F)) return -1;
+    return T * saved_pitch(F) * 4;
+}
+
+int64_t gated_nt_workspace(const void* X, const void* Wg, const void* Wu, int64_t T, int64_t D, int64_t F, int64_t ldx,
+                           int64_t ldg, int64_t ldu)
+{
+    if (!good_sizes(T, D, F)) return -1;
+    return ForwardSpace<_Float16>(nullptr, X, Wg, Wu, T, D, F, ldx, ldg, ldu).bytes;
+}
+
+int64_t gated_nt_backward_workspace(int64_t T, int64_t D, int64_t F)
+{
+    if (!good_sizes(T, D, F)) return -1;
+    return BackwardSpace<_Float16>(nullptr, T, D, F).bytes;
+}
+
+int gated_nt(const void* X, const void* Wg, const void* Wu, void* H, void* saved, int64_t T, int64_t D, int64_t F,
+             int64_t ldx, int64_t ldg, int64_t ldu, int64_t ldh, int32_t type, int32_t activation, void* workspace,
+             int64_t workspace_bytes, hipStream_t stream)
+{
+    using namespace abi;
+    if (!good_sizes(T, D, F)) return hipErrorInvalidValue;
+    if (!good_pitch(ldx, D) || !good_pitch(ldg, D) || !good_pitch(ldu, D) || !good_pitch(ldh, F))
+        return hipErrorInvalidValue;
+    if (type != GATED_NT_F16 && type != GATED_NT_BF16) return hipErrorInvalidValue;
+    if (activation != GATED_NT_SILU && activation != GATED_NT_GELU_TANH) return hipErrorInvalidValue;
+    if (T == 0 || F == 0) return hipSuccess;
+    if (!good_pointer(X, T, D, 2) || !good_pointer(Wg, F, D, 2) || !good_pointer(Wu, F, D, 2) ||
+        !good_pointer(H, T, F, 2) || (uintptr_t)saved % 16 || (uintptr_t)workspace % 16)
+        return hipErrorInvalidValue;
+    const int64_t need = gated_nt_workspace(X, Wg, Wu, T, D, F, ldx, ldg, ldu);
+    if (need > 0 && (!workspace || workspace_bytes < need)) return hipErrorInvalidValue;
+    const Range h(H, T, F, ldh, 2), s(saved, 1, saved ? gated_nt_saved_bytes(T, F) : 0, 0, 1);
+    const Range w(workspace, 1, need, 0, 1);
+    const Range in[] = {Range(X, T, D, ldx, 2), Range(Wg, F, D, ldg, 2), Range(Wu, F, D, ldu, 2)};
+    for (const Range& r : in)
+        if (h.meets(r) || s.meets(r) || w.meets(r)) return hipErrorInvalidValue;
+    if (h.meets(s) || h.meets(w) || s.meets(w)) return hipErrorInvalidValue;
+#define FORWARD(E, SAVE)                                                                                         \
+    forward<E, SAVE>((const E*)X, (const E*)Wg, (const E*)Wu, (E*)H, (float*)saved, T, D, F, ldx, ldg, ldu, ldh, \
+                     activation, workspace, stream)
+    if (type == GATED_NT_F16) return saved ? FORWARD(_Float16, true) : FORWARD(_Float16, false);
+    return saved ? FORWARD(__bf16, true) : FORWARD(__bf16, false);
+#undef FORWARD
+}
+
+int gated_nt_backward(const void* dH, const void* X, const void* Wg, const void* Wu, const void* saved, void* dX,
+                      void* dWg, void* dWu, int64_t T, int64_t D, int64_t F, int64_t lddh, int64_t ldx, int64_t ldg,
+                      int64_t ldu, int64_t lddx, int64_t lddg, int64_t lddu, int32_t type, void* workspace,
+                      int64_t workspace_bytes, hipStream_t stream)
+{
+    using namespace abi;
+    if (!good_sizes(T, D, F)) return hipErrorInvalidValue;
+    if (!good_pitch(lddh, F) || !good_pitch(ldx, D) || !good_pitch(ldg, D) || !good_pitch(ldu, D) ||
+        !good_pitch(lddx, D) || !good_pitch(lddg, D) || !good_pitch(lddu, D))
+        return hipErrorInvalidValue;
+    if (up(T, 8) > kMaxPitch) return hipErrorInvalidValue;  // rows of the transposed operands
+    if (type != GATED_NT_F16 && type != GATED_NT_BF16) return hipErrorInvalidValue;
+    if (!good_pointer(dH, T, F, 2) || !good_pointer(X, T, D, 2) || !good_pointer(Wg, F, D, 2) ||
+        !good_pointer(Wu, F, D, 2) || !good_pointer(saved, T, F, 16) || !good_pointer(dX, T, D, 2) ||
+        !good_pointer(dWg, F, D, 2) || !good_pointer(dWu, F, D, 2) || (uintptr_t)workspace % 16)
+        return hipErrorInvalidValue;
+    const int64_t need = gated_nt_backward_workspace(T, D, F);
+    if (need > 0 && (!workspace || workspace_bytes < need)) return hipErrorInvalidValue;
+    const Range in[] = {Range(dH, T, F, lddh, 2), Range(X, T, D, ldx, 2), Range(Wg, F, D, ldg, 2),
+                        Range(Wu, F, D, ldu, 2), Range(saved, 1, gated_nt_saved_bytes(T, F), 0, 1)};
+    const Range out[] = {Range(dX, T, D, lddx, 2), Range(dWg, F, D, lddg, 2), Range(dWu, F, D, lddu, 2),
+                         Range(workspace, 1, need, 0, 1)};
+    for (int i = 0; i < 4; ++i) {
+        for (const Range& r : in)
+            if (out[i].meets(r)) return hipErrorInvalidValue;
+        for (int k = 0; k < i; ++k)
+            if (out[i].meets(out[k])) return hipErrorInvalidValue;
+    }
+#define BACKWARD(E)                                                                                                    \
+    backward<E>((const E*)dH, (const E*)X, (const E*)Wg, (const E*)Wu, (const float*)saved, (E*)dX, (E*)dWg, (E*)dWu, T, \
+                D, F, lddh, ldx, ldg, ldu, lddx, lddg, lddu, workspace, stream)
+    return type == GATED_NT_F16 ? BACKWARD(_Float16) : BACKWARD(__bf16);
+#undef BACKWARD
+}
+
+}  // extern "C"

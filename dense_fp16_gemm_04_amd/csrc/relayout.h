@@ -1,0 +1,85 @@
+// Copies that bring an operand into the form the tiled products read: rows
+// on 16 bytes, padded with zeros to a multiple of eight elements, as they are
+// or transposed.
+#ifndef DENSE_FP16_GEMM_RELAYOUT_H
+#define DENSE_FP16_GEMM_RELAYOUT_H
+
+#include "cdna4.h"
+
+namespace relayout {
+
+using namespace cdna4;
+
+constexpr int kTile = 64;       // a workgroup moves a 64 x 64 tile
+constexpr int kThreads = 256;   // as 16 columns of four elements by 16 rows, four times
+constexpr int kPitch = 68;      // LDS row pitch in elements: 8-byte aligned, 34 banks apart
+
+// Four elements of a row, columns c .. c + 3 of `cols`, zero past the end.
+template <class E>
+__device__ __forceinline__ typename Elem<E>::x4 load4(const E* row, int c, int cols, bool vec)
+{
+    typename Elem<E>::x4 v = {};
+    if (vec && c + 3 < cols) {
+        v = *(const typename Elem<E>::x4*)(row + c);
+    } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            if (c + e < cols) v[e] = row[c + e];
+    }
+    return v;
+}
+
+// Writes a 64 x 64 tile that LDS holds row-major (pitch kPitch) transposed:
+// dst[c][r] for tile row r and column c, whole rows of `rows` in groups of
+// eight bytes (dst's pitch is a multiple of 8; rows past `rows_valid` hold
+// zeros in LDS, and `rows` is its multiple of eight).
+template <class E>
+__device__ __forceinline__ void store_transposed(const E* tile, E* dst, int64_t ldd, int r0, int c0, int rows, int cols)
+{
+    const int x = threadIdx.x & 15, y = threadIdx.x >> 4;
+#pragma unroll
+    for (int it = 0; it < 4; ++it) {
+        const int c = it * 16 + y, r = x * 4;
+        if (c0 + c >= cols || r0 + r >= rows) continue;
+        typename Elem<E>::x4 v;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[e] = tile[(r + e) * kPitch + c];
+        *(typename Elem<E>::x4*)(dst + (int64_t)(c0 + c) * ldd + r0 + r) = v;
+    }
+}
+
+// dst[r][c] = src[r][c] for c < cols, 0 for cols <= c < ldd.
+template <class E>
+__global__ void __launch_bounds__(kThreads) copy_rows(const E* __restrict__ src, int64_t lds_, E* __restrict__ dst,
+                                                      int64_t ldd, int64_t rows, int cols)
+{
+    const int64_t per = ldd / 4;
+    for (int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x; i < rows * per; i += (int64_t)gridDim.x * kThreads) {
+        const int64_t r = i / per;
+        const int c = (int)(i - r * per) * 4;
+        *(typename Elem<E>::x4*)(dst + r * ldd + c) = load4(src + r * lds_, c, cols, false);
+    }
+}
+
+// dst[c][r] = src[r][c] for r < rows, 0 for rows <= r < padded.
+template <class E>
+__global__ void __launch_bounds__(kThreads) transpose(const E* __restrict__ src, int64_t lds_, E* __restrict__ dst,
+                                                      int64_t ldd, int rows, int cols, int padded, int tiles_c, int vec)
+{
+    __shared__ E tile[kTile * kPitch];
+    const int r0 = (int)(blockIdx.x / tiles_c) * kTile, c0 = (int)(blockIdx.x % tiles_c) * kTile;
+    const int x = threadIdx.x & 15, y = threadIdx.x >> 4;
+#pragma unroll
+    for (int it = 0; it < 4; ++it) {
+        const int r = it * 16 + y;
+        typename Elem<E>::x4 v = {};
+        if (r0 + r < rows) v = load4(src + (int64_t)(r0 + r) * lds_, c0 + x * 4, cols, vec);
+        *(typename Elem<E>::x4*)(tile + r * kPitch + x * 4) = v;
+    }
+    __syncthreads();
+    store_transposed(tile, dst, ldd, r0, c0, padded, cols);
+}
+
+}  // namespace relayout
+
+#endif

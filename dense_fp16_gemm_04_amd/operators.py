@@ -1,0 +1,301 @@
+"""ctypes bindings of the operators beside the product (argument marshalling only).
+
+``libgated_nt.so``, ``liborthogonalize_ns.so`` and ``libgemv_w4.so`` with the
+C ABIs of ``include/gated_nt.h``, ``include/orthogonalize_ns.h`` and
+``include/gemv_w4.h``.  As in ``binding``, PyTorch supplies device memory
+(results and workspaces) and the current stream, all arithmetic runs in the
+libraries' HIP kernels, a missing library raises ``RuntimeError`` and a
+refused call ``TypeError``, ``ValueError`` or ``GemmError``.  Nothing here
+takes part in autograd: a training step calls the backward function itself.
+
+Matrices may be views: the elements of a row are adjacent, rows may lie any
+distance apart that does not make them overlap.
+"""
+from __future__ import annotations
+
+import ctypes
+import os
+import threading
+
+from .binding import GemmError, _stream
+
+_HERE = os.path.dirname(os.path.abspath(__file__))
+
+_i64 = ctypes.c_int64
+_i32 = ctypes.c_int32
+_p = ctypes.c_void_p
+_int = ctypes.c_int
+
+# library -> {function declared in include/<library>.h: its ctypes signature}
+SIGNATURES = {
+    "gated_nt": {
+        "gated_nt": ([_p] * 5 + [_i64] * 7 + [_i32, _i32, _p, _i64, _p], _int),
+        "gated_nt_backward": ([_p] * 8 + [_i64] * 10 + [_i32, _p, _i64, _p], _int),
+        "gated_nt_saved_bytes": ([_i64] * 2, _i64),
+        "gated_nt_workspace": ([_p] * 3 + [_i64] * 6, _i64),
+        "gated_nt_backward_workspace": ([_i64] * 3, _i64),
+        "gated_nt_version": ([], _int),
+    },
+    "orthogonalize_ns": {
+        "orthogonalize_ns": ([_p, _p] + [_i64] * 7 + [_i32, _i32, ctypes.POINTER(ctypes.c_double), ctypes.c_double,
+                                                      _p, _i64, _p], _int),
+        "orthogonalize_ns_workspace": ([_i64] * 3, _i64),
+        "orthogonalize_ns_version": ([], _int),
+    },
+    "gemv_w4": {
+        "gemv_w4": ([_p] * 5 + [_i64] * 7 + [_i32, _p], _int),
+        "gemv_w4_version": ([], _int),
+    },
+}
+
+ACTIVATIONS = {"silu": 0, "gelu_tanh": 1}
+
+_libs = {}
+_lock = threading.Lock()
+
+
+def library_path(name: str) -> str:
+    return os.path.join(_HERE, "lib%s.so" % name)
+
+
+def load(name: str):
+    """Load an operator's library once; raise if it has not been built."""
+    lib = _libs.get(name)
+    if lib is not None:
+        return lib
+    with _lock:
+        if name not in _libs:
+            path = library_path(name)
+            if not os.path.exists(path):
+                raise RuntimeError("lib%s.so is not built (%s); run "
+                                   "`python -c 'import __graft_entry__ as g; g.build()'`" % (name, path))
+            lib = ctypes.CDLL(path)
+            for fn, (args, res) in SIGNATURES[name].items():
+                f = getattr(lib, fn)
+                f.argtypes = args
+                f.restype = res
+            _libs[name] = lib
+    return _libs[name]
+
+
+def _types():
+    import torch
+    return {torch.float16: 0, torch.bfloat16: 1}
+
+
+def _check_matrix(name, t, dtypes, device=None, shape=None):
+    """t is a GPU matrix of one of `dtypes` whose rows do not overlap; its row pitch."""
+    import torch
+    if not isinstance(t, torch.Tensor):
+        raise TypeError("%s must be a torch tensor" % name)
+    if t.dtype not in dtypes:
+        raise TypeError("%s must be %s, got %s" % (name, " or ".join(str(d).replace("torch.", "") for d in dtypes),
+                                                   str(t.dtype).replace("torch.", "")))
+    if t.dim() != 2 or (shape is not None and tuple(t.shape) != tuple(shape)):
+        raise ValueError("%s must be a matrix%s, got %s" % (
+            name, "" if shape is None else " of shape %s" % (tuple(shape),), tuple(t.shape)))
+    if not t.is_cuda or (device is not None and t.get_device() != device):
+        raise ValueError("%s must be on %s" % (name, "a GPU" if device is None else "the first operand's GPU"))
+    rows, cols = t.shape
+    if (cols > 1 and t.stride(1) != 1) or (rows > 1 and cols > 0 and t.stride(0) < cols):
+        raise ValueError("%s must have adjacent elements in a row and rows that do not overlap, got strides %s" % (
+            name, t.stride()))
+    return t.stride(0) if rows > 1 and cols > 0 else cols
+
+
+def _out(name, out, shape, dtype, device):
+    import torch
+    if out is None:
+        out = torch.empty(shape, dtype=dtype, device=torch.device("cuda", device))
+    return out, _check_matrix(name, out, (dtype,), device, shape)
+
+
+def _workspace(nbytes, device):
+    """(tensor, address) of a workspace from torch's allocator: freed on
+    return, and handed out again only to work later on the same stream."""
+    import torch
+    if nbytes <= 0:
+        return None, None
+    w = torch.empty(nbytes, dtype=torch.uint8, device=torch.device("cuda", device))
+    return w, w.data_ptr()
+
+
+def _call(library, name, device, *args):
+    """Call an entry point on `device` and its current stream (the last argument)."""
+    import torch
+    fn = getattr(load(library), name)
+    if device == torch.cuda.current_device():
+        rc = fn(*args, _stream(device))
+    else:
+        with torch.cuda.device(device):
+            rc = fn(*args, _stream(device))
+    if rc != 0:
+        raise GemmError(name, rc)
+
+
+def _check_gated(x, w_gate, w_up):
+    dtypes = tuple(_types())
+    ldx = _check_matrix("x", x, dtypes)
+    device = x.get_device()
+    ldg = _check_matrix("w_gate", w_gate, (x.dtype,), device)
+    if w_gate.shape[1] != x.shape[1]:
+        raise ValueError("need x [T, D] and w_gate, w_up [F, D], got %s and %s" % (tuple(x.shape), tuple(w_gate.shape)))
+    ldu = _check_matrix("w_up", w_up, (x.dtype,), device, w_gate.shape)
+    return device, ldx, ldg, ldu
+
+
+def _gated(x, w_gate, w_up, activation, out, train):
+    import torch
+    device, ldx, ldg, ldu = _check_gated(x, w_gate, w_up)
+    if activation not in ACTIVATIONS:
+        raise ValueError("activation must be one of %s, got %r" % (", ".join(sorted(ACTIVATIONS)), activation))
+    (T, D), F = x.shape, w_gate.shape[0]
+    out, ldh = _out("out", out, (T, F), x.dtype, device)
+    lib = load("gated_nt")
+    saved = None
+    if train:
+        nbytes = lib.gated_nt_saved_bytes(T, F)
+        if nbytes < 0:
+            raise GemmError("gated_nt", 1)
+        saved = torch.empty(nbytes, dtype=torch.uint8, device=x.device)
+    ptrs = (x.data_ptr(), w_gate.data_ptr(), w_up.data_ptr())
+    nbytes = lib.gated_nt_workspace(*ptrs, T, D, F, ldx, ldg, ldu)
+    keep, workspace = _workspace(nbytes, device)
+    _call("gated_nt", "gated_nt", device, *ptrs, out.data_ptr(), saved.data_ptr() if train else None, T, D, F, ldx, ldg,
+          ldu, ldh, _types()[x.dtype], ACTIVATIONS[activation], workspace, max(nbytes, 0))
+    return out, saved
+
+
+def gated_nt(x, w_gate, w_up, activation: str = "silu", out=None):
+    """out[T, F] = act(x @ w_gate^T) * (x @ w_up^T) for x [T, D] and weights [F, D].
+
+    float16 or bfloat16; ``activation`` is "silu" or "gelu_tanh".  Sums,
+    activation and product in 32 bits, rounded once.  Enqueued on the current
+    stream of x's device; returns ``out``.
+    """
+    return _gated(x, w_gate, w_up, activation, out, False)[0]
+
+
+def gated_nt_train(x, w_gate, w_up, activation: str = "silu", out=None):
+    """``gated_nt`` that also keeps what its backward pass reads: (out, saved).
+
+    ``saved`` (8 bytes per output, 32-bit values in the library's own layout)
+    is for ``gated_nt_backward`` with the same x and weights.
+    """
+    return _gated(x, w_gate, w_up, activation, out, True)
+
+
+def gated_nt_backward(dh, x, w_gate, w_up, saved, out=None):
+    """The gradients (dx, dw_gate, dw_up) of ``gated_nt_train`` for the gradient dh [T, F] of its output.
+
+    ``out``: three matrices to write them to, or None for new ones.  They are
+    written, not added to.
+    """
+    import torch
+    device, ldx, ldg, ldu = _check_gated(x, w_gate, w_up)
+    (T, D), F = x.shape, w_gate.shape[0]
+    lddh = _check_matrix("dh", dh, (x.dtype,), device, (T, F))
+    lib = load("gated_nt")
+    need = lib.gated_nt_saved_bytes(T, F)
+    nbytes = lib.gated_nt_backward_workspace(T, D, F)
+    if need < 0 or nbytes < 0:
+        raise GemmError("gated_nt_backward", 1)
+    if not isinstance(saved, torch.Tensor) or saved.dtype != torch.uint8 or saved.dim() != 1 \
+            or saved.numel() != need or not saved.is_contiguous() or (need and saved.get_device() != device):
+        raise ValueError("saved must be what gated_nt_train returned for x, w_gate and w_up")
+    if out is not None and len(out) != 3:
+        raise ValueError("out must be the three matrices dx, dw_gate and dw_up")
+    outs = []
+    for name, given, shape in zip(("dx", "dw_gate", "dw_up"), out or (None,) * 3, ((T, D), (F, D), (F, D))):
+        outs.append(_out("out's " + name, given, shape, x.dtype, device))
+    keep, workspace = _workspace(nbytes, device)
+    _call("gated_nt", "gated_nt_backward", device, dh.data_ptr(), x.data_ptr(), w_gate.data_ptr(), w_up.data_ptr(),
+          saved.data_ptr(), *(t.data_ptr() for t, _ in outs), T, D, F, lddh, ldx, ldg, ldu, *(ld for _, ld in outs),
+          _types()[x.dtype], workspace, nbytes)
+    return tuple(t for t, _ in outs)
+
+
+def orthogonalize_ns(g, steps: int = 5, coefficients=(3.4445, -4.7750, 2.0315), eps: float = 1e-7, out=None):
+    """The update g [rows, cols] (or [batch, rows, cols]) with its singular values driven towards 1, in bfloat16.
+
+    x = g / (|g|_F + eps), then ``steps`` times x = a x + (b s + c s s) x with
+    s = x x^T.  ``coefficients`` is one triple (a, b, c), or one for each
+    step.  g is float16, bfloat16 or float32; the iterates are held in
+    binary16, hence the bfloat16 result.
+    """
+    import torch
+    if not isinstance(g, torch.Tensor):
+        raise TypeError("g must be a torch tensor")
+    types = {**_types(), torch.float32: 2}
+    if g.dim() not in (2, 3):
+        raise ValueError("g must be [rows, cols] or [batch, rows, cols], got %s" % (tuple(g.shape),))
+    steps = int(steps)
+    if not 0 <= steps <= 64:
+        raise ValueError("steps must be 0 .. 64, got %d" % steps)
+    triples = [tuple(float(v) for v in c) for c in coefficients] if steps and hasattr(coefficients[0], "__len__") \
+        else [tuple(float(v) for v in coefficients)] * steps
+    if len(triples) != steps or any(len(c) != 3 for c in triples):
+        raise ValueError("coefficients must be one triple, or one for each of the %d steps" % steps)
+    batch = g.shape[0] if g.dim() == 3 else 1
+    rows, cols = g.shape[-2:]
+
+    def first(t):  # one matrix of the batch (of an empty one: any of its shape)
+        return t if t.dim() == 2 else t[0] if t.shape[0] else t.new_empty(rows, cols)
+
+    ldg = _check_matrix("g", first(g), tuple(types))
+    device = g.get_device()
+    if out is None:
+        out = torch.empty(g.shape, dtype=torch.bfloat16, device=g.device)
+    if not isinstance(out, torch.Tensor) or out.shape != g.shape:
+        raise ValueError("out must be a bfloat16 tensor of g's shape %s" % (tuple(g.shape),))
+    ldo = _check_matrix("out", first(out), (torch.bfloat16,), device, (rows, cols))
+    if g.numel() == 0:
+        return out
+    stride_g, stride_o = (t.stride(0) if t.dim() == 3 and batch > 1 else 0 for t in (g, out))
+    if batch > 1 and (stride_g < 0 or stride_o < (rows - 1) * ldo + cols):
+        raise ValueError("out's matrices must not overlap, got strides %s" % (out.stride(),))
+    lib = load("orthogonalize_ns")
+    nbytes = lib.orthogonalize_ns_workspace(batch, rows, cols)
+    if nbytes < 0:
+        raise GemmError("orthogonalize_ns", 1)
+    keep, workspace = _workspace(nbytes, device)
+    flat = (ctypes.c_double * max(1, 3 * steps))(*(v for c in triples for v in c))
+    _call("orthogonalize_ns", "orthogonalize_ns", device, g.data_ptr(), out.data_ptr(), batch, rows, cols, ldg, stride_g,
+          ldo, stride_o, types[g.dtype], steps, flat, float(eps), workspace, nbytes)
+    return out
+
+
+def gemv_w4(x, q, scales, zeros=None, out=None):
+    """out[M, N] = x[M, K] @ w^T for 4-bit weights w[n, k] = (q[n, k] - zeros[n, k // group]) * scales[n, k // group].
+
+    ``q`` is uint8 [N, K / 2], even k in the low half of a byte; ``scales``
+    [N, K / group] of x's type gives the group (a power of two from 32 on, or
+    K); ``zeros`` likewise, or None for 8.  x is float16 or bfloat16.
+    Enqueued on the current stream of x's device; returns ``out``.
+    """
+    import torch
+    ldx = _check_matrix("x", x, tuple(_types()))
+    device = x.get_device()
+    M, K = x.shape
+    ldq = _check_matrix("q", q, (torch.uint8,), device)
+    N = q.shape[0]
+    if K % 32 or q.shape[1] != K // 2:
+        raise ValueError("need x [M, K] and q [N, K / 2] with K a multiple of 32, got %s and %s" % (
+            tuple(x.shape), tuple(q.shape)))
+    if q.numel() and (q.data_ptr() % 16 or (N > 1 and ldq % 16)):
+        raise ValueError("q's rows must start on 16 bytes")
+    for name, t in (("scales", scales), ("zeros", zeros)):
+        if t is None and name == "zeros":
+            continue
+        _check_matrix(name, t, (x.dtype,), device)
+        if t.shape[0] != N or t.shape != scales.shape or not t.is_contiguous():
+            raise ValueError("%s must be contiguous [%d, groups], got %s" % (name, N, tuple(t.shape)))
+    groups = scales.shape[1]
+    group = K // groups if groups and K % groups == 0 else 0
+    if K and (group == 0 or ((group < 32 or group & (group - 1)) and group != K)):
+        raise ValueError("K / scales.shape[1] must be a power of two from 32 on, or K: got %d / %d" % (K, groups))
+    out, ldy = _out("out", out, (M, N), x.dtype, device)
+    _call("gemv_w4", "gemv_w4", device, x.data_ptr(), q.data_ptr(), scales.data_ptr(),
+          None if zeros is None else zeros.data_ptr(), out.data_ptr(), M, N, K, group, ldx, max(ldq, K // 2), ldy,
+          _types()[x.dtype])
+    return out

@@ -1,0 +1,242 @@
+"""The operators beside the product without a GPU: their libraries export what
+the headers declare and refuse bad arguments before enqueuing anything; the
+bindings' checks; the plain forms' own gradients against differences."""
+from __future__ import annotations
+
+import ctypes
+import json
+import os
+import re
+
+import pytest
+import torch
+
+import _operators as plain
+import dense_fp16_gemm_04_amd as fw
+from dense_fp16_gemm_04_amd import build, operators
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+INVALID = 1  # hipErrorInvalidValue
+# addresses that are never touched: 64 MiB apart, 16-byte aligned
+A, B, C, D, E, F, G, H, W = (0x10000000 + i * 0x4000000 for i in range(9))
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    if not all(os.path.exists(operators.library_path(n)) for n in build.OPERATORS):
+        import __graft_entry__
+        __graft_entry__.build()
+
+
+@pytest.mark.parametrize("name", build.OPERATORS)
+def test_declared_symbols_and_version(name):
+    text = open(os.path.join(ROOT, "include", name + ".h")).read()
+    declared = sorted(set(re.findall(r"\b(%s\w*)\s*\(" % name, re.sub(r"/\*.*?\*/", "", text, flags=re.S))))
+    assert sorted(operators.SIGNATURES[name]) == declared
+    lib = operators.load(name)
+    version = re.search(r"#define\s+%s_VERSION\s+(\d+)" % name.upper(), text)
+    assert getattr(lib, name + "_version")() == int(version.group(1))
+
+
+@pytest.mark.parametrize("name", build.OPERATORS)
+def test_no_kernel_spills(name):
+    _, _, resources = build.operator_paths(name)
+    kernels = json.load(open(resources))["kernels"]
+    assert kernels and build.spilling(kernels) == []
+    for k, r in kernels.items():
+        assert r["vgprs"] + r["agprs"] <= 512 and r["lds_bytes"] <= 160 * 1024, k
+
+
+def test_missing_library_raises(monkeypatch, tmp_path):
+    monkeypatch.setattr(operators, "_HERE", str(tmp_path))
+    monkeypatch.setattr(operators, "_libs", {})
+    with pytest.raises(RuntimeError, match="not built"):
+        operators.load("gated_nt")
+
+
+# ------------------------------------------------------------- gated_nt --
+
+def gated_args(**kw):
+    a = dict(X=A, Wg=B, Wu=C, H=D, saved=None, T=4, D=16, F=8, ldx=16, ldg=16, ldu=16, ldh=8, type=0, act=0, ws=None,
+             ws_bytes=0, stream=None)
+    assert set(kw) <= set(a)
+    a.update(kw)
+    return list(a.values())
+
+
+@pytest.mark.parametrize("kw", [
+    dict(T=-1), dict(D=-1), dict(F=-1), dict(T=1 << 31), dict(D=1 << 31, ldx=1 << 31, ldg=1 << 31, ldu=1 << 31),
+    dict(ldx=15), dict(ldg=15), dict(ldu=15), dict(ldh=7), dict(ldx=1 << 21), dict(ldh=1 << 21),
+    dict(type=2), dict(type=-1), dict(act=2), dict(act=-1),
+    dict(X=None), dict(Wg=None), dict(Wu=None), dict(H=None), dict(X=A + 1), dict(H=D + 1), dict(saved=E + 8),
+    dict(H=A + 16), dict(H=B), dict(H=C), dict(saved=A), dict(saved=D),
+    dict(X=A + 2),                            # needs a copy, and there is no workspace
+    dict(X=A + 2, ws=W, ws_bytes=8), dict(X=A + 2, ws=W + 8, ws_bytes=1 << 20),
+    dict(X=A + 2, ws=A, ws_bytes=1 << 20), dict(X=A + 2, ws=D, ws_bytes=1 << 20),
+    dict(ldg=17), dict(D=15, ldx=16),
+])
+def test_gated_refuses(kw):
+    assert operators.load("gated_nt").gated_nt(*gated_args(**kw)) == INVALID
+
+
+def test_gated_empty_is_a_no_op():
+    lib = operators.load("gated_nt")
+    assert lib.gated_nt(*gated_args(T=0, X=None, H=None)) == 0
+    assert lib.gated_nt(*gated_args(F=0, Wg=None, Wu=None, H=None, ldh=0)) == 0
+
+
+def test_gated_sizes():
+    lib = operators.load("gated_nt")
+    assert lib.gated_nt_saved_bytes(3, 5) == 3 * 8 * 2 * 4   # columns in fours, two values, four bytes
+    assert lib.gated_nt_saved_bytes(-1, 5) == -1 and lib.gated_nt_saved_bytes(3, 1 << 31) == -1
+    assert lib.gated_nt_workspace(A, B, C, 4, 16, 8, 16, 16, 16) == 0
+    assert lib.gated_nt_workspace(A, B, C, 4, 16, 8, 24, 16, 32) == 0   # any pitch that is a multiple of 8
+    assert lib.gated_nt_workspace(A, B, C, 4, 15, 8, 16, 16, 16) >= (4 + 8 + 8) * 16 * 2
+    assert lib.gated_nt_workspace(A + 2, B, C, 4, 16, 8, 16, 16, 16) >= 4 * 16 * 2
+    assert lib.gated_nt_workspace(A, B, C, -1, 16, 8, 16, 16, 16) == -1
+    assert lib.gated_nt_backward_workspace(-1, 16, 8) == -1
+    assert lib.gated_nt_backward_workspace(4, 16, 8) > 0
+
+
+def backward_args(**kw):
+    a = dict(dH=A, X=B, Wg=C, Wu=D, saved=E, dX=F, dWg=G, dWu=H, T=4, D=16, F=8, lddh=8, ldx=16, ldg=16, ldu=16,
+             lddx=16, lddg=16, lddu=16, type=0, ws=W, ws_bytes=1 << 20, stream=None)
+    assert set(kw) <= set(a)
+    a.update(kw)
+    return list(a.values())
+
+
+@pytest.mark.parametrize("kw", [
+    dict(T=-1), dict(D=-1), dict(F=-1), dict(T=1 << 21), dict(lddh=7), dict(ldx=15), dict(ldg=15), dict(ldu=15),
+    dict(lddx=15), dict(lddg=15), dict(lddu=15), dict(type=2), dict(dH=None), dict(X=None), dict(Wg=None),
+    dict(Wu=None), dict(saved=None), dict(saved=E + 8), dict(dX=None), dict(dWg=None), dict(dWu=None), dict(ws=None),
+    dict(ws_bytes=64), dict(ws=W + 8), dict(dX=B), dict(dWg=C), dict(dWu=G + 32), dict(dX=E), dict(ws=A), dict(ws=F),
+])
+def test_gated_backward_refuses(kw):
+    assert operators.load("gated_nt").gated_nt_backward(*backward_args(**kw)) == INVALID
+
+
+# ----------------------------------------------------- orthogonalize_ns --
+
+def ns_args(**kw):
+    a = dict(G=A, out=B, batch=2, rows=8, cols=16, ldg=16, stride_g=128, ldo=16, stride_o=128, type=0, steps=5,
+             coefficients=(ctypes.c_double * 15)(*([3.4445, -4.775, 2.0315] * 5)), eps=1e-7, ws=W, ws_bytes=1 << 20,
+             stream=None)
+    assert set(kw) <= set(a)
+    a.update(kw)
+    return list(a.values())
+
+
+@pytest.mark.parametrize("kw", [
+    dict(batch=-1), dict(rows=-1), dict(cols=-1), dict(batch=1 << 16), dict(rows=1 << 21), dict(cols=1 << 21),
+    dict(ldg=15), dict(ldo=15), dict(stride_g=-1), dict(stride_o=127), dict(type=3), dict(type=-1), dict(steps=-1),
+    dict(steps=65), dict(coefficients=None), dict(G=None), dict(out=None), dict(ws=None), dict(ws_bytes=64),
+    dict(ws=W + 8), dict(G=A + 1), dict(G=A + 2, type=2), dict(out=B + 1), dict(out=A + 16), dict(ws=A), dict(ws=B),
+])
+def test_ns_refuses(kw):
+    assert operators.load("orthogonalize_ns").orthogonalize_ns(*ns_args(**kw)) == INVALID
+
+
+def test_ns_empty_and_workspace():
+    lib = operators.load("orthogonalize_ns")
+    for kw in (dict(batch=0), dict(rows=0), dict(cols=0, ldg=0, ldo=0)):
+        assert lib.orthogonalize_ns(*ns_args(G=None, out=None, ws=None, ws_bytes=0, **kw)) == 0
+    assert lib.orthogonalize_ns_workspace(0, 4, 4) == 0
+    assert lib.orthogonalize_ns_workspace(-1, 4, 4) == -1
+    assert lib.orthogonalize_ns_workspace(1, 8, 16) > 0
+
+
+# -------------------------------------------------------------- gemv_w4 --
+
+def w4_args(**kw):
+    a = dict(X=A, Q=B, scale=C, zero=None, Y=D, M=2, N=8, K=64, group=32, ldx=64, ldq=32, ldy=8, type=0, stream=None)
+    assert set(kw) <= set(a)
+    a.update(kw)
+    return list(a.values())
+
+
+@pytest.mark.parametrize("kw", [
+    dict(M=-1), dict(N=-1), dict(K=-32), dict(M=1 << 31), dict(N=1 << 31), dict(K=1 << 21, ldx=1 << 21, ldq=1 << 20),
+    dict(K=40, ldx=64), dict(ldx=63), dict(ldq=31), dict(ldq=40), dict(ldy=7), dict(group=0), dict(group=16),
+    dict(K=192, ldx=192, ldq=96, group=96), dict(group=-32), dict(type=2), dict(type=-1), dict(X=None), dict(Q=None),
+    dict(scale=None), dict(Y=None), dict(X=A + 1), dict(Q=B + 8), dict(scale=C + 1), dict(zero=E + 1), dict(Y=D + 1),
+    dict(Y=A), dict(Y=B), dict(Y=C), dict(zero=D),
+])
+def test_w4_refuses(kw):
+    assert operators.load("gemv_w4").gemv_w4(*w4_args(**kw)) == INVALID
+
+
+def test_w4_empty_is_a_no_op():
+    lib = operators.load("gemv_w4")
+    assert lib.gemv_w4(*w4_args(M=0, X=None, Y=None)) == 0
+    assert lib.gemv_w4(*w4_args(N=0, Q=None, scale=None, Y=None, ldy=0)) == 0
+
+
+# ------------------------------------------------------------- bindings --
+
+def test_bindings_refuse_host_tensors_and_wrong_types():
+    x = torch.zeros(4, 16, dtype=torch.float16)
+    w = torch.zeros(8, 16, dtype=torch.float16)
+    for call in (lambda: fw.gated_nt(x, w, w), lambda: fw.gated_nt_train(x, w, w),
+                 lambda: fw.gated_nt_backward(x[:, :8], x, w, w, torch.zeros(0, dtype=torch.uint8)),
+                 lambda: fw.orthogonalize_ns(w), lambda: fw.gemv_w4(x, w, w)):
+        with pytest.raises(ValueError, match="GPU"):
+            call()
+    with pytest.raises(TypeError):
+        fw.gated_nt(x.float(), w, w)
+    with pytest.raises(TypeError):
+        fw.gated_nt([1.0], w, w)
+    with pytest.raises(TypeError):
+        fw.orthogonalize_ns(w.double())
+    with pytest.raises(TypeError):
+        fw.orthogonalize_ns("w")
+    with pytest.raises(TypeError):
+        fw.gemv_w4(x.float(), w, w)
+    with pytest.raises(ValueError):
+        fw.orthogonalize_ns(w[0])
+    with pytest.raises(ValueError, match="steps"):
+        fw.orthogonalize_ns(w, steps=65)
+    with pytest.raises(ValueError, match="coefficients"):
+        fw.orthogonalize_ns(w, coefficients=(1.0, 2.0))
+    with pytest.raises(ValueError, match="coefficients"):
+        fw.orthogonalize_ns(w, steps=2, coefficients=[(1.0, 2.0, 3.0)])
+
+
+# ------------------------------------------------- the plain forms here --
+
+@pytest.mark.parametrize("act", ["silu", "gelu_tanh"])
+def test_plain_gradients_match_differences(act):
+    gen = torch.Generator().manual_seed(7)
+    t = [torch.randn(*s, generator=gen, dtype=torch.float64) for s in ((5, 9), (7, 9), (7, 9))]
+    dh = torch.randn(5, 7, generator=gen, dtype=torch.float64)
+
+    def loss(x, wg, wu):
+        a, _ = plain.activation(x @ wg.T, act)
+        return (a * (x @ wu.T) * dh).sum()
+
+    a, da = plain.activation(t[0] @ t[1].T, act)
+    u = t[0] @ t[2].T
+    dg, du = dh * u * da, dh * a
+    grads = [dg @ t[1] + du @ t[2], dg.T @ t[0], du.T @ t[0]]
+    for i in range(3):
+        v = torch.randn(t[i].shape, generator=gen, dtype=torch.float64)
+        h = 1e-5
+        plus, minus = ([w + s * h * v if k == i else w for k, w in enumerate(t)] for s in (1, -1))
+        d = (loss(*plus) - loss(*minus)) / (2 * h)
+        assert abs(float(d - (grads[i] * v).sum())) <= 1e-7 * max(1.0, abs(float(d)))
+
+
+def test_plain_newton_schulz_acts_on_singular_values():
+    g = torch.randn(12, 20, generator=torch.Generator().manual_seed(3), dtype=torch.float64)
+    u, s, vt = torch.linalg.svd(g, full_matrices=False)
+    s = s / (s.norm() + 1e-7)
+    for _ in range(5):
+        s = 3.4445 * s - 4.7750 * s ** 3 + 2.0315 * s ** 5
+    want = u @ torch.diag(s) @ vt
+    assert (plain.newton_schulz(g) - want).abs().max() < 1e-9
+    assert (plain.newton_schulz(g.T) - want.T).abs().max() < 1e-9
+
+
+def test_plain_packing_round_trips():
+    c = torch.randint(0, 16, (3, 64), generator=torch.Generator().manual_seed(1))
+    assert torch.equal(plain.unpack(plain.pack(c)), c.double())
