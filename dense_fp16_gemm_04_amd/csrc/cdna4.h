@@ -81,10 +81,11 @@ __device__ __forceinline__ int swizzle(int row, int chunk) { return chunk ^ ((ro
 
 // Workgroup (or persistent tile) number -> tile.  Workgroups are dealt to
 // the XCDs in turn, so numbers are first renamed to give each XCD one
-// contiguous range; that range is swept in groups of `group_m` tile rows,
-// column by column, so tiles that run together share rows of both operands.
-__device__ __forceinline__ void tile_of(int id, int tiles_m, int tiles_n, int group_m, int& tm, int& tn)
+// contiguous range; that range is swept in groups of eight tile rows, column
+// by column, so tiles that run together share rows of both operands.
+__device__ __forceinline__ void tile_of(int id, int tiles_m, int tiles_n, int& tm, int& tn)
 {
+    constexpr int group_m = 8;
     const int total = tiles_m * tiles_n;
     const int per = total / kXcds, extra = total % kXcds;
     const int x = id % kXcds;

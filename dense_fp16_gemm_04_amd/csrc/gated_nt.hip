@@ -16,7 +16,7 @@
 #include <algorithm>
 
 #include "abi.h"
-#include "nt_core.h"
+#include "nt_launch.h"
 #include "relayout.h"
 
 namespace {
@@ -54,19 +54,20 @@ __device__ __forceinline__ float act_slope(const Activation& c, float g, float s
 // 128-byte line.
 __host__ __device__ __forceinline__ int64_t saved_pitch(int64_t F) { return (F + 3) / 4 * 8; }
 
-template <class E, bool SAVE>
+template <class E, bool SAVE, bool WHOLE>
 struct GatedOp {
+    static constexpr bool kPersist = true;
     const E *X, *Wg, *Wu;
     E* H;
     float* saved;
-    int M, F, K, lda, ldg, ldu, ldh, tiles_m, tiles_n, group_m, vec;
+    int M, F, K, lda, ldg, ldu, ldh, tiles, tiles_m, tiles_n;
     Activation act;
 
     template <int BM, int BN>
     __device__ __forceinline__ bool tile(int id, Tile& t) const
     {
         int tm, tn;
-        tile_of(id, tiles_m, tiles_n, group_m, tm, tn);
+        tile_of(id, tiles_m, tiles_n, tm, tn);
         t.m0 = tm * BM;
         t.n0 = tn * (BN / 2);
         t.batch = 0;
@@ -86,36 +87,66 @@ struct GatedOp {
         return rows_from(q & 1 ? Wu : Wg, t.n0 + (q >> 1) * (BN / 4), F, q & 1 ? ldu : ldg, n);
     }
     __device__ __forceinline__ int b_pitch(int q) const { return q & 1 ? ldu : ldg; }
+    // Where a tile's rows of H and of `saved` lie.
+    struct Out {
+        __amdgpu_buffer_rsrc_t h, s;
+        uint32_t pitch_h, pitch_s;
+    };
+    __device__ __forceinline__ Out out_rows(int m0, int rows) const
+    {
+        Out o;
+        o.pitch_h = (uint32_t)ldh * 2u;
+        o.pitch_s = (uint32_t)saved_pitch(F) * 4u;
+        const uint32_t n = (uint32_t)min(rows, M - m0);
+        o.h = make_rsrc(H + (int64_t)m0 * ldh, n * o.pitch_h);
+        if constexpr (SAVE) o.s = make_rsrc(saved + m0 * saved_pitch(F), n * o.pitch_s);
+        return o;
+    }
+    // Columns f .. f + 3 of the tile's row r from g and u.
+    __device__ __forceinline__ void finish(const Out& o, int r, int f, const f32x4& g4, const f32x4& u4) const
+    {
+        f32x4 h, p, q;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const float g = g4[e], u = u4[e];
+            float s;
+            q[e] = act_value(act, g, s);
+            h[e] = q[e] * u;
+            if constexpr (SAVE) p[e] = u * act_slope(act, g, s);
+        }
+        buffer_store4<E, WHOLE>(o.h, (uint32_t)r * o.pitch_h + (uint32_t)f * 2u, f, F, h);
+        if constexpr (SAVE) {
+            const uint32_t at = f < F ? (uint32_t)r * o.pitch_s + (uint32_t)f * 8u : kOob;
+            __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, p), o.s, at, 0, 0);
+            __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, q), o.s, at, 16, 0);
+        }
+    }
     template <class T>
     __device__ __forceinline__ void epilogue(const Tile& t, const Acc<T>& acc, int lane, int wm, int wn,
                                              unsigned char*) const
     {
         constexpr int HF = T::FN / 2;
+        const Out o = out_rows(t.m0, T::BM);
 #pragma unroll
-        for (int i = 0; i < T::FM; ++i) {
-            const int m = t.m0 + wm * T::WTM + i * 16 + (lane & 15);
-            if (m >= M) continue;
+        for (int i = 0; i < T::FM; ++i)
 #pragma unroll
-            for (int j = 0; j < HF; ++j) {
-                const int f = t.n0 + wn * (T::WTN / 2) + j * 16 + 4 * (lane >> 4);
-                f32x4 h, p, q;
+            for (int j = 0; j < HF; ++j)
+                finish(o, wm * T::WTM + i * 16 + (lane & 15), t.n0 + wn * (T::WTN / 2) + j * 16 + 4 * (lane >> 4),
+                       acc[i][j], acc[i][j + HF]);
+    }
+    template <class T>
+    __device__ __forceinline__ void epilogue256(const Tile& t, const f32x4 (&acc)[8][8], int lane, int wave,
+                                                unsigned char*, unsigned char*) const
+    {
+        const Out o = out_rows(t.m0, 256);
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const float g = acc[i][j][e], u = acc[i][j + HF][e];
-                    float s;
-                    q[e] = act_value(act, g, s);
-                    h[e] = q[e] * u;
-                    if constexpr (SAVE) p[e] = u * act_slope(act, g, s);
-                }
-                store4<E>(H + (int64_t)m * ldh, f, F, h, vec);
-                if constexpr (SAVE)
-                    if (f < F) {
-                        float* at = saved + m * saved_pitch(F) + f * 2;
-                        *(f32x4*)at = p;
-                        *(f32x4*)(at + 4) = q;
-                    }
+        for (int i = 0; i < 8; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int ln = pinned(lane);
+                finish(o, (wave >> 1) * 128 + i * 16 + (ln & 15), t.n0 + (wave & 1) * 64 + j * 16 + 4 * (ln >> 4),
+                       acc[i][j], acc[i][j + 4]);
             }
-        }
     }
 };
 
@@ -166,33 +197,10 @@ gated_slopes(const E* __restrict__ dH, const float* __restrict__ saved, E* __res
 
 // ------------------------------------------------------------------ host --
 
-template <class E>
-using Tile128 = Shape<E, 128, 128, 3, 1>;
-template <class E>
-using Tile64 = Shape<E, 64, 64, 3, 2>;
-
 bool vec4(const void* p, int64_t ld) { return (uintptr_t)p % 8 == 0 && ld % 4 == 0; }
+// a result's rows take four columns at a time
+bool whole_rows(const void* p, int64_t cols, int64_t ld) { return vec4(p, ld) && cols % 4 == 0; }
 bool vec8(const void* p, int64_t ld) { return (uintptr_t)p % 16 == 0 && ld % 8 == 0; }
-
-template <class T, class OP>
-int launch_tiles(OP op, int64_t rows, int64_t cols, int bn, int batch, hipStream_t stream)
-{
-    const int64_t tm = (rows + T::BM - 1) / T::BM, tn = (cols + bn - 1) / bn;
-    if (tm * tn * batch > abi::kMaxDim) return hipErrorInvalidValue;
-    op.tiles_m = (int)tm;
-    op.tiles_n = (int)tn;
-    op.group_m = 8;
-    hipLaunchKernelGGL((nt_tile<T, OP>), dim3((unsigned)(tm * tn * batch)), dim3(T::THREADS), 0, stream, op);
-    return (int)hipGetLastError();
-}
-
-template <class E, class OP>
-int launch_product(const OP& op, int64_t rows, int64_t cols, int split, int batch, hipStream_t stream)
-{
-    const int64_t big = ((rows + 127) / 128) * ((cols * split + 127) / 128) * batch;
-    if (big >= 128) return launch_tiles<Tile128<E>>(op, rows, cols, 128 / split, batch, stream);
-    return launch_tiles<Tile64<E>>(op, rows, cols, 64 / split, batch, stream);
-}
 
 template <class E>
 int launch_copy(const E* src, int64_t ld, E* dst, int64_t ldd, int64_t rows, int64_t cols, hipStream_t stream)
@@ -214,6 +222,23 @@ int launch_transpose(const E* src, int64_t ld, E* dst, int64_t ldd, int64_t rows
     hipLaunchKernelGGL(relayout::transpose<E>, dim3((unsigned)(tr * tc)), dim3(256), 0, stream, src, ld, dst, ldd,
                        (int)rows, (int)cols, (int)padded, (int)tc, (int)vec4(src, ld));
     return (int)hipGetLastError();
+}
+
+// C [M, N] = A B^T, both operands with K elements to a row.
+template <class E>
+int product(const E* A, const E* B, E* C, int64_t M, int64_t N, int64_t K, int64_t ldc, hipStream_t stream)
+{
+    auto with = [&](auto op) {
+        op.A = A;
+        op.B = B;
+        op.C = C;
+        op.M = (int)M;
+        op.N = (int)N;
+        op.K = op.lda = op.ldb = (int)K;
+        op.ldc = (int)ldc;
+        return launch_grid<E>(op, M, N, 1, 1, K, stream);
+    };
+    return whole_rows(C, N, ldc) ? with(StoreOp<E, true>{}) : with(StoreOp<E, false>{});
 }
 
 // Copies of the operands that the kernels cannot read in place.
@@ -269,14 +294,14 @@ bool good_sizes(int64_t T, int64_t D, int64_t F)
            T <= abi::kMaxDim - 256;
 }
 
-template <class E, bool SAVE>
+template <class E, bool SAVE, bool WHOLE>
 int forward(const E* X, const E* Wg, const E* Wu, E* H, float* saved, int64_t T, int64_t D, int64_t F, int64_t ldx,
             int64_t ldg, int64_t ldu, int64_t ldh, int32_t activation, void* workspace, hipStream_t stream)
 {
     const ForwardSpace<E> w(workspace, X, Wg, Wu, T, D, F, ldx, ldg, ldu);
     const int64_t Dp = abi::up(D, 8);
     int rc = hipSuccess;
-    GatedOp<E, SAVE> op = {};
+    GatedOp<E, SAVE, WHOLE> op = {};
     op.X = X;
     op.Wg = Wg;
     op.Wu = Wu;
@@ -304,9 +329,8 @@ int forward(const E* X, const E* Wg, const E* Wu, E* H, float* saved, int64_t T,
     op.M = (int)T;
     op.F = (int)F;
     op.ldh = (int)ldh;
-    op.vec = vec4(H, ldh);
     op.act = activation_of(activation);
-    return launch_product<E>(op, T, F, 2, 1, stream);
+    return launch_grid<E>(op, T, F, 2, 1, Dp, stream);
 }
 
 template <class E>
@@ -327,31 +351,12 @@ int backward(const E* dH, const E* X, const E* Wg, const E* Wu, const float* sav
         // [Wg; Wu]^T, D x 2 Fp, zeros between the two
         if ((rc = launch_transpose(Wg, ldg, w.wt, 2 * w.Fp, F, D, w.Fp, stream))) return rc;
         if ((rc = launch_transpose(Wu, ldu, w.wt + w.Fp, 2 * w.Fp, F, D, w.Fp, stream))) return rc;
-        StoreOp<E> op = {};
-        op.A = w.dgu;
-        op.B = w.wt;
-        op.C[0] = dX;
-        op.M = (int)T;
-        op.N = (int)D;
-        op.K = op.lda = op.ldb = (int)(2 * w.Fp);
-        op.ldc = (int)lddx;
-        op.vec = vec4(dX, lddx);
-        if ((rc = launch_product<E>(op, T, D, 1, 1, stream))) return rc;
+        if ((rc = product(w.dgu, w.wt, dX, T, D, 2 * w.Fp, lddx, stream))) return rc;
     }
     if (F > 0 && D > 0) {
         if ((rc = launch_transpose(X, ldx, w.xt, w.Tp, T, D, w.Tp, stream))) return rc;
-        for (int i = 0; i < 2; ++i) {
-            StoreOp<E> op = {};
-            op.A = i ? w.dut : w.dgt;
-            op.B = w.xt;
-            op.C[0] = i ? dWu : dWg;
-            op.M = (int)F;
-            op.N = (int)D;
-            op.K = op.lda = op.ldb = (int)w.Tp;
-            op.ldc = (int)(i ? lddu : lddg);
-            op.vec = vec4(op.C[0], op.ldc);
-            if ((rc = launch_product<E>(op, F, D, 1, 1, stream))) return rc;
-        }
+        if ((rc = product(w.dgt, w.xt, dWg, F, D, w.Tp, lddg, stream))) return rc;
+        if ((rc = product(w.dut, w.xt, dWu, F, D, w.Tp, lddu, stream))) return rc;
     }
     return hipSuccess;
 }
@@ -403,11 +408,14 @@ int gated_nt(const void* X, const void* Wg, const void* Wu, void* H, void* saved
     for (const Range& r : in)
         if (h.meets(r) || s.meets(r) || w.meets(r)) return hipErrorInvalidValue;
     if (h.meets(s) || h.meets(w) || s.meets(w)) return hipErrorInvalidValue;
-#define FORWARD(E, SAVE)                                                                                         \
-    forward<E, SAVE>((const E*)X, (const E*)Wg, (const E*)Wu, (E*)H, (float*)saved, T, D, F, ldx, ldg, ldu, ldh, \
-                     activation, workspace, stream)
-    if (type == GATED_NT_F16) return saved ? FORWARD(_Float16, true) : FORWARD(_Float16, false);
-    return saved ? FORWARD(__bf16, true) : FORWARD(__bf16, false);
+#define FORWARD(E, SAVE, WHOLE)                                                                                 \
+    forward<E, SAVE, WHOLE>((const E*)X, (const E*)Wg, (const E*)Wu, (E*)H, (float*)saved, T, D, F, ldx, ldg, ldu, \
+                            ldh, activation, workspace, stream)
+#define FORWARD_OF(E)                                                                  \
+    (whole_rows(H, F, ldh) ? (saved ? FORWARD(E, true, true) : FORWARD(E, false, true)) \
+                           : (saved ? FORWARD(E, true, false) : FORWARD(E, false, false)))
+    return type == GATED_NT_F16 ? FORWARD_OF(_Float16) : FORWARD_OF(__bf16);
+#undef FORWARD_OF
 #undef FORWARD
 }
 

@@ -155,43 +155,364 @@ __global__ void __launch_bounds__(T::THREADS, T::OCC) nt_tile(const OP op)
     op.template epilogue<T>(t, acc, lane, wm, wn, smem);
 }
 
-// Stores four consecutive columns of one row: n .. n + 3 of N, as one 8-byte
-// piece where `vec` says that rows take it.
-template <class E>
-__device__ __forceinline__ void store4(E* row, int n, int N, const f32x4& v, bool vec)
+// One 256 x 256 tile after another per workgroup, one workgroup per CU, four
+// waves, one per SIMD, each holding a 128 x 128 quarter of the tile in its
+// 256 AGPRs.  LDS is a ring of five 32 KiB slots of one operand tile each
+// (A of step j in slot 2j mod 5, B in slot 2j + 1 mod 5), and the load
+// stream runs on across tiles: a tile's last two steps load the first two of
+// the next.  Every MFMA is an asm statement, so the source order is the issue
+// order: a fragment read of the next sub-step after every third MFMA, a
+// global->LDS load after every eighth, one barrier a step.
+//
+// With one wave per SIMD nothing hides scalar or vector arithmetic between
+// two MFMAs.  The steps that load whole K ranges therefore run as a cycle of
+// five, one per position of the ring, in which every slot is a constant of
+// the code, every LDS address a register and an immediate, and the K
+// position one scalar register; the others (K's tail, the two that start the
+// next tile, up to four before and after the cycles) keep the ring position
+// in a register.
+//
+// OP as for nt_tile, with `int tiles` (their number) and the epilogue
+//   epilogue256<T>(t, acc, lane, wave, s0, s1)
+// s0 and s1 are the slots that no load is writing (the same in every wave); a
+// barrier follows.  Nothing clears the accumulators: a tile's first MFMAs add
+// to an inline zero.
+//
+// Needs three steps at least: K > 128.
+template <class E_>
+struct Shape256 {
+    using E = E_;
+    using x8 = typename Elem<E>::x8;
+    static constexpr int BM = 256, BN = 256, BK = 64, THREADS = 256;
+    static constexpr int WTM = 128, WTN = 128, FM = 8, FN = 8;
+    static constexpr int ROW_BYTES = 128;
+    static constexpr int SLOT = 32768;
+    static constexpr int RS = 3, LS = 8;  // MFMAs per fragment read, per load
+};
+
+template <bool B>
+struct Flag {
+    static constexpr bool value = B;
+};
+template <int V>
+struct Int {
+    static constexpr int value = V;
+};
+
+// acc += b * a with the accumulator in AGPRs; the memory clobber keeps every
+// LDS and global access on its side.
+__device__ __forceinline__ void mfma_agpr(f32x4& acc, const Elem<_Float16>::x8& b, const Elem<_Float16>::x8& a)
+{
+    asm volatile("v_mfma_f32_16x16x32_f16 %0, %1, %2, %0" : "+a"(acc) : "v"(b), "v"(a) : "memory");
+}
+__device__ __forceinline__ void mfma_agpr(f32x4& acc, const Elem<__bf16>::x8& b, const Elem<__bf16>::x8& a)
+{
+    asm volatile("v_mfma_f32_16x16x32_bf16 %0, %1, %2, %0" : "+a"(acc) : "v"(b), "v"(a) : "memory");
+}
+
+// The same with nothing to add to.  (The old value is an operand only to keep
+// the accumulator in its registers: as a plain output it made the register
+// allocator spill.)
+__device__ __forceinline__ void mfma_agpr_first(f32x4& acc, const Elem<_Float16>::x8& b, const Elem<_Float16>::x8& a)
+{
+    asm volatile("v_mfma_f32_16x16x32_f16 %0, %1, %2, 0" : "+a"(acc) : "v"(b), "v"(a) : "memory");
+}
+__device__ __forceinline__ void mfma_agpr_first(f32x4& acc, const Elem<__bf16>::x8& b, const Elem<__bf16>::x8& a)
+{
+    asm volatile("v_mfma_f32_16x16x32_bf16 %0, %1, %2, 0" : "+a"(acc) : "v"(b), "v"(a) : "memory");
+}
+
+template <class T, class OP>
+__global__ void __launch_bounds__(T::THREADS, 1) nt_persist(const OP op)
+{
+    using x8 = typename T::x8;
+    constexpr int SLOT = T::SLOT, G = 64, R = 16;  // MFMAs and fragment reads per sub-step
+    __shared__ __attribute__((aligned(1024))) unsigned char smem[5 * SLOT];
+
+    const int lane = threadIdx.x & (kWave - 1);
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+    const int wm = wave >> 1, wn = wave & 1;
+    const int K = op.K;
+    const int nk = (K + T::BK - 1) / T::BK;
+    const int nfull = K / T::BK;  // steps wholly inside K
+    const uint32_t pitch_a = (uint32_t)op.lda * 2u, pitch_b = (uint32_t)op.b_pitch(wave) * 2u;
+
+    // Load l of a wave fills rows 8 l .. + 7 of its quarter of an operand's
+    // tile, KiB wave * 8 + l of the slot.  Loads of a group of four share the
+    // LDS base (M0); the instruction offset (l & 3) KiB places them, and as
+    // the hardware adds it to the global offset too, the VGPR offset gives it
+    // back (no wrap: row 8 l starts at 8 l * pitch >= l KiB, the pitch being
+    // at least 128 bytes).
+    const int lr = lane >> 3, lp = lane & 7;
+    const int c01[2] = {swizzle(lr, lp), swizzle(8 + lr, lp)};
+    uint32_t va[8], vb[8];
+#pragma unroll
+    for (int l = 0; l < 8; ++l) {
+        const uint32_t c = (uint32_t)c01[l & 1] * 16u - (uint32_t)(l & 3) * 1024u;
+        va[l] = (uint32_t)(l * 8 + lr) * pitch_a + c;
+        vb[l] = (uint32_t)(l * 8 + lr) * pitch_b + c;
+        asm volatile("" : "+v"(va[l]), "+v"(vb[l]));
+    }
+    int wave_bytes = __builtin_amdgcn_readfirstlane(wave * 8192);
+
+    // The tile being loaded runs up to one ahead of the one being computed.
+    int id = blockIdx.x;
+    if (id >= op.tiles) return;
+    Tile t;
+    op.template tile<T::BM, T::BN>(id, t);
+    __amdgpu_buffer_rsrc_t la, lb;
+    auto operands = [&]() __attribute__((always_inline)) {
+        int na = 0, nb = 0;
+        const void* pa = op.a_rows(t, wave * 64, na);
+        const void* pb = op.template b_rows<T::BN>(t, wave * 64, nb);
+        la = make_rsrc(pa, (uint32_t)min(na, 64) * pitch_a);
+        lb = make_rsrc(pb, (uint32_t)min(nb, 64) * pitch_b);
+    };
+    operands();
+
+    auto load = [&](unsigned char* dst, int l, uint32_t off, uint32_t soff) __attribute__((always_inline)) {
+        lds_void* d = (lds_void*)(dst + (l & 4) * 1024);
+        // (the instruction offset must be a constant, and a buffer resource
+        // cannot be the result of ?:)
+#define NT_LOAD(RS)                                                                                  \
+    switch (l & 3) {                                                                                 \
+        case 0: __builtin_amdgcn_raw_ptr_buffer_load_lds(RS, d, 16, off, soff, 0, 0); break;         \
+        case 1: __builtin_amdgcn_raw_ptr_buffer_load_lds(RS, d, 16, off, soff, 1024, 0); break;      \
+        case 2: __builtin_amdgcn_raw_ptr_buffer_load_lds(RS, d, 16, off, soff, 2048, 0); break;      \
+        default: __builtin_amdgcn_raw_ptr_buffer_load_lds(RS, d, 16, off, soff, 1024 * 3, 0); break; \
+    }
+        if (l < 8) {
+            NT_LOAD(la)
+        } else {
+            NT_LOAD(lb)
+        }
+#undef NT_LOAD
+    };
+    // Load l (0 .. 7 of A, 8 .. 15 of B) of step ks of the loading tile into
+    // slot `where`; chunks at or past K read as zero.  The K position is part
+    // of the vector offset: past the end it may exceed the buffer.
+    auto load_any = [&](int where, int ks, int l) __attribute__((always_inline)) {
+        const uint32_t v = l < 8 ? va[l & 7] : vb[l & 7];
+        const uint32_t koff = (uint32_t)ks * (T::BK * 2);
+        // (the mark less the instruction offset, so that the sum stays out of range)
+        const uint32_t off = c01[l & 1] * 8 < K - ks * T::BK ? v + koff : kOob;
+        load(smem + where * SLOT + wave_bytes, l, off, 0);
+    };
+
+    const int fr = lane & 15, fh = lane >> 4;
+    const int pos[2] = {swizzle(fr, fh) * 16, swizzle(fr, 4 + fh) * 16};
+    const int arow = (wm * T::WTM + fr) * T::ROW_BYTES, brow = (wn * T::WTN + fr) * T::ROW_BYTES;
+    // LDS address of operand x's fragment rows at k-half kk, plus c * 64 KiB:
+    // slots 2c and 2c + 1 lie within an immediate's reach of it.
+    uint32_t rdb[3][2][2];
+#pragma unroll
+    for (int c = 0; c < 3; ++c)
+#pragma unroll
+        for (int kk = 0; kk < 2; ++kk) {
+            rdb[c][0][kk] = (uint32_t)(c * 65536 + arow + pos[kk]);
+            rdb[c][1][kk] = (uint32_t)(c * 65536 + brow + pos[kk]);
+        }
+
+    x8 fa[2][T::FM], fb[2][T::FN];
+    f32x4 acc[T::FM][T::FN];
+
+    // Fragment read idx of set `set`: B's blocks, then A's from the last to
+    // the first, the order in which the other set's MFMAs last used them.
+    auto read_any = [&](int set, const unsigned char* abase, const unsigned char* bbase, int idx)
+                        __attribute__((always_inline)) {
+        if (idx < 8)
+            fb[set][idx] = *(const x8*)(bbase + brow + pos[set] + idx * 16 * T::ROW_BYTES);
+        else
+            fa[set][15 - idx] = *(const x8*)(abase + arow + pos[set] + (15 - idx) * 16 * T::ROW_BYTES);
+    };
+    auto read_fast = [&](auto sa_c, auto sb_c, int set, int idx) __attribute__((always_inline)) {
+        constexpr int SA = decltype(sa_c)::value, SB = decltype(sb_c)::value;
+        if (idx < 8)
+            fb[set][idx] = *(const x8*)(smem + rdb[SB / 2][1][set] + (SB % 2) * SLOT + idx * 16 * T::ROW_BYTES);
+        else
+            fa[set][15 - idx] =
+                *(const x8*)(smem + rdb[SA / 2][0][set] + (SA % 2) * SLOT + (15 - idx) * 16 * T::ROW_BYTES);
+    };
+    // MFMA number n of a sub-step: down the columns of blocks and back up
+    // every second one, so that neighbours share a fragment.
+    auto mma = [&](int set, int n, auto first) __attribute__((always_inline)) {
+        const int j = n / 8, i = (j & 1) ? 7 - n % 8 : n % 8;
+        if constexpr (decltype(first)::value)
+            mfma_agpr_first(acc[i][j], fb[set][j], fa[set][i]);
+        else
+            mfma_agpr(acc[i][j], fb[set][j], fa[set][i]);
+    };
+    auto substep = [&](int set, const unsigned char* abase, const unsigned char* bbase, auto ld, auto rd, int where,
+                       int lstep, int l0, auto first) __attribute__((always_inline)) {
+#pragma unroll
+        for (int n = 0; n < G; ++n) {
+            mma(set, n, first);
+            if constexpr (decltype(rd)::value)
+                if (n % T::RS == 0 && n / T::RS < R) read_any(1 - set, abase, bbase, n / T::RS);
+            if constexpr (decltype(ld)::value)
+                if (n % T::LS == T::LS / 2) load_any(where, lstep, l0 + n / T::LS);
+        }
+    };
+    auto substep_fast = [&](int set, auto ra, auto rb, auto where_c, int l0, uint32_t soff)
+                            __attribute__((always_inline)) {
+        constexpr int WHERE = decltype(where_c)::value;
+#pragma unroll
+        for (int n = 0; n < G; ++n) {
+            mma(set, n, Flag<false>{});
+            if (n % T::RS == 0 && n / T::RS < R) read_fast(ra, rb, 1 - set, n / T::RS);
+            if (n % T::LS == T::LS / 2) {
+                const int l = l0 + n / T::LS;
+                load(smem + WHERE * SLOT + wave_bytes, l, l < 8 ? va[l & 7] : vb[l & 7], soff);
+            }
+        }
+    };
+    // A step with its A tile in slot S that loads K bytes soff .. + 127.  The
+    // base registers are redefined in place, by no instruction, so that base
+    // plus offset is not hoisted into registers of its own.
+    auto step_fast = [&](auto s_c, uint32_t soff) __attribute__((always_inline)) {
+        constexpr int S = decltype(s_c)::value;
+#pragma unroll
+        for (int c = 0; c < 3; ++c)
+#pragma unroll
+            for (int kk = 0; kk < 2; ++kk) asm volatile("" : "+v"(rdb[c][0][kk]), "+v"(rdb[c][1][kk]));
+        asm volatile("" : "+s"(wave_bytes));
+        substep_fast(0, Int<S>{}, Int<(S + 1) % 5>{}, Int<(S + 4) % 5>{}, 0, soff);
+        lds_barrier<8>();
+        substep_fast(1, Int<(S + 2) % 5>{}, Int<(S + 3) % 5>{}, Int<S>{}, 8, soff);
+    };
+
+#pragma unroll
+    for (int i = 0; i < T::FM; ++i)
+#pragma unroll
+        for (int j = 0; j < T::FN; ++j) asm volatile("" : "=a"(acc[i][j]));  // (any value)
+    // steps 0 and 1 of the first tile into slots 0 .. 3, then wait for step 0
+#pragma unroll
+    for (int s = 0; s < 2; ++s)
+#pragma unroll
+        for (int l = 0; l < 16; ++l) load_any(l < 8 ? 2 * s : 2 * s + 1, s, l);
+    lds_barrier<16>();
+#pragma unroll
+    for (int idx = 0; idx < R; ++idx) read_any(0, smem, smem + SLOT, idx);
+    int sa = 0;  // slot of the computed step's A tile; its B, then A, B, A of the next two follow
+    auto slot = [&](int i) __attribute__((always_inline)) { return smem + (sa + i >= 5 ? sa + i - 5 : sa + i) * SLOT; };
+    // Sub-step 0 loads A of step lstep into the slot after the next step's;
+    // sub-step 1 reads the next step's first fragments and loads its B into
+    // the slot this step's A leaves, unless LAST (the last of a tile, whose
+    // epilogue may use both slots first).
+    auto step = [&](int lstep, auto last, auto first) __attribute__((always_inline)) {
+        constexpr bool LAST = decltype(last)::value;
+        const int a2 = sa + 4 >= 5 ? sa - 1 : sa + 4;
+        substep(0, slot(0), slot(1), Flag<true>{}, Flag<true>{}, a2, lstep, 0, first);
+        lds_barrier<8>();  // all but the A tile just loaded have landed
+        substep(1, slot(2), slot(3), Flag<!LAST>{}, Flag<!LAST>{}, sa, lstep, 8, Flag<false>{});
+    };
+    auto advance = [&]() __attribute__((always_inline)) { sa = sa + 2 >= 5 ? sa - 3 : sa + 2; };
+    for (;;) {
+        step(2, Flag<false>{}, Flag<true>{});
+        advance();
+        int ks = 1;
+        // general steps until the ring is back at slot 0, then whole cycles
+        for (; ks + 2 < nfull && sa != 0; ++ks) {
+            step(ks + 2, Flag<false>{}, Flag<false>{});
+            advance();
+        }
+        uint32_t soff = (uint32_t)(ks + 2) * T::ROW_BYTES;
+        for (; ks + 2 + 5 <= nfull; ks += 5) {
+            step_fast(Int<0>{}, soff);
+            step_fast(Int<2>{}, soff + T::ROW_BYTES);
+            step_fast(Int<4>{}, soff + 2 * T::ROW_BYTES);
+            step_fast(Int<1>{}, soff + 3 * T::ROW_BYTES);
+            step_fast(Int<3>{}, soff + 4 * T::ROW_BYTES);
+            soff += 5 * T::ROW_BYTES;
+        }
+        for (; ks + 2 < nk; ++ks) {
+            step(ks + 2, Flag<false>{}, Flag<false>{});
+            advance();
+        }
+        // The last two steps load steps 0 and 1 of the next tile (after the
+        // last one: zeros from past the end of K, into slots never read).
+        const Tile done = t;
+        const int next = id + (int)gridDim.x;
+        int lbase = nk;
+        if (next < op.tiles) {
+            op.template tile<T::BM, T::BN>(next, t);
+            operands();
+            lbase = 0;
+        }
+        step(lbase, Flag<false>{}, Flag<false>{});
+        advance();
+        step(lbase + 1, Flag<true>{}, Flag<false>{});
+        // the last MFMAs write their accumulators before they are read: asm
+        // hides them from the compiler's hazard checks
+        asm volatile("s_nop 7\n\ts_nop 7\n\ts_nop 7" ::: "memory");
+        __builtin_amdgcn_sched_barrier(0);
+        op.template epilogue256<T>(done, acc, lane, wave, slot(0), slot(1));
+        if (next >= op.tiles) break;
+        // every wave is done with this step's slots
+        lds_barrier<63>();
+        // B of the next tile's step 1 where the last step's A was
+#pragma unroll
+        for (int l = 8; l < 16; ++l) load_any(sa, lbase + 1, l);
+        advance();
+#pragma unroll
+        for (int idx = 0; idx < R; ++idx) read_any(0, slot(0), slot(1), idx);
+        id = next;
+    }
+    // no load may still be writing LDS when the workgroup ends
+    lds_barrier<0>();
+}
+
+// The lane, as if newly read: addresses derived from it are computed where
+// they are used, not early and kept (or spilled) through the K loop.
+__device__ __forceinline__ int pinned(int lane)
+{
+    asm volatile("" : "+v"(lane)::"memory");
+    return lane;
+}
+
+// Stores four consecutive columns of one row through a buffer, without a
+// branch: `at` is the byte offset of row and first column, past the buffer
+// for rows that do not exist.  WHOLE: rows take 8-byte pieces and N is a
+// multiple of 4; otherwise each element goes out alone.  (A template, not a
+// condition: with two ways through an epilogue that holds 256 accumulators
+// the register allocator spills.)
+template <class E, bool WHOLE>
+__device__ __forceinline__ void buffer_store4(__amdgpu_buffer_rsrc_t rs, uint32_t at, int n, int N, const f32x4& v)
 {
     const typename Elem<E>::x4 h = round4<E>(v);
-    if (vec && n + 3 < N) {
-        *(typename Elem<E>::x4*)(row + n) = h;
+    if constexpr (WHOLE) {
+        __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(u32x2, h), rs, n < N ? at : kOob, 0, 0);
     } else {
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-            if (n + e < N) row[n + e] = h[e];
+        for (int e = 0; e < 4; ++e) {
+            const E one = h[e];
+            __builtin_amdgcn_raw_buffer_store_b16(__builtin_bit_cast(uint16_t, one), rs,
+                                                  n + e < N ? at + (uint32_t)e * 2u : kOob, 0, 0);
+        }
     }
 }
 
-// C = A B^T, `batch` products of one shape.
-template <class E>
+// C = A B^T.
+template <class E, bool WHOLE>
 struct StoreOp {
+    static constexpr bool kPersist = true;
     const E *A, *B;
-    E* C[2];  // batch 0 and 1
-    int M, N, K, lda, ldb, ldc, tiles_m, tiles_n, group_m, vec;
-    int64_t stride_a;  // A of batch 1 (B is shared)
+    E* C;
+    int M, N, K, lda, ldb, ldc, tiles, tiles_m, tiles_n;
 
     template <int BM, int BN>
     __device__ __forceinline__ bool tile(int id, Tile& t) const
     {
-        const int per = tiles_m * tiles_n;
-        t.batch = id / per;
         int tm, tn;
-        tile_of(id - t.batch * per, tiles_m, tiles_n, group_m, tm, tn);
+        tile_of(id, tiles_m, tiles_n, tm, tn);
+        t.batch = 0;
         t.m0 = tm * BM;
         t.n0 = tn * BN;
         return true;
     }
     __device__ __forceinline__ const E* a_rows(const Tile& t, int row, int& n) const
     {
-        return rows_from(A + t.batch * stride_a, t.m0 + row, M, lda, n);
+        return rows_from(A, t.m0 + row, M, lda, n);
     }
     template <int BN>
     __device__ __forceinline__ const E* b_rows(const Tile& t, int row, int& n) const
@@ -199,18 +520,38 @@ struct StoreOp {
         return rows_from(B, t.n0 + row, N, ldb, n);
     }
     __device__ __forceinline__ int b_pitch(int) const { return ldb; }
+    __device__ __forceinline__ void finish(__amdgpu_buffer_rsrc_t out, int r, int n, const f32x4& v) const
+    {
+        buffer_store4<E, WHOLE>(out, ((uint32_t)r * (uint32_t)ldc + (uint32_t)n) * 2u, n, N, v);
+    }
+    __device__ __forceinline__ __amdgpu_buffer_rsrc_t out_rows(int m0, int rows) const
+    {
+        return make_rsrc(C + (int64_t)m0 * ldc, (uint32_t)min(rows, M - m0) * (uint32_t)ldc * 2u);
+    }
     template <class T>
     __device__ __forceinline__ void epilogue(const Tile& t, const Acc<T>& acc, int lane, int wm, int wn,
                                              unsigned char*) const
     {
-        E* out = t.batch ? C[1] : C[0];
+        const __amdgpu_buffer_rsrc_t out = out_rows(t.m0, T::BM);
 #pragma unroll
-        for (int i = 0; i < T::FM; ++i) {
-            const int m = t.m0 + wm * T::WTM + i * 16 + (lane & 15);
-            if (m >= M) continue;
+        for (int i = 0; i < T::FM; ++i)
 #pragma unroll
             for (int j = 0; j < T::FN; ++j)
-                store4<E>(out + (int64_t)m * ldc, t.n0 + wn * T::WTN + j * 16 + 4 * (lane >> 4), N, acc[i][j], vec);
+                finish(out, wm * T::WTM + i * 16 + (lane & 15), t.n0 + wn * T::WTN + j * 16 + 4 * (lane >> 4),
+                       acc[i][j]);
+    }
+    template <class T>
+    __device__ __forceinline__ void epilogue256(const Tile& t, const f32x4 (&acc)[8][8], int lane, int wave,
+                                                unsigned char*, unsigned char*) const
+    {
+        const __amdgpu_buffer_rsrc_t out = out_rows(t.m0, 256);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int ln = pinned(lane);
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                finish(out, (wave >> 1) * 128 + i * 16 + (ln & 15), t.n0 + (wave & 1) * 128 + j * 16 + 4 * (ln >> 4),
+                       acc[i][j]);
         }
     }
 };

@@ -15,7 +15,7 @@
 #include <cmath>
 
 #include "abi.h"
-#include "nt_core.h"
+#include "nt_launch.h"
 #include "relayout.h"
 
 namespace {
@@ -102,14 +102,106 @@ __global__ void __launch_bounds__(256) ns_copy_out(const half* __restrict__ X, i
     }
 }
 
+// Where a tile goes: rows of a matrix from the tile's first one on, `pitch`
+// bytes apart, and how many columns it has.
+struct Rows {
+    __amdgpu_buffer_rsrc_t rs;
+    uint32_t pitch;
+    int cols;
+};
+template <class E>
+__device__ __forceinline__ Rows rows_at(E* base, int row, int rows, int most, int ld, int cols)
+{
+    Rows r;
+    r.pitch = (uint32_t)ld * 2u;
+    r.rs = make_rsrc(base + (int64_t)row * ld, (uint32_t)min(most, rows - row) * r.pitch);
+    r.cols = cols;
+    return r;
+}
+
+// How a tile is written: as it is, transposed, or both; rows in whole pieces
+// (8 bytes, 16 for the transpose) or element by element.
+enum { kAsIs = 1, kTurned = 2, kPieces = 4 };
+
+// Writes the BM x BN tile at (m0, n0), of which a wave holds FM x FN blocks
+// of 16 x 16.  The transpose goes through LDS: a lane's four values belong to
+// four of its rows.  It is staged as rows n of BM columns m, ROUNDS turns of
+// BN / ROUNDS rows, wave column wn's in stage[wn]; 16-byte chunk c of row n
+// sits at c ^ 2 ((n / 4) % 8), so that the four rows that 64 lanes write lie
+// in different banks.  It then leaves in whole rows, 16 bytes per lane.
+template <class E, int HOW, int BM, int FM, int FN, int ROUNDS, class Value>
+__device__ __forceinline__ void write_tile(const f32x4 (&acc)[FM][FN], Value value, const Rows& direct,
+                                           const Rows& turned, int m0, int n0, int lane, int wave,
+                                           unsigned char* stage0, unsigned char* stage1)
+{
+    constexpr int WTM = FM * 16, WTN = FN * 16, PITCH = BM * 2, CH = BM / 8;
+    constexpr int RW = WTN / ROUNDS;                   // staged rows per wave column
+    constexpr int RPI = 64 / CH, ITERS = 2 * RW / 4 / RPI;  // rows per wave-wide read; reads per wave
+    static_assert(ITERS * RPI * 4 == 2 * RW, "rows split evenly over the waves");
+    const int wm = wave >> 1, wn = wave & 1;
+    unsigned char* mine = wn ? stage1 : stage0;
+#pragma unroll
+    for (int h = 0; h < ROUNDS; ++h) {
+#pragma unroll
+        for (int i = 0; i < FM; ++i) {
+            const int ln = pinned(lane);
+            const int r = wm * WTM + i * 16 + (ln & 15);
+#pragma unroll
+            for (int jj = 0; jj < FN / ROUNDS; ++jj) {
+                const int j = h * (FN / ROUNDS) + jj;
+                const int c = wn * WTN + j * 16 + 4 * (ln >> 4);
+                const f32x4 v = value(r, c, acc[i][j]);
+                if constexpr (HOW & kAsIs)
+                    buffer_store4<E, (HOW & kPieces) != 0>(
+                        direct.rs, (uint32_t)r * direct.pitch + (uint32_t)(n0 + c) * 2u, n0 + c, direct.cols, v);
+                if constexpr (HOW & kTurned) {
+                    const typename Elem<E>::x4 e4 = round4<E>(v);
+                    const int row = jj * 16 + 4 * (ln >> 4);  // (row / 4 is the same for the four)
+                    unsigned char* at = mine + row * PITCH + (((r >> 3) ^ ((2 * ((row >> 2) & 7)) & (CH - 1))) << 4) +
+                                        (r & 7) * 2;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) *(E*)(at + e * PITCH) = e4[e];
+                }
+            }
+        }
+        if constexpr (HOW & kTurned) {
+            lds_barrier<63>();
+            const int ln = pinned(lane);
+#pragma unroll
+            for (int it = 0; it < ITERS; ++it) {
+                const int row = (wave * ITERS + it) * RPI + ln / CH;  // of both wave columns'
+                const int side = row / RW, local = row - side * RW, ch = ln % CH;
+                const unsigned char* from = (side ? stage1 : stage0) + local * PITCH +
+                                            ((ch ^ ((2 * ((local >> 2) & 7)) & (CH - 1))) << 4);
+                const typename Elem<E>::x8 v = *(const typename Elem<E>::x8*)from;
+                const int m = m0 + ch * 8;
+                const uint32_t at = (uint32_t)(side * WTN + h * RW + local) * turned.pitch + (uint32_t)m * 2u;
+                if constexpr (HOW & kPieces) {
+                    __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, v), turned.rs,
+                                                           m < turned.cols ? at : kOob, 0, 0);
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        const E one = v[e];
+                        __builtin_amdgcn_raw_buffer_store_b16(__builtin_bit_cast(uint16_t, one), turned.rs,
+                                                              m + e < turned.cols ? at + (uint32_t)e * 2u : kOob, 0, 0);
+                    }
+                }
+            }
+            lds_barrier<63>();
+        }
+    }
+}
+
 // S (POLY false: alpha A A^T) or P (POLY true: alpha A A^T + beta A + gamma I,
 // A symmetric), [m, m] with pitch mp, tiles on and below the diagonal and
 // their transposes.
 template <bool POLY>
 struct SymmetricOp {
+    static constexpr bool kPersist = true;
     const half* A;
     half* C;
-    int M, K, lda, mp, per;  // per: tiles of one matrix
+    int M, K, lda, mp, tiles, per;  // per: tiles of one matrix
     int64_t stride_a, stride_c;
     float alpha, beta, gamma;
 
@@ -137,50 +229,57 @@ struct SymmetricOp {
         return rows_from(A + t.batch * stride_a, t.n0 + row, M, lda, n);
     }
     __device__ __forceinline__ int b_pitch(int) const { return lda; }
+    template <int BM, int FM, int FN, int ROUNDS>
+    __device__ __forceinline__ void write(const Tile& t, const f32x4 (&acc)[FM][FN], int lane, int wave,
+                                          unsigned char* stage0, unsigned char* stage1) const
+    {
+        half* c = C + t.batch * stride_c;
+        const Rows direct = rows_at(c, t.m0, M, BM, mp, mp);
+        // Rows M .. mp - 1 of the accumulator are zero: the transpose's
+        // padding.  A tile on the diagonal has no mirror image to write.
+        Rows turned = rows_at(c, t.n0, M, BM, mp, mp);
+        if (t.m0 == t.n0) turned.rs = make_rsrc(c, 0);
+        const Rows old = rows_at(A + t.batch * stride_a, t.m0, M, BM, lda, mp);
+        auto value = [&](int r, int col, const f32x4& sum) __attribute__((always_inline)) {
+            f32x4 v = sum * alpha;
+            if constexpr (POLY) {
+                const int n = t.n0 + col;
+                const uint32_t at = n < mp ? (uint32_t)r * old.pitch + (uint32_t)n * 2u : kOob;
+                const half4 a4 = __builtin_bit_cast(half4, __builtin_amdgcn_raw_buffer_load_b64(old.rs, at, 0, 0));
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    v[e] += __builtin_fmaf(beta, (float)a4[e], n + e == t.m0 + r ? gamma : 0.0f);
+            }
+            return v;
+        };
+        write_tile<half, kAsIs | kTurned | kPieces, BM, FM, FN, ROUNDS>(acc, value, direct, turned, t.m0, t.n0, lane,
+                                                                        wave, stage0, stage1);
+    }
     template <class T>
     __device__ __forceinline__ void epilogue(const Tile& t, const Acc<T>& acc, int lane, int wm, int wn,
-                                             unsigned char*) const
+                                             unsigned char* smem) const
     {
-        const half* s = A + t.batch * stride_a;
-        half* c = C + t.batch * stride_c;
-        const bool mirror = t.m0 != t.n0;
-#pragma unroll
-        for (int i = 0; i < T::FM; ++i) {
-            const int m = t.m0 + wm * T::WTM + i * 16 + (lane & 15);
-            // rows M .. mp - 1 of the accumulator are zero: the transposed
-            // tile's padding
-            if (m >= mp) continue;
-#pragma unroll
-            for (int j = 0; j < T::FN; ++j) {
-                const int n = t.n0 + wn * T::WTN + j * 16 + 4 * (lane >> 4);
-                if (n >= mp) continue;
-                f32x4 v = acc[i][j] * alpha;
-                if constexpr (POLY) {
-                    if (m < M) {
-                        const half4 a4 = *(const half4*)(s + (int64_t)m * lda + n);
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) v[e] += beta * (float)a4[e] + (n + e == m ? gamma : 0.0f);
-                    }
-                }
-                const half4 h = round4<half>(v);
-                if (m < M) *(half4*)(c + (int64_t)m * mp + n) = h;
-                if (mirror)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        if (n + e < M) c[(int64_t)(n + e) * mp + m] = h[e];
-            }
-        }
+        write<T::BM, T::FM, T::FN, 1>(t, acc, lane, wm * 2 + wn, smem, smem + T::BM * T::WTN * 2);
+    }
+    template <class T>
+    __device__ __forceinline__ void epilogue256(const Tile& t, const f32x4 (&acc)[8][8], int lane, int wave,
+                                                unsigned char* s0, unsigned char* s1) const
+    {
+        write<256, 8, 8, 2>(t, acc, lane, wave, s0, s1);
     }
 };
 
 // X' = P X [m, n] and its transpose [n, m] in binary16, or (LAST) the result
-// in bfloat16, times alpha, in the layout that out has.
-template <bool LAST>
+// in bfloat16, times alpha, in out's layout: out's rows are X's (HOW has
+// kAsIs) or X^T's (kTurned).
+template <bool LAST, int HOW>
 struct ApplyOp {
+    // (element by element, the 256 x 256 kernel would spill scalar registers)
+    static constexpr bool kPersist = (HOW & kPieces) != 0;
     const half *P, *Xt;
     half *X, *XtNew;
     __bf16* out;
-    int M, N, K, lda, ldb, np, tiles_m, tiles_n, tall, vec, ldo;
+    int M, N, K, lda, ldb, np, tiles, tiles_m, tiles_n, ldo;
     int64_t stride_p, stride_x, stride_o;
     float alpha;
 
@@ -190,7 +289,7 @@ struct ApplyOp {
         const int per = tiles_m * tiles_n;
         t.batch = id / per;
         int tm, tn;
-        tile_of(id - t.batch * per, tiles_m, tiles_n, 8, tm, tn);
+        tile_of(id - t.batch * per, tiles_m, tiles_n, tm, tn);
         t.m0 = tm * BM;
         t.n0 = tn * BN;
         return true;
@@ -205,44 +304,42 @@ struct ApplyOp {
         return rows_from(Xt + t.batch * stride_x, t.n0 + row, N, ldb, n);
     }
     __device__ __forceinline__ int b_pitch(int) const { return ldb; }
+    template <int BM, int FM, int FN, int ROUNDS>
+    __device__ __forceinline__ void write(const Tile& t, const f32x4 (&acc)[FM][FN], int lane, int wave,
+                                          unsigned char* stage0, unsigned char* stage1) const
+    {
+        auto value = [&](int, int, const f32x4& sum) __attribute__((always_inline)) { return LAST ? sum * alpha : sum; };
+        if constexpr (LAST) {
+            __bf16* o = out + t.batch * stride_o;
+            Rows direct = {}, turned = {};
+            if constexpr (HOW & kAsIs) direct = rows_at(o, t.m0, M, BM, ldo, N);
+            if constexpr (HOW & kTurned) turned = rows_at(o, t.n0, N, BM, ldo, M);
+            write_tile<__bf16, HOW, BM, FM, FN, ROUNDS>(acc, value, direct, turned, t.m0, t.n0, lane, wave, stage0,
+                                                        stage1);
+        } else {
+            // (columns N .. np - 1 and rows M .. ldb - 1 of the accumulator
+            // are zero: the padding of both)
+            const Rows direct = rows_at(X + t.batch * stride_x, t.m0, M, BM, np, np);
+            const Rows turned = rows_at(XtNew + t.batch * stride_x, t.n0, N, BM, ldb, ldb);
+            write_tile<half, HOW, BM, FM, FN, ROUNDS>(acc, value, direct, turned, t.m0, t.n0, lane, wave, stage0,
+                                                      stage1);
+        }
+    }
     template <class T>
     __device__ __forceinline__ void epilogue(const Tile& t, const Acc<T>& acc, int lane, int wm, int wn,
-                                             unsigned char*) const
+                                             unsigned char* smem) const
     {
-#pragma unroll
-        for (int i = 0; i < T::FM; ++i) {
-            const int m = t.m0 + wm * T::WTM + i * 16 + (lane & 15);
-            // (rows M .. ldb - 1: zeros, the padding of X'^T)
-            if (m >= (LAST ? M : ldb)) continue;
-#pragma unroll
-            for (int j = 0; j < T::FN; ++j) {
-                const int n = t.n0 + wn * T::WTN + j * 16 + 4 * (lane >> 4);
-                if constexpr (LAST) {
-                    __bf16* o = out + t.batch * stride_o;
-                    const f32x4 v = acc[i][j] * alpha;
-                    if (!tall) {
-                        store4<__bf16>(o + (int64_t)m * ldo, n, N, v, vec);
-                    } else {
-#pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            if (n + e < N) o[(int64_t)(n + e) * ldo + m] = (__bf16)v[e];
-                    }
-                } else {
-                    const half4 h = round4<half>(acc[i][j]);
-                    if (m < M && n < np) *(half4*)(X + t.batch * stride_x + (int64_t)m * np + n) = h;
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        if (n + e < N) XtNew[t.batch * stride_x + (int64_t)(n + e) * ldb + m] = h[e];
-                }
-            }
-        }
+        write<T::BM, T::FM, T::FN, 1>(t, acc, lane, wm * 2 + wn, smem, smem + T::BM * T::WTN * 2);
+    }
+    template <class T>
+    __device__ __forceinline__ void epilogue256(const Tile& t, const f32x4 (&acc)[8][8], int lane, int wave,
+                                                unsigned char* s0, unsigned char* s1) const
+    {
+        write<256, 8, 8, 2>(t, acc, lane, wave, s0, s1);
     }
 };
 
 // ------------------------------------------------------------------ host --
-
-using Tile128 = Shape<half, 128, 128, 3, 1>;
-using Tile64 = Shape<half, 64, 64, 3, 2>;
 
 struct Space {
     double* partial;
@@ -271,32 +368,12 @@ struct Space {
 int64_t triangle(int64_t t) { return t * (t + 1) / 2; }
 
 template <class OP>
-int launch_symmetric(OP op, int64_t m, int64_t batch, hipStream_t stream)
+int launch_symmetric(const OP& op, int64_t m, int64_t batch, hipStream_t stream)
 {
-    const bool big = triangle((m + 127) / 128) * batch >= 128;
-    const int64_t edge = big ? 128 : 64, per = triangle((m + edge - 1) / edge);
-    if (per * batch > abi::kMaxDim) return hipErrorInvalidValue;
-    op.per = (int)per;
-    if (big)
-        hipLaunchKernelGGL((nt_tile<Tile128, OP>), dim3((unsigned)(per * batch)), dim3(256), 0, stream, op);
-    else
-        hipLaunchKernelGGL((nt_tile<Tile64, OP>), dim3((unsigned)(per * batch)), dim3(256), 0, stream, op);
-    return (int)hipGetLastError();
-}
-
-template <class OP>
-int launch_apply(OP op, int64_t m, int64_t n, int64_t batch, hipStream_t stream)
-{
-    const bool big = ((m + 127) / 128) * ((n + 127) / 128) * batch >= 128;
-    const int64_t edge = big ? 128 : 64, tm = (m + edge - 1) / edge, tn = (n + edge - 1) / edge;
-    if (tm * tn * batch > abi::kMaxDim) return hipErrorInvalidValue;
-    op.tiles_m = (int)tm;
-    op.tiles_n = (int)tn;
-    if (big)
-        hipLaunchKernelGGL((nt_tile<Tile128, OP>), dim3((unsigned)(tm * tn * batch)), dim3(256), 0, stream, op);
-    else
-        hipLaunchKernelGGL((nt_tile<Tile64, OP>), dim3((unsigned)(tm * tn * batch)), dim3(256), 0, stream, op);
-    return (int)hipGetLastError();
+    auto per = [=](int64_t edge) { return triangle((m + edge - 1) / edge); };
+    return launch<half>(
+        op, op.K, [=](int64_t edge) { return per(edge) * batch; }, [=](OP& o, int edge) { o.per = (int)per(edge); },
+        stream);
 }
 
 template <class E>
@@ -360,16 +437,21 @@ int run(const E* G, __bf16* out, int64_t batch, int64_t rows, int64_t cols, int6
             op.N = (int)w.n;
             op.K = op.lda = op.ldb = (int)w.mp;
             op.np = (int)w.np;
-            op.tall = tall;
-            op.vec = (uintptr_t)out % 8 == 0 && ldo % 4 == 0 && (batch == 1 || stride_o % 4 == 0);
             op.ldo = (int)ldo;
             op.stride_p = w.stride_s;
             op.stride_x = w.stride_x;
             op.stride_o = stride_o;
             op.alpha = (float)(1.0 / scale);
-            return launch_apply(op, w.m, w.n, batch, stream);
+            return launch_grid<half>(op, w.m, w.n, 1, batch, op.K, stream);
         };
-        if ((rc = i + 1 < steps ? apply(ApplyOp<false>{}) : apply(ApplyOp<true>{}))) return rc;
+        const bool eights = (uintptr_t)out % 16 == 0 && ldo % 8 == 0 && cols % 8 == 0 && stride_o % 8 == 0;
+        if (i + 1 < steps)
+            rc = apply(ApplyOp<false, kAsIs | kTurned | kPieces>{});
+        else if (tall)
+            rc = eights ? apply(ApplyOp<true, kTurned | kPieces>{}) : apply(ApplyOp<true, kTurned>{});
+        else
+            rc = eights ? apply(ApplyOp<true, kAsIs | kPieces>{}) : apply(ApplyOp<true, kAsIs>{});
+        if (rc) return rc;
     }
     return hipSuccess;
 }
@@ -399,7 +481,7 @@ int orthogonalize_ns(const void* G, void* out, int64_t batch, int64_t rows, int6
 {
     using namespace abi;
     if (!good_sizes(batch, rows, cols)) return hipErrorInvalidValue;
-    if (ldg < cols || ldg > kMaxDim || ldo < cols || ldo > kMaxDim) return hipErrorInvalidValue;
+    if (ldg < cols || ldg > kMaxDim || ldo < cols || ldo > kMaxPitch) return hipErrorInvalidValue;
     if (type < ORTHOGONALIZE_NS_F16 || type > ORTHOGONALIZE_NS_F32) return hipErrorInvalidValue;
     if (steps < 0 || steps > 64 || (steps > 0 && !coefficients)) return hipErrorInvalidValue;
     if (batch == 0 || rows == 0 || cols == 0) return hipSuccess;

@@ -25,8 +25,8 @@
  * caller's and may be reused by work enqueued later on the same stream.
  *
  * hipErrorInvalidValue before anything is enqueued: a negative size, a size
- * of 2^21 - 8 or more in rows or cols, batch of 2^16 or more, a pitch below
- * the row, a matrix stride that makes out's matrices overlap, an unknown
+ * above 2^21 - 9 in rows or cols, batch of 2^16 or more, a pitch below the
+ * row, ldo of 2^21 or more, a matrix stride that makes out's matrices overlap, an unknown
  * type, steps below 0 or above 64, null coefficients with steps > 0, a null
  * or misaligned pointer with a non-zero extent, out or the workspace meeting
  * G or each other, a workspace that is too small.

@@ -88,6 +88,20 @@ def test_gated_many_tiles(shape):
         plain.assert_within(g, w, b, name)
 
 
+# more 256 x 256 tiles than CUs, and every way through their K loop: 3 to 17
+# steps, whole and with a tail, so that tiles start at every ring position
+@pytest.mark.parametrize("D", [136, 192, 200, 256, 320, 328, 448, 520, 640, 712, 1080])
+@pytest.mark.parametrize("t", ["fp16", "bf16"])
+def test_gated_tiles_in_turn(D, t):
+    T, F = 256 * 18 + 5, 128 * 16 - 3
+    x, wg, wu = gated_inputs(T, D, F, plain.TYPES[t], seed=D)
+    h, saved = fw.gated_nt_train(x, wg, wu)
+    want, bound = plain.gated(x, wg, wu, "silu")
+    plain.assert_within(h, want, bound, "h")
+    # the whole-piece stores of an output whose rows are a multiple of four
+    plain.assert_within(fw.gated_nt(x, wg[:2040], wu[:2040]), want[:, :2040], bound[:, :2040], "whole pieces")
+
+
 @pytest.mark.parametrize("act", ["silu", "gelu_tanh"])
 def test_gated_gradients_match_differences(act):
     T, D, F = 37, 72, 50
@@ -238,9 +252,13 @@ def test_ns_batch_equals_its_matrices(shape):
         assert torch.equal(out[i], fw.orthogonalize_ns(g[i]))
 
 
-def test_ns_large_tiles():
-    g = normal(2, 1030, 1536, seed=8, t=torch.bfloat16)
-    ns_close(fw.orthogonalize_ns(g), g)
+@pytest.mark.parametrize("shape", [(2, 1030, 1536), (6, 1537, 1030), (9, 1024, 1280), (40, 516, 520)], ids=str)
+def test_ns_large_tiles(shape):
+    """Tiles of every size, more of them than CUs, with tails and without."""
+    g = normal(*shape, seed=8, t=torch.bfloat16)
+    out = fw.orthogonalize_ns(g, steps=2)
+    ns_close(out[:2], g[:2], steps=2)
+    ns_close(out[-1], g[-1], steps=2)
 
 
 def test_ns_steps_and_coefficients():
