@@ -56,7 +56,7 @@ __host__ __device__ __forceinline__ int64_t saved_pitch(int64_t F) { return (F +
 
 template <class E, bool SAVE, bool WHOLE>
 struct GatedOp {
-    static constexpr bool kPersist = true;
+    static constexpr bool kPersist = true, kOblong = true;  // (256 x 256, 256 x 128 tiles)
     const E *X, *Wg, *Wu;
     E* H;
     float* saved;
@@ -64,29 +64,30 @@ struct GatedOp {
     Activation act;
 
     template <int BM, int BN>
-    __device__ __forceinline__ bool tile(int id, Tile& t) const
+    __device__ __forceinline__ void tile(int id, Tile& t) const
     {
         int tm, tn;
         tile_of(id, tiles_m, tiles_n, tm, tn);
         t.m0 = tm * BM;
         t.n0 = tn * (BN / 2);
         t.batch = 0;
-        return true;
     }
     __device__ __forceinline__ const E* a_rows(const Tile& t, int row, int& n) const
     {
         return rows_from(X, t.m0 + row, M, lda, n);
     }
-    // Quarter q of the B tile: rows of Wg for even q, of Wu for odd q, the
-    // same BN / 4 rows for both of a pair; a wave's sub-tile (half of the
-    // tile's columns) is one pair.
-    template <int BN>
+    // A wave's WTN rows of the B tile are WTN / 2 of Wg, then the same of Wu.
+    template <int WTN>
     __device__ __forceinline__ const E* b_rows(const Tile& t, int row, int& n) const
     {
-        const int q = row / (BN / 4);
-        return rows_from(q & 1 ? Wu : Wg, t.n0 + (q >> 1) * (BN / 4), F, q & 1 ? ldu : ldg, n);
+        const bool up = row % WTN >= WTN / 2;
+        return rows_from(up ? Wu : Wg, t.n0 + row / WTN * (WTN / 2) + row % (WTN / 2), F, up ? ldu : ldg, n);
     }
-    __device__ __forceinline__ int b_pitch(int q) const { return q & 1 ? ldu : ldg; }
+    template <int WTN>
+    __device__ __forceinline__ int b_pitch(int row) const
+    {
+        return row % WTN >= WTN / 2 ? ldu : ldg;
+    }
     // Where a tile's rows of H and of `saved` lie.
     struct Out {
         __amdgpu_buffer_rsrc_t h, s;
@@ -122,30 +123,18 @@ struct GatedOp {
         }
     }
     template <class T>
-    __device__ __forceinline__ void epilogue(const Tile& t, const Acc<T>& acc, int lane, int wm, int wn,
-                                             unsigned char*) const
+    __device__ __forceinline__ void epilogue(const Tile& t, const f32x4 (&acc)[T::FM][T::FN], int lane, int wave,
+                                             unsigned char*, unsigned char*) const
     {
         constexpr int HF = T::FN / 2;
         const Out o = out_rows(t.m0, T::BM);
 #pragma unroll
         for (int i = 0; i < T::FM; ++i)
 #pragma unroll
-            for (int j = 0; j < HF; ++j)
-                finish(o, wm * T::WTM + i * 16 + (lane & 15), t.n0 + wn * (T::WTN / 2) + j * 16 + 4 * (lane >> 4),
-                       acc[i][j], acc[i][j + HF]);
-    }
-    template <class T>
-    __device__ __forceinline__ void epilogue256(const Tile& t, const f32x4 (&acc)[8][8], int lane, int wave,
-                                                unsigned char*, unsigned char*) const
-    {
-        const Out o = out_rows(t.m0, 256);
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
+            for (int j = 0; j < HF; ++j) {
                 const int ln = pinned(lane);
-                finish(o, (wave >> 1) * 128 + i * 16 + (ln & 15), t.n0 + (wave & 1) * 64 + j * 16 + 4 * (ln >> 4),
-                       acc[i][j], acc[i][j + 4]);
+                finish(o, wave / T::WAVES_N * T::WTM + i * 16 + (ln & 15),
+                       t.n0 + wave % T::WAVES_N * (T::WTN / 2) + j * 16 + 4 * (ln >> 4), acc[i][j], acc[i][j + HF]);
             }
     }
 };

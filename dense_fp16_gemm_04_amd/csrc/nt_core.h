@@ -1,25 +1,35 @@
 // Tiled NT products (both operands row-major, k contiguous) on gfx950, with
 // the operands' rows and the epilogue supplied by an operation OP.
 //
-// nt_tile: one BM x BN tile of the accumulator per workgroup, four waves
-// (2 x 2), a ring of S stages in LDS filled by direct global->LDS loads, and
-// v_mfma_f32_16x16x32 with 32-bit accumulators.  In a wave's sub-tile lane l
-// holds, of the 16 x 16 block (i, j), row l % 16 and columns 4 * (l / 16) ..
-// + 3 (the B fragment is the MFMA's first operand, which gives the block
-// transposed: four consecutive columns per lane).
+// Three kernels share one scheme: a BM x BN tile of the accumulator per
+// workgroup, K in steps of 64, operand tiles in an LDS ring filled by direct
+// global->LDS loads, and v_mfma_f32_16x16x32 with 32-bit accumulators.
+//   nt_persist  256 x 256, four waves, one workgroup per CU walking its tiles
+//   nt_ordered  256 x 128 and 128 x 128, eight waves, four of which load
+//   nt_tile     64 x 64, four waves, scheduled by the compiler
+// A wave holds a WTM x WTN sub-tile as FM x FN blocks of 16 x 16: lane l has,
+// of block (i, j), row l % 16 and columns 4 * (l / 16) .. + 3 (the B fragment
+// is the MFMA's first operand, which gives the block transposed: four
+// consecutive columns per lane).
 //
 // OP has, as device functions,
-//   bool tile<BM, BN>(id, Tile&)   what tile number `id` is (row and column
+//   tile<BM, BN>(id, Tile&)        what tile number `id` is (row and column
 //                                  of its first element, batch);
 //   const E* a_rows(t, row, &n)    A's row `row` of the tile's BM and how
 //                                  many rows exist from there (rows_from);
-//   const E* b_rows<BN>(t, row, &n)  the same for B;
-//   epilogue<T>(t, acc, lane, wm, wn, smem)
-//   int b_pitch(q)                 the pitch of B's rows in quarter q
-// and the fields K (elements, a multiple of 8) and lda (A's row pitch in
-// elements; pitches are multiples of 8 and below 2^21).  Every row starts on
-// 16 bytes.  Each of the four waves loads a quarter of each
-// operand's tile, so the rows of one quarter are evenly spaced.
+//   const E* b_rows<WTN>(t, row, &n)  the same for B, and
+//   int b_pitch<WTN>(row)             the pitch of that row's operand: BN / 8
+//                                     rows from a multiple of BN / 8 on are
+//                                     evenly spaced
+//   epilogue<T>(t, acc, lane, wave, s0, s1)
+//                                  writes the sub-tiles out; s0 and s1 point
+//                                  to LDS for T::WTN / T::ROUNDS rows of BM
+//                                  16-bit values for the first wave column and
+//                                  for the others; a barrier has passed that
+//                                  makes it free, and another follows
+// and the fields K (elements, a multiple of 8), lda (A's row pitch in
+// elements; pitches are multiples of 8 and below 2^21), tiles.  Every row
+// starts on 16 bytes.
 #ifndef DENSE_FP16_GEMM_NT_CORE_H
 #define DENSE_FP16_GEMM_NT_CORE_H
 
@@ -44,70 +54,117 @@ __device__ __forceinline__ const E* rows_from(const E* base, int row, int rows, 
     return base + (row < rows ? (int64_t)row * ld : 0);
 }
 
-template <class E_, int BM_, int BN_, int STAGES_, int OCC_>
+// WM x WN waves; RS, LS: MFMAs per fragment read and per load (nt_ordered).
+template <class E_, int BM_, int BN_, int WM, int WN, int STAGES_, int OCC_, int LOADERS_, int RS_ = 1, int LS_ = 1>
 struct Shape {
     using E = E_;
     using x8 = typename Elem<E>::x8;
     static constexpr int BM = BM_, BN = BN_, BK = 64, STAGES = STAGES_, OCC = OCC_;
-    static constexpr int WAVES = 4, THREADS = 256;
-    static constexpr int WTM = BM / 2, WTN = BN / 2;   // a wave's sub-tile
-    static constexpr int FM = WTM / 16, FN = WTN / 16;
+    static constexpr int WAVES_M = WM, WAVES_N = WN, WAVES = WM * WN, THREADS = WAVES * kWave;
+    static constexpr int WTM = BM / WM, WTN = BN / WN;  // a wave's sub-tile
+    static constexpr int FM = WTM / 16, FN = WTN / 16, ROUNDS = 1;
     static constexpr int ROW_BYTES = 128;
     static constexpr int A_BYTES = BM * ROW_BYTES, B_BYTES = BN * ROW_BYTES;
     static constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
     static constexpr int LDS_BYTES = STAGES * STAGE_BYTES;
-    static constexpr int A_LOADS = BM / 32, B_LOADS = BN / 32;  // 8 rows each, per wave
+    static constexpr int LOADERS = LOADERS_;             // waves 0 .. LOADERS - 1 load
+    static constexpr int A_LOADS = BM / 8 / LOADERS, B_LOADS = BN / 8 / LOADERS;  // 8 rows each, per wave
     static constexpr int LOADS = A_LOADS + B_LOADS;
+    static constexpr int RS = RS_, LS = LS_;
+    static_assert(LOADERS == 4 && BM % 64 == 0 && BN % 64 == 0, "a wave loads whole 16-row groups");
     static_assert(LDS_BYTES <= 160 * 1024, "gfx950 has 160 KiB of LDS per workgroup");
-    static_assert(STAGES >= 2 && LOADS * (STAGES - 2) <= 63, "vmcnt holds at most 63");
+    static_assert(STAGES >= 2 && LOADS * (STAGES - 1) <= 63, "vmcnt holds at most 63");
 };
 
+template <bool B>
+struct Flag {
+    static constexpr bool value = B;
+};
+template <int V>
+struct Int {
+    static constexpr int value = V;
+};
+
+// The loads of one wave: load l of an operand fills rows 8 l .. 8 l + 7 of
+// the wave's quarter of its tile; lane -> row lane / 8, position lane % 8,
+// which the swizzle fills with chunk pos ^ ((row / 2) % 8).  (A quarter starts
+// at a multiple of 16 rows, so the row's place within it decides.)  B's
+// quarter is two operands of BN / 8 rows, which the gated layer needs.
 template <class T>
-using Acc = f32x4[T::FM][T::FN];
+struct Loader {
+    __amdgpu_buffer_rsrc_t ra, rb0, rb1;
+    uint32_t va[T::A_LOADS], vb[T::B_LOADS];
+    int c01[2], wave;
+    template <class OP>
+    __device__ __forceinline__ Loader(const OP& op, const Tile& t, int lane, int w) : wave(w)
+    {
+        constexpr int BR = T::BN / 8;
+        const int row_b = w * (T::BN / 4);
+        const uint32_t pitch_a = (uint32_t)op.lda * 2u;
+        const uint32_t pitch_0 = (uint32_t)op.template b_pitch<T::WTN>(row_b) * 2u;
+        const uint32_t pitch_1 = (uint32_t)op.template b_pitch<T::WTN>(row_b + BR) * 2u;
+        int na = 0, n0 = 0, n1 = 0;
+        const void* pa = op.a_rows(t, w * (T::BM / 4), na);
+        const void* p0 = op.template b_rows<T::WTN>(t, row_b, n0);
+        const void* p1 = op.template b_rows<T::WTN>(t, row_b + BR, n1);
+        ra = make_rsrc(pa, (uint32_t)min(na, T::BM / 4) * pitch_a);
+        rb0 = make_rsrc(p0, (uint32_t)min(n0, BR) * pitch_0);
+        rb1 = make_rsrc(p1, (uint32_t)min(n1, BR) * pitch_1);
+        const int lr = lane >> 3, lp = lane & 7;
+        c01[0] = swizzle(lr, lp);
+        c01[1] = swizzle(8 + lr, lp);
+#pragma unroll
+        for (int l = 0; l < T::A_LOADS; ++l) va[l] = (uint32_t)(l * 8 + lr) * pitch_a + (uint32_t)c01[l & 1] * 16u;
+#pragma unroll
+        for (int l = 0; l < T::B_LOADS; ++l) {
+            const bool second = l >= T::B_LOADS / 2;
+            vb[l] = (uint32_t)((second ? l - T::B_LOADS / 2 : l) * 8 + lr) * (second ? pitch_1 : pitch_0) +
+                    (uint32_t)c01[l & 1] * 16u;
+        }
+    }
+    // Load l (A's first) of K step ks into the stage at `base`.  MASKED: the
+    // step may reach past K, where chunks read as zero; the K position is then
+    // part of the vector offset, since it may exceed the buffer.
+    template <class Masked>
+    __device__ __forceinline__ void load(unsigned char* base, int l, int ks, int K, Masked) const
+    {
+        const int lb = l - T::A_LOADS;
+        const bool is_a = l < T::A_LOADS;
+        uint32_t off = is_a ? va[is_a ? l : 0] : vb[is_a ? 0 : lb], soff = (uint32_t)ks * (T::BK * 2);
+        if constexpr (Masked::value) {
+            off = c01[l & 1] * 8 < K - ks * T::BK ? off + soff : kOob;
+            soff = 0;
+        }
+        // (a buffer resource cannot be the result of ?:)
+        if (is_a)
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(ra, (lds_void*)(base + (wave * T::A_LOADS + l) * 1024), 16, off,
+                                                     soff, 0, 0);
+        else if (lb < T::B_LOADS / 2)
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(
+                rb0, (lds_void*)(base + T::A_BYTES + (wave * T::B_LOADS + lb) * 1024), 16, off, soff, 0, 0);
+        else
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(
+                rb1, (lds_void*)(base + T::A_BYTES + (wave * T::B_LOADS + lb) * 1024), 16, off, soff, 0, 0);
+    }
+};
 
 template <class T, class OP>
 __global__ void __launch_bounds__(T::THREADS, T::OCC) nt_tile(const OP op)
 {
     using x8 = typename T::x8;
+    static_assert(T::WAVES == 4, "every wave loads");
     __shared__ __attribute__((aligned(1024))) unsigned char smem[T::LDS_BYTES];
     const int lane = threadIdx.x & (kWave - 1);
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
-    const int wm = wave / 2, wn = wave % 2;
+    const int wm = wave / T::WAVES_N, wn = wave % T::WAVES_N;
 
     Tile t;
-    if (!op.template tile<T::BM, T::BN>(blockIdx.x, t)) return;
-
-    // Loads: load l of a wave fills rows 8 l .. 8 l + 7 of the wave's quarter
-    // of the operand's tile; lane -> row lane / 8, position lane % 8, which
-    // the swizzle fills with chunk pos ^ ((row / 2) % 8).  (A quarter starts
-    // at a multiple of 16 rows, so the row's place within it decides.)
-    const uint32_t pitch_a = (uint32_t)op.lda * 2u, pitch_b = (uint32_t)op.b_pitch(wave) * 2u;
-    int na = 0, nb = 0;
-    const void* pa = op.a_rows(t, wave * (T::BM / 4), na);
-    const void* pb = op.template b_rows<T::BN>(t, wave * (T::BN / 4), nb);
-    const __amdgpu_buffer_rsrc_t ra = make_rsrc(pa, (uint32_t)min(na, T::BM / 4) * pitch_a);
-    const __amdgpu_buffer_rsrc_t rb = make_rsrc(pb, (uint32_t)min(nb, T::BN / 4) * pitch_b);
-    const int lr = lane >> 3, lp = lane & 7;
-    const int c0 = swizzle(lr, lp), c1 = swizzle(8 + lr, lp);
+    op.template tile<T::BM, T::BN>(blockIdx.x, t);
+    const Loader<T> loader(op, t, lane, wave);
     const int K = op.K;
     auto issue = [&](int stage, int ks) __attribute__((always_inline)) {
-        const int krem = K - ks * T::BK;
-        const uint32_t koff = (uint32_t)ks * (T::BK * 2);
-        unsigned char* base = smem + stage * T::STAGE_BYTES;
 #pragma unroll
-        for (int l = 0; l < T::A_LOADS; ++l) {
-            const int c = l & 1 ? c1 : c0;
-            const uint32_t off = c * 8 < krem ? koff + (uint32_t)(l * 8 + lr) * pitch_a + (uint32_t)c * 16u : kOob;
-            __builtin_amdgcn_raw_ptr_buffer_load_lds(ra, (lds_void*)(base + (wave * T::A_LOADS + l) * 1024), 16, off, 0,
-                                                     0, 0);
-        }
-#pragma unroll
-        for (int l = 0; l < T::B_LOADS; ++l) {
-            const int c = l & 1 ? c1 : c0;
-            const uint32_t off = c * 8 < krem ? koff + (uint32_t)(l * 8 + lr) * pitch_b + (uint32_t)c * 16u : kOob;
-            __builtin_amdgcn_raw_ptr_buffer_load_lds(
-                rb, (lds_void*)(base + T::A_BYTES + (wave * T::B_LOADS + l) * 1024), 16, off, 0, 0, 0);
-        }
+        for (int l = 0; l < T::LOADS; ++l) loader.load(smem + stage * T::STAGE_BYTES, l, ks, K, Flag<true>{});
     };
 
     const int fr = lane & 15, fh = lane >> 4;
@@ -115,7 +172,7 @@ __global__ void __launch_bounds__(T::THREADS, T::OCC) nt_tile(const OP op)
     const int arow = (wm * T::WTM + fr) * T::ROW_BYTES;
     const int brow = T::A_BYTES + (wn * T::WTN + fr) * T::ROW_BYTES;
 
-    Acc<T> acc;
+    f32x4 acc[T::FM][T::FN];
 #pragma unroll
     for (int i = 0; i < T::FM; ++i)
 #pragma unroll
@@ -152,7 +209,121 @@ __global__ void __launch_bounds__(T::THREADS, T::OCC) nt_tile(const OP op)
     // no load may still be writing LDS when the ring is used again or the
     // workgroup ends
     lds_barrier<0>();
-    op.template epilogue<T>(t, acc, lane, wm, wn, smem);
+    op.template epilogue<T>(t, acc, lane, wave, smem, smem + T::BM * T::WTN * 2);
+}
+
+// acc += b * a with the accumulator in AGPRs; the memory clobber keeps every
+// LDS and global access on its side, so the source order of a loop built from
+// these is its issue order.
+__device__ __forceinline__ void mfma_agpr(f32x4& acc, const Elem<_Float16>::x8& b, const Elem<_Float16>::x8& a)
+{
+    asm volatile("v_mfma_f32_16x16x32_f16 %0, %1, %2, %0" : "+a"(acc) : "v"(b), "v"(a) : "memory");
+}
+__device__ __forceinline__ void mfma_agpr(f32x4& acc, const Elem<__bf16>::x8& b, const Elem<__bf16>::x8& a)
+{
+    asm volatile("v_mfma_f32_16x16x32_bf16 %0, %1, %2, %0" : "+a"(acc) : "v"(b), "v"(a) : "memory");
+}
+
+// One tile per workgroup, eight waves (two per SIMD), every instruction of
+// the K loop in a fixed order.  Waves 0 .. 3 (one per SIMD) issue the loads,
+// so that each SIMD has a wave that never waits on the vector memory queue.
+// A step is two sub-steps of 32 k:
+//   sub-step 0: its MFMAs, with the fragment reads of sub-step 1 between them;
+//   barrier:    the wave's loads of the next step have landed, its reads are
+//               back, so every wave is done with this step's operand tiles;
+//   sub-step 1: its MFMAs, with the next step's first fragment reads and the
+//               loads of step ks + S, into the stage this step leaves.
+template <class T, class OP>
+__global__ void __launch_bounds__(T::THREADS, 1) nt_ordered(const OP op)
+{
+    using x8 = typename T::x8;
+    constexpr int S = T::STAGES, G = T::FM * T::FN, R = T::FM + T::FN;
+    static_assert(T::WAVES == 8, "two waves per SIMD, one of which loads");
+    static_assert(T::RS * (R - 1) < G && T::LS * (T::LOADS - 1) + T::LS / 2 < G, "reads and loads fit in a sub-step");
+    __shared__ __attribute__((aligned(1024))) unsigned char smem[T::LDS_BYTES];
+    const int lane = threadIdx.x & (kWave - 1);
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+    const int wm = wave / T::WAVES_N, wn = wave % T::WAVES_N;
+
+    Tile t;
+    op.template tile<T::BM, T::BN>(blockIdx.x, t);
+    const Loader<T> loader(op, t, lane, wave & 3);
+    const int K = op.K;
+
+    const int fr = lane & 15, fh = lane >> 4;
+    const int pos[2] = {swizzle(fr, fh) * 16, swizzle(fr, 4 + fh) * 16};
+    const int arow = (wm * T::WTM + fr) * T::ROW_BYTES;
+    const int brow = T::A_BYTES + (wn * T::WTN + fr) * T::ROW_BYTES;
+
+    x8 fa[2][T::FM], fb[2][T::FN];
+    f32x4 acc[T::FM][T::FN];
+#pragma unroll
+    for (int i = 0; i < T::FM; ++i)
+#pragma unroll
+        for (int j = 0; j < T::FN; ++j) acc[i][j] = f32x4{0, 0, 0, 0};
+
+    // fragment read idx of set `set`, in the order the MFMAs need them
+    auto read_one = [&](int set, const unsigned char* base, int idx) __attribute__((always_inline)) {
+        if (idx == 0)
+            fa[set][0] = *(const x8*)(base + arow + pos[set]);
+        else if (idx <= T::FN)
+            fb[set][idx - 1] = *(const x8*)(base + brow + pos[set] + (idx - 1) * 16 * T::ROW_BYTES);
+        else
+            fa[set][idx - T::FN] = *(const x8*)(base + arow + pos[set] + (idx - T::FN) * 16 * T::ROW_BYTES);
+    };
+    // MFMAs along the rows of blocks and back, so that neighbours share a fragment
+    auto substep = [&](int set, const unsigned char* reads, auto ld, unsigned char* into, int lstep, auto masked)
+                       __attribute__((always_inline)) {
+#pragma unroll
+        for (int n = 0; n < G; ++n) {
+            const int i = n / T::FN, j = (i & 1) ? T::FN - 1 - n % T::FN : n % T::FN;
+            mfma_agpr(acc[i][j], fb[set][j], fa[set][i]);
+            if (n % T::RS == 0 && n / T::RS < R) read_one(1 - set, reads, n / T::RS);
+            if constexpr (decltype(ld)::value)
+                if (n % T::LS == T::LS / 2 && n / T::LS < T::LOADS) loader.load(into, n / T::LS, lstep, K, masked);
+        }
+    };
+
+    const int nk = (K + T::BK - 1) / T::BK, nfull = K / T::BK;
+    auto run = [&](auto ldtag) __attribute__((always_inline)) {
+        constexpr bool LD = decltype(ldtag)::value;
+        // every stage is free at the start: fill them all, then wait for step 0
+#pragma unroll
+        for (int s = 0; s < S; ++s)
+#pragma unroll
+            for (int l = 0; l < T::LOADS; ++l)
+                if constexpr (LD) loader.load(smem + s * T::STAGE_BYTES, l, s, K, Flag<true>{});
+        lds_barrier<T::LOADS * (S - 1)>();
+#pragma unroll
+        for (int idx = 0; idx < R; ++idx) read_one(0, smem, idx);
+        int cur = 0;
+        auto step = [&](int ks, auto masked) __attribute__((always_inline)) {
+            const int nxt = cur + 1 == S ? 0 : cur + 1;
+            unsigned char* base = smem + cur * T::STAGE_BYTES;
+            unsigned char* next = smem + nxt * T::STAGE_BYTES;
+            substep(0, base, Flag<false>{}, base, 0, masked);
+            lds_barrier<T::LOADS * (S - 2)>();
+            // (steps past the end of K load zeros into stages never read)
+            substep(1, next, Flag<LD>{}, base, ks + S, masked);
+            cur = nxt;
+        };
+        int ks = 0;
+        for (; ks < nk && ks + S < nfull; ++ks) step(ks, Flag<false>{});
+        for (; ks < nk; ++ks) step(ks, Flag<true>{});
+    };
+    if (nk > 0) {
+        if (wave < T::LOADERS)
+            run(Flag<true>{});
+        else
+            run(Flag<false>{});
+        // the last MFMAs write their accumulators before they are read: asm
+        // hides them from the compiler's hazard checks
+        asm volatile("s_nop 7\n\ts_nop 7\n\ts_nop 7" ::: "memory");
+    }
+    // no load may still be writing LDS when the ring is used again or the
+    // workgroup ends
+    lds_barrier<0>();
+    op.template epilogue<T>(t, acc, lane, wave, smem, smem + T::BM * T::WTN * 2);
 }
 
 // One 256 x 256 tile after another per workgroup, one workgroup per CU, four
@@ -172,11 +343,8 @@ __global__ void __launch_bounds__(T::THREADS, T::OCC) nt_tile(const OP op)
 // next tile, up to four before and after the cycles) keep the ring position
 // in a register.
 //
-// OP as for nt_tile, with `int tiles` (their number) and the epilogue
-//   epilogue256<T>(t, acc, lane, wave, s0, s1)
-// s0 and s1 are the slots that no load is writing (the same in every wave); a
-// barrier follows.  Nothing clears the accumulators: a tile's first MFMAs add
-// to an inline zero.
+// The epilogue has the two slots that no load is writing.  Nothing clears the
+// accumulators: a tile's first MFMAs add to an inline zero.
 //
 // Needs three steps at least: K > 128.
 template <class E_>
@@ -184,31 +352,12 @@ struct Shape256 {
     using E = E_;
     using x8 = typename Elem<E>::x8;
     static constexpr int BM = 256, BN = 256, BK = 64, THREADS = 256;
-    static constexpr int WTM = 128, WTN = 128, FM = 8, FN = 8;
+    static constexpr int WAVES_M = 2, WAVES_N = 2, WAVES = 4;
+    static constexpr int WTM = 128, WTN = 128, FM = 8, FN = 8, ROUNDS = 2;
     static constexpr int ROW_BYTES = 128;
     static constexpr int SLOT = 32768;
     static constexpr int RS = 3, LS = 8;  // MFMAs per fragment read, per load
 };
-
-template <bool B>
-struct Flag {
-    static constexpr bool value = B;
-};
-template <int V>
-struct Int {
-    static constexpr int value = V;
-};
-
-// acc += b * a with the accumulator in AGPRs; the memory clobber keeps every
-// LDS and global access on its side.
-__device__ __forceinline__ void mfma_agpr(f32x4& acc, const Elem<_Float16>::x8& b, const Elem<_Float16>::x8& a)
-{
-    asm volatile("v_mfma_f32_16x16x32_f16 %0, %1, %2, %0" : "+a"(acc) : "v"(b), "v"(a) : "memory");
-}
-__device__ __forceinline__ void mfma_agpr(f32x4& acc, const Elem<__bf16>::x8& b, const Elem<__bf16>::x8& a)
-{
-    asm volatile("v_mfma_f32_16x16x32_bf16 %0, %1, %2, %0" : "+a"(acc) : "v"(b), "v"(a) : "memory");
-}
 
 // The same with nothing to add to.  (The old value is an operand only to keep
 // the accumulator in its registers: as a plain output it made the register
@@ -235,7 +384,7 @@ __global__ void __launch_bounds__(T::THREADS, 1) nt_persist(const OP op)
     const int K = op.K;
     const int nk = (K + T::BK - 1) / T::BK;
     const int nfull = K / T::BK;  // steps wholly inside K
-    const uint32_t pitch_a = (uint32_t)op.lda * 2u, pitch_b = (uint32_t)op.b_pitch(wave) * 2u;
+    const uint32_t pitch_a = (uint32_t)op.lda * 2u, pitch_b = (uint32_t)op.template b_pitch<T::WTN>(wave * 64) * 2u;
 
     // Load l of a wave fills rows 8 l .. + 7 of its quarter of an operand's
     // tile, KiB wave * 8 + l of the slot.  Loads of a group of four share the
@@ -264,7 +413,7 @@ __global__ void __launch_bounds__(T::THREADS, 1) nt_persist(const OP op)
     auto operands = [&]() __attribute__((always_inline)) {
         int na = 0, nb = 0;
         const void* pa = op.a_rows(t, wave * 64, na);
-        const void* pb = op.template b_rows<T::BN>(t, wave * 64, nb);
+        const void* pb = op.template b_rows<T::WTN>(t, wave * 64, nb);
         la = make_rsrc(pa, (uint32_t)min(na, 64) * pitch_a);
         lb = make_rsrc(pb, (uint32_t)min(nb, 64) * pitch_b);
     };
@@ -446,7 +595,7 @@ __global__ void __launch_bounds__(T::THREADS, 1) nt_persist(const OP op)
         // hides them from the compiler's hazard checks
         asm volatile("s_nop 7\n\ts_nop 7\n\ts_nop 7" ::: "memory");
         __builtin_amdgcn_sched_barrier(0);
-        op.template epilogue256<T>(done, acc, lane, wave, slot(0), slot(1));
+        op.template epilogue<T>(done, acc, lane, wave, slot(0), slot(1));
         if (next >= op.tiles) break;
         // every wave is done with this step's slots
         lds_barrier<63>();
@@ -495,63 +644,49 @@ __device__ __forceinline__ void buffer_store4(__amdgpu_buffer_rsrc_t rs, uint32_
 // C = A B^T.
 template <class E, bool WHOLE>
 struct StoreOp {
-    static constexpr bool kPersist = true;
+    static constexpr bool kPersist = true, kOblong = true;  // (256 x 256, 256 x 128 tiles)
     const E *A, *B;
     E* C;
     int M, N, K, lda, ldb, ldc, tiles, tiles_m, tiles_n;
 
     template <int BM, int BN>
-    __device__ __forceinline__ bool tile(int id, Tile& t) const
+    __device__ __forceinline__ void tile(int id, Tile& t) const
     {
         int tm, tn;
         tile_of(id, tiles_m, tiles_n, tm, tn);
         t.batch = 0;
         t.m0 = tm * BM;
         t.n0 = tn * BN;
-        return true;
     }
     __device__ __forceinline__ const E* a_rows(const Tile& t, int row, int& n) const
     {
         return rows_from(A, t.m0 + row, M, lda, n);
     }
-    template <int BN>
+    template <int WTN>
     __device__ __forceinline__ const E* b_rows(const Tile& t, int row, int& n) const
     {
         return rows_from(B, t.n0 + row, N, ldb, n);
     }
-    __device__ __forceinline__ int b_pitch(int) const { return ldb; }
-    __device__ __forceinline__ void finish(__amdgpu_buffer_rsrc_t out, int r, int n, const f32x4& v) const
+    template <int WTN>
+    __device__ __forceinline__ int b_pitch(int) const
     {
-        buffer_store4<E, WHOLE>(out, ((uint32_t)r * (uint32_t)ldc + (uint32_t)n) * 2u, n, N, v);
-    }
-    __device__ __forceinline__ __amdgpu_buffer_rsrc_t out_rows(int m0, int rows) const
-    {
-        return make_rsrc(C + (int64_t)m0 * ldc, (uint32_t)min(rows, M - m0) * (uint32_t)ldc * 2u);
+        return ldb;
     }
     template <class T>
-    __device__ __forceinline__ void epilogue(const Tile& t, const Acc<T>& acc, int lane, int wm, int wn,
-                                             unsigned char*) const
+    __device__ __forceinline__ void epilogue(const Tile& t, const f32x4 (&acc)[T::FM][T::FN], int lane, int wave,
+                                             unsigned char*, unsigned char*) const
     {
-        const __amdgpu_buffer_rsrc_t out = out_rows(t.m0, T::BM);
+        const __amdgpu_buffer_rsrc_t out =
+            make_rsrc(C + (int64_t)t.m0 * ldc, (uint32_t)min(T::BM, M - t.m0) * (uint32_t)ldc * 2u);
 #pragma unroll
-        for (int i = 0; i < T::FM; ++i)
-#pragma unroll
-            for (int j = 0; j < T::FN; ++j)
-                finish(out, wm * T::WTM + i * 16 + (lane & 15), t.n0 + wn * T::WTN + j * 16 + 4 * (lane >> 4),
-                       acc[i][j]);
-    }
-    template <class T>
-    __device__ __forceinline__ void epilogue256(const Tile& t, const f32x4 (&acc)[8][8], int lane, int wave,
-                                                unsigned char*, unsigned char*) const
-    {
-        const __amdgpu_buffer_rsrc_t out = out_rows(t.m0, 256);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
+        for (int i = 0; i < T::FM; ++i) {
             const int ln = pinned(lane);
+            const int r = wave / T::WAVES_N * T::WTM + i * 16 + (ln & 15);
 #pragma unroll
-            for (int j = 0; j < 8; ++j)
-                finish(out, (wave >> 1) * 128 + i * 16 + (ln & 15), t.n0 + (wave & 1) * 128 + j * 16 + 4 * (ln >> 4),
-                       acc[i][j]);
+            for (int j = 0; j < T::FN; ++j) {
+                const int n = t.n0 + wave % T::WAVES_N * T::WTN + j * 16 + 4 * (ln >> 4);
+                buffer_store4<E, WHOLE>(out, ((uint32_t)r * (uint32_t)ldc + (uint32_t)n) * 2u, n, N, acc[i][j]);
+            }
         }
     }
 };

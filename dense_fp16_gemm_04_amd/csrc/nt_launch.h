@@ -22,59 +22,64 @@ inline int num_cus()
     return n;
 }
 
-// Time of `tiles` tiles of edge x edge sums over K: whole waves of tiles over
-// the CUs at the rate that the kernel sustains on a full chip, plus a fixed
-// cost per wave; a wave that leaves CUs idle runs the others up to 1.25 times
-// faster (clock and L2 headroom).
+// The kernels, by their tiles, with the rate that each sustains on a full
+// chip and the fixed cost of a wave of tiles (pipeline fill and epilogue).
 struct Kind {
-    int edge;
-    double tflops;   // on a full chip of 256 CUs
-    double wave_us;  // pipeline fill and epilogue
+    int bm, bn;
+    double tflops;  // on 256 CUs
+    double wave_us;
 };
-constexpr Kind kKinds[] = {{256, 1450.0, 4.0}, {128, 760.0, 3.0}, {64, 480.0, 3.0}};
+constexpr Kind kKinds[] = {{256, 256, 1450.0, 4.0}, {256, 128, 1250.0, 3.0}, {128, 128, 1050.0, 3.0}, {64, 64, 480.0, 3.0}};
+constexpr int kNumKinds = 4;
 
+// Time of `tiles` tiles of sums over K: whole waves of tiles over the CUs at
+// the kernel's rate plus the fixed cost of each; a wave that leaves CUs idle
+// runs the others up to 1.25 times faster (clock and L2 headroom).
 inline double model_us(const Kind& k, int64_t tiles, int64_t K, int cus)
 {
     const int64_t full = tiles / cus, rest = tiles % cus;
-    const double us = 2.0 * k.edge * k.edge * (double)K / (k.tflops * 1e12 / 256) * 1e6;
+    const double us = 2.0 * k.bm * k.bn * (double)K / (k.tflops * 1e12 / 256) * 1e6;
     double sum = (double)full * (us + k.wave_us);
     if (rest) sum += us / (1.0 + 0.25 * (1.0 - (double)rest / cus)) + k.wave_us;
     return sum;
 }
 
-// Runs OP over `count(edge)` tiles with the kernel that the model finds
-// fastest.  256 x 256 tiles need three K steps and
-// an OP that offers them (kPersist).
+// Runs OP over `count(kind)` tiles with the kernel that the model finds
+// fastest (a count of -1: not with this kind).  256 x 256 tiles need three K
+// steps and an OP that offers them (kPersist).
 template <class E, class OP, class Count, class Prepare>
 int launch(OP op, int64_t K, Count count, Prepare prepare, hipStream_t stream)
 {
     const int cus = num_cus();
     int best = -1;
+    int64_t tiles = 0;
     double best_us = 0;
-    for (int i = 0; i < 3; ++i) {
-        if (kKinds[i].edge == 256 && (!OP::kPersist || K <= 128)) continue;
-        const double us = model_us(kKinds[i], count(kKinds[i].edge), K, cus);
+    for (int i = 0; i < kNumKinds; ++i) {
+        if (i == 0 && (!OP::kPersist || K <= 128)) continue;
+        const int64_t n = count(kKinds[i]);
+        if (n < 0) continue;
+        const double us = model_us(kKinds[i], n, K, cus);
         if (best < 0 || us < best_us) {
             best = i;
             best_us = us;
+            tiles = n;
         }
     }
-    const int64_t tiles = count(kKinds[best].edge);
     if (tiles > abi::kMaxDim) return hipErrorInvalidValue;
     if (tiles == 0) return hipSuccess;
     op.tiles = (int)tiles;
-    prepare(op, kKinds[best].edge);
-    if constexpr (OP::kPersist) {
-        if (best == 0) {
+    prepare(op, kKinds[best]);
+    const dim3 grid((unsigned)tiles);
+    if constexpr (OP::kPersist)
+        if (best == 0)
             hipLaunchKernelGGL((nt_persist<Shape256<E>, OP>), dim3((unsigned)std::min<int64_t>(tiles, cus)), dim3(256),
                                0, stream, op);
-            return (int)hipGetLastError();
-        }
-    }
-    if (best == 1)
-        hipLaunchKernelGGL((nt_tile<Shape<E, 128, 128, 3, 1>, OP>), dim3((unsigned)tiles), dim3(256), 0, stream, op);
-    else
-        hipLaunchKernelGGL((nt_tile<Shape<E, 64, 64, 3, 2>, OP>), dim3((unsigned)tiles), dim3(256), 0, stream, op);
+    if constexpr (OP::kOblong)
+        if (best == 1)
+            hipLaunchKernelGGL((nt_ordered<Shape<E, 256, 128, 4, 2, 3, 1, 4>, OP>), grid, dim3(512), 0, stream, op);
+    if (best == 2)
+        hipLaunchKernelGGL((nt_ordered<Shape<E, 128, 128, 2, 4, 3, 1, 4>, OP>), grid, dim3(512), 0, stream, op);
+    if (best == 3) hipLaunchKernelGGL((nt_tile<Shape<E, 64, 64, 2, 2, 3, 2, 4>, OP>), grid, dim3(256), 0, stream, op);
     return (int)hipGetLastError();
 }
 
@@ -83,13 +88,13 @@ int launch(OP op, int64_t K, Count count, Prepare prepare, hipStream_t stream)
 template <class E, class OP>
 int launch_grid(const OP& op, int64_t rows, int64_t cols, int split, int64_t batch, int64_t K, hipStream_t stream)
 {
-    auto tm = [=](int64_t edge) { return (rows + edge - 1) / edge; };
-    auto tn = [=](int64_t edge) { return (cols * split + edge - 1) / edge; };
+    auto tm = [=](const Kind& k) { return (rows + k.bm - 1) / k.bm; };
+    auto tn = [=](const Kind& k) { return (cols * split + k.bn - 1) / k.bn; };
     return launch<E>(
-        op, K, [=](int64_t edge) { return tm(edge) * tn(edge) * batch; },
-        [=](OP& o, int edge) {
-            o.tiles_m = (int)tm(edge);
-            o.tiles_n = (int)tn(edge);
+        op, K, [=](const Kind& k) { return tm(k) * tn(k) * batch; },
+        [=](OP& o, const Kind& k) {
+            o.tiles_m = (int)tm(k);
+            o.tiles_n = (int)tn(k);
         },
         stream);
 }

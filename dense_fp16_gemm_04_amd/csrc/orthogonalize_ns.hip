@@ -25,22 +25,37 @@ using namespace nt;
 typedef _Float16 half;
 using half4 = Elem<half>::x4;
 
-constexpr int kNormBlocks = 64;  // partial sums of squares per matrix
+constexpr int kNormBlocks = 256;  // partial sums of squares per matrix
 
 // Partial sums of squares, in 64 bits (a 32-bit sum would overflow for
-// entries past 2^63 and lose small ones beside large ones).
+// entries past 2^63 and lose small ones beside large ones).  Four elements of
+// a row at a time; `per`: groups of four to a row.
 template <class E>
 __global__ void __launch_bounds__(256) ns_squares(const E* __restrict__ G, int64_t ldg, int64_t stride, int rows,
-                                                  int cols, double* __restrict__ partial)
+                                                  int cols, int per, int vec, double* __restrict__ partial)
 {
     const int b = blockIdx.x / kNormBlocks, k = blockIdx.x % kNormBlocks;
     const E* g = G + b * stride;
     double s = 0;
-    const int64_t total = (int64_t)rows * cols;
-    for (int64_t i = (int64_t)k * 256 + threadIdx.x; i < total; i += kNormBlocks * 256) {
-        const int64_t r = i / cols;
-        const double v = (double)(float)g[r * ldg + (i - r * cols)];
-        s += v * v;
+    // a workgroup takes pieces of 256 groups of a row, or several short rows
+    const int lanes = min(per, 256), step = 256 / lanes, pieces = (per + 255) / 256;
+    const int lane = threadIdx.x % lanes, first = threadIdx.x / lanes;
+    const int64_t units = first < step ? (int64_t)rows * pieces : 0;
+    typedef E x4 __attribute__((ext_vector_type(4)));
+    for (int64_t u = (int64_t)k * step + first; u < units; u += kNormBlocks * step) {
+        const int64_t r = pieces == 1 ? u : u / pieces;
+        const int c = ((int)(u - r * pieces) * 256 + lane) * 4;
+        const E* at = g + r * ldg + c;
+        x4 v = {};
+        if (vec && c + 3 < cols) {
+            v = *(const x4*)at;
+        } else {
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (c + e < cols) v[e] = at[e];
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s += (double)(float)v[e] * (double)(float)v[e];
     }
     __shared__ double part[256];
     part[threadIdx.x] = s;
@@ -58,20 +73,21 @@ template <class E>
 __global__ void __launch_bounds__(relayout::kThreads)
 ns_start(const E* __restrict__ G, int64_t ldg, int64_t stride_g, int rows, int cols, const double* __restrict__ partial,
          double eps, double scale, half* __restrict__ D1, half* __restrict__ D2, int64_t stride_x, int p1, int p2,
-         int tiles_r, int tiles_c)
+         int tiles_r, int tiles_c, int vec)
 {
     using namespace relayout;
     __shared__ half tile[kTile * kPitch];
-    __shared__ float factor;
     const int per = tiles_r * tiles_c, b = blockIdx.x / per, id = blockIdx.x % per;
     const int r0 = id / tiles_c * kTile, c0 = id % tiles_c * kTile;
-    if (threadIdx.x == 0) {
-        double s = 0;
-        for (int i = 0; i < kNormBlocks; ++i) s += partial[b * kNormBlocks + i];
-        factor = (float)(scale / (sqrt(s) + eps));
+    __shared__ double part[4];
+    {
+        static_assert(kNormBlocks == kThreads, "one partial sum per thread");
+        double s = partial[b * kNormBlocks + threadIdx.x];
+        for (int d = 32; d > 0; d >>= 1) s += __shfl_xor(s, d);
+        if (threadIdx.x % 64 == 0) part[threadIdx.x / 64] = s;
     }
     __syncthreads();
-    const float f = factor;
+    const float f = (float)(scale / (sqrt(part[0] + part[1] + part[2] + part[3]) + eps));
     const E* g = G + b * stride_g;
     half* d1 = D1 + b * stride_x;
     const int x = threadIdx.x & 15, y = threadIdx.x >> 4;
@@ -80,9 +96,17 @@ ns_start(const E* __restrict__ G, int64_t ldg, int64_t stride_g, int rows, int c
         const int r = it * 16 + y, c = c0 + x * 4;
         half4 v = {};
         if (r0 + r < rows) {
+            const E* at = g + (r0 + r) * ldg + c;
+            if (vec && c + 3 < cols) {
+                typedef E x4 __attribute__((ext_vector_type(4)));
+                const x4 w = *(const x4*)at;
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-                if (c + e < cols) v[e] = (half)((float)g[(r0 + r) * ldg + c + e] * f);
+                for (int e = 0; e < 4; ++e) v[e] = (half)((float)w[e] * f);
+            } else {
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    if (c + e < cols) v[e] = (half)((float)at[e] * f);
+            }
             if (c < p1) *(half4*)(d1 + (int64_t)(r0 + r) * p1 + c) = v;
         }
         *(half4*)(tile + r * kPitch + x * 4) = v;
@@ -123,23 +147,24 @@ __device__ __forceinline__ Rows rows_at(E* base, int row, int rows, int most, in
 // (8 bytes, 16 for the transpose) or element by element.
 enum { kAsIs = 1, kTurned = 2, kPieces = 4 };
 
-// Writes the BM x BN tile at (m0, n0), of which a wave holds FM x FN blocks
-// of 16 x 16.  The transpose goes through LDS: a lane's four values belong to
+// Writes the tile at (m0, n0).  The transpose goes through LDS: a lane's four values belong to
 // four of its rows.  It is staged as rows n of BM columns m, ROUNDS turns of
 // BN / ROUNDS rows, wave column wn's in stage[wn]; 16-byte chunk c of row n
 // sits at c ^ 2 ((n / 4) % 8), so that the four rows that 64 lanes write lie
 // in different banks.  It then leaves in whole rows, 16 bytes per lane.
-template <class E, int HOW, int BM, int FM, int FN, int ROUNDS, class Value>
-__device__ __forceinline__ void write_tile(const f32x4 (&acc)[FM][FN], Value value, const Rows& direct,
+template <class E, int HOW, class T, class Value>
+__device__ __forceinline__ void write_tile(const f32x4 (&acc)[T::FM][T::FN], Value value, const Rows& direct,
                                            const Rows& turned, int m0, int n0, int lane, int wave,
                                            unsigned char* stage0, unsigned char* stage1)
 {
-    constexpr int WTM = FM * 16, WTN = FN * 16, PITCH = BM * 2, CH = BM / 8;
-    constexpr int RW = WTN / ROUNDS;                   // staged rows per wave column
-    constexpr int RPI = 64 / CH, ITERS = 2 * RW / 4 / RPI;  // rows per wave-wide read; reads per wave
-    static_assert(ITERS * RPI * 4 == 2 * RW, "rows split evenly over the waves");
-    const int wm = wave >> 1, wn = wave & 1;
-    unsigned char* mine = wn ? stage1 : stage0;
+    constexpr int FM = T::FM, FN = T::FN, WTM = T::WTM, WTN = T::WTN, ROUNDS = T::ROUNDS;
+    constexpr int PITCH = T::BM * 2, CH = T::BM / 8;
+    constexpr int RW = WTN / ROUNDS;  // staged rows per wave column
+    constexpr int RPI = 64 / CH;      // rows per wave-wide read
+    constexpr int ITERS = T::WAVES_N * RW / T::WAVES / RPI;
+    static_assert(ITERS * RPI * T::WAVES == T::WAVES_N * RW, "rows split evenly over the waves");
+    const int wm = wave / T::WAVES_N, wn = wave % T::WAVES_N;
+    unsigned char* mine = wn ? stage1 + (wn - 1) * RW * PITCH : stage0;
 #pragma unroll
     for (int h = 0; h < ROUNDS; ++h) {
 #pragma unroll
@@ -171,7 +196,7 @@ __device__ __forceinline__ void write_tile(const f32x4 (&acc)[FM][FN], Value val
             for (int it = 0; it < ITERS; ++it) {
                 const int row = (wave * ITERS + it) * RPI + ln / CH;  // of both wave columns'
                 const int side = row / RW, local = row - side * RW, ch = ln % CH;
-                const unsigned char* from = (side ? stage1 : stage0) + local * PITCH +
+                const unsigned char* from = (side ? stage1 + (side - 1) * RW * PITCH : stage0) + local * PITCH +
                                             ((ch ^ ((2 * ((local >> 2) & 7)) & (CH - 1))) << 4);
                 const typename Elem<E>::x8 v = *(const typename Elem<E>::x8*)from;
                 const int m = m0 + ch * 8;
@@ -198,7 +223,7 @@ __device__ __forceinline__ void write_tile(const f32x4 (&acc)[FM][FN], Value val
 // their transposes.
 template <bool POLY>
 struct SymmetricOp {
-    static constexpr bool kPersist = true;
+    static constexpr bool kPersist = true, kOblong = false;  // (square tiles)
     const half* A;
     half* C;
     int M, K, lda, mp, tiles, per;  // per: tiles of one matrix
@@ -206,9 +231,8 @@ struct SymmetricOp {
     float alpha, beta, gamma;
 
     template <int BM, int BN>
-    __device__ __forceinline__ bool tile(int id, Tile& t) const
+    __device__ __forceinline__ void tile(int id, Tile& t) const
     {
-        static_assert(BM == BN, "square tiles");
         t.batch = id / per;
         id -= t.batch * per;
         // row r of the triangle holds tiles r (r + 1) / 2 .. + r
@@ -217,29 +241,32 @@ struct SymmetricOp {
         while ((r + 1) * (r + 2) / 2 <= id) ++r;
         t.m0 = r * BM;
         t.n0 = (id - r * (r + 1) / 2) * BN;
-        return true;
     }
     __device__ __forceinline__ const half* a_rows(const Tile& t, int row, int& n) const
     {
         return rows_from(A + t.batch * stride_a, t.m0 + row, M, lda, n);
     }
-    template <int BN>
+    template <int WTN>
     __device__ __forceinline__ const half* b_rows(const Tile& t, int row, int& n) const
     {
         return rows_from(A + t.batch * stride_a, t.n0 + row, M, lda, n);
     }
-    __device__ __forceinline__ int b_pitch(int) const { return lda; }
-    template <int BM, int FM, int FN, int ROUNDS>
-    __device__ __forceinline__ void write(const Tile& t, const f32x4 (&acc)[FM][FN], int lane, int wave,
-                                          unsigned char* stage0, unsigned char* stage1) const
+    template <int WTN>
+    __device__ __forceinline__ int b_pitch(int) const
+    {
+        return lda;
+    }
+    template <class T>
+    __device__ __forceinline__ void epilogue(const Tile& t, const f32x4 (&acc)[T::FM][T::FN], int lane, int wave,
+                                             unsigned char* s0, unsigned char* s1) const
     {
         half* c = C + t.batch * stride_c;
-        const Rows direct = rows_at(c, t.m0, M, BM, mp, mp);
+        const Rows direct = rows_at(c, t.m0, M, T::BM, mp, mp);
         // Rows M .. mp - 1 of the accumulator are zero: the transpose's
         // padding.  A tile on the diagonal has no mirror image to write.
-        Rows turned = rows_at(c, t.n0, M, BM, mp, mp);
+        Rows turned = rows_at(c, t.n0, M, T::BN, mp, mp);
         if (t.m0 == t.n0) turned.rs = make_rsrc(c, 0);
-        const Rows old = rows_at(A + t.batch * stride_a, t.m0, M, BM, lda, mp);
+        const Rows old = rows_at(A + t.batch * stride_a, t.m0, M, T::BM, lda, mp);
         auto value = [&](int r, int col, const f32x4& sum) __attribute__((always_inline)) {
             f32x4 v = sum * alpha;
             if constexpr (POLY) {
@@ -252,20 +279,7 @@ struct SymmetricOp {
             }
             return v;
         };
-        write_tile<half, kAsIs | kTurned | kPieces, BM, FM, FN, ROUNDS>(acc, value, direct, turned, t.m0, t.n0, lane,
-                                                                        wave, stage0, stage1);
-    }
-    template <class T>
-    __device__ __forceinline__ void epilogue(const Tile& t, const Acc<T>& acc, int lane, int wm, int wn,
-                                             unsigned char* smem) const
-    {
-        write<T::BM, T::FM, T::FN, 1>(t, acc, lane, wm * 2 + wn, smem, smem + T::BM * T::WTN * 2);
-    }
-    template <class T>
-    __device__ __forceinline__ void epilogue256(const Tile& t, const f32x4 (&acc)[8][8], int lane, int wave,
-                                                unsigned char* s0, unsigned char* s1) const
-    {
-        write<256, 8, 8, 2>(t, acc, lane, wave, s0, s1);
+        write_tile<half, kAsIs | kTurned | kPieces, T>(acc, value, direct, turned, t.m0, t.n0, lane, wave, s0, s1);
     }
 };
 
@@ -275,7 +289,7 @@ struct SymmetricOp {
 template <bool LAST, int HOW>
 struct ApplyOp {
     // (element by element, the 256 x 256 kernel would spill scalar registers)
-    static constexpr bool kPersist = (HOW & kPieces) != 0;
+    static constexpr bool kPersist = (HOW & kPieces) != 0, kOblong = true;
     const half *P, *Xt;
     half *X, *XtNew;
     __bf16* out;
@@ -284,7 +298,7 @@ struct ApplyOp {
     float alpha;
 
     template <int BM, int BN>
-    __device__ __forceinline__ bool tile(int id, Tile& t) const
+    __device__ __forceinline__ void tile(int id, Tile& t) const
     {
         const int per = tiles_m * tiles_n;
         t.batch = id / per;
@@ -292,50 +306,39 @@ struct ApplyOp {
         tile_of(id - t.batch * per, tiles_m, tiles_n, tm, tn);
         t.m0 = tm * BM;
         t.n0 = tn * BN;
-        return true;
     }
     __device__ __forceinline__ const half* a_rows(const Tile& t, int row, int& n) const
     {
         return rows_from(P + t.batch * stride_p, t.m0 + row, M, lda, n);
     }
-    template <int BN>
+    template <int WTN>
     __device__ __forceinline__ const half* b_rows(const Tile& t, int row, int& n) const
     {
         return rows_from(Xt + t.batch * stride_x, t.n0 + row, N, ldb, n);
     }
-    __device__ __forceinline__ int b_pitch(int) const { return ldb; }
-    template <int BM, int FM, int FN, int ROUNDS>
-    __device__ __forceinline__ void write(const Tile& t, const f32x4 (&acc)[FM][FN], int lane, int wave,
-                                          unsigned char* stage0, unsigned char* stage1) const
+    template <int WTN>
+    __device__ __forceinline__ int b_pitch(int) const
+    {
+        return ldb;
+    }
+    template <class T>
+    __device__ __forceinline__ void epilogue(const Tile& t, const f32x4 (&acc)[T::FM][T::FN], int lane, int wave,
+                                             unsigned char* s0, unsigned char* s1) const
     {
         auto value = [&](int, int, const f32x4& sum) __attribute__((always_inline)) { return LAST ? sum * alpha : sum; };
         if constexpr (LAST) {
             __bf16* o = out + t.batch * stride_o;
             Rows direct = {}, turned = {};
-            if constexpr (HOW & kAsIs) direct = rows_at(o, t.m0, M, BM, ldo, N);
-            if constexpr (HOW & kTurned) turned = rows_at(o, t.n0, N, BM, ldo, M);
-            write_tile<__bf16, HOW, BM, FM, FN, ROUNDS>(acc, value, direct, turned, t.m0, t.n0, lane, wave, stage0,
-                                                        stage1);
+            if constexpr (HOW & kAsIs) direct = rows_at(o, t.m0, M, T::BM, ldo, N);
+            if constexpr (HOW & kTurned) turned = rows_at(o, t.n0, N, T::BN, ldo, M);
+            write_tile<__bf16, HOW, T>(acc, value, direct, turned, t.m0, t.n0, lane, wave, s0, s1);
         } else {
             // (columns N .. np - 1 and rows M .. ldb - 1 of the accumulator
             // are zero: the padding of both)
-            const Rows direct = rows_at(X + t.batch * stride_x, t.m0, M, BM, np, np);
-            const Rows turned = rows_at(XtNew + t.batch * stride_x, t.n0, N, BM, ldb, ldb);
-            write_tile<half, HOW, BM, FM, FN, ROUNDS>(acc, value, direct, turned, t.m0, t.n0, lane, wave, stage0,
-                                                      stage1);
+            const Rows direct = rows_at(X + t.batch * stride_x, t.m0, M, T::BM, np, np);
+            const Rows turned = rows_at(XtNew + t.batch * stride_x, t.n0, N, T::BN, ldb, ldb);
+            write_tile<half, HOW, T>(acc, value, direct, turned, t.m0, t.n0, lane, wave, s0, s1);
         }
-    }
-    template <class T>
-    __device__ __forceinline__ void epilogue(const Tile& t, const Acc<T>& acc, int lane, int wm, int wn,
-                                             unsigned char* smem) const
-    {
-        write<T::BM, T::FM, T::FN, 1>(t, acc, lane, wm * 2 + wn, smem, smem + T::BM * T::WTN * 2);
-    }
-    template <class T>
-    __device__ __forceinline__ void epilogue256(const Tile& t, const f32x4 (&acc)[8][8], int lane, int wave,
-                                                unsigned char* s0, unsigned char* s1) const
-    {
-        write<256, 8, 8, 2>(t, acc, lane, wave, s0, s1);
     }
 };
 
@@ -370,10 +373,10 @@ int64_t triangle(int64_t t) { return t * (t + 1) / 2; }
 template <class OP>
 int launch_symmetric(const OP& op, int64_t m, int64_t batch, hipStream_t stream)
 {
-    auto per = [=](int64_t edge) { return triangle((m + edge - 1) / edge); };
+    auto per = [=](const Kind& k) { return triangle((m + k.bm - 1) / k.bm); };
     return launch<half>(
-        op, op.K, [=](int64_t edge) { return per(edge) * batch; }, [=](OP& o, int edge) { o.per = (int)per(edge); },
-        stream);
+        op, op.K, [=](const Kind& k) { return k.bm == k.bn ? per(k) * batch : -1; },
+        [=](OP& o, const Kind& k) { o.per = (int)per(k); }, stream);
 }
 
 template <class E>
@@ -388,8 +391,9 @@ int run(const E* G, __bf16* out, int64_t batch, int64_t rows, int64_t cols, int6
     const int k = std::min(12, (int)std::lround(0.5 * std::log2((double)w.n)));
     const double scale = std::ldexp(1.0, k);
     int rc;
+    const int vec = (uintptr_t)G % (4 * sizeof(E)) == 0 && ldg % 4 == 0 && stride_g % 4 == 0;
     hipLaunchKernelGGL(ns_squares<E>, dim3((unsigned)(batch * kNormBlocks)), dim3(256), 0, stream, G, ldg, stride_g,
-                       (int)rows, (int)cols, w.partial);
+                       (int)rows, (int)cols, (int)((cols + 3) / 4), vec, w.partial);
     if ((rc = (int)hipGetLastError())) return rc;
     const int64_t pr = abi::up(rows, 8), pc = abi::up(cols, 8);
     const int64_t tr = (pr + 63) / 64, tc = (pc + 63) / 64;
@@ -397,7 +401,7 @@ int run(const E* G, __bf16* out, int64_t batch, int64_t rows, int64_t cols, int6
     half* d1 = tall ? w.xt[0] : w.x[0];
     half* d2 = tall ? w.x[0] : w.xt[0];
     hipLaunchKernelGGL(ns_start<E>, dim3((unsigned)(tr * tc * batch)), dim3(256), 0, stream, G, ldg, stride_g, (int)rows,
-                       (int)cols, w.partial, eps, scale, d1, d2, w.stride_x, (int)pc, (int)pr, (int)tr, (int)tc);
+                       (int)cols, w.partial, eps, scale, d1, d2, w.stride_x, (int)pc, (int)pr, (int)tr, (int)tc, vec);
     if ((rc = (int)hipGetLastError())) return rc;
     if (steps == 0) {
         const int64_t total = batch * rows * cols;
