@@ -1,9 +1,12 @@
 // Products of a few rows with 4-bit weights for gfx950: include/gemv_w4.h.
 //
-// A workgroup of eight waves takes 16 rows of W and 16 * MB rows of X; the
-// waves share K in chunks of 128, each adds up its own in registers, and the
-// eight partial sums meet in LDS.  Per chunk a lane reads 16 bytes (32 codes)
-// of one row of W, so a wave reads 64 adjacent bytes of each of its 16 rows.
+// A workgroup of eight waves takes 16 R rows of W and 16 MB rows of X; the
+// waves share K in ranges of whole chunks of 128, each adds up its own in
+// registers, and the eight partial sums meet in LDS.  Per chunk a lane reads
+// 16 bytes (32 codes) of one row of W, so a wave reads 64 adjacent bytes of
+// each of 16 rows.  W is read once per 16 MB rows of X and x, from L2, once per
+// 16 R rows of W; what counts is bytes in flight: codes are loaded WD chunks
+// ahead, x XD runs of 32 k ahead.
 //
 // Lane l = 16 h + r holds codes 32 h .. + 31 of row r as four words.  The
 // matrix cores sum over the lanes h, so a sum that one scale can be applied
@@ -80,152 +83,238 @@ __device__ __forceinline__ u32x4 pair_order(const u32x4& x)
     return v;
 }
 
+// One, two or four adjacent 16-bit values, two to a register.
+template <int N>
+struct Few {
+    uint32_t v[(N + 1) / 2];
+};
+// Loads the first n (the same for all lanes).
+template <class E, int N>
+__device__ __forceinline__ void load_few(Few<N>& f, const E* p, int n)
+{
+    if (n == N) {
+        if constexpr (N == 1)
+            f.v[0] = *(const uint16_t*)p;
+        else
+            __builtin_memcpy(f.v, p, 2 * N);
+    } else {
+#pragma unroll
+        for (int i = 0; i < (N + 1) / 2; ++i) {
+            const uint32_t lo = 2 * i < n ? ((const uint16_t*)p)[2 * i] : 0;
+            const uint32_t hi = 2 * i + 1 < n ? ((const uint16_t*)p)[2 * i + 1] : 0;
+            f.v[i] = lo | hi << 16;
+        }
+    }
+}
+template <class E, int N>
+__device__ __forceinline__ float few(const Few<N>& f, int i)
+{
+    const uint32_t word = f.v[i / 2];
+    const uint16_t bits = (uint16_t)(i % 2 ? word >> 16 : word);
+    return (float)__builtin_bit_cast(E, bits);
+}
+
 // FLUSH: runs of 32 k per group sum (4: the group holds whole chunks).
-template <class E, int MB, int FLUSH, bool ZERO>
+template <class E, int MB, int R, int FLUSH, bool ZERO>
 __global__ void __launch_bounds__(kThreads)
 gemv_w4_kernel(const E* __restrict__ X, const unsigned char* __restrict__ Q, const E* __restrict__ scale,
                const E* __restrict__ zero, E* __restrict__ Y, int M, int N, int K, int shift, int groups, int64_t ldx,
-               int64_t ldq, int64_t ldy, int x_vec)
+               int64_t ldq, int64_t ldy)
 {
+    using x8 = typename Elem<E>::x8;
     constexpr bool SUM = ZERO || !Code<E>::exact;  // the group's sum of x is needed
-    __shared__ float part[kWaves][MB][16][17];
+    constexpr int SC = 4 / FLUSH;                  // scales of a chunk
+    constexpr int WD = MB * R == 1 ? 4 : MB * R <= 4 ? 2 : 1, XD = MB == 1 ? 4 : MB == 2 ? 2 : 1;
+    __shared__ float part[kWaves][MB * R][16][17];
     const int lane = threadIdx.x & (kWave - 1);
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
     const int r = lane & 15, h = lane >> 4;
-    const int n0 = blockIdx.x * 16, m0 = blockIdx.y * 16 * MB;
-    const int n = min(n0 + r, N - 1);  // rows past N repeat the last one and are not stored
-    const unsigned char* q = Q + n * ldq;
-    const E* srow = scale + (int64_t)n * groups;
-    const E* zrow = ZERO ? zero + (int64_t)n * groups : nullptr;
-
-    f32x4 total[MB];
+    const int n0 = blockIdx.x * 16 * R, m0 = blockIdx.y * 16 * MB;
+    // Rows past the end repeat the last one: what they give is not stored.
+    const unsigned char* q[R];
+    const E *sp[R], *zp[R], *xp[MB];
 #pragma unroll
-    for (int b = 0; b < MB; ++b) total[b] = f32x4{0, 0, 0, 0};
-
-    auto load_x = [&](int b, int k) __attribute__((always_inline)) {
-        const int m = m0 + b * 16 + r;
-        u32x4 v = {0, 0, 0, 0};
-        if (m < M && k < K) {
-            const E* p = X + m * ldx + k;
-            if (x_vec) {
-                v = *(const u32x4*)p;
-            } else {
-                typename Elem<E>::x8 e;
+    for (int i = 0; i < R; ++i) {
+        const int64_t n = min(n0 + 16 * i + r, N - 1);
+        q[i] = Q + n * ldq + 16 * h;
+        sp[i] = scale + n * groups;
+        zp[i] = ZERO ? zero + n * groups : nullptr;
+    }
 #pragma unroll
-                for (int i = 0; i < 8; ++i) e[i] = p[i];
-                v = __builtin_bit_cast(u32x4, e);
-            }
+    for (int b = 0; b < MB; ++b) xp[b] = X + (int64_t)min(m0 + 16 * b + r, M - 1) * ldx + 8 * h;
+
+    f32x4 total[R][MB], acc[R][MB], sum[MB];
+#pragma unroll
+    for (int i = 0; i < R; ++i)
+#pragma unroll
+        for (int b = 0; b < MB; ++b) total[i][b] = f32x4{0, 0, 0, 0};
+
+    const int chunks = (K + kChunk - 1) / kChunk, each = (chunks + kWaves - 1) / kWaves;
+    const int first = wave * each, last = min(first + each, chunks), runs = min(last * 4, K / 32);
+    struct Chunk {
+        u32x4 w[R];
+        Few<SC> s[R], z[R];
+    } c[WD];
+    u32x4 x[XD][MB];
+    auto fetch = [&](Chunk& c, int at) __attribute__((always_inline)) {
+        const int k0 = at * kChunk;
+        const bool whole = k0 + kChunk <= K;  // (the same for all lanes)
+#pragma unroll
+        for (int i = 0; i < R; ++i) {
+            if (whole || k0 + 32 * h < K)
+                c.w[i] = *(const u32x4*)(q[i] + k0 / 2);
+            else
+                c.w[i] = u32x4{0, 0, 0, 0};
+            // the chunk's scales lie side by side where a group is shorter than it
+            const int group = k0 >> shift, n = whole ? SC : min(SC, groups - group);
+            load_few<E, SC>(c.s[i], sp[i] + group, n);
+            if constexpr (ZERO) load_few<E, SC>(c.z[i], zp[i] + group, n);
         }
-        return v;
     };
+    // (x of runs that the wave does not have is zero: the last chunk may hold
+    // fewer than four)
+    auto fetch_x = [&](u32x4 (&v)[MB], int run) __attribute__((always_inline)) {
+        if (run < runs)
+#pragma unroll
+            for (int b = 0; b < MB; ++b) __builtin_memcpy(&v[b], xp[b] + run * 32, 16);  // (any 2-byte boundary)
+        else
+#pragma unroll
+            for (int b = 0; b < MB; ++b) v[b] = u32x4{0, 0, 0, 0};
+    };
+    const u32x4 ones_bits = {Code<E>::ones, Code<E>::ones, Code<E>::ones, Code<E>::ones};
+    const x8 ones = __builtin_bit_cast(x8, ones_bits);
 
-    const int chunks = (K + kChunk - 1) / kChunk;
-    for (int c = wave; c < chunks; c += kWaves) {
-        const int k0 = c * kChunk;
-        u32x4 w = {0, 0, 0, 0};
-        if (k0 + 32 * h < K) w = *(const u32x4*)(q + k0 / 2 + 16 * h);
-        float s[4 / FLUSH], z[4 / FLUSH];
-#pragma unroll
-        for (int g = 0; g < 4 / FLUSH; ++g) {
-            const int at = min((k0 + 32 * FLUSH * g) >> shift, groups - 1);
-            s[g] = (float)srow[at];
-            z[g] = (ZERO ? (float)zrow[at] : 8.0f) - Code<E>::bias;
-        }
-        u32x4 x[4][MB];
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-#pragma unroll
-            for (int b = 0; b < MB; ++b) x[j][b] = load_x(b, k0 + 32 * j + 8 * h);
+    auto add = [&](Chunk& c, int at) __attribute__((always_inline)) {
         // 4 x 4 words across the lanes h: word j of lane h <- word h of lane j
-        {
+#pragma unroll
+        for (int i = 0; i < R; ++i) {
+            u32x4& w = c.w[i];
             auto a = __builtin_amdgcn_permlane32_swap(w[0], w[2], false, false);
             auto b = __builtin_amdgcn_permlane32_swap(w[1], w[3], false, false);
             auto lo = __builtin_amdgcn_permlane16_swap(a[0], b[0], false, false);
             auto hi = __builtin_amdgcn_permlane16_swap(a[1], b[1], false, false);
-            w[0] = lo[0];
-            w[1] = lo[1];
-            w[2] = hi[0];
-            w[3] = hi[1];
+            w = u32x4{lo[0], lo[1], hi[0], hi[1]};
         }
-        f32x4 acc[MB], sum[MB];
-        const u32x4 ones_bits = {Code<E>::ones, Code<E>::ones, Code<E>::ones, Code<E>::ones};
-        const typename Elem<E>::x8 ones = __builtin_bit_cast(typename Elem<E>::x8, ones_bits);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
+            // (one run after another where their sums would not fit together)
+            if constexpr (MB * R >= 8) __builtin_amdgcn_sched_barrier(0);
             if (j % FLUSH == 0)
 #pragma unroll
-                for (int b = 0; b < MB; ++b) acc[b] = sum[b] = f32x4{0, 0, 0, 0};
-            const typename Elem<E>::x8 wv = codes<E>(w[j]);
+                for (int b = 0; b < MB; ++b) {
+                    sum[b] = f32x4{0, 0, 0, 0};
+#pragma unroll
+                    for (int i = 0; i < R; ++i) acc[i][b] = f32x4{0, 0, 0, 0};
+                }
+            x8 xv[MB];
 #pragma unroll
             for (int b = 0; b < MB; ++b) {
-                const typename Elem<E>::x8 xv = __builtin_bit_cast(typename Elem<E>::x8, pair_order(x[j][b]));
-                acc[b] = Elem<E>::mfma(xv, wv, acc[b]);
-                if constexpr (SUM) sum[b] = Elem<E>::mfma(xv, ones, sum[b]);
+                xv[b] = __builtin_bit_cast(x8, pair_order(x[j % XD][b]));
+                if constexpr (SUM) sum[b] = Elem<E>::mfma(xv[b], ones, sum[b]);
+            }
+            fetch_x(x[j % XD], at * 4 + j + XD);
+#pragma unroll
+            for (int i = 0; i < R; ++i) {
+                const x8 wv = codes<E>(c.w[i][j]);
+#pragma unroll
+                for (int b = 0; b < MB; ++b) acc[i][b] = Elem<E>::mfma(xv[b], wv, acc[i][b]);
             }
             if (j % FLUSH == FLUSH - 1)
 #pragma unroll
-                for (int b = 0; b < MB; ++b)
+                for (int i = 0; i < R; ++i) {
+                    const float s = few<E, SC>(c.s[i], j / FLUSH);
+                    const float z = (ZERO ? few<E, SC>(c.z[i], j / FLUSH) : 8.0f) - Code<E>::bias;
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        float v = acc[b][e];
-                        if constexpr (SUM) v = __builtin_fmaf(-z[j / FLUSH], sum[b][e], v);
-                        total[b][e] = __builtin_fmaf(s[j / FLUSH], v, total[b][e]);
-                    }
+                    for (int b = 0; b < MB; ++b)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            float v = acc[i][b][e];
+                            if constexpr (SUM) v = __builtin_fmaf(-z, sum[b][e], v);
+                            total[i][b][e] = __builtin_fmaf(s, v, total[i][b][e]);
+                        }
+                }
         }
-    }
+    };
+
 #pragma unroll
-    for (int b = 0; b < MB; ++b)
+    for (int d = 0; d < WD; ++d)
+        if (first + d < last) fetch(c[d], first + d);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) part[wave][b][4 * h + e][r] = total[b][e];
+    for (int d = 0; d < XD; ++d) fetch_x(x[d], first * 4 + d);
+    for (int at = first; at < last; at += WD)
+#pragma unroll
+        for (int d = 0; d < WD; ++d)
+            if (at + d < last) {
+                add(c[d], at + d);
+                if (at + d + WD < last) fetch(c[d], at + d + WD);
+            }
+
+#pragma unroll
+    for (int i = 0; i < R; ++i)
+#pragma unroll
+        for (int b = 0; b < MB; ++b)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) part[wave][i * MB + b][4 * h + e][r] = total[i][b][e];
     __syncthreads();
-    for (int i = threadIdx.x; i < MB * 256; i += kThreads) {
-        const int b = i >> 8, m = (i >> 4) & 15, c = i & 15;
+    for (int at = threadIdx.x; at < R * MB * 256; at += kThreads) {
+        const int p = at >> 8, m = m0 + p % MB * 16 + ((at >> 4) & 15), n = n0 + p / MB * 16 + (at & 15);
         float v = 0.0f;
 #pragma unroll
-        for (int w = 0; w < kWaves; ++w) v += part[w][b][m][c];
-        if (m0 + b * 16 + m < M && n0 + c < N) Y[(int64_t)(m0 + b * 16 + m) * ldy + n0 + c] = (E)v;
+        for (int w = 0; w < kWaves; ++w) v += part[w][p][(at >> 4) & 15][at & 15];
+        if (m < M && n < N) Y[(int64_t)m * ldy + n] = (E)v;
     }
 }
 
-template <class E, int MB, int FLUSH, bool ZERO>
-int launch(const void* X, const void* Q, const void* scale, const void* zero, void* Y, int64_t M, int64_t N, int64_t K,
-           int shift, int64_t groups, int64_t ldx, int64_t ldq, int64_t ldy, hipStream_t stream)
+struct Args {
+    const void *X, *Q, *scale, *zero;
+    void* Y;
+    int64_t M, N, K;
+    int shift;
+    int64_t groups, ldx, ldq, ldy;
+    hipStream_t stream;
+};
+
+template <class E, int MB, int R, int FLUSH, bool ZERO>
+int launch(const Args& a)
 {
-    const int x_vec = (uintptr_t)X % 16 == 0 && (M == 1 || ldx % 8 == 0);
     // grid.y holds 65535 at most: more rows go in further launches
     constexpr int64_t most = (int64_t)65535 * 16 * MB;
-    for (int64_t m = 0; m < M; m += most) {
-        const int64_t rows = std::min(most, M - m);
-        hipLaunchKernelGGL((gemv_w4_kernel<E, MB, FLUSH, ZERO>),
-                           dim3((unsigned)((N + 15) / 16), (unsigned)((rows + 16 * MB - 1) / (16 * MB))), dim3(kThreads),
-                           0, stream, (const E*)X + m * ldx, (const unsigned char*)Q, (const E*)scale, (const E*)zero,
-                           (E*)Y + m * ldy, (int)rows, (int)N, (int)K, shift, (int)groups, ldx, ldq, ldy, x_vec);
+    for (int64_t m = 0; m < a.M; m += most) {
+        const int64_t rows = std::min(most, a.M - m);
+        hipLaunchKernelGGL((gemv_w4_kernel<E, MB, R, FLUSH, ZERO>),
+                           dim3((unsigned)((a.N + 16 * R - 1) / (16 * R)), (unsigned)((rows + 16 * MB - 1) / (16 * MB))),
+                           dim3(kThreads), 0, a.stream, (const E*)a.X + m * a.ldx, (const unsigned char*)a.Q,
+                           (const E*)a.scale, (const E*)a.zero, (E*)a.Y + m * a.ldy, (int)rows, (int)a.N, (int)a.K,
+                           a.shift, (int)a.groups, a.ldx, a.ldq, a.ldy);
         const int rc = (int)hipGetLastError();
         if (rc) return rc;
     }
     return hipSuccess;
 }
 
-template <class E, int MB, bool ZERO>
-int by_group(const void* X, const void* Q, const void* scale, const void* zero, void* Y, int64_t M, int64_t N, int64_t K,
-             int shift, int64_t groups, int64_t ldx, int64_t ldq, int64_t ldy, hipStream_t stream)
+template <class E, int MB, int R, int FLUSH>
+int by_zero(const Args& a)
 {
-    if (shift >= 7) return launch<E, MB, 4, ZERO>(X, Q, scale, zero, Y, M, N, K, shift, groups, ldx, ldq, ldy, stream);
-    if (shift == 6) return launch<E, MB, 2, ZERO>(X, Q, scale, zero, Y, M, N, K, shift, groups, ldx, ldq, ldy, stream);
-    return launch<E, MB, 1, ZERO>(X, Q, scale, zero, Y, M, N, K, shift, groups, ldx, ldq, ldy, stream);
+    return a.zero ? launch<E, MB, R, FLUSH, true>(a) : launch<E, MB, R, FLUSH, false>(a);
 }
 
 template <class E>
-int run(const void* X, const void* Q, const void* scale, const void* zero, void* Y, int64_t M, int64_t N, int64_t K,
-        int shift, int64_t groups, int64_t ldx, int64_t ldq, int64_t ldy, hipStream_t stream)
+int run(const Args& a)
 {
-#define ROWS(MB)                                                                                                 \
-    (zero ? by_group<E, MB, true>(X, Q, scale, zero, Y, M, N, K, shift, groups, ldx, ldq, ldy, stream)           \
-          : by_group<E, MB, false>(X, Q, scale, zero, Y, M, N, K, shift, groups, ldx, ldq, ldy, stream))
-    if (M <= 16) return ROWS(1);
-    if (M <= 32) return ROWS(2);
-    return ROWS(4);
-#undef ROWS
+    // as many rows of W to a workgroup as leave one for every CU; with 64 rows
+    // of X, groups of 32 need the registers that more rows of W would
+    const int64_t mb = a.M <= 16 ? 1 : a.M <= 32 ? 2 : 4;
+    const int64_t blocks = (a.N + 15) / 16 * ((a.M + 16 * mb - 1) / (16 * mb));
+    const bool two = blocks >= 2 * 256;
+#define BY_GROUP(MB, R)                             \
+    (a.shift >= 7   ? by_zero<E, MB, R, 4>(a)       \
+     : a.shift == 6 ? by_zero<E, MB, R, 2>(a)       \
+                    : by_zero<E, MB, R, 1>(a))
+    if (mb == 1) return two ? BY_GROUP(1, 2) : BY_GROUP(1, 1);
+    if (mb == 2) return two ? BY_GROUP(2, 2) : BY_GROUP(2, 1);
+    if (two && a.shift >= 6) return a.shift >= 7 ? by_zero<E, 4, 2, 4>(a) : by_zero<E, 4, 2, 2>(a);
+    return BY_GROUP(4, 1);
+#undef BY_GROUP
 }
 
 }  // namespace
@@ -257,8 +346,8 @@ int gemv_w4(const void* X, const void* Q, const void* scale, const void* zero, v
     int shift = 30;  // one group: every k belongs to it
     if (group != K)
         for (shift = 5; ((int64_t)1 << shift) < group; ++shift) {}
-    return type == GEMV_W4_F16 ? run<_Float16>(X, Q, scale, zero, Y, M, N, K, shift, groups, ldx, ldq, ldy, stream)
-                               : run<__bf16>(X, Q, scale, zero, Y, M, N, K, shift, groups, ldx, ldq, ldy, stream);
+    const Args a{X, Q, scale, zero, Y, M, N, K, shift, groups, ldx, ldq, ldy, stream};
+    return type == GEMV_W4_F16 ? run<_Float16>(a) : run<__bf16>(a);
 }
 
 }  // extern "C"

@@ -17,6 +17,8 @@ import ctypes
 import os
 import threading
 
+import torch
+
 from .binding import GemmError, _stream
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -49,6 +51,8 @@ SIGNATURES = {
 }
 
 ACTIVATIONS = {"silu": 0, "gelu_tanh": 1}
+_TYPES = {torch.float16: 0, torch.bfloat16: 1}
+_TYPES_AND_F32 = {**_TYPES, torch.float32: 2}
 
 _libs = {}
 _lock = threading.Lock()
@@ -78,51 +82,42 @@ def load(name: str):
     return _libs[name]
 
 
-def _types():
-    import torch
-    return {torch.float16: 0, torch.bfloat16: 1}
-
-
-def _check_matrix(name, t, dtypes, device=None, shape=None):
-    """t is a GPU matrix of one of `dtypes` whose rows do not overlap; its row pitch."""
-    import torch
+def _pitch(name, t, types, device=None, shape=None):
+    """The row pitch of t, a GPU matrix of one of `types` whose rows do not overlap."""
+    # (what holds is found out first and told apart only where it does not:
+    # these checks are half of a short call's time on the host)
+    if isinstance(t, torch.Tensor) and t.dtype in types and t.dim() == 2:
+        index = t.get_device()
+        rows, cols = size = t.shape
+        ld, one = t.stride()
+        if index >= 0 and (device is None or index == device) and (shape is None or size == shape) \
+                and (one == 1 or cols <= 1) and (ld >= cols or rows <= 1):
+            return ld if rows > 1 and cols > 0 else cols
     if not isinstance(t, torch.Tensor):
         raise TypeError("%s must be a torch tensor" % name)
-    if t.dtype not in dtypes:
-        raise TypeError("%s must be %s, got %s" % (name, " or ".join(str(d).replace("torch.", "") for d in dtypes),
+    if t.dtype not in types:
+        raise TypeError("%s must be %s, got %s" % (name, " or ".join(str(d).replace("torch.", "") for d in types),
                                                    str(t.dtype).replace("torch.", "")))
     if t.dim() != 2 or (shape is not None and tuple(t.shape) != tuple(shape)):
         raise ValueError("%s must be a matrix%s, got %s" % (
             name, "" if shape is None else " of shape %s" % (tuple(shape),), tuple(t.shape)))
     if not t.is_cuda or (device is not None and t.get_device() != device):
         raise ValueError("%s must be on %s" % (name, "a GPU" if device is None else "the first operand's GPU"))
-    rows, cols = t.shape
-    if (cols > 1 and t.stride(1) != 1) or (rows > 1 and cols > 0 and t.stride(0) < cols):
-        raise ValueError("%s must have adjacent elements in a row and rows that do not overlap, got strides %s" % (
-            name, t.stride()))
-    return t.stride(0) if rows > 1 and cols > 0 else cols
+    raise ValueError("%s must have adjacent elements in a row and rows that do not overlap, got strides %s" % (
+        name, t.stride()))
 
 
-def _out(name, out, shape, dtype, device):
-    import torch
-    if out is None:
-        out = torch.empty(shape, dtype=dtype, device=torch.device("cuda", device))
-    return out, _check_matrix(name, out, (dtype,), device, shape)
-
-
-def _workspace(nbytes, device):
+def _workspace(like, nbytes):
     """(tensor, address) of a workspace from torch's allocator: freed on
     return, and handed out again only to work later on the same stream."""
-    import torch
     if nbytes <= 0:
         return None, None
-    w = torch.empty(nbytes, dtype=torch.uint8, device=torch.device("cuda", device))
+    w = like.new_empty(nbytes, dtype=torch.uint8)
     return w, w.data_ptr()
 
 
 def _call(library, name, device, *args):
     """Call an entry point on `device` and its current stream (the last argument)."""
-    import torch
     fn = getattr(load(library), name)
     if device == torch.cuda.current_device():
         rc = fn(*args, _stream(device))
@@ -134,35 +129,41 @@ def _call(library, name, device, *args):
 
 
 def _check_gated(x, w_gate, w_up):
-    dtypes = tuple(_types())
-    ldx = _check_matrix("x", x, dtypes)
+    """(device, T, D, F, row pitches of x, w_gate and w_up)."""
+    ldx = _pitch("x", x, _TYPES)
     device = x.get_device()
-    ldg = _check_matrix("w_gate", w_gate, (x.dtype,), device)
-    if w_gate.shape[1] != x.shape[1]:
+    types = (x.dtype,)
+    ldg = _pitch("w_gate", w_gate, types, device)
+    T, D = x.shape
+    F, K = w_gate.shape
+    if K != D:
         raise ValueError("need x [T, D] and w_gate, w_up [F, D], got %s and %s" % (tuple(x.shape), tuple(w_gate.shape)))
-    ldu = _check_matrix("w_up", w_up, (x.dtype,), device, w_gate.shape)
-    return device, ldx, ldg, ldu
+    ldu = _pitch("w_up", w_up, types, device, w_gate.shape)
+    return device, T, D, F, ldx, ldg, ldu
 
 
 def _gated(x, w_gate, w_up, activation, out, train):
-    import torch
-    device, ldx, ldg, ldu = _check_gated(x, w_gate, w_up)
-    if activation not in ACTIVATIONS:
+    device, T, D, F, ldx, ldg, ldu = _check_gated(x, w_gate, w_up)
+    act = ACTIVATIONS.get(activation)
+    if act is None:
         raise ValueError("activation must be one of %s, got %r" % (", ".join(sorted(ACTIVATIONS)), activation))
-    (T, D), F = x.shape, w_gate.shape[0]
-    out, ldh = _out("out", out, (T, F), x.dtype, device)
+    if out is None:
+        out = x.new_empty((T, F))
+        ldh = F
+    else:
+        ldh = _pitch("out", out, (x.dtype,), device, (T, F))
     lib = load("gated_nt")
     saved = None
     if train:
         nbytes = lib.gated_nt_saved_bytes(T, F)
         if nbytes < 0:
             raise GemmError("gated_nt", 1)
-        saved = torch.empty(nbytes, dtype=torch.uint8, device=x.device)
-    ptrs = (x.data_ptr(), w_gate.data_ptr(), w_up.data_ptr())
-    nbytes = lib.gated_nt_workspace(*ptrs, T, D, F, ldx, ldg, ldu)
-    keep, workspace = _workspace(nbytes, device)
-    _call("gated_nt", "gated_nt", device, *ptrs, out.data_ptr(), saved.data_ptr() if train else None, T, D, F, ldx, ldg,
-          ldu, ldh, _types()[x.dtype], ACTIVATIONS[activation], workspace, max(nbytes, 0))
+        saved = x.new_empty(nbytes, dtype=torch.uint8)
+    px, pg, pu = x.data_ptr(), w_gate.data_ptr(), w_up.data_ptr()
+    nbytes = lib.gated_nt_workspace(px, pg, pu, T, D, F, ldx, ldg, ldu)
+    keep, workspace = _workspace(x, nbytes)
+    _call("gated_nt", "gated_nt", device, px, pg, pu, out.data_ptr(), saved.data_ptr() if train else None, T, D, F, ldx,
+          ldg, ldu, ldh, _TYPES[x.dtype], act, workspace, max(nbytes, 0))
     return out, saved
 
 
@@ -191,10 +192,9 @@ def gated_nt_backward(dh, x, w_gate, w_up, saved, out=None):
     ``out``: three matrices to write them to, or None for new ones.  They are
     written, not added to.
     """
-    import torch
-    device, ldx, ldg, ldu = _check_gated(x, w_gate, w_up)
-    (T, D), F = x.shape, w_gate.shape[0]
-    lddh = _check_matrix("dh", dh, (x.dtype,), device, (T, F))
+    device, T, D, F, ldx, ldg, ldu = _check_gated(x, w_gate, w_up)
+    types = (x.dtype,)
+    lddh = _pitch("dh", dh, types, device, (T, F))
     lib = load("gated_nt")
     need = lib.gated_nt_saved_bytes(T, F)
     nbytes = lib.gated_nt_backward_workspace(T, D, F)
@@ -203,16 +203,21 @@ def gated_nt_backward(dh, x, w_gate, w_up, saved, out=None):
     if not isinstance(saved, torch.Tensor) or saved.dtype != torch.uint8 or saved.dim() != 1 \
             or saved.numel() != need or not saved.is_contiguous() or (need and saved.get_device() != device):
         raise ValueError("saved must be what gated_nt_train returned for x, w_gate and w_up")
-    if out is not None and len(out) != 3:
-        raise ValueError("out must be the three matrices dx, dw_gate and dw_up")
-    outs = []
-    for name, given, shape in zip(("dx", "dw_gate", "dw_up"), out or (None,) * 3, ((T, D), (F, D), (F, D))):
-        outs.append(_out("out's " + name, given, shape, x.dtype, device))
-    keep, workspace = _workspace(nbytes, device)
+    if out is None:
+        dx, dw_gate, dw_up = x.new_empty((T, D)), x.new_empty((F, D)), x.new_empty((F, D))
+        lddx = lddg = lddu = D
+    else:
+        if len(out) != 3:
+            raise ValueError("out must be the three matrices dx, dw_gate and dw_up")
+        dx, dw_gate, dw_up = out
+        lddx = _pitch("out's dx", dx, types, device, (T, D))
+        lddg = _pitch("out's dw_gate", dw_gate, types, device, (F, D))
+        lddu = _pitch("out's dw_up", dw_up, types, device, (F, D))
+    keep, workspace = _workspace(x, nbytes)
     _call("gated_nt", "gated_nt_backward", device, dh.data_ptr(), x.data_ptr(), w_gate.data_ptr(), w_up.data_ptr(),
-          saved.data_ptr(), *(t.data_ptr() for t, _ in outs), T, D, F, lddh, ldx, ldg, ldu, *(ld for _, ld in outs),
-          _types()[x.dtype], workspace, nbytes)
-    return tuple(t for t, _ in outs)
+          saved.data_ptr(), dx.data_ptr(), dw_gate.data_ptr(), dw_up.data_ptr(), T, D, F, lddh, ldx, ldg, ldu, lddx, lddg,
+          lddu, _TYPES[x.dtype], workspace, nbytes)
+    return dx, dw_gate, dw_up
 
 
 def orthogonalize_ns(g, steps: int = 5, coefficients=(3.4445, -4.7750, 2.0315), eps: float = 1e-7, out=None):
@@ -223,10 +228,8 @@ def orthogonalize_ns(g, steps: int = 5, coefficients=(3.4445, -4.7750, 2.0315), 
     step.  g is float16, bfloat16 or float32; the iterates are held in
     binary16, hence the bfloat16 result.
     """
-    import torch
     if not isinstance(g, torch.Tensor):
         raise TypeError("g must be a torch tensor")
-    types = {**_types(), torch.float32: 2}
     if g.dim() not in (2, 3):
         raise ValueError("g must be [rows, cols] or [batch, rows, cols], got %s" % (tuple(g.shape),))
     steps = int(steps)
@@ -242,13 +245,13 @@ def orthogonalize_ns(g, steps: int = 5, coefficients=(3.4445, -4.7750, 2.0315), 
     def first(t):  # one matrix of the batch (of an empty one: any of its shape)
         return t if t.dim() == 2 else t[0] if t.shape[0] else t.new_empty(rows, cols)
 
-    ldg = _check_matrix("g", first(g), tuple(types))
+    ldg = _pitch("g", first(g), _TYPES_AND_F32)
     device = g.get_device()
     if out is None:
-        out = torch.empty(g.shape, dtype=torch.bfloat16, device=g.device)
+        out = g.new_empty(g.shape, dtype=torch.bfloat16)
     if not isinstance(out, torch.Tensor) or out.shape != g.shape:
         raise ValueError("out must be a bfloat16 tensor of g's shape %s" % (tuple(g.shape),))
-    ldo = _check_matrix("out", first(out), (torch.bfloat16,), device, (rows, cols))
+    ldo = _pitch("out", first(out), (torch.bfloat16,), device, (rows, cols))
     if g.numel() == 0:
         return out
     stride_g, stride_o = (t.stride(0) if t.dim() == 3 and batch > 1 else 0 for t in (g, out))
@@ -258,10 +261,10 @@ def orthogonalize_ns(g, steps: int = 5, coefficients=(3.4445, -4.7750, 2.0315), 
     nbytes = lib.orthogonalize_ns_workspace(batch, rows, cols)
     if nbytes < 0:
         raise GemmError("orthogonalize_ns", 1)
-    keep, workspace = _workspace(nbytes, device)
+    keep, workspace = _workspace(g, nbytes)
     flat = (ctypes.c_double * max(1, 3 * steps))(*(v for c in triples for v in c))
     _call("orthogonalize_ns", "orthogonalize_ns", device, g.data_ptr(), out.data_ptr(), batch, rows, cols, ldg, stride_g,
-          ldo, stride_o, types[g.dtype], steps, flat, float(eps), workspace, nbytes)
+          ldo, stride_o, _TYPES_AND_F32[g.dtype], steps, flat, float(eps), workspace, nbytes)
     return out
 
 
@@ -273,29 +276,34 @@ def gemv_w4(x, q, scales, zeros=None, out=None):
     K); ``zeros`` likewise, or None for 8.  x is float16 or bfloat16.
     Enqueued on the current stream of x's device; returns ``out``.
     """
-    import torch
-    ldx = _check_matrix("x", x, tuple(_types()))
+    ldx = _pitch("x", x, _TYPES)
     device = x.get_device()
+    types = (x.dtype,)
+    ldq = _pitch("q", q, (torch.uint8,), device)
     M, K = x.shape
-    ldq = _check_matrix("q", q, (torch.uint8,), device)
-    N = q.shape[0]
-    if K % 32 or q.shape[1] != K // 2:
+    N, half = q.shape
+    if K % 32 or half * 2 != K:
         raise ValueError("need x [M, K] and q [N, K / 2] with K a multiple of 32, got %s and %s" % (
             tuple(x.shape), tuple(q.shape)))
-    if q.numel() and (q.data_ptr() % 16 or (N > 1 and ldq % 16)):
+    pq = q.data_ptr()
+    if (pq % 16 or (N > 1 and ldq % 16)) and N and K:
         raise ValueError("q's rows must start on 16 bytes")
-    for name, t in (("scales", scales), ("zeros", zeros)):
-        if t is None and name == "zeros":
-            continue
-        _check_matrix(name, t, (x.dtype,), device)
-        if t.shape[0] != N or t.shape != scales.shape or not t.is_contiguous():
-            raise ValueError("%s must be contiguous [%d, groups], got %s" % (name, N, tuple(t.shape)))
-    groups = scales.shape[1]
+    _pitch("scales", scales, types, device)
+    rows, groups = scales.shape
+    if rows != N or not scales.is_contiguous():
+        raise ValueError("scales must be contiguous [%d, groups], got %s" % (N, tuple(scales.shape)))
+    if zeros is not None:
+        _pitch("zeros", zeros, types, device, scales.shape)
+        if not zeros.is_contiguous():
+            raise ValueError("zeros must be contiguous")
     group = K // groups if groups and K % groups == 0 else 0
     if K and (group == 0 or ((group < 32 or group & (group - 1)) and group != K)):
         raise ValueError("K / scales.shape[1] must be a power of two from 32 on, or K: got %d / %d" % (K, groups))
-    out, ldy = _out("out", out, (M, N), x.dtype, device)
-    _call("gemv_w4", "gemv_w4", device, x.data_ptr(), q.data_ptr(), scales.data_ptr(),
-          None if zeros is None else zeros.data_ptr(), out.data_ptr(), M, N, K, group, ldx, max(ldq, K // 2), ldy,
-          _types()[x.dtype])
+    if out is None:
+        out = x.new_empty((M, N))
+        ldy = N
+    else:
+        ldy = _pitch("out", out, types, device, (M, N))
+    _call("gemv_w4", "gemv_w4", device, x.data_ptr(), pq, scales.data_ptr(), None if zeros is None else zeros.data_ptr(),
+          out.data_ptr(), M, N, K, group, ldx, ldq if N > 1 else half, ldy, _TYPES[x.dtype])
     return out
