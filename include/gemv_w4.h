@@ -27,7 +27,7 @@
  * hipErrorInvalidValue before anything is enqueued: a negative size or one of
  * 2^31 or more, K no multiple of 32 or of group, K of 2^21 or more, a group
  * that is neither a power of two from 32 on nor K itself, a pitch below the
- * row, ldq no multiple of 16, Q not 16-byte aligned, an unknown type, a null
+ * row, ldx or ldq above 2^23, ldq no multiple of 16, Q not 16-byte aligned, an unknown type, a null
  * or odd pointer with a non-zero extent, Y meeting an input.  M == 0 or N ==
  * 0 writes nothing; K == 0 writes +0.
  */
