@@ -314,6 +314,248 @@ gemv_w4_kernel(const E* __restrict__ X, const unsigned char* __restrict__ Q, con
     }
 }
 
+// ---------------------------------------------------------- many rows of X --
+//
+// 64 rows of X by 64 FN rows of W per workgroup of sixteen waves, K in blocks
+// of 256: x (four tiles of 64 rows by 64 k, 32 KiB) and codes (FN x 8 KiB) in
+// LDS rings of three blocks, filled by direct global->LDS loads two blocks
+// ahead.  Waves 4 q .. 4 q + 3 take x's tile q of every block; each of the
+// four takes all rows of x and 16 FN rows of W, so each code becomes a number
+// once per 64 rows of x and the numbers never reach LDS.  The four partial
+// sums meet in LDS at the end.  (With four waves walking all of K, one to a
+// SIMD, the chain from a barrier through LDS, the unpacking and the matrix
+// cores to the next stood in full view: 28 us instead of 12 at 256 rows, 4096
+// x 4096.)
+//
+// The codes are the first operand here: lane l's four results belong to row
+// l % 16 of x and rows 4 h .. 4 h + 3 of W, eight adjacent bytes of Y.
+// Scales therefore come by fours; a block's are kept in LDS by group, read
+// from memory a block ahead.  Codes are unpacked in their own order (a byte
+// permute, a mask, a packed fused multiply or shift), since x is used by
+// one wave's 16 FN rows only and would be permuted more often than they.
+
+template <class E>
+struct Unpack;
+template <>
+struct Unpack<_Float16> {
+    // pair (q, q') of a byte: 1024 + q and 1024 + 16 q', made q - 8 and q' - 8
+    static constexpr uint32_t magic = 0x64006400u, mask = 0x00f0000fu;
+    static __device__ __forceinline__ uint32_t pair(uint32_t b, uint32_t magic, uint32_t mask)
+    {
+        const half2_t p = __builtin_bit_cast(half2_t, masked(b, mask, magic));
+        const half2_t by = {(_Float16)1.0f, (_Float16)0.0625f}, off = {(_Float16)-1032.0f, (_Float16)-72.0f};
+        const half2_t v = __builtin_elementwise_fma(p, by, off);
+        return __builtin_bit_cast(uint32_t, v);
+    }
+};
+template <>
+struct Unpack<__bf16> {
+    // 128 + q and 128 + q'
+    static constexpr uint32_t magic = 0x43004300u, mask = 0x000f000fu;
+    static __device__ __forceinline__ uint32_t pair(uint32_t b, uint32_t magic, uint32_t mask)
+    {
+        typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
+        const u16x2 shift = {0, 4};
+        const u16x2 v = __builtin_bit_cast(u16x2, b) >> shift;
+        return masked(__builtin_bit_cast(uint32_t, v), mask, magic);
+    }
+};
+
+// FLUSH: runs of 32 k per sum that a scale is applied to; a wave has two of a
+// group at most.
+template <class E, int FN, int FLUSH, bool ZERO>
+__global__ void __launch_bounds__(1024, 1)
+gemm_w4_kernel(const E* __restrict__ X, const unsigned char* __restrict__ Q, const E* __restrict__ scale,
+               const E* __restrict__ zero, E* __restrict__ Y, int M, int N, int K, int shift, int groups, int64_t ldx,
+               int64_t ldq, int64_t ldy, int tiles_m, int tiles_n, int whole)
+{
+    using x8 = typename Elem<E>::x8;
+    using x4 = typename Elem<E>::x4;
+    static_assert(FLUSH <= 2, "a wave's part of a block is two runs");
+    constexpr bool SUM = ZERO || !Code<E>::exact;
+    constexpr int BM = 64, BN = 64 * FN, NS = 8 / FLUSH;  // scales of a block's row
+    constexpr int X_BYTES = 4 * BM * 128, W_BYTES = BN * 128, S_BYTES = NS * BN * 2;
+    __shared__ __attribute__((aligned(1024))) unsigned char smem[3 * X_BYTES + 3 * W_BYTES + 4 * S_BYTES];
+    static_assert(sizeof(smem) <= 160 * 1024 && 12 * 4096 * FN <= 3 * X_BYTES, "gfx950 has 160 KiB of LDS");
+    unsigned char* const xs = smem;
+    unsigned char* const ws = smem + 3 * X_BYTES;
+    unsigned char* const ss = ws + 3 * W_BYTES;  // two blocks' scales, then two blocks' zero points
+    const int tid = threadIdx.x, lane = tid & (kWave - 1);
+    const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
+    const int q = wave >> 2, part = wave & 3;  // x's tile, and which 16 FN rows of W
+    const int r = lane & 15, h = lane >> 4;
+    int tm, tn;
+    tile_of(blockIdx.x, tiles_m, tiles_n, tm, tn);
+    const int m0 = tm * BM, n0 = tn * BN;
+    const uint32_t pitch_x = (uint32_t)ldx * 2u, pitch_q = (uint32_t)ldq;
+    const __amdgpu_buffer_rsrc_t bx = make_rsrc(X + (int64_t)m0 * ldx, (uint32_t)min(BM, M - m0) * pitch_x);
+    const __amdgpu_buffer_rsrc_t bq = make_rsrc(Q + (int64_t)n0 * ldq, (uint32_t)min(BN, N - n0) * pitch_q);
+    const uint32_t s_bytes = (uint32_t)min(BN, N - n0) * (uint32_t)groups * 2u;
+    const __amdgpu_buffer_rsrc_t bs = make_rsrc(scale + (int64_t)n0 * groups, s_bytes);
+    const __amdgpu_buffer_rsrc_t bz = make_rsrc(ZERO ? zero + (int64_t)n0 * groups : scale, ZERO ? s_bytes : 0u);
+
+    // A load fills eight rows of a tile: row lane / 8, position lane % 8,
+    // which the swizzle gives chunk pos ^ ((row / 2) % 8).  Wave 4 q + p loads
+    // rows 16 p .. + 15 of x's tile q, and wave w rows 8 w .. + 7 of the codes.
+    const int lr = lane >> 3, lp = lane & 7;
+    const int c01[2] = {swizzle(lr, lp), swizzle(8 + lr, lp)};
+    auto load = [&](int stage, int block) __attribute__((always_inline)) {
+        if (wave < 8 * FN) {
+            const int c = c01[wave & 1], k = block * kBlock + c * 32;
+            const uint32_t off = k < K ? (uint32_t)(wave * 8 + lr) * pitch_q + (uint32_t)(k / 2) : kOob;
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(bq, (lds_void*)(ws + stage * W_BYTES + wave * 1024), 16, off, 0, 0,
+                                                     0);
+        }
+#pragma unroll
+        for (int l = 0; l < 2; ++l) {
+            const int c = c01[l], k = block * kBlock + q * 64 + c * 8;
+            const uint32_t off = k < K ? (uint32_t)(part * 16 + l * 8 + lr) * pitch_x + (uint32_t)k * 2u : kOob;
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(bx, (lds_void*)(xs + stage * X_BYTES + (wave * 2 + l) * 1024), 16,
+                                                     off, 0, 0, 0);
+        }
+    };
+    uint16_t sv = 0, zv = 0;
+    const bool has_scale = tid < BN * NS;
+    auto load_s = [&](int block) __attribute__((always_inline)) {
+        const int k = block * kBlock + 32 * FLUSH * (tid % NS);
+        const uint32_t off = k < K && has_scale
+                                 ? ((uint32_t)(tid / NS) * (uint32_t)groups + (uint32_t)(k >> shift)) * 2u
+                                 : kOob;
+        sv = __builtin_amdgcn_raw_buffer_load_b16(bs, off, 0, 0);
+        if constexpr (ZERO) zv = __builtin_amdgcn_raw_buffer_load_b16(bz, off, 0, 0);
+    };
+    auto keep_s = [&](int block) __attribute__((always_inline)) {
+        if (has_scale) {
+            unsigned char* to = ss + (block & 1) * S_BYTES + (tid % NS * BN + tid / NS) * 2;
+            *(uint16_t*)to = sv;
+            if constexpr (ZERO) *(uint16_t*)(to + 2 * S_BYTES) = zv;
+        }
+    };
+
+    f32x4 total[4][FN], acc[4][FN], sum[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < FN; ++j) total[i][j] = f32x4{0, 0, 0, 0};
+    const u32x4 ones_bits = {Code<E>::ones, Code<E>::ones, Code<E>::ones, Code<E>::ones};
+    const x8 ones = __builtin_bit_cast(x8, ones_bits);
+    uint32_t magic = Unpack<E>::magic, mask = Unpack<E>::mask;
+    asm volatile("" : "+v"(magic), "+s"(mask));
+
+    // This wave's part of block b.
+    auto compute = [&](int b, const unsigned char* xt, const unsigned char* wt) __attribute__((always_inline)) {
+        // words 0, 1 of lanes h: the codes of the 64 k's runs, from the half of
+        // 128 that holds them
+        uint32_t w[FN][2];
+#pragma unroll
+        for (int j = 0; j < FN; ++j) {
+            const u32x4 v = across(
+                *(const u32x4*)(wt + (part * 16 * FN + 16 * j + r) * 128 + swizzle(r, 4 * (q >> 1) + h) * 16));
+            w[j][0] = q & 1 ? v[2] : v[0];
+            w[j][1] = q & 1 ? v[3] : v[1];
+        }
+#pragma unroll
+        for (int kk = 0; kk < 2; ++kk) {
+            x8 xv[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) xv[i] = *(const x8*)(xt + (16 * i + r) * 128 + swizzle(r, 4 * kk + h) * 16);
+            if (kk % FLUSH == 0)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    sum[i] = f32x4{0, 0, 0, 0};
+#pragma unroll
+                    for (int j = 0; j < FN; ++j) acc[i][j] = f32x4{0, 0, 0, 0};
+                }
+#pragma unroll
+            for (int j = 0; j < FN; ++j) {
+                const uint32_t word = w[j][kk];
+                const u32x4 bits = {Unpack<E>::pair(__builtin_amdgcn_perm(0, word, 0x0c000c00u), magic, mask),
+                                    Unpack<E>::pair(__builtin_amdgcn_perm(0, word, 0x0c010c01u), magic, mask),
+                                    Unpack<E>::pair(__builtin_amdgcn_perm(0, word, 0x0c020c02u), magic, mask),
+                                    Unpack<E>::pair(__builtin_amdgcn_perm(0, word, 0x0c030c03u), magic, mask)};
+                const x8 wv = __builtin_bit_cast(x8, bits);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) acc[i][j] = Elem<E>::mfma(wv, xv[i], acc[i][j]);
+            }
+            if constexpr (SUM)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) sum[i] = Elem<E>::mfma(ones, xv[i], sum[i]);
+            if (kk % FLUSH == FLUSH - 1)
+#pragma unroll
+                for (int j = 0; j < FN; ++j) {
+                    const int g = (2 * q + kk) / FLUSH;
+                    const unsigned char* at =
+                        ss + (b & 1) * S_BYTES + (g * BN + part * 16 * FN + 16 * j + 4 * h) * 2;
+                    const x4 s4 = *(const x4*)at;
+                    f32x4 z4 = f32x4{8.0f, 8.0f, 8.0f, 8.0f};
+                    if constexpr (ZERO) {
+                        const x4 v = *(const x4*)(at + 2 * S_BYTES);
+                        z4 = f32x4{(float)v[0], (float)v[1], (float)v[2], (float)v[3]};
+                    }
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            float v = acc[i][j][e];
+                            if constexpr (SUM) v = __builtin_fmaf(Code<E>::bias - z4[e], sum[i][e], v);
+                            total[i][j][e] = __builtin_fmaf((float)s4[e], v, total[i][j][e]);
+                        }
+                }
+        }
+    };
+
+    // At a block's barrier only the next block's two loads of x may be in
+    // flight (its codes were issued before them).  The scales' loads go first,
+    // so that waiting for them does not mean waiting for the loads behind.
+    const int blocks = (K + kBlock - 1) / kBlock;
+    load_s(0);
+    load(0, 0);
+    load(1, 1);
+    keep_s(0);
+    int st = 0;
+    for (int b = 0; b < blocks; ++b) {
+        lds_barrier<2>();
+        load_s(b + 1);
+        load(st == 0 ? 2 : st - 1, b + 2);  // (past the end of K: zeros, never read)
+        compute(b, xs + st * X_BYTES + q * (BM * 128), ws + st * W_BYTES);
+        keep_s(b + 1);
+        st = st == 2 ? 0 : st + 1;
+    }
+    lds_barrier<0>();  // no load may still be writing LDS when it is used again
+
+    // Partial sums of waves 4 .. 15 through LDS to waves 0 .. 3.
+    if (q > 0)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int j = 0; j < FN; ++j)
+                *(f32x4*)(smem + ((((wave - 4) * 4 + i) * FN + j) * 64 + lane) * 16) = total[i][j];
+    __syncthreads();
+    if (q > 0) return;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int m = m0 + 16 * i + r;
+#pragma unroll
+        for (int j = 0; j < FN; ++j) {
+            f32x4 sum4 = total[i][j];
+#pragma unroll
+            for (int o = 0; o < 3; ++o)
+                sum4 += *(const f32x4*)(smem + ((((o * 4 + part) * 4 + i) * FN + j) * 64 + lane) * 16);
+            const int n = n0 + part * 16 * FN + 16 * j + 4 * h;
+            if (m >= M) continue;
+            const x4 v = round4<E>(sum4);
+            E* y = Y + (int64_t)m * ldy + n;
+            if (whole && n + 3 < N) {
+                *(x4*)y = v;
+            } else {
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    if (n + e < N) y[e] = v[e];
+            }
+        }
+    }
+}
+
 struct Args {
     const void *X, *Q, *scale, *zero;
     void* Y;
@@ -341,31 +583,57 @@ int launch(const Args& a)
     return hipSuccess;
 }
 
-template <class E, int MB, int R, int FLUSH, bool EIGHTS>
-int by_zero(const Args& a)
+template <class E, int FN, int FLUSH, bool ZERO>
+int launch_gemm(const Args& a)
 {
-    return a.zero ? launch<E, MB, R, FLUSH, true, EIGHTS>(a) : launch<E, MB, R, FLUSH, false, EIGHTS>(a);
+    const int64_t tm = (a.M + 63) / 64, tn = (a.N + 64 * FN - 1) / (64 * FN);
+    if (tm * tn > abi::kMaxDim) return hipErrorInvalidValue;
+    const int whole = (uintptr_t)a.Y % 8 == 0 && a.ldy % 4 == 0;
+    hipLaunchKernelGGL((gemm_w4_kernel<E, FN, FLUSH, ZERO>), dim3((unsigned)(tm * tn)), dim3(1024), 0, a.stream,
+                       (const E*)a.X, (const unsigned char*)a.Q, (const E*)a.scale, (const E*)a.zero, (E*)a.Y, (int)a.M,
+                       (int)a.N, (int)a.K, a.shift, (int)a.groups, a.ldx, a.ldq, a.ldy, (int)tm, (int)tn, whole);
+    return (int)hipGetLastError();
 }
 
+// KIND(FLUSH, ZERO) by the group's size and the zero points.
+#define BY_GROUP(a, KIND)                                        \
+    ((a).shift >= 7   ? ((a).zero ? KIND(4, true) : KIND(4, false)) \
+     : (a).shift == 6 ? ((a).zero ? KIND(2, true) : KIND(2, false)) \
+                      : ((a).zero ? KIND(1, true) : KIND(1, false)))
+
 template <class E, int MB, int R, bool EIGHTS = true>
-int by_group(const Args& a)
+int few_rows(const Args& a)
 {
-    if (a.shift >= 7) return by_zero<E, MB, R, 4, EIGHTS>(a);
-    if (a.shift == 6) return by_zero<E, MB, R, 2, EIGHTS>(a);
-    return by_zero<E, MB, R, 1, EIGHTS>(a);
+#define KIND(FLUSH, ZERO) launch<E, MB, R, FLUSH, ZERO, EIGHTS>(a)
+    return BY_GROUP(a, KIND);
+#undef KIND
+}
+
+template <class E>
+int many_rows(const Args& a)
+{
+    // Twice the rows of W for each read of x where both are enough for all
+    // CUs; with the sums of x that zero points (and bfloat16) need, twice the
+    // totals do not fit in 128 registers.
+    if constexpr (Code<E>::exact)
+        if (!a.zero && (a.N + 127) / 128 * ((a.M + 63) / 64) >= 256)
+            return a.shift >= 6 ? launch_gemm<E, 2, 2, false>(a) : launch_gemm<E, 2, 1, false>(a);
+    if (a.shift >= 6) return a.zero ? launch_gemm<E, 1, 2, true>(a) : launch_gemm<E, 1, 2, false>(a);
+    return a.zero ? launch_gemm<E, 1, 1, true>(a) : launch_gemm<E, 1, 1, false>(a);
 }
 
 template <class E>
 int run(const Args& a)
 {
-    if ((uintptr_t)a.X % 16 || (a.M > 1 && a.ldx % 8)) return by_group<E, 1, 1, false>(a);
-    // as many rows of W to a workgroup as leave one for every CU
-    const int64_t mb = a.M <= 16 ? 1 : a.M <= 32 ? 2 : 4;
-    const int64_t blocks = (a.N + 15) / 16 * ((a.M + 16 * mb - 1) / (16 * mb));
-    const bool two = blocks >= 2 * 256;
-    if (mb == 1) return two ? by_group<E, 1, 2>(a) : by_group<E, 1, 1>(a);
-    if (mb == 2) return two ? by_group<E, 2, 2>(a) : by_group<E, 2, 1>(a);
-    return two ? by_group<E, 4, 2>(a) : by_group<E, 4, 1>(a);
+    if ((uintptr_t)a.X % 16 || (a.M > 1 && a.ldx % 8)) return few_rows<E, 1, 1, false>(a);
+    // As many rows of W to a workgroup as leave one for every CU.  Up to two
+    // workgroups of 32 x 32 a CU that kernel is the faster one (48 rows of X,
+    // 4096 x 4096: 11 us against 21; 64 rows, 8192 x 4096: 19 and 19; 256
+    // rows, 4096 x 4096: 36 against 22).
+    if (a.M <= 16) return (a.N + 15) / 16 >= 2 * 256 ? few_rows<E, 1, 2>(a) : few_rows<E, 1, 1>(a);
+    if (a.M <= 32 && (a.N + 15) / 16 < 2 * 256) return few_rows<E, 2, 1>(a);
+    if (a.M <= 32 || (a.M + 31) / 32 * ((a.N + 31) / 32) < 2 * 256) return few_rows<E, 2, 2>(a);
+    return many_rows<E>(a);
 }
 
 }  // namespace
