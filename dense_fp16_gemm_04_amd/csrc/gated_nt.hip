@@ -49,12 +49,14 @@ __device__ __forceinline__ float act_slope(const Activation& c, float g, float s
     return __builtin_fmaf(g * s * (1.0f - s), dz, s);
 }
 
-// `saved`: for four columns f .. f + 3 of row t, four values P then four Q
-// (32 bytes): a 16 x 16 block's row of one matrix core result is one whole
-// 128-byte line.
-__host__ __device__ __forceinline__ int64_t saved_pitch(int64_t F) { return (F + 3) / 4 * 8; }
+// `saved` in blocks of 16 x 16, row of blocks by row: P of a block, then Q,
+// each as 64 times four values in the order in which a wave's lanes hold
+// them (lane l: row l % 16, columns 4 (l / 16) .. + 3), so that a wave stores
+// and loads 1 KiB at once.
+__host__ __device__ __forceinline__ int64_t blocks_of(int64_t n) { return (n + 15) / 16; }
+constexpr int kBlockFloats = 512;
 
-template <class E, bool SAVE, bool WHOLE>
+template <class E, bool SAVE, bool EIGHTS>
 struct GatedOp {
     static constexpr bool kPersist = true, kOblong = true;  // (256 x 256, 256 x 128 tiles)
     const E *X, *Wg, *Wu;
@@ -88,60 +90,52 @@ struct GatedOp {
     {
         return row % WTN >= WTN / 2 ? ldu : ldg;
     }
-    // Where a tile's rows of H and of `saved` lie.
-    struct Out {
-        __amdgpu_buffer_rsrc_t h, s;
-        uint32_t pitch_h, pitch_s;
-    };
-    __device__ __forceinline__ Out out_rows(int m0, int rows) const
-    {
-        Out o;
-        o.pitch_h = (uint32_t)ldh * 2u;
-        o.pitch_s = (uint32_t)saved_pitch(F) * 4u;
-        const uint32_t n = (uint32_t)min(rows, M - m0);
-        o.h = make_rsrc(H + (int64_t)m0 * ldh, n * o.pitch_h);
-        if constexpr (SAVE) o.s = make_rsrc(saved + m0 * saved_pitch(F), n * o.pitch_s);
-        return o;
-    }
-    // Columns f .. f + 3 of the tile's row r from g and u.
-    __device__ __forceinline__ void finish(const Out& o, int r, int f, const f32x4& g4, const f32x4& u4) const
-    {
-        f32x4 h, p, q;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const float g = g4[e], u = u4[e];
-            float s;
-            q[e] = act_value(act, g, s);
-            h[e] = q[e] * u;
-            if constexpr (SAVE) p[e] = u * act_slope(act, g, s);
-        }
-        buffer_store4<E, WHOLE>(o.h, (uint32_t)r * o.pitch_h + (uint32_t)f * 2u, f, F, h);
-        if constexpr (SAVE) {
-            const uint32_t at = f < F ? (uint32_t)r * o.pitch_s + (uint32_t)f * 8u : kOob;
-            __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, p), o.s, at, 0, 0);
-            __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, q), o.s, at, 16, 0);
-        }
-    }
     template <class T>
     __device__ __forceinline__ void epilogue(const Tile& t, const f32x4 (&acc)[T::FM][T::FN], int lane, int wave,
-                                             unsigned char*, unsigned char*) const
+                                             unsigned char* s0, unsigned char* s1) const
     {
         constexpr int HF = T::FN / 2;
-        const Out o = out_rows(t.m0, T::BM);
+        // the tile's rows of blocks of `saved` (below 2^31 bytes)
+        const int bf = (int)blocks_of(F);
+        const uint32_t pitch_s = (uint32_t)bf * (kBlockFloats * 4u);
+        __amdgpu_buffer_rsrc_t rs;
+        if constexpr (SAVE)
+            rs = make_rsrc((unsigned char*)saved + (int64_t)(t.m0 / 16) * pitch_s,
+                           (uint32_t)min(T::BM / 16, (int)blocks_of(M) - t.m0 / 16) * pitch_s);
+        auto value = [&](int i, int j) __attribute__((always_inline)) {
+            const f32x4 g4 = acc[i][j], u4 = acc[i][j + HF];
+            f32x4 h, p, q;
 #pragma unroll
-        for (int i = 0; i < T::FM; ++i)
-#pragma unroll
-            for (int j = 0; j < HF; ++j) {
-                const int ln = pinned(lane);
-                finish(o, wave / T::WAVES_N * T::WTM + i * 16 + (ln & 15),
-                       t.n0 + wave % T::WAVES_N * (T::WTN / 2) + j * 16 + 4 * (ln >> 4), acc[i][j], acc[i][j + HF]);
+            for (int e = 0; e < 4; ++e) {
+                const float g = g4[e], u = u4[e];
+                float s;
+                q[e] = act_value(act, g, s);
+                h[e] = q[e] * u;
+                if constexpr (SAVE) p[e] = u * act_slope(act, g, s);
             }
+            if constexpr (SAVE) {
+                __builtin_amdgcn_sched_barrier(0);  // (block by block, for the registers' sake)
+                const int b = (t.n0 + wave % T::WAVES_N * (T::WTN / 2)) / 16 + j;
+                const uint32_t row = as_vector(pitch_s) * (uint32_t)(wave / T::WAVES_N * T::FM + i);
+                const uint32_t at = (b < bf ? row + (uint32_t)b * (kBlockFloats * 4u) : kOob) + pinned(lane) * 16u;
+                __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, p), rs, at, 0, 0);
+                // (the distance is part of the vector offset, which makes it an
+                // immediate.  Given as the scalar offset it takes a register,
+                // after which the compiler lets the next instruction write the
+                // store's data registers: the first of them then came out
+                // wrong now and then in the last lanes of each sixteen.)
+                __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, q), rs, at + kBlockFloats * 2u, 0, 0);
+            }
+            return round4<E>(h);
+        };
+        write_rows<T, HF, EIGHTS>(value, rows_at(H, t.m0, M, T::BM, ldh, t.n0, F), lane, wave, s0, s1);
     }
 };
 
 // dG = dH * P, dU = dH * Q for a 64 x 64 tile: row-major into rows of dGU
 // (dG at column 0, dU at column Fp), transposed into dGT and dUT (pitch Tp).
 // Rows and columns past the end, up to multiples of eight, become zeros.
+// dH comes in by rows and turns in LDS to the blocks that `saved` holds.
 // Bound by its bytes: 2 + 8 read, 8 written per element.
 template <class E>
 __global__ void __launch_bounds__(relayout::kThreads)
@@ -152,34 +146,55 @@ gated_slopes(const E* __restrict__ dH, const float* __restrict__ saved, E* __res
     using namespace relayout;
     __shared__ E tg[kTile * kPitch], tu[kTile * kPitch];
     const int t0 = (int)(blockIdx.x / tiles_f) * kTile, f0 = (int)(blockIdx.x % tiles_f) * kTile;
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int x = threadIdx.x & 15, y = threadIdx.x >> 4;
+    // wave w takes the blocks of rows 16 w .. + 15; their P and Q first
+    const int64_t bt = t0 / 16 + wave, bf0 = f0 / 16, bf = blocks_of(F);
+    f32x4 p[4], q[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        p[j] = q[j] = f32x4{0, 0, 0, 0};
+        if (bt * 16 < T && bf0 + j < bf) {
+            const float* at = saved + (bt * bf + bf0 + j) * kBlockFloats + lane * 4;
+            p[j] = *(const f32x4*)at;
+            q[j] = *(const f32x4*)(at + kBlockFloats / 2);
+        }
+    }
+#pragma unroll
+    for (int it = 0; it < 4; ++it) {
+        const int r = it * 16 + y;
+        x4 d = {};
+        if (t0 + r < T) d = load4(dH + (int64_t)(t0 + r) * lddh, f0 + x * 4, F, vec);
+        *(x4*)(tg + r * kPitch + x * 4) = d;
+    }
+    __syncthreads();
+    const int row = wave * 16 + (lane & 15);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const int at = row * kPitch + j * 16 + 4 * (lane >> 4);
+        const x4 d = *(const x4*)(tg + at);
+        x4 vg, vu;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            // (a row or column that is not there has d, P and Q zero; 0 beside
+            // an infinite P of the same row is the product it is)
+            vg[e] = (E)((float)d[e] * p[j][e]);
+            vu[e] = (E)((float)d[e] * q[j][e]);
+        }
+        *(x4*)(tg + at) = vg;  // (each element of dH is read by one lane, this one)
+        *(x4*)(tu + at) = vu;
+    }
+    __syncthreads();
     const int f = f0 + x * 4;
 #pragma unroll
     for (int it = 0; it < 4; ++it) {
-        const int r = it * 16 + y, t = t0 + r;
-        x4 vg = {}, vu = {};
-        if (t < T) {
-            if (f < F) {
-                const x4 d = load4(dH + (int64_t)t * lddh, f, F, vec);
-                const float* at = saved + t * saved_pitch(F) + f * 2;
-                const f32x4 p = *(const f32x4*)at, q = *(const f32x4*)(at + 4);
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    if (f + e < F) {
-                        vg[e] = (E)((float)d[e] * p[e]);
-                        vu[e] = (E)((float)d[e] * q[e]);
-                    }
-            }
-            if (f < Fp) {
-                E* row = dGU + (int64_t)t * 2 * Fp;
-                *(x4*)(row + f) = vg;
-                *(x4*)(row + Fp + f) = vu;
-            }
+        const int r = it * 16 + y;
+        if (t0 + r < T && f < Fp) {
+            E* to = dGU + (int64_t)(t0 + r) * 2 * Fp;
+            *(x4*)(to + f) = *(const x4*)(tg + r * kPitch + x * 4);
+            *(x4*)(to + Fp + f) = *(const x4*)(tu + r * kPitch + x * 4);
         }
-        *(x4*)(tg + r * kPitch + x * 4) = vg;
-        *(x4*)(tu + r * kPitch + x * 4) = vu;
     }
-    __syncthreads();
     store_transposed(tg, dGT, Tp, t0, f0, Tp, F);
     store_transposed(tu, dUT, Tp, t0, f0, Tp, F);
 }
@@ -187,9 +202,9 @@ gated_slopes(const E* __restrict__ dH, const float* __restrict__ saved, E* __res
 // ------------------------------------------------------------------ host --
 
 bool vec4(const void* p, int64_t ld) { return (uintptr_t)p % 8 == 0 && ld % 4 == 0; }
-// a result's rows take four columns at a time
-bool whole_rows(const void* p, int64_t cols, int64_t ld) { return vec4(p, ld) && cols % 4 == 0; }
 bool vec8(const void* p, int64_t ld) { return (uintptr_t)p % 16 == 0 && ld % 8 == 0; }
+// a result's rows take eight columns at a time
+bool eights(const void* p, int64_t cols, int64_t ld) { return vec8(p, ld) && cols % 8 == 0; }
 
 template <class E>
 int launch_copy(const E* src, int64_t ld, E* dst, int64_t ldd, int64_t rows, int64_t cols, hipStream_t stream)
@@ -227,7 +242,7 @@ int product(const E* A, const E* B, E* C, int64_t M, int64_t N, int64_t K, int64
         op.ldc = (int)ldc;
         return launch_grid<E>(op, M, N, 1, 1, K, stream);
     };
-    return whole_rows(C, N, ldc) ? with(StoreOp<E, true>{}) : with(StoreOp<E, false>{});
+    return eights(C, N, ldc) ? with(StoreOp<E, true>{}) : with(StoreOp<E, false>{});
 }
 
 // Copies of the operands that the kernels cannot read in place.
@@ -283,14 +298,14 @@ bool good_sizes(int64_t T, int64_t D, int64_t F)
            T <= abi::kMaxDim - 256;
 }
 
-template <class E, bool SAVE, bool WHOLE>
+template <class E, bool SAVE, bool EIGHTS>
 int forward(const E* X, const E* Wg, const E* Wu, E* H, float* saved, int64_t T, int64_t D, int64_t F, int64_t ldx,
             int64_t ldg, int64_t ldu, int64_t ldh, int32_t activation, void* workspace, hipStream_t stream)
 {
     const ForwardSpace<E> w(workspace, X, Wg, Wu, T, D, F, ldx, ldg, ldu);
     const int64_t Dp = abi::up(D, 8);
     int rc = hipSuccess;
-    GatedOp<E, SAVE, WHOLE> op = {};
+    GatedOp<E, SAVE, EIGHTS> op = {};
     op.X = X;
     op.Wg = Wg;
     op.Wu = Wu;
@@ -359,7 +374,7 @@ int gated_nt_version(void) { return GATED_NT_VERSION; }
 int64_t gated_nt_saved_bytes(int64_t T, int64_t F)
 {
     if (!good_sizes(T, 0, F)) return -1;
-    return T * saved_pitch(F) * 4;
+    return blocks_of(T) * blocks_of(F) * kBlockFloats * 4;
 }
 
 int64_t gated_nt_workspace(const void* X, const void* Wg, const void* Wu, int64_t T, int64_t D, int64_t F, int64_t ldx,
@@ -397,11 +412,11 @@ int gated_nt(const void* X, const void* Wg, const void* Wu, void* H, void* saved
     for (const Range& r : in)
         if (h.meets(r) || s.meets(r) || w.meets(r)) return hipErrorInvalidValue;
     if (h.meets(s) || h.meets(w) || s.meets(w)) return hipErrorInvalidValue;
-#define FORWARD(E, SAVE, WHOLE)                                                                                 \
-    forward<E, SAVE, WHOLE>((const E*)X, (const E*)Wg, (const E*)Wu, (E*)H, (float*)saved, T, D, F, ldx, ldg, ldu, \
+#define FORWARD(E, SAVE, EIGHTS)                                                                                 \
+    forward<E, SAVE, EIGHTS>((const E*)X, (const E*)Wg, (const E*)Wu, (E*)H, (float*)saved, T, D, F, ldx, ldg, ldu, \
                             ldh, activation, workspace, stream)
 #define FORWARD_OF(E)                                                                  \
-    (whole_rows(H, F, ldh) ? (saved ? FORWARD(E, true, true) : FORWARD(E, false, true)) \
+    (eights(H, F, ldh) ? (saved ? FORWARD(E, true, true) : FORWARD(E, false, true)) \
                            : (saved ? FORWARD(E, true, false) : FORWARD(E, false, false)))
     return type == GATED_NT_F16 ? FORWARD_OF(_Float16) : FORWARD_OF(__bf16);
 #undef FORWARD_OF

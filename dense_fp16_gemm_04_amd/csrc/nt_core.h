@@ -22,11 +22,10 @@
 //                                     rows from a multiple of BN / 8 on are
 //                                     evenly spaced
 //   epilogue<T>(t, acc, lane, wave, s0, s1)
-//                                  writes the sub-tiles out; s0 and s1 point
-//                                  to LDS for T::WTN / T::ROUNDS rows of BM
-//                                  16-bit values for the first wave column and
-//                                  for the others; a barrier has passed that
-//                                  makes it free, and another follows
+//                                  writes the sub-tiles out, through
+//                                  T::STAGE_MAX bytes of LDS: 32 KiB at s0 and
+//                                  the rest at s1; a barrier has passed that
+//                                  makes them free, and another follows
 // and the fields K (elements, a multiple of 8), lda (A's row pitch in
 // elements; pitches are multiples of 8 and below 2^21), tiles.  Every row
 // starts on 16 bytes.
@@ -62,11 +61,11 @@ struct Shape {
     static constexpr int BM = BM_, BN = BN_, BK = 64, STAGES = STAGES_, OCC = OCC_;
     static constexpr int WAVES_M = WM, WAVES_N = WN, WAVES = WM * WN, THREADS = WAVES * kWave;
     static constexpr int WTM = BM / WM, WTN = BN / WN;  // a wave's sub-tile
-    static constexpr int FM = WTM / 16, FN = WTN / 16, ROUNDS = 1;
+    static constexpr int FM = WTM / 16, FN = WTN / 16;
     static constexpr int ROW_BYTES = 128;
     static constexpr int A_BYTES = BM * ROW_BYTES, B_BYTES = BN * ROW_BYTES;
     static constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
-    static constexpr int LDS_BYTES = STAGES * STAGE_BYTES;
+    static constexpr int LDS_BYTES = STAGES * STAGE_BYTES, STAGE_MAX = LDS_BYTES;
     static constexpr int LOADERS = LOADERS_;             // waves 0 .. LOADERS - 1 load
     static constexpr int A_LOADS = BM / 8 / LOADERS, B_LOADS = BN / 8 / LOADERS;  // 8 rows each, per wave
     static constexpr int LOADS = A_LOADS + B_LOADS;
@@ -209,7 +208,7 @@ __global__ void __launch_bounds__(T::THREADS, T::OCC) nt_tile(const OP op)
     // no load may still be writing LDS when the ring is used again or the
     // workgroup ends
     lds_barrier<0>();
-    op.template epilogue<T>(t, acc, lane, wave, smem, smem + T::BM * T::WTN * 2);
+    op.template epilogue<T>(t, acc, lane, wave, smem, smem + 32768);
 }
 
 // acc += b * a with the accumulator in AGPRs; the memory clobber keeps every
@@ -323,7 +322,7 @@ __global__ void __launch_bounds__(T::THREADS, 1) nt_ordered(const OP op)
     // no load may still be writing LDS when the ring is used again or the
     // workgroup ends
     lds_barrier<0>();
-    op.template epilogue<T>(t, acc, lane, wave, smem, smem + T::BM * T::WTN * 2);
+    op.template epilogue<T>(t, acc, lane, wave, smem, smem + 32768);
 }
 
 // One 256 x 256 tile after another per workgroup, one workgroup per CU, four
@@ -353,9 +352,9 @@ struct Shape256 {
     using x8 = typename Elem<E>::x8;
     static constexpr int BM = 256, BN = 256, BK = 64, THREADS = 256;
     static constexpr int WAVES_M = 2, WAVES_N = 2, WAVES = 4;
-    static constexpr int WTM = 128, WTN = 128, FM = 8, FN = 8, ROUNDS = 2;
+    static constexpr int WTM = 128, WTN = 128, FM = 8, FN = 8;
     static constexpr int ROW_BYTES = 128;
-    static constexpr int SLOT = 32768;
+    static constexpr int SLOT = 32768, STAGE_MAX = 2 * SLOT;
     static constexpr int RS = 3, LS = 8;  // MFMAs per fragment read, per load
 };
 
@@ -369,6 +368,23 @@ __device__ __forceinline__ void mfma_agpr_first(f32x4& acc, const Elem<_Float16>
 __device__ __forceinline__ void mfma_agpr_first(f32x4& acc, const Elem<__bf16>::x8& b, const Elem<__bf16>::x8& a)
 {
     asm volatile("v_mfma_f32_16x16x32_bf16 %0, %1, %2, 0" : "+a"(acc) : "v"(b), "v"(a) : "memory");
+}
+
+// The kernel's argument, read again: what only the epilogue uses then needs
+// no scalar register through the K loop (kept, some would spill).
+template <class OP>
+__device__ __forceinline__ OP argument_again()
+{
+    typedef const __attribute__((address_space(4))) uint32_t word;
+    word* p = (word*)__builtin_amdgcn_kernarg_segment_ptr();
+    asm volatile("" : "+s"(p));
+    struct Words {
+        uint32_t w[sizeof(OP) / 4];
+    } a;
+    static_assert(sizeof(Words) == sizeof(OP), "whole words");
+#pragma unroll
+    for (unsigned i = 0; i < sizeof(OP) / 4; ++i) a.w[i] = p[i];
+    return __builtin_bit_cast(OP, a);
 }
 
 template <class T, class OP>
@@ -406,18 +422,19 @@ __global__ void __launch_bounds__(T::THREADS, 1) nt_persist(const OP op)
 
     // The tile being loaded runs up to one ahead of the one being computed.
     int id = blockIdx.x;
-    if (id >= op.tiles) return;
+    const int tiles = op.tiles;
+    if (id >= tiles) return;
     Tile t;
-    op.template tile<T::BM, T::BN>(id, t);
     __amdgpu_buffer_rsrc_t la, lb;
-    auto operands = [&]() __attribute__((always_inline)) {
+    auto start = [&](const OP& o, int n) __attribute__((always_inline)) {
+        o.template tile<T::BM, T::BN>(n, t);
         int na = 0, nb = 0;
-        const void* pa = op.a_rows(t, wave * 64, na);
-        const void* pb = op.template b_rows<T::WTN>(t, wave * 64, nb);
-        la = make_rsrc(pa, (uint32_t)min(na, 64) * pitch_a);
-        lb = make_rsrc(pb, (uint32_t)min(nb, 64) * pitch_b);
+        const void* pa = o.a_rows(t, wave * 64, na);
+        const void* pb = o.template b_rows<T::WTN>(t, wave * 64, nb);
+        la = make_rsrc(pa, (uint32_t)min(na, 64) * (uint32_t)o.lda * 2u);
+        lb = make_rsrc(pb, (uint32_t)min(nb, 64) * (uint32_t)o.template b_pitch<T::WTN>(wave * 64) * 2u);
     };
-    operands();
+    start(op, id);
 
     auto load = [&](unsigned char* dst, int l, uint32_t off, uint32_t soff) __attribute__((always_inline)) {
         lds_void* d = (lds_void*)(dst + (l & 4) * 1024);
@@ -583,9 +600,8 @@ __global__ void __launch_bounds__(T::THREADS, 1) nt_persist(const OP op)
         const Tile done = t;
         const int next = id + (int)gridDim.x;
         int lbase = nk;
-        if (next < op.tiles) {
-            op.template tile<T::BM, T::BN>(next, t);
-            operands();
+        if (next < tiles) {
+            start(argument_again<OP>(), next);
             lbase = 0;
         }
         step(lbase, Flag<false>{}, Flag<false>{});
@@ -595,8 +611,9 @@ __global__ void __launch_bounds__(T::THREADS, 1) nt_persist(const OP op)
         // hides them from the compiler's hazard checks
         asm volatile("s_nop 7\n\ts_nop 7\n\ts_nop 7" ::: "memory");
         __builtin_amdgcn_sched_barrier(0);
-        op.template epilogue<T>(done, acc, lane, wave, slot(0), slot(1));
-        if (next >= op.tiles) break;
+        const OP again = argument_again<OP>();
+        again.template epilogue<T>(done, acc, lane, wave, slot(0), slot(1));
+        if (next >= tiles) break;
         // every wave is done with this step's slots
         lds_barrier<63>();
         // B of the next tile's step 1 where the last step's A was
@@ -619,30 +636,190 @@ __device__ __forceinline__ int pinned(int lane)
     return lane;
 }
 
-// Stores four consecutive columns of one row through a buffer, without a
-// branch: `at` is the byte offset of row and first column, past the buffer
-// for rows that do not exist.  WHOLE: rows take 8-byte pieces and N is a
-// multiple of 4; otherwise each element goes out alone.  (A template, not a
-// condition: with two ways through an epilogue that holds 256 accumulators
-// the register allocator spills.)
-template <class E, bool WHOLE>
-__device__ __forceinline__ void buffer_store4(__amdgpu_buffer_rsrc_t rs, uint32_t at, int n, int N, const f32x4& v)
+// The same of a value that all lanes share, as a vector: offsets made of it
+// then need no scalar register each.
+__device__ __forceinline__ uint32_t as_vector(uint32_t v)
 {
-    const typename Elem<E>::x4 h = round4<E>(v);
-    if constexpr (WHOLE) {
-        __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(u32x2, h), rs, n < N ? at : kOob, 0, 0);
-    } else {
+    asm volatile("" : "+v"(v));
+    return v;
+}
+
+// LDS image of part of a tile: rows of COLS 16-bit values, 16-byte chunk c of
+// row x at c ^ (x % 16) (or % COLS / 8): the eight-byte pieces that the lanes
+// of a wave put fall on the banks evenly, and whole rows are read back without
+// conflicts.  The first 32 KiB lie at s0, the rest at s1.
+template <int COLS>
+struct Image {
+    static constexpr int PITCH = COLS * 2, CH = COLS / 8, KEY = (CH < 16 ? CH : 16) - 1;
+    unsigned char *s0, *s1;
+    __device__ __forceinline__ unsigned char* row(int x) const
+    {
+        const int off = x * PITCH;
+        return off < 32768 ? s0 + off : s1 + (off - 32768);
+    }
+    // where four values at row x, column c (a multiple of four) lie
+    template <class V>
+    __device__ __forceinline__ V* at(int x, int c) const
+    {
+        static_assert(sizeof(V) == 8, "four 16-bit values");
+        return (V*)(row(x) + (((c >> 3) ^ (x & KEY)) << 4) + (c & 4) * 2);
+    }
+    template <class V>
+    __device__ __forceinline__ void put(int x, int c, const V& v) const
+    {
+        *at<V>(x, c) = v;
+    }
+    __device__ __forceinline__ u32x4 get(int x, int chunk) const
+    {
+        return *(const u32x4*)(row(x) + ((chunk ^ (x & KEY)) << 4));
+    }
+};
+
+// Where a tile's rows go: a buffer from the tile's first row on, `pitch`
+// bytes to a row, columns first .. cols - 1.
+struct Rows {
+    __amdgpu_buffer_rsrc_t rs;
+    uint32_t pitch;
+    int first, cols;
+};
+template <class E>
+__device__ __forceinline__ Rows rows_at(E* base, int row, int rows, int most, int ld, int first, int cols)
+{
+    Rows r;
+    r.pitch = (uint32_t)ld * 2u;
+    r.rs = make_rsrc(base + (int64_t)row * ld, (uint32_t)min(most, rows - row) * r.pitch);
+    r.first = first;
+    r.cols = cols;
+    return r;
+}
+
+// Writes ROWS rows of an image out, whole rows by adjacent lanes, 16 bytes
+// each; `to(x)` is the row of `out` that image row x belongs to.  A store is
+// served 16 lanes at a time, a cache line each cycle: stored from the
+// accumulators' layout, where 16 adjacent lanes hold 16 rows, each would take
+// 64 cycles.  EIGHTS: out's rows take 16-byte pieces and hold a multiple of
+// eight columns; otherwise each element goes out alone.  (Templates, not
+// conditions: with two ways through an epilogue that holds 256 accumulators
+// the register allocator spills.)
+template <class T, int COLS, int ROWS, bool EIGHTS, class To>
+__device__ __forceinline__ void drain(const Image<COLS>& image, const Rows& out, To to, int lane, int wave)
+{
+    constexpr int CH = COLS / 8, RPI = 64 / CH, ITERS = ROWS / RPI / T::WAVES;
+    static_assert(ITERS * RPI * T::WAVES == ROWS, "rows split evenly over the waves");
+    const int ln = pinned(lane);
+    const int ch = ln % CH, n = out.first + ch * 8;
+    const int x0 = (int)as_vector((uint32_t)wave * (ITERS * RPI)) + ln / CH;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const E one = h[e];
-            __builtin_amdgcn_raw_buffer_store_b16(__builtin_bit_cast(uint16_t, one), rs,
-                                                  n + e < N ? at + (uint32_t)e * 2u : kOob, 0, 0);
+    for (int it = 0; it < ITERS; ++it) {
+        const int x = x0 + it * RPI;
+        const u32x4 v = image.get(x, ch);
+        const uint32_t at = (uint32_t)to(x) * out.pitch + (uint32_t)n * 2u;
+        if constexpr (EIGHTS) {
+            __builtin_amdgcn_raw_buffer_store_b128(v, out.rs, n < out.cols ? at : kOob, 0, 0);
+        } else {
+            // (one after another: the comparisons' results are scalar registers)
+            __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const uint32_t word = v[e / 2];
+                __builtin_amdgcn_raw_buffer_store_b16((uint16_t)(e & 1 ? word >> 16 : word), out.rs,
+                                                      n + e < out.cols ? at + (uint32_t)e * 2u : kOob, 0, 0);
+            }
         }
     }
 }
 
+// The other way: fills ROWS rows of an image from `in`, zeros where there is
+// nothing; rows take 16-byte pieces.
+template <class T, int COLS, int ROWS, class To>
+__device__ __forceinline__ void fill(const Image<COLS>& image, const Rows& in, To to, int lane, int wave)
+{
+    constexpr int CH = COLS / 8, RPI = 64 / CH, ITERS = ROWS / RPI / T::WAVES;
+    const int ln = pinned(lane);
+    const int x0 = (int)as_vector((uint32_t)wave * (ITERS * RPI)) + ln / CH;
+#pragma unroll
+    for (int it = 0; it < ITERS; ++it) {
+        const int x = x0 + it * RPI, n = in.first + ((ln % CH) ^ (x & Image<COLS>::KEY)) * 8;
+        const uint32_t at = (uint32_t)to(x) * in.pitch + (uint32_t)n * 2u;
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(in.rs, (lds_void*)image.row((wave * ITERS + it) * RPI), 16,
+                                                 n < in.cols ? at : kOob, 0, 0, 0);
+    }
+}
+
+// The tile row by row: value(i, j) is the four columns that this lane holds
+// of block (i, j) of FN in a wave row.
+template <class T, int FN, bool EIGHTS, class Value>
+__device__ __forceinline__ void write_rows(Value value, const Rows& out, int lane, int wave, unsigned char* s0,
+                                           unsigned char* s1)
+{
+    constexpr int WCOLS = FN * 16, COLS = WCOLS * T::WAVES_N, ROUNDS = T::BM * COLS * 2 > T::STAGE_MAX ? 2 : 1;
+    constexpr int RW = T::WTM / ROUNDS;  // staged rows of a wave row
+    static_assert(T::BM * COLS * 2 <= ROUNDS * T::STAGE_MAX, "a round fits");
+    const Image<COLS> image{s0, s1};
+    const int wm = wave / T::WAVES_N, wn = wave % T::WAVES_N;
+#pragma unroll
+    for (int h = 0; h < ROUNDS; ++h) {
+        const int ln = pinned(lane);
+#pragma unroll
+        for (int i = 0; i < T::FM / ROUNDS; ++i)
+#pragma unroll
+            for (int j = 0; j < FN; ++j)
+                image.put(wm * RW + i * 16 + (ln & 15), wn * WCOLS + j * 16 + 4 * (ln >> 4),
+                          value(h * (T::FM / ROUNDS) + i, j));
+        lds_barrier<63>();
+        drain<T, COLS, T::WAVES_M * RW, EIGHTS>(
+            image, out, [&](int x) { return x / RW * T::WTM + h * RW + x % RW; }, lane, wave);
+        lds_barrier<63>();
+    }
+}
+
+// Lanes 4 q .. 4 q + 3 hold values a, b, c, d of rows 4 q .. 4 q + 3; after
+// this they hold the four rows' a, the four rows' b, and so on.
+template <class X4>
+__device__ __forceinline__ X4 quad_transposed(const X4& v, int lane)
+{
+    const u32x2 d = __builtin_bit_cast(u32x2, v);
+    // with the neighbour: the even lane gets the pair's a and c, the odd one b and d
+    const bool odd = lane & 1, far = lane & 2;
+    const uint32_t n0 = __builtin_amdgcn_mov_dpp(d[0], 0xb1, 0xf, 0xf, true);  // quad_perm 1, 0, 3, 2
+    const uint32_t n1 = __builtin_amdgcn_mov_dpp(d[1], 0xb1, 0xf, 0xf, true);
+    const uint32_t sel = odd ? 0x03020706u : 0x05040100u;  // (own bytes 0 .. 3, the neighbour's 4 .. 7)
+    const uint32_t p0 = __builtin_amdgcn_perm(n0, d[0], sel), p1 = __builtin_amdgcn_perm(n1, d[1], sel);
+    // with the pair two lanes on: lanes 0, 1 give c, d (p1) and get a, b
+    const uint32_t give = far ? p0 : p1;
+    const uint32_t got = __builtin_amdgcn_mov_dpp(give, 0x4e, 0xf, 0xf, true);  // quad_perm 2, 3, 0, 1
+    const u32x2 r = {far ? got : p0, far ? p1 : got};
+    return __builtin_bit_cast(X4, r);
+}
+
+// The tile's transpose, row by row (rows n of BM columns m).  A lane's four
+// values belong to four rows of it, so four lanes exchange theirs first.
+template <class T, bool EIGHTS, class Value>
+__device__ __forceinline__ void write_turned(Value value, const Rows& out, int lane, int wave, unsigned char* s0,
+                                             unsigned char* s1)
+{
+    constexpr int ROUNDS = T::BM * T::BN * 2 > T::STAGE_MAX ? 2 : 1;
+    constexpr int RW = T::WTN / ROUNDS;  // staged rows of a wave column
+    const Image<T::BM> image{s0, s1};
+    const int wm = wave / T::WAVES_N, wn = wave % T::WAVES_N;
+#pragma unroll
+    for (int h = 0; h < ROUNDS; ++h) {
+        const int ln = pinned(lane);
+#pragma unroll
+        for (int i = 0; i < T::FM; ++i)
+#pragma unroll
+            for (int j = 0; j < T::FN / ROUNDS; ++j)
+                image.put(wn * RW + j * 16 + 4 * (ln >> 4) + (ln & 3), wm * T::WTM + i * 16 + (ln & 12),
+                          quad_transposed(value(i, h * (T::FN / ROUNDS) + j), ln));
+        lds_barrier<63>();
+        drain<T, T::BM, T::WAVES_N * RW, EIGHTS>(
+            image, out, [&](int x) { return x / RW * T::WTN + h * RW + x % RW; }, lane, wave);
+        lds_barrier<63>();
+    }
+}
+
 // C = A B^T.
-template <class E, bool WHOLE>
+template <class E, bool EIGHTS>
 struct StoreOp {
     static constexpr bool kPersist = true, kOblong = true;  // (256 x 256, 256 x 128 tiles)
     const E *A, *B;
@@ -674,20 +851,10 @@ struct StoreOp {
     }
     template <class T>
     __device__ __forceinline__ void epilogue(const Tile& t, const f32x4 (&acc)[T::FM][T::FN], int lane, int wave,
-                                             unsigned char*, unsigned char*) const
+                                             unsigned char* s0, unsigned char* s1) const
     {
-        const __amdgpu_buffer_rsrc_t out =
-            make_rsrc(C + (int64_t)t.m0 * ldc, (uint32_t)min(T::BM, M - t.m0) * (uint32_t)ldc * 2u);
-#pragma unroll
-        for (int i = 0; i < T::FM; ++i) {
-            const int ln = pinned(lane);
-            const int r = wave / T::WAVES_N * T::WTM + i * 16 + (ln & 15);
-#pragma unroll
-            for (int j = 0; j < T::FN; ++j) {
-                const int n = t.n0 + wave % T::WAVES_N * T::WTN + j * 16 + 4 * (ln >> 4);
-                buffer_store4<E, WHOLE>(out, ((uint32_t)r * (uint32_t)ldc + (uint32_t)n) * 2u, n, N, acc[i][j]);
-            }
-        }
+        write_rows<T, T::FN, EIGHTS>([&](int i, int j) { return round4<E>(acc[i][j]); },
+                                     rows_at(C, t.m0, M, T::BM, ldc, t.n0, N), lane, wave, s0, s1);
     }
 };
 

@@ -126,97 +126,9 @@ __global__ void __launch_bounds__(256) ns_copy_out(const half* __restrict__ X, i
     }
 }
 
-// Where a tile goes: rows of a matrix from the tile's first one on, `pitch`
-// bytes apart, and how many columns it has.
-struct Rows {
-    __amdgpu_buffer_rsrc_t rs;
-    uint32_t pitch;
-    int cols;
-};
-template <class E>
-__device__ __forceinline__ Rows rows_at(E* base, int row, int rows, int most, int ld, int cols)
-{
-    Rows r;
-    r.pitch = (uint32_t)ld * 2u;
-    r.rs = make_rsrc(base + (int64_t)row * ld, (uint32_t)min(most, rows - row) * r.pitch);
-    r.cols = cols;
-    return r;
-}
-
-// How a tile is written: as it is, transposed, or both; rows in whole pieces
-// (8 bytes, 16 for the transpose) or element by element.
-enum { kAsIs = 1, kTurned = 2, kPieces = 4 };
-
-// Writes the tile at (m0, n0).  The transpose goes through LDS: a lane's four values belong to
-// four of its rows.  It is staged as rows n of BM columns m, ROUNDS turns of
-// BN / ROUNDS rows, wave column wn's in stage[wn]; 16-byte chunk c of row n
-// sits at c ^ 2 ((n / 4) % 8), so that the four rows that 64 lanes write lie
-// in different banks.  It then leaves in whole rows, 16 bytes per lane.
-template <class E, int HOW, class T, class Value>
-__device__ __forceinline__ void write_tile(const f32x4 (&acc)[T::FM][T::FN], Value value, const Rows& direct,
-                                           const Rows& turned, int m0, int n0, int lane, int wave,
-                                           unsigned char* stage0, unsigned char* stage1)
-{
-    constexpr int FM = T::FM, FN = T::FN, WTM = T::WTM, WTN = T::WTN, ROUNDS = T::ROUNDS;
-    constexpr int PITCH = T::BM * 2, CH = T::BM / 8;
-    constexpr int RW = WTN / ROUNDS;  // staged rows per wave column
-    constexpr int RPI = 64 / CH;      // rows per wave-wide read
-    constexpr int ITERS = T::WAVES_N * RW / T::WAVES / RPI;
-    static_assert(ITERS * RPI * T::WAVES == T::WAVES_N * RW, "rows split evenly over the waves");
-    const int wm = wave / T::WAVES_N, wn = wave % T::WAVES_N;
-    unsigned char* mine = wn ? stage1 + (wn - 1) * RW * PITCH : stage0;
-#pragma unroll
-    for (int h = 0; h < ROUNDS; ++h) {
-#pragma unroll
-        for (int i = 0; i < FM; ++i) {
-            const int ln = pinned(lane);
-            const int r = wm * WTM + i * 16 + (ln & 15);
-#pragma unroll
-            for (int jj = 0; jj < FN / ROUNDS; ++jj) {
-                const int j = h * (FN / ROUNDS) + jj;
-                const int c = wn * WTN + j * 16 + 4 * (ln >> 4);
-                const f32x4 v = value(r, c, acc[i][j]);
-                if constexpr (HOW & kAsIs)
-                    buffer_store4<E, (HOW & kPieces) != 0>(
-                        direct.rs, (uint32_t)r * direct.pitch + (uint32_t)(n0 + c) * 2u, n0 + c, direct.cols, v);
-                if constexpr (HOW & kTurned) {
-                    const typename Elem<E>::x4 e4 = round4<E>(v);
-                    const int row = jj * 16 + 4 * (ln >> 4);  // (row / 4 is the same for the four)
-                    unsigned char* at = mine + row * PITCH + (((r >> 3) ^ ((2 * ((row >> 2) & 7)) & (CH - 1))) << 4) +
-                                        (r & 7) * 2;
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) *(E*)(at + e * PITCH) = e4[e];
-                }
-            }
-        }
-        if constexpr (HOW & kTurned) {
-            lds_barrier<63>();
-            const int ln = pinned(lane);
-#pragma unroll
-            for (int it = 0; it < ITERS; ++it) {
-                const int row = (wave * ITERS + it) * RPI + ln / CH;  // of both wave columns'
-                const int side = row / RW, local = row - side * RW, ch = ln % CH;
-                const unsigned char* from = (side ? stage1 + (side - 1) * RW * PITCH : stage0) + local * PITCH +
-                                            ((ch ^ ((2 * ((local >> 2) & 7)) & (CH - 1))) << 4);
-                const typename Elem<E>::x8 v = *(const typename Elem<E>::x8*)from;
-                const int m = m0 + ch * 8;
-                const uint32_t at = (uint32_t)(side * WTN + h * RW + local) * turned.pitch + (uint32_t)m * 2u;
-                if constexpr (HOW & kPieces) {
-                    __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, v), turned.rs,
-                                                           m < turned.cols ? at : kOob, 0, 0);
-                } else {
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        const E one = v[e];
-                        __builtin_amdgcn_raw_buffer_store_b16(__builtin_bit_cast(uint16_t, one), turned.rs,
-                                                              m + e < turned.cols ? at + (uint32_t)e * 2u : kOob, 0, 0);
-                    }
-                }
-            }
-            lds_barrier<63>();
-        }
-    }
-}
+// How a tile is written: as it is, transposed, or both; in 16-byte pieces or
+// element by element.
+enum { kAsIs = 1, kTurned = 2, kEights = 4 };
 
 // S (POLY false: alpha A A^T) or P (POLY true: alpha A A^T + beta A + gamma I,
 // A symmetric), [m, m] with pitch mp, tiles on and below the diagonal and
@@ -261,25 +173,62 @@ struct SymmetricOp {
                                              unsigned char* s0, unsigned char* s1) const
     {
         half* c = C + t.batch * stride_c;
-        const Rows direct = rows_at(c, t.m0, M, T::BM, mp, mp);
+        half4 v[T::FM][T::FN];
+        const Rows direct = rows_at(c, t.m0, M, T::BM, mp, t.n0, mp);
+        if constexpr (POLY) {
+            // the tile of A through LDS to the values that use it, which
+            // take its place there
+            constexpr int ROUNDS = T::BM * T::BN * 2 > T::STAGE_MAX ? 2 : 1, RW = T::WTM / ROUNDS, IR = T::FM / ROUNDS;
+            const Rows old = rows_at(A + t.batch * stride_a, t.m0, M, T::BM, lda, t.n0, mp);
+            const Image<T::BN> image{s0, s1};
+            const int wm = wave / T::WAVES_N, wn = wave % T::WAVES_N;
+            // (in vector registers: the scalar ones are all taken)
+            float gamma_here = t.m0 == t.n0 && wm == wn ? gamma : 0.0f, scale = alpha, linear = beta;
+            asm volatile("" : "+v"(gamma_here), "+v"(scale), "+v"(linear));
+            f32x4 diagonal;  // of a block: row l % 16 is column 4 (l / 16) + e
+#pragma unroll
+            for (int e = 0; e < 4; ++e) diagonal[e] = (lane & 15) == 4 * (lane >> 4) + e ? 1.0f : 0.0f;
+#pragma unroll
+            for (int h = 0; h < ROUNDS; ++h) {
+                auto to = [&](int x) { return x / RW * T::WTM + h * RW + x % RW; };
+                fill<T, T::BN, T::WAVES_M * RW>(image, old, to, lane, wave);
+                lds_barrier<0>();
+                const int ln = pinned(lane);
+#pragma unroll
+                for (int i = 0; i < IR; ++i)
+#pragma unroll
+                    for (int j = 0; j < T::FN; ++j) {
+                        const int x = wm * RW + i * 16 + (ln & 15), col = wn * T::WTN + j * 16 + 4 * (ln >> 4);
+                        half4* at = image.template at<half4>(x, col);
+                        const half4 a4 = *at;
+                        f32x4 w = acc[h * IR + i][j] * scale;
+                        // (where a wave's part is square, only its blocks (i, i)
+                        // can lie on the diagonal)
+                        constexpr bool SQUARE = T::WTM == T::WTN;
+                        const float on = SQUARE ? gamma_here
+                                         : t.m0 + wm * T::WTM + (h * IR + i) * 16 == t.n0 + wn * T::WTN + j * 16
+                                             ? gamma
+                                             : 0.0f;
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            w[e] = __builtin_fmaf(linear, (float)a4[e], w[e]);
+                            if (!SQUARE || h * IR + i == j) w[e] = __builtin_fmaf(diagonal[e], on, w[e]);
+                        }
+                        *at = v[h * IR + i][j] = round4<half>(w);
+                    }
+                lds_barrier<63>();
+                drain<T, T::BN, T::WAVES_M * RW, true>(image, direct, to, lane, wave);
+                lds_barrier<63>();
+            }
+        } else {
+            write_rows<T, T::FN, true>([&](int i, int j) { return v[i][j] = round4<half>(acc[i][j] * alpha); }, direct,
+                                       lane, wave, s0, s1);
+        }
         // Rows M .. mp - 1 of the accumulator are zero: the transpose's
         // padding.  A tile on the diagonal has no mirror image to write.
-        Rows turned = rows_at(c, t.n0, M, T::BN, mp, mp);
+        Rows turned = rows_at(c, t.n0, M, T::BN, mp, t.m0, mp);
         if (t.m0 == t.n0) turned.rs = make_rsrc(c, 0);
-        const Rows old = rows_at(A + t.batch * stride_a, t.m0, M, T::BM, lda, mp);
-        auto value = [&](int r, int col, const f32x4& sum) __attribute__((always_inline)) {
-            f32x4 v = sum * alpha;
-            if constexpr (POLY) {
-                const int n = t.n0 + col;
-                const uint32_t at = n < mp ? (uint32_t)r * old.pitch + (uint32_t)n * 2u : kOob;
-                const half4 a4 = __builtin_bit_cast(half4, __builtin_amdgcn_raw_buffer_load_b64(old.rs, at, 0, 0));
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    v[e] += __builtin_fmaf(beta, (float)a4[e], n + e == t.m0 + r ? gamma : 0.0f);
-            }
-            return v;
-        };
-        write_tile<half, kAsIs | kTurned | kPieces, T>(acc, value, direct, turned, t.m0, t.n0, lane, wave, s0, s1);
+        write_turned<T, true>([&](int i, int j) { return v[i][j]; }, turned, lane, wave, s0, s1);
     }
 };
 
@@ -289,7 +238,7 @@ struct SymmetricOp {
 template <bool LAST, int HOW>
 struct ApplyOp {
     // (element by element, the 256 x 256 kernel would spill scalar registers)
-    static constexpr bool kPersist = (HOW & kPieces) != 0, kOblong = true;
+    static constexpr bool kPersist = (HOW & kEights) != 0, kOblong = true;
     const half *P, *Xt;
     half *X, *XtNew;
     __bf16* out;
@@ -325,19 +274,22 @@ struct ApplyOp {
     __device__ __forceinline__ void epilogue(const Tile& t, const f32x4 (&acc)[T::FM][T::FN], int lane, int wave,
                                              unsigned char* s0, unsigned char* s1) const
     {
-        auto value = [&](int, int, const f32x4& sum) __attribute__((always_inline)) { return LAST ? sum * alpha : sum; };
+        constexpr bool EIGHTS = (HOW & kEights) != 0;
         if constexpr (LAST) {
             __bf16* o = out + t.batch * stride_o;
-            Rows direct = {}, turned = {};
-            if constexpr (HOW & kAsIs) direct = rows_at(o, t.m0, M, T::BM, ldo, N);
-            if constexpr (HOW & kTurned) turned = rows_at(o, t.n0, N, T::BN, ldo, M);
-            write_tile<__bf16, HOW, T>(acc, value, direct, turned, t.m0, t.n0, lane, wave, s0, s1);
+            auto value = [&](int i, int j) { return round4<__bf16>(acc[i][j] * alpha); };
+            if constexpr (HOW & kAsIs)
+                write_rows<T, T::FN, EIGHTS>(value, rows_at(o, t.m0, M, T::BM, ldo, t.n0, N), lane, wave, s0, s1);
+            if constexpr (HOW & kTurned)
+                write_turned<T, EIGHTS>(value, rows_at(o, t.n0, N, T::BN, ldo, t.m0, M), lane, wave, s0, s1);
         } else {
             // (columns N .. np - 1 and rows M .. ldb - 1 of the accumulator
             // are zero: the padding of both)
-            const Rows direct = rows_at(X + t.batch * stride_x, t.m0, M, T::BM, np, np);
-            const Rows turned = rows_at(XtNew + t.batch * stride_x, t.n0, N, T::BN, ldb, ldb);
-            write_tile<half, HOW, T>(acc, value, direct, turned, t.m0, t.n0, lane, wave, s0, s1);
+            auto value = [&](int i, int j) { return round4<half>(acc[i][j]); };
+            write_rows<T, T::FN, true>(value, rows_at(X + t.batch * stride_x, t.m0, M, T::BM, np, t.n0, np), lane, wave,
+                                       s0, s1);
+            write_turned<T, true>(value, rows_at(XtNew + t.batch * stride_x, t.n0, N, T::BN, ldb, t.m0, ldb), lane, wave,
+                                  s0, s1);
         }
     }
 };
@@ -450,11 +402,11 @@ int run(const E* G, __bf16* out, int64_t batch, int64_t rows, int64_t cols, int6
         };
         const bool eights = (uintptr_t)out % 16 == 0 && ldo % 8 == 0 && cols % 8 == 0 && stride_o % 8 == 0;
         if (i + 1 < steps)
-            rc = apply(ApplyOp<false, kAsIs | kTurned | kPieces>{});
+            rc = apply(ApplyOp<false, kAsIs | kTurned | kEights>{});
         else if (tall)
-            rc = eights ? apply(ApplyOp<true, kTurned | kPieces>{}) : apply(ApplyOp<true, kTurned>{});
+            rc = eights ? apply(ApplyOp<true, kTurned | kEights>{}) : apply(ApplyOp<true, kTurned>{});
         else
-            rc = eights ? apply(ApplyOp<true, kAsIs | kPieces>{}) : apply(ApplyOp<true, kAsIs>{});
+            rc = eights ? apply(ApplyOp<true, kAsIs | kEights>{}) : apply(ApplyOp<true, kAsIs>{});
         if (rc) return rc;
     }
     return hipSuccess;

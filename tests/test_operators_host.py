@@ -47,6 +47,20 @@ def test_no_kernel_spills(name):
         assert r["vgprs"] + r["agprs"] <= 512 and r["lds_bytes"] <= 160 * 1024, k
 
 
+@pytest.mark.parametrize("name", build.OPERATORS)
+def test_wide_buffer_stores_take_no_scalar_offset(name, tmp_path):
+    """After a store of more than eight bytes whose offset is a scalar register
+    the compiler lets the next instruction write the store's data registers,
+    and the store then wrote the new value now and then (seen in the last lanes
+    of each sixteen).  With an immediate offset it keeps them apart."""
+    import _isa
+    asm = _isa.disassemble(operators.library_path(name), tmp_path)
+    stores = [l.split("//")[0].strip() for l in asm.splitlines() if re.search(r"\bbuffer_store_dwordx[34]\b", l)]
+    assert stores or name == "gemv_w4"
+    bad = [l for l in stores if not re.search(r", 0 (offen|idxen)|, off, s\[[0-9:]+\], 0", l)]
+    assert bad == []
+
+
 def test_missing_library_raises(monkeypatch, tmp_path):
     monkeypatch.setattr(operators, "_HERE", str(tmp_path))
     monkeypatch.setattr(operators, "_libs", {})
@@ -87,7 +101,7 @@ def test_gated_empty_is_a_no_op():
 
 def test_gated_sizes():
     lib = operators.load("gated_nt")
-    assert lib.gated_nt_saved_bytes(3, 5) == 3 * 8 * 2 * 4   # columns in fours, two values, four bytes
+    assert lib.gated_nt_saved_bytes(3, 17) == 2 * 256 * 2 * 4   # blocks of 16 x 16, two values, four bytes
     assert lib.gated_nt_saved_bytes(-1, 5) == -1 and lib.gated_nt_saved_bytes(3, 1 << 31) == -1
     assert lib.gated_nt_workspace(A, B, C, 4, 16, 8, 16, 16, 16) == 0
     assert lib.gated_nt_workspace(A, B, C, 4, 16, 8, 24, 16, 32) == 0   # any pitch that is a multiple of 8
