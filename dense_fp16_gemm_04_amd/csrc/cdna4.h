@@ -79,17 +79,22 @@ __device__ __forceinline__ void lds_barrier()
 // 16-byte read serves fall on 16 different bank groups.
 __device__ __forceinline__ int swizzle(int row, int chunk) { return chunk ^ ((row >> 1) & 7); }
 
-// Workgroup (or persistent tile) number -> tile.  Workgroups are dealt to
-// the XCDs in turn, so numbers are first renamed to give each XCD one
-// contiguous range; that range is swept in groups of eight tile rows, column
-// by column, so tiles that run together share rows of both operands.
-__device__ __forceinline__ void tile_of(int id, int tiles_m, int tiles_n, int& tm, int& tn)
+// Workgroup (or persistent tile) number -> place in the linear order of all
+// tiles.  Workgroups are dealt to the XCDs in turn, so numbers are renamed to
+// give each XCD, with its own L2, one contiguous range.
+__device__ __forceinline__ int xcd_order(int id, int total)
 {
-    constexpr int group_m = 8;
-    const int total = tiles_m * tiles_n;
     const int per = total / kXcds, extra = total % kXcds;
     const int x = id % kXcds;
-    const int lin = x * per + (x < extra ? x : extra) + id / kXcds;
+    return x * per + (x < extra ? x : extra) + id / kXcds;
+}
+
+// Place in the linear order of one matrix -> tile.  Groups of eight tile rows
+// are swept column by column, so tiles that run together share rows of both
+// operands.
+__device__ __forceinline__ void grid_tile(int lin, int tiles_m, int tiles_n, int& tm, int& tn)
+{
+    constexpr int group_m = 8;
     const int width = group_m * tiles_n;
     const int g = lin / width;
     const int first = g * group_m;
@@ -97,6 +102,31 @@ __device__ __forceinline__ void tile_of(int id, int tiles_m, int tiles_n, int& t
     const int r = lin - g * width;
     tm = first + r % rows;
     tn = r / rows;
+}
+
+// The same for the tiles that reach the diagonal of a square matrix of
+// `tiles` tile rows or lie below it, q tiles wide to each tile row's height:
+// of a group's rows first the columns before the group's own, then the rest
+// row by row.
+__device__ __forceinline__ void triangle_tile(int lin, int tiles, int q, int& tm, int& tn)
+{
+    constexpr int group_m = 8;
+    auto before = [=](int row) { return q * (row * (row + 1) / 2); };
+    int row = (int)((__builtin_sqrtf(8.0f * (float)(lin / q) + 1.0f) - 1.0f) * 0.5f);  // off by one at most
+    while (before(row) > lin) --row;
+    while (before(row + 1) <= lin) ++row;
+    const int first = row / group_m * group_m, rows = min(tiles - first, group_m);
+    int r = lin - before(first);
+    if (r < rows * q * first) {
+        tm = first + r % rows;
+        tn = r / rows;
+        return;
+    }
+    r -= rows * q * first;
+    int i = 0;
+    while (before(i + 1) <= r) ++i;
+    tm = first + i;
+    tn = q * first + r - before(i);
 }
 
 }  // namespace cdna4

@@ -58,7 +58,7 @@ constexpr int kBlockFloats = 512;
 
 template <class E, bool SAVE, bool EIGHTS>
 struct GatedOp {
-    static constexpr bool kPersist = true, kOblong = true;  // (256 x 256, 256 x 128 tiles)
+    static constexpr bool kPersist = true, kOblong = true, kSplit = false;
     const E *X, *Wg, *Wu;
     E* H;
     float* saved;
@@ -69,7 +69,7 @@ struct GatedOp {
     __device__ __forceinline__ void tile(int id, Tile& t) const
     {
         int tm, tn;
-        tile_of(id, tiles_m, tiles_n, tm, tn);
+        grid_tile(xcd_order(id, tiles), tiles_m, tiles_n, tm, tn);
         t.m0 = tm * BM;
         t.n0 = tn * (BN / 2);
         t.batch = 0;
@@ -228,21 +228,26 @@ int launch_transpose(const E* src, int64_t ld, E* dst, int64_t ldd, int64_t rows
     return (int)hipGetLastError();
 }
 
-// C [M, N] = A B^T, both operands with K elements to a row.
+// C [M, N] = A B^T, all operands with K elements to a row; with a second A
+// and C, two products with the same B at once.
 template <class E>
-int product(const E* A, const E* B, E* C, int64_t M, int64_t N, int64_t K, int64_t ldc, hipStream_t stream)
+int product(const E* A0, const E* A1, const E* B, E* C0, E* C1, int64_t M, int64_t N, int64_t K, int64_t ldc0, int64_t ldc1,
+            float* partial, hipStream_t stream)
 {
     auto with = [&](auto op) {
-        op.A = A;
+        op.A[0] = A0;
+        op.A[1] = A1;
         op.B = B;
-        op.C = C;
+        op.C[0] = C0;
+        op.C[1] = C1;
         op.M = (int)M;
         op.N = (int)N;
         op.K = op.lda = op.ldb = (int)K;
-        op.ldc = (int)ldc;
-        return launch_grid<E>(op, M, N, 1, 1, K, stream);
+        op.ldc[0] = (int)ldc0;
+        op.ldc[1] = (int)ldc1;
+        return launch_grid<E>(op, M, N, 1, A1 ? 2 : 1, K, partial, stream);
     };
-    return eights(C, N, ldc) ? with(StoreOp<E, true>{}) : with(StoreOp<E, false>{});
+    return eights(C0, N, ldc0) && (!A1 || eights(C1, N, ldc1)) ? with(StoreOp<E, true>{}) : with(StoreOp<E, false>{});
 }
 
 // Copies of the operands that the kernels cannot read in place.
@@ -270,6 +275,7 @@ struct ForwardSpace {
 template <class E>
 struct BackwardSpace {
     E *wt, *xt, *dgu, *dgt, *dut;
+    float* partial;
     int64_t Tp, Fp, bytes;
     BackwardSpace(void* base, int64_t T, int64_t D, int64_t F)
     {
@@ -281,6 +287,7 @@ struct BackwardSpace {
         dgu = c.take<E>(T * 2 * Fp);
         dgt = c.take<E>(F * Tp);
         dut = c.take<E>(F * Tp);
+        partial = std::max(2 * Fp, Tp) >= kSplitK ? c.take<float>(kSplitFloats) : nullptr;
         bytes = c.used();
     }
 };
@@ -334,7 +341,7 @@ int forward(const E* X, const E* Wg, const E* Wu, E* H, float* saved, int64_t T,
     op.F = (int)F;
     op.ldh = (int)ldh;
     op.act = activation_of(activation);
-    return launch_grid<E>(op, T, F, 2, 1, Dp, stream);
+    return launch_grid<E>(op, T, F, 2, 1, Dp, nullptr, stream);
 }
 
 template <class E>
@@ -355,12 +362,11 @@ int backward(const E* dH, const E* X, const E* Wg, const E* Wu, const float* sav
         // [Wg; Wu]^T, D x 2 Fp, zeros between the two
         if ((rc = launch_transpose(Wg, ldg, w.wt, 2 * w.Fp, F, D, w.Fp, stream))) return rc;
         if ((rc = launch_transpose(Wu, ldu, w.wt + w.Fp, 2 * w.Fp, F, D, w.Fp, stream))) return rc;
-        if ((rc = product(w.dgu, w.wt, dX, T, D, 2 * w.Fp, lddx, stream))) return rc;
+        if ((rc = product<E>(w.dgu, nullptr, w.wt, dX, nullptr, T, D, 2 * w.Fp, lddx, 0, w.partial, stream))) return rc;
     }
     if (F > 0 && D > 0) {
         if ((rc = launch_transpose(X, ldx, w.xt, w.Tp, T, D, w.Tp, stream))) return rc;
-        if ((rc = product(w.dgt, w.xt, dWg, F, D, w.Tp, lddg, stream))) return rc;
-        if ((rc = product(w.dut, w.xt, dWu, F, D, w.Tp, lddu, stream))) return rc;
+        if ((rc = product<E>(w.dgt, w.dut, w.xt, dWg, dWu, F, D, w.Tp, lddg, lddu, w.partial, stream))) return rc;
     }
     return hipSuccess;
 }

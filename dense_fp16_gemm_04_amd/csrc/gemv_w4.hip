@@ -385,7 +385,7 @@ gemm_w4_kernel(const E* __restrict__ X, const unsigned char* __restrict__ Q, con
     const int q = wave >> 2, part = wave & 3;  // x's tile, and which 16 FN rows of W
     const int r = lane & 15, h = lane >> 4;
     int tm, tn;
-    tile_of(blockIdx.x, tiles_m, tiles_n, tm, tn);
+    grid_tile(xcd_order(blockIdx.x, tiles_m * tiles_n), tiles_m, tiles_n, tm, tn);
     const int m0 = tm * BM, n0 = tn * BN;
     const uint32_t pitch_x = (uint32_t)ldx * 2u, pitch_q = (uint32_t)ldq;
     const __amdgpu_buffer_rsrc_t bx = make_rsrc(X + (int64_t)m0 * ldx, (uint32_t)min(BM, M - m0) * pitch_x);

@@ -26,6 +26,8 @@
 //                                  T::STAGE_MAX bytes of LDS: 32 KiB at s0 and
 //                                  the rest at s1; a barrier has passed that
 //                                  makes them free, and another follows
+//   bool outside(t)                (kSplit) nothing of the result is in a
+//                                  sub-tile that starts there
 // and the fields K (elements, a multiple of 8), lda (A's row pitch in
 // elements; pitches are multiples of 8 and below 2^21), tiles.  Every row
 // starts on 16 bytes.
@@ -40,6 +42,7 @@ using namespace cdna4;
 
 struct Tile {
     int m0, n0, batch;
+    bool mirror;  // (symmetric results) the tile's transpose is written too
 };
 
 // Row `row` of an operand of `rows` rows and the number of rows from there
@@ -232,8 +235,19 @@ __device__ __forceinline__ void mfma_agpr(f32x4& acc, const Elem<__bf16>::x8& b,
 //               back, so every wave is done with this step's operand tiles;
 //   sub-step 1: its MFMAs, with the next step's first fragment reads and the
 //               loads of step ks + S, into the stage this step leaves.
+//
+// Split: tiles `full` and on are summed by `parts` workgroups each, over
+// equal shares of K's steps; each leaves its accumulators, in the lanes'
+// order, in `partial`, and nt_join adds them (in a fixed order) and writes
+// the tile out.  This fills the CUs that a last wave of few tiles would
+// leave idle.
+struct Split {
+    int full, parts;
+    float* partial;
+};
+
 template <class T, class OP>
-__global__ void __launch_bounds__(T::THREADS, 1) nt_ordered(const OP op)
+__global__ void __launch_bounds__(T::THREADS, 1) nt_ordered(const OP op, const Split split)
 {
     using x8 = typename T::x8;
     constexpr int S = T::STAGES, G = T::FM * T::FN, R = T::FM + T::FN;
@@ -244,10 +258,19 @@ __global__ void __launch_bounds__(T::THREADS, 1) nt_ordered(const OP op)
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
     const int wm = wave / T::WAVES_N, wn = wave % T::WAVES_N;
 
-    Tile t;
-    op.template tile<T::BM, T::BN>(blockIdx.x, t);
-    const Loader<T> loader(op, t, lane, wave & 3);
     const int K = op.K;
+    const int nk = (K + T::BK - 1) / T::BK, nfull = K / T::BK;
+    int id = blockIdx.x, part = -1, begin = 0, end = nk;  // the steps to add up
+    if (id >= split.full) {
+        const int n = id - split.full;
+        id = split.full + n / split.parts;
+        part = n % split.parts;
+        begin = (int)((int64_t)nk * part / split.parts);
+        end = (int)((int64_t)nk * (part + 1) / split.parts);
+    }
+    Tile t;
+    op.template tile<T::BM, T::BN>(id, t);
+    const Loader<T> loader(op, t, lane, wave & 3);
 
     const int fr = lane & 15, fh = lane >> 4;
     const int pos[2] = {swizzle(fr, fh) * 16, swizzle(fr, 4 + fh) * 16};
@@ -283,7 +306,6 @@ __global__ void __launch_bounds__(T::THREADS, 1) nt_ordered(const OP op)
         }
     };
 
-    const int nk = (K + T::BK - 1) / T::BK, nfull = K / T::BK;
     auto run = [&](auto ldtag) __attribute__((always_inline)) {
         constexpr bool LD = decltype(ldtag)::value;
         // every stage is free at the start: fill them all, then wait for step 0
@@ -291,7 +313,7 @@ __global__ void __launch_bounds__(T::THREADS, 1) nt_ordered(const OP op)
         for (int s = 0; s < S; ++s)
 #pragma unroll
             for (int l = 0; l < T::LOADS; ++l)
-                if constexpr (LD) loader.load(smem + s * T::STAGE_BYTES, l, s, K, Flag<true>{});
+                if constexpr (LD) loader.load(smem + s * T::STAGE_BYTES, l, begin + s, K, Flag<true>{});
         lds_barrier<T::LOADS * (S - 1)>();
 #pragma unroll
         for (int idx = 0; idx < R; ++idx) read_one(0, smem, idx);
@@ -302,15 +324,16 @@ __global__ void __launch_bounds__(T::THREADS, 1) nt_ordered(const OP op)
             unsigned char* next = smem + nxt * T::STAGE_BYTES;
             substep(0, base, Flag<false>{}, base, 0, masked);
             lds_barrier<T::LOADS * (S - 2)>();
-            // (steps past the end of K load zeros into stages never read)
+            // (what steps past the last load, zeros past the end of K, is
+            // never read)
             substep(1, next, Flag<LD>{}, base, ks + S, masked);
             cur = nxt;
         };
-        int ks = 0;
-        for (; ks < nk && ks + S < nfull; ++ks) step(ks, Flag<false>{});
-        for (; ks < nk; ++ks) step(ks, Flag<true>{});
+        int ks = begin;
+        for (; ks < end && ks + S < nfull; ++ks) step(ks, Flag<false>{});
+        for (; ks < end; ++ks) step(ks, Flag<true>{});
     };
-    if (nk > 0) {
+    if (end > begin) {
         if (wave < T::LOADERS)
             run(Flag<true>{});
         else
@@ -322,7 +345,74 @@ __global__ void __launch_bounds__(T::THREADS, 1) nt_ordered(const OP op)
     // no load may still be writing LDS when the ring is used again or the
     // workgroup ends
     lds_barrier<0>();
-    op.template epilogue<T>(t, acc, lane, wave, smem, smem + 32768);
+    if (part < 0) {
+        op.template epilogue<T>(t, acc, lane, wave, smem, smem + 32768);
+        return;
+    }
+    float* to = split.partial + ((int64_t)((id - split.full) * split.parts + part) * T::WAVES + wave) * (G * 256) + lane * 4;
+#pragma unroll
+    for (int i = 0; i < T::FM; ++i)
+#pragma unroll
+        for (int j = 0; j < T::FN; ++j) *(f32x4*)(to + (i * T::FN + j) * 256) = acc[i][j];
+}
+
+// Adds up the parts of the tiles that nt_ordered split and writes them out: a
+// workgroup for the sub-tile of each wave of a tile, so that few tiles still
+// read with many CUs, of four waves that take every fourth part (one wave
+// walking all parts took 24 us for sixteen, one workgroup for a whole tile 15).
+template <class T>
+struct WaveShape {
+    using E = typename T::E;
+    static constexpr int BM = T::WTM, BN = T::WTN, WAVES_M = 1, WAVES_N = 1, WAVES = 1;
+    static constexpr int WTM = T::WTM, WTN = T::WTN, FM = T::FM, FN = T::FN, STAGE_MAX = BM * BN * 2;
+};
+constexpr int kJoinWaves = 4;
+
+template <class T, class OP>
+__global__ void __launch_bounds__(kJoinWaves * kWave) nt_join(const OP op, const Split split)
+{
+    using W = WaveShape<T>;
+    constexpr int G = T::FM * T::FN;
+    __shared__ __attribute__((aligned(1024))) unsigned char smem[(kJoinWaves - 1) * G * 1024];
+    static_assert(sizeof(smem) >= W::STAGE_MAX, "the image fits");
+    const int lane = threadIdx.x & (kWave - 1), share = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+    const int n = blockIdx.x / T::WAVES, wave = blockIdx.x % T::WAVES;
+    Tile t;
+    op.template tile<T::BM, T::BN>(split.full + n, t);
+    t.m0 += wave / T::WAVES_N * T::WTM;
+    t.n0 += wave % T::WAVES_N * T::WTN;
+    if (op.outside(t)) return;
+    f32x4 acc[T::FM][T::FN];
+#pragma unroll
+    for (int i = 0; i < T::FM; ++i)
+#pragma unroll
+        for (int j = 0; j < T::FN; ++j) acc[i][j] = f32x4{0, 0, 0, 0};
+    const float* from = split.partial + ((int64_t)n * split.parts * T::WAVES + wave) * (G * 256) + lane * 4;
+    constexpr int AHEAD = 32 / G;  // parts whose loads are in flight together
+#pragma unroll AHEAD
+    for (int p = share; p < split.parts; p += kJoinWaves) {
+        const float* at = from + (int64_t)p * (T::WAVES * G * 256);
+#pragma unroll
+        for (int i = 0; i < T::FM; ++i)
+#pragma unroll
+            for (int j = 0; j < T::FN; ++j) acc[i][j] += *(const f32x4*)(at + (i * T::FN + j) * 256);
+    }
+    f32x4* sums = (f32x4*)smem + lane;
+    if (share > 0)
+#pragma unroll
+        for (int i = 0; i < T::FM; ++i)
+#pragma unroll
+            for (int j = 0; j < T::FN; ++j) sums[((share - 1) * G + i * T::FN + j) * 64] = acc[i][j];
+    __syncthreads();
+    if (share > 0) return;
+#pragma unroll
+    for (int s = 0; s < kJoinWaves - 1; ++s)
+#pragma unroll
+        for (int i = 0; i < T::FM; ++i)
+#pragma unroll
+            for (int j = 0; j < T::FN; ++j) acc[i][j] += sums[(s * G + i * T::FN + j) * 64];
+    lds_barrier<0>();
+    op.template epilogue<W>(t, acc, lane, 0, smem, smem);
 }
 
 // One 256 x 256 tile after another per workgroup, one workgroup per CU, four
@@ -821,23 +911,25 @@ __device__ __forceinline__ void write_turned(Value value, const Rows& out, int l
 // C = A B^T.
 template <class E, bool EIGHTS>
 struct StoreOp {
-    static constexpr bool kPersist = true, kOblong = true;  // (256 x 256, 256 x 128 tiles)
-    const E *A, *B;
-    E* C;
-    int M, N, K, lda, ldb, ldc, tiles, tiles_m, tiles_n;
+    static constexpr bool kPersist = true, kOblong = true, kSplit = true;  // (256 x 256, 256 x 128 tiles)
+    const E *A[2], *B;  // one product, or two with the same B
+    E* C[2];
+    int M, N, K, lda, ldb, ldc[2], tiles, tiles_m, tiles_n;
 
     template <int BM, int BN>
     __device__ __forceinline__ void tile(int id, Tile& t) const
     {
         int tm, tn;
-        tile_of(id, tiles_m, tiles_n, tm, tn);
-        t.batch = 0;
+        id = xcd_order(id, tiles);
+        t.batch = id >= tiles_m * tiles_n;
+        grid_tile(t.batch ? id - tiles_m * tiles_n : id, tiles_m, tiles_n, tm, tn);
         t.m0 = tm * BM;
         t.n0 = tn * BN;
     }
+    __device__ __forceinline__ bool outside(const Tile& t) const { return t.m0 >= M || t.n0 >= N; }
     __device__ __forceinline__ const E* a_rows(const Tile& t, int row, int& n) const
     {
-        return rows_from(A, t.m0 + row, M, lda, n);
+        return rows_from(t.batch ? A[1] : A[0], t.m0 + row, M, lda, n);
     }
     template <int WTN>
     __device__ __forceinline__ const E* b_rows(const Tile& t, int row, int& n) const
@@ -854,7 +946,7 @@ struct StoreOp {
                                              unsigned char* s0, unsigned char* s1) const
     {
         write_rows<T, T::FN, EIGHTS>([&](int i, int j) { return round4<E>(acc[i][j]); },
-                                     rows_at(C, t.m0, M, T::BM, ldc, t.n0, N), lane, wave, s0, s1);
+                                     rows_at(t.batch ? C[1] : C[0], t.m0, M, T::BM, t.batch ? ldc[1] : ldc[0], t.n0, N), lane, wave, s0, s1);
     }
 };
 

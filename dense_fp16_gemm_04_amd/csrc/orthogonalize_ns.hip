@@ -135,7 +135,7 @@ enum { kAsIs = 1, kTurned = 2, kEights = 4 };
 // their transposes.
 template <bool POLY>
 struct SymmetricOp {
-    static constexpr bool kPersist = true, kOblong = false;  // (square tiles)
+    static constexpr bool kPersist = true, kOblong = true, kSplit = true;
     const half* A;
     half* C;
     int M, K, lda, mp, tiles, per;  // per: tiles of one matrix
@@ -145,15 +145,17 @@ struct SymmetricOp {
     template <int BM, int BN>
     __device__ __forceinline__ void tile(int id, Tile& t) const
     {
+        id = xcd_order(id, tiles);
         t.batch = id / per;
-        id -= t.batch * per;
-        // row r of the triangle holds tiles r (r + 1) / 2 .. + r
-        int r = (int)((__builtin_sqrtf(8.0f * (float)id + 1.0f) - 1.0f) * 0.5f);
-        while (r * (r + 1) / 2 > id) --r;
-        while ((r + 1) * (r + 2) / 2 <= id) ++r;
-        t.m0 = r * BM;
-        t.n0 = (id - r * (r + 1) / 2) * BN;
+        int tm, tn;
+        triangle_tile(id - t.batch * per, (M + BM - 1) / BM, BM / BN, tm, tn);
+        t.m0 = tm * BM;
+        t.n0 = tn * BN;
+        // what a tile that reaches the diagonal mirrors is written by itself
+        // or its neighbour
+        t.mirror = t.n0 < t.m0;
     }
+    __device__ __forceinline__ bool outside(const Tile& t) const { return t.m0 >= M || t.n0 >= M; }
     __device__ __forceinline__ const half* a_rows(const Tile& t, int row, int& n) const
     {
         return rows_from(A + t.batch * stride_a, t.m0 + row, M, lda, n);
@@ -183,7 +185,7 @@ struct SymmetricOp {
             const Image<T::BN> image{s0, s1};
             const int wm = wave / T::WAVES_N, wn = wave % T::WAVES_N;
             // (in vector registers: the scalar ones are all taken)
-            float gamma_here = t.m0 == t.n0 && wm == wn ? gamma : 0.0f, scale = alpha, linear = beta;
+            float gamma_here = t.m0 + wm * T::WTM == t.n0 + wn * T::WTN ? gamma : 0.0f, scale = alpha, linear = beta;
             asm volatile("" : "+v"(gamma_here), "+v"(scale), "+v"(linear));
             f32x4 diagonal;  // of a block: row l % 16 is column 4 (l / 16) + e
 #pragma unroll
@@ -225,9 +227,9 @@ struct SymmetricOp {
                                        lane, wave, s0, s1);
         }
         // Rows M .. mp - 1 of the accumulator are zero: the transpose's
-        // padding.  A tile on the diagonal has no mirror image to write.
+        // padding.
         Rows turned = rows_at(c, t.n0, M, T::BN, mp, t.m0, mp);
-        if (t.m0 == t.n0) turned.rs = make_rsrc(c, 0);
+        if (!(T::WAVES == 1 ? t.mirror : t.n0 < t.m0)) turned.rs = make_rsrc(c, 0);  // (a whole tile's, of a sub-tile)
         write_turned<T, true>([&](int i, int j) { return v[i][j]; }, turned, lane, wave, s0, s1);
     }
 };
@@ -238,7 +240,7 @@ struct SymmetricOp {
 template <bool LAST, int HOW>
 struct ApplyOp {
     // (element by element, the 256 x 256 kernel would spill scalar registers)
-    static constexpr bool kPersist = (HOW & kEights) != 0, kOblong = true;
+    static constexpr bool kPersist = (HOW & kEights) != 0, kOblong = true, kSplit = true;
     const half *P, *Xt;
     half *X, *XtNew;
     __bf16* out;
@@ -250,12 +252,14 @@ struct ApplyOp {
     __device__ __forceinline__ void tile(int id, Tile& t) const
     {
         const int per = tiles_m * tiles_n;
+        id = xcd_order(id, tiles);  // (whole matrices of a batch to an XCD)
         t.batch = id / per;
         int tm, tn;
-        tile_of(id - t.batch * per, tiles_m, tiles_n, tm, tn);
+        grid_tile(id - t.batch * per, tiles_m, tiles_n, tm, tn);
         t.m0 = tm * BM;
         t.n0 = tn * BN;
     }
+    __device__ __forceinline__ bool outside(const Tile& t) const { return t.m0 >= M || t.n0 >= N; }
     __device__ __forceinline__ const half* a_rows(const Tile& t, int row, int& n) const
     {
         return rows_from(P + t.batch * stride_p, t.m0 + row, M, lda, n);
@@ -299,6 +303,7 @@ struct ApplyOp {
 struct Space {
     double* partial;
     half *x[2], *xt[2], *s, *p;
+    float* sums;  // of split tiles
     int64_t m, n, mp, np, stride_x, stride_s, bytes;
     Space(void* base, int64_t batch, int64_t rows, int64_t cols)
     {
@@ -316,6 +321,7 @@ struct Space {
         }
         s = c.take<half>(batch * stride_s);
         p = c.take<half>(batch * stride_s);
+        sums = n >= kSplitK ? c.take<float>(kSplitFloats) : nullptr;
         bytes = c.used();
     }
 };
@@ -323,11 +329,11 @@ struct Space {
 int64_t triangle(int64_t t) { return t * (t + 1) / 2; }
 
 template <class OP>
-int launch_symmetric(const OP& op, int64_t m, int64_t batch, hipStream_t stream)
+int launch_symmetric(const OP& op, int64_t m, int64_t batch, float* partial, hipStream_t stream)
 {
-    auto per = [=](const Kind& k) { return triangle((m + k.bm - 1) / k.bm); };
+    auto per = [=](const Kind& k) { return k.bm / k.bn * triangle((m + k.bm - 1) / k.bm); };
     return launch<half>(
-        op, op.K, [=](const Kind& k) { return k.bm == k.bn ? per(k) * batch : -1; },
+        op, op.K, partial, [=](const Kind& k) { return per(k) * batch; },
         [=](OP& o, const Kind& k) { o.per = (int)per(k); }, stream);
 }
 
@@ -372,7 +378,7 @@ int run(const E* G, __bf16* out, int64_t batch, int64_t rows, int64_t cols, int6
         s.stride_a = w.stride_x;
         s.stride_c = w.stride_s;
         s.alpha = (float)(1.0 / (scale * scale));
-        if ((rc = launch_symmetric(s, w.m, batch, stream))) return rc;
+        if ((rc = launch_symmetric(s, w.m, batch, w.sums, stream))) return rc;
         SymmetricOp<true> p = {};
         p.A = w.s;
         p.C = w.p;
@@ -382,7 +388,7 @@ int run(const E* G, __bf16* out, int64_t batch, int64_t rows, int64_t cols, int6
         p.alpha = (float)coefficients[3 * i + 2];
         p.beta = (float)coefficients[3 * i + 1];
         p.gamma = (float)coefficients[3 * i];
-        if ((rc = launch_symmetric(p, w.m, batch, stream))) return rc;
+        if ((rc = launch_symmetric(p, w.m, batch, w.sums, stream))) return rc;
         auto apply = [&](auto op) {
             op.P = w.p;
             op.Xt = w.xt[from];
@@ -398,7 +404,7 @@ int run(const E* G, __bf16* out, int64_t batch, int64_t rows, int64_t cols, int6
             op.stride_x = w.stride_x;
             op.stride_o = stride_o;
             op.alpha = (float)(1.0 / scale);
-            return launch_grid<half>(op, w.m, w.n, 1, batch, op.K, stream);
+            return launch_grid<half>(op, w.m, w.n, 1, batch, op.K, w.sums, stream);
         };
         const bool eights = (uintptr_t)out % 16 == 0 && ldo % 8 == 0 && cols % 8 == 0 && stride_o % 8 == 0;
         if (i + 1 < steps)

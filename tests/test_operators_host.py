@@ -114,7 +114,7 @@ def test_gated_sizes():
 
 def backward_args(**kw):
     a = dict(dH=A, X=B, Wg=C, Wu=D, saved=E, dX=F, dWg=G, dWu=H, T=4, D=16, F=8, lddh=8, ldx=16, ldg=16, ldu=16,
-             lddx=16, lddg=16, lddu=16, type=0, ws=W, ws_bytes=1 << 20, stream=None)
+             lddx=16, lddg=16, lddu=16, type=0, ws=W, ws_bytes=1 << 25, stream=None)
     assert set(kw) <= set(a)
     a.update(kw)
     return list(a.values())
@@ -134,7 +134,7 @@ def test_gated_backward_refuses(kw):
 
 def ns_args(**kw):
     a = dict(G=A, out=B, batch=2, rows=8, cols=16, ldg=16, stride_g=128, ldo=16, stride_o=128, type=0, steps=5,
-             coefficients=(ctypes.c_double * 15)(*([3.4445, -4.775, 2.0315] * 5)), eps=1e-7, ws=W, ws_bytes=1 << 20,
+             coefficients=(ctypes.c_double * 15)(*([3.4445, -4.775, 2.0315] * 5)), eps=1e-7, ws=W, ws_bytes=1 << 25,
              stream=None)
     assert set(kw) <= set(a)
     a.update(kw)
