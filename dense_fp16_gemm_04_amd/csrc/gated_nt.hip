@@ -138,14 +138,27 @@ struct GatedOp {
 // dH comes in by rows and turns in LDS to the blocks that `saved` holds.
 // Bound by its bytes: 2 + 8 read, 8 written per element.
 template <class E>
-__global__ void __launch_bounds__(relayout::kThreads)
-gated_slopes(const E* __restrict__ dH, const float* __restrict__ saved, E* __restrict__ dGU, E* __restrict__ dGT,
-             E* __restrict__ dUT, int T, int F, int64_t lddh, int Fp, int Tp, int tiles_f, int vec)
+struct Slopes {
+    const E* dH;
+    const float* saved;
+    E *dGU, *dGT, *dUT;
+    int T, F, Fp, Tp, vec;
+    int64_t lddh;
+
+    __host__ __device__ int64_t tiles() const
+    {
+        return (int64_t)((Tp + relayout::kTile - 1) / relayout::kTile) * ((Fp + relayout::kTile - 1) / relayout::kTile);
+    }
+    __device__ __forceinline__ void run(int id, E* tg, E* tu) const;
+};
+
+template <class E>
+__device__ __forceinline__ void Slopes<E>::run(int id, E* tg, E* tu) const
 {
     using x4 = typename Elem<E>::x4;
     using namespace relayout;
-    __shared__ E tg[kTile * kPitch], tu[kTile * kPitch];
-    const int t0 = (int)(blockIdx.x / tiles_f) * kTile, f0 = (int)(blockIdx.x % tiles_f) * kTile;
+    const int tiles_f = (Fp + kTile - 1) / kTile;
+    const int t0 = id / tiles_f * kTile, f0 = id % tiles_f * kTile;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int x = threadIdx.x & 15, y = threadIdx.x >> 4;
     // wave w takes the blocks of rows 16 w .. + 15; their P and Q first
@@ -199,6 +212,30 @@ gated_slopes(const E* __restrict__ dH, const float* __restrict__ saved, E* __res
     store_transposed(tu, dUT, Tp, t0, f0, Tp, F);
 }
 
+// All that the backward pass's products read, in one launch: the slopes and
+// up to three transposes, a 64 x 64 tile to a workgroup.
+template <class E>
+struct Prepare {
+    Slopes<E> slopes;
+    relayout::Transpose<E> turn[3];
+    int first[3];  // their first workgroups
+};
+
+template <class E>
+__global__ void __launch_bounds__(relayout::kThreads) gated_prepare(const Prepare<E> p)
+{
+    __shared__ E tiles[2][relayout::kTile * relayout::kPitch];
+    const int id = blockIdx.x;
+    if (id < p.first[0])
+        p.slopes.run(id, tiles[0], tiles[1]);
+    else if (id < p.first[1])
+        p.turn[0].run(id - p.first[0], tiles[0]);
+    else if (id < p.first[2])
+        p.turn[1].run(id - p.first[1], tiles[0]);
+    else
+        p.turn[2].run(id - p.first[2], tiles[0]);
+}
+
 // ------------------------------------------------------------------ host --
 
 bool vec4(const void* p, int64_t ld) { return (uintptr_t)p % 8 == 0 && ld % 4 == 0; }
@@ -213,18 +250,6 @@ int launch_copy(const E* src, int64_t ld, E* dst, int64_t ldd, int64_t rows, int
     if (work == 0) return hipSuccess;
     hipLaunchKernelGGL(relayout::copy_rows<E>, dim3((unsigned)std::min<int64_t>((work + 255) / 256, 65536)), dim3(256), 0,
                        stream, src, ld, dst, ldd, rows, (int)cols);
-    return (int)hipGetLastError();
-}
-
-template <class E>
-int launch_transpose(const E* src, int64_t ld, E* dst, int64_t ldd, int64_t rows, int64_t cols, int64_t padded,
-                     hipStream_t stream)
-{
-    const int64_t tr = (padded + 63) / 64, tc = (cols + 63) / 64;
-    if (tr * tc == 0) return hipSuccess;
-    if (tr * tc > abi::kMaxDim) return hipErrorInvalidValue;
-    hipLaunchKernelGGL(relayout::transpose<E>, dim3((unsigned)(tr * tc)), dim3(256), 0, stream, src, ld, dst, ldd,
-                       (int)rows, (int)cols, (int)padded, (int)tc, (int)vec4(src, ld));
     return (int)hipGetLastError();
 }
 
@@ -351,21 +376,29 @@ int backward(const E* dH, const E* X, const E* Wg, const E* Wu, const float* sav
 {
     const BackwardSpace<E> w(workspace, T, D, F);
     int rc;
-    const int64_t tt = (w.Tp + 63) / 64, tf = (w.Fp + 63) / 64;
-    if (tt * tf > abi::kMaxDim) return hipErrorInvalidValue;
-    if (tt * tf > 0) {
-        hipLaunchKernelGGL(gated_slopes<E>, dim3((unsigned)(tt * tf)), dim3(256), 0, stream, dH, saved, w.dgu, w.dgt,
-                           w.dut, (int)T, (int)F, lddh, (int)w.Fp, (int)w.Tp, (int)tf, (int)vec4(dH, lddh));
+    Prepare<E> p = {};
+    p.slopes = {dH, saved, w.dgu, w.dgt, w.dut, (int)T, (int)F, (int)w.Fp, (int)w.Tp, (int)vec4(dH, lddh), lddh};
+    if (T > 0) {
+        // [Wg; Wu]^T, D x 2 Fp, zeros between the two
+        p.turn[0] = {Wg, w.wt, ldg, 2 * w.Fp, (int)F, (int)D, (int)w.Fp, (int)vec4(Wg, ldg)};
+        p.turn[1] = {Wu, w.wt + w.Fp, ldu, 2 * w.Fp, (int)F, (int)D, (int)w.Fp, (int)vec4(Wu, ldu)};
+    }
+    if (F > 0) p.turn[2] = {X, w.xt, ldx, w.Tp, (int)T, (int)D, (int)w.Tp, (int)vec4(X, ldx)};
+    int64_t n = p.slopes.tiles();
+    for (int i = 0; i < 3; ++i) {
+        if (n > abi::kMaxDim) return hipErrorInvalidValue;
+        p.first[i] = (int)n;
+        n += p.turn[i].tiles();
+    }
+    if (n > abi::kMaxDim) return hipErrorInvalidValue;
+    if (n > 0) {
+        hipLaunchKernelGGL(gated_prepare<E>, dim3((unsigned)n), dim3(relayout::kThreads), 0, stream, p);
         if ((rc = (int)hipGetLastError())) return rc;
     }
     if (T > 0 && D > 0) {
-        // [Wg; Wu]^T, D x 2 Fp, zeros between the two
-        if ((rc = launch_transpose(Wg, ldg, w.wt, 2 * w.Fp, F, D, w.Fp, stream))) return rc;
-        if ((rc = launch_transpose(Wu, ldu, w.wt + w.Fp, 2 * w.Fp, F, D, w.Fp, stream))) return rc;
         if ((rc = product<E>(w.dgu, nullptr, w.wt, dX, nullptr, T, D, 2 * w.Fp, lddx, 0, w.partial, stream))) return rc;
     }
     if (F > 0 && D > 0) {
-        if ((rc = launch_transpose(X, ldx, w.xt, w.Tp, T, D, w.Tp, stream))) return rc;
         if ((rc = product<E>(w.dgt, w.dut, w.xt, dWg, dWu, F, D, w.Tp, lddg, lddu, w.partial, stream))) return rc;
     }
     return hipSuccess;

@@ -29,7 +29,7 @@ struct Kind {
     double tflops;  // on 256 CUs
     double wave_us;
 };
-constexpr Kind kKinds[] = {{256, 256, 1450.0, 4.0}, {256, 128, 1250.0, 3.0}, {128, 128, 1050.0, 3.0}, {64, 64, 480.0, 3.0}};
+constexpr Kind kKinds[] = {{256, 256, 1450.0, 6.0}, {256, 128, 1280.0, 5.0}, {128, 128, 1060.0, 3.5}, {64, 64, 600.0, 3.0}};
 constexpr int kNumKinds = 4;
 
 // Time of `tiles` tiles of sums over K: whole waves of tiles over the CUs at
@@ -58,8 +58,9 @@ inline double split_us(const Kind& k, int64_t tiles, int64_t K, int cus, int& pa
     double best = -1;
     const int most = rest ? (int)std::min<int64_t>(std::min<int64_t>(std::min(cus, kMaxParts) / rest, 16), K / (kSplitK / 2)) : 1;
     for (int p = 2; p <= most; ++p) {
-        // (a part more takes joining about 0.3 us)
-        const double sum = (double)full * (us + k.wave_us) + us / p + k.wave_us + 6.0 + 0.3 * p;
+        // (measured: 1000 x 1032 x 5472 as 72 tiles in 3 parts 23 + 5 us,
+        // as 36 of 256 x 128 in 7 parts 23 + 9)
+        const double sum = (double)full * (us + k.wave_us) + us / p + k.wave_us + 8.0 + 0.4 * p * (k.bm / 128);
         if (best < 0 || sum < best) {
             best = sum;
             parts = p;

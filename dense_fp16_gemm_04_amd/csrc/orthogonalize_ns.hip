@@ -42,20 +42,29 @@ __global__ void __launch_bounds__(256) ns_squares(const E* __restrict__ G, int64
     const int lane = threadIdx.x % lanes, first = threadIdx.x / lanes;
     const int64_t units = first < step ? (int64_t)rows * pieces : 0;
     typedef E x4 __attribute__((ext_vector_type(4)));
-    for (int64_t u = (int64_t)k * step + first; u < units; u += kNormBlocks * step) {
-        const int64_t r = pieces == 1 ? u : u / pieces;
-        const int c = ((int)(u - r * pieces) * 256 + lane) * 4;
-        const E* at = g + r * ldg + c;
-        x4 v = {};
-        if (vec && c + 3 < cols) {
-            v = *(const x4*)at;
-        } else {
+    const int64_t stride_u = (int64_t)kNormBlocks * step;
+    for (int64_t u0 = (int64_t)k * step + first; u0 < units; u0 += 4 * stride_u) {
+        x4 v[4];
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-                if (c + e < cols) v[e] = at[e];
+        for (int i = 0; i < 4; ++i) {  // (four loads in flight)
+            const int64_t u = u0 + i * stride_u;
+            const int64_t r = pieces == 1 ? u : u / pieces;
+            const int c = ((int)(u - r * pieces) * 256 + lane) * 4;
+            const E* at = g + r * ldg + c;
+            v[i] = x4{};
+            if (u >= units) continue;
+            if (vec && c + 3 < cols) {
+                v[i] = *(const x4*)at;
+            } else {
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    if (c + e < cols) v[i][e] = at[e];
+            }
         }
 #pragma unroll
-        for (int e = 0; e < 4; ++e) s += (double)(float)v[e] * (double)(float)v[e];
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) s += (double)(float)v[i][e] * (double)(float)v[i][e];
     }
     __shared__ double part[256];
     part[threadIdx.x] = s;

@@ -61,24 +61,35 @@ __global__ void __launch_bounds__(kThreads) copy_rows(const E* __restrict__ src,
     }
 }
 
-// dst[c][r] = src[r][c] for r < rows, 0 for rows <= r < padded.
+// dst[c][r] = src[r][c] for r < rows, 0 for rows <= r < padded: tile number
+// `id` of tiles().
 template <class E>
-__global__ void __launch_bounds__(kThreads) transpose(const E* __restrict__ src, int64_t lds_, E* __restrict__ dst,
-                                                      int64_t ldd, int rows, int cols, int padded, int tiles_c, int vec)
-{
-    __shared__ E tile[kTile * kPitch];
-    const int r0 = (int)(blockIdx.x / tiles_c) * kTile, c0 = (int)(blockIdx.x % tiles_c) * kTile;
-    const int x = threadIdx.x & 15, y = threadIdx.x >> 4;
-#pragma unroll
-    for (int it = 0; it < 4; ++it) {
-        const int r = it * 16 + y;
-        typename Elem<E>::x4 v = {};
-        if (r0 + r < rows) v = load4(src + (int64_t)(r0 + r) * lds_, c0 + x * 4, cols, vec);
-        *(typename Elem<E>::x4*)(tile + r * kPitch + x * 4) = v;
+struct Transpose {
+    const E* src;
+    E* dst;
+    int64_t lds_, ldd;
+    int rows, cols, padded, vec;
+
+    __host__ __device__ int64_t tiles() const
+    {
+        return (int64_t)((padded + kTile - 1) / kTile) * ((cols + kTile - 1) / kTile);
     }
-    __syncthreads();
-    store_transposed(tile, dst, ldd, r0, c0, padded, cols);
-}
+    __device__ __forceinline__ void run(int id, E* tile) const
+    {
+        const int tiles_c = (cols + kTile - 1) / kTile;
+        const int r0 = id / tiles_c * kTile, c0 = id % tiles_c * kTile;
+        const int x = threadIdx.x & 15, y = threadIdx.x >> 4;
+#pragma unroll
+        for (int it = 0; it < 4; ++it) {
+            const int r = it * 16 + y;
+            typename Elem<E>::x4 v = {};
+            if (r0 + r < rows) v = load4(src + (int64_t)(r0 + r) * lds_, c0 + x * 4, cols, vec);
+            *(typename Elem<E>::x4*)(tile + r * kPitch + x * 4) = v;
+        }
+        __syncthreads();
+        store_transposed(tile, dst, ldd, r0, c0, padded, cols);
+    }
+};
 
 }  // namespace relayout
 
