@@ -6,9 +6,15 @@
 //   X' = P X                [m, n] = P (X^T)^T from X^T [n, m]
 // so both X and X^T are kept, and the product that makes X' writes both.  S
 // and P are symmetric: only tiles on and below the diagonal are computed,
-// and the others are written as their transposes.  a is part of P: P's
-// diagonal is then near 1 once the singular values are, and its rounding
-// costs a third of what the rounding of bS + cSS (diagonal near -2.7) does.
+// and the others are written as their transposes.
+//
+// Rounding.  a is part of P: P's diagonal is then near 1 once the singular
+// values are, where that of bS + cSS is near -2.7.  The diagonal is still by
+// far P's largest part, so its rounding is taken back: row r of X' is
+// multiplied by d / binary16(d) of P's diagonal entry d, which makes that
+// entry exact and the others, small ones, off by as much.  (Relative error of
+// the bfloat16 result, 54 x 1286: 2.60e-3 without, 1.94e-3 with, 1.90e-3 with
+// an exact P; 40 x 4000: 3.13e-3, 2.27e-3, 2.28e-3.)
 #include "orthogonalize_ns.h"
 
 #include <algorithm>
@@ -144,9 +150,10 @@ enum { kAsIs = 1, kTurned = 2, kEights = 4 };
 // their transposes.
 template <bool POLY>
 struct SymmetricOp {
-    static constexpr bool kPersist = true, kOblong = true, kSplit = true;
+    static constexpr bool kPersist = !POLY, kOblong = true, kSplit = true;  // (P's epilogue would spill there)
     const half* A;
     half* C;
+    float* diag;  // (POLY) C's diagonal before it is rounded
     int M, K, lda, mp, tiles, per;  // per: tiles of one matrix
     int64_t stride_a, stride_c;
     float alpha, beta, gamma;
@@ -193,12 +200,14 @@ struct SymmetricOp {
             const Rows old = rows_at(A + t.batch * stride_a, t.m0, M, T::BM, lda, t.n0, mp);
             const Image<T::BN> image{s0, s1};
             const int wm = wave / T::WAVES_N, wn = wave % T::WAVES_N;
-            // (in vector registers: the scalar ones are all taken)
-            float gamma_here = t.m0 + wm * T::WTM == t.n0 + wn * T::WTN ? gamma : 0.0f, scale = alpha, linear = beta;
-            asm volatile("" : "+v"(gamma_here), "+v"(scale), "+v"(linear));
+            const float gamma_here = t.m0 + wm * T::WTM == t.n0 + wn * T::WTN ? gamma : 0.0f;
             f32x4 diagonal;  // of a block: row l % 16 is column 4 (l / 16) + e
 #pragma unroll
             for (int e = 0; e < 4; ++e) diagonal[e] = (lane & 15) == 4 * (lane >> 4) + e ? 1.0f : 0.0f;
+            auto on_diagonal = [&](int i, int j) { return t.m0 + wm * T::WTM + i * 16 == t.n0 + wn * T::WTN + j * 16; };
+            float mine[T::FM];  // the lane's entry of each block row on the diagonal, if it has one
+#pragma unroll
+            for (int i = 0; i < T::FM; ++i) mine[i] = 0.0f;
 #pragma unroll
             for (int h = 0; h < ROUNDS; ++h) {
                 auto to = [&](int x) { return x / RW * T::WTM + h * RW + x % RW; };
@@ -212,24 +221,38 @@ struct SymmetricOp {
                         const int x = wm * RW + i * 16 + (ln & 15), col = wn * T::WTN + j * 16 + 4 * (ln >> 4);
                         half4* at = image.template at<half4>(x, col);
                         const half4 a4 = *at;
-                        f32x4 w = acc[h * IR + i][j] * scale;
+                        f32x4 w = acc[h * IR + i][j] * alpha;
                         // (where a wave's part is square, only its blocks (i, i)
                         // can lie on the diagonal)
                         constexpr bool SQUARE = T::WTM == T::WTN;
-                        const float on = SQUARE ? gamma_here
-                                         : t.m0 + wm * T::WTM + (h * IR + i) * 16 == t.n0 + wn * T::WTN + j * 16
-                                             ? gamma
-                                             : 0.0f;
+                        const float on = SQUARE ? gamma_here : on_diagonal(h * IR + i, j) ? gamma : 0.0f;
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
-                            w[e] = __builtin_fmaf(linear, (float)a4[e], w[e]);
+                            w[e] = __builtin_fmaf(beta, (float)a4[e], w[e]);
                             if (!SQUARE || h * IR + i == j) w[e] = __builtin_fmaf(diagonal[e], on, w[e]);
                         }
-                        *at = v[h * IR + i][j] = round4<half>(w);
+                        const half4 w16 = round4<half>(w);
+                        *at = v[h * IR + i][j] = w16;
+                        if (!SQUARE || h * IR + i == j) {
+                            float d = diagonal[0] * w[0];
+#pragma unroll
+                            for (int e = 1; e < 4; ++e) d = __builtin_fmaf(diagonal[e], w[e], d);
+                            mine[h * IR + i] = SQUARE || on_diagonal(h * IR + i, j) ? d : mine[h * IR + i];
+                        }
                     }
                 lds_barrier<63>();
                 drain<T, T::BN, T::WAVES_M * RW, true>(image, direct, to, lane, wave);
                 lds_barrier<63>();
+            }
+            // (the waves whose rows have no entry in the tile store nothing)
+            const __amdgpu_buffer_rsrc_t entries =
+                make_rsrc(diag + (int64_t)t.batch * mp + t.m0, (uint32_t)max(0, min(T::BM, M - t.m0)) * 4u);
+            const int ln = pinned(lane);
+#pragma unroll
+            for (int i = 0; i < T::FM; ++i) {
+                const int m = wm * T::WTM + i * 16, n = t.m0 + m - t.n0 - wn * T::WTN;  // the entry's column in the wave's
+                const uint32_t at = (ln & 15) >> 2 == ln >> 4 && n >= 0 && n < T::WTN ? (uint32_t)(m + (ln & 15)) * 4u : kOob;
+                __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(uint32_t, mine[i]), entries, at, 0, 0);
             }
         } else {
             write_rows<T, T::FN, true>([&](int i, int j) { return v[i][j] = round4<half>(acc[i][j] * alpha); }, direct,
@@ -251,6 +274,7 @@ struct ApplyOp {
     // (element by element, the 256 x 256 kernel would spill scalar registers)
     static constexpr bool kPersist = (HOW & kEights) != 0, kOblong = true, kSplit = true;
     const half *P, *Xt;
+    const float* diag;  // P's diagonal before it was rounded
     half *X, *XtNew;
     __bf16* out;
     int M, N, K, lda, ldb, np, tiles, tiles_m, tiles_n, ldo;
@@ -288,9 +312,26 @@ struct ApplyOp {
                                              unsigned char* s0, unsigned char* s1) const
     {
         constexpr bool EIGHTS = (HOW & kEights) != 0;
+        // Each row's factor: what rounding took from its diagonal entry.  (A
+        // subnormal one is left as it is, its quotient may be far from 1; a
+        // part of a joined tile may lie past M.)
+        const __amdgpu_buffer_rsrc_t entries =
+            make_rsrc(diag + (int64_t)t.batch * lda + t.m0, (uint32_t)max(0, min(T::BM, M - t.m0)) * 4u);
+        float f[T::FM];
+#pragma unroll
+        for (int i = 0; i < T::FM; ++i) {
+            const uint32_t at = (uint32_t)(wave / T::WAVES_N * T::WTM + i * 16 + (pinned(lane) & 15)) * 4u;
+            f[i] = __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(entries, at, 0, 0));
+        }
+#pragma unroll
+        for (int i = 0; i < T::FM; ++i) {
+            const float d16 = (float)(half)f[i];
+            f[i] = __builtin_fabsf(d16) >= 0x1p-14f ? f[i] * __builtin_amdgcn_rcpf(d16) : 1.0f;
+            if constexpr (LAST) f[i] *= alpha;
+        }
         if constexpr (LAST) {
             __bf16* o = out + t.batch * stride_o;
-            auto value = [&](int i, int j) { return round4<__bf16>(acc[i][j] * alpha); };
+            auto value = [&](int i, int j) { return round4<__bf16>(acc[i][j] * f[i]); };
             if constexpr (HOW & kAsIs)
                 write_rows<T, T::FN, EIGHTS>(value, rows_at(o, t.m0, M, T::BM, ldo, t.n0, N), lane, wave, s0, s1);
             if constexpr (HOW & kTurned)
@@ -298,7 +339,7 @@ struct ApplyOp {
         } else {
             // (columns N .. np - 1 and rows M .. ldb - 1 of the accumulator
             // are zero: the padding of both)
-            auto value = [&](int i, int j) { return round4<half>(acc[i][j]); };
+            auto value = [&](int i, int j) { return round4<half>(acc[i][j] * f[i]); };
             write_rows<T, T::FN, true>(value, rows_at(X + t.batch * stride_x, t.m0, M, T::BM, np, t.n0, np), lane, wave,
                                        s0, s1);
             write_turned<T, true>(value, rows_at(XtNew + t.batch * stride_x, t.n0, N, T::BN, ldb, t.m0, ldb), lane, wave,
@@ -312,7 +353,7 @@ struct ApplyOp {
 struct Space {
     double* partial;
     half *x[2], *xt[2], *s, *p;
-    float* sums;  // of split tiles
+    float *diag, *sums;  // P's diagonal; of split tiles
     int64_t m, n, mp, np, stride_x, stride_s, bytes;
     Space(void* base, int64_t batch, int64_t rows, int64_t cols)
     {
@@ -330,6 +371,7 @@ struct Space {
         }
         s = c.take<half>(batch * stride_s);
         p = c.take<half>(batch * stride_s);
+        diag = c.take<float>(batch * mp);
         sums = n >= kSplitK ? c.take<float>(kSplitFloats) : nullptr;
         bytes = c.used();
     }
@@ -391,6 +433,7 @@ int run(const E* G, __bf16* out, int64_t batch, int64_t rows, int64_t cols, int6
         SymmetricOp<true> p = {};
         p.A = w.s;
         p.C = w.p;
+        p.diag = w.diag;
         p.M = (int)w.m;
         p.K = p.lda = p.mp = (int)w.mp;
         p.stride_a = p.stride_c = w.stride_s;
@@ -400,6 +443,7 @@ int run(const E* G, __bf16* out, int64_t batch, int64_t rows, int64_t cols, int6
         if ((rc = launch_symmetric(p, w.m, batch, w.sums, stream))) return rc;
         auto apply = [&](auto op) {
             op.P = w.p;
+            op.diag = w.diag;
             op.Xt = w.xt[from];
             op.X = w.x[to];
             op.XtNew = w.xt[to];

@@ -16,8 +16,10 @@
  * |G|_F is summed in 64 bits, the products' sums are in 32 bits.  X, S and
  * the polynomial aI + bS + cSS are held in binary16 between the products (X
  * times a power of two that brings a typical entry near 1), which is 8 times
- * finer than the bfloat16 that the update is usually computed in; the result
- * is therefore bfloat16, whatever G's type.  A matrix whose norm is not
+ * finer than the bfloat16 that the update is usually computed in; what
+ * rounding takes from the polynomial's diagonal, its largest part, is put
+ * back into the product's rows.  The result is therefore bfloat16, whatever
+ * G's type: its error is about 1.2 times that of its own rounding.  A matrix whose norm is not
  * finite, or that holds a NaN, gives NaN; the zero matrix gives zeros.
  *
  * Ownership, concurrency, errors and capture are those of gemm_nt_f16.h.  The

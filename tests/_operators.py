@@ -84,7 +84,8 @@ def gated_gradients(dh, x, wg, wu, act):
 def newton_schulz(g, steps=5, coefficients=(3.4445, -4.7750, 2.0315), eps=1e-7, rounded=False):
     """The iteration in 64 bits; `rounded`: with X, S and the polynomial
     rounded to binary16 where the operator's documentation holds them so (X
-    times the power of two nearest sqrt(longer side))."""
+    times the power of two nearest sqrt(longer side), rows times what rounding
+    took from the polynomial's diagonal)."""
     x = g.double().cpu()
     if x.dim() == 3:
         return torch.stack([newton_schulz(v, steps, coefficients, eps, rounded) for v in x])
@@ -97,7 +98,11 @@ def newton_schulz(g, steps=5, coefficients=(3.4445, -4.7750, 2.0315), eps=1e-7, 
     for k in range(steps):
         a, b, c = coefficients[k] if hasattr(coefficients[0], "__len__") else coefficients
         s = r(x @ x.T)
-        x = r(a * torch.eye(len(s), dtype=torch.float64) + b * s + c * (s @ s)) @ x
+        p = a * torch.eye(len(s), dtype=torch.float64) + b * s + c * (s @ s)
+        x = r(p) @ x
+        if rounded:
+            d, d16 = p.diagonal(), r(p).diagonal()
+            x = x * torch.where(d16.abs() >= 2.0 ** -14, d / d16, torch.ones_like(d))[:, None]
         if k + 1 < steps:
             x = r(x, scale)
     return x.T if tall else x
