@@ -36,6 +36,8 @@ inline bool good_pointer(const void* p, int64_t rows, int64_t cols, uintptr_t al
 }
 
 inline bool good_dim(int64_t n) { return n >= 0 && n <= kMaxDim; }
+// What one launch may hold: 2^32 - 1 threads in a dimension.
+inline bool good_grid(int64_t workgroups, int64_t threads) { return workgroups <= (((int64_t)1 << 32) - 1) / threads; }
 inline bool good_pitch(int64_t ld, int64_t cols) { return ld >= cols && ld <= kMaxPitch; }
 
 // Hands out 16-byte aligned pieces of a workspace; with no base it only adds

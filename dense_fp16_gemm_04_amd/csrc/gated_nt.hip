@@ -189,10 +189,11 @@ __device__ __forceinline__ void Slopes<E>::run(int id, E* tg, E* tu) const
         x4 vg, vu;
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-            // (a row or column that is not there has d, P and Q zero; 0 beside
-            // an infinite P of the same row is the product it is)
-            vg[e] = (E)((float)d[e] * p[j][e]);
-            vu[e] = (E)((float)d[e] * q[j][e]);
+            // (of a row or column that is not there P and Q may be anything:
+            // an infinite weight times the zeros past the end is NaN)
+            const bool there = t0 + row < T && f0 + j * 16 + 4 * (lane >> 4) + e < F;
+            vg[e] = (E)(there ? (float)d[e] * p[j][e] : 0.0f);
+            vu[e] = (E)(there ? (float)d[e] * q[j][e] : 0.0f);
         }
         *(x4*)(tg + at) = vg;  // (each element of dH is read by one lane, this one)
         *(x4*)(tu + at) = vu;
@@ -242,16 +243,6 @@ bool vec4(const void* p, int64_t ld) { return (uintptr_t)p % 8 == 0 && ld % 4 ==
 bool vec8(const void* p, int64_t ld) { return (uintptr_t)p % 16 == 0 && ld % 8 == 0; }
 // a result's rows take eight columns at a time
 bool eights(const void* p, int64_t cols, int64_t ld) { return vec8(p, ld) && cols % 8 == 0; }
-
-template <class E>
-int launch_copy(const E* src, int64_t ld, E* dst, int64_t ldd, int64_t rows, int64_t cols, hipStream_t stream)
-{
-    const int64_t work = rows * (ldd / 4);
-    if (work == 0) return hipSuccess;
-    hipLaunchKernelGGL(relayout::copy_rows<E>, dim3((unsigned)std::min<int64_t>((work + 255) / 256, 65536)), dim3(256), 0,
-                       stream, src, ld, dst, ldd, rows, (int)cols);
-    return (int)hipGetLastError();
-}
 
 // C [M, N] = A B^T, all operands with K elements to a row; with a second A
 // and C, two products with the same B at once.
@@ -336,7 +327,6 @@ int forward(const E* X, const E* Wg, const E* Wu, E* H, float* saved, int64_t T,
 {
     const ForwardSpace<E> w(workspace, X, Wg, Wu, T, D, F, ldx, ldg, ldu);
     const int64_t Dp = abi::up(D, 8);
-    int rc = hipSuccess;
     GatedOp<E, SAVE, EIGHTS> op = {};
     op.X = X;
     op.Wg = Wg;
@@ -345,20 +335,22 @@ int forward(const E* X, const E* Wg, const E* Wu, E* H, float* saved, int64_t T,
     op.ldg = (int)ldg;
     op.ldu = (int)ldu;
     op.K = (int)Dp;
-    if (w.copy_x) {
-        if ((rc = launch_copy(X, ldx, w.x, Dp, T, D, stream))) return rc;
-        op.X = w.x;
-        op.lda = (int)Dp;
-    }
-    if (w.copy_g) {
-        if ((rc = launch_copy(Wg, ldg, w.g, Dp, F, D, stream))) return rc;
-        op.Wg = w.g;
-        op.ldg = (int)Dp;
-    }
-    if (w.copy_u) {
-        if ((rc = launch_copy(Wu, ldu, w.u, Dp, F, D, stream))) return rc;
-        op.Wu = w.u;
-        op.ldu = (int)Dp;
+    relayout::Copies<E> copies = {};
+    auto copied = [&](bool copy, const E*& src, int& ld, E* dst, int64_t rows) {
+        if (!copy) return;
+        copies.job[copies.jobs++] = {src, dst, ld, rows};
+        src = dst;
+        ld = (int)Dp;
+    };
+    copied(w.copy_x, op.X, op.lda, w.x, T);
+    copied(w.copy_g, op.Wg, op.ldg, w.g, F);
+    copied(w.copy_u, op.Wu, op.ldu, w.u, F);
+    if (copies.jobs && Dp) {
+        const int64_t work = std::max(T, F) * (Dp / 4);
+        hipLaunchKernelGGL(relayout::copy_rows<E>, dim3((unsigned)std::min<int64_t>((work + 255) / 256, 16384), copies.jobs),
+                           dim3(relayout::kThreads), 0, stream, copies, (int)D, (int)Dp);
+        const int rc = (int)hipGetLastError();
+        if (rc) return rc;
     }
     op.H = H;
     op.saved = saved;
@@ -386,11 +378,10 @@ int backward(const E* dH, const E* X, const E* Wg, const E* Wu, const float* sav
     if (F > 0) p.turn[2] = {X, w.xt, ldx, w.Tp, (int)T, (int)D, (int)w.Tp, (int)vec4(X, ldx)};
     int64_t n = p.slopes.tiles();
     for (int i = 0; i < 3; ++i) {
-        if (n > abi::kMaxDim) return hipErrorInvalidValue;
         p.first[i] = (int)n;
         n += p.turn[i].tiles();
     }
-    if (n > abi::kMaxDim) return hipErrorInvalidValue;
+    if (!abi::good_grid(n, relayout::kThreads)) return hipErrorInvalidValue;  // (nothing is enqueued yet)
     if (n > 0) {
         hipLaunchKernelGGL(gated_prepare<E>, dim3((unsigned)n), dim3(relayout::kThreads), 0, stream, p);
         if ((rc = (int)hipGetLastError())) return rc;
@@ -440,6 +431,7 @@ int gated_nt(const void* X, const void* Wg, const void* Wu, void* H, void* saved
     if (type != GATED_NT_F16 && type != GATED_NT_BF16) return hipErrorInvalidValue;
     if (activation != GATED_NT_SILU && activation != GATED_NT_GELU_TANH) return hipErrorInvalidValue;
     if (T == 0 || F == 0) return hipSuccess;
+    if (!nt::fits(T, 2 * F, 1)) return hipErrorInvalidValue;
     if (!good_pointer(X, T, D, 2) || !good_pointer(Wg, F, D, 2) || !good_pointer(Wu, F, D, 2) ||
         !good_pointer(H, T, F, 2) || (uintptr_t)saved % 16 || (uintptr_t)workspace % 16)
         return hipErrorInvalidValue;
@@ -473,6 +465,7 @@ int gated_nt_backward(const void* dH, const void* X, const void* Wg, const void*
         !good_pitch(lddx, D) || !good_pitch(lddg, D) || !good_pitch(lddu, D))
         return hipErrorInvalidValue;
     if (up(T, 8) > kMaxPitch) return hipErrorInvalidValue;  // rows of the transposed operands
+    if (!nt::fits(T, D, 1) || !nt::fits(F, D, 2)) return hipErrorInvalidValue;
     if (type != GATED_NT_F16 && type != GATED_NT_BF16) return hipErrorInvalidValue;
     if (!good_pointer(dH, T, F, 2) || !good_pointer(X, T, D, 2) || !good_pointer(Wg, F, D, 2) ||
         !good_pointer(Wu, F, D, 2) || !good_pointer(saved, T, F, 16) || !good_pointer(dX, T, D, 2) ||

@@ -570,6 +570,7 @@ int launch(const Args& a)
 {
     // grid.y holds 65535 at most: more rows go in further launches
     constexpr int64_t most = (int64_t)65535 * 16 * MB;
+    if (!abi::good_grid((a.N + 16 * R - 1) / (16 * R), kThreads)) return hipErrorInvalidValue;
     for (int64_t m = 0; m < a.M; m += most) {
         const int64_t rows = std::min(most, a.M - m);
         hipLaunchKernelGGL((gemv_w4_kernel<E, MB, R, FLUSH, ZERO, EIGHTS>),
@@ -587,7 +588,7 @@ template <class E, int FN, int FLUSH, bool ZERO>
 int launch_gemm(const Args& a)
 {
     const int64_t tm = (a.M + 63) / 64, tn = (a.N + 64 * FN - 1) / (64 * FN);
-    if (tm * tn > abi::kMaxDim) return hipErrorInvalidValue;
+    if (!abi::good_grid(tm * tn, 1024)) return hipErrorInvalidValue;
     const int whole = (uintptr_t)a.Y % 8 == 0 && a.ldy % 4 == 0;
     hipLaunchKernelGGL((gemm_w4_kernel<E, FN, FLUSH, ZERO>), dim3((unsigned)(tm * tn)), dim3(1024), 0, a.stream,
                        (const E*)a.X, (const unsigned char*)a.Q, (const E*)a.scale, (const E*)a.zero, (E*)a.Y, (int)a.M,

@@ -100,6 +100,7 @@ int launch(OP op, int64_t K, float* partial, Count count, Prepare prepare, hipSt
         if (i == 0 && (!OP::kPersist || K <= 128)) continue;
         if (i == 1 && !OP::kOblong) continue;
         const int64_t n = count(kKinds[i]);
+        if (!abi::good_grid(n, i == 1 || i == 2 ? 512 : 256)) continue;
         const double us = model_us(kKinds[i], n, K, cus);
         if (best < 0 || us < best_us) {
             best = i;
@@ -116,7 +117,7 @@ int launch(OP op, int64_t K, float* partial, Count count, Prepare prepare, hipSt
             parts = p;
         }
     }
-    if (tiles > abi::kMaxDim) return hipErrorInvalidValue;
+    if (best < 0) return hipErrorInvalidValue;
     if (tiles == 0) return hipSuccess;
     op.tiles = (int)tiles;
     prepare(op, kKinds[best]);
@@ -134,6 +135,12 @@ int launch(OP op, int64_t K, float* partial, Count count, Prepare prepare, hipSt
     if (best == 3)
         hipLaunchKernelGGL((nt_tile<Shape<E, 64, 64, 2, 2, 3, 2, 4>, OP>), dim3((unsigned)tiles), dim3(256), 0, stream, op);
     return (int)hipGetLastError();
+}
+
+// The largest of the kinds that every OP has, 256 x 128, can hold the result.
+inline bool fits(int64_t rows, int64_t cols, int64_t batch)
+{
+    return abi::good_grid((rows + 255) / 256 * ((cols + 127) / 128) * batch, 512);
 }
 
 // A rows x cols grid of tiles, `batch` times; `split` columns of the product

@@ -246,7 +246,7 @@ struct SymmetricOp {
             }
             // (the waves whose rows have no entry in the tile store nothing)
             const __amdgpu_buffer_rsrc_t entries =
-                make_rsrc(diag + (int64_t)t.batch * mp + t.m0, (uint32_t)max(0, min(T::BM, M - t.m0)) * 4u);
+                make_rsrc(diag + (int64_t)t.batch * mp + t.m0, (uint32_t)min(T::BM, M - t.m0) * 4u);
             const int ln = pinned(lane);
 #pragma unroll
             for (int i = 0; i < T::FM; ++i) {
@@ -313,10 +313,9 @@ struct ApplyOp {
     {
         constexpr bool EIGHTS = (HOW & kEights) != 0;
         // Each row's factor: what rounding took from its diagonal entry.  (A
-        // subnormal one is left as it is, its quotient may be far from 1; a
-        // part of a joined tile may lie past M.)
+        // subnormal one is left as it is, its quotient may be far from 1.)
         const __amdgpu_buffer_rsrc_t entries =
-            make_rsrc(diag + (int64_t)t.batch * lda + t.m0, (uint32_t)max(0, min(T::BM, M - t.m0)) * 4u);
+            make_rsrc(diag + (int64_t)t.batch * lda + t.m0, (uint32_t)min(T::BM, M - t.m0) * 4u);
         float f[T::FM];
 #pragma unroll
         for (int i = 0; i < T::FM; ++i) {
@@ -394,6 +393,10 @@ int run(const E* G, __bf16* out, int64_t batch, int64_t rows, int64_t cols, int6
 {
     const Space w(workspace, batch, rows, cols);
     const bool tall = rows > cols;
+    const int64_t pr = abi::up(rows, 8), pc = abi::up(cols, 8);
+    const int64_t tr = (pr + 63) / 64, tc = (pc + 63) / 64;
+    // (the products have no more tiles than that)
+    if (!abi::good_grid(tr * tc * batch, 256)) return hipErrorInvalidValue;
     // an entry of an orthonormal X is about 1 / sqrt(n); X is held times
     // 2^k near sqrt(n), at most 2^12, so entries (at most about 1.2 before
     // the scale) neither leave binary16's range nor its full precision
@@ -404,9 +407,6 @@ int run(const E* G, __bf16* out, int64_t batch, int64_t rows, int64_t cols, int6
     hipLaunchKernelGGL(ns_squares<E>, dim3((unsigned)(batch * kNormBlocks)), dim3(256), 0, stream, G, ldg, stride_g,
                        (int)rows, (int)cols, (int)((cols + 3) / 4), vec, w.partial);
     if ((rc = (int)hipGetLastError())) return rc;
-    const int64_t pr = abi::up(rows, 8), pc = abi::up(cols, 8);
-    const int64_t tr = (pr + 63) / 64, tc = (pc + 63) / 64;
-    if (tr * tc * batch > abi::kMaxDim) return hipErrorInvalidValue;
     half* d1 = tall ? w.xt[0] : w.x[0];
     half* d2 = tall ? w.x[0] : w.xt[0];
     hipLaunchKernelGGL(ns_start<E>, dim3((unsigned)(tr * tc * batch)), dim3(256), 0, stream, G, ldg, stride_g, (int)rows,
@@ -498,7 +498,7 @@ int orthogonalize_ns(const void* G, void* out, int64_t batch, int64_t rows, int6
     if (!good_sizes(batch, rows, cols)) return hipErrorInvalidValue;
     if (ldg < cols || ldg > kMaxDim || ldo < cols || ldo > kMaxPitch) return hipErrorInvalidValue;
     if (type < ORTHOGONALIZE_NS_F16 || type > ORTHOGONALIZE_NS_F32) return hipErrorInvalidValue;
-    if (steps < 0 || steps > 64 || (steps > 0 && !coefficients)) return hipErrorInvalidValue;
+    if (steps < 0 || steps > 64 || (steps > 0 && !coefficients) || !(eps >= 0)) return hipErrorInvalidValue;
     if (batch == 0 || rows == 0 || cols == 0) return hipSuccess;
     const int64_t elem = type == ORTHOGONALIZE_NS_F32 ? 4 : 2;
     const int64_t span_g = (rows - 1) * ldg + cols, span_o = (rows - 1) * ldo + cols;

@@ -48,16 +48,28 @@ __device__ __forceinline__ void store_transposed(const E* tile, E* dst, int64_t 
     }
 }
 
+// Up to three operands of one width in one launch, one to each blockIdx.y:
 // dst[r][c] = src[r][c] for c < cols, 0 for cols <= c < ldd.
 template <class E>
-__global__ void __launch_bounds__(kThreads) copy_rows(const E* __restrict__ src, int64_t lds_, E* __restrict__ dst,
-                                                      int64_t ldd, int64_t rows, int cols)
+struct Copies {
+    struct Job {
+        const E* src;
+        E* dst;
+        int64_t lds_, rows;
+    } job[3];
+    int jobs;
+};
+
+template <class E>
+__global__ void __launch_bounds__(kThreads) copy_rows(const Copies<E> copies, int cols, int ldd)
 {
-    const int64_t per = ldd / 4;
-    for (int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x; i < rows * per; i += (int64_t)gridDim.x * kThreads) {
-        const int64_t r = i / per;
+    const typename Copies<E>::Job j = copies.job[blockIdx.y];
+    const uint32_t per = (uint32_t)ldd / 4;
+    const int64_t groups = j.rows * per;
+    for (int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x; i < groups; i += (int64_t)gridDim.x * kThreads) {
+        const int64_t r = groups >> 32 ? i / per : (uint32_t)i / per;
         const int c = (int)(i - r * per) * 4;
-        *(typename Elem<E>::x4*)(dst + r * ldd + c) = load4(src + r * lds_, c, cols, false);
+        *(typename Elem<E>::x4*)(j.dst + r * ldd + c) = load4(j.src + r * j.lds_, c, cols, false);
     }
 }
 

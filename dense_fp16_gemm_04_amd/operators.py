@@ -235,7 +235,11 @@ def orthogonalize_ns(g, steps: int = 5, coefficients=(3.4445, -4.7750, 2.0315), 
     steps = int(steps)
     if not 0 <= steps <= 64:
         raise ValueError("steps must be 0 .. 64, got %d" % steps)
-    triples = [tuple(float(v) for v in c) for c in coefficients] if steps and hasattr(coefficients[0], "__len__") \
+    eps = float(eps)
+    if not eps >= 0:
+        raise ValueError("eps must not be negative, got %r" % eps)
+    coefficients = list(coefficients)
+    triples = [tuple(float(v) for v in c) for c in coefficients] if coefficients and hasattr(coefficients[0], "__len__") \
         else [tuple(float(v) for v in coefficients)] * steps
     if len(triples) != steps or any(len(c) != 3 for c in triples):
         raise ValueError("coefficients must be one triple, or one for each of the %d steps" % steps)
@@ -256,7 +260,7 @@ def orthogonalize_ns(g, steps: int = 5, coefficients=(3.4445, -4.7750, 2.0315), 
         return out
     stride_g, stride_o = (t.stride(0) if t.dim() == 3 and batch > 1 else 0 for t in (g, out))
     if batch > 1 and (stride_g < 0 or stride_o < (rows - 1) * ldo + cols):
-        raise ValueError("out's matrices must not overlap, got strides %s" % (out.stride(),))
+        raise ValueError("out's matrices must lie one after another and not overlap, got strides %s" % (out.stride(),))
     lib = load("orthogonalize_ns")
     nbytes = lib.orthogonalize_ns_workspace(batch, rows, cols)
     if nbytes < 0:
@@ -264,7 +268,7 @@ def orthogonalize_ns(g, steps: int = 5, coefficients=(3.4445, -4.7750, 2.0315), 
     keep, workspace = _workspace(g, nbytes)
     flat = (ctypes.c_double * max(1, 3 * steps))(*(v for c in triples for v in c))
     _call("orthogonalize_ns", "orthogonalize_ns", device, g.data_ptr(), out.data_ptr(), batch, rows, cols, ldg, stride_g,
-          ldo, stride_o, _TYPES_AND_F32[g.dtype], steps, flat, float(eps), workspace, nbytes)
+          ldo, stride_o, _TYPES_AND_F32[g.dtype], steps, flat, eps, workspace, nbytes)
     return out
 
 

@@ -19,8 +19,9 @@
  * finer than the bfloat16 that the update is usually computed in; what
  * rounding takes from the polynomial's diagonal, its largest part, is put
  * back into the product's rows.  The result is therefore bfloat16, whatever
- * G's type: its error is about 1.2 times that of its own rounding.  A matrix whose norm is not
- * finite, or that holds a NaN, gives NaN; the zero matrix gives zeros.
+ * G's type: its error is 1.05 to 1.4 times that of its own rounding.  A matrix
+ * whose norm is not finite, or that holds a NaN, gives NaN; the zero matrix
+ * gives zeros.
  *
  * Ownership, concurrency, errors and capture are those of gemm_nt_f16.h.  The
  * workspace (orthogonalize_ns_workspace bytes, 16-byte aligned) is the
@@ -28,10 +29,11 @@
  *
  * hipErrorInvalidValue before anything is enqueued: a negative size, a size
  * above 2^21 - 9 in rows or cols, batch of 2^16 or more, a pitch below the
- * row, ldo of 2^21 or more, a matrix stride that makes out's matrices overlap, an unknown
- * type, steps below 0 or above 64, null coefficients with steps > 0, a null
- * or misaligned pointer with a non-zero extent, out or the workspace meeting
- * G or each other, a workspace that is too small.
+ * row, ldo of 2^21 or more, matrices of out that do not lie one after
+ * another, an unknown type, steps below 0 or above 64, null coefficients with
+ * steps > 0, eps below 0 or NaN, a null or misaligned pointer with a non-zero
+ * extent, out or the workspace meeting G or each other, a workspace that is
+ * too small, more tiles than a launch can hold (2^24 of 64 x 64).
  */
 #ifndef ORTHOGONALIZE_NS_H
 #define ORTHOGONALIZE_NS_H

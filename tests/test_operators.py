@@ -102,6 +102,63 @@ def test_gated_tiles_in_turn(D, t):
     plain.assert_within(fw.gated_nt(x, wg[:2040], wu[:2040]), want[:, :2040], bound[:, :2040], "whole pieces")
 
 
+# sums so long (2F for dx, T for the weights) that the few tiles are split over
+# K and joined; results with and without rows of eights
+@pytest.mark.parametrize("t", ["fp16", "bf16"])
+@pytest.mark.parametrize("shape", [(300, 296, 5001), (304, 301, 5000), (5003, 296, 136), (600, 1032, 2736)], ids=str)
+def test_gated_long_sums(shape, t):
+    T, D, F = shape
+    x, wg, wu = gated_inputs(T, D, F, plain.TYPES[t], seed=7)
+    h, saved = fw.gated_nt_train(x, wg, wu)
+    want, bound = plain.gated(x, wg, wu, "silu")
+    plain.assert_within(h, want, bound, "h")
+    dh = normal(T, F, seed=8, std=0.1, t=plain.TYPES[t])
+    got = fw.gated_nt_backward(dh, x, wg, wu, saved)
+    want, bounds = plain.gated_gradients(dh, x, wg, wu, "silu")
+    for name, g, w, b in zip(("dx", "dw_gate", "dw_up"), got, want, bounds):
+        plain.assert_within(g, w, b, name)
+    for g, again in zip(got, fw.gated_nt_backward(dh, x, wg, wu, saved)):
+        assert torch.equal(g, again)
+
+
+def test_gated_results_past_32_bits():
+    """2.45e9 elements of h: offsets of rows, saved blocks and transposes."""
+    T, D, F = 70000, 32, 35000
+    t = torch.bfloat16
+    x, wg, wu = gated_inputs(T, D, F, t, seed=9)
+    h, saved = fw.gated_nt_train(x, wg, wu)
+    rows, cols = torch.tensor([0, 61357, 69999]), torch.tensor([0, 1, 17501, 34999])
+    want, bound = plain.gated(x[rows], wg, wu, "silu")
+    plain.assert_within(h[rows], want, bound, "h")
+    dh = torch.randn(T, F, dtype=t, device=DEV, generator=torch.Generator(DEV).manual_seed(10))
+    dx, dwg, dwu = fw.gated_nt_backward(dh, x, wg, wu, saved)
+    (want, _, _), (bound, _, _) = plain.gated_gradients(dh[rows], x[rows], wg, wu, "silu")
+    plain.assert_within(dx[rows], want, bound, "dx")
+    (_, *want), (_, *bound) = plain.gated_gradients(dh[:, cols], x, wg[cols], wu[cols], "silu")
+    plain.assert_within(dwg[cols], want[0], bound[0], "dw_gate")
+    plain.assert_within(dwu[cols], want[1], bound[1], "dw_up")
+
+
+@pytest.mark.parametrize("t", ["fp16", "bf16"])
+def test_gated_infinite_weights_do_not_meet_the_padding(t):
+    """One infinite weight: act(g) = +inf in its column, and so is the gradient
+    of w_up's row; NaN would be zeros past the last token times that weight."""
+    T, D, F = 5, 16, 20
+    t = plain.TYPES[t]
+    x, wg, wu = gated_inputs(T, D, F, t, seed=33)
+    x = x.abs() + 0.25
+    dh = normal(T, F, seed=36, t=t).abs() + 0.25
+    _, saved = fw.gated_nt_train(x, wg, wu)
+    clean = fw.gated_nt_backward(dh, x, wg, wu, saved)
+    bad = wg.clone()
+    bad[3, 0] = float("inf")
+    _, saved = fw.gated_nt_train(x, bad, wu)
+    _, dwg, dwu = fw.gated_nt_backward(dh, x, bad, wu, saved)
+    assert (dwu[3] == float("inf")).all()
+    keep = [r for r in range(F) if r != 3]
+    assert torch.equal(dwu[keep], clean[2][keep]) and torch.equal(dwg[keep], clean[1][keep])
+
+
 @pytest.mark.parametrize("act", ["silu", "gelu_tanh"])
 def test_gated_gradients_match_differences(act):
     T, D, F = 37, 72, 50
@@ -261,6 +318,32 @@ def test_ns_large_tiles(shape):
     ns_close(out[-1], g[-1], steps=2)
 
 
+@pytest.mark.parametrize("shape", [(300, 9000), (9001, 203), (2, 520, 6000), (1100, 2900)], ids=str)
+def test_ns_long_sums(shape):
+    """Few tiles of long sums, split over K and joined."""
+    g = normal(*shape, seed=12, t=torch.bfloat16)
+    out = fw.orthogonalize_ns(g, steps=3)
+    ns_close(out, g, steps=3)
+    assert torch.equal(out, fw.orthogonalize_ns(g, steps=3))
+
+
+def test_ns_batch_past_32_bits():
+    """2.6e9 elements in all."""
+    g = torch.randn(20000, 256, 512, dtype=torch.bfloat16, device=DEV, generator=torch.Generator(DEV).manual_seed(13))
+    out = fw.orthogonalize_ns(g, steps=2)
+    for i in (0, 16383, 19999):
+        ns_close(out[i], g[i], steps=2)
+
+
+def test_ns_small_diagonals_of_the_polynomial():
+    """Diagonal entries of P of every size: 0, below binary16's range, ordinary."""
+    g = torch.eye(24, 40, device=DEV) * torch.linspace(0.05, 1.0, 24, device=DEV)[:, None]
+    s = g.double().cpu()
+    s = (s / s.norm()).square().sum(1)  # S is diagonal, and so is P: a + b s + c s s
+    for a in (0.0, -float(s[10]), 1e-7, 3.0):
+        ns_close(fw.orthogonalize_ns(g, steps=1, coefficients=(a, 1.0, 0.0)), g, steps=1, coefficients=(a, 1.0, 0.0))
+
+
 def test_ns_steps_and_coefficients():
     g = normal(40, 70, seed=5)
     for steps in (0, 1, 2, 7):
@@ -351,6 +434,52 @@ def test_w4(shape, zeros, t):
     got = fw.gemv_w4(x, q, s, z)
     want, bound = plain.product_w4(x, q, s, z)
     plain.assert_within(got, want, bound)
+
+
+# results of 512 tiles of 32 x 32 and more, for which 64 rows of x are taken at
+# a time (by 64 of w, or 128 where binary16 has no zero points); K below, at
+# and past whole blocks of 256
+W4_MANY = [(33, 8200, 288, 32), (64, 8192, 512, 64), (70, 5600, 32, 32), (129, 4100, 480, 480), (200, 2400, 1280, 128),
+           (513, 3650, 96, 32), (520, 3700, 704, 64), (1030, 2049, 256, 256)]
+
+
+@pytest.mark.parametrize("t", ["fp16", "bf16"])
+@pytest.mark.parametrize("zeros", [None, "any"])
+@pytest.mark.parametrize("shape", W4_MANY, ids=str)
+def test_w4_many_rows(shape, zeros, t):
+    M, N, K, group = shape
+    x, q, s, z = w4_inputs(M, N, K, group, zeros, plain.TYPES[t], seed=sum(shape))
+    got = fw.gemv_w4(x, q, s, z)
+    want, bound = plain.product_w4(x, q, s, z)
+    plain.assert_within(got, want, bound)
+    assert torch.equal(got, fw.gemv_w4(x, q, s, z))
+
+
+@pytest.mark.parametrize("offset", [0, 1])
+@pytest.mark.parametrize("zeros", [None, "whole"])
+def test_w4_many_rows_in_views(zeros, offset):
+    """Rows and results inside larger buffers; a NaN and an infinity stay in their rows."""
+    x, q, s, z = w4_inputs(150, 4101, 320, 64, zeros, torch.float16, seed=6)
+    x[5, 7] = float("nan")
+    x[149, 319] = float("inf")
+    ref = fw.gemv_w4(x, q, s, z)
+    assert torch.isnan(ref[5]).all() and not torch.isfinite(ref[149]).any()
+    keep = [r for r in range(150) if r not in (5, 149)]
+    want, bound = plain.product_w4(x[keep], q, s, z)
+    plain.assert_within(ref[keep], want, bound)
+    vy, big = framed(torch.zeros_like(ref), offset=offset)
+    fw.gemv_w4(framed(x)[0], q, s, z, out=vy)
+    assert torch.equal(vy[keep], ref[keep]) and frame_intact(vy, big)
+    # (x off 16 bytes: another kernel, the same bounds)
+    plain.assert_within(fw.gemv_w4(framed(x, offset=1)[0], q, s, z)[keep], want, bound)
+
+
+def test_w4_results_past_32_bits():
+    M, N, K = 70000, 35000, 32
+    x, q, s, z = w4_inputs(M, N, K, 32, "whole", torch.float16, seed=7)
+    rows = torch.tensor([0, 61357, 69999])
+    want, bound = plain.product_w4(x[rows], q, s, z)
+    plain.assert_within(fw.gemv_w4(x, q, s, z)[rows], want, bound)
 
 
 @pytest.mark.parametrize("t", ["fp16", "bf16"])

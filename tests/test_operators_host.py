@@ -130,6 +130,29 @@ def test_gated_backward_refuses(kw):
     assert operators.load("gated_nt").gated_nt_backward(*backward_args(**kw)) == INVALID
 
 
+def test_results_of_too_many_tiles_are_refused():
+    """More than 2^32 threads: refused before anything is enqueued."""
+    lib = operators.load("gated_nt")
+    far = 1 << 50
+    big = dict(T=1 << 28, D=8, F=1 << 19, ldx=8, ldg=8, ldu=8, ldh=1 << 19, X=A, Wg=far, Wu=2 * far, H=3 * far)
+    assert lib.gated_nt(*gated_args(**big)) == INVALID
+    lib = operators.load("gemv_w4")
+    w4 = dict(X=A, Q=far, scale=2 * far, Y=3 * far)
+    assert lib.gemv_w4(*w4_args(N=(1 << 30), ldy=1 << 30, **w4)) == INVALID
+    assert lib.gemv_w4(*w4_args(M=1 << 20, N=1 << 20, ldy=1 << 20, **w4)) == INVALID
+    lib = operators.load("orthogonalize_ns")
+    n, batch = 1 << 20, (1 << 16) - 1
+    assert lib.orthogonalize_ns(*ns_args(G=far, out=3 * far, rows=1, cols=n, ldg=n, ldo=n, stride_g=n, stride_o=n,
+                                         batch=batch, ws=5 * far, ws_bytes=1 << 49)) == INVALID
+
+
+def test_a_backward_pass_over_too_many_rows_is_refused():
+    far = 1 << 45
+    where = {k: (i + 1) * far for i, k in enumerate(("dH", "X", "Wg", "Wu", "saved", "dX", "dWg", "dWu", "ws"))}
+    call = operators.load("gated_nt").gated_nt_backward
+    assert call(*backward_args(T=(1 << 21) - 7, ws_bytes=1 << 40, **where)) == INVALID
+
+
 # ----------------------------------------------------- orthogonalize_ns --
 
 def ns_args(**kw):
@@ -149,6 +172,19 @@ def ns_args(**kw):
 ])
 def test_ns_refuses(kw):
     assert operators.load("orthogonalize_ns").orthogonalize_ns(*ns_args(**kw)) == INVALID
+
+
+@pytest.mark.parametrize("eps", [-1.0, -1e-300, float("nan"), float("-inf")])
+def test_ns_refuses_eps(eps):
+    assert operators.load("orthogonalize_ns").orthogonalize_ns(*ns_args(eps=eps)) == INVALID
+    with pytest.raises(ValueError, match="eps"):
+        fw.orthogonalize_ns(torch.zeros(4, 4), eps=eps)
+
+
+@pytest.mark.parametrize("coefficients", [(), [()], [(1.0, 2.0)], (1.0,), [(1.0, 2.0, 3.0)] * 6])
+def test_ns_refuses_coefficients(coefficients):
+    with pytest.raises(ValueError, match="coefficients"):
+        fw.orthogonalize_ns(torch.zeros(4, 4), coefficients=coefficients)
 
 
 def test_ns_empty_and_workspace():
