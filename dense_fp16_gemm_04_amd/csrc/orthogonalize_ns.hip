@@ -15,12 +15,15 @@
 // entry exact and the others, small ones, off by as much.  (Relative error of
 // the bfloat16 result, 54 x 1286: 2.60e-3 without, 1.94e-3 with, 1.90e-3 with
 // an exact P; 40 x 4000: 3.13e-3, 2.27e-3, 2.28e-3.)
+//
+// Matrices of at most 64 rows take one launch a step: ns_narrow.h.
 #include "orthogonalize_ns.h"
 
 #include <algorithm>
 #include <cmath>
 
 #include "abi.h"
+#include "ns_narrow.h"
 #include "nt_launch.h"
 #include "relayout.h"
 
@@ -376,6 +379,21 @@ struct Space {
     }
 };
 
+struct NarrowSpace {
+    double* partial;
+    half* xt;
+    float* shares[2];
+    int64_t bytes;
+    NarrowSpace(void* base, int64_t batch, const narrow::Plan& p)
+    {
+        abi::Carve c(base);
+        partial = c.take<double>(batch * kNormBlocks);
+        xt = c.take<half>(batch * p.chunks * narrow::kShare);
+        for (float*& s : shares) s = c.take<float>(batch * p.shares * narrow::kShare);
+        bytes = c.used();
+    }
+};
+
 int64_t triangle(int64_t t) { return t * (t + 1) / 2; }
 
 template <class OP>
@@ -387,26 +405,82 @@ int launch_symmetric(const OP& op, int64_t m, int64_t batch, float* partial, hip
         [=](OP& o, const Kind& k) { o.per = (int)per(k); }, stream);
 }
 
+// X is held times 2^k near sqrt(n), at most 2^12: an entry of an orthonormal X
+// is about 1 / sqrt(n), so entries (at most about 1.2 before the scale)
+// neither leave binary16's range nor its full precision.
+int scale_bits(int64_t n) { return std::min(12, (int)std::lround(0.5 * std::log2((double)n))); }
+
+template <class E>
+int squares(const E* G, int64_t batch, int64_t rows, int64_t cols, int64_t ldg, int64_t stride_g, int vec, double* partial,
+            hipStream_t stream)
+{
+    hipLaunchKernelGGL(ns_squares<E>, dim3((unsigned)(batch * kNormBlocks)), dim3(256), 0, stream, G, ldg, stride_g,
+                       (int)rows, (int)cols, (int)((cols + 3) / 4), vec, partial);
+    return (int)hipGetLastError();
+}
+
+template <class E>
+int run_narrow(const narrow::Plan& plan, const E* G, __bf16* out, int64_t batch, int64_t rows, int64_t cols, int64_t ldg,
+               int64_t stride_g, int64_t ldo, int64_t stride_o, int32_t steps, const double* coefficients, double eps,
+               void* workspace, hipStream_t stream)
+{
+    const NarrowSpace w(workspace, batch, plan);
+    const unsigned grid = (unsigned)(batch * plan.shares);  // (below 2^16 * 2^8)
+    const int vec = (uintptr_t)G % (4 * sizeof(E)) == 0 && ldg % 4 == 0 && stride_g % 4 == 0;
+    int rc = squares(G, batch, rows, cols, ldg, stride_g, vec, w.partial, stream);
+    if (rc) return rc;
+    narrow::Args a = {};
+    a.xt = w.xt;
+    a.out = out;
+    a.m = (int)std::min(rows, cols);
+    a.n = (int)std::max(rows, cols);
+    a.shares = (int)plan.shares;
+    a.chunks = (int)plan.chunks;
+    a.cw = (int)plan.cw;
+    a.tall = rows > cols;
+    a.vec = (uintptr_t)out % 8 == 0 && ldo % 4 == 0 && stride_o % 4 == 0;
+    a.ldo = ldo;
+    a.stride_o = stride_o;
+    const double scale = std::ldexp(1.0, scale_bits(a.n));
+    a.alpha = (float)(1.0 / (scale * scale));
+    a.last = (float)(1.0 / scale);
+    a.to = w.shares[0];
+    hipLaunchKernelGGL((narrow::ns_narrow_begin<E>), dim3(grid), dim3(narrow::kThreads), 0, stream, a, G, ldg,
+                       stride_g, w.partial, eps, scale);
+    if ((rc = (int)hipGetLastError())) return rc;
+    for (int i = 0; i < steps; ++i) {
+        a.from = w.shares[i & 1];
+        a.to = w.shares[~i & 1];
+        a.a = (float)coefficients[3 * i];
+        a.b = (float)coefficients[3 * i + 1];
+        a.c = (float)coefficients[3 * i + 2];
+        if (i + 1 < steps)
+            hipLaunchKernelGGL((narrow::ns_narrow_step<false>), dim3(grid), dim3(narrow::kThreads), 0, stream, a);
+        else
+            hipLaunchKernelGGL((narrow::ns_narrow_step<true>), dim3(grid), dim3(narrow::kThreads), 0, stream, a);
+        if ((rc = (int)hipGetLastError())) return rc;
+    }
+    return hipSuccess;
+}
+
 template <class E>
 int run(const E* G, __bf16* out, int64_t batch, int64_t rows, int64_t cols, int64_t ldg, int64_t stride_g, int64_t ldo,
         int64_t stride_o, int32_t steps, const double* coefficients, double eps, void* workspace, hipStream_t stream)
 {
+    const narrow::Plan plan(std::min(rows, cols), std::max(rows, cols));
+    if (plan.used && steps > 0)
+        return run_narrow(plan, G, out, batch, rows, cols, ldg, stride_g, ldo, stride_o, steps, coefficients, eps,
+                                 workspace, stream);
     const Space w(workspace, batch, rows, cols);
     const bool tall = rows > cols;
     const int64_t pr = abi::up(rows, 8), pc = abi::up(cols, 8);
     const int64_t tr = (pr + 63) / 64, tc = (pc + 63) / 64;
     // (the products have no more tiles than that)
     if (!abi::good_grid(tr * tc * batch, 256)) return hipErrorInvalidValue;
-    // an entry of an orthonormal X is about 1 / sqrt(n); X is held times
-    // 2^k near sqrt(n), at most 2^12, so entries (at most about 1.2 before
-    // the scale) neither leave binary16's range nor its full precision
-    const int k = std::min(12, (int)std::lround(0.5 * std::log2((double)w.n)));
-    const double scale = std::ldexp(1.0, k);
+    const double scale = std::ldexp(1.0, scale_bits(w.n));
     int rc;
     const int vec = (uintptr_t)G % (4 * sizeof(E)) == 0 && ldg % 4 == 0 && stride_g % 4 == 0;
-    hipLaunchKernelGGL(ns_squares<E>, dim3((unsigned)(batch * kNormBlocks)), dim3(256), 0, stream, G, ldg, stride_g,
-                       (int)rows, (int)cols, (int)((cols + 3) / 4), vec, w.partial);
-    if ((rc = (int)hipGetLastError())) return rc;
+    if ((rc = squares(G, batch, rows, cols, ldg, stride_g, vec, w.partial, stream))) return rc;
     half* d1 = tall ? w.xt[0] : w.x[0];
     half* d2 = tall ? w.x[0] : w.xt[0];
     hipLaunchKernelGGL(ns_start<E>, dim3((unsigned)(tr * tc * batch)), dim3(256), 0, stream, G, ldg, stride_g, (int)rows,
@@ -487,7 +561,8 @@ int64_t orthogonalize_ns_workspace(int64_t batch, int64_t rows, int64_t cols)
 {
     if (!good_sizes(batch, rows, cols)) return -1;
     if (batch == 0 || rows == 0 || cols == 0) return 0;
-    return Space(nullptr, batch, rows, cols).bytes;
+    const narrow::Plan plan(std::min(rows, cols), std::max(rows, cols));
+    return std::max(Space(nullptr, batch, rows, cols).bytes, plan.used ? NarrowSpace(nullptr, batch, plan).bytes : 0);
 }
 
 int orthogonalize_ns(const void* G, void* out, int64_t batch, int64_t rows, int64_t cols, int64_t ldg, int64_t stride_g,

@@ -327,12 +327,40 @@ def test_ns_long_sums(shape):
     assert torch.equal(out, fw.orthogonalize_ns(g, steps=3))
 
 
-def test_ns_batch_past_32_bits():
+@pytest.mark.parametrize("shape", [(20000, 256, 512), (5000, 64, 8192)], ids=str)
+def test_ns_batch_past_32_bits(shape):
     """2.6e9 elements in all."""
-    g = torch.randn(20000, 256, 512, dtype=torch.bfloat16, device=DEV, generator=torch.Generator(DEV).manual_seed(13))
+    g = torch.randn(*shape, dtype=torch.bfloat16, device=DEV, generator=torch.Generator(DEV).manual_seed(13))
     out = fw.orthogonalize_ns(g, steps=2)
-    for i in (0, 16383, 19999):
+    for i in (0, shape[0] * 5 // 6, shape[0] - 1):
         ns_close(out[i], g[i], steps=2)
+
+
+@pytest.mark.parametrize("t", ["fp16", "bf16", "fp32"])
+@pytest.mark.parametrize("shape", [(64, 4096), (50, 8192), (8192, 33), (64, 8193), (8200, 64), (1, 5000), (7, 129),
+                                   (193, 64), (63, 1025), (2, 64, 64), (3, 1279, 17)], ids=str)
+def test_ns_few_rows(shape, t):
+    """Sixty-four rows or fewer: one to all chunks of columns, one to many workgroups."""
+    g = normal(*shape, seed=14, std=0.02, t=plain.TYPES[t])
+    out = fw.orthogonalize_ns(g)
+    ns_close(out, g)
+    assert torch.equal(out, fw.orthogonalize_ns(g))
+    ns_close(fw.orthogonalize_ns(g, steps=1), g, steps=1)
+    ns_close(fw.orthogonalize_ns(g, steps=0), g, steps=0)
+
+
+@pytest.mark.parametrize("shape", [(40, 333), (333, 40), (64, 128)], ids=str)
+@pytest.mark.parametrize("offset", [0, 1, 4])
+def test_ns_few_rows_in_views(shape, offset):
+    g = normal(*shape, seed=15, t=torch.float16)
+    ref = fw.orthogonalize_ns(g)
+    vo, big = framed(torch.zeros(shape, dtype=torch.bfloat16, device=DEV), offset=offset)
+    assert fw.orthogonalize_ns(framed(g, offset=offset)[0], out=vo) is vo
+    assert torch.equal(vo, ref) and frame_intact(vo, big)
+    wide = torch.stack((g, -g, 2 * g, g))
+    wide[1, 3, 3] = float("nan")
+    out = fw.orthogonalize_ns(wide)
+    assert torch.equal(out[0], ref) and torch.equal(out[3], ref) and torch.isnan(out[1]).all()
 
 
 def test_ns_small_diagonals_of_the_polynomial():
