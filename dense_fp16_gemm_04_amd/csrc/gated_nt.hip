@@ -132,6 +132,114 @@ struct GatedOp {
     }
 };
 
+// The forward pass of up to 16 MB rows of X, where reading the weights is all the
+// work: a workgroup of eight waves takes G rows of each weight, and the waves
+// take K's steps of 64 in turn.  Each has an LDS ring of its own, filled by
+// direct loads (whole 128-byte lines to eight adjacent lanes) and waited for
+// without barriers; the eight partial sums meet in LDS.  Bound by the weights'
+// bytes: one row by 8192 x 4096 twice 27.7 us, 4.85 TB/s.
+constexpr int kFewWaves = 8;
+
+template <class E, int MB, int G, bool SAVE>
+__global__ void __launch_bounds__(kFewWaves * kWave, 2) gated_few(const GatedOp<E, SAVE, true> op)
+{
+    using x8 = typename Elem<E>::x8;
+    constexpr int NB = 2 * G / 16;                               // blocks of 16 weight rows
+    constexpr int X_LOADS = 2 * MB, LOADS = X_LOADS + 2 * G / 8;  // eight rows each
+    constexpr int STAGE = LOADS * 1024, S = LOADS == 4 ? 4 : 3, PITCH = 20;
+    static_assert(MB * NB * 16 * PITCH * 4 <= S * STAGE, "the partial sums fit");
+    __shared__ __attribute__((aligned(1024))) unsigned char smem[kFewWaves * S * STAGE];
+    const int lane = threadIdx.x & (kWave - 1);
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+    unsigned char* const mine = smem + wave * (S * STAGE);
+    const int r = lane & 15, h = lane >> 4;
+    const int n0 = blockIdx.x * G, K = op.K;
+    const uint32_t rows = (uint32_t)min(G, op.F - n0);
+    const uint32_t pitch_g = (uint32_t)op.ldg * 2u, pitch_u = (uint32_t)op.ldu * 2u, pitch_x = (uint32_t)op.lda * 2u;
+    const __amdgpu_buffer_rsrc_t bg = make_rsrc(op.Wg + (int64_t)n0 * op.ldg, rows * pitch_g);
+    const __amdgpu_buffer_rsrc_t bu = make_rsrc(op.Wu + (int64_t)n0 * op.ldu, rows * pitch_u);
+    const __amdgpu_buffer_rsrc_t bx = make_rsrc(op.X, (uint32_t)op.M * pitch_x);
+    const int lr = lane >> 3, lp = lane & 7;
+    const int c01[2] = {swizzle(lr, lp), swizzle(8 + lr, lp)};
+    // rows of the stage: x's, then G of Wg, then G of Wu
+    auto issue = [&](int slot, int ks) __attribute__((always_inline)) {
+#pragma unroll
+        for (int l = 0; l < LOADS; ++l) {
+            const int c = c01[l & 1], w = l - X_LOADS;
+            const bool up = w >= G / 8;
+            const uint32_t row = (uint32_t)((l < X_LOADS ? l : up ? w - G / 8 : w) * 8 + lr);
+            const uint32_t at = row * (l < X_LOADS ? pitch_x : up ? pitch_u : pitch_g) + (uint32_t)(ks * 128 + c * 16);
+            const uint32_t off = c * 8 < K - ks * 64 ? at : kOob;
+            lds_void* to = (lds_void*)(mine + slot * STAGE + l * 1024);
+            if (l < X_LOADS)
+                __builtin_amdgcn_raw_ptr_buffer_load_lds(bx, to, 16, off, 0, 0, 0);
+            else if (!up)
+                __builtin_amdgcn_raw_ptr_buffer_load_lds(bg, to, 16, off, 0, 0, 0);
+            else
+                __builtin_amdgcn_raw_ptr_buffer_load_lds(bu, to, 16, off, 0, 0, 0);
+        }
+    };
+    f32x4 acc[MB][NB];
+#pragma unroll
+    for (int i = 0; i < MB; ++i)
+#pragma unroll
+        for (int j = 0; j < NB; ++j) acc[i][j] = f32x4{0, 0, 0, 0};
+    const int nk = (K + 63) / 64;
+#pragma unroll
+    for (int s = 0; s < S - 1; ++s) issue(s, wave + s * kFewWaves);
+    int cur = 0, fill = S - 1;
+    for (int ks = wave; ks < nk; ks += kFewWaves) {
+        // the step's loads have landed, and the last step's reads are back:
+        // its slot may be filled (past the end: with zeros, never read)
+        asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"i"((S - 2) * LOADS) : "memory");
+        issue(fill, ks + (S - 1) * kFewWaves);
+        const unsigned char* base = mine + cur * STAGE + r * 128;
+#pragma unroll
+        for (int kk = 0; kk < 2; ++kk) {
+            const int pos = swizzle(r, 4 * kk + h) * 16;
+            x8 fx[MB];
+#pragma unroll
+            for (int i = 0; i < MB; ++i) fx[i] = *(const x8*)(base + i * 2048 + pos);
+#pragma unroll
+            for (int j = 0; j < NB; ++j) {
+                const x8 fw = *(const x8*)(base + (MB + j) * 2048 + pos);
+#pragma unroll
+                for (int i = 0; i < MB; ++i) acc[i][j] = Elem<E>::mfma(fw, fx[i], acc[i][j]);
+            }
+        }
+        cur = cur + 1 == S ? 0 : cur + 1;
+        fill = fill + 1 == S ? 0 : fill + 1;
+    }
+    lds_barrier<0>();  // no load may still be writing LDS when it is used again
+    // the lane has row 16 i + r of x, weight rows 4 h .. + 3 of block j
+    float* part = (float*)smem;
+    constexpr int WAVE = NB * 16 * MB * PITCH;
+#pragma unroll
+    for (int i = 0; i < MB; ++i)
+#pragma unroll
+        for (int j = 0; j < NB; ++j)
+            *(f32x4*)(part + wave * WAVE + ((j * MB + i) * 16 + r) * PITCH + 4 * h) = acc[i][j];
+    __syncthreads();
+    const int t = threadIdx.x / G, c = threadIdx.x % G, f = n0 + c;
+    if (t >= op.M || f >= op.F) return;  // (which t below 16 MB is)
+    float g = 0.0f, u = 0.0f;
+#pragma unroll
+    for (int w = 0; w < kFewWaves; ++w) {
+        const float* at = part + w * WAVE + t * PITCH + c;
+        g += at[0];
+        u += at[NB == 2 ? 16 * MB * PITCH : G];
+    }
+    float s;
+    const float q = act_value(op.act, g, s);
+    op.H[(int64_t)t * op.ldh + f] = (E)(q * u);
+    if constexpr (SAVE) {
+        float* at = op.saved + ((int64_t)(t / 16) * blocks_of(op.F) + f / 16) * kBlockFloats +
+                    (t % 16 + 16 * (f % 16 / 4)) * 4 + f % 4;
+        at[0] = u * act_slope(op.act, g, s);
+        at[kBlockFloats / 2] = q;
+    }
+}
+
 // dG = dH * P, dU = dH * Q for a 64 x 64 tile: row-major into rows of dGU
 // (dG at column 0, dU at column Fp), transposed into dGT and dUT (pitch Tp).
 // Rows and columns past the end, up to multiples of eight, become zeros.
@@ -358,6 +466,20 @@ int forward(const E* X, const E* Wg, const E* Wu, E* H, float* saved, int64_t T,
     op.F = (int)F;
     op.ldh = (int)ldh;
     op.act = activation_of(activation);
+    // Few rows and too few columns of H for a tile on every CU.  (One row by
+    // 8192 x 1024 twice 11 us, as tiles 33; 8192 x 2560 18 and 34; 8192 x 4096
+    // 28 and 37; 8192 x 5120 38 and 38, 2048 x 5120 12.8 and 11.8.  32 rows:
+    // 8192 x 1024 16 and 34, 8192 x 4096 36 and 39, 4096 x 8000 37 and 26.)
+    if (T <= 32 && F <= 16 * num_cus()) {
+        auto few = __builtin_bit_cast(GatedOp<E, SAVE, true>, op);
+        auto with = [&](auto kernel, int columns) {
+            hipLaunchKernelGGL(kernel, dim3((unsigned)((F + columns - 1) / columns)), dim3(kFewWaves * kWave), 0, stream, few);
+            return (int)hipGetLastError();
+        };
+        if (T > 16) return with(gated_few<E, 2, 8, SAVE>, 8);
+        // (8192 x 1792: 12 us by 8 columns, 15 by 16; 8192 x 2304: 21 and 18)
+        return F <= 8 * num_cus() ? with(gated_few<E, 1, 8, SAVE>, 8) : with(gated_few<E, 1, 16, SAVE>, 16);
+    }
     return launch_grid<E>(op, T, F, 2, 1, Dp, nullptr, stream);
 }
 

@@ -74,6 +74,30 @@ def test_gated_forward_and_gradients(shape, act, t):
         plain.assert_within(g, w, b, name)
 
 
+# up to 32 rows: K's steps of 64 dealt to eight waves, 8 or 16 columns of h
+# to a workgroup
+@pytest.mark.parametrize("t", ["fp16", "bf16"])
+@pytest.mark.parametrize("shape", [(1, 4096, 24), (2, 2056, 4100), (5, 1000, 333), (8, 72, 8200), (9, 520, 40),
+                                   (16, 8192, 130), (16, 1536, 4097), (13, 33, 5000), (4, 600, 1), (17, 4096, 100), (24, 200, 4100),
+                                   (32, 1032, 331), (31, 8192, 9)], ids=str)
+def test_gated_few_rows(shape, t):
+    T, D, F = shape
+    x, wg, wu = gated_inputs(T, D, F, plain.TYPES[t], seed=sum(shape))
+    h, saved = fw.gated_nt_train(x, wg, wu, activation="gelu_tanh")
+    want, bound = plain.gated(x, wg, wu, "gelu_tanh")
+    plain.assert_within(h, want, bound, "h")
+    assert torch.equal(h, fw.gated_nt(x, wg, wu, activation="gelu_tanh"))
+    dh = normal(T, F, seed=37, t=plain.TYPES[t])
+    got = fw.gated_nt_backward(dh, x, wg, wu, saved)
+    want, bounds = plain.gated_gradients(dh, x, wg, wu, "gelu_tanh")
+    for name, g, w, b in zip(("dx", "dw_gate", "dw_up"), got, want, bounds):
+        plain.assert_within(g, w, b, name)
+    for offset in (0, 1, 4):
+        vh, big = framed(torch.zeros(T, F, dtype=plain.TYPES[t], device=DEV), offset=offset)
+        fw.gated_nt(framed(x, offset=offset)[0], framed(wg, offset=offset)[0], wu, activation="gelu_tanh", out=vh)
+        assert torch.equal(vh, h) and frame_intact(vh, big)
+
+
 @pytest.mark.parametrize("shape", [(2048, 256, 4096), (4096, 520, 1000), (513, 1024, 2056)], ids=str)
 def test_gated_many_tiles(shape):
     T, D, F = shape
