@@ -50,7 +50,7 @@ __global__ void __launch_bounds__(256) ns_squares(const E* __restrict__ G, int64
     const int lanes = min(per, 256), step = 256 / lanes, pieces = (per + 255) / 256;
     const int lane = threadIdx.x % lanes, first = threadIdx.x / lanes;
     const int64_t units = first < step ? (int64_t)rows * pieces : 0;
-    typedef E x4 __attribute__((ext_vector_type(4)));
+    using x4 = relayout::Four<E>;
     const int64_t stride_u = (int64_t)kNormBlocks * step;
     for (int64_t u0 = (int64_t)k * step + first; u0 < units; u0 += 4 * stride_u) {
         x4 v[4];
@@ -59,16 +59,8 @@ __global__ void __launch_bounds__(256) ns_squares(const E* __restrict__ G, int64
             const int64_t u = u0 + i * stride_u;
             const int64_t r = pieces == 1 ? u : u / pieces;
             const int c = ((int)(u - r * pieces) * 256 + lane) * 4;
-            const E* at = g + r * ldg + c;
             v[i] = x4{};
-            if (u >= units) continue;
-            if (vec && c + 3 < cols) {
-                v[i] = *(const x4*)at;
-            } else {
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    if (c + e < cols) v[i][e] = at[e];
-            }
+            if (u < units) v[i] = relayout::load4(g + r * ldg, c, cols, vec);
         }
 #pragma unroll
         for (int i = 0; i < 4; ++i)
@@ -114,17 +106,9 @@ ns_start(const E* __restrict__ G, int64_t ldg, int64_t stride_g, int rows, int c
         const int r = it * 16 + y, c = c0 + x * 4;
         half4 v = {};
         if (r0 + r < rows) {
-            const E* at = g + (r0 + r) * ldg + c;
-            if (vec && c + 3 < cols) {
-                typedef E x4 __attribute__((ext_vector_type(4)));
-                const x4 w = *(const x4*)at;
+            const Four<E> w = load4(g + (r0 + r) * ldg, c, cols, vec);
 #pragma unroll
-                for (int e = 0; e < 4; ++e) v[e] = (half)((float)w[e] * f);
-            } else {
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    if (c + e < cols) v[e] = (half)((float)at[e] * f);
-            }
+            for (int e = 0; e < 4; ++e) v[e] = (half)((float)w[e] * f);
             if (c < p1) *(half4*)(d1 + (int64_t)(r0 + r) * p1 + c) = v;
         }
         *(half4*)(tile + r * kPitch + x * 4) = v;

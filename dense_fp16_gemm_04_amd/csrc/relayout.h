@@ -14,17 +14,23 @@ constexpr int kTile = 64;       // a workgroup moves a 64 x 64 tile
 constexpr int kThreads = 256;   // as 16 columns of four elements by 16 rows, four times
 constexpr int kPitch = 68;      // LDS row pitch in elements: 8-byte aligned, 34 banks apart
 
-// Four elements of a row, columns c .. c + 3 of `cols`, zero past the end.
 template <class E>
-__device__ __forceinline__ typename Elem<E>::x4 load4(const E* row, int c, int cols, bool vec)
+using Four = E __attribute__((ext_vector_type(4)));
+
+// Four elements of a row, columns c .. c + 3 of `cols` (at least one), zero
+// past the end.  One by one they are loaded whether there or not, the last
+// element instead: with branches around them the compiler waits for each.
+template <class E>
+__device__ __forceinline__ Four<E> load4(const E* row, int c, int cols, bool vec)
 {
-    typename Elem<E>::x4 v = {};
+    Four<E> v;
     if (vec && c + 3 < cols) {
-        v = *(const typename Elem<E>::x4*)(row + c);
+        v = *(const Four<E>*)(row + c);
     } else {
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-            if (c + e < cols) v[e] = row[c + e];
+        for (int e = 0; e < 4; ++e) v[e] = row[min(c + e, cols - 1)];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[e] = c + e < cols ? v[e] : (E)0.0f;
     }
     return v;
 }
