@@ -17,6 +17,10 @@
 // an exact P; 40 x 4000: 3.13e-3, 2.27e-3, 2.28e-3.)
 //
 // Matrices of at most 64 rows take one launch a step: ns_narrow.h.
+//
+// 4096 x 4096, five steps: 1287 us, 1068 TFLOP/s of what symmetry leaves: a step
+// is S 76 + 8 us, P 77 + 10 (tiles, and joining the last wave's split sums), X'
+// 117.  256 x 256: 72 us, seventeen launches of 3.5 to 5.
 #include "orthogonalize_ns.h"
 
 #include <algorithm>
