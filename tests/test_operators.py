@@ -664,6 +664,62 @@ def test_captured_graphs_replay():
                 assert torch.equal(a, b)
 
 
+def small_calls(x, wg, wu, g, tall, q, s, xs):
+    """The kernels of few rows: decoding, small updates, and a prompt in 4 bits."""
+    return [fw.gated_nt(x, wg, wu), fw.gated_nt(x[:3], wg, wu), fw.orthogonalize_ns(g), fw.orthogonalize_ns(tall),
+            fw.gemv_w4(xs, q, s), fw.gemv_w4(xs[:9], q, s)]
+
+
+def small_inputs(seed, T=20):
+    x, wg, wu = gated_inputs(T, 1160, 515, torch.bfloat16, seed=seed)
+    _, q, s, _ = w4_inputs(1, 8200, 288, 32, None, torch.float16, seed=seed)
+    return [x, wg, wu, normal(3, 40, 777, seed=seed + 6), normal(900, 64, seed=seed + 7, t=torch.float16), q, s,
+            normal(70, 288, seed=seed + 8, t=torch.float16)]
+
+
+def test_small_calls_on_streams_and_in_graphs():
+    sets = [small_inputs(110), small_inputs(120, T=32)]
+    want = [small_calls(*a) for a in sets]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in sets]
+    got = [None] * len(sets)
+    for _ in range(3):
+        for i, st in enumerate(streams):
+            with torch.cuda.stream(st):
+                got[i] = small_calls(*sets[i])
+    torch.cuda.synchronize()
+    for w, g in zip(want, got):
+        assert all(torch.equal(a, b) for a, b in zip(w, g))
+    graphs, outs = [], []
+    for args in sets:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            outs.append(small_calls(*args))
+        graphs.append(g)
+    for k in range(4):
+        for args, g, out in zip(sets, graphs, outs):
+            for i, v in enumerate(small_inputs(130 + k, T=args[0].shape[0])):
+                args[i].copy_(v)
+            g.replay()
+            torch.cuda.synchronize()
+            kept = [o.clone() for o in out]
+            assert all(torch.equal(a, b) for a, b in zip(kept, small_calls(*args)))
+
+
+@pytest.mark.parametrize("T", [1, 4, 16, 29])
+def test_gated_few_rows_keep_special_values_to_themselves(T):
+    x, wg, wu = gated_inputs(T, 600, 300, torch.float16, seed=38)
+    clean = fw.gated_nt(x, wg, wu)
+    bad = x.clone()
+    bad[T - 1, 599] = float("nan")
+    got = fw.gated_nt(bad, wg, wu)
+    assert torch.isnan(got[T - 1]).all() and torch.equal(got[:T - 1], clean[:T - 1])
+    heavy = wg.clone()
+    heavy[299, 0] = float("inf")
+    got = fw.gated_nt(x, heavy, wu)
+    assert torch.equal(got[:, :299], clean[:, :299]) and not torch.isfinite(got[x[:, 0] > 0, 299]).any()
+
+
 def test_on_another_current_device(monkeypatch):
     """The operand's device is entered when another one is current (simulated on one GPU)."""
     args = everything_inputs(90)
