@@ -247,7 +247,7 @@ __global__ void __launch_bounds__(kFewWaves * kWave, 2) gated_few(const GatedOp<
 
 // dG = dH * P, dU = dH * Q for a 64 x 64 tile: row-major into rows of dGU
 // (dG at column 0, dU at column Fp), transposed into dGT and dUT (pitch Tp).
-// Rows and columns past the end, up to multiples of eight, become zeros.
+// Rows and columns past the end, up to Tp and Fp, become zeros.
 // dH comes in by rows and turns in LDS to the blocks that `saved` holds.
 // Bound by its bytes: 2 + 8 read, 8 written per element.
 template <class E>
@@ -401,6 +401,12 @@ struct ForwardSpace {
     }
 };
 
+// Rows of the gradients' operands start on 128 bytes: the 64 x 64 tiles that
+// write them then write whole cache lines (by 16 bytes, lines are shared by
+// workgroups of different XCDs, whose L2s write parts of them: 2595 x 264 x
+// 13232 backward 320 us, and 250 by lines; 6872 x 1551 x 2957 425 and 360).
+constexpr int64_t kLine = 64;
+
 template <class E>
 struct BackwardSpace {
     E *wt, *xt, *dgu, *dgt, *dut;
@@ -409,8 +415,8 @@ struct BackwardSpace {
     BackwardSpace(void* base, int64_t T, int64_t D, int64_t F)
     {
         abi::Carve c(base);
-        Tp = abi::up(T, 8);
-        Fp = abi::up(F, 8);
+        Tp = abi::up(T, kLine);
+        Fp = abi::up(F, kLine);
         wt = c.take<E>(D * 2 * Fp);
         xt = c.take<E>(D * Tp);
         dgu = c.take<E>(T * 2 * Fp);
@@ -430,7 +436,7 @@ Activation activation_of(int32_t a)
 bool good_sizes(int64_t T, int64_t D, int64_t F)
 {
     // a row of [dG dU] has 2F elements (and padding)
-    return abi::good_dim(T) && D >= 0 && D <= abi::kMaxPitch - 8 && F >= 0 && 2 * F <= abi::kMaxPitch - 16 &&
+    return abi::good_dim(T) && D >= 0 && D <= abi::kMaxPitch - 8 && F >= 0 && 2 * F <= abi::kMaxPitch - 127 &&
            T <= abi::kMaxDim - 256;
 }
 
@@ -591,7 +597,7 @@ int gated_nt_backward(const void* dH, const void* X, const void* Wg, const void*
     if (!good_pitch(lddh, F) || !good_pitch(ldx, D) || !good_pitch(ldg, D) || !good_pitch(ldu, D) ||
         !good_pitch(lddx, D) || !good_pitch(lddg, D) || !good_pitch(lddu, D))
         return hipErrorInvalidValue;
-    if (up(T, 8) > kMaxPitch) return hipErrorInvalidValue;  // rows of the transposed operands
+    if (up(T, kLine) > kMaxPitch) return hipErrorInvalidValue;  // rows of the transposed operands
     if (!nt::fits(T, D, 1) || !nt::fits(F, D, 2)) return hipErrorInvalidValue;
     if (type != GATED_NT_F16 && type != GATED_NT_BF16) return hipErrorInvalidValue;
     if (!good_pointer(dH, T, F, 2) || !good_pointer(X, T, D, 2) || !good_pointer(Wg, F, D, 2) ||

@@ -1,5 +1,5 @@
 // Copies that bring an operand into the form the tiled products read: rows
-// on 16 bytes, padded with zeros to a multiple of eight elements, as they are
+// on 16 bytes or more, padded with zeros to a multiple of eight elements, as they are
 // or transposed.
 #ifndef DENSE_FP16_GEMM_RELAYOUT_H
 #define DENSE_FP16_GEMM_RELAYOUT_H
@@ -38,7 +38,7 @@ __device__ __forceinline__ Four<E> load4(const E* row, int c, int cols, bool vec
 // Writes a 64 x 64 tile that LDS holds row-major (pitch kPitch) transposed:
 // dst[c][r] for tile row r and column c, whole rows of `rows` in groups of
 // eight bytes (dst's pitch is a multiple of 8; rows past `rows_valid` hold
-// zeros in LDS, and `rows` is its multiple of eight).
+// zeros in LDS, and `rows` is a multiple of eight from it on).
 template <class E>
 __device__ __forceinline__ void store_transposed(const E* tile, E* dst, int64_t ldd, int r0, int c0, int rows, int cols)
 {
