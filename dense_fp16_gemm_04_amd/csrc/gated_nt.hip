@@ -379,6 +379,12 @@ int product(const E* A0, const E* A1, const E* B, E* C0, E* C1, int64_t M, int64
     return eights(C0, N, ldc0) && (!A1 || eights(C1, N, ldc1)) ? with(StoreOp<E, true>{}) : with(StoreOp<E, false>{});
 }
 
+// Rows of what is copied, transposed or computed for the products start on 128
+// bytes: the 64 x 64 tiles that write them then write whole cache lines (by 16 bytes, lines are shared by
+// workgroups of different XCDs, whose L2s write parts of them: 2595 x 264 x
+// 13232 backward 320 us, and 250 by lines; 6872 x 1551 x 2957 425 and 360).
+constexpr int64_t kLine = 64;
+
 // Copies of the operands that the kernels cannot read in place.
 template <class E>
 struct ForwardSpace {
@@ -393,19 +399,13 @@ struct ForwardSpace {
         copy_x = D % 8 || !vec8(X, ldx);
         copy_g = D % 8 || !vec8(Wg, ldg);
         copy_u = D % 8 || !vec8(Wu, ldu);
-        const int64_t Dp = abi::up(D, 8);
-        x = copy_x ? c.take<E>(T * Dp) : nullptr;
-        g = copy_g ? c.take<E>(F * Dp) : nullptr;
-        u = copy_u ? c.take<E>(F * Dp) : nullptr;
+        const int64_t ld = abi::up(D, kLine);
+        x = copy_x ? c.take<E>(T * ld) : nullptr;
+        g = copy_g ? c.take<E>(F * ld) : nullptr;
+        u = copy_u ? c.take<E>(F * ld) : nullptr;
         bytes = c.used();
     }
 };
-
-// Rows of the gradients' operands start on 128 bytes: the 64 x 64 tiles that
-// write them then write whole cache lines (by 16 bytes, lines are shared by
-// workgroups of different XCDs, whose L2s write parts of them: 2595 x 264 x
-// 13232 backward 320 us, and 250 by lines; 6872 x 1551 x 2957 425 and 360).
-constexpr int64_t kLine = 64;
 
 template <class E>
 struct BackwardSpace {
@@ -436,7 +436,7 @@ Activation activation_of(int32_t a)
 bool good_sizes(int64_t T, int64_t D, int64_t F)
 {
     // a row of [dG dU] has 2F elements (and padding)
-    return abi::good_dim(T) && D >= 0 && D <= abi::kMaxPitch - 8 && F >= 0 && 2 * F <= abi::kMaxPitch - 127 &&
+    return abi::good_dim(T) && D >= 0 && D <= abi::kMaxPitch - 63 && F >= 0 && 2 * F <= abi::kMaxPitch - 127 &&
            T <= abi::kMaxDim - 256;
 }
 
@@ -445,7 +445,7 @@ int forward(const E* X, const E* Wg, const E* Wu, E* H, float* saved, int64_t T,
             int64_t ldg, int64_t ldu, int64_t ldh, int32_t activation, void* workspace, hipStream_t stream)
 {
     const ForwardSpace<E> w(workspace, X, Wg, Wu, T, D, F, ldx, ldg, ldu);
-    const int64_t Dp = abi::up(D, 8);
+    const int64_t Dp = abi::up(D, 8), copied_ld = abi::up(D, kLine);
     GatedOp<E, SAVE, EIGHTS> op = {};
     op.X = X;
     op.Wg = Wg;
@@ -459,15 +459,15 @@ int forward(const E* X, const E* Wg, const E* Wu, E* H, float* saved, int64_t T,
         if (!copy) return;
         copies.job[copies.jobs++] = {src, dst, ld, rows};
         src = dst;
-        ld = (int)Dp;
+        ld = (int)copied_ld;
     };
     copied(w.copy_x, op.X, op.lda, w.x, T);
     copied(w.copy_g, op.Wg, op.ldg, w.g, F);
     copied(w.copy_u, op.Wu, op.ldu, w.u, F);
     if (copies.jobs && Dp) {
-        const int64_t work = std::max(T, F) * (Dp / 4);
+        const int64_t work = std::max(T, F) * (copied_ld / 4);
         hipLaunchKernelGGL(relayout::copy_rows<E>, dim3((unsigned)std::min<int64_t>((work + 255) / 256, 16384), copies.jobs),
-                           dim3(relayout::kThreads), 0, stream, copies, (int)D, (int)Dp);
+                           dim3(relayout::kThreads), 0, stream, copies, (int)D, (int)copied_ld);
         const int rc = (int)hipGetLastError();
         if (rc) return rc;
     }

@@ -137,7 +137,7 @@ __global__ void __launch_bounds__(256) ns_copy_out(const half* __restrict__ X, i
 enum { kAsIs = 1, kTurned = 2, kEights = 4 };
 
 // S (POLY false: alpha A A^T) or P (POLY true: alpha A A^T + beta A + gamma I,
-// A symmetric), [m, m] with pitch mp, tiles on and below the diagonal and
+// A symmetric), [m, mp] with pitch ldc, tiles on and below the diagonal and
 // their transposes.
 template <bool POLY>
 struct SymmetricOp {
@@ -145,7 +145,7 @@ struct SymmetricOp {
     const half* A;
     half* C;
     float* diag;  // (POLY) C's diagonal before it is rounded
-    int M, K, lda, mp, tiles, per;  // per: tiles of one matrix
+    int M, K, lda, ldc, mp, tiles, per;  // per: tiles of one matrix
     int64_t stride_a, stride_c;
     float alpha, beta, gamma;
 
@@ -183,7 +183,7 @@ struct SymmetricOp {
     {
         half* c = C + t.batch * stride_c;
         half4 v[T::FM][T::FN];
-        const Rows direct = rows_at(c, t.m0, M, T::BM, mp, t.n0, mp);
+        const Rows direct = rows_at(c, t.m0, M, T::BM, ldc, t.n0, mp);
         if constexpr (POLY) {
             // the tile of A through LDS to the values that use it, which
             // take its place there
@@ -251,7 +251,7 @@ struct SymmetricOp {
         }
         // Rows M .. mp - 1 of the accumulator are zero: the transpose's
         // padding.
-        Rows turned = rows_at(c, t.n0, M, T::BN, mp, t.m0, mp);
+        Rows turned = rows_at(c, t.n0, M, T::BN, ldc, t.m0, mp);
         if (!(T::WAVES == 1 ? t.mirror : t.n0 < t.m0)) turned.rs = make_rsrc(c, 0);  // (a whole tile's, of a sub-tile)
         write_turned<T, true>([&](int i, int j) { return v[i][j]; }, turned, lane, wave, s0, s1);
     }
@@ -268,7 +268,7 @@ struct ApplyOp {
     const float* diag;  // P's diagonal before it was rounded
     half *X, *XtNew;
     __bf16* out;
-    int M, N, K, lda, ldb, np, tiles, tiles_m, tiles_n, ldo;
+    int M, N, K, lda, ldb, ldx, np, tiles, tiles_m, tiles_n, ldo;  // ldb, ldx: of X^T and X
     int64_t stride_p, stride_x, stride_o;
     float alpha;
 
@@ -306,7 +306,7 @@ struct ApplyOp {
         // Each row's factor: what rounding took from its diagonal entry.  (A
         // subnormal one is left as it is, its quotient may be far from 1.)
         const __amdgpu_buffer_rsrc_t entries =
-            make_rsrc(diag + (int64_t)t.batch * lda + t.m0, (uint32_t)min(T::BM, M - t.m0) * 4u);
+            make_rsrc(diag + (int64_t)t.batch * K + t.m0, (uint32_t)min(T::BM, M - t.m0) * 4u);
         float f[T::FM];
 #pragma unroll
         for (int i = 0; i < T::FM; ++i) {
@@ -327,12 +327,12 @@ struct ApplyOp {
             if constexpr (HOW & kTurned)
                 write_turned<T, EIGHTS>(value, rows_at(o, t.n0, N, T::BN, ldo, t.m0, M), lane, wave, s0, s1);
         } else {
-            // (columns N .. np - 1 and rows M .. ldb - 1 of the accumulator
+            // (columns N .. np - 1 and rows M .. K - 1 of the accumulator
             // are zero: the padding of both)
             auto value = [&](int i, int j) { return round4<half>(acc[i][j] * f[i]); };
-            write_rows<T, T::FN, true>(value, rows_at(X + t.batch * stride_x, t.m0, M, T::BM, np, t.n0, np), lane, wave,
+            write_rows<T, T::FN, true>(value, rows_at(X + t.batch * stride_x, t.m0, M, T::BM, ldx, t.n0, np), lane, wave,
                                        s0, s1);
-            write_turned<T, true>(value, rows_at(XtNew + t.batch * stride_x, t.n0, N, T::BN, ldb, t.m0, ldb), lane, wave,
+            write_turned<T, true>(value, rows_at(XtNew + t.batch * stride_x, t.n0, N, T::BN, ldb, t.m0, K), lane, wave,
                                   s0, s1);
         }
     }
@@ -340,19 +340,25 @@ struct ApplyOp {
 
 // ------------------------------------------------------------------ host --
 
+// Rows start on 128 bytes: the tiles that read and write them then do so by
+// whole cache lines.
+constexpr int64_t kLine = 64;
+
 struct Space {
     double* partial;
     half *x[2], *xt[2], *s, *p;
     float *diag, *sums;  // P's diagonal; of split tiles
-    int64_t m, n, mp, np, stride_x, stride_s, bytes;
+    int64_t m, n, mp, np, lm, ln, stride_x, stride_s, bytes;
     Space(void* base, int64_t batch, int64_t rows, int64_t cols)
     {
         m = std::min(rows, cols);
         n = std::max(rows, cols);
         mp = abi::up(m, 8);
         np = abi::up(n, 8);
-        stride_x = mp * np;
-        stride_s = mp * mp;
+        lm = abi::up(m, kLine);
+        ln = abi::up(n, kLine);
+        stride_x = std::max(mp * ln, np * lm);
+        stride_s = mp * lm;
         abi::Carve c(base);
         partial = c.take<double>(batch * kNormBlocks);
         for (int i = 0; i < 2; ++i) {
@@ -461,8 +467,8 @@ int run(const E* G, __bf16* out, int64_t batch, int64_t rows, int64_t cols, int6
                                  workspace, stream);
     const Space w(workspace, batch, rows, cols);
     const bool tall = rows > cols;
-    const int64_t pr = abi::up(rows, 8), pc = abi::up(cols, 8);
-    const int64_t tr = (pr + 63) / 64, tc = (pc + 63) / 64;
+    const int64_t pr = abi::up(rows, kLine), pc = abi::up(cols, kLine);
+    const int64_t tr = pr / 64, tc = pc / 64;
     // (the products have no more tiles than that)
     if (!abi::good_grid(tr * tc * batch, 256)) return hipErrorInvalidValue;
     const double scale = std::ldexp(1.0, scale_bits(w.n));
@@ -486,7 +492,9 @@ int run(const E* G, __bf16* out, int64_t batch, int64_t rows, int64_t cols, int6
         s.A = w.x[from];
         s.C = w.s;
         s.M = (int)w.m;
-        s.K = s.lda = (int)w.np;
+        s.K = (int)w.np;
+        s.lda = (int)w.ln;
+        s.ldc = (int)w.lm;
         s.mp = (int)w.mp;
         s.stride_a = w.stride_x;
         s.stride_c = w.stride_s;
@@ -497,7 +505,8 @@ int run(const E* G, __bf16* out, int64_t batch, int64_t rows, int64_t cols, int6
         p.C = w.p;
         p.diag = w.diag;
         p.M = (int)w.m;
-        p.K = p.lda = p.mp = (int)w.mp;
+        p.K = p.mp = (int)w.mp;
+        p.lda = p.ldc = (int)w.lm;
         p.stride_a = p.stride_c = w.stride_s;
         p.alpha = (float)coefficients[3 * i + 2];
         p.beta = (float)coefficients[3 * i + 1];
@@ -512,7 +521,9 @@ int run(const E* G, __bf16* out, int64_t batch, int64_t rows, int64_t cols, int6
             op.out = out;
             op.M = (int)w.m;
             op.N = (int)w.n;
-            op.K = op.lda = op.ldb = (int)w.mp;
+            op.K = (int)w.mp;
+            op.lda = op.ldb = (int)w.lm;
+            op.ldx = (int)w.ln;
             op.np = (int)w.np;
             op.ldo = (int)ldo;
             op.stride_p = w.stride_s;
@@ -535,8 +546,8 @@ int run(const E* G, __bf16* out, int64_t batch, int64_t rows, int64_t cols, int6
 
 bool good_sizes(int64_t batch, int64_t rows, int64_t cols)
 {
-    return batch >= 0 && batch < (1 << 16) && rows >= 0 && rows <= abi::kMaxPitch - 8 && cols >= 0 &&
-           cols <= abi::kMaxPitch - 8;
+    return batch >= 0 && batch < (1 << 16) && rows >= 0 && rows <= abi::kMaxPitch - 63 && cols >= 0 &&
+           cols <= abi::kMaxPitch - 63;
 }
 
 }  // namespace

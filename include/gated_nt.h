@@ -34,7 +34,7 @@
  *
  * hipErrorInvalidValue before anything is enqueued: a negative size, T above
  * 2^31 - 257 (2^21 - 64 in the backward pass, whose sums run over T), D above
- * 2^21 - 9, F above 2^20 - 64, a result of more tiles than a launch can hold
+ * 2^21 - 64, F above 2^20 - 64, a result of more tiles than a launch can hold
  * (2^23 of 256 x 128), a row pitch below the row or of 2^21 or more, an
  * unknown type or activation, a null or odd pointer with a non-zero extent, `saved`
  * not 16-byte aligned, an output whose first-to-last-element range meets an

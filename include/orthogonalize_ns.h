@@ -28,7 +28,7 @@
  * caller's and may be reused by work enqueued later on the same stream.
  *
  * hipErrorInvalidValue before anything is enqueued: a negative size, a size
- * above 2^21 - 9 in rows or cols, batch of 2^16 or more, a pitch below the
+ * above 2^21 - 64 in rows or cols, batch of 2^16 or more, a pitch below the
  * row, ldo of 2^21 or more, matrices of out that do not lie one after
  * another, an unknown type, steps below 0 or above 64, null coefficients with
  * steps > 0, eps below 0 or NaN, a null or misaligned pointer with a non-zero
