@@ -12,9 +12,9 @@
 // terms to a sum, and dWg, dWu are two of one shape over T, all in NT form on
 // transposed copies of X and of the weights.
 //
-// Measured (binary16 forward 4096 x 4096 x 8192: 375 us, 1467 TFLOP/s, the
-// matrix cores busy 87% of the cycles; bfloat16 step 8192 x 4096 x 8192: 2482
-// us, 1329 TFLOP/s, of which the forward pass 865, the gradients' operands 300
+// Measured (binary16 forward 4096 x 4096 x 8192: 371 us, 1482 TFLOP/s, the
+// matrix cores busy 87% of the cycles; bfloat16 step 8192 x 4096 x 8192: 2473
+// us, 1334 TFLOP/s, of which the forward pass 865, the gradients' operands 300
 // to 345 at 5.4 TB/s, the two products 788 each).
 #include "gated_nt.h"
 
