@@ -11,7 +11,6 @@
 namespace cdna4 {
 
 typedef float f32x4 __attribute__((ext_vector_type(4)));
-typedef float f32x2 __attribute__((ext_vector_type(2)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 typedef __attribute__((address_space(3))) void lds_void;
@@ -20,7 +19,6 @@ constexpr int kWave = 64;
 constexpr int kXcds = 8;                // MI355X: 8 dies, workgroups dealt to them in turn
 constexpr uint32_t kOob = 0x80000000u;  // a buffer offset past every tile: loads 0, stores nothing
 constexpr int kRsrcWord3 = 0x00020000;  // buffer resource word 3: 32-bit data, no swizzle
-constexpr int kPolicyNt = 2;            // the nontemporal bit of a buffer access
 
 // A 16-bit element type: its vectors, the MFMA that multiplies it, and its
 // rounding (to nearest, ties to even, both by one conversion instruction).

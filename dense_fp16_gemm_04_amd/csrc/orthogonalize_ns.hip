@@ -187,7 +187,7 @@ struct SymmetricOp {
         if constexpr (POLY) {
             // the tile of A through LDS to the values that use it, which
             // take its place there
-            constexpr int ROUNDS = T::BM * T::BN * 2 > T::STAGE_MAX ? 2 : 1, RW = T::WTM / ROUNDS, IR = T::FM / ROUNDS;
+            static_assert(T::BM * T::BN * 2 <= T::STAGE_MAX, "the tile fits");
             const Rows old = rows_at(A + t.batch * stride_a, t.m0, M, T::BM, lda, t.n0, mp);
             const Image<T::BN> image{s0, s1};
             const int wm = wave / T::WAVES_N, wn = wave % T::WAVES_N;
@@ -199,50 +199,46 @@ struct SymmetricOp {
             float mine[T::FM];  // the lane's entry of each block row on the diagonal, if it has one
 #pragma unroll
             for (int i = 0; i < T::FM; ++i) mine[i] = 0.0f;
+            auto same = [](int x) { return x; };
+            fill<T, T::BN, T::BM>(image, old, same, lane, wave);
+            lds_barrier<0>();
+            const int at_row = wm * T::WTM + (lane & 15), at_col = wn * T::WTN + 4 * (lane >> 4);
 #pragma unroll
-            for (int h = 0; h < ROUNDS; ++h) {
-                auto to = [&](int x) { return x / RW * T::WTM + h * RW + x % RW; };
-                fill<T, T::BN, T::WAVES_M * RW>(image, old, to, lane, wave);
-                lds_barrier<0>();
-                const int ln = pinned(lane);
+            for (int i = 0; i < T::FM; ++i)
 #pragma unroll
-                for (int i = 0; i < IR; ++i)
+                for (int j = 0; j < T::FN; ++j) {
+                    half4* at = image.template at<half4>(at_row + i * 16, at_col + j * 16);
+                    const half4 a4 = *at;
+                    f32x4 w = acc[i][j] * alpha;
+                    // (where a wave's part is square, only its blocks (i, i)
+                    // can lie on the diagonal)
+                    constexpr bool SQUARE = T::WTM == T::WTN;
+                    const float on = SQUARE ? gamma_here : on_diagonal(i, j) ? gamma : 0.0f;
 #pragma unroll
-                    for (int j = 0; j < T::FN; ++j) {
-                        const int x = wm * RW + i * 16 + (ln & 15), col = wn * T::WTN + j * 16 + 4 * (ln >> 4);
-                        half4* at = image.template at<half4>(x, col);
-                        const half4 a4 = *at;
-                        f32x4 w = acc[h * IR + i][j] * alpha;
-                        // (where a wave's part is square, only its blocks (i, i)
-                        // can lie on the diagonal)
-                        constexpr bool SQUARE = T::WTM == T::WTN;
-                        const float on = SQUARE ? gamma_here : on_diagonal(h * IR + i, j) ? gamma : 0.0f;
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            w[e] = __builtin_fmaf(beta, (float)a4[e], w[e]);
-                            if (!SQUARE || h * IR + i == j) w[e] = __builtin_fmaf(diagonal[e], on, w[e]);
-                        }
-                        const half4 w16 = round4<half>(w);
-                        *at = v[h * IR + i][j] = w16;
-                        if (!SQUARE || h * IR + i == j) {
-                            float d = diagonal[0] * w[0];
-#pragma unroll
-                            for (int e = 1; e < 4; ++e) d = __builtin_fmaf(diagonal[e], w[e], d);
-                            mine[h * IR + i] = SQUARE || on_diagonal(h * IR + i, j) ? d : mine[h * IR + i];
-                        }
+                    for (int e = 0; e < 4; ++e) {
+                        w[e] = __builtin_fmaf(beta, (float)a4[e], w[e]);
+                        if (!SQUARE || i == j) w[e] = __builtin_fmaf(diagonal[e], on, w[e]);
                     }
-                lds_barrier<63>();
-                drain<T, T::BN, T::WAVES_M * RW, true>(image, direct, to, lane, wave);
-                lds_barrier<63>();
-            }
+                    const half4 w16 = round4<half>(w);
+                    *at = v[i][j] = w16;
+                    if (!SQUARE || i == j) {
+                        float d = diagonal[0] * w[0];
+#pragma unroll
+                        for (int e = 1; e < 4; ++e) d = __builtin_fmaf(diagonal[e], w[e], d);
+                        mine[i] = SQUARE || on_diagonal(i, j) ? d : mine[i];
+                    }
+                }
+            lds_barrier<63>();
+            drain<T, T::BN, T::BM, true>(image, direct, same, lane, wave);
+            lds_barrier<63>();
             // (the waves whose rows have no entry in the tile store nothing)
             const __amdgpu_buffer_rsrc_t entries =
                 make_rsrc(diag + (int64_t)t.batch * mp + t.m0, (uint32_t)min(T::BM, M - t.m0) * 4u);
-            const int ln = pinned(lane);
 #pragma unroll
             for (int i = 0; i < T::FM; ++i) {
                 const int m = wm * T::WTM + i * 16, n = t.m0 + m - t.n0 - wn * T::WTN;  // the entry's column in the wave's
-                const uint32_t at = (ln & 15) >> 2 == ln >> 4 && n >= 0 && n < T::WTN ? (uint32_t)(m + (ln & 15)) * 4u : kOob;
+                const uint32_t at =
+                    (lane & 15) >> 2 == lane >> 4 && n >= 0 && n < T::WTN ? (uint32_t)(m + (lane & 15)) * 4u : kOob;
                 __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(uint32_t, mine[i]), entries, at, 0, 0);
             }
         } else {
