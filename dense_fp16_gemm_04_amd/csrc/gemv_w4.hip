@@ -121,6 +121,37 @@ struct Few {
     }
 };
 
+// A sum that is not finite, from the definition term by term.  The kernels add
+// up (q + offset) x and take offset + zero times the sum of x out again: an
+// infinite x then gives inf - inf in place of the infinity that (q - zero) x
+// is, and bfloat16 x past 2^128 / 143 overflow where q - zero alone would not.
+// Whatever goes wrong so leaves an infinity or a NaN, so those results, and
+// only those, are computed once more, in 64 bits, which no x, zero and scale
+// overflow.  A wave takes one result, its lanes eight k each in turn (one row
+// with an infinity by 8192 x 4096: 57 us instead of 9; a result to a lane
+// took 305).  Rows that begin with a NaN, as those of unused memory and of
+// masked tokens do, stay as they are: their results are NaN.
+__device__ __forceinline__ bool is_finite(float v)
+{
+    return (__builtin_bit_cast(uint32_t, v) & 0x7f800000u) != 0x7f800000u;
+}
+__device__ __forceinline__ bool is_nan(float v) { return v != v; }
+template <class E>
+__device__ __forceinline__ float by_terms(const E* __restrict__ x, const unsigned char* __restrict__ q,
+                                          const E* __restrict__ scale, const E* __restrict__ zero, int K, int shift, int lane)
+{
+    double sum = 0;
+#pragma unroll 1
+    for (int k = lane * 8; k < K; k += kWave * 8) {  // (a group holds whole eights)
+        const uint32_t w = *(const uint32_t*)(q + k / 2);
+        const double s = (double)(float)scale[k >> shift], z = zero ? (double)(float)zero[k >> shift] : 8.0;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) sum += (double)(float)x[k + e] * (((double)(w >> 4 * e & 15) - z) * s);
+    }
+    for (int d = kWave / 2; d > 0; d >>= 1) sum += __shfl_xor(sum, d);
+    return (float)sum;
+}
+
 // FLUSH: runs of 32 k per group sum (4: the group holds whole chunks of 128).
 // EIGHTS: x's rows start on 16 bytes; otherwise its elements come one by one.
 //
@@ -313,7 +344,18 @@ gemv_w4_kernel(const E* __restrict__ X, const unsigned char* __restrict__ Q, con
         float v = 0.0f;
 #pragma unroll
         for (int w = 0; w < kWaves; ++w) v += (*(const Part*)(smem + w * REGION))[p][(at >> 4) & 15][at & 15];
-        if (m < M && n < N) Y[(int64_t)m * ldy + n] = (E)v;
+        const bool there = m < M && n < N;
+        // (a wave's lanes are all in the loop or none)
+        uint64_t doubts = __ballot(there && !is_finite(v) && !is_nan((float)X[m * ldx]));
+        while (doubts) {
+            const int of = __builtin_ctzll(doubts);
+            doubts &= doubts - 1;
+            const int md = __builtin_amdgcn_readlane(m, of), nd = __builtin_amdgcn_readlane(n, of);
+            const float sum64 = by_terms(X + md * ldx, Q + nd * ldq, scale + (int64_t)nd * groups,
+                                         ZERO ? zero + (int64_t)nd * groups : nullptr, K, shift, lane);
+            v = lane == of ? sum64 : v;
+        }
+        if (there) Y[(int64_t)m * ldy + n] = (E)v;
     }
 }
 
@@ -541,6 +583,7 @@ gemm_w4_kernel(const E* __restrict__ X, const unsigned char* __restrict__ Q, con
                 *(f32x4*)(smem + ((((wave - 4) * 4 + i) * FN + j) * 64 + lane) * 16) = total[i][j];
     __syncthreads();
     if (q > 0) return;
+    uint32_t doubts = 0;  // bit (i FN + j) 4 + e: of the lane's results
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const int m = m0 + 16 * i + r;
@@ -552,6 +595,9 @@ gemm_w4_kernel(const E* __restrict__ X, const unsigned char* __restrict__ Q, con
                 sum4 += *(const f32x4*)(smem + ((((o * 4 + part) * 4 + i) * FN + j) * 64 + lane) * 16);
             const int n = n0 + part * 16 * FN + 16 * j + 4 * h;
             if (m >= M) continue;
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                doubts |= is_finite(sum4[e]) || n + e >= N ? 0u : 1u << ((i * FN + j) * 4 + e);
             const x4 v = round4<E>(sum4);
             E* y = Y + (int64_t)m * ldy + n;
             if (whole && n + 3 < N) {
@@ -561,6 +607,22 @@ gemm_w4_kernel(const E* __restrict__ X, const unsigned char* __restrict__ Q, con
                 for (int e = 0; e < 4; ++e)
                     if (n + e < N) y[e] = v[e];
             }
+        }
+    }
+    for (int i = 0; i < 4; ++i) {
+        const uint32_t row = ((1u << (4 * FN)) - 1) << (i * 4 * FN);
+        if ((doubts & row) && is_nan((float)X[(m0 + 16 * i + r) * ldx])) doubts &= ~row;
+    }
+    while (const uint64_t lanes = __ballot(doubts != 0)) {
+        const int of = __builtin_ctzll(lanes);
+        const int bit = __builtin_ctz((uint32_t)__builtin_amdgcn_readlane((int)doubts, of)), block = bit >> 2;
+        const int m = m0 + 16 * (block / FN) + (of & 15);
+        const int n = n0 + part * 16 * FN + 16 * (block % FN) + 4 * (of >> 4) + (bit & 3);
+        const float sum64 = by_terms(X + m * ldx, Q + n * ldq, scale + (int64_t)n * groups,
+                                     ZERO ? zero + (int64_t)n * groups : nullptr, K, shift, lane);
+        if (lane == of) {
+            Y[(int64_t)m * ldy + n] = (E)sum64;
+            doubts &= doubts - 1;
         }
     }
 }

@@ -13,9 +13,16 @@
  *   Y       [M, N]          of X's type, rows ldy elements apart
  *
  * Codes enter the matrix cores as whole numbers, which both types hold
- * exactly; a group's sum is multiplied by its scale in 32 bits, and zero
- * points enter as zero * (sum of the group's x).  Y is rounded once, to
- * nearest even.  The order of the additions is fixed for given sizes.
+ * exactly (binary16: code - 8; bfloat16: code + 128); a group's sum is
+ * multiplied by its scale in 32 bits, and zero points, with the offset, enter
+ * as (zero + offset) * (sum of the group's x).  Y is rounded once, to nearest
+ * even.  The order of the additions is fixed for given sizes.
+ *
+ * Infinities and NaN in X, scale and zero give what the definition gives,
+ * and large finite X do not overflow on the way: results that are not finite
+ * are computed again term by term in 64 bits, unless their row of X begins
+ * with a NaN.  That costs time where rows hold infinities or a later NaN (one
+ * such row: 57 us for 8192 x 4096 weights instead of 9).
  *
  * M may be any number of rows: one to sixteen cost the same, since reading
  * the weights is all the work; further on each 32 rows (small results) or 64
