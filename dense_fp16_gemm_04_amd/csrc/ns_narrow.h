@@ -68,6 +68,27 @@ __device__ __forceinline__ void store_share(const f32x4 (&acc)[kBlocks], float* 
     for (int j = 0; j < kBlocks; ++j) *(f32x4*)(at + j * 256) = acc[j];
 }
 
+// An entry of G to one of X: times scale / (norm + eps), the norm from four
+// partial sums of squares.  As a power of two and a rest: in 32 bits the
+// factor alone would overflow for norms below 2^-112 and lose bits above 2^140.
+struct Factor {
+    float rest;
+    int bits = 0;
+    __device__ __forceinline__ Factor(const double* part, double eps, double scale)
+    {
+        const double norm = sqrt(part[0] + part[1] + part[2] + part[3]) + eps;
+        double f = scale / norm;
+        // (an eps of next to nothing and the zero matrix: zeros)
+        if (norm > 0 && f > 0x1p1000) f = 0x1p1000;
+        if (f > 0 && f <= 0x1p1000) {
+            bits = ilogb(f);
+            f = ldexp(f, -bits);
+        }
+        rest = (float)f;
+    }
+    __device__ __forceinline__ half operator()(float g) const { return (half)(ldexpf(g, bits) * rest); }
+};
+
 // X^T and the shares of S from G: `partial` holds the sums of its squares.
 template <class E>
 __global__ void __launch_bounds__(kThreads)
@@ -84,7 +105,7 @@ ns_narrow_begin(const Args a, const E* __restrict__ G, int64_t ldg, int64_t stri
         if (lane == 0) part[wave] = s;
     }
     __syncthreads();
-    const float f = (float)(scale / (sqrt(part[0] + part[1] + part[2] + part[3]) + eps));
+    const Factor f(part, eps, scale);
     const E* g = G + b * stride_g;
     half* xt = a.xt + (int64_t)b * a.chunks * kRows * kRows;
     f32x4 acc[kBlocks] = {};
@@ -103,7 +124,7 @@ ns_narrow_begin(const Args a, const E* __restrict__ G, int64_t ldg, int64_t stri
 #pragma unroll
         for (int i = 0; i < kRows / 4; ++i) {
             const int at = i * kThreads + tid, slow = at / kRows, fast = at % kRows;
-            x[a.tall ? fast * kPitch + slow : slow * kPitch + fast] = (half)((float)v[i] * f);
+            x[a.tall ? fast * kPitch + slow : slow * kPitch + fast] = f((float)v[i]);
         }
         __syncthreads();
 #pragma unroll

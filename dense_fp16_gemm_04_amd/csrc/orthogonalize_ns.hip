@@ -81,7 +81,7 @@ __global__ void __launch_bounds__(256) ns_squares(const E* __restrict__ G, int64
     if (threadIdx.x == 0) partial[blockIdx.x] = part[0];
 }
 
-// D1 [rows, p1] = G * scale / (norm + eps) and D2 [cols, p2] its transpose,
+// D1 [rows, p1] = G * scale / (norm + eps) (narrow::Factor) and D2 [cols, p2] its transpose,
 // both padded with zeros to their pitches.
 template <class E>
 __global__ void __launch_bounds__(relayout::kThreads)
@@ -101,7 +101,7 @@ ns_start(const E* __restrict__ G, int64_t ldg, int64_t stride_g, int rows, int c
         if (threadIdx.x % 64 == 0) part[threadIdx.x / 64] = s;
     }
     __syncthreads();
-    const float f = (float)(scale / (sqrt(part[0] + part[1] + part[2] + part[3]) + eps));
+    const narrow::Factor f(part, eps, scale);
     const E* g = G + b * stride_g;
     half* d1 = D1 + b * stride_x;
     const int x = threadIdx.x & 15, y = threadIdx.x >> 4;
@@ -112,7 +112,7 @@ ns_start(const E* __restrict__ G, int64_t ldg, int64_t stride_g, int rows, int c
         if (r0 + r < rows) {
             const Four<E> w = load4(g + (r0 + r) * ldg, c, cols, vec);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) v[e] = (half)((float)w[e] * f);
+            for (int e = 0; e < 4; ++e) v[e] = f((float)w[e]);
             if (c < p1) *(half4*)(d1 + (int64_t)(r0 + r) * p1 + c) = v;
         }
         *(half4*)(tile + r * kPitch + x * 4) = v;

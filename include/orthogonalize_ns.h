@@ -19,9 +19,9 @@
  * finer than the bfloat16 that the update is usually computed in; what
  * rounding takes from the polynomial's diagonal, its largest part, is put
  * back into the product's rows.  The result is therefore bfloat16, whatever
- * G's type: its error is 1.05 to 1.4 times that of its own rounding.  A matrix
- * whose norm is not finite, or that holds a NaN, gives NaN; the zero matrix
- * gives zeros.
+ * G's type: its error is 1.05 to 1.4 times that of its own rounding.  With
+ * steps > 0 a matrix that holds an infinity or a NaN gives NaN; with none,
+ * G / inf.  The zero matrix gives zeros, and 0 / 0 with eps = 0.
  *
  * Ownership, concurrency, errors and capture are those of gemm_nt_f16.h.  The
  * workspace (orthogonalize_ns_workspace bytes, 16-byte aligned) is the
