@@ -40,7 +40,9 @@ struct Args {
     __bf16* out;
     int m, n, shares, chunks, cw, tall, vec;  // tall: out (and G) are X^T
     int64_t ldo, stride_o;
-    float alpha, a, b, c, last;  // S = alpha * sum; P = a + b S + c S S; out = last * X
+    // S = alpha * sum; P = a + b S + c S S; X' (or out) = next * P X, with X, S
+    // and P times their powers of two
+    float alpha, a, b, c, next;
 };
 
 constexpr int kRows = 64, kThreads = kRows * 4, kBlocks = kRows / 16, kFragments = kRows / 32;
@@ -204,9 +206,9 @@ __global__ void __launch_bounds__(kThreads) ns_narrow_step(const Args a)
         const int turned = (4 * h + (lane & 3)) * kPitch + wave * 16 + (lane & 12);
 #pragma unroll
         for (int j = 0; j < kBlocks; ++j) {
-            const f32x4 v = y[j] * *(const f32x4*)(ratio + j * 16 + 4 * h);
+            const f32x4 v = y[j] * (*(const f32x4*)(ratio + j * 16 + 4 * h) * a.next);
             if constexpr (LAST) {
-                const Elem<__bf16>::x4 w = round4<__bf16>(v * a.last);
+                const Elem<__bf16>::x4 w = round4<__bf16>(v);
                 typedef Elem<__bf16>::x4 out4;
                 if (a.tall)
                     *(out4*)(x + mine + j * 16) = w;  // rows of X^T

@@ -16,6 +16,13 @@
 // the bfloat16 result, 54 x 1286: 2.60e-3 without, 1.94e-3 with, 1.90e-3 with
 // an exact P; 40 x 4000: 3.13e-3, 2.27e-3, 2.28e-3.)
 //
+// Range.  X, S and P are each held times a power of two that brings the largest
+// entry they can have near 2^14 (Ranges), so that small ones, of rows and
+// columns far below the others, keep their bits: of 256 x 1024 of noise with a
+// row 10^-5 of the others that row is 1.9e-3 off, one of 10^-7 6e-3.  (With X
+// near sqrt(n) times its typical entry and S and P as they are 2.8e-2, and 1:
+// it came out as zero.)
+//
 // Matrices of at most 64 rows take one launch a step: ns_narrow.h.
 //
 // 4096 x 4096, five steps: 1255 us, 1095 TFLOP/s of what symmetry leaves: a step
@@ -137,7 +144,7 @@ __global__ void __launch_bounds__(256) ns_copy_out(const half* __restrict__ X, i
 enum { kAsIs = 1, kTurned = 2, kEights = 4 };
 
 // S (POLY false: alpha A A^T) or P (POLY true: alpha A A^T + beta A + gamma I,
-// A symmetric), [m, mp] with pitch ldc, tiles on and below the diagonal and
+// A symmetric), each times its power of two, [m, mp] with pitch ldc, tiles on and below the diagonal and
 // their transposes.
 template <bool POLY>
 struct SymmetricOp {
@@ -254,7 +261,7 @@ struct SymmetricOp {
 };
 
 // X' = P X [m, n] and its transpose [n, m] in binary16, or (LAST) the result
-// in bfloat16, times alpha, in out's layout: out's rows are X's (HOW has
+// in bfloat16, in out's layout, each times alpha: out's rows are X's (HOW has
 // kAsIs) or X^T's (kTurned).
 template <bool LAST, int HOW>
 struct ApplyOp {
@@ -313,7 +320,7 @@ struct ApplyOp {
         for (int i = 0; i < T::FM; ++i) {
             const float d16 = (float)(half)f[i];
             f[i] = __builtin_fabsf(d16) >= 0x1p-14f ? f[i] * __builtin_amdgcn_rcpf(d16) : 1.0f;
-            if constexpr (LAST) f[i] *= alpha;
+            f[i] *= alpha;
         }
         if constexpr (LAST) {
             __bf16* o = out + t.batch * stride_o;
@@ -395,10 +402,63 @@ int launch_symmetric(const OP& op, int64_t m, int64_t batch, float* partial, hip
         [=](OP& o, const Kind& k) { o.per = (int)per(k); }, stream);
 }
 
-// X is held times 2^k near sqrt(n), at most 2^12: an entry of an orthonormal X
-// is about 1 / sqrt(n), so entries (at most about 1.2 before the scale)
-// neither leave binary16's range nor its full precision.
-int scale_bits(int64_t n) { return std::min(12, (int)std::lround(0.5 * std::log2((double)n))); }
+// The powers of two of a step.  Singular values lie in 0 .. sigma, which is 1
+// at the start, |G|_F being at least the largest; no entry of X exceeds sigma,
+// none of S its square, none of P the polynomial's largest value there.  Each
+// is held times the 2^k that brings its bound to 2^14 at most and above 2^13:
+// binary16 ends at 2^16, so rounding has room, and below at 2^-24.  Of a
+// polynomial that could blow up values near 1 but is given smaller ones the
+// bounds say nothing: S and P are then held as they are, and X, whose typical
+// entry is 1 / sqrt(n) when it is orthonormal, times sqrt(n).
+struct Ranges {
+    double sigma = 1.0;
+    int least, x, s = 0, p = 0;
+    explicit Ranges(int64_t n) : least(std::min(12, (int)std::lround(0.5 * std::log2((double)n)))) { x = bits(sigma, least); }
+    static int bits(double bound, int least)
+    {
+        int e = 0;
+        const double m = std::frexp(std::max(bound, 1e-300), &e);
+        return std::min(60, std::max(least, 14 - (m == 0.5 ? e - 1 : e)));
+    }
+    // S and P of the step (a, b, c); leaves sigma and x for the next one
+    void step(double a, double b, double c)
+    {
+        const double u1 = sigma * sigma;
+        auto p_at = [=](double u) { return std::fabs(a + u * (b + u * c)); };
+        auto x_at = [=](double u) { return std::sqrt(u) * p_at(u); };
+        // the ends, and where the derivatives in u = sigma^2 are zero
+        double p_most = std::max(p_at(0), p_at(u1)), x_most = x_at(u1);
+        auto inside = [=](double u) { return u > 0 && u < u1; };
+        if (inside(-b / (2 * c))) p_most = std::max(p_most, p_at(-b / (2 * c)));
+        if (c == 0) {
+            if (inside(-a / (3 * b))) x_most = std::max(x_most, x_at(-a / (3 * b)));
+        } else {
+            const double root = std::sqrt(std::max(0.0, 9 * b * b - 20 * a * c));
+            for (double u : {(-3 * b + root) / (10 * c), (-3 * b - root) / (10 * c)})
+                if (inside(u)) x_most = std::max(x_most, x_at(u));
+        }
+        s = bits(u1, 0);
+        p = bits(p_most, 0);
+        sigma = std::min(x_most, 1e70);
+        x = bits(sigma, least);
+    }
+};
+
+// Factors of a step's products and sums, for X, S and P times their powers of two.
+struct Factors {
+    float s, c, b, a, next, out;  // S, S S, S and I in P; P X, as the next X and as the result
+    Factors(Ranges& r, const double* abc)
+    {
+        const int x = r.x;
+        r.step(abc[0], abc[1], abc[2]);
+        s = (float)std::ldexp(1.0, r.s - 2 * x);
+        c = (float)std::ldexp(abc[2], r.p - 2 * r.s);
+        b = (float)std::ldexp(abc[1], r.p - r.s);
+        a = (float)std::ldexp(abc[0], r.p);
+        next = (float)std::ldexp(1.0, r.x - r.p - x);
+        out = (float)std::ldexp(1.0, -r.p - x);
+    }
+};
 
 template <class E>
 int squares(const E* G, int64_t batch, int64_t rows, int64_t cols, int64_t ldg, int64_t stride_g, int vec, double* partial,
@@ -431,9 +491,8 @@ int run_narrow(const narrow::Plan& plan, const E* G, __bf16* out, int64_t batch,
     a.vec = (uintptr_t)out % 8 == 0 && ldo % 4 == 0 && stride_o % 4 == 0;
     a.ldo = ldo;
     a.stride_o = stride_o;
-    const double scale = std::ldexp(1.0, scale_bits(a.n));
-    a.alpha = (float)(1.0 / (scale * scale));
-    a.last = (float)(1.0 / scale);
+    Ranges ranges(a.n);
+    const double scale = std::ldexp(1.0, ranges.x);
     a.to = w.shares[0];
     hipLaunchKernelGGL((narrow::ns_narrow_begin<E>), dim3(grid), dim3(narrow::kThreads), 0, stream, a, G, ldg,
                        stride_g, w.partial, eps, scale);
@@ -441,9 +500,12 @@ int run_narrow(const narrow::Plan& plan, const E* G, __bf16* out, int64_t batch,
     for (int i = 0; i < steps; ++i) {
         a.from = w.shares[i & 1];
         a.to = w.shares[~i & 1];
-        a.a = (float)coefficients[3 * i];
-        a.b = (float)coefficients[3 * i + 1];
-        a.c = (float)coefficients[3 * i + 2];
+        const Factors f(ranges, coefficients + 3 * i);
+        a.alpha = f.s;
+        a.a = f.a;
+        a.b = f.b;
+        a.c = f.c;
+        a.next = i + 1 < steps ? f.next : f.out;
         if (i + 1 < steps)
             hipLaunchKernelGGL((narrow::ns_narrow_step<false>), dim3(grid), dim3(narrow::kThreads), 0, stream, a);
         else
@@ -467,7 +529,8 @@ int run(const E* G, __bf16* out, int64_t batch, int64_t rows, int64_t cols, int6
     const int64_t tr = pr / 64, tc = pc / 64;
     // (the products have no more tiles than that)
     if (!abi::good_grid(tr * tc * batch, 256)) return hipErrorInvalidValue;
-    const double scale = std::ldexp(1.0, scale_bits(w.n));
+    Ranges ranges(w.n);
+    const double scale = std::ldexp(1.0, ranges.x);
     int rc;
     const int vec = (uintptr_t)G % (4 * sizeof(E)) == 0 && ldg % 4 == 0 && stride_g % 4 == 0;
     if ((rc = squares(G, batch, rows, cols, ldg, stride_g, vec, w.partial, stream))) return rc;
@@ -484,6 +547,7 @@ int run(const E* G, __bf16* out, int64_t batch, int64_t rows, int64_t cols, int6
     }
     for (int i = 0; i < steps; ++i) {
         const int from = i & 1, to = from ^ 1;
+        const Factors f(ranges, coefficients + 3 * i);
         SymmetricOp<false> s = {};
         s.A = w.x[from];
         s.C = w.s;
@@ -494,7 +558,7 @@ int run(const E* G, __bf16* out, int64_t batch, int64_t rows, int64_t cols, int6
         s.mp = (int)w.mp;
         s.stride_a = w.stride_x;
         s.stride_c = w.stride_s;
-        s.alpha = (float)(1.0 / (scale * scale));
+        s.alpha = f.s;
         if ((rc = launch_symmetric(s, w.m, batch, w.sums, stream))) return rc;
         SymmetricOp<true> p = {};
         p.A = w.s;
@@ -504,9 +568,9 @@ int run(const E* G, __bf16* out, int64_t batch, int64_t rows, int64_t cols, int6
         p.K = p.mp = (int)w.mp;
         p.lda = p.ldc = (int)w.lm;
         p.stride_a = p.stride_c = w.stride_s;
-        p.alpha = (float)coefficients[3 * i + 2];
-        p.beta = (float)coefficients[3 * i + 1];
-        p.gamma = (float)coefficients[3 * i];
+        p.alpha = f.c;
+        p.beta = f.b;
+        p.gamma = f.a;
         if ((rc = launch_symmetric(p, w.m, batch, w.sums, stream))) return rc;
         auto apply = [&](auto op) {
             op.P = w.p;
@@ -525,7 +589,7 @@ int run(const E* G, __bf16* out, int64_t batch, int64_t rows, int64_t cols, int6
             op.stride_p = w.stride_s;
             op.stride_x = w.stride_x;
             op.stride_o = stride_o;
-            op.alpha = (float)(1.0 / scale);
+            op.alpha = i + 1 < steps ? f.next : f.out;
             return launch_grid<half>(op, w.m, w.n, 1, batch, op.K, w.sums, stream);
         };
         const bool eights = (uintptr_t)out % 16 == 0 && ldo % 8 == 0 && cols % 8 == 0 && stride_o % 8 == 0;

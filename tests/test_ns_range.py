@@ -1,10 +1,13 @@
 """Newton-Schulz at the ends of G's range: norms whose inverse 32 bits cannot
-hold, zero matrices, infinities."""
+hold, zero matrices, infinities, rows and columns far below the others, and
+polynomials that grow and shrink."""
 from __future__ import annotations
 
 import pytest
 import torch
 
+import _ns
+import _operators as plain
 import dense_fp16_gemm_04_amd as fw
 from test_operators import DEV, _built, normal, ns_close  # noqa: F401
 
@@ -57,3 +60,39 @@ def test_ns_of_infinities(shape):
     assert (out[~torch.isnan(out)] == 0).all()
     g[..., 1, 2] = float("nan")
     assert torch.isnan(fw.orthogonalize_ns(g, steps=0)).all()
+
+
+@pytest.mark.parametrize("line", ["row", "column"])
+@pytest.mark.parametrize("power", [-3, -5, -6, -7])
+@pytest.mark.parametrize("shape", [(256, 1024), (60, 1500), (900, 500)], ids=str)
+def test_ns_keeps_rows_and_columns_far_below_the_others(shape, power, line):
+    g = _ns.with_small(shape, line, power)
+    exact = plain.newton_schulz(g)
+    got = fw.orthogonalize_ns(g.to(DEV)).cpu()
+    pick = (lambda v: v[7]) if line == "row" else (lambda v: v[:, 7])
+    # a bfloat16 rounding and 1.45 times it in all; below 10^-6, where binary16
+    # ends (X's entries near 10^-7 / sqrt(rows * columns) times 2^14 are some
+    # forty of its smallest steps), two in a hundred
+    assert _ns.distance(pick(got), pick(exact)) <= (0.02 if power < -6 else 1.6 * 1.7e-3)
+
+
+@pytest.mark.parametrize("coefficients", [(1.5, -0.5, 0.0), (1.875, -1.25, 0.375), (0.01, 0.0, 0.0), (1.0, 0.0, 0.0),
+                                          (0.0, 1.0, 0.0), (-2.0, 0.5, 0.25), (0.5, 3.0, 0.0), (3.0, 4.0, 30.0),
+                                          (8.0, -20.0, 13.0)], ids=str)
+@pytest.mark.parametrize("shape", [(100, 300), (40, 900)], ids=str)
+def test_ns_of_other_polynomials(shape, coefficients):
+    """Growing, shrinking and unlike ones: each has its own ranges.  Of two the
+    bounds run away while these matrices' values stay small."""
+    g = _ns.noise(shape)
+    kw = dict(steps=2 if coefficients[0] == 0 else 3, coefficients=coefficients)
+    exact, host = plain.newton_schulz(g, **kw), _ns.held(g, **kw)
+    got = fw.orthogonalize_ns(g.to(DEV), **kw)
+    # a polynomial that blows values up past 65504 is outside what the operator
+    # holds, and says so
+    if not torch.isfinite(host).all():
+        assert not torch.isfinite(got).any()
+        return
+    assert torch.isfinite(got).all()
+    assert _ns.distance(got, exact) <= _ns.SAME * _ns.distance(host.bfloat16(), exact) + 2.0 ** -10
+    if coefficients == (1.0, 0.0, 0.0):
+        assert _ns.distance(got, exact) <= 1.2 * _ns.own_rounding(exact)
