@@ -226,7 +226,9 @@ def orthogonalize_ns(g, steps: int = 5, coefficients=(3.4445, -4.7750, 2.0315), 
     x = g / (|g|_F + eps), then ``steps`` times x = a x + (b s + c s s) x with
     s = x x^T.  ``coefficients`` is one triple (a, b, c), or one for each
     step.  g is float16, bfloat16 or float32; the iterates are held in
-    binary16, hence the bfloat16 result.
+    binary16, hence the bfloat16 result, whose error for noise is up to 1.4
+    times that of its rounding, and 5.6 times for singular values that fall off
+    to 10^-4 (``include/orthogonalize_ns.h``).
     """
     if not isinstance(g, torch.Tensor):
         raise TypeError("g must be a torch tensor")

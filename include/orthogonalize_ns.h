@@ -20,6 +20,14 @@
  * put back into the product's rows.  The result is therefore bfloat16,
  * whatever G's type.
  *
+ * Error, |out - exact|_F over |exact|_F, as a multiple of what rounding the
+ * exact result alone leaves (1.66e-3), five steps:
+ *   noise, sides from 1 to 9000                           1.05 to 1.4
+ *   256 x 1024, singular values that fall evenly in the
+ *   logarithm from 1 to 10^-1, 10^-2, 10^-4, 10^-6        1.2, 2.4, 5.6, 7.4
+ * The steps amplify small singular values by up to 3.4 each, and with them the
+ * rounding of the X that they are part of.
+ *
  * X, S and the polynomial are held times powers of two that use binary16's
  * range: rows and columns 10^-6 of the others are as near the exact result as
  * those, 10^-7 about 1% off.  With polynomials that blow values up past 65504
