@@ -245,6 +245,63 @@ __global__ void __launch_bounds__(kFewWaves * kWave, 2) gated_few(const GatedOp<
     }
 }
 
+// binary16 ends at 2^-24, and gradients often lie near it: dG and dU are
+// therefore held times a power of two that brings dH's largest finite entry to
+// 2^-4 .. 2^-3, which leaves them 2^19 upwards (P and Q are about 1) and, below,
+// full precision to 2^-11 of that entry; the products' epilogues take it out.
+// (dW's error for dH of 1e-5 and 1e-6, 512 rows: 2.8e-3 and 2.7e-2 without;
+// 3.0e-4 and 1.2e-3 with, of which its own rounding 2.2e-4 and 1.2e-3.)  bfloat16 has the range of 32 bits and needs none.
+template <class E>
+constexpr bool kScaled = false;
+template <>
+constexpr bool kScaled<_Float16> = true;
+constexpr int kMostBlocks = 1024;  // (8 MB of loads in flight)
+
+// Largest finite magnitudes of dH, one to a workgroup, as bits; and the factor
+// of products of nothing.
+struct Most {
+    const _Float16* dH;
+    int64_t lddh;
+    int T, F, vec;
+    uint32_t* most;
+    float* factor;
+
+    __device__ __forceinline__ void run(int id) const
+    {
+        if (T == 0 || F == 0) {
+            if (id == 0 && threadIdx.x == 0) *factor = 1.0f;
+            return;
+        }
+        uint32_t m = 0;
+        relayout::each_four(dH, lddh, T, F, vec, id, kMostBlocks, [&](const relayout::Four<_Float16>& v) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const uint32_t bits = __builtin_bit_cast(uint16_t, v[e]) & 0x7fffu;
+                m = max(m, bits < 0x7c00u ? bits : 0u);
+            }
+        });
+        for (int d = 32; d > 0; d >>= 1) m = max(m, (uint32_t)__shfl_xor((int)m, d));
+        __shared__ uint32_t part[4];
+        if (threadIdx.x % 64 == 0) part[threadIdx.x / 64] = m;
+        __syncthreads();
+        if (threadIdx.x == 0) most[id] = max(max(part[0], part[1]), max(part[2], part[3]));
+    }
+};
+
+// The power of two, the same in every workgroup of 256 threads.
+__device__ __forceinline__ int scale_of(const uint32_t* most, uint32_t (&part)[4])
+{
+    static_assert(kMostBlocks == 4 * relayout::kThreads, "four to a thread");
+    const u32x4 four = ((const u32x4*)most)[threadIdx.x];
+    uint32_t m = max(max(four[0], four[1]), max(four[2], four[3]));
+    for (int d = 32; d > 0; d >>= 1) m = max(m, (uint32_t)__shfl_xor((int)m, d));
+    if (threadIdx.x % 64 == 0) part[threadIdx.x / 64] = m;
+    __syncthreads();
+    m = max(max(part[0], part[1]), max(part[2], part[3]));
+    const float f = (float)__builtin_bit_cast(_Float16, (uint16_t)m);
+    return m ? -4 - ilogbf(f) : 0;
+}
+
 // dG = dH * P, dU = dH * Q for a 64 x 64 tile: row-major into rows of dGU
 // (dG at column 0, dU at column Fp), transposed into dGT and dUT (pitch Tp).
 // Rows and columns past the end, up to Tp and Fp, become zeros.
@@ -257,6 +314,8 @@ struct Slopes {
     E *dGU, *dGT, *dUT;
     int T, F, Fp, Tp, vec;
     int64_t lddh;
+    const uint32_t* most;  // (kScaled) of dH
+    float* factor;         // what takes the power of two out of the products
 
     __host__ __device__ int64_t tiles() const
     {
@@ -293,7 +352,15 @@ __device__ __forceinline__ void Slopes<E>::run(int id, E* tg, E* tu) const
         if (t0 + r < T) d = load4(dH + (int64_t)(t0 + r) * lddh, f0 + x * 4, F, vec);
         *(x4*)(tg + r * kPitch + x * 4) = d;
     }
-    __syncthreads();
+    float scale = 1.0f;
+    if constexpr (kScaled<E>) {
+        __shared__ uint32_t part[4];
+        const int k = scale_of(most, part);  // (meets the other waves)
+        scale = ldexpf(1.0f, k);
+        if (id == 0 && threadIdx.x == 0) *factor = ldexpf(1.0f, -k);
+    } else {
+        __syncthreads();
+    }
     const int row = wave * 16 + (lane & 15);
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
@@ -305,8 +372,8 @@ __device__ __forceinline__ void Slopes<E>::run(int id, E* tg, E* tu) const
             // (of a row or column that is not there P and Q may be anything:
             // an infinite weight times the zeros past the end is NaN)
             const bool there = t0 + row < T && f0 + j * 16 + 4 * (lane >> 4) + e < F;
-            vg[e] = (E)(there ? (float)d[e] * p[j][e] : 0.0f);
-            vu[e] = (E)(there ? (float)d[e] * q[j][e] : 0.0f);
+            vg[e] = (E)(there ? (float)d[e] * scale * p[j][e] : 0.0f);
+            vu[e] = (E)(there ? (float)d[e] * scale * q[j][e] : 0.0f);
         }
         *(x4*)(tg + at) = vg;  // (each element of dH is read by one lane, this one)
         *(x4*)(tu + at) = vu;
@@ -326,28 +393,43 @@ __device__ __forceinline__ void Slopes<E>::run(int id, E* tg, E* tu) const
     store_transposed(tu, dUT, Tp, t0, f0, Tp, F);
 }
 
-// All that the backward pass's products read, in one launch: the slopes and
-// up to three transposes, a 64 x 64 tile to a workgroup.
+// All that the backward pass's products read: the slopes and up to three
+// transposes, a 64 x 64 tile to a workgroup, in one launch.  In binary16 the
+// slopes wait for dH's largest entry, which a launch before theirs finds beside
+// the transposes (1000 x 1032 x 2730: 73 us for the whole pass, 76 in a launch of
+// its own and the rest in one, 66 in bfloat16).
 template <class E>
 struct Prepare {
+    Most most;
     Slopes<E> slopes;
     relayout::Transpose<E> turn[3];
-    int first[3];  // their first workgroups
+    int first[3];  // the transposes' first workgroups
 };
 
-template <class E>
+template <class E, bool SLOPES>
 __global__ void __launch_bounds__(relayout::kThreads) gated_prepare(const Prepare<E> p)
 {
     __shared__ E tiles[2][relayout::kTile * relayout::kPitch];
     const int id = blockIdx.x;
-    if (id < p.first[0])
-        p.slopes.run(id, tiles[0], tiles[1]);
-    else if (id < p.first[1])
+    if (id < p.first[0]) {
+        if constexpr (SLOPES)
+            p.slopes.run(id, tiles[0], tiles[1]);
+        else
+            p.most.run(id);
+    } else if (id < p.first[1]) {
         p.turn[0].run(id - p.first[0], tiles[0]);
-    else if (id < p.first[2])
+    } else if (id < p.first[2]) {
         p.turn[1].run(id - p.first[1], tiles[0]);
-    else
+    } else {
         p.turn[2].run(id - p.first[2], tiles[0]);
+    }
+}
+
+template <class E>
+__global__ void __launch_bounds__(relayout::kThreads) gated_slopes(const Slopes<E> slopes)
+{
+    __shared__ E tiles[2][relayout::kTile * relayout::kPitch];
+    slopes.run(blockIdx.x, tiles[0], tiles[1]);
 }
 
 // ------------------------------------------------------------------ host --
@@ -357,13 +439,14 @@ bool vec8(const void* p, int64_t ld) { return (uintptr_t)p % 16 == 0 && ld % 8 =
 // a result's rows take eight columns at a time
 bool eights(const void* p, int64_t cols, int64_t ld) { return vec8(p, ld) && cols % 8 == 0; }
 
-// C [M, N] = A B^T, all operands with K elements to a row; with a second A
-// and C, two products with the same B at once.
+// C [M, N] = A B^T (kScaled: times *factor), all operands with K
+// elements to a row; with a second A and C, two products with the same B at once.
 template <class E>
 int product(const E* A0, const E* A1, const E* B, E* C0, E* C1, int64_t M, int64_t N, int64_t K, int64_t ldc0, int64_t ldc1,
-            float* partial, hipStream_t stream)
+            const float* factor, float* partial, hipStream_t stream)
 {
     auto with = [&](auto op) {
+        op.factor = factor;
         op.A[0] = A0;
         op.A[1] = A1;
         op.B = B;
@@ -376,7 +459,7 @@ int product(const E* A0, const E* A1, const E* B, E* C0, E* C1, int64_t M, int64
         op.ldc[1] = (int)ldc1;
         return launch_grid<E>(op, M, N, 1, A1 ? 2 : 1, K, partial, stream);
     };
-    return eights(C0, N, ldc0) && (!A1 || eights(C1, N, ldc1)) ? with(StoreOp<E, true>{}) : with(StoreOp<E, false>{});
+    return eights(C0, N, ldc0) && (!A1 || eights(C1, N, ldc1)) ? with(StoreOp<E, true, kScaled<E>>{}) : with(StoreOp<E, false, kScaled<E>>{});
 }
 
 // Rows of what is copied, transposed or computed for the products start on 128
@@ -410,7 +493,8 @@ struct ForwardSpace {
 template <class E>
 struct BackwardSpace {
     E *wt, *xt, *dgu, *dgt, *dut;
-    float* partial;
+    float *partial, *factor;
+    uint32_t* most;
     int64_t Tp, Fp, bytes;
     BackwardSpace(void* base, int64_t T, int64_t D, int64_t F)
     {
@@ -423,6 +507,8 @@ struct BackwardSpace {
         dgt = c.take<E>(F * Tp);
         dut = c.take<E>(F * Tp);
         partial = std::max(2 * Fp, Tp) >= kSplitK ? c.take<float>(kSplitFloats) : nullptr;
+        factor = c.take<float>(1);
+        most = c.take<uint32_t>(kMostBlocks);
         bytes = c.used();
     }
 };
@@ -502,28 +588,37 @@ int backward(const E* dH, const E* X, const E* Wg, const E* Wu, const float* sav
     const BackwardSpace<E> w(workspace, T, D, F);
     int rc;
     Prepare<E> p = {};
-    p.slopes = {dH, saved, w.dgu, w.dgt, w.dut, (int)T, (int)F, (int)w.Fp, (int)w.Tp, (int)vec4(dH, lddh), lddh};
+    p.slopes = {dH, saved, w.dgu, w.dgt, w.dut, (int)T, (int)F, (int)w.Fp, (int)w.Tp, (int)vec4(dH, lddh), lddh,
+                w.most, w.factor};
     if (T > 0) {
         // [Wg; Wu]^T, D x 2 Fp, zeros between the two
         p.turn[0] = {Wg, w.wt, ldg, 2 * w.Fp, (int)F, (int)D, (int)w.Fp, (int)vec4(Wg, ldg)};
         p.turn[1] = {Wu, w.wt + w.Fp, ldu, 2 * w.Fp, (int)F, (int)D, (int)w.Fp, (int)vec4(Wu, ldu)};
     }
     if (F > 0) p.turn[2] = {X, w.xt, ldx, w.Tp, (int)T, (int)D, (int)w.Tp, (int)vec4(X, ldx)};
-    int64_t n = p.slopes.tiles();
+    const int64_t slopes = p.slopes.tiles();
+    int64_t n = kScaled<E> ? kMostBlocks : slopes;
     for (int i = 0; i < 3; ++i) {
         p.first[i] = (int)n;
         n += p.turn[i].tiles();
     }
-    if (!abi::good_grid(n, relayout::kThreads)) return hipErrorInvalidValue;  // (nothing is enqueued yet)
+    // (nothing is enqueued yet)
+    if (!abi::good_grid(std::max(n, slopes), relayout::kThreads)) return hipErrorInvalidValue;
+    if constexpr (kScaled<E>) p.most = {dH, lddh, (int)T, (int)F, p.slopes.vec, w.most, w.factor};
     if (n > 0) {
-        hipLaunchKernelGGL(gated_prepare<E>, dim3((unsigned)n), dim3(relayout::kThreads), 0, stream, p);
+        hipLaunchKernelGGL((gated_prepare<E, !kScaled<E>>), dim3((unsigned)n), dim3(relayout::kThreads), 0, stream, p);
         if ((rc = (int)hipGetLastError())) return rc;
     }
+    if constexpr (kScaled<E>)
+        if (slopes > 0) {
+            hipLaunchKernelGGL(gated_slopes<E>, dim3((unsigned)slopes), dim3(relayout::kThreads), 0, stream, p.slopes);
+            if ((rc = (int)hipGetLastError())) return rc;
+        }
     if (T > 0 && D > 0) {
-        if ((rc = product<E>(w.dgu, nullptr, w.wt, dX, nullptr, T, D, 2 * w.Fp, lddx, 0, w.partial, stream))) return rc;
+        if ((rc = product<E>(w.dgu, nullptr, w.wt, dX, nullptr, T, D, 2 * w.Fp, lddx, 0, w.factor, w.partial, stream))) return rc;
     }
     if (F > 0 && D > 0) {
-        if ((rc = product<E>(w.dgt, w.dut, w.xt, dWg, dWu, F, D, w.Tp, lddg, lddu, w.partial, stream))) return rc;
+        if ((rc = product<E>(w.dgt, w.dut, w.xt, dWg, dWu, F, D, w.Tp, lddg, lddu, w.factor, w.partial, stream))) return rc;
     }
     return hipSuccess;
 }

@@ -914,12 +914,13 @@ __device__ __forceinline__ void write_turned(Value value, const Rows& out, int l
     }
 }
 
-// C = A B^T.
-template <class E, bool EIGHTS>
+// C = A B^T; SCALED: times *factor.
+template <class E, bool EIGHTS, bool SCALED>
 struct StoreOp {
     static constexpr bool kPersist = true, kOblong = true, kSplit = true;  // (256 x 256, 256 x 128 tiles)
     const E *A[2], *B;  // one product, or two with the same B
     E* C[2];
+    const float* factor;
     int M, N, K, lda, ldb, ldc[2], tiles, tiles_m, tiles_n;
 
     template <int BM, int BN>
@@ -951,7 +952,10 @@ struct StoreOp {
     __device__ __forceinline__ void epilogue(const Tile& t, const f32x4 (&acc)[T::FM][T::FN], int lane, int wave,
                                              unsigned char* s0, unsigned char* s1) const
     {
-        write_rows<T, T::FN, EIGHTS>([&](int i, int j) { return round4<E>(acc[i][j]); },
+        // (from constant memory: a scalar register, of which 256 x 256 has some left)
+        float f = 1.0f;
+        if constexpr (SCALED) f = *(const __attribute__((address_space(4))) float*)factor;
+        write_rows<T, T::FN, EIGHTS>([&](int i, int j) { return round4<E>(SCALED ? acc[i][j] * f : acc[i][j]); },
                                      rows_at(t.batch ? C[1] : C[0], t.m0, M, T::BM, t.batch ? ldc[1] : ldc[0], t.n0, N), lane, wave, s0, s1);
     }
 };

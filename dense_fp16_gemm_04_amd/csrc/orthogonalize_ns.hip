@@ -48,36 +48,17 @@ using half4 = Elem<half>::x4;
 constexpr int kNormBlocks = 256;  // partial sums of squares per matrix
 
 // Partial sums of squares, in 64 bits (a 32-bit sum would overflow for
-// entries past 2^63 and lose small ones beside large ones).  Four elements of
-// a row at a time; `per`: groups of four to a row.
+// entries past 2^63 and lose small ones beside large ones).
 template <class E>
 __global__ void __launch_bounds__(256) ns_squares(const E* __restrict__ G, int64_t ldg, int64_t stride, int rows,
-                                                  int cols, int per, int vec, double* __restrict__ partial)
+                                                  int cols, int vec, double* __restrict__ partial)
 {
     const int b = blockIdx.x / kNormBlocks, k = blockIdx.x % kNormBlocks;
-    const E* g = G + b * stride;
     double s = 0;
-    // a workgroup takes pieces of 256 groups of a row, or several short rows
-    const int lanes = min(per, 256), step = 256 / lanes, pieces = (per + 255) / 256;
-    const int lane = threadIdx.x % lanes, first = threadIdx.x / lanes;
-    const int64_t units = first < step ? (int64_t)rows * pieces : 0;
-    using x4 = relayout::Four<E>;
-    const int64_t stride_u = (int64_t)kNormBlocks * step;
-    for (int64_t u0 = (int64_t)k * step + first; u0 < units; u0 += 4 * stride_u) {
-        x4 v[4];
+    relayout::each_four(G + b * stride, ldg, rows, cols, vec, k, kNormBlocks, [&](const relayout::Four<E>& v) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {  // (four loads in flight)
-            const int64_t u = u0 + i * stride_u;
-            const int64_t r = pieces == 1 ? u : u / pieces;
-            const int c = ((int)(u - r * pieces) * 256 + lane) * 4;
-            v[i] = x4{};
-            if (u < units) v[i] = relayout::load4(g + r * ldg, c, cols, vec);
-        }
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) s += (double)(float)v[i][e] * (double)(float)v[i][e];
-    }
+        for (int e = 0; e < 4; ++e) s += (double)(float)v[e] * (double)(float)v[e];
+    });
     __shared__ double part[256];
     part[threadIdx.x] = s;
     __syncthreads();
@@ -465,7 +446,7 @@ int squares(const E* G, int64_t batch, int64_t rows, int64_t cols, int64_t ldg, 
             hipStream_t stream)
 {
     hipLaunchKernelGGL(ns_squares<E>, dim3((unsigned)(batch * kNormBlocks)), dim3(256), 0, stream, G, ldg, stride_g,
-                       (int)rows, (int)cols, (int)((cols + 3) / 4), vec, partial);
+                       (int)rows, (int)cols, vec, partial);
     return (int)hipGetLastError();
 }
 

@@ -35,6 +35,33 @@ __device__ __forceinline__ Four<E> load4(const E* row, int c, int cols, bool vec
     return v;
 }
 
+// A matrix's elements by fours, workgroup `block` of `blocks` of 256 threads
+// taking its share: `each(v)` of all fours of a thread's (zeros past a row's
+// end), four loads in flight.
+template <class E, class Each>
+__device__ __forceinline__ void each_four(const E* src, int64_t lds_, int rows, int cols, bool vec, int block, int blocks,
+                                          Each each)
+{
+    // a workgroup takes pieces of 256 groups of a row, or several short rows
+    const int per = (int)(((int64_t)cols + 3) / 4), lanes = min(per, 256), step = 256 / lanes, pieces = (per + 255) / 256;
+    const int lane = threadIdx.x % lanes, first = threadIdx.x / lanes;
+    const int64_t units = first < step ? (int64_t)rows * pieces : 0;
+    const int64_t stride = (int64_t)blocks * step;
+    for (int64_t u0 = (int64_t)block * step + first; u0 < units; u0 += 4 * stride) {
+        Four<E> v[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int64_t u = u0 + i * stride;
+            const int64_t r = pieces == 1 ? u : u / pieces;
+            const int c = ((int)(u - r * pieces) * 256 + lane) * 4;
+            v[i] = Four<E>{};
+            if (u < units) v[i] = load4(src + r * lds_, c, cols, vec);
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) each(v[i]);
+    }
+}
+
 // Writes a 64 x 64 tile that LDS holds row-major (pitch kPitch) transposed:
 // dst[c][r] for tile row r and column c, whole rows of `rows` in groups of
 // eight bytes (dst's pitch is a multiple of 8; rows past `rows_valid` hold

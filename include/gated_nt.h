@@ -26,6 +26,12 @@
  * gradients' error; in the operands' type each would add as much as the
  * final rounding does.
  *
+ * The rounding of dG and dU adds about as much to a gradient's error as its own
+ * rounding (sqrt 2 of it in all).  In binary16 they are held times a power of
+ * two that follows dH's largest finite entry, so this holds for dH of any size;
+ * entries of dG and dU below 2^-11 of dH's largest lose bits, and ones above
+ * 2^19 times it overflow.
+ *
  * Ownership, concurrency, errors and capture are those of gemm_nt_f16.h: the
  * caller owns every buffer, calls enqueue on `stream` and return a hipError_t
  * as int.  A call that needs a workspace takes it from the caller
