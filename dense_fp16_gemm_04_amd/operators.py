@@ -7,6 +7,8 @@ C ABIs of ``include/gated_nt.h``, ``include/orthogonalize_ns.h`` and
 libraries' HIP kernels, a missing library raises ``RuntimeError`` and a
 refused call ``TypeError``, ``ValueError`` or ``GemmError``.  Nothing here
 takes part in autograd: a training step calls the backward function itself.
+A new result of inputs that require gradients raises when they are asked of it
+(results in ``out`` and those of the training pair are the caller's affair).
 
 Matrices may be views: the elements of a row are adjacent, rows may lie any
 distance apart that does not make them overlap.
@@ -116,6 +118,26 @@ def _workspace(like, nbytes):
     return w, w.data_ptr()
 
 
+class _NoGradients(torch.autograd.Function):
+    """The result of a call, of which no gradient can be had."""
+
+    @staticmethod
+    def forward(ctx, message, result, *inputs):
+        ctx.message = message
+        return result[0]  # (in a tuple: not an input itself)
+
+    @staticmethod
+    def backward(ctx, grad):
+        raise RuntimeError(ctx.message)
+
+
+def _without_gradients(result, message, *inputs):
+    """`result` as it is, or one whose backward pass raises where autograd would have to go on to `inputs`."""
+    if torch.is_grad_enabled() and any(t.requires_grad for t in inputs if t is not None):
+        return _NoGradients.apply(message, (result,), *inputs)
+    return result
+
+
 def _call(library, name, device, *args):
     """Call an entry point on `device` and its current stream (the last argument)."""
     fn = getattr(load(library), name)
@@ -172,16 +194,22 @@ def gated_nt(x, w_gate, w_up, activation: str = "silu", out=None):
 
     float16 or bfloat16; ``activation`` is "silu" or "gelu_tanh".  Sums,
     activation and product in 32 bits, rounded once.  Enqueued on the current
-    stream of x's device; returns ``out``.
+    stream of x's device; returns ``out``.  Not differentiated by autograd:
+    ``gated_nt_train`` and ``gated_nt_backward`` are its training form.
     """
-    return _gated(x, w_gate, w_up, activation, out, False)[0]
+    h = _gated(x, w_gate, w_up, activation, out, False)[0]
+    if out is None and (x.requires_grad or w_gate.requires_grad or w_up.requires_grad):
+        return _without_gradients(
+            h, "gated_nt has no gradients in autograd: use gated_nt_train and gated_nt_backward", x, w_gate, w_up)
+    return h
 
 
 def gated_nt_train(x, w_gate, w_up, activation: str = "silu", out=None):
     """``gated_nt`` that also keeps what its backward pass reads: (out, saved).
 
     ``saved`` (8 bytes per output, 32-bit values in the library's own layout)
-    is for ``gated_nt_backward`` with the same x and weights.
+    is for ``gated_nt_backward`` with the same x and weights.  Neither requires
+    gradients, whatever the inputs do.
     """
     return _gated(x, w_gate, w_up, activation, out, True)
 
@@ -253,7 +281,8 @@ def orthogonalize_ns(g, steps: int = 5, coefficients=(3.4445, -4.7750, 2.0315), 
 
     ldg = _pitch("g", first(g), _TYPES_AND_F32)
     device = g.get_device()
-    if out is None:
+    new = out is None
+    if new:
         out = g.new_empty(g.shape, dtype=torch.bfloat16)
     if not isinstance(out, torch.Tensor) or out.shape != g.shape:
         raise ValueError("out must be a bfloat16 tensor of g's shape %s" % (tuple(g.shape),))
@@ -271,6 +300,8 @@ def orthogonalize_ns(g, steps: int = 5, coefficients=(3.4445, -4.7750, 2.0315), 
     flat = (ctypes.c_double * max(1, 3 * steps))(*(v for c in triples for v in c))
     _call("orthogonalize_ns", "orthogonalize_ns", device, g.data_ptr(), out.data_ptr(), batch, rows, cols, ldg, stride_g,
           ldo, stride_o, _TYPES_AND_F32[g.dtype], steps, flat, eps, workspace, nbytes)
+    if new and g.requires_grad:
+        return _without_gradients(out, "orthogonalize_ns has no gradients in autograd", g)
     return out
 
 
@@ -305,11 +336,14 @@ def gemv_w4(x, q, scales, zeros=None, out=None):
     group = K // groups if groups and K % groups == 0 else 0
     if K and (group == 0 or ((group < 32 or group & (group - 1)) and group != K)):
         raise ValueError("K / scales.shape[1] must be a power of two from 32 on, or K: got %d / %d" % (K, groups))
-    if out is None:
+    new = out is None
+    if new:
         out = x.new_empty((M, N))
         ldy = N
     else:
         ldy = _pitch("out", out, types, device, (M, N))
     _call("gemv_w4", "gemv_w4", device, x.data_ptr(), pq, scales.data_ptr(), None if zeros is None else zeros.data_ptr(),
           out.data_ptr(), M, N, K, group, ldx, ldq if N > 1 else half, ldy, _TYPES[x.dtype])
+    if new and (x.requires_grad or scales.requires_grad or (zeros is not None and zeros.requires_grad)):
+        return _without_gradients(out, "gemv_w4 has no gradients in autograd", x, scales, zeros)
     return out
