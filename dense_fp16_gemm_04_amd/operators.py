@@ -276,8 +276,8 @@ def orthogonalize_ns(g, steps: int = 5, coefficients=(3.4445, -4.7750, 2.0315), 
     batch = g.shape[0] if g.dim() == 3 else 1
     rows, cols = g.shape[-2:]
 
-    def first(t):  # one matrix of the batch (of an empty one: any of its shape)
-        return t if t.dim() == 2 else t[0] if t.shape[0] else t.new_empty(rows, cols)
+    def first(t):  # one matrix of the batch (of an empty one: none of its rows)
+        return t if t.dim() == 2 else t[0] if t.shape[0] else t.new_empty(0, cols)
 
     ldg = _pitch("g", first(g), _TYPES_AND_F32)
     device = g.get_device()
@@ -286,7 +286,7 @@ def orthogonalize_ns(g, steps: int = 5, coefficients=(3.4445, -4.7750, 2.0315), 
         out = g.new_empty(g.shape, dtype=torch.bfloat16)
     if not isinstance(out, torch.Tensor) or out.shape != g.shape:
         raise ValueError("out must be a bfloat16 tensor of g's shape %s" % (tuple(g.shape),))
-    ldo = _pitch("out", first(out), (torch.bfloat16,), device, (rows, cols))
+    ldo = _pitch("out", first(out), (torch.bfloat16,), device)
     if g.numel() == 0:
         return out
     stride_g, stride_o = (t.stride(0) if t.dim() == 3 and batch > 1 else 0 for t in (g, out))
