@@ -268,7 +268,7 @@ def orthogonalize_ns(g, steps: int = 5, coefficients=(3.4445, -4.7750, 2.0315), 
     eps = float(eps)
     if not eps >= 0:
         raise ValueError("eps must not be negative, got %r" % eps)
-    coefficients = list(coefficients)
+    coefficients = coefficients.tolist() if hasattr(coefficients, "tolist") else list(coefficients)
     triples = [tuple(float(v) for v in c) for c in coefficients] if coefficients and hasattr(coefficients[0], "__len__") \
         else [tuple(float(v) for v in coefficients)] * steps
     if len(triples) != steps or any(len(c) != 3 for c in triples):

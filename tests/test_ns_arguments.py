@@ -1,10 +1,25 @@
-"""Newton-Schulz's Python arguments: empty batches of any shape."""
+"""Newton-Schulz's Python arguments: coefficients in any container, empty batches of any shape."""
 from __future__ import annotations
 
+import numpy as np
 import pytest
 import torch
 
 import dense_fp16_gemm_04_amd as fw
+
+TRIPLE = (3.4445, -4.7750, 2.0315)
+
+
+@pytest.mark.parametrize("of", [tuple, list, np.array, torch.tensor, iter], ids=str)
+def test_ns_takes_coefficients_in_any_container(of):
+    """They are accepted: what is refused is a matrix in host memory."""
+    for coefficients in (TRIPLE, [TRIPLE] * 3):
+        with pytest.raises(ValueError, match="GPU"):
+            fw.orthogonalize_ns(torch.zeros(4, 4), steps=3, coefficients=of(coefficients))
+    for coefficients in (TRIPLE[:2], [TRIPLE] * 2):
+        with pytest.raises(ValueError, match="coefficients"):
+            fw.orthogonalize_ns(torch.zeros(4, 4), steps=3, coefficients=of(coefficients))
+
 
 @pytest.mark.gpu
 def test_ns_of_an_empty_batch_takes_no_memory():
@@ -19,3 +34,13 @@ def test_ns_of_an_empty_batch_takes_no_memory():
         fw.orthogonalize_ns(g.double())
     with pytest.raises(TypeError):
         fw.orthogonalize_ns(g, out=g)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("of", [np.array, torch.tensor], ids=str)
+def test_ns_results_with_coefficients_of_a_container(of):
+    g = torch.randn(40, 70, generator=torch.Generator().manual_seed(1)).to("cuda:0")
+    assert torch.equal(fw.orthogonalize_ns(g, coefficients=of(TRIPLE)).float().isfinite(), torch.ones_like(g, dtype=bool))
+    per_step = [(4.0, -6.0, 3.0), (3.0, -3.5, 1.5)]
+    assert torch.equal(fw.orthogonalize_ns(g, steps=2, coefficients=of(per_step)),
+                       fw.orthogonalize_ns(g, steps=2, coefficients=per_step))
