@@ -15,7 +15,9 @@
 //
 // Five steps of 64 x 64, 256, 1024, 4096 and 8192, one matrix: 34, 34, 41, 60
 // and 82 us, as three launches a step 64, 66, 74, 126 and 105; of 32 x 64: 32
-// and 58.  With 128 rows the same scheme took 64 us for 256 columns and 87 for
+// and 58.  Longer ones, 64 x 16384, 65536, 262144 and 1048576: 100, 183, 422 and
+// 962, and 117, 228, 646 and 4116; sixteen of 64 x 16384 193 and 293, 64 of 64 x
+// 65536 2847 and 3901.  With 128 rows the same scheme took 64 us for 256 columns and 87 for
 // 1024, the three launches 65 and 78: repeating P costs what the launches did.
 #ifndef DENSE_FP16_GEMM_NS_NARROW_H
 #define DENSE_FP16_GEMM_NS_NARROW_H
@@ -250,11 +252,11 @@ __global__ void __launch_bounds__(kThreads) ns_narrow_step(const Args a)
 
 // The layout of the work, by the sizes of one matrix.
 struct Plan {
-    bool used = false;  // or the tiled products, which are faster past these sizes
+    bool used = false;  // or the tiled products, which are faster for more rows
     int64_t shares = 0, chunks = 0, cw = 1;
     Plan(int64_t m, int64_t n)
     {
-        if (m > kRows || n > 8192) return;
+        if (m > kRows) return;
         used = true;
         chunks = (n + kRows - 1) / kRows;
         // a step reads all shares and walks cw chunks, each of which takes

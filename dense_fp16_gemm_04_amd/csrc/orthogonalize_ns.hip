@@ -456,7 +456,7 @@ int run_narrow(const narrow::Plan& plan, const E* G, __bf16* out, int64_t batch,
                void* workspace, hipStream_t stream)
 {
     const NarrowSpace w(workspace, batch, plan);
-    const unsigned grid = (unsigned)(batch * plan.shares);  // (below 2^16 * 2^8)
+    const unsigned grid = (unsigned)(batch * plan.shares);  // (no more than 64 x 64 tiles)
     const int vec = (uintptr_t)G % (4 * sizeof(E)) == 0 && ldg % 4 == 0 && stride_g % 4 == 0;
     int rc = squares(G, batch, rows, cols, ldg, stride_g, vec, w.partial, stream);
     if (rc) return rc;
@@ -500,16 +500,16 @@ template <class E>
 int run(const E* G, __bf16* out, int64_t batch, int64_t rows, int64_t cols, int64_t ldg, int64_t stride_g, int64_t ldo,
         int64_t stride_o, int32_t steps, const double* coefficients, double eps, void* workspace, hipStream_t stream)
 {
+    const int64_t pr = abi::up(rows, kLine), pc = abi::up(cols, kLine);
+    const int64_t tr = pr / 64, tc = pc / 64;
+    // (no launch here has more workgroups than that)
+    if (!abi::good_grid(tr * tc * batch, 256)) return hipErrorInvalidValue;
     const narrow::Plan plan(std::min(rows, cols), std::max(rows, cols));
     if (plan.used && steps > 0)
         return run_narrow(plan, G, out, batch, rows, cols, ldg, stride_g, ldo, stride_o, steps, coefficients, eps,
                                  workspace, stream);
     const Space w(workspace, batch, rows, cols);
     const bool tall = rows > cols;
-    const int64_t pr = abi::up(rows, kLine), pc = abi::up(cols, kLine);
-    const int64_t tr = pr / 64, tc = pc / 64;
-    // (the products have no more tiles than that)
-    if (!abi::good_grid(tr * tc * batch, 256)) return hipErrorInvalidValue;
     Ranges ranges(w.n);
     const double scale = std::ldexp(1.0, ranges.x);
     int rc;

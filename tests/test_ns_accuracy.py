@@ -52,6 +52,19 @@ def test_ns_is_as_near_the_exact_iteration_as_documented(shape, t):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("shape", [(64, 16500), (33, 100001), (150000, 5), (1, 70000), (3, 20, 20000)], ids=str)
+def test_ns_of_few_long_rows(shape):
+    """Sixty-four rows or fewer, of any length."""
+    g = _ns.noise(shape)
+    got = fw.orthogonalize_ns(g.to(DEV)).cpu()
+    for a, b in zip(g if g.dim() == 3 else [g], got if g.dim() == 3 else [got]):
+        exact, host = plain.newton_schulz(a), _ns.held(a)
+        plain.assert_within(b, exact, _ns.entry_bound(exact, host))
+        assert _ns.distance(b, exact) <= _ns.SAME * _ns.distance(host.bfloat16(), exact)
+    assert torch.equal(got, fw.orthogonalize_ns(g.to(DEV)).cpu())
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("shape", [(1100, 2900), (2, 520, 2000), (9, 1024, 1280)], ids=str)
 def test_ns_large_is_as_near_the_exact_iteration_as_documented(shape):
     """Two steps (the host's 64-bit products take long)."""

@@ -44,3 +44,13 @@ def test_ns_results_with_coefficients_of_a_container(of):
     per_step = [(4.0, -6.0, 3.0), (3.0, -3.5, 1.5)]
     assert torch.equal(fw.orthogonalize_ns(g, steps=2, coefficients=of(per_step)),
                        fw.orthogonalize_ns(g, steps=2, coefficients=per_step))
+
+
+def test_ns_of_too_many_few_long_rows_is_refused():
+    """More than 2^32 threads, of sixty-four rows or fewer."""
+    from test_operators_host import INVALID, ns_args
+    from dense_fp16_gemm_04_amd import operators
+    far, n, batch = 1 << 50, (1 << 21) - 64, (1 << 16) - 1
+    lib = operators.load("orthogonalize_ns")
+    assert lib.orthogonalize_ns(*ns_args(G=far, out=3 * far, rows=2, cols=n, ldg=n, ldo=n, stride_g=2 * n, stride_o=2 * n,
+                                         batch=batch, ws=5 * far, ws_bytes=1 << 60)) == INVALID
