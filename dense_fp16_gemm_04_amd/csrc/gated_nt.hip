@@ -63,7 +63,7 @@ constexpr int kBlockFloats = 512;
 
 template <class E, bool SAVE, bool EIGHTS>
 struct GatedOp {
-    static constexpr bool kPersist = true, kOblong = true, kSplit = false;
+    static constexpr bool kPersist = true, kSplit = false;
     const E *X, *Wg, *Wu;
     E* H;
     float* saved;

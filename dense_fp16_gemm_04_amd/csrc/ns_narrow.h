@@ -103,11 +103,10 @@ ns_narrow_begin(const Args a, const E* __restrict__ G, int64_t ldg, int64_t stri
     __shared__ double part[4];
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid / 64);
     const int b = blockIdx.x / a.shares, share = blockIdx.x % a.shares;
-    if (wave < 4) {
-        double s = partial[b * 256 + tid];
-        for (int d = 32; d > 0; d >>= 1) s += __shfl_xor(s, d);
-        if (lane == 0) part[wave] = s;
-    }
+    static_assert(kThreads == 256, "one partial sum per thread");
+    double s = partial[b * 256 + tid];
+    for (int d = 32; d > 0; d >>= 1) s += __shfl_xor(s, d);
+    if (lane == 0) part[wave] = s;
     __syncthreads();
     const Factor f(part, eps, scale);
     const E* g = G + b * stride_g;

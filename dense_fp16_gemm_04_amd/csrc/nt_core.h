@@ -917,7 +917,7 @@ __device__ __forceinline__ void write_turned(Value value, const Rows& out, int l
 // C = A B^T; SCALED: times *factor.
 template <class E, bool EIGHTS, bool SCALED>
 struct StoreOp {
-    static constexpr bool kPersist = true, kOblong = true, kSplit = true;  // (256 x 256, 256 x 128 tiles)
+    static constexpr bool kPersist = true, kSplit = true;
     const E *A[2], *B;  // one product, or two with the same B
     E* C[2];
     const float* factor;

@@ -86,9 +86,9 @@ int launch_ordered(const OP& op, int tiles, int rest, int parts, float* partial,
 }
 
 // Runs OP over `count(kind)` tiles with the kernel that the model finds
-// fastest.  256 x 256 tiles need three K
-// steps and an OP that offers them (kPersist); a split needs `partial`
-// (kSplitFloats floats).
+// fastest.  256 x 256 tiles need three K steps and an OP that offers them
+// (kPersist); a split needs `partial` (kSplitFloats floats) and one that offers
+// it (kSplit).
 template <class E, class OP, class Count, class Prepare>
 int launch(OP op, int64_t K, float* partial, Count count, Prepare prepare, hipStream_t stream)
 {
@@ -98,7 +98,6 @@ int launch(OP op, int64_t K, float* partial, Count count, Prepare prepare, hipSt
     double best_us = 0;
     for (int i = 0; i < kNumKinds; ++i) {
         if (i == 0 && (!OP::kPersist || K <= 128)) continue;
-        if (i == 1 && !OP::kOblong) continue;
         const int64_t n = count(kKinds[i]);
         if (!abi::good_grid(n, i == 1 || i == 2 ? 512 : 256)) continue;
         const double us = model_us(kKinds[i], n, K, cus);
@@ -109,7 +108,7 @@ int launch(OP op, int64_t K, float* partial, Count count, Prepare prepare, hipSt
             parts = 1;
         }
         int p = 1;
-        const double split = (i == 2 || (i == 1 && OP::kOblong)) && partial ? split_us(kKinds[i], n, K, cus, p) : -1;
+        const double split = (i == 1 || i == 2) && partial ? split_us(kKinds[i], n, K, cus, p) : -1;
         if (split > 0 && split < best_us) {
             best = i;
             best_us = split;
@@ -125,10 +124,9 @@ int launch(OP op, int64_t K, float* partial, Count count, Prepare prepare, hipSt
         if (best == 0)
             hipLaunchKernelGGL((nt_persist<Shape256<E>, OP>), dim3((unsigned)std::min<int64_t>(tiles, cus)), dim3(256),
                                0, stream, op);
-    if constexpr (OP::kOblong)
-        if (best == 1)
-            return launch_ordered<Shape<E, 256, 128, 4, 2, 3, 1, 4>>(op, (int)tiles, (int)(tiles % cus), parts, partial,
-                                                                     stream);
+    if (best == 1)
+        return launch_ordered<Shape<E, 256, 128, 4, 2, 3, 1, 4>>(op, (int)tiles, (int)(tiles % cus), parts, partial,
+                                                                 stream);
     if (best == 2)
         return launch_ordered<Shape<E, 128, 128, 2, 4, 3, 1, 4>>(op, (int)tiles, (int)(tiles % cus), parts, partial,
                                                                  stream);

@@ -129,7 +129,7 @@ enum { kAsIs = 1, kTurned = 2, kEights = 4 };
 // their transposes.
 template <bool POLY>
 struct SymmetricOp {
-    static constexpr bool kPersist = !POLY, kOblong = true, kSplit = true;  // (P's epilogue would spill there)
+    static constexpr bool kPersist = !POLY, kSplit = true;  // (P's epilogue would spill there)
     const half* A;
     half* C;
     float* diag;  // (POLY) C's diagonal before it is rounded
@@ -247,7 +247,7 @@ struct SymmetricOp {
 template <bool LAST, int HOW>
 struct ApplyOp {
     // (element by element, the 256 x 256 kernel would spill scalar registers)
-    static constexpr bool kPersist = (HOW & kEights) != 0, kOblong = true, kSplit = true;
+    static constexpr bool kPersist = (HOW & kEights) != 0, kSplit = true;
     const half *P, *Xt;
     const float* diag;  // P's diagonal before it was rounded
     half *X, *XtNew;
