@@ -12,10 +12,10 @@
 // terms to a sum, and dWg, dWu are two of one shape over T, all in NT form on
 // transposed copies of X and of the weights.
 //
-// Measured (binary16 forward 4096 x 4096 x 8192: 371 us, 1482 TFLOP/s, the
-// matrix cores busy 87% of the cycles; bfloat16 step 8192 x 4096 x 8192: 2473
-// us, 1334 TFLOP/s, of which the forward pass 865, the gradients' operands 300
-// to 345 at 5.4 TB/s, the two products 788 each).
+// Measured: binary16 forward 4096 x 4096 x 8192, 371 to 401 us on four boxes (1480
+// to 1370 TFLOP/s, the matrix cores busy 87% of the cycles).  bfloat16 step 8192 x
+// 4096 x 8192, 2473 to 2586 us on as many; 2584 of one trace are the forward pass
+// 798, the gradients' operands 344 at 4.7 TB/s, and the two products 721 each.
 #include "gated_nt.h"
 
 #include <algorithm>
@@ -248,7 +248,7 @@ __global__ void __launch_bounds__(kFewWaves * kWave, 2) gated_few(const GatedOp<
 // binary16 ends at 2^-24, and gradients often lie near it: dG and dU are
 // therefore held times a power of two that brings dH's largest finite entry to
 // 2^-4 .. 2^-3, which leaves them 2^19 upwards (P and Q are about 1) and, below,
-// full precision to 2^-11 of that entry; the products' epilogues take it out.
+// full precision to 2^-10 of that entry; the products' epilogues take it out.
 // (dW's error for dH of 1e-5 and 1e-6, 512 rows: 2.8e-3 and 2.7e-2 without;
 // 3.0e-4 and 1.2e-3 with, of which its own rounding 2.2e-4 and 1.2e-3.)  bfloat16 has the range of 32 bits and needs none.
 template <class E>

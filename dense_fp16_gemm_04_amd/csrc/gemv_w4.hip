@@ -25,8 +25,8 @@
 // with the zero point.  One mask gives codes i and i + 4 of a word as a pair,
 // so x's pairs are put in that order too.
 //
-// One row by 16384 x 16384: 34.5 us, 3.9 TB/s of codes (41 with zero points, 48
-// in bfloat16); by 8192 x 4096 7.0 us, less than the call takes on the host.
+// One row by 16384 x 16384: 34 us, 3.9 TB/s of codes (39 with zero points, 36
+// in bfloat16); by 8192 x 4096 7.3 us, less than the call takes on the host.
 //
 // With x as the first operand of v_mfma_f32_16x16x32, lane l's four results
 // belong to row l % 16 of W and rows 4 h .. 4 h + 3 of X: one scale per lane.
@@ -373,10 +373,10 @@ gemv_w4_kernel(const E* __restrict__ X, const unsigned char* __restrict__ Q, con
 // x 4096, binary16.)
 //
 // Bound by a block's chain and the vector instructions that unpack codes and
-// apply scales: 256 rows by 4096 x 4096 take 22 us (24 in bfloat16, whose
+// apply scales: 256 rows by 4096 x 4096 take 21 us (24 in bfloat16, whose
 // offset needs the sums of x), 128 rows, half as many workgroups, 21; the
-// matrix cores are busy 31% of that.  512 rows by 8192 x 8192: 110 us, 624
-// TFLOP/s, as FN is 2; 165 in bfloat16.
+// matrix cores are busy 31% of that.  512 rows by 8192 x 8192: 105 us, 655
+// TFLOP/s, as FN is 2; 174 in bfloat16.
 //
 // The codes are the first operand here: lane l's four results belong to row
 // l % 16 of x and rows 4 h .. 4 h + 3 of W, eight adjacent bytes of Y.

@@ -29,7 +29,7 @@
  * The rounding of dG and dU adds about as much to a gradient's error as its own
  * rounding (sqrt 2 of it in all).  In binary16 they are held times a power of
  * two that follows dH's largest finite entry, so this holds for dH of any size;
- * entries of dG and dU below 2^-11 of dH's largest lose bits, and ones above
+ * entries of dG and dU below 2^-10 of dH's largest lose bits, and ones above
  * 2^19 times it overflow.
  *
  * Ownership, concurrency, errors and capture are those of gemm_nt_f16.h: the
@@ -53,6 +53,10 @@
  * 16 bytes at a time: an operand whose pointer is not 16-byte aligned or
  * whose pitch or D is no multiple of 8 is first copied into the workspace
  * (all such in one launch; 160 x 539 x 1434: 14 us, and 10 with D = 544).
+ * Copied weights cross memory three times, which is most of the time of a few
+ * rows: one row by 8192 x 4097 takes 87 us and a workspace of 136 MB, by 8192 x
+ * 4096 30 us and none.  The backward pass lays out both weights anew whatever T
+ * is (one row by 8192 x 4096: 136 us).
  */
 #ifndef GATED_NT_H
 #define GATED_NT_H

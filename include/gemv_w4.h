@@ -41,7 +41,7 @@
  *
  * Any 2-byte aligned X is accepted, but rows of it that do not start on 16
  * bytes are read element by element, 16 at a time (4096 x 4096 weights, 16
- * and 64 rows: 23 and 83 us, and 10 and 10 for aligned ones).
+ * and 64 rows: 21 and 77 us, and 8 and 11 for aligned ones).
  */
 #ifndef GEMV_W4_H
 #define GEMV_W4_H
