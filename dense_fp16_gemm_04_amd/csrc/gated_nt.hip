@@ -12,7 +12,7 @@
 // terms to a sum, and dWg, dWu are two of one shape over T, all in NT form on
 // transposed copies of X and of the weights.
 //
-// Measured: binary16 forward 4096 x 4096 x 8192, 371 to 401 us on four boxes (1480
+// Measured: binary16 forward 4096 x 4096 x 8192, 371 to 401 us on four MI355X (1480
 // to 1370 TFLOP/s, the matrix cores busy 87% of the cycles).  bfloat16 step 8192 x
 // 4096 x 8192, 2473 to 2586 us on as many; 2584 of one trace are the forward pass
 // 798, the gradients' operands 344 at 4.7 TB/s, and the two products 721 each.

@@ -26,7 +26,7 @@
 // Matrices of at most 64 rows take one launch a step: ns_narrow.h.
 //
 // 4096 x 4096, five steps: 1375 us, 1000 TFLOP/s of what symmetry leaves (1255 on
-// the fastest box): a step is S 71 + 7.5 us, P 73 + 8 (tiles, and joining the last
+// the fastest of four MI355X): a step is S 71 + 7.5 us, P 73 + 8 (tiles, and joining the last
 // wave's split sums), X' 108 and the last one 103; sums of squares and X 41.  256 x
 // 256: 70 us, seventeen launches of 3 to 5.
 #include "orthogonalize_ns.h"

@@ -96,3 +96,20 @@ def test_ns_of_other_polynomials(shape, coefficients):
     assert _ns.distance(got, exact) <= _ns.SAME * _ns.distance(host.bfloat16(), exact) + 2.0 ** -10
     if coefficients == (1.0, 0.0, 0.0):
         assert _ns.distance(got, exact) <= 1.2 * _ns.own_rounding(exact)
+
+
+@pytest.mark.parametrize("power, off", [(-5, 1.6 * 1.7e-3), (-6, 8e-3), (-7, 0.08)])
+def test_ns_keeps_rows_of_a_large_matrix_as_documented(power, off):
+    """4096 x 4096, whose entries are near 2^-12: one of a row 10^-7 of the others
+    is 2^14 * 2^-12 * 10^-7 = 4e-7, seven of binary16's smallest steps, which round
+    it by 0.29 of one on average (4%; 0.4% for 10^-6), and the steps after it,
+    of entries that have grown, by less."""
+    g = normal(4096, 4096, seed=6)
+    g[7] *= 10.0 ** power
+    x = g.double()
+    x = x / (x.norm() + 1e-7)
+    a, b, c = _ns.MUON
+    for _ in range(5):
+        s = x @ x.T
+        x = a * x + (b * s + c * (s @ s)) @ x
+    assert _ns.distance(fw.orthogonalize_ns(g)[7], x[7].cpu()) <= off
