@@ -250,7 +250,8 @@ __global__ void __launch_bounds__(kFewWaves * kWave, 2) gated_few(const GatedOp<
 // 2^-4 .. 2^-3, which leaves them 2^19 upwards (P and Q are about 1) and, below,
 // full precision to 2^-10 of that entry; the products' epilogues take it out.
 // (dW's error for dH of 1e-5 and 1e-6, 512 rows: 2.8e-3 and 2.7e-2 without;
-// 3.0e-4 and 1.2e-3 with, of which its own rounding 2.2e-4 and 1.2e-3.)  bfloat16 has the range of 32 bits and needs none.
+// 3.0e-4 and 1.2e-3 with, of which its own rounding 2.2e-4 and 1.2e-3.)
+// bfloat16 has the range of 32 bits and needs none.
 template <class E>
 constexpr bool kScaled = false;
 template <>
@@ -459,7 +460,8 @@ int product(const E* A0, const E* A1, const E* B, E* C0, E* C1, int64_t M, int64
         op.ldc[1] = (int)ldc1;
         return launch_grid<E>(op, M, N, 1, A1 ? 2 : 1, K, partial, stream);
     };
-    return eights(C0, N, ldc0) && (!A1 || eights(C1, N, ldc1)) ? with(StoreOp<E, true, kScaled<E>>{}) : with(StoreOp<E, false, kScaled<E>>{});
+    return eights(C0, N, ldc0) && (!A1 || eights(C1, N, ldc1)) ? with(StoreOp<E, true, kScaled<E>>{})
+                                                               : with(StoreOp<E, false, kScaled<E>>{});
 }
 
 // Rows of what is copied, transposed or computed for the products start on 128
@@ -615,10 +617,12 @@ int backward(const E* dH, const E* X, const E* Wg, const E* Wu, const float* sav
             if ((rc = (int)hipGetLastError())) return rc;
         }
     if (T > 0 && D > 0) {
-        if ((rc = product<E>(w.dgu, nullptr, w.wt, dX, nullptr, T, D, 2 * w.Fp, lddx, 0, w.factor, w.partial, stream))) return rc;
+        rc = product<E>(w.dgu, nullptr, w.wt, dX, nullptr, T, D, 2 * w.Fp, lddx, 0, w.factor, w.partial, stream);
+        if (rc) return rc;
     }
     if (F > 0 && D > 0) {
-        if ((rc = product<E>(w.dgt, w.dut, w.xt, dWg, dWu, F, D, w.Tp, lddg, lddu, w.factor, w.partial, stream))) return rc;
+        rc = product<E>(w.dgt, w.dut, w.xt, dWg, dWu, F, D, w.Tp, lddg, lddu, w.factor, w.partial, stream);
+        if (rc) return rc;
     }
     return hipSuccess;
 }

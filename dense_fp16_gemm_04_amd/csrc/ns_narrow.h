@@ -17,8 +17,8 @@
 // and 82 us, as three launches a step 64, 66, 74, 126 and 105; of 32 x 64: 32
 // and 58.  Longer ones, 64 x 16384, 65536, 262144 and 1048576: 100, 183, 422 and
 // 962, and 117, 228, 646 and 4116; sixteen of 64 x 16384 193 and 293, 64 of 64 x
-// 65536 2847 and 3901.  With 128 rows the same scheme took 64 us for 256 columns and 87 for
-// 1024, the three launches 65 and 78: repeating P costs what the launches did.
+// 65536 2847 and 3901.  With 128 rows the same scheme took 64 us for 256 columns
+// and 87 for 1024, the three launches 65 and 78: repeating P costs what the launches did.
 #ifndef DENSE_FP16_GEMM_NS_NARROW_H
 #define DENSE_FP16_GEMM_NS_NARROW_H
 

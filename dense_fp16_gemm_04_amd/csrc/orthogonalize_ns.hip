@@ -26,9 +26,9 @@
 // Matrices of at most 64 rows take one launch a step: ns_narrow.h.
 //
 // 4096 x 4096, five steps: 1375 us, 1000 TFLOP/s of what symmetry leaves (1255 on
-// the fastest of four MI355X): a step is S 71 + 7.5 us, P 73 + 8 (tiles, and joining the last
-// wave's split sums), X' 108 and the last one 103; sums of squares and X 41.  256 x
-// 256: 70 us, seventeen launches of 3 to 5.
+// the fastest of four MI355X): a step is S 71 + 7.5 us, P 73 + 8 (tiles, and
+// joining the last wave's split sums), X' 108 and the last one 103; sums of
+// squares and X 41.  256 x 256: 70 us, seventeen launches of 3 to 5.
 #include "orthogonalize_ns.h"
 
 #include <algorithm>
@@ -70,8 +70,8 @@ __global__ void __launch_bounds__(256) ns_squares(const E* __restrict__ G, int64
     if (threadIdx.x == 0) partial[blockIdx.x] = part[0];
 }
 
-// D1 [rows, p1] = G * scale / (norm + eps) (narrow::Factor) and D2 [cols, p2] its transpose,
-// both padded with zeros to their pitches.
+// D1 [rows, p1] = G * scale / (norm + eps) (narrow::Factor) and D2 [cols, p2]
+// its transpose, both padded with zeros to their pitches.
 template <class E>
 __global__ void __launch_bounds__(relayout::kThreads)
 ns_start(const E* __restrict__ G, int64_t ldg, int64_t stride_g, int rows, int cols, const double* __restrict__ partial,
@@ -126,8 +126,8 @@ __global__ void __launch_bounds__(256) ns_copy_out(const half* __restrict__ X, i
 enum { kAsIs = 1, kTurned = 2, kEights = 4 };
 
 // S (POLY false: alpha A A^T) or P (POLY true: alpha A A^T + beta A + gamma I,
-// A symmetric), each times its power of two, [m, mp] with pitch ldc, tiles on and below the diagonal and
-// their transposes.
+// A symmetric), each times its power of two, [m, mp] with pitch ldc, tiles on
+// and below the diagonal and their transposes.
 template <bool POLY>
 struct SymmetricOp {
     static constexpr bool kPersist = !POLY, kSplit = true;  // (P's epilogue would spill there)

@@ -1,8 +1,7 @@
 """Static race check of the operators' LDS rings (no GPU).
 
-The rules of ``test_lds_ring`` (what may land, be read and be overwritten
-when) over models written from these kernels' source
-order:
+The rules of ``test_lds_ring`` (what may land, be read and be overwritten when)
+over models written from these kernels' source order:
 * the persistent 256 x 256 kernel, whose ring is the product's own, with up to
   four rounds of its results through two slots; its K loop in the built code
   objects must issue the model's schedule, for every operation that has one;
