@@ -9,7 +9,9 @@ Beside it stand the operators of a linear layer's life, each with a library
 and a C ABI of its own: the gated feed-forward layer and its gradients
 (``gated_nt``, ``gated_nt_train``, ``gated_nt_backward``), the orthogonalised
 update of a weight (``orthogonalize_ns``) and the product with 4-bit weights
-(``gemv_w4``).
+(``gemv_w4``).  Around them stand those of a training step: the layer norm
+(``layer_norm``, ``layer_norm_train``, ``layer_norm_backward``) and dropout with
+the sum of a residual (``dropout``, ``dropout_backward``).
 """
 from __future__ import annotations
 
@@ -28,15 +30,24 @@ __all__ = [
     "gated_nt_backward",
     "orthogonalize_ns",
     "gemv_w4",
+    "layer_norm",
+    "layer_norm_train",
+    "layer_norm_backward",
+    "dropout",
+    "dropout_backward",
 ]
 
 _OPERATORS = ("gated_nt", "gated_nt_train", "gated_nt_backward", "orthogonalize_ns", "gemv_w4")
+_TRAINING = ("layer_norm", "layer_norm_train", "layer_norm_backward", "dropout", "dropout_backward")
 
 
 def __getattr__(name):
     if name in _OPERATORS:
         from . import operators
         return getattr(operators, name)
+    if name in _TRAINING:
+        from . import training
+        return getattr(training, name)
     if name in __all__:
         from . import binding
         return getattr(binding, name)

@@ -1,6 +1,6 @@
 """Build the gfx950 libraries in this package directory: ``libgemm_nt_f16.so``
 (the GEMM kernels and their C ABI), one library for each operator beside it
-(``OPERATORS``) and ``libpower_probe.so`` (the power probe, a measuring
+(``OPERATORS``, ``STEP_OPERATORS``) and ``libpower_probe.so`` (the power probe, a measuring
 instrument that no product path loads).
 
 One hipcc invocation per library compiles it ahead of time for gfx950 only.  ``-Xclang -target-feature -Xclang -packed-fp32-ops`` keeps the
@@ -36,6 +36,8 @@ PROBE_LIB = os.path.join(HERE, "libpower_probe.so")
 PROBE_RESOURCES = os.path.join(HERE, "libpower_probe.resources.json")
 # csrc/<name>.hip -> lib<name>.so, with the C ABI of include/<name>.h
 OPERATORS = ("gated_nt", "orthogonalize_ns", "gemv_w4")
+# the same, of the operators around a training step's products
+STEP_OPERATORS = ("layer_norm", "dropout")
 ARCH = "gfx950"
 
 
@@ -134,7 +136,7 @@ def build(verbose: bool = False, extra=()) -> str:
     """Every library, compiled side by side (`extra` flags for the GEMM
     library only); returns the GEMM library's path."""
     jobs = [(SRC, LIB, RESOURCES, verbose, extra), (PROBE_SRC, PROBE_LIB, PROBE_RESOURCES, verbose)]
-    jobs += [(*operator_paths(name), verbose) for name in OPERATORS]
+    jobs += [(*operator_paths(name), verbose) for name in OPERATORS + STEP_OPERATORS]
     with ThreadPoolExecutor(max_workers=len(jobs)) as pool:
         for done in [pool.submit(compile_library, *job) for job in jobs]:
             done.result()

@@ -1,0 +1,590 @@
+// The layer norm of a matrix's rows and its backward pass for gfx950:
+// include/layer_norm.h.
+//
+// Both passes are bound by their bytes: a row is read once, held in registers
+// (as it came, in its type) through its sums, and written once.
+#include "layer_norm.h"
+
+#include <algorithm>
+
+#include "abi.h"
+#include "cus.h"
+#include "rows.h"
+
+namespace {
+
+using namespace rows;
+
+// Chunk i of a lane is number i * G + lane of its row: adjacent lanes take
+// adjacent chunks.
+template <class E, class P>
+struct Forward {
+    const E* X;
+    const P *weight, *bias;  // null: 1 and 0
+    E* Y;
+    float* saved;  // null: not kept
+    int64_t ldx, ldy;
+    int rows, cols;
+    float eps;
+};
+
+__device__ __forceinline__ float deviation(float sum, int cols, float eps) { return 1.0f / __builtin_sqrtf(sum / (float)cols + eps); }
+
+// The squares of a chunk's distances from the mean.  Only a row's last chunk
+// may have elements that are not there: those lanes take the other way.  (`left`
+// is new to the compiler each time: it would keep the comparisons through the
+// rows, in more scalar registers than there are.)
+template <class E, int N>
+__device__ __forceinline__ float squares(const Vec<E, N>& v, float mean, int left, float sum)
+{
+    if (left >= N) {
+#pragma unroll
+        for (int e = 0; e < N; ++e) {
+            const float d = (float)v[e] - mean;
+            sum = __builtin_fmaf(d, d, sum);
+        }
+    } else {
+        asm volatile("" : "+v"(left));
+#pragma unroll
+        for (int e = 0; e < N; ++e) {
+            const float d = e < left ? (float)v[e] - mean : 0.0f;
+            sum = __builtin_fmaf(d, d, sum);
+        }
+    }
+    return sum;
+}
+
+// weight and bias of a chunk.
+template <class P, int N>
+__device__ __forceinline__ void load_params(const P* weight, const P* bias, int c, int left, Vec<P, N>& w, Vec<P, N>& b)
+{
+    w = (P)1.0f;
+    b = (P)0.0f;
+    if (left > 0 && weight) w = load<P, N>(weight + c, left);
+    if (left > 0 && bias) b = load<P, N>(bias + c, left);
+}
+
+// Rows of up to G * C chunks, G lanes to a row; G below 64: several rows to a wave.
+// Lanes with few chunks keep weight and bias for all their rows.
+template <class E, class P, int G, int C>
+__global__ void __launch_bounds__(G > 256 ? G : 256) norm_rows(const Forward<E, P> f)
+{
+    constexpr int N = kChunk<E>, R = (G > 256 ? G : 256) / G;
+    constexpr bool KEEP = C <= 2;
+    __shared__ Parts<G, 1> parts;
+    const int lane = threadIdx.x % G, mine = threadIdx.x / G, cols = f.cols;
+    Vec<P, N> kw[KEEP ? C : 1], kb[KEEP ? C : 1];
+    if constexpr (KEEP)
+#pragma unroll
+        for (int i = 0; i < C; ++i) {
+            const int c = (i * G + lane) * N;
+            load_params<P, N>(f.weight, f.bias, c, cols - c, kw[i], kb[i]);
+        }
+    for (int64_t first = (int64_t)blockIdx.x * R; first < f.rows; first += (int64_t)gridDim.x * R) {
+        const int64_t row = first + mine;
+        const bool there = row < f.rows;
+        const E* x = f.X + row * f.ldx;
+        Vec<E, N> v[C];
+        float s[1] = {0.0f};
+#pragma unroll
+        for (int i = 0; i < C; ++i) {
+            const int c = (i * G + lane) * N;
+            v[i] = Vec<E, N>{};
+            if (there && c < cols) v[i] = load<E, N>(x + c, cols - c);
+        }
+#pragma unroll
+        for (int i = 0; i < C; ++i)
+#pragma unroll
+            for (int e = 0; e < N; ++e) s[0] += (float)v[i][e];
+        sums<G, 1>(s, parts, 0);
+        const float mean = s[0] / (float)cols;
+        s[0] = 0.0f;
+#pragma unroll
+        for (int i = 0; i < C; ++i) s[0] = squares<E, N>(v[i], mean, cols - (i * G + lane) * N, s[0]);
+        sums<G, 1>(s, parts, 1);
+        const float r = deviation(s[0], cols, f.eps);
+        if (there && f.saved && lane == 0) {
+            f.saved[2 * row] = mean;
+            f.saved[2 * row + 1] = r;
+        }
+        E* y = f.Y + row * f.ldy;
+#pragma unroll
+        for (int i = 0; i < C; ++i) {
+            const int c = (i * G + lane) * N;
+            Vec<P, N> w, b;
+            if constexpr (KEEP) {
+                w = kw[i];
+                b = kb[i];
+            } else {
+                load_params<P, N>(f.weight, f.bias, c, cols - c, w, b);
+            }
+            Vec<E, N> o;
+#pragma unroll
+            for (int e = 0; e < N; ++e) o[e] = (E)__builtin_fmaf(((float)v[i][e] - mean) * r, (float)w[e], (float)b[e]);
+            if (there && c < cols) store<E, N>(y + c, cols - c, o);
+        }
+    }
+}
+
+// Rows of any length, a workgroup to a row that is read three times.
+constexpr int kWide = 1024;
+
+template <class E, class P>
+__global__ void __launch_bounds__(kWide) norm_wide(const Forward<E, P> f)
+{
+    constexpr int N = kChunk<E>;
+    __shared__ Parts<kWide, 1> parts;
+    const int cols = f.cols;
+    for (int64_t row = blockIdx.x; row < f.rows; row += gridDim.x) {
+        const E* x = f.X + row * f.ldx;
+        E* y = f.Y + row * f.ldy;
+        float s[1] = {0.0f};
+        for (int64_t c = (int64_t)threadIdx.x * N; c < cols; c += kWide * N) {
+            const Vec<E, N> v = load<E, N>(x + c, cols - (int)c);
+#pragma unroll
+            for (int e = 0; e < N; ++e) s[0] += (float)v[e];
+        }
+        sums<kWide, 1>(s, parts, 0);
+        const float mean = s[0] / (float)cols;
+        s[0] = 0.0f;
+        for (int64_t c = (int64_t)threadIdx.x * N; c < cols; c += kWide * N) {
+            const Vec<E, N> v = load<E, N>(x + c, cols - (int)c);
+            s[0] = squares<E, N>(v, mean, cols - (int)c, s[0]);
+        }
+        sums<kWide, 1>(s, parts, 1);
+        const float r = deviation(s[0], cols, f.eps);
+        if (f.saved && threadIdx.x == 0) {
+            f.saved[2 * row] = mean;
+            f.saved[2 * row + 1] = r;
+        }
+        for (int64_t c = (int64_t)threadIdx.x * N; c < cols; c += kWide * N) {
+            const int left = cols - (int)c;
+            const Vec<E, N> v = load<E, N>(x + c, left);
+            Vec<P, N> w, b;
+            load_params<P, N>(f.weight, f.bias, (int)c, left, w, b);
+            Vec<E, N> o;
+#pragma unroll
+            for (int e = 0; e < N; ++e) o[e] = (E)__builtin_fmaf(((float)v[e] - mean) * r, (float)w[e], (float)b[e]);
+            store<E, N>(y + c, left, o);
+        }
+    }
+}
+
+template <class E, class P>
+struct Backward {
+    const E *dY, *X;
+    const P* weight;
+    const float* saved;
+    E* dX;
+    float* partial;  // [workgroups][2][cols]: sums of dY h and of dY; null: neither
+    int64_t lddy, ldx, lddx;
+    int rows, cols;
+};
+
+// Rows of up to G * C chunks: dX, and each workgroup's sums over its rows.  The
+// next row's loads are in flight while a row is worked on, where registers allow.
+template <class E, class P, int G, int C>
+__global__ void __launch_bounds__(G > 256 ? G : 256) norm_back_rows(const Backward<E, P> f)
+{
+    constexpr int N = kChunk<E>, T = G > 256 ? G : 256, R = T / G;
+    constexpr bool AHEAD = C * N < 32;
+    __shared__ Parts<G, 2> parts;
+    __shared__ float meet[R > 1 ? R * G * C * N : 1];
+    const int lane = threadIdx.x % G, mine = threadIdx.x / G, cols = f.cols;
+    const int64_t step = (int64_t)gridDim.x * R;
+    Vec<P, N> w[C];
+#pragma unroll
+    for (int i = 0; i < C; ++i) {
+        const int c = (i * G + lane) * N;
+        w[i] = (P)1.0f;
+        if (c < cols && f.weight) w[i] = load<P, N>(f.weight + c, cols - c);
+    }
+    float aw[C][N], ab[C][N];
+#pragma unroll
+    for (int i = 0; i < C; ++i)
+#pragma unroll
+        for (int e = 0; e < N; ++e) aw[i][e] = ab[i][e] = 0.0f;
+
+    struct Row {
+        Vec<E, N> x[C], d[C];
+        float mean, r;
+    };
+    auto fetch = [&](int64_t row) __attribute__((always_inline)) {
+        Row v;
+        const bool there = row < f.rows;
+        v.mean = there ? f.saved[2 * row] : 0.0f;
+        v.r = there ? f.saved[2 * row + 1] : 0.0f;
+#pragma unroll
+        for (int i = 0; i < C; ++i) {
+            const int c = (i * G + lane) * N;
+            v.x[i] = Vec<E, N>{};
+            v.d[i] = Vec<E, N>{};
+            if (there && c < cols) {
+                v.x[i] = load<E, N>(f.X + row * f.ldx + c, cols - c);
+                v.d[i] = load<E, N>(f.dY + row * f.lddy + c, cols - c);
+            }
+        }
+        return v;
+    };
+    int turn = 0;
+    int64_t first = (int64_t)blockIdx.x * R;
+    Row next = {};
+    if constexpr (AHEAD) next = fetch(first + mine);
+    for (; first < f.rows; first += step) {
+        const int64_t row = first + mine;
+        Row v;
+        if constexpr (AHEAD) {
+            v = next;
+            next = fetch(row + step);
+        } else {
+            v = fetch(row);
+        }
+        float s[2] = {0.0f, 0.0f};
+#pragma unroll
+        for (int i = 0; i < C; ++i)
+#pragma unroll
+            for (int e = 0; e < N; ++e) {
+                const float h = ((float)v.x[i][e] - v.mean) * v.r, dy = (float)v.d[i][e], g = dy * (float)w[i][e];
+                s[0] += g;
+                s[1] = __builtin_fmaf(g, h, s[1]);
+                aw[i][e] = __builtin_fmaf(dy, h, aw[i][e]);
+                ab[i][e] += dy;
+            }
+        sums<G, 2>(s, parts, turn++);
+        const float mg = s[0] / (float)cols, mgh = s[1] / (float)cols;
+        E* to = f.dX + row * f.lddx;
+#pragma unroll
+        for (int i = 0; i < C; ++i) {
+            const int c = (i * G + lane) * N;
+            Vec<E, N> o;
+#pragma unroll
+            for (int e = 0; e < N; ++e) {
+                const float h = ((float)v.x[i][e] - v.mean) * v.r, g = (float)v.d[i][e] * (float)w[i][e];
+                o[e] = (E)(v.r * (g - mg - h * mgh));
+            }
+            if (row < f.rows && c < cols) store<E, N>(to + c, cols - c, o);
+        }
+    }
+    if (!f.partial) return;
+    float* const out = f.partial + (int64_t)blockIdx.x * 2 * cols;
+    if constexpr (R == 1) {
+#pragma unroll
+        for (int i = 0; i < C; ++i) {
+            const int c = (i * G + lane) * N;
+#pragma unroll
+            for (int e = 0; e < N; ++e)
+                if (c + e < cols) {
+                    out[c + e] = aw[i][e];
+                    out[cols + c + e] = ab[i][e];
+                }
+        }
+    } else {
+        // the groups' sums meet in LDS, first those of dY h
+        constexpr int W = G * C * N;
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            __syncthreads();
+#pragma unroll
+            for (int i = 0; i < C; ++i)
+#pragma unroll
+                for (int e = 0; e < N; ++e) meet[mine * W + (i * G + lane) * N + e] = k ? ab[i][e] : aw[i][e];
+            __syncthreads();
+            for (int c = threadIdx.x; c < cols; c += T) {
+                float sum = 0.0f;
+#pragma unroll
+                for (int g = 0; g < R; ++g) sum += meet[g * W + c];
+                out[k * cols + c] = sum;
+            }
+        }
+    }
+}
+
+// Rows of any length: their two means first, a workgroup to a row, then dX and
+// the sums of a tile of columns over a share of the rows.
+template <class E, class P>
+__global__ void __launch_bounds__(kWide) norm_back_means(const Backward<E, P> f, float* means)
+{
+    constexpr int N = kChunk<E>;
+    __shared__ Parts<kWide, 2> parts;
+    const int cols = f.cols;
+    int turn = 0;
+    for (int64_t row = blockIdx.x; row < f.rows; row += gridDim.x) {
+        const E *x = f.X + row * f.ldx, *d = f.dY + row * f.lddy;
+        const float mean = f.saved[2 * row], r = f.saved[2 * row + 1];
+        float s[2] = {0.0f, 0.0f};
+        for (int64_t c = (int64_t)threadIdx.x * N; c < cols; c += kWide * N) {
+            const int left = cols - (int)c;
+            const Vec<E, N> vx = load<E, N>(x + c, left), vd = load<E, N>(d + c, left);
+            Vec<P, N> w = (P)1.0f;
+            if (f.weight) w = load<P, N>(f.weight + c, left);
+#pragma unroll
+            for (int e = 0; e < N; ++e) {
+                const float g = (float)vd[e] * (float)w[e];
+                s[0] += g;
+                s[1] = __builtin_fmaf(g, ((float)vx[e] - mean) * r, s[1]);
+            }
+        }
+        sums<kWide, 2>(s, parts, turn++);
+        if (threadIdx.x == 0) {
+            means[2 * row] = s[0] / (float)cols;
+            means[2 * row + 1] = s[1] / (float)cols;
+        }
+    }
+}
+
+constexpr int kTileThreads = 256;
+
+template <class E, class P>
+__global__ void __launch_bounds__(kTileThreads) norm_back_tiles(const Backward<E, P> f, const float* means)
+{
+    constexpr int N = kChunk<E>;
+    const int cols = f.cols;
+    const int64_t c = ((int64_t)blockIdx.y * kTileThreads + threadIdx.x) * N;
+    if (c >= cols) return;
+    const int left = cols - (int)c;
+    Vec<P, N> w = (P)1.0f;
+    if (f.weight) w = load<P, N>(f.weight + c, left);
+    float aw[N], ab[N];
+#pragma unroll
+    for (int e = 0; e < N; ++e) aw[e] = ab[e] = 0.0f;
+    for (int64_t row = blockIdx.x; row < f.rows; row += gridDim.x) {
+        const Vec<E, N> x = load<E, N>(f.X + row * f.ldx + c, left), d = load<E, N>(f.dY + row * f.lddy + c, left);
+        const float mean = f.saved[2 * row], r = f.saved[2 * row + 1], mg = means[2 * row], mgh = means[2 * row + 1];
+        Vec<E, N> o;
+#pragma unroll
+        for (int e = 0; e < N; ++e) {
+            const float h = ((float)x[e] - mean) * r, dy = (float)d[e];
+            aw[e] = __builtin_fmaf(dy, h, aw[e]);
+            ab[e] += dy;
+            o[e] = (E)(r * (dy * (float)w[e] - mg - h * mgh));
+        }
+        store<E, N>(f.dX + row * f.lddx + c, left, o);
+    }
+    if (!f.partial) return;
+    float* const out = f.partial + (int64_t)blockIdx.x * 2 * cols + c;
+#pragma unroll
+    for (int e = 0; e < N; ++e)
+        if (e < left) {
+            out[e] = aw[e];
+            out[cols + e] = ab[e];
+        }
+}
+
+// Adds the workgroups' sums: 64 columns to a workgroup, sixteen waves that take
+// every sixteenth of the parts.  blockIdx.y: dweight, dbias.
+template <class P>
+__global__ void __launch_bounds__(1024) norm_columns(const float* partial, int parts, int cols, P* dweight, P* dbias)
+{
+    __shared__ float meet[16][kWave];
+    const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
+    P* const to = blockIdx.y ? dbias : dweight;
+    if (!to) return;
+    const int64_t c = (int64_t)blockIdx.x * kWave + lane;
+    float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    if (c < cols) {
+        const float* at = partial + blockIdx.y * (int64_t)cols + c;
+        int p = wave;
+        for (; p + 48 < parts; p += 64)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) s[k] += at[(int64_t)(p + 16 * k) * 2 * cols];
+        for (; p < parts; p += 16) s[0] += at[(int64_t)p * 2 * cols];
+    }
+    meet[wave][lane] = (s[0] + s[1]) + (s[2] + s[3]);
+    __syncthreads();
+    if (wave == 0 && c < cols) {
+        float sum = 0.0f;
+#pragma unroll
+        for (int w = 0; w < 16; ++w) sum += meet[w][lane];
+        to[c] = (P)sum;
+    }
+}
+
+// ------------------------------------------------------------------ host --
+
+int64_t chunks_of(int64_t cols, int32_t type) { return type == LAYER_NORM_F32 ? (cols + 3) / 4 : (cols + 7) / 8; }
+
+// Workgroups that share the rows of a backward pass, `per` rows each at a time.
+int64_t sharers(int64_t rows, int64_t per, int64_t most) { return std::min((rows + per - 1) / per, most); }
+
+// How the backward pass takes rows of so many chunks: G lanes with C chunks each
+// (0: rows of any length).
+struct Way {
+    int g, c;
+};
+Way way_of(int64_t chunks)
+{
+    for (const Way w : {Way{8, 1}, Way{16, 1}, Way{32, 1}, Way{64, 1}, Way{64, 2}, Way{256, 1}, Way{256, 2}, Way{256, 4}, Way{512, 4}})
+        if (chunks <= w.g * w.c) return w;
+    return {0, 0};
+}
+
+int64_t back_groups(int64_t rows, int64_t cols, int32_t type)
+{
+    const Way w = way_of(chunks_of(cols, type));
+    const int cus = cus::num_cus();
+    if (w.g == 0) return sharers(rows, 1, 64);
+    return sharers(rows, w.g > 256 ? 1 : 256 / w.g, w.c >= 4 ? cus : 2 * cus);
+}
+
+template <class E, class P>
+int forward(const Forward<E, P>& f, hipStream_t stream)
+{
+    const int64_t chunks = (f.cols + kChunk<E> - 1) / kChunk<E>;
+    const int64_t most = (int64_t)cus::num_cus() * 8;
+    auto with = [&](auto kernel, int threads, int per) {
+        const int64_t n = std::min((f.rows + (int64_t)per - 1) / per, most);
+        hipLaunchKernelGGL(kernel, dim3((unsigned)n), dim3(threads), 0, stream, f);
+        return (int)hipGetLastError();
+    };
+    if (chunks <= 8) return with(norm_rows<E, P, 8, 1>, 256, 32);
+    if (chunks <= 16) return with(norm_rows<E, P, 16, 1>, 256, 16);
+    if (chunks <= 32) return with(norm_rows<E, P, 32, 1>, 256, 8);
+    if (chunks <= 64) return with(norm_rows<E, P, 64, 1>, 256, 4);
+    if (chunks <= 128) return with(norm_rows<E, P, 64, 2>, 256, 4);
+    if (chunks <= 256) return with(norm_rows<E, P, 256, 1>, 256, 1);
+    if (chunks <= 512) return with(norm_rows<E, P, 256, 2>, 256, 1);
+    if (chunks <= 1024) return with(norm_rows<E, P, 256, 4>, 256, 1);
+    if (chunks <= 2048) return with(norm_rows<E, P, 512, 4>, 512, 1);
+    if (chunks <= 4096) return with(norm_rows<E, P, 1024, 4>, 1024, 1);
+    return with(norm_wide<E, P>, kWide, 1);
+}
+
+template <class E, class P>
+int backward(Backward<E, P> f, P* dweight, P* dbias, float* partial, float* means, int64_t groups, hipStream_t stream)
+{
+    f.partial = dweight || dbias ? partial : nullptr;
+    const int64_t chunks = (f.cols + kChunk<E> - 1) / kChunk<E>;
+    const Way w = way_of(chunks);
+    int rc = hipSuccess;
+    if (f.rows > 0) {
+        auto with = [&](auto kernel) {
+            hipLaunchKernelGGL(kernel, dim3((unsigned)groups), dim3(std::max(256, w.g)), 0, stream, f);
+            return (int)hipGetLastError();
+        };
+        if (w.g == 8) rc = with(norm_back_rows<E, P, 8, 1>);
+        else if (w.g == 16) rc = with(norm_back_rows<E, P, 16, 1>);
+        else if (w.g == 32) rc = with(norm_back_rows<E, P, 32, 1>);
+        else if (w.g == 64 && w.c == 1) rc = with(norm_back_rows<E, P, 64, 1>);
+        else if (w.g == 64) rc = with(norm_back_rows<E, P, 64, 2>);
+        else if (w.g == 256 && w.c == 1) rc = with(norm_back_rows<E, P, 256, 1>);
+        else if (w.g == 256 && w.c == 2) rc = with(norm_back_rows<E, P, 256, 2>);
+        else if (w.g == 256 && w.c == 4) rc = with(norm_back_rows<E, P, 256, 4>);
+        else if (w.g == 512) rc = with(norm_back_rows<E, P, 512, 4>);
+        else {
+            hipLaunchKernelGGL((norm_back_means<E, P>), dim3((unsigned)std::min<int64_t>(f.rows, 2 * cus::num_cus())), dim3(kWide), 0,
+                               stream, f, means);
+            if ((rc = (int)hipGetLastError())) return rc;
+            const int64_t tiles = (chunks + kTileThreads - 1) / kTileThreads;
+            hipLaunchKernelGGL((norm_back_tiles<E, P>), dim3((unsigned)groups, (unsigned)tiles), dim3(kTileThreads), 0, stream, f,
+                               (const float*)means);
+            rc = (int)hipGetLastError();
+        }
+        if (rc) return rc;
+    }
+    if (dweight || dbias) {
+        hipLaunchKernelGGL(norm_columns<P>, dim3((unsigned)(((int64_t)f.cols + kWave - 1) / kWave), 2), dim3(1024), 0, stream,
+                           (const float*)partial, (int)groups, f.cols, dweight, dbias);
+        rc = (int)hipGetLastError();
+    }
+    return rc;
+}
+
+struct BackwardSpace {
+    float *partial, *means;
+    int64_t bytes, groups;
+    BackwardSpace(void* base, int64_t rows, int64_t cols, int32_t type)
+    {
+        abi::Carve c(base);
+        groups = back_groups(rows, cols, type);
+        partial = c.take<float>(groups * 2 * cols);
+        means = way_of(chunks_of(cols, type)).g ? nullptr : c.take<float>(2 * rows);
+        bytes = c.used();
+    }
+};
+
+// Rows of up to 2^24 elements: what a launch over their columns may hold.
+bool good_size(int64_t rows, int64_t cols, int64_t ld) { return cols <= 1 << 24 && good_span(rows, cols, ld); }
+
+bool good_types(int32_t type, int32_t param)
+{
+    return type >= LAYER_NORM_F16 && type <= LAYER_NORM_F32 && (param == type || param == LAYER_NORM_F32);
+}
+int64_t size_of(int32_t type) { return type == LAYER_NORM_F32 ? 4 : 2; }
+
+}  // namespace
+
+extern "C" {
+
+int layer_norm_version(void) { return LAYER_NORM_VERSION; }
+
+int64_t layer_norm_backward_workspace(int64_t rows, int64_t cols)
+{
+    if (!good_size(rows, cols, cols)) return -1;
+    // (of either width of elements)
+    return std::max(BackwardSpace(nullptr, rows, cols, LAYER_NORM_F32).bytes, BackwardSpace(nullptr, rows, cols, LAYER_NORM_F16).bytes);
+}
+
+#define FOR_TYPES(CALL)                                                                              \
+    (type == LAYER_NORM_F32 ? CALL(float, float)                                                     \
+     : type == LAYER_NORM_F16                                                                        \
+         ? (param_type == LAYER_NORM_F32 ? CALL(_Float16, float) : CALL(_Float16, _Float16))         \
+         : (param_type == LAYER_NORM_F32 ? CALL(__bf16, float) : CALL(__bf16, __bf16)))
+
+int layer_norm(const void* X, const void* weight, const void* bias, void* Y, void* saved, int64_t rows, int64_t cols,
+               int64_t ldx, int64_t ldy, int32_t type, int32_t param_type, double eps, hipStream_t stream)
+{
+    using namespace abi;
+    if (!good_types(type, param_type) || !(eps >= 0) || !good_size(rows, cols, ldx) || !good_size(rows, cols, ldy))
+        return hipErrorInvalidValue;
+    if (rows == 0 || cols == 0) return hipSuccess;
+    const int64_t es = size_of(type), ps = size_of(param_type);
+    if (!good_pointer(X, rows, cols, es) || !good_pointer(Y, rows, cols, es) || (uintptr_t)weight % ps || (uintptr_t)bias % ps ||
+        (uintptr_t)saved % 8)
+        return hipErrorInvalidValue;
+    const Range y(Y, rows, cols, ldy, es), s(saved, 1, saved ? 2 * rows : 0, 0, 4);
+    const Range in[] = {Range(X, rows, cols, ldx, es), Range(weight, 1, weight ? cols : 0, 0, ps), Range(bias, 1, bias ? cols : 0, 0, ps)};
+    for (const Range& r : in)
+        if (y.meets(r) || s.meets(r)) return hipErrorInvalidValue;
+    if (y.meets(s)) return hipErrorInvalidValue;
+#define FORWARD(E, P)                                                                                                       \
+    forward<E, P>({(const E*)X, (const P*)weight, (const P*)bias, (E*)Y, (float*)saved, ldx, ldy, (int)rows, (int)cols, (float)eps}, \
+                  stream)
+    return FOR_TYPES(FORWARD);
+#undef FORWARD
+}
+
+int layer_norm_backward(const void* dY, const void* X, const void* weight, const void* saved, void* dX, void* dweight,
+                        void* dbias, int64_t rows, int64_t cols, int64_t lddy, int64_t ldx, int64_t lddx, int32_t type,
+                        int32_t param_type, void* workspace, int64_t workspace_bytes, hipStream_t stream)
+{
+    using namespace abi;
+    if (!good_types(type, param_type) || !good_size(rows, cols, lddy) || !good_size(rows, cols, ldx) || !good_size(rows, cols, lddx))
+        return hipErrorInvalidValue;
+    if (cols == 0) return hipSuccess;
+    const int64_t es = size_of(type), ps = size_of(param_type);
+    if (!good_pointer(dY, rows, cols, es) || !good_pointer(X, rows, cols, es) || !good_pointer(dX, rows, cols, es) ||
+        !good_pointer(saved, rows, cols, 8) || (uintptr_t)weight % ps || (uintptr_t)dweight % ps || (uintptr_t)dbias % ps ||
+        (uintptr_t)workspace % 16)
+        return hipErrorInvalidValue;
+    const int64_t need = layer_norm_backward_workspace(rows, cols);
+    if (need > 0 && (!workspace || workspace_bytes < need)) return hipErrorInvalidValue;
+    const Range in[] = {Range(dY, rows, cols, lddy, es), Range(X, rows, cols, ldx, es), Range(weight, 1, weight ? cols : 0, 0, ps),
+                        Range(saved, 1, 2 * rows, 0, 4)};
+    const Range out[] = {Range(dX, rows, cols, lddx, es), Range(dweight, 1, dweight ? cols : 0, 0, ps),
+                         Range(dbias, 1, dbias ? cols : 0, 0, ps), Range(workspace, 1, need, 0, 1)};
+    for (int i = 0; i < 4; ++i) {
+        for (const Range& r : in)
+            if (out[i].meets(r)) return hipErrorInvalidValue;
+        for (int k = 0; k < i; ++k)
+            if (out[i].meets(out[k])) return hipErrorInvalidValue;
+    }
+    const BackwardSpace w(workspace, rows, cols, type);
+#define BACKWARD(E, P)                                                                                                         \
+    backward<E, P>({(const E*)dY, (const E*)X, (const P*)weight, (const float*)saved, (E*)dX, nullptr, lddy, ldx, lddx, (int)rows, \
+                    (int)cols},                                                                                                \
+                   (P*)dweight, (P*)dbias, w.partial, w.means, w.groups, stream)
+    return FOR_TYPES(BACKWARD);
+#undef BACKWARD
+}
+
+}  // extern "C"

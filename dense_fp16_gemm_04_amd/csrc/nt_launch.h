@@ -5,22 +5,12 @@
 #include <algorithm>
 
 #include "abi.h"
+#include "cus.h"
 #include "nt_core.h"
 
 namespace nt {
 
-inline int num_cus()
-{
-    static int cache[64];
-    int device = 0;
-    if (hipGetDevice(&device) != hipSuccess || device < 0 || device >= 64) return 256;
-    int n = __atomic_load_n(&cache[device], __ATOMIC_RELAXED);
-    if (n == 0) {
-        if (hipDeviceGetAttribute(&n, hipDeviceAttributeMultiprocessorCount, device) != hipSuccess || n <= 0) n = 256;
-        __atomic_store_n(&cache[device], n, __ATOMIC_RELAXED);
-    }
-    return n;
-}
+using cus::num_cus;
 
 // The kernels, by their tiles, with the rate that each sustains on a full
 // chip and the fixed cost of a wave of tiles (pipeline fill and epilogue).

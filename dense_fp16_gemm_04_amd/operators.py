@@ -27,6 +27,7 @@ _HERE = os.path.dirname(os.path.abspath(__file__))
 
 _i64 = ctypes.c_int64
 _i32 = ctypes.c_int32
+_u64 = ctypes.c_uint64
 _p = ctypes.c_void_p
 _int = ctypes.c_int
 
@@ -49,6 +50,16 @@ SIGNATURES = {
     "gemv_w4": {
         "gemv_w4": ([_p] * 5 + [_i64] * 7 + [_i32, _p], _int),
         "gemv_w4_version": ([], _int),
+    },
+    "layer_norm": {
+        "layer_norm": ([_p] * 5 + [_i64] * 4 + [_i32, _i32, ctypes.c_double, _p], _int),
+        "layer_norm_backward": ([_p] * 7 + [_i64] * 5 + [_i32, _i32, _p, _i64, _p], _int),
+        "layer_norm_backward_workspace": ([_i64] * 2, _i64),
+        "layer_norm_version": ([], _int),
+    },
+    "dropout": {
+        "dropout": ([_p] * 3 + [_i64] * 5 + [_i32, ctypes.c_double, _u64, _u64, _p, _p], _int),
+        "dropout_version": ([], _int),
     },
 }
 

@@ -1,0 +1,178 @@
+"""ctypes bindings of the operators around a training step's products (argument
+marshalling only): the layer norm, and dropout with the sum of a residual, each
+with its backward pass.
+
+``liblayer_norm.so`` and ``libdropout.so`` with the C ABIs of
+``include/layer_norm.h`` and ``include/dropout.h``.  As in ``operators``: PyTorch supplies device
+memory and the current stream, a missing library raises ``RuntimeError`` and a
+refused call ``TypeError``, ``ValueError`` or ``GemmError``, matrices may be
+views whose rows' elements are adjacent, and nothing takes part in autograd: a
+training step calls the backward functions itself, and a new result of inputs
+that require gradients raises when they are asked of it.
+"""
+from __future__ import annotations
+
+import torch
+
+from .binding import GemmError
+from .operators import _TYPES_AND_F32, _call, _pitch, _without_gradients, _workspace, load
+
+_WORDS = 1 << 64
+
+
+def _vector(name, t, types, device, size):
+    """Check t, `size` adjacent elements of one of `types` on `device`."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError("%s must be a torch tensor" % name)
+    if t.dtype not in types:
+        raise TypeError("%s must be %s, got %s" % (name, " or ".join(str(d).replace("torch.", "") for d in types),
+                                                   str(t.dtype).replace("torch.", "")))
+    if t.dim() != 1 or t.shape[0] != size or not t.is_contiguous():
+        raise ValueError("%s must be contiguous [%d], got %s" % (name, size, tuple(t.shape)))
+    if t.get_device() != device:
+        raise ValueError("%s must be on the first operand's GPU" % name)
+
+
+# ----------------------------------------------------------- layer_norm --
+
+def _check_norm(x, weight, bias):
+    """(device, pitch of x, type of the parameters)."""
+    ldx = _pitch("x", x, _TYPES_AND_F32)
+    device = x.get_device()
+    types = (x.dtype, torch.float32)
+    for name, t in (("weight", weight), ("bias", bias)):
+        if t is not None:
+            _vector(name, t, types, device, x.shape[1])
+            types = (t.dtype,)  # one type for both
+    return device, ldx, types[0]
+
+
+def _norm(x, weight, bias, eps, out, train):
+    device, ldx, params = _check_norm(x, weight, bias)
+    eps = float(eps)
+    if not eps >= 0:
+        raise ValueError("eps must not be negative, got %r" % eps)
+    rows, cols = x.shape
+    if out is None:
+        out = x.new_empty((rows, cols))
+        ldy = cols
+    else:
+        ldy = _pitch("out", out, (x.dtype,), device, (rows, cols))
+    saved = x.new_empty((rows, 2), dtype=torch.float32) if train else None
+    _call("layer_norm", "layer_norm", device, x.data_ptr(), None if weight is None else weight.data_ptr(),
+          None if bias is None else bias.data_ptr(), out.data_ptr(), saved.data_ptr() if train else None, rows, cols, ldx, ldy,
+          _TYPES_AND_F32[x.dtype], _TYPES_AND_F32[params], eps)
+    return out, saved
+
+
+def layer_norm(x, weight=None, bias=None, eps: float = 1e-5, out=None):
+    """(x - mean) / sqrt(variance + eps) * weight + bias over the rows of x [rows, cols].
+
+    float16, bfloat16 or float32; weight and bias [cols], both of x's type or
+    both float32, or None for 1 and 0.  Statistics in 32 bits, rounded once.
+    Enqueued on the current stream of x's device; returns ``out``.  Not
+    differentiated by autograd: ``layer_norm_train`` and
+    ``layer_norm_backward`` are its training form.
+    """
+    y = _norm(x, weight, bias, eps, out, False)[0]
+    if out is None and any(t is not None and t.requires_grad for t in (x, weight, bias)):
+        return _without_gradients(
+            y, "layer_norm has no gradients in autograd: use layer_norm_train and layer_norm_backward", x, weight, bias)
+    return y
+
+
+def layer_norm_train(x, weight=None, bias=None, eps: float = 1e-5, out=None):
+    """``layer_norm`` that also keeps what its backward pass reads: (out, saved).
+
+    ``saved`` is float32 [rows, 2]: each row's mean and 1 / sqrt(variance + eps).
+    Neither requires gradients, whatever the inputs do.
+    """
+    return _norm(x, weight, bias, eps, out, True)
+
+
+def layer_norm_backward(dy, x, weight, bias, saved, out=None):
+    """The gradients (dx, dweight, dbias) of ``layer_norm_train`` for the gradient dy of its output.
+
+    None for a weight or bias that is None.  ``out``: the three to write them
+    to (None where there is none), or None for new ones.  They are written,
+    not added to.
+    """
+    device, ldx, params = _check_norm(x, weight, bias)
+    rows, cols = x.shape
+    lddy = _pitch("dy", dy, (x.dtype,), device, (rows, cols))
+    if not isinstance(saved, torch.Tensor) or saved.dtype != torch.float32 or tuple(saved.shape) != (rows, 2) \
+            or not saved.is_contiguous() or saved.get_device() != device:
+        raise ValueError("saved must be what layer_norm_train returned for x")
+    if out is None:
+        dx = x.new_empty((rows, cols))
+        dw, db = (None if t is None else torch.empty_like(t, requires_grad=False) for t in (weight, bias))
+        lddx = cols
+    else:
+        if len(out) != 3:
+            raise ValueError("out must be dx, dweight and dbias")
+        dx, dw, db = out
+        lddx = _pitch("out's dx", dx, (x.dtype,), device, (rows, cols))
+        for name, t, of in (("dweight", dw, weight), ("dbias", db, bias)):
+            if (t is None) != (of is None):
+                raise ValueError("out's %s must be given where its parameter is, and only there" % name)
+            if t is not None:
+                _vector("out's " + name, t, (params,), device, cols)
+    nbytes = load("layer_norm").layer_norm_backward_workspace(rows, cols)
+    if nbytes < 0:
+        raise GemmError("layer_norm_backward", 1)
+    keep, workspace = _workspace(x, nbytes)
+    _call("layer_norm", "layer_norm_backward", device, dy.data_ptr(), x.data_ptr(), None if weight is None else weight.data_ptr(),
+          saved.data_ptr(), dx.data_ptr(), None if dw is None else dw.data_ptr(), None if db is None else db.data_ptr(), rows, cols,
+          lddy, ldx, lddx, _TYPES_AND_F32[x.dtype], _TYPES_AND_F32[params], workspace, nbytes)
+    return dx, dw, db
+
+
+# -------------------------------------------------------------- dropout --
+
+def _dropout(x, p, seed, offset, residual, out):
+    ldx = _pitch("x", x, _TYPES_AND_F32)
+    device = x.get_device()
+    p = float(p)
+    if not 0 <= p <= 1:
+        raise ValueError("p must be 0 .. 1, got %r" % p)
+    state = None
+    if isinstance(seed, torch.Tensor):
+        _vector("seed, if not a number,", seed, (torch.int64,), device, 2)
+        state, seed = seed.data_ptr(), 0
+    seed, offset = int(seed), int(offset)
+    if not 0 <= seed < _WORDS or not 0 <= offset < _WORDS:
+        raise ValueError("seed and offset must be 0 .. 2^64 - 1, got %d and %d" % (seed, offset))
+    ldr = 0
+    if residual is not None:
+        ldr = _pitch("residual", residual, (x.dtype,), device, x.shape)
+    if out is None:
+        out = x.new_empty(x.shape)
+        ldy = x.shape[1]
+    else:
+        ldy = _pitch("out", out, (x.dtype,), device, x.shape)
+    _call("dropout", "dropout", device, x.data_ptr(), None if residual is None else residual.data_ptr(), out.data_ptr(), *x.shape,
+          ldx, ldr, ldy, _TYPES_AND_F32[x.dtype], p, seed, offset, state)
+    return out
+
+
+def dropout(x, p: float, seed, offset: int = 0, residual=None, out=None):
+    """x [rows, cols] with each element dropped with probability p and the others scaled by 1 / (1 - p), plus residual.
+
+    The mask is drawn from ``seed`` and ``offset`` by a counter-based generator
+    (``include/dropout.h``) and not stored: the same numbers give the same mask,
+    another offset an independent one.  p is held to 2^-17.  ``seed`` may be an
+    int64 tensor (seed, offset) on x's GPU, read when the call runs, to whose
+    offset ``offset`` is added: a captured graph then draws anew each time it is
+    replayed.  float16, bfloat16 or float32; ``out`` may be x or residual.  Not
+    differentiated by autograd: ``dropout_backward`` gives x's gradient, and the
+    residual's is the result's own.
+    """
+    y = _dropout(x, p, seed, offset, residual, out)
+    if out is None and (x.requires_grad or (residual is not None and residual.requires_grad)):
+        return _without_gradients(y, "dropout has no gradients in autograd: use dropout_backward", x, residual)
+    return y
+
+
+def dropout_backward(dy, p: float, seed, offset: int = 0, out=None):
+    """x's gradient for the gradient dy of ``dropout``'s result with the same p, seed and offset; ``out`` may be dy."""
+    return _dropout(dy, p, seed, offset, None, out)
