@@ -10,8 +10,10 @@ and a C ABI of its own: the gated feed-forward layer and its gradients
 (``gated_nt``, ``gated_nt_train``, ``gated_nt_backward``), the orthogonalised
 update of a weight (``orthogonalize_ns``) and the product with 4-bit weights
 (``gemv_w4``).  Around them stand those of a training step: the layer norm
-(``layer_norm``, ``layer_norm_train``, ``layer_norm_backward``) and dropout with
-the sum of a residual (``dropout``, ``dropout_backward``).
+(``layer_norm``, ``layer_norm_train``, ``layer_norm_backward``), dropout with
+the sum of a residual (``dropout``, ``dropout_backward``) and the loss over a
+vocabulary (``linear_cross_entropy``, ``linear_cross_entropy_train``,
+``linear_cross_entropy_backward``).
 """
 from __future__ import annotations
 
@@ -35,10 +37,14 @@ __all__ = [
     "layer_norm_backward",
     "dropout",
     "dropout_backward",
+    "linear_cross_entropy",
+    "linear_cross_entropy_train",
+    "linear_cross_entropy_backward",
 ]
 
 _OPERATORS = ("gated_nt", "gated_nt_train", "gated_nt_backward", "orthogonalize_ns", "gemv_w4")
-_TRAINING = ("layer_norm", "layer_norm_train", "layer_norm_backward", "dropout", "dropout_backward")
+_TRAINING = ("layer_norm", "layer_norm_train", "layer_norm_backward", "dropout", "dropout_backward", "linear_cross_entropy",
+             "linear_cross_entropy_train", "linear_cross_entropy_backward")
 
 
 def __getattr__(name):

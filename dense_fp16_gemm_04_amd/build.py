@@ -37,7 +37,7 @@ PROBE_RESOURCES = os.path.join(HERE, "libpower_probe.resources.json")
 # csrc/<name>.hip -> lib<name>.so, with the C ABI of include/<name>.h
 OPERATORS = ("gated_nt", "orthogonalize_ns", "gemv_w4")
 # the same, of the operators around a training step's products
-STEP_OPERATORS = ("layer_norm", "dropout")
+STEP_OPERATORS = ("layer_norm", "dropout", "linear_cross_entropy")
 ARCH = "gfx950"
 
 

@@ -1,0 +1,880 @@
+// The softmax cross entropy of a linear layer's outputs over a vocabulary, and
+// its gradients, for gfx950: include/linear_cross_entropy.h.
+//
+// Forward: one NT product X W^T whose epilogue reduces each row of a wave's
+// sub-tile to its largest output and the sum of exponentials about it, eight
+// bytes for 32 to 128 outputs; a second kernel joins them.
+//
+// Backward, a piece of the vocabulary at a time: the product again, whose
+// epilogue turns outputs to dl = softmax - onehot and writes it row-major, and
+// times dloss transposed; dX += dl W, with sums kept in 32 bits from piece to
+// piece, and dW = (dloss dl)^T X, both in NT form on transposed copies of W's piece
+// and of X.
+#include "linear_cross_entropy.h"
+
+#include <algorithm>
+
+#include "abi.h"
+#include "nt_launch.h"
+#include "relayout.h"
+
+namespace {
+
+using namespace nt;
+
+constexpr float kLog2e = 1.44269504f;
+
+typedef float f32x2 __attribute__((ext_vector_type(2)));
+
+// The largest and the sum over the four groups of 16 lanes, which hold a row.
+__device__ __forceinline__ float max_over_groups(float v)
+{
+    v = fmaxf(v, __shfl_xor(v, 16));
+    return fmaxf(v, __shfl_xor(v, 32));
+}
+__device__ __forceinline__ float sum_over_groups(float v)
+{
+    v += __shfl_xor(v, 16);
+    return v + __shfl_xor(v, 32);
+}
+
+// What exponentials are taken about: the largest output, or 0 where that is
+// -infinity (there are none, or all are: the sum is then 0, not NaN).
+__device__ __forceinline__ float about(float m) { return m == -INFINITY ? 0.0f : m; }
+
+// A block's values, where it holds 256 accumulation registers read one by one and
+// anew each time: a value that the compiler reads twice it keeps in a vector
+// register from the first time on, and all of them spill.  (The kernel has
+// waited for its last MFMAs before the epilogue.)
+template <class T>
+__device__ __forceinline__ f32x4 read(const f32x4& acc)
+{
+    if constexpr (T::FM * T::FN < 64) return acc;
+    f32x4 v;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) asm volatile("v_accvgpr_read_b32 %0, %1" : "=v"(v[e]) : "a"(acc[e]));
+    return v;
+}
+
+// The value is computed here, not later with what it is made of kept until then.
+__device__ __forceinline__ float done(float v)
+{
+    asm volatile("" : "+v"(v));
+    return v;
+}
+
+template <class E>
+struct LseOp {
+    static constexpr bool kPersist = true, kSplit = true;
+    const E *X, *W;
+    const int64_t* target;
+    float* tl;     // [M]: the target's output
+    f32x2* parts;  // [segments][Mp]: (largest, sum) of WTN columns of a row
+    int64_t target_stride, Mp;
+    int M, N, K, lda, ldb, tiles, tiles_m, tiles_n;
+
+    template <int BM, int BN>
+    __device__ __forceinline__ void tile(int id, Tile& t) const
+    {
+        int tm, tn;
+        grid_tile(xcd_order(id, tiles), tiles_m, tiles_n, tm, tn);
+        t.m0 = tm * BM;
+        t.n0 = tn * BN;
+        t.batch = 0;
+    }
+    __device__ __forceinline__ bool outside(const Tile& t) const { return t.m0 >= M || t.n0 >= N; }
+    __device__ __forceinline__ const E* a_rows(const Tile& t, int row, int& n) const
+    {
+        return rows_from(X, t.m0 + row, M, lda, n);
+    }
+    template <int WTN>
+    __device__ __forceinline__ const E* b_rows(const Tile& t, int row, int& n) const
+    {
+        return rows_from(W, t.n0 + row, N, ldb, n);
+    }
+    template <int WTN>
+    __device__ __forceinline__ int b_pitch(int) const
+    {
+        return ldb;
+    }
+    template <class T>
+    __device__ __forceinline__ void epilogue(const Tile& t, const f32x4 (&acc)[T::FM][T::FN], int lane, int wave, unsigned char*,
+                                             unsigned char*) const
+    {
+        // (One basic block up to the targets: values that live across a branch
+        // are taken out of the accumulation registers before it, and spill.)
+        const int ln = pinned(lane);
+        const int m0 = t.m0 + wave / T::WAVES_N * T::WTM, n0 = t.n0 + wave % T::WAVES_N * T::WTN;
+        // -infinity is added to columns that are not there, 0 to the others
+        const int there = N - n0 - 4 * (ln >> 4);  // of the lane's columns, from its first on
+        float top[T::FM], sum[T::FM];
+#pragma unroll
+        for (int i = 0; i < T::FM; ++i) top[i] = -INFINITY;
+#pragma unroll
+        for (int j = 0; j < T::FN; ++j) {
+            const f32x4 bias = absent(j, there);
+#pragma unroll
+            for (int i = 0; i < T::FM; ++i) top[i] = done(fmaxf(top[i], largest(read<T>(acc[i][j]) + bias)));
+        }
+#pragma unroll
+        for (int i = 0; i < T::FM; ++i) {
+            top[i] = max_over_groups(top[i]);
+            sum[i] = 0.0f;
+        }
+#pragma unroll
+        for (int j = 0; j < T::FN; ++j) {
+            const f32x4 bias = absent(j, there);
+#pragma unroll
+            for (int i = 0; i < T::FM; ++i) {
+                const f32x4 l = read<T>(acc[i][j]);
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    sum[i] += __builtin_amdgcn_exp2f(__builtin_fmaf(l[e] - about(top[i]), kLog2e, bias[e]));
+                sum[i] = done(sum[i]);
+            }
+        }
+        __builtin_amdgcn_sched_barrier(0);
+        // (sub-tiles past the last column have no part)
+        const __amdgpu_buffer_rsrc_t to =
+            make_rsrc(parts + (int64_t)(n0 / T::WTN) * Mp + m0, n0 < N && m0 < M ? (uint32_t)min(M - m0, T::WTM) * 8u : 0u);
+        int at[T::FM];  // the target's place among the lane's columns
+        bool any = false;
+#pragma unroll
+        for (int i = 0; i < T::FM; ++i) {
+            const int row = m0 + i * 16 + (ln & 15);
+            const f32x2 part = {top[i], sum_over_groups(sum[i])};
+            __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(u32x2, part), to, ln < 16 ? (i * 16 + ln) * 8 : kOob, 0, 0);
+            const int64_t c = target[min(row, M - 1) * target_stride] - n0;
+            at[i] = row < M && c >= 0 && c < min(T::WTN, N - n0) ? (int)c - 4 * (ln >> 4) : -1;
+            any |= at[i] >= 0;
+        }
+        if (!__any(any)) return;
+        // the lane's value in the target's column: few sub-tiles have any
+        float found[T::FM];
+#pragma unroll
+        for (int i = 0; i < T::FM; ++i) {
+            bool mine = false;
+            found[i] = 0.0f;
+#pragma unroll
+            for (int j = 0; j < T::FN; ++j) {
+                const f32x4 l = read<T>(acc[i][j]);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const bool here = at[i] == j * 16 + e;
+                    found[i] = here ? l[e] : found[i];
+                    mine |= here;
+                }
+                found[i] = done(found[i]);
+            }
+            at[i] = mine ? 0 : -1;
+        }
+#pragma unroll
+        for (int i = 0; i < T::FM; ++i)
+            if (at[i] == 0) tl[m0 + i * 16 + (ln & 15)] = found[i];
+    }
+    static __device__ __forceinline__ float largest(const f32x4& v) { return fmaxf(fmaxf(v[0], v[1]), fmaxf(v[2], v[3])); }
+    static __device__ __forceinline__ f32x4 absent(int j, int there)
+    {
+        f32x4 v;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[e] = j * 16 + e < there ? 0.0f : -INFINITY;
+        return v;
+    }
+};
+
+// Joins the parts of R rows to a workgroup: 1024 / R threads take every so many
+// of a row's, and meet in LDS.
+constexpr int kJoin = 1024;
+
+struct Join {
+    const f32x2* parts;
+    const int64_t* target;
+    const float* tl;
+    float *loss, *saved;  // saved null: not kept
+    int64_t target_stride, ignore, Mp;
+    int M, N, segments;
+};
+
+// (largest, sum) of two parts.
+__device__ __forceinline__ f32x2 joined(const f32x2& a, const f32x2& b)
+{
+    const float m = fmaxf(a[0], b[0]), c = about(m);
+    return f32x2{m, a[1] * __builtin_amdgcn_exp2f((a[0] - c) * kLog2e) + b[1] * __builtin_amdgcn_exp2f((b[0] - c) * kLog2e)};
+}
+
+template <int R>
+__global__ void __launch_bounds__(kJoin) lse_join(const Join f)
+{
+    constexpr int S = kJoin / R;
+    __shared__ f32x2 meet[S][R];
+    const int r = threadIdx.x % R, s = threadIdx.x / R;
+    const int64_t row = (int64_t)blockIdx.x * R + r;
+    f32x2 all = {-INFINITY, 0.0f};
+    if (row < f.M) {
+        const f32x2* at = f.parts + row;
+        int p = s;
+        for (; p + 3 * S < f.segments; p += 4 * S) {
+            f32x2 v[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) v[k] = at[(p + k * S) * f.Mp];
+            all = joined(all, joined(joined(v[0], v[1]), joined(v[2], v[3])));
+        }
+        for (; p < f.segments; p += S) all = joined(all, at[p * f.Mp]);
+    }
+    meet[s][r] = all;
+#pragma unroll
+    for (int half = S / 2; half > 0; half /= 2) {
+        __syncthreads();
+        if (s < half) meet[s][r] = joined(meet[s][r], meet[s + half][r]);
+    }
+    if (s > 0 || row >= f.M) return;
+    all = meet[0][r];
+    const int64_t c = f.target[row * f.target_stride];
+    const bool there = c >= 0 && c < f.N;
+    const bool ignored = c == f.ignore;
+    const float tl = ignored ? 0.0f : there ? f.tl[row] : NAN;
+    f.loss[row] = ignored ? 0.0f : (all[0] - tl) + logf(all[1]);
+    if (f.saved) {
+        f.saved[3 * row] = all[0];
+        f.saved[3 * row + 1] = all[1];
+        f.saved[3 * row + 2] = tl;
+    }
+}
+
+// ------------------------------------------------------------- backward --
+
+// binary16 ends at 2^-24: dl is held times 2^15.  bfloat16 has the range of 32
+// bits and needs no shift.
+template <class E>
+constexpr float kShift = 0.0f;
+template <>
+constexpr float kShift<_Float16> = 15.0f;
+
+// What the backward pass needs of a row.  dl 2^shift = exp2(min(l - top, 0)
+// log2 e + bias) but in the target's column, where it is `hit`; what makes dW is
+// that times `weight`, dloss over its largest magnitude, which dW's product puts
+// back: where all tokens have one dloss, as of a mean, its digits then are in no
+// rounding (8192 x 4096 x 131072 in bfloat16: dW 3.0e-3 off with dloss itself in
+// them, twice what its own rounding leaves).  A row that is ignored or not there has 0, -infinity, 0, 0: then
+// the minimum, which takes the number of a number and NaN, makes dl zero whatever
+// l is.  So it does where l is of a column that is not there, and of columns that
+// are l is no larger than top but by another order of summation.
+struct RowInfo {
+    float top, bias, weight, hit;
+};
+
+// The rows' numbers, by one workgroup: dloss' largest magnitude has to be known first.
+template <class E>
+struct RowNumbers {
+    const float *dloss, *saved;
+    const int64_t* target;
+    int64_t dloss_stride, target_stride, ignore;
+    int M, Mp, N;  // Mp: rows of whole tiles
+    RowInfo* info;
+    int* column;    // of the target, or -1
+    float* factor;  // to dW's sums
+
+    __device__ __forceinline__ void run() const
+    {
+        __shared__ float part[relayout::kThreads / kWave];
+        float most = 0.0f;
+        for (int row = threadIdx.x; row < M; row += relayout::kThreads) {
+            const float g = fabsf(dloss[row * dloss_stride]);
+            if (target[row * target_stride] != ignore && g < INFINITY) most = fmaxf(most, g);
+        }
+        for (int d = 32; d > 0; d >>= 1) most = fmaxf(most, __shfl_xor(most, d));
+        if (threadIdx.x % kWave == 0) part[threadIdx.x / kWave] = most;
+        __syncthreads();
+        most = fmaxf(fmaxf(part[0], part[1]), fmaxf(part[2], part[3]));
+        if (most == 0.0f) most = 1.0f;
+        if (threadIdx.x == 0) *factor = most * exp2f(-kShift<E>);
+        for (int row = threadIdx.x; row < Mp; row += relayout::kThreads) {
+            RowInfo r = {0.0f, -INFINITY, 0.0f, 0.0f};
+            int at = -1;
+            if (row < M) {
+                const int64_t c = target[row * target_stride];
+                if (c != ignore) {
+                    const float top = saved[3 * (int64_t)row], sum = saved[3 * (int64_t)row + 1], tl = saved[3 * (int64_t)row + 2];
+                    const bool there = c >= 0 && c < N;
+                    r.top = top;
+                    r.bias = there ? kShift<E> - log2f(sum) : NAN;
+                    r.weight = dloss[row * dloss_stride] / most;
+                    r.hit = (expf(tl - top) - sum) / sum * exp2f(kShift<E>);
+                    at = there ? (int)c : -1;
+                }
+            }
+            info[row] = r;
+            column[row] = at;
+        }
+    }
+};
+
+// X^T with zeros in the columns of tokens that are ignored (0 times what they
+// hold may be NaN), by tiles of 64 x 64.
+template <class E>
+struct TurnX {
+    relayout::Transpose<E> turn;
+    const int64_t* target;
+    int64_t target_stride, ignore;
+
+    __device__ __forceinline__ void run(int id, E* tile) const
+    {
+        using namespace relayout;
+        const int tiles_c = (turn.cols + kTile - 1) / kTile;
+        const int r0 = id / tiles_c * kTile, c0 = id % tiles_c * kTile;
+        const int x = threadIdx.x & 15, y = threadIdx.x >> 4;
+#pragma unroll
+        for (int it = 0; it < 4; ++it) {
+            const int r = it * 16 + y;
+            typename Elem<E>::x4 v = {};
+            if (r0 + r < turn.rows && target[(r0 + r) * target_stride] != ignore)
+                v = load4(turn.src + (int64_t)(r0 + r) * turn.lds_, c0 + x * 4, turn.cols, turn.vec);
+            *(typename Elem<E>::x4*)(tile + r * kPitch + x * 4) = v;
+        }
+        __syncthreads();
+        store_transposed(tile, turn.dst, turn.ldd, r0, c0, turn.padded, turn.cols);
+    }
+};
+
+// What the products read, in one launch: the rows' numbers and X^T (for the
+// first piece), and W^T of a piece.
+template <class E>
+struct Prepare {
+    RowNumbers<E> rows;
+    TurnX<E> x;
+    relayout::Transpose<E> w;
+    int first, second;  // the transposes' first workgroups
+};
+
+template <class E>
+__global__ void __launch_bounds__(relayout::kThreads) loss_prepare(const Prepare<E> p)
+{
+    __shared__ E tile[relayout::kTile * relayout::kPitch];
+    const int id = blockIdx.x;
+    if (id < p.first)
+        p.rows.run();
+    else if (id < p.second)
+        p.x.run(id - p.first, tile);
+    else
+        p.w.run(id - p.second, tile);
+}
+
+// dl of a piece of the vocabulary: row-major to dl (pitch ldd), times dloss and
+// transposed to dlt (pitch ldt).
+template <class E>
+struct DlOp {
+    static constexpr bool kPersist = true, kSplit = false;
+    const E *X, *W;  // W from the piece's first row on
+    E *dl, *dlt;
+    const RowInfo* info;
+    const int* column;
+    int M, N, K, lda, ldb, ldd, ldt, first, tiles, tiles_m, tiles_n;
+
+    template <int BM, int BN>
+    __device__ __forceinline__ void tile(int id, Tile& t) const
+    {
+        int tm, tn;
+        grid_tile(xcd_order(id, tiles), tiles_m, tiles_n, tm, tn);
+        t.m0 = tm * BM;
+        t.n0 = tn * BN;
+        t.batch = 0;
+    }
+    __device__ __forceinline__ const E* a_rows(const Tile& t, int row, int& n) const
+    {
+        return rows_from(X, t.m0 + row, M, lda, n);
+    }
+    template <int WTN>
+    __device__ __forceinline__ const E* b_rows(const Tile& t, int row, int& n) const
+    {
+        return rows_from(W, t.n0 + row, N, ldb, n);
+    }
+    template <int WTN>
+    __device__ __forceinline__ int b_pitch(int) const
+    {
+        return ldb;
+    }
+    template <class T>
+    __device__ __forceinline__ void epilogue(const Tile& t, const f32x4 (&acc)[T::FM][T::FN], int lane, int wave, unsigned char* s0,
+                                             unsigned char* s1) const
+    {
+        const int ln = pinned(lane), wm = wave / T::WAVES_N, wn = wave % T::WAVES_N;
+        const RowInfo* const rows = info + t.m0 + wm * T::WTM + (ln & 15);
+        float top[T::FM], bias[T::FM];
+#pragma unroll
+        for (int i = 0; i < T::FM; ++i) {
+            top[i] = rows[i * 16].top;
+            bias[i] = rows[i * 16].bias;
+        }
+        auto dl_of = [&](int i, int j) __attribute__((always_inline)) {
+            f32x4 v = read<T>(acc[i][j]);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) v[e] = __builtin_amdgcn_exp2f(__builtin_fmaf(fminf(v[e] - top[i], 0.0f), kLog2e, bias[i]));
+            __builtin_amdgcn_sched_barrier(0);  // (block by block, for the registers' sake)
+            return v;
+        };
+        // a row's target, if among the wave's columns, from the first of them
+        int at[T::FM];
+        float hit[T::FM], weight[T::FM];
+#pragma unroll
+        for (int i = 0; i < T::FM; ++i) {
+            at[i] = column[t.m0 + wm * T::WTM + i * 16 + (ln & 15)] - first - t.n0 - wn * T::WTN;
+            hit[i] = rows[i * 16].hit;
+            weight[i] = rows[i * 16].weight;
+        }
+        constexpr int ROUNDS = T::BM * T::BN * 2 > T::STAGE_MAX ? 2 : 1, IR = T::FM / ROUNDS, CR = T::WTN / ROUNDS;
+        // (Columns past N, up to a chunk of eight, hold numbers, which meet zeros.
+        // A row without a target among the round's columns gets a value that it
+        // has: a branch would take all accumulators out of their registers.)
+        write_rows<T, T::FN, true>([&](int i, int j) { return round4<E>(dl_of(i, j)); },
+                                   rows_at(dl, t.m0, M, T::BM, ldd, t.n0, (N + 7) & ~7), lane, wave, s0, s1,
+                                   [&](const Image<T::BN>& image, int h) __attribute__((always_inline)) {
+#pragma unroll
+                                       for (int i = 0; i < IR; ++i) {
+                                           const int k = h * IR + i;
+                                           const bool here = at[k] >= 0 && at[k] < T::WTN;
+                                           image.set((wm * IR + i) * 16 + (ln & 15), wn * T::WTN + (here ? at[k] : 4 * (ln >> 4)),
+                                                     (E)(here ? hit[k] : dl_of(k, 0)[0]));
+                                       }
+                                   });
+        write_turned<T, true>([&](int i, int j) { return round4<E>(dl_of(i, j) * weight[i]); },
+                              rows_at(dlt, t.n0, N, T::BN, ldt, t.m0, (M + 7) & ~7), lane, wave, s0, s1,
+                              [&](const Image<T::BM>& image, int h) __attribute__((always_inline)) {
+#pragma unroll
+                                  for (int i = 0; i < T::FM; ++i) {
+                                      const int c = at[i] - h * CR;
+                                      const bool here = c >= 0 && c < CR;
+                                      image.set(wn * CR + (here ? c : 4 * (ln >> 4)), wm * T::WTM + i * 16 + (ln & 15),
+                                                (E)((here ? hit[i] : dl_of(i, h * (T::FN / ROUNDS))[0]) * weight[i]));
+                                  }
+                              });
+    }
+};
+
+// sums += A B^T, sums in blocks of 16 x 16, row of blocks by row, in the order in
+// which a wave's lanes hold them (lane l: row l % 16, columns 4 (l / 16) .. + 3).
+constexpr int kBlockFloats = 256;
+
+template <class E>
+struct AddOp {
+    static constexpr bool kPersist = true, kSplit = true;
+    const E *A, *B;
+    float* sums;
+    int M, N, K, lda, ldb, fresh, tiles, tiles_m, tiles_n;  // fresh: sums hold nothing yet
+
+    template <int BM, int BN>
+    __device__ __forceinline__ void tile(int id, Tile& t) const
+    {
+        int tm, tn;
+        grid_tile(xcd_order(id, tiles), tiles_m, tiles_n, tm, tn);
+        t.m0 = tm * BM;
+        t.n0 = tn * BN;
+        t.batch = 0;
+    }
+    __device__ __forceinline__ bool outside(const Tile& t) const { return t.m0 >= M || t.n0 >= N; }
+    __device__ __forceinline__ const E* a_rows(const Tile& t, int row, int& n) const
+    {
+        return rows_from(A, t.m0 + row, M, lda, n);
+    }
+    template <int WTN>
+    __device__ __forceinline__ const E* b_rows(const Tile& t, int row, int& n) const
+    {
+        return rows_from(B, t.n0 + row, N, ldb, n);
+    }
+    template <int WTN>
+    __device__ __forceinline__ int b_pitch(int) const
+    {
+        return ldb;
+    }
+    template <class T>
+    __device__ __forceinline__ void epilogue(const Tile& t, const f32x4 (&acc)[T::FM][T::FN], int lane, int wave, unsigned char*,
+                                             unsigned char*) const
+    {
+        const int ln = pinned(lane);
+        const int bm = (t.m0 + wave / T::WAVES_N * T::WTM) / 16, bn = (t.n0 + wave % T::WAVES_N * T::WTN) / 16;
+        // (what is not there is out of the buffers' range, and so are sums that
+        // hold nothing yet: read as zeros, not written)
+        const int rows = (M + 15) / 16 - bm, cols = (N + 15) / 16, left = max(cols - bn, 0);
+#pragma unroll
+        for (int i = 0; i < T::FM; ++i) {
+            __builtin_amdgcn_sched_barrier(0);  // (row by row of blocks, for the registers' sake)
+            const float* const at = sums + ((int64_t)(bm + i) * cols + bn) * kBlockFloats;
+            const uint32_t bytes = i < rows ? (uint32_t)left * (kBlockFloats * 4u) : 0u;
+            const __amdgpu_buffer_rsrc_t to = make_rsrc(at, bytes), from = make_rsrc(at, fresh ? 0u : bytes);
+            u32x4 old[T::FN];
+#pragma unroll
+            for (int j = 0; j < T::FN; ++j)
+                old[j] = __builtin_amdgcn_raw_buffer_load_b128(from, ln * 16 + j * (kBlockFloats * 4), 0, 0);
+#pragma unroll
+            for (int j = 0; j < T::FN; ++j) {
+                const f32x4 v = acc[i][j] + __builtin_bit_cast(f32x4, old[j]);
+                __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, v), to, ln * 16 + j * (kBlockFloats * 4), 0, 0);
+            }
+        }
+    }
+};
+
+// dX[t] = dloss[t] 2^-shift sums[t], rounded: a wave to a block of 16 x 16.  What
+// rounding took from the target's dl, most of a row's error where few terms are
+// large, is put back first: dX (300 x 200 x 513, binary16) 2.73e-4 off without.
+template <class E>
+struct Finish {
+    const float *sums, *dloss;
+    const RowInfo* info;
+    const int* column;
+    const E* W;
+    E* dX;
+    int64_t dloss_stride, ldw, ld;
+    int M, N, vec_w, vec;
+};
+
+template <class E>
+__global__ void __launch_bounds__(256) loss_finish(const Finish<E> f)
+{
+    const int64_t cols = (f.N + 15) / 16, blocks = (int64_t)((f.M + 15) / 16) * cols;
+    const int lane = threadIdx.x % kWave;
+    for (int64_t b = (int64_t)blockIdx.x * 4 + threadIdx.x / kWave; b < blocks; b += (int64_t)gridDim.x * 4) {
+        f32x4 v = *(const f32x4*)(f.sums + b * kBlockFloats + lane * 4);
+        const int row = (int)(b / cols) * 16 + (lane & 15), c = (int)(b % cols) * 16 + 4 * (lane >> 4);
+        if (row >= f.M || c >= f.N) continue;
+        const RowInfo r = f.info[row];
+        const int at = f.column[row];
+        if (at >= 0) {
+            const float lost = r.hit - (float)(E)r.hit;
+            const relayout::Four<E> w = relayout::load4(f.W + at * f.ldw, c, f.N, f.vec_w);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const float add = lost * (float)w[e];
+                v[e] += fabsf(add) < INFINITY ? add : 0.0f;  // (an infinity is in the sum already)
+            }
+        }
+        // (a row that is ignored, whatever its dloss)
+        const float g = r.bias == -INFINITY ? 0.0f : f.dloss[row * f.dloss_stride] * __builtin_amdgcn_exp2f(-kShift<E>);
+        const typename Elem<E>::x4 o = round4<E>(v * g);
+        E* const to = f.dX + row * f.ld + c;
+        if (f.vec && c + 4 <= f.N)
+            *(typename Elem<E>::x4*)to = o;
+        else
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (c + e < f.N) to[e] = o[e];
+    }
+}
+
+// ------------------------------------------------------------------ host --
+
+bool vec4(const void* p, int64_t ld) { return (uintptr_t)p % 8 == 0 && ld % 4 == 0; }
+bool vec8(const void* p, int64_t ld) { return (uintptr_t)p % 16 == 0 && ld % 8 == 0; }
+
+// Rows of what is copied, transposed or kept start on 128 bytes, and are written
+// in whole cache lines.
+constexpr int64_t kLine = 64;
+
+// The parts of up to this many outputs may be of 32 columns, of more 64 at least
+// (which leaves out the smaller tiles): 8 bytes each.
+constexpr int64_t kSmall = (int64_t)1 << 26;
+int64_t part_width(int64_t T, int64_t V) { return T <= kSmall / V ? 32 : 64; }
+
+// Rows of X or W copied to where they can be read 16 bytes at a time.
+template <class E>
+struct Copied {
+    const E* at;
+    int ld;
+    int enqueue(E* to, int64_t rows, int64_t D, hipStream_t stream)
+    {
+        relayout::Copies<E> c = {};
+        c.job[c.jobs++] = {at, to, ld, rows};
+        at = to;
+        ld = (int)abi::up(D, kLine);
+        if (!rows || !ld) return hipSuccess;
+        const int64_t work = rows * (ld / 4);
+        hipLaunchKernelGGL(relayout::copy_rows<E>, dim3((unsigned)std::min<int64_t>((work + 255) / 256, 16384)),
+                           dim3(relayout::kThreads), 0, stream, c, (int)D, ld);
+        return (int)hipGetLastError();
+    }
+};
+
+template <class E>
+struct ForwardSpace {
+    E *x, *w;
+    float *tl, *partial;
+    f32x2* parts;
+    int64_t Mp, bytes;
+    bool copy_x, copy_w;
+    ForwardSpace(void* base, const void* X, const void* W, int64_t T, int64_t D, int64_t V, int64_t ldx, int64_t ldw)
+    {
+        abi::Carve c(base);
+        copy_x = D % 8 || !vec8(X, ldx);
+        copy_w = D % 8 || !vec8(W, ldw);
+        const int64_t ld = abi::up(D, kLine), width = part_width(T, V);
+        Mp = abi::up(T, 16);
+        x = copy_x ? c.take<E>(T * ld) : nullptr;
+        w = copy_w ? c.take<E>(V * ld) : nullptr;
+        tl = c.take<float>(T);
+        parts = c.take<f32x2>((V + width - 1) / width * Mp);
+        partial = abi::up(D, 8) >= kSplitK ? c.take<float>(kSplitFloats) : nullptr;
+        bytes = T ? c.used() : 0;
+    }
+};
+
+template <class E>
+int forward(const E* X, const E* W, const int64_t* target, float* loss, float* saved, int64_t T, int64_t D, int64_t V, int64_t ldx,
+            int64_t ldw, int64_t target_stride, int64_t ignore, void* workspace, hipStream_t stream)
+{
+    const ForwardSpace<E> w(workspace, X, W, T, D, V, ldx, ldw);
+    int rc;
+    Copied<E> cx{X, (int)ldx}, cw{W, (int)ldw};
+    if (w.copy_x && (rc = cx.enqueue(w.x, T, D, stream))) return rc;
+    if (w.copy_w && (rc = cw.enqueue(w.w, V, D, stream))) return rc;
+    LseOp<E> op = {};
+    op.X = cx.at;
+    op.W = cw.at;
+    op.target = target;
+    op.tl = w.tl;
+    op.parts = w.parts;
+    op.target_stride = target_stride;
+    op.Mp = w.Mp;
+    op.M = (int)T;
+    op.N = (int)V;
+    op.K = (int)abi::up(D, 8);
+    op.lda = cx.ld;
+    op.ldb = cw.ld;
+    int wtn = 0;
+    rc = launch<E>(
+        op, op.K, w.partial,
+        [&](const Kind& k) {
+            const bool wide = k.bn == 256 || k.bm == 256;  // (sub-tiles of 64 columns or more)
+            if (!wide && part_width(T, V) > 32) return INT64_MAX;
+            return (T + k.bm - 1) / k.bm * ((V + k.bn - 1) / k.bn);
+        },
+        [&](LseOp<E>& o, const Kind& k) {
+            o.tiles_m = (int)((T + k.bm - 1) / k.bm);
+            o.tiles_n = (int)((V + k.bn - 1) / k.bn);
+            wtn = k.bn == 256 ? 128 : k.bm == 256 ? 64 : 32;
+        },
+        stream);
+    if (rc) return rc;
+    const Join j = {w.parts, target, w.tl, loss, saved, target_stride, ignore, w.Mp, (int)T, (int)V, (int)((V + wtn - 1) / wtn)};
+    if (T <= 8 * 2048)
+        hipLaunchKernelGGL(lse_join<8>, dim3((unsigned)((T + 7) / 8)), dim3(kJoin), 0, stream, j);
+    else
+        hipLaunchKernelGGL(lse_join<32>, dim3((unsigned)((T + 31) / 32)), dim3(kJoin), 0, stream, j);
+    return (int)hipGetLastError();
+}
+
+// Columns of the vocabulary to a piece: dl of 2^27 elements, 256 MB, twice, in
+// rows of 2^20 at most (a pitch is below 2^21); the pieces alike, of whole tiles.
+int64_t piece_of(int64_t T, int64_t V)
+{
+    const int64_t most = std::min<int64_t>(std::max<int64_t>(((int64_t)1 << 27) / std::max<int64_t>(T, 1), 1024), 1 << 20);
+    const int64_t pieces = (V + most - 1) / most;
+    return std::min(V, abi::up((V + pieces - 1) / pieces, 256));
+}
+
+template <class E>
+struct BackwardSpace {
+    E *x, *w, *xt, *wt, *dl, *dlt;
+    RowInfo* info;
+    int* column;
+    float *sums, *factor, *partial;
+    int64_t Tp, Vp, piece, rows, bytes;
+    bool copy_x, copy_w;
+    BackwardSpace(void* base, const void* X, const void* W, int64_t T, int64_t D, int64_t V, int64_t ldx, int64_t ldw)
+    {
+        abi::Carve c(base);
+        copy_x = D % 8 || !vec8(X, ldx);
+        copy_w = D % 8 || !vec8(W, ldw);
+        const int64_t ld = abi::up(D, kLine);
+        piece = piece_of(T, V);
+        Tp = abi::up(T, kLine);
+        Vp = abi::up(piece, kLine);
+        rows = abi::up(T, 256);
+        x = copy_x ? c.take<E>(T * ld) : nullptr;
+        w = copy_w ? c.take<E>(piece * ld) : nullptr;
+        xt = c.take<E>(D * Tp);
+        wt = c.take<E>(D * Vp);
+        dl = c.take<E>(T * Vp);
+        dlt = c.take<E>(piece * Tp);
+        info = c.take<RowInfo>(rows);
+        column = c.take<int>(rows);
+        sums = c.take<float>((T + 15) / 16 * ((D + 15) / 16) * kBlockFloats);
+        factor = c.take<float>(1);
+        partial = c.take<float>(kSplitFloats);
+        bytes = c.used();
+    }
+};
+
+template <class E>
+int backward(const float* dloss, const E* X, const E* W, const int64_t* target, const float* saved, E* dX, E* dW, int64_t T, int64_t D,
+             int64_t V, int64_t dloss_stride, int64_t ldx, int64_t ldw, int64_t target_stride, int64_t lddx, int64_t lddw, int64_t ignore,
+             void* workspace, hipStream_t stream)
+{
+    const BackwardSpace<E> w(workspace, X, W, T, D, V, ldx, ldw);
+    int rc;
+    Copied<E> cx{X, (int)ldx};
+    if (w.copy_x && (rc = cx.enqueue(w.x, T, D, stream))) return rc;
+    for (int64_t v0 = 0; v0 < V; v0 += w.piece) {
+        const int64_t n = std::min(w.piece, V - v0);
+        const E* const W0 = W + v0 * ldw;
+        Prepare<E> p = {};
+        if (v0 == 0) {
+            p.rows = {dloss, saved, target, dloss_stride, target_stride, ignore, (int)T, (int)w.rows, (int)V, w.info, w.column, w.factor};
+            p.x = {{X, w.xt, ldx, w.Tp, (int)T, (int)D, (int)w.Tp, (int)vec4(X, ldx)}, target, target_stride, ignore};
+            p.first = 1;
+        }
+        p.w = {W0, w.wt, ldw, w.Vp, (int)n, (int)D, (int)abi::up(n, kLine), (int)vec4(W0, ldw)};
+        p.second = p.first + (int)p.x.turn.tiles();
+        const int64_t groups = p.second + (T > 0 ? p.w.tiles() : 0);
+        if (groups > 0) {
+            hipLaunchKernelGGL(loss_prepare<E>, dim3((unsigned)groups), dim3(relayout::kThreads), 0, stream, p);
+            if ((rc = (int)hipGetLastError())) return rc;
+        }
+        if (T > 0) {
+            Copied<E> cw{W0, (int)ldw};
+            if (w.copy_w && (rc = cw.enqueue(w.w, n, D, stream))) return rc;
+            DlOp<E> op = {};
+            op.X = cx.at;
+            op.W = cw.at;
+            op.dl = w.dl;
+            op.dlt = w.dlt;
+            op.info = w.info;
+            op.column = w.column;
+            op.M = (int)T;
+            op.N = (int)n;
+            op.K = (int)abi::up(D, 8);
+            op.lda = cx.ld;
+            op.ldb = cw.ld;
+            op.ldd = (int)w.Vp;
+            op.ldt = (int)w.Tp;
+            op.first = (int)v0;
+            if ((rc = launch_grid<E>(op, T, n, 1, 1, op.K, nullptr, stream))) return rc;
+            if (D > 0) {
+                AddOp<E> add = {};
+                add.A = w.dl;
+                add.B = w.wt;
+                add.sums = w.sums;
+                add.M = (int)T;
+                add.N = (int)D;
+                add.K = (int)abi::up(n, 8);
+                add.lda = add.ldb = (int)w.Vp;
+                add.fresh = v0 == 0;
+                if ((rc = launch_grid<E>(add, T, D, 1, 1, add.K, add.K >= kSplitK ? w.partial : nullptr, stream))) return rc;
+            }
+        }
+        if (D > 0) {
+            auto product = [&](auto op) {
+                op.factor = w.factor;
+                op.A[0] = w.dlt;
+                op.B = w.xt;
+                op.C[0] = dW + v0 * lddw;
+                op.M = (int)n;
+                op.N = (int)D;
+                op.K = (int)abi::up(T, 8);
+                op.lda = op.ldb = (int)w.Tp;
+                op.ldc[0] = (int)lddw;
+                return launch_grid<E>(op, n, D, 1, 1, op.K, op.K >= kSplitK ? w.partial : nullptr, stream);
+            };
+            const bool eights = vec8(dW, lddw) && D % 8 == 0;
+            rc = eights ? product(StoreOp<E, true, true>{}) : product(StoreOp<E, false, true>{});
+            if (rc) return rc;
+        }
+    }
+    if (T > 0 && D > 0) {
+        const int64_t blocks = (T + 15) / 16 * ((D + 15) / 16);
+        const Finish<E> f = {w.sums, dloss, w.info, w.column, W, dX, dloss_stride, ldw, lddx, (int)T, (int)D, (int)vec4(W, ldw),
+                             (int)vec4(dX, lddx)};
+        hipLaunchKernelGGL(loss_finish<E>, dim3((unsigned)std::min<int64_t>((blocks + 3) / 4, 65536)), dim3(256), 0, stream, f);
+        rc = (int)hipGetLastError();
+        if (rc) return rc;
+    }
+    return hipSuccess;
+}
+
+bool good_sizes(int64_t T, int64_t D, int64_t V)
+{
+    return T >= 0 && T <= abi::kMaxDim - 256 && D >= 0 && D <= abi::kMaxPitch - 63 && V > 0 && V <= abi::kMaxDim - 256;
+}
+bool good_backward_sizes(int64_t T, int64_t D, int64_t V) { return good_sizes(T, D, V) && T <= abi::kMaxPitch - 63; }
+bool good_stride(int64_t s) { return s >= 0 && s <= (int64_t)1 << 31; }
+
+}  // namespace
+
+extern "C" {
+
+int linear_cross_entropy_version(void) { return LINEAR_CROSS_ENTROPY_VERSION; }
+
+int64_t linear_cross_entropy_workspace(const void* X, const void* W, int64_t T, int64_t D, int64_t V, int64_t ldx, int64_t ldw)
+{
+    if (!good_sizes(T, D, V)) return -1;
+    return ForwardSpace<_Float16>(nullptr, X, W, T, D, V, ldx, ldw).bytes;
+}
+
+int64_t linear_cross_entropy_backward_workspace(const void* X, const void* W, int64_t T, int64_t D, int64_t V, int64_t ldx, int64_t ldw)
+{
+    if (!good_backward_sizes(T, D, V)) return -1;
+    return BackwardSpace<_Float16>(nullptr, X, W, T, D, V, ldx, ldw).bytes;
+}
+
+int linear_cross_entropy(const void* X, const void* W, const int64_t* target, float* loss, float* saved, int64_t T, int64_t D, int64_t V,
+                         int64_t ldx, int64_t ldw, int64_t target_stride, int32_t type, int64_t ignore_index, void* workspace,
+                         int64_t workspace_bytes, hipStream_t stream)
+{
+    using namespace abi;
+    if (!good_sizes(T, D, V) || !good_pitch(ldx, D) || !good_pitch(ldw, D) || !good_stride(target_stride)) return hipErrorInvalidValue;
+    if (type != LINEAR_CROSS_ENTROPY_F16 && type != LINEAR_CROSS_ENTROPY_BF16) return hipErrorInvalidValue;
+    if (T == 0) return hipSuccess;
+    if (!nt::fits(T, V, 1)) return hipErrorInvalidValue;
+    if (!good_pointer(X, T, D, 2) || !good_pointer(W, V, D, 2) || !good_pointer(target, T, 1, 8) || !good_pointer(loss, T, 1, 4) ||
+        (uintptr_t)saved % 4 || (uintptr_t)workspace % 16)
+        return hipErrorInvalidValue;
+    const int64_t need = linear_cross_entropy_workspace(X, W, T, D, V, ldx, ldw);
+    if (!workspace || workspace_bytes < need) return hipErrorInvalidValue;
+    const Range in[] = {Range(X, T, D, ldx, 2), Range(W, V, D, ldw, 2), Range(target, T, 1, target_stride, 8)};
+    const Range out[] = {Range(loss, 1, T, 0, 4), Range(saved, 1, saved ? 3 * T : 0, 0, 4), Range(workspace, 1, need, 0, 1)};
+    for (int i = 0; i < 3; ++i) {
+        for (const Range& r : in)
+            if (out[i].meets(r)) return hipErrorInvalidValue;
+        for (int k = 0; k < i; ++k)
+            if (out[i].meets(out[k])) return hipErrorInvalidValue;
+    }
+#define FORWARD(E) \
+    forward<E>((const E*)X, (const E*)W, target, loss, saved, T, D, V, ldx, ldw, target_stride, ignore_index, workspace, stream)
+    return type == LINEAR_CROSS_ENTROPY_F16 ? FORWARD(_Float16) : FORWARD(__bf16);
+#undef FORWARD
+}
+
+int linear_cross_entropy_backward(const float* dloss, const void* X, const void* W, const int64_t* target, const float* saved, void* dX,
+                                  void* dW, int64_t T, int64_t D, int64_t V, int64_t dloss_stride, int64_t ldx, int64_t ldw,
+                                  int64_t target_stride, int64_t lddx, int64_t lddw, int32_t type, int64_t ignore_index, void* workspace,
+                                  int64_t workspace_bytes, hipStream_t stream)
+{
+    using namespace abi;
+    if (!good_backward_sizes(T, D, V) || !good_pitch(ldx, D) || !good_pitch(ldw, D) || !good_pitch(lddx, D) || !good_pitch(lddw, D) ||
+        !good_stride(target_stride) || !good_stride(dloss_stride))
+        return hipErrorInvalidValue;
+    if (type != LINEAR_CROSS_ENTROPY_F16 && type != LINEAR_CROSS_ENTROPY_BF16) return hipErrorInvalidValue;
+    if (!nt::fits(T, piece_of(T, V), 1) || !nt::fits(T, D, 1) || !nt::fits(piece_of(T, V), D, 1)) return hipErrorInvalidValue;
+    // (the transposes' tiles, and the one workgroup beside them)
+    const int64_t tiles = (up(piece_of(T, V), kLine) / 64 + up(T, kLine) / 64) * ((D + 63) / 64);
+    if (!good_grid(tiles + 1, relayout::kThreads)) return hipErrorInvalidValue;
+    if (!good_pointer(dloss, T, 1, 4) || !good_pointer(X, T, D, 2) || !good_pointer(W, V, D, 2) || !good_pointer(target, T, 1, 8) ||
+        !good_pointer(saved, T, 1, 4) || !good_pointer(dX, T, D, 2) || !good_pointer(dW, V, D, 2) || (uintptr_t)workspace % 16)
+        return hipErrorInvalidValue;
+    const int64_t need = linear_cross_entropy_backward_workspace(X, W, T, D, V, ldx, ldw);
+    if (!workspace || workspace_bytes < need) return hipErrorInvalidValue;
+    const Range in[] = {Range(dloss, T, 1, dloss_stride, 4), Range(X, T, D, ldx, 2), Range(W, V, D, ldw, 2),
+                        Range(target, T, 1, target_stride, 8), Range(saved, 1, 3 * T, 0, 4)};
+    const Range out[] = {Range(dX, T, D, lddx, 2), Range(dW, V, D, lddw, 2), Range(workspace, 1, need, 0, 1)};
+    for (int i = 0; i < 3; ++i) {
+        for (const Range& r : in)
+            if (out[i].meets(r)) return hipErrorInvalidValue;
+        for (int k = 0; k < i; ++k)
+            if (out[i].meets(out[k])) return hipErrorInvalidValue;
+    }
+#define BACKWARD(E)                                                                                                                  \
+    backward<E>(dloss, (const E*)X, (const E*)W, target, saved, (E*)dX, (E*)dW, T, D, V, dloss_stride, ldx, ldw, target_stride, lddx, \
+                lddw, ignore_index, workspace, stream)
+    return type == LINEAR_CROSS_ENTROPY_F16 ? BACKWARD(_Float16) : BACKWARD(__bf16);
+#undef BACKWARD
+}
+
+}  // extern "C"

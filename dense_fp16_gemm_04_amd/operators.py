@@ -61,6 +61,13 @@ SIGNATURES = {
         "dropout": ([_p] * 3 + [_i64] * 5 + [_i32, ctypes.c_double, _u64, _u64, _p, _p], _int),
         "dropout_version": ([], _int),
     },
+    "linear_cross_entropy": {
+        "linear_cross_entropy": ([_p] * 5 + [_i64] * 6 + [_i32, _i64, _p, _i64, _p], _int),
+        "linear_cross_entropy_backward": ([_p] * 7 + [_i64] * 9 + [_i32, _i64, _p, _i64, _p], _int),
+        "linear_cross_entropy_workspace": ([_p] * 2 + [_i64] * 5, _i64),
+        "linear_cross_entropy_backward_workspace": ([_p] * 2 + [_i64] * 5, _i64),
+        "linear_cross_entropy_version": ([], _int),
+    },
 }
 
 ACTIVATIONS = {"silu": 0, "gelu_tanh": 1}

@@ -1,9 +1,10 @@
 """ctypes bindings of the operators around a training step's products (argument
-marshalling only): the layer norm, and dropout with the sum of a residual, each
-with its backward pass.
+marshalling only): the layer norm, dropout with the sum of a residual, and the
+loss over a vocabulary, each with its backward pass.
 
-``liblayer_norm.so`` and ``libdropout.so`` with the C ABIs of
-``include/layer_norm.h`` and ``include/dropout.h``.  As in ``operators``: PyTorch supplies device
+``liblayer_norm.so``, ``libdropout.so`` and ``liblinear_cross_entropy.so`` with
+the C ABIs of ``include/layer_norm.h``, ``include/dropout.h`` and
+``include/linear_cross_entropy.h``.  As in ``operators``: PyTorch supplies device
 memory and the current stream, a missing library raises ``RuntimeError`` and a
 refused call ``TypeError``, ``ValueError`` or ``GemmError``, matrices may be
 views whose rows' elements are adjacent, and nothing takes part in autograd: a
@@ -15,7 +16,7 @@ from __future__ import annotations
 import torch
 
 from .binding import GemmError
-from .operators import _TYPES_AND_F32, _call, _pitch, _without_gradients, _workspace, load
+from .operators import _TYPES, _TYPES_AND_F32, _call, _pitch, _without_gradients, _workspace, load
 
 _WORDS = 1 << 64
 
@@ -176,3 +177,106 @@ def dropout(x, p: float, seed, offset: int = 0, residual=None, out=None):
 def dropout_backward(dy, p: float, seed, offset: int = 0, out=None):
     """x's gradient for the gradient dy of ``dropout``'s result with the same p, seed and offset; ``out`` may be dy."""
     return _dropout(dy, p, seed, offset, None, out)
+
+
+# ------------------------------------------------- linear_cross_entropy --
+
+def _strided(name, t, dtype, device, size):
+    """The stride of t, `size` elements of `dtype` on `device`, any distance apart."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError("%s must be a torch tensor" % name)
+    if t.dtype != dtype:
+        raise TypeError("%s must be %s, got %s" % (name, str(dtype).replace("torch.", ""), str(t.dtype).replace("torch.", "")))
+    if t.dim() != 1 or t.shape[0] != size:
+        raise ValueError("%s must be [%d], got %s" % (name, size, tuple(t.shape)))
+    if t.get_device() != device:
+        raise ValueError("%s must be on the first operand's GPU" % name)
+    return t.stride(0) if size > 1 else 1
+
+
+def _check_loss(x, w, target):
+    """(device, T, D, V, pitches of x and w, stride of target)."""
+    ldx = _pitch("x", x, _TYPES)
+    device = x.get_device()
+    ldw = _pitch("w", w, (x.dtype,), device)
+    T, D = x.shape
+    V, K = w.shape
+    if K != D or V == 0:
+        raise ValueError("need x [T, D] and w [V, D] with V above 0, got %s and %s" % (tuple(x.shape), tuple(w.shape)))
+    return device, T, D, V, ldx, ldw, _strided("target", target, torch.int64, device, T)
+
+
+def _loss(x, w, target, ignore_index, out, train):
+    device, T, D, V, ldx, ldw, stride = _check_loss(x, w, target)
+    if out is None:
+        out = x.new_empty(T, dtype=torch.float32)
+    else:
+        _vector("out", out, (torch.float32,), device, T)
+    saved = x.new_empty((T, 3), dtype=torch.float32) if train else None
+    px, pw = x.data_ptr(), w.data_ptr()
+    nbytes = load("linear_cross_entropy").linear_cross_entropy_workspace(px, pw, T, D, V, ldx, ldw)
+    if nbytes < 0:
+        raise GemmError("linear_cross_entropy", 1)
+    keep, workspace = _workspace(x, nbytes)
+    _call("linear_cross_entropy", "linear_cross_entropy", device, px, pw, target.data_ptr(), out.data_ptr(),
+          saved.data_ptr() if train else None, T, D, V, ldx, ldw, stride, _TYPES[x.dtype], int(ignore_index), workspace, nbytes)
+    return out, saved
+
+
+def linear_cross_entropy(x, w, target, ignore_index: int = -100, out=None):
+    """loss[t] = log sum_v exp(l[t, v]) - l[t, target[t]] of l = x @ w^T, for x [T, D], w [V, D] and int64 target [T].
+
+    float16 or bfloat16; losses float32, one for each token, 0 where target is
+    ``ignore_index`` (whatever x holds there), NaN where it is neither that nor
+    in 0 .. V - 1.  l is summed in 32 bits and not kept.  Enqueued on the
+    current stream of x's device; returns ``out``.  Not differentiated by
+    autograd: ``linear_cross_entropy_train`` and
+    ``linear_cross_entropy_backward`` are its training form.
+    """
+    loss = _loss(x, w, target, ignore_index, out, False)[0]
+    if out is None and (x.requires_grad or w.requires_grad):
+        return _without_gradients(loss, "linear_cross_entropy has no gradients in autograd: use linear_cross_entropy_train and "
+                                  "linear_cross_entropy_backward", x, w)
+    return loss
+
+
+def linear_cross_entropy_train(x, w, target, ignore_index: int = -100, out=None):
+    """``linear_cross_entropy`` that also keeps what its backward pass reads: (out, saved).
+
+    ``saved`` is float32 [T, 3]: each row's largest l, the sum of exp(l -
+    largest), and the target's l.  Neither requires gradients, whatever the
+    inputs do.
+    """
+    return _loss(x, w, target, ignore_index, out, True)
+
+
+def linear_cross_entropy_backward(dloss, x, w, target, saved, ignore_index: int = -100, out=None):
+    """The gradients (dx, dw) of ``linear_cross_entropy_train`` for the gradient dloss [T] (float32) of its losses.
+
+    dloss may be one number expanded.  ``out``: two matrices to write them to,
+    or None for new ones.  They are written, not added to.
+    """
+    device, T, D, V, ldx, ldw, stride = _check_loss(x, w, target)
+    types = (x.dtype,)
+    sg = _strided("dloss", dloss, torch.float32, device, T)
+    if not isinstance(saved, torch.Tensor) or saved.dtype != torch.float32 or tuple(saved.shape) != (T, 3) \
+            or not saved.is_contiguous() or saved.get_device() != device:
+        raise ValueError("saved must be what linear_cross_entropy_train returned for x, w and target")
+    if out is None:
+        dx, dw = x.new_empty((T, D)), x.new_empty((V, D))
+        lddx = lddw = D
+    else:
+        if len(out) != 2:
+            raise ValueError("out must be the two matrices dx and dw")
+        dx, dw = out
+        lddx = _pitch("out's dx", dx, types, device, (T, D))
+        lddw = _pitch("out's dw", dw, types, device, (V, D))
+    px, pw = x.data_ptr(), w.data_ptr()
+    nbytes = load("linear_cross_entropy").linear_cross_entropy_backward_workspace(px, pw, T, D, V, ldx, ldw)
+    if nbytes < 0:
+        raise GemmError("linear_cross_entropy_backward", 1)
+    keep, workspace = _workspace(x, nbytes)
+    _call("linear_cross_entropy", "linear_cross_entropy_backward", device, dloss.data_ptr(), px, pw, target.data_ptr(),
+          saved.data_ptr(), dx.data_ptr(), dw.data_ptr(), T, D, V, sg, ldx, ldw, stride, lddx, lddw, _TYPES[x.dtype],
+          int(ignore_index), workspace, nbytes)
+    return dx, dw

@@ -126,3 +126,77 @@ def dropout(x, p, seed, offset=0, residual=None):
     scaled = torch.where(keep, x * (65536 / (65536 - d) if d < 65536 else 0.0), torch.zeros((), dtype=torch.float64))
     y = scaled if residual is None else scaled + residual.double().cpu()
     return y, EPS * (scaled.abs() + y.abs()) + rounded(y, t)
+
+
+# ------------------------------------------------- linear_cross_entropy --
+
+def _wander(squares, n):
+    """Error of 32-bit sums of n terms whose squares add up to `squares` (as in _tight)."""
+    return (n / 32 + 24) * 2.0 ** -23 * 3 * squares.sqrt()
+
+
+def loss(x, w, target, ignore=-100):
+    """(loss, bound, parts) on x's device; parts are for loss_gradients.
+
+    Of the sum of exponentials, all positive: each term is off by what its
+    logarithm is, and every addition (34 in a wave, then one for each join,
+    whose two exponentials count four) by EPS of the whole.
+    """
+    x, w = x.double(), w.double()
+    T, D = x.shape
+    V = w.shape[0]
+    valid = target != ignore
+    x = torch.where(valid[:, None], x, torch.zeros_like(x))  # (what a token that is ignored holds says nothing)
+    l = x @ w.T
+    l_off = _wander(x.square() @ w.square().T, D)
+    top = l.max(1, keepdim=True).values
+    e = (l - top).exp()
+    s = e.sum(1, keepdim=True)
+    p = e / s
+    at = torch.where(valid, target, torch.zeros_like(target))[:, None]
+    adds = 34 + 4 * (V // 4096 + 9)
+    s_rel = (p * (l_off + (3 * (top - l) + 4) * EPS)).sum(1, keepdim=True) + adds * EPS + l_off.gather(1, l.argmax(1, keepdim=True))
+    tl = l.gather(1, at)
+    y = (top - tl + s.log())[:, 0]
+    bound = (s_rel + l_off.gather(1, at) + 3 * EPS * (top - tl + s.log().abs() + 1))[:, 0] + 2 * EPS * y.abs()
+    zero = torch.zeros_like(y)
+    return torch.where(valid, y, zero), torch.where(valid, bound, zero), (x, w, valid, at, p, l, top, s, s_rel, l_off)
+
+
+def loss_gradients(dloss, t, parts):
+    """((dx, dw), their bounds); t: the operands' type."""
+    x, w, valid, at, p, l, top, s, s_rel, l_off = parts
+    T, D = x.shape
+    V = w.shape[0]
+    rel, absolute = half_step(t)
+    g = torch.where(valid, dloss.double(), torch.zeros_like(dloss.double()))[:, None]
+    p_off = p * (l_off + s_rel + (5 * (top - l) + 5 * s.log().abs() + 80) * EPS)
+    dl = p.clone()
+    dl.scatter_add_(1, at, -torch.ones_like(s))
+    p_off.scatter_add_(1, at, torch.full_like(s, 2 * EPS))
+    small = 2.0 ** -40 if t == torch.float16 else absolute
+    most = float(g.abs().max()) if T else 0.0
+    rounding = rel * dl.abs() + small
+    rounding.scatter_(1, at, torch.full_like(s, 4 * EPS))  # (what it takes there is put back)
+
+    def sums(a, off, rnd, b, n, factor):
+        y = a @ b
+        walk = _wander((a.abs() + rnd).square() @ b.square(), n)
+        bound = off @ b.abs() + 6 * (rnd.square() @ b.square()).sqrt() + walk
+        y, bound = factor * y, factor.abs() * bound * (1 + 4 * EPS)
+        return y, bound + rel * (1 + rel) * y.abs() + absolute
+
+    one = torch.ones((), dtype=torch.float64, device=x.device)
+    dx = sums(dl, p_off, rounding, w, V, g)
+    gd = g * dl
+    dw = sums(gd.T, (g.abs() * p_off).T + 4 * EPS * gd.abs().T, (rel * gd.abs() + most * small).T, x, T, one)
+    return (dx[0], dw[0]), (dx[1], dw[1])
+
+
+def assert_near(got, want, bound, what=""):
+    """assert_within on the device that the values are on."""
+    bad = ~((got.double() - want).abs() <= bound)
+    if bad.any():
+        i = tuple(int(v) for v in bad.nonzero()[0])
+        raise AssertionError("%s: %d of %d outside; first at %s: got %r, want %r, bound %r" % (
+            what, int(bad.sum()), bad.numel(), i, float(got[i]), float(want[i]), float(bound[i])))

@@ -206,3 +206,108 @@ def test_norm_bounds_reject_what_is_wrong(cols, t):
     if cols <= 300 or t == torch.float32 and cols <= 5000:
         assert outside(lost, dx, bounds[0])
     assert outside(dw - g[0] * h[0], dw, bounds[1]) and outside(db - g[0], db, bounds[2])
+
+
+# ------------------------------------------------- linear_cross_entropy --
+
+def loss_args(**kw):
+    a = dict(X=A, W=B, target=C, loss=D, saved=E, T=4, D=16, V=8, ldx=16, ldw=16, stride=1, type=0, ignore=-100, ws=W, ws_bytes=1 << 25,
+             stream=None)
+    assert set(kw) <= set(a)
+    a.update(kw)
+    return list(a.values())
+
+
+@pytest.mark.parametrize("kw", [
+    dict(T=-1), dict(D=-1), dict(V=-1), dict(V=0), dict(T=1 << 31), dict(V=1 << 31), dict(D=1 << 21, ldx=1 << 21, ldw=1 << 21), dict(ldx=15),
+    dict(ldw=15), dict(ldx=1 << 21), dict(stride=-1), dict(stride=(1 << 31) + 1), dict(type=2), dict(type=-1), dict(X=None), dict(W=None),
+    dict(target=None), dict(loss=None), dict(X=A + 1), dict(W=B + 1), dict(target=C + 4), dict(loss=D + 2), dict(saved=E + 2),
+    dict(ws=None), dict(ws_bytes=64), dict(ws=W + 8), dict(loss=A), dict(loss=B), dict(loss=C), dict(saved=A), dict(saved=D), dict(ws=A),
+    dict(ws=D), dict(D=512, ldx=512, ldw=512, ws_bytes=1 << 20), dict(T=1 << 28, V=1 << 28, ws_bytes=1 << 60),
+])
+def test_loss_refuses(kw):
+    assert operators.load("linear_cross_entropy").linear_cross_entropy(*loss_args(**kw)) == INVALID
+
+
+def loss_back_args(**kw):
+    far = 1 << 40
+    a = dict(dloss=A, X=B, W=C, target=D, saved=E, dX=F, dW=G, T=4, D=16, V=8, sg=1, ldx=16, ldw=16, st=1, lddx=16, lddw=16, type=0,
+             ignore=-100, ws=far, ws_bytes=1 << 28, stream=None)
+    assert set(kw) <= set(a)
+    a.update(kw)
+    return list(a.values())
+
+
+@pytest.mark.parametrize("kw", [
+    dict(T=-1), dict(D=-1), dict(V=0), dict(T=(1 << 21) - 63), dict(V=1 << 31), dict(ldx=15), dict(ldw=15), dict(lddx=15), dict(lddw=15),
+    dict(sg=-1), dict(st=-1), dict(type=2), dict(dloss=None), dict(X=None), dict(W=None), dict(target=None), dict(saved=None), dict(dX=None),
+    dict(dW=None), dict(dloss=A + 2), dict(X=B + 1), dict(target=D + 4), dict(saved=E + 2), dict(dX=F + 1), dict(ws=None), dict(ws_bytes=64),
+    dict(ws=(1 << 40) + 8), dict(dX=B), dict(dX=G), dict(dW=C), dict(dW=A), dict(dX=E), dict(ws=A), dict(ws=G),
+])
+def test_loss_backward_refuses(kw):
+    assert operators.load("linear_cross_entropy").linear_cross_entropy_backward(*loss_back_args(**kw)) == INVALID
+
+
+def test_loss_empty_and_workspace():
+    lib = operators.load("linear_cross_entropy")
+    assert lib.linear_cross_entropy(*loss_args(T=0, X=None, target=None, loss=None, ws=None, ws_bytes=0)) == 0
+    assert lib.linear_cross_entropy_workspace(A, B, 0, 16, 8, 16, 16) == 0
+    assert lib.linear_cross_entropy_workspace(A, B, 4, 16, 0, 16, 16) == -1
+    plain_bytes = lib.linear_cross_entropy_workspace(A, B, 64, 64, 1000, 64, 64)
+    assert 0 < plain_bytes < 1 << 20
+    assert lib.linear_cross_entropy_workspace(A, B + 2, 64, 64, 1000, 64, 64) >= plain_bytes + 1000 * 64 * 2
+    assert lib.linear_cross_entropy_workspace(A, B, 64, 63, 1000, 64, 64) >= plain_bytes + 1064 * 64 * 2
+    assert lib.linear_cross_entropy_backward_workspace(A, B, 4, 16, 8, 16, 16) > 0
+    assert lib.linear_cross_entropy_backward_workspace(A, B, 1 << 21, 16, 8, 16, 16) == -1
+    # a piece of the vocabulary at a time: far below what the outputs would take
+    T, D, V = 8192, 4096, 131072
+    assert lib.linear_cross_entropy_workspace(A, B, T, D, V, D, D) < T * V // 4
+    assert lib.linear_cross_entropy_backward_workspace(A, B, T, D, V, D, D) < T * V
+
+
+def test_loss_bindings_refuse_host_tensors():
+    x, w = torch.zeros(4, 16, dtype=torch.float16), torch.zeros(8, 16, dtype=torch.float16)
+    target = torch.zeros(4, dtype=torch.int64)
+    for call in (lambda: fw.linear_cross_entropy(x, w, target), lambda: fw.linear_cross_entropy_train(x, w, target),
+                 lambda: fw.linear_cross_entropy_backward(torch.zeros(4), x, w, target, torch.zeros(4, 3))):
+        with pytest.raises(ValueError, match="GPU"):
+            call()
+
+
+@pytest.mark.parametrize("t", ["fp16", "bf16"])
+@pytest.mark.parametrize("shape", [(5, 16, 40), (60, 72, 300)], ids=str)
+def test_loss_bounds_reject_what_is_wrong(shape, t):
+    """Zeros, a lost column of the vocabulary, a lost token, a one-hot that is missing, and gradients of another token's dloss."""
+    T, D, V = shape
+    t = plain.TYPES[t]
+    gen = torch.Generator().manual_seed(V)
+    x, w = torch.randn(T, D, generator=gen).to(t), (torch.randn(V, D, generator=gen) * D ** -0.5).to(t)
+    target, g = torch.randint(0, V, (T,), generator=gen), torch.rand(T, generator=gen) + 0.1
+    y, bound, parts = plain.loss(x, w, target)
+    (dx, dw), (bx, bw) = plain.loss_gradients(g, t, parts)
+
+    def outside(got, want, bound):
+        return bool(((got - want).abs() > bound).any())
+
+    for want, b in ((y, bound), (dx, bx), (dw, bw)):
+        assert outside(torch.zeros_like(want), want, b)
+    p, w64, x64 = parts[4], w.double(), x.double()
+    assert outside(y + (1 - p[:, 0]).log(), y, bound)
+    assert outside(dx - g.double()[:, None] * p[:, :1] * w64[:1], dx, bx)
+    assert outside(dx + g.double()[:, None] * w64[target], dx, bx) and outside(dx.roll(1, 0), dx, bx)
+    dl = g.double()[:, None] * (p - torch.nn.functional.one_hot(target, V))
+    assert outside(dw - dl[:1].T @ x64[:1], dw, bw)
+
+
+def test_plain_loss_gradients_match_differences():
+    gen = torch.Generator().manual_seed(9)
+    x, w = torch.randn(6, 5, generator=gen, dtype=torch.float64), torch.randn(11, 5, generator=gen, dtype=torch.float64)
+    target = torch.tensor([0, 3, -100, 10, 3, 7])
+    g = torch.randn(6, generator=gen, dtype=torch.float64)
+    _, _, parts = plain.loss(x, w, target)
+    grads, _ = plain.loss_gradients(g, torch.float16, parts)
+    for i in range(2):
+        v = torch.randn((x, w)[i].shape, generator=gen, dtype=torch.float64)
+        ends = [(plain.loss(*(u + s * 1e-6 * v if k == i else u for k, u in enumerate((x, w))), target)[0] * g).sum() for s in (1, -1)]
+        slope = float(ends[0] - ends[1]) / 2e-6
+        assert abs(slope - float((grads[i] * v).sum())) <= 1e-6 * max(1.0, abs(slope))
