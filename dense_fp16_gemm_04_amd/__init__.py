@@ -48,13 +48,14 @@ _TRAINING = ("layer_norm", "layer_norm_train", "layer_norm_backward", "dropout",
 
 
 def __getattr__(name):
+    # (the first time; then it is the module's own)
     if name in _OPERATORS:
-        from . import operators
-        return getattr(operators, name)
-    if name in _TRAINING:
-        from . import training
-        return getattr(training, name)
-    if name in __all__:
-        from . import binding
-        return getattr(binding, name)
-    raise AttributeError(name)
+        from . import operators as module
+    elif name in _TRAINING:
+        from . import training as module
+    elif name in __all__:
+        from . import binding as module
+    else:
+        raise AttributeError(name)
+    value = globals()[name] = getattr(module, name)
+    return value

@@ -259,6 +259,12 @@ constexpr float kShift<_Float16> = 15.0f;
 // the minimum, which takes the number of a number and NaN, makes dl zero whatever
 // l is.  So it does where l is of a column that is not there, and of columns that
 // are l is no larger than top but by another order of summation.
+//
+// The target's dl is most of a row's size, and its rounding most of dX's error
+// where few terms are large.  Each row of dl is therefore held times what makes
+// `hit` a number of the type (1 and half a step at most), which `back`, the factor to the row's
+// sums, and `weight` take out again: dX (300 x 200 x 513, binary16) 2.28e-4 off,
+// its own rounding, and 2.73e-4 without.
 struct RowInfo {
     float top, bias, weight, hit;
 };
@@ -272,6 +278,7 @@ struct RowNumbers {
     int M, Mp, N;  // Mp: rows of whole tiles
     RowInfo* info;
     int* column;    // of the target, or -1
+    float* back;    // to dX's sums
     float* factor;  // to dW's sums
 
     __device__ __forceinline__ void run() const
@@ -290,20 +297,25 @@ struct RowNumbers {
         if (threadIdx.x == 0) *factor = most * exp2f(-kShift<E>);
         for (int row = threadIdx.x; row < Mp; row += relayout::kThreads) {
             RowInfo r = {0.0f, -INFINITY, 0.0f, 0.0f};
+            float b = 0.0f;
             int at = -1;
             if (row < M) {
                 const int64_t c = target[row * target_stride];
                 if (c != ignore) {
                     const float top = saved[3 * (int64_t)row], sum = saved[3 * (int64_t)row + 1], tl = saved[3 * (int64_t)row + 2];
                     const bool there = c >= 0 && c < N;
+                    const float g = dloss[row * dloss_stride], hit = (expf(tl - top) - sum) / sum * exp2f(kShift<E>);
+                    r.hit = (float)(E)hit;
+                    const float times = r.hit == 0.0f ? 1.0f : r.hit / hit;
                     r.top = top;
-                    r.bias = there ? kShift<E> - log2f(sum) : NAN;
-                    r.weight = dloss[row * dloss_stride] / most;
-                    r.hit = (expf(tl - top) - sum) / sum * exp2f(kShift<E>);
+                    r.bias = there ? kShift<E> - log2f(sum) + log2f(times) : NAN;
+                    r.weight = g / most / times;
+                    b = g * exp2f(-kShift<E>) / times;
                     at = there ? (int)c : -1;
                 }
             }
             info[row] = r;
+            back[row] = b;
             column[row] = at;
         }
     }
@@ -421,32 +433,54 @@ struct DlOp {
             hit[i] = rows[i * 16].hit;
             weight[i] = rows[i * 16].weight;
         }
-        constexpr int ROUNDS = T::BM * T::BN * 2 > T::STAGE_MAX ? 2 : 1, IR = T::FM / ROUNDS, CR = T::WTN / ROUNDS;
-        // (Columns past N, up to a chunk of eight, hold numbers, which meet zeros.
-        // A row without a target among the round's columns gets a value that it
-        // has: a branch would take all accumulators out of their registers.)
-        write_rows<T, T::FN, true>([&](int i, int j) { return round4<E>(dl_of(i, j)); },
-                                   rows_at(dl, t.m0, M, T::BM, ldd, t.n0, (N + 7) & ~7), lane, wave, s0, s1,
-                                   [&](const Image<T::BN>& image, int h) __attribute__((always_inline)) {
+        // Both images at once, so that each exponential is taken once; of 256 x 256
+        // tiles, whose LDS holds a quarter of both, in four rounds of 32 rows of
+        // each wave.  (Row-major first, then transposed with the exponentials
+        // taken again, two rounds each: 107 us for 1000 x 1032 x 32001, and 98.)
+        constexpr int ROUNDS = T::BM * T::BN * 4 > T::STAGE_MAX ? 4 : 1, IR = T::FM / ROUNDS, RW = T::WTM / ROUNDS;
+        constexpr int TC = T::BM / ROUNDS, TCH = TC / 8, RPI = 64 / TCH, ITERS = T::BN / RPI / T::WAVES;
+        static_assert(T::BM * T::BN * 4 <= ROUNDS * T::STAGE_MAX && ITERS * RPI * T::WAVES == T::BN, "both images fit");
+        constexpr int BYTES = T::BM * T::BN * 2 / ROUNDS;
+        const Image<T::BN> image{s0, s0 + 32768};
+        const Image<TC> turned{ROUNDS > 1 ? s1 : s0 + BYTES, s0 + BYTES + 32768};
+        static_assert(ROUNDS == 1 || BYTES == 32768, "an image to a slot");
+        // (columns past N, up to a chunk of eight, hold numbers, which meet zeros)
+        const Rows to = rows_at(dl, t.m0, M, T::BM, ldd, t.n0, (N + 7) & ~7);
+        const Rows to_t = rows_at(dlt, t.n0, N, T::BN, ldt, t.m0, (M + 7) & ~7);
 #pragma unroll
-                                       for (int i = 0; i < IR; ++i) {
-                                           const int k = h * IR + i;
-                                           const bool here = at[k] >= 0 && at[k] < T::WTN;
-                                           image.set((wm * IR + i) * 16 + (ln & 15), wn * T::WTN + (here ? at[k] : 4 * (ln >> 4)),
-                                                     (E)(here ? hit[k] : dl_of(k, 0)[0]));
-                                       }
-                                   });
-        write_turned<T, true>([&](int i, int j) { return round4<E>(dl_of(i, j) * weight[i]); },
-                              rows_at(dlt, t.n0, N, T::BN, ldt, t.m0, (M + 7) & ~7), lane, wave, s0, s1,
-                              [&](const Image<T::BM>& image, int h) __attribute__((always_inline)) {
+        for (int h = 0; h < ROUNDS; ++h) {
+            const int l = pinned(lane), r = l & 15, q = 4 * (l >> 4);
 #pragma unroll
-                                  for (int i = 0; i < T::FM; ++i) {
-                                      const int c = at[i] - h * CR;
-                                      const bool here = c >= 0 && c < CR;
-                                      image.set(wn * CR + (here ? c : 4 * (ln >> 4)), wm * T::WTM + i * 16 + (ln & 15),
-                                                (E)((here ? hit[i] : dl_of(i, h * (T::FN / ROUNDS))[0]) * weight[i]));
-                                  }
-                              });
+            for (int k = 0; k < IR; ++k) {
+                const int i = h * IR + k, row = wm * RW + k * 16;
+                float own = 0.0f;
+#pragma unroll
+                for (int j = 0; j < T::FN; ++j) {
+                    const f32x4 v = dl_of(i, j);
+                    if (j == 0) own = v[0];
+                    image.put(row + r, wn * T::WTN + j * 16 + q, round4<E>(v));
+                    turned.put(wn * T::WTN + j * 16 + q + (l & 3), row + (l & 12), quad_transposed(round4<E>(v * weight[i]), l));
+                }
+                // The target's column.  (A row without one here gets a value that it
+                // has: a branch would take all accumulators out of their registers.)
+                const bool here = at[i] >= 0 && at[i] < T::WTN;
+                const int c = wn * T::WTN + (here ? at[i] : q);
+                const float v = here ? hit[i] : own;
+                image.set(row + r, c, (E)v);
+                turned.set(c, row + r, (E)(v * weight[i]));
+            }
+            lds_barrier<63>();
+            drain<T, T::BN, T::WAVES_M * RW, true>(image, to, [&](int x) { return x / RW * T::WTM + h * RW + x % RW; }, lane, wave);
+            const int ch = l % TCH, m = t.m0 + ch * 8 / RW * T::WTM + h * RW + ch * 8 % RW;
+            const int x0 = (int)as_vector((uint32_t)wave * (ITERS * RPI)) + l / TCH;
+#pragma unroll
+            for (int it = 0; it < ITERS; ++it) {
+                const int x = x0 + it * RPI;
+                __builtin_amdgcn_raw_buffer_store_b128(turned.get(x, ch), to_t.rs, m < to_t.cols ? (uint32_t)x * to_t.pitch + (uint32_t)m * 2u : kOob,
+                                                       0, 0);
+            }
+            lds_barrier<63>();
+        }
     }
 };
 
@@ -513,52 +547,41 @@ struct AddOp {
     }
 };
 
-// dX[t] = dloss[t] 2^-shift sums[t], rounded: a wave to a block of 16 x 16.  What
-// rounding took from the target's dl, most of a row's error where few terms are
-// large, is put back first: dX (300 x 200 x 513, binary16) 2.73e-4 off without.
-template <class E>
-struct Finish {
-    const float *sums, *dloss;
-    const RowInfo* info;
-    const int* column;
-    const E* W;
+// The last piece's: dX[t] = back[t] (A B^T and, MORE, the sums of the pieces before),
+// rounded.  EIGHTS: dX's rows take 16-byte pieces and hold a multiple of eight.
+template <class E, bool EIGHTS, bool MORE>
+struct DxOp : AddOp<E> {
+    using Base = AddOp<E>;
     E* dX;
-    int64_t dloss_stride, ldw, ld;
-    int M, N, vec_w, vec;
-};
+    const float* back;
+    int ldx, pad;
 
-template <class E>
-__global__ void __launch_bounds__(256) loss_finish(const Finish<E> f)
-{
-    const int64_t cols = (f.N + 15) / 16, blocks = (int64_t)((f.M + 15) / 16) * cols;
-    const int lane = threadIdx.x % kWave;
-    for (int64_t b = (int64_t)blockIdx.x * 4 + threadIdx.x / kWave; b < blocks; b += (int64_t)gridDim.x * 4) {
-        f32x4 v = *(const f32x4*)(f.sums + b * kBlockFloats + lane * 4);
-        const int row = (int)(b / cols) * 16 + (lane & 15), c = (int)(b % cols) * 16 + 4 * (lane >> 4);
-        if (row >= f.M || c >= f.N) continue;
-        const RowInfo r = f.info[row];
-        const int at = f.column[row];
-        if (at >= 0) {
-            const float lost = r.hit - (float)(E)r.hit;
-            const relayout::Four<E> w = relayout::load4(f.W + at * f.ldw, c, f.N, f.vec_w);
+    template <class T>
+    __device__ __forceinline__ void epilogue(const Tile& t, const f32x4 (&acc)[T::FM][T::FN], int lane, int wave, unsigned char* s0,
+                                             unsigned char* s1) const
+    {
+        const int ln = pinned(lane), M = Base::M, N = Base::N;
+        const int bm = (t.m0 + wave / T::WAVES_N * T::WTM) / 16, bn = (t.n0 + wave % T::WAVES_N * T::WTN) / 16;
+        const int rows = (M + 15) / 16 - bm, cols = (N + 15) / 16, left = max(cols - bn, 0);
+        float g[T::FM];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const float add = lost * (float)w[e];
-                v[e] += fabsf(add) < INFINITY ? add : 0.0f;  // (an infinity is in the sum already)
-            }
-        }
-        // (a row that is ignored, whatever its dloss)
-        const float g = r.bias == -INFINITY ? 0.0f : f.dloss[row * f.dloss_stride] * __builtin_amdgcn_exp2f(-kShift<E>);
-        const typename Elem<E>::x4 o = round4<E>(v * g);
-        E* const to = f.dX + row * f.ld + c;
-        if (f.vec && c + 4 <= f.N)
-            *(typename Elem<E>::x4*)to = o;
-        else
+        for (int i = 0; i < T::FM; ++i) g[i] = back[(bm + i) * 16 + (ln & 15)];
+        f32x4 old[T::FN];
+        write_rows<T, T::FN, EIGHTS>(
+            [&](int i, int j) __attribute__((always_inline)) {
+                if constexpr (MORE)
+                    if (j == 0) {
+                        const float* const at = Base::sums + ((int64_t)(bm + i) * cols + bn) * kBlockFloats;
+                        const __amdgpu_buffer_rsrc_t from = make_rsrc(at, i < rows ? (uint32_t)left * (kBlockFloats * 4u) : 0u);
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-                if (c + e < f.N) to[e] = o[e];
+                        for (int k = 0; k < T::FN; ++k)
+                            old[k] = __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(from, ln * 16 + k * (kBlockFloats * 4), 0, 0));
+                    }
+                return round4<E>((MORE ? acc[i][j] + old[j] : acc[i][j]) * g[i]);
+            },
+            rows_at(dX, t.m0, M, T::BM, ldx, t.n0, N), lane, wave, s0, s1);
     }
-}
+};
 
 // ------------------------------------------------------------------ host --
 
@@ -675,7 +698,7 @@ struct BackwardSpace {
     E *x, *w, *xt, *wt, *dl, *dlt;
     RowInfo* info;
     int* column;
-    float *sums, *factor, *partial;
+    float *back, *sums, *factor, *partial;
     int64_t Tp, Vp, piece, rows, bytes;
     bool copy_x, copy_w;
     BackwardSpace(void* base, const void* X, const void* W, int64_t T, int64_t D, int64_t V, int64_t ldx, int64_t ldw)
@@ -696,7 +719,8 @@ struct BackwardSpace {
         dlt = c.take<E>(piece * Tp);
         info = c.take<RowInfo>(rows);
         column = c.take<int>(rows);
-        sums = c.take<float>((T + 15) / 16 * ((D + 15) / 16) * kBlockFloats);
+        back = c.take<float>(rows);
+        sums = piece < V ? c.take<float>((T + 15) / 16 * ((D + 15) / 16) * kBlockFloats) : nullptr;
         factor = c.take<float>(1);
         partial = c.take<float>(kSplitFloats);
         bytes = c.used();
@@ -717,7 +741,7 @@ int backward(const float* dloss, const E* X, const E* W, const int64_t* target, 
         const E* const W0 = W + v0 * ldw;
         Prepare<E> p = {};
         if (v0 == 0) {
-            p.rows = {dloss, saved, target, dloss_stride, target_stride, ignore, (int)T, (int)w.rows, (int)V, w.info, w.column, w.factor};
+            p.rows = {dloss, saved, target, dloss_stride, target_stride, ignore, (int)T, (int)w.rows, (int)V, w.info, w.column, w.back, w.factor};
             p.x = {{X, w.xt, ldx, w.Tp, (int)T, (int)D, (int)w.Tp, (int)vec4(X, ldx)}, target, target_stride, ignore};
             p.first = 1;
         }
@@ -748,16 +772,31 @@ int backward(const float* dloss, const E* X, const E* W, const int64_t* target, 
             op.first = (int)v0;
             if ((rc = launch_grid<E>(op, T, n, 1, 1, op.K, nullptr, stream))) return rc;
             if (D > 0) {
-                AddOp<E> add = {};
-                add.A = w.dl;
-                add.B = w.wt;
-                add.sums = w.sums;
-                add.M = (int)T;
-                add.N = (int)D;
-                add.K = (int)abi::up(n, 8);
-                add.lda = add.ldb = (int)w.Vp;
-                add.fresh = v0 == 0;
-                if ((rc = launch_grid<E>(add, T, D, 1, 1, add.K, add.K >= kSplitK ? w.partial : nullptr, stream))) return rc;
+                auto product = [&](auto op) {
+                    op.A = w.dl;
+                    op.B = w.wt;
+                    op.sums = w.sums;
+                    op.M = (int)T;
+                    op.N = (int)D;
+                    op.K = (int)abi::up(n, 8);
+                    op.lda = op.ldb = (int)w.Vp;
+                    op.fresh = v0 == 0;
+                    return launch_grid<E>(op, T, D, 1, 1, op.K, op.K >= kSplitK ? w.partial : nullptr, stream);
+                };
+                auto last = [&](auto op) {
+                    op.dX = dX;
+                    op.back = w.back;
+                    op.ldx = (int)lddx;
+                    return product(op);
+                };
+                const bool eights = vec8(dX, lddx) && D % 8 == 0;
+                if (v0 + n < V)
+                    rc = product(AddOp<E>{});
+                else if (v0 == 0)
+                    rc = eights ? last(DxOp<E, true, false>{}) : last(DxOp<E, false, false>{});
+                else
+                    rc = eights ? last(DxOp<E, true, true>{}) : last(DxOp<E, false, true>{});
+                if (rc) return rc;
             }
         }
         if (D > 0) {
@@ -777,14 +816,6 @@ int backward(const float* dloss, const E* X, const E* W, const int64_t* target, 
             rc = eights ? product(StoreOp<E, true, true>{}) : product(StoreOp<E, false, true>{});
             if (rc) return rc;
         }
-    }
-    if (T > 0 && D > 0) {
-        const int64_t blocks = (T + 15) / 16 * ((D + 15) / 16);
-        const Finish<E> f = {w.sums, dloss, w.info, w.column, W, dX, dloss_stride, ldw, lddx, (int)T, (int)D, (int)vec4(W, ldw),
-                             (int)vec4(dX, lddx)};
-        hipLaunchKernelGGL(loss_finish<E>, dim3((unsigned)std::min<int64_t>((blocks + 3) / 4, 65536)), dim3(256), 0, stream, f);
-        rc = (int)hipGetLastError();
-        if (rc) return rc;
     }
     return hipSuccess;
 }

@@ -850,21 +850,11 @@ __device__ __forceinline__ void fill(const Image<COLS>& image, const Rows& in, T
     }
 }
 
-// What an epilogue changes in an image before it goes out, after the wave's own
-// values are in it: nothing.
-struct AsItIs {
-    template <class I>
-    __device__ __forceinline__ void operator()(const I&, int) const
-    {
-    }
-};
-
 // The tile row by row: value(i, j) is the four columns that this lane holds
-// of block (i, j) of FN in a wave row.  `fix(image, h)` may change what the wave
-// has put into round h's image (rows h RW .. + RW - 1 of each wave row).
-template <class T, int FN, bool EIGHTS, class Value, class Fix = AsItIs>
+// of block (i, j) of FN in a wave row.
+template <class T, int FN, bool EIGHTS, class Value>
 __device__ __forceinline__ void write_rows(Value value, const Rows& out, int lane, int wave, unsigned char* s0,
-                                           unsigned char* s1, Fix fix = Fix{})
+                                           unsigned char* s1)
 {
     constexpr int WCOLS = FN * 16, COLS = WCOLS * T::WAVES_N, ROUNDS = T::BM * COLS * 2 > T::STAGE_MAX ? 2 : 1;
     constexpr int RW = T::WTM / ROUNDS;  // staged rows of a wave row
@@ -880,7 +870,6 @@ __device__ __forceinline__ void write_rows(Value value, const Rows& out, int lan
             for (int j = 0; j < FN; ++j)
                 image.put(wm * RW + i * 16 + (ln & 15), wn * WCOLS + j * 16 + 4 * (ln >> 4),
                           value(h * (T::FM / ROUNDS) + i, j));
-        fix(image, h);
         lds_barrier<63>();
         drain<T, COLS, T::WAVES_M * RW, EIGHTS>(
             image, out, [&](int x) { return x / RW * T::WTM + h * RW + x % RW; }, lane, wave);
@@ -908,11 +897,10 @@ __device__ __forceinline__ X4 quad_transposed(const X4& v, int lane)
 }
 
 // The tile's transpose, row by row (rows n of BM columns m).  A lane's four
-// values belong to four rows of it, so four lanes exchange theirs first.  `fix` as
-// above, of rows h RW .. + RW - 1 of each wave column.
-template <class T, bool EIGHTS, class Value, class Fix = AsItIs>
+// values belong to four rows of it, so four lanes exchange theirs first.
+template <class T, bool EIGHTS, class Value>
 __device__ __forceinline__ void write_turned(Value value, const Rows& out, int lane, int wave, unsigned char* s0,
-                                             unsigned char* s1, Fix fix = Fix{})
+                                             unsigned char* s1)
 {
     constexpr int ROUNDS = T::BM * T::BN * 2 > T::STAGE_MAX ? 2 : 1;
     constexpr int RW = T::WTN / ROUNDS;  // staged rows of a wave column
@@ -927,7 +915,6 @@ __device__ __forceinline__ void write_turned(Value value, const Rows& out, int l
             for (int j = 0; j < T::FN / ROUNDS; ++j)
                 image.put(wn * RW + j * 16 + 4 * (ln >> 4) + (ln & 3), wm * T::WTM + i * 16 + (ln & 12),
                           quad_transposed(value(i, h * (T::FN / ROUNDS) + j), ln));
-        fix(image, h);
         lds_barrier<63>();
         drain<T, T::BM, T::WAVES_N * RW, EIGHTS>(
             image, out, [&](int x) { return x / RW * T::WTN + h * RW + x % RW; }, lane, wave);

@@ -156,9 +156,14 @@ def _without_gradients(result, message, *inputs):
     return result
 
 
+_entries = {}
+
+
 def _call(library, name, device, *args):
     """Call an entry point on `device` and its current stream (the last argument)."""
-    fn = getattr(load(library), name)
+    fn = _entries.get(name)
+    if fn is None:
+        fn = _entries[name] = getattr(load(library), name)
     if device == torch.cuda.current_device():
         rc = fn(*args, _stream(device))
     else:

@@ -21,8 +21,16 @@ from .operators import _TYPES, _TYPES_AND_F32, _call, _pitch, _without_gradients
 _WORDS = 1 << 64
 
 
+def _new(x, pitch):
+    """A new matrix like x, whose rows are `pitch` apart, with rows that are adjacent."""
+    return torch.empty_like(x, requires_grad=False) if pitch == x.shape[1] and x.is_contiguous() else x.new_empty(x.shape)
+
+
 def _vector(name, t, types, device, size):
     """Check t, `size` adjacent elements of one of `types` on `device`."""
+    # (what holds is found out first and told apart only where it does not)
+    if isinstance(t, torch.Tensor) and t.dtype in types and t.shape == (size,) and t.get_device() == device and t.is_contiguous():
+        return
     if not isinstance(t, torch.Tensor):
         raise TypeError("%s must be a torch tensor" % name)
     if t.dtype not in types:
@@ -55,7 +63,7 @@ def _norm(x, weight, bias, eps, out, train):
         raise ValueError("eps must not be negative, got %r" % eps)
     rows, cols = x.shape
     if out is None:
-        out = x.new_empty((rows, cols))
+        out = _new(x, ldx)
         ldy = cols
     else:
         ldy = _pitch("out", out, (x.dtype,), device, (rows, cols))
@@ -105,7 +113,7 @@ def layer_norm_backward(dy, x, weight, bias, saved, out=None):
             or not saved.is_contiguous() or saved.get_device() != device:
         raise ValueError("saved must be what layer_norm_train returned for x")
     if out is None:
-        dx = x.new_empty((rows, cols))
+        dx = _new(x, ldx)
         dw, db = (None if t is None else torch.empty_like(t, requires_grad=False) for t in (weight, bias))
         lddx = cols
     else:
@@ -147,7 +155,7 @@ def _dropout(x, p, seed, offset, residual, out):
     if residual is not None:
         ldr = _pitch("residual", residual, (x.dtype,), device, x.shape)
     if out is None:
-        out = x.new_empty(x.shape)
+        out = _new(x, ldx)
         ldy = x.shape[1]
     else:
         ldy = _pitch("out", out, (x.dtype,), device, x.shape)
