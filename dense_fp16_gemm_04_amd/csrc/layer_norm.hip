@@ -83,15 +83,14 @@ __global__ void __launch_bounds__(G > 256 ? G : 256) norm_rows(const Forward<E, 
     for (int64_t first = (int64_t)blockIdx.x * R; first < f.rows; first += (int64_t)gridDim.x * R) {
         const int64_t row = first + mine;
         const bool there = row < f.rows;
-        const E* x = f.X + row * f.ldx;
         Vec<E, N> v[C];
-        float s[1] = {0.0f};
 #pragma unroll
         for (int i = 0; i < C; ++i) {
             const int c = (i * G + lane) * N;
             v[i] = Vec<E, N>{};
-            if (there && c < cols) v[i] = load<E, N>(x + c, cols - c);
+            if (there && c < cols) v[i] = load<E, N>(f.X + row * f.ldx + c, cols - c);
         }
+        float s[1] = {0.0f};
 #pragma unroll
         for (int i = 0; i < C; ++i)
 #pragma unroll
@@ -370,33 +369,15 @@ __global__ void __launch_bounds__(kTileThreads) norm_back_tiles(const Backward<E
         }
 }
 
-// Adds the workgroups' sums: 64 columns to a workgroup, sixteen waves that take
-// every sixteenth of the parts.  blockIdx.y: dweight, dbias.
-template <class P>
-__global__ void __launch_bounds__(1024) norm_columns(const float* partial, int parts, int cols, P* dweight, P* dbias)
+// Adds the workgroups' sums.  blockIdx.y: dweight, dbias.
+template <class P, int C>
+__global__ void __launch_bounds__(kSumThreads) norm_columns(const float* partial, int parts, int cols, P* dweight, P* dbias)
 {
-    __shared__ float meet[16][kWave];
-    const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
     P* const to = blockIdx.y ? dbias : dweight;
     if (!to) return;
-    const int64_t c = (int64_t)blockIdx.x * kWave + lane;
-    float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-    if (c < cols) {
-        const float* at = partial + blockIdx.y * (int64_t)cols + c;
-        int p = wave;
-        for (; p + 48 < parts; p += 64)
-#pragma unroll
-            for (int k = 0; k < 4; ++k) s[k] += at[(int64_t)(p + 16 * k) * 2 * cols];
-        for (; p < parts; p += 16) s[0] += at[(int64_t)p * 2 * cols];
-    }
-    meet[wave][lane] = (s[0] + s[1]) + (s[2] + s[3]);
-    __syncthreads();
-    if (wave == 0 && c < cols) {
-        float sum = 0.0f;
-#pragma unroll
-        for (int w = 0; w < 16; ++w) sum += meet[w][lane];
-        to[c] = (P)sum;
-    }
+    const int64_t c = (int64_t)blockIdx.x * C + threadIdx.x % C;
+    const float sum = columns_sum<C>(c < cols ? partial + blockIdx.y * (int64_t)cols + c : nullptr, 2 * (int64_t)cols, parts);
+    if (threadIdx.x < C && c < cols) to[c] = (P)sum;
 }
 
 // ------------------------------------------------------------------ host --
@@ -423,7 +404,13 @@ int64_t back_groups(int64_t rows, int64_t cols, int32_t type)
     const Way w = way_of(chunks_of(cols, type));
     const int cus = cus::num_cus();
     if (w.g == 0) return sharers(rows, 1, 64);
-    return sharers(rows, w.g > 256 ? 1 : 256 / w.g, w.c >= 4 ? cus : 2 * cus);
+    // Each workgroup's sums cross memory twice, and fewer workgroups hide less: with 1, 2
+    // and 3 for each CU 8192 x 4096 in bfloat16 takes 49, 42 and 46 us, 2048 x 8192 (whose
+    // lanes hold more) 32, 32 and 48, 1000 x 2731 16, 18 and 20 (four rows to a
+    // workgroup, or two), 20000 x 300 34, 21 and 17.
+    const int64_t per = w.g > 256 ? 1 : 256 / w.g;
+    if (w.c == 1 && w.g <= 64) return sharers(rows, per, 4 * cus);
+    return sharers(rows, per, w.c >= 4 || rows <= 4 * cus * per ? cus : 2 * cus);
 }
 
 template <class E, class P>
@@ -482,8 +469,10 @@ int backward(Backward<E, P> f, P* dweight, P* dbias, float* partial, float* mean
         if (rc) return rc;
     }
     if (dweight || dbias) {
-        hipLaunchKernelGGL(norm_columns<P>, dim3((unsigned)(((int64_t)f.cols + kWave - 1) / kWave), 2), dim3(1024), 0, stream,
-                           (const float*)partial, (int)groups, f.cols, dweight, dbias);
+        const bool wide = wide_sums(f.cols, 2, cus::num_cus());
+        const int64_t columns = wide ? 64 : 16;
+        hipLaunchKernelGGL((wide ? norm_columns<P, 64> : norm_columns<P, 16>), dim3((unsigned)((f.cols + columns - 1) / columns), 2),
+                           dim3(kSumThreads), 0, stream, (const float*)partial, (int)groups, f.cols, dweight, dbias);
         rc = (int)hipGetLastError();
     }
     return rc;

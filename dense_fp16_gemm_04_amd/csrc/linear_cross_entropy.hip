@@ -243,6 +243,8 @@ __global__ void __launch_bounds__(kJoin) lse_join(const Join f)
 
 // ------------------------------------------------------------- backward --
 
+#include "loss_few.h"
+
 // binary16 ends at 2^-24: dl is held times 2^15.  bfloat16 has the range of 32
 // bits and needs no shift.
 template <class E>
@@ -321,41 +323,51 @@ struct RowNumbers {
     }
 };
 
-// X^T with zeros in the columns of tokens that are ignored (0 times what they
-// hold may be NaN), by tiles of 64 x 64.
+// An operand's rows laid out as the products read them, by tiles of 64 x 64 read
+// once: copied to rows of whole cache lines (where they cannot be read in place) and
+// transposed (where a gradient sums over them), zeros past their end.  Of tokens
+// that are ignored the transpose holds zeros: 0 times what they hold may be NaN.
 template <class E>
-struct TurnX {
-    relayout::Transpose<E> turn;
-    const int64_t* target;
+struct LayOut {
+    const E* src;
+    E *copy, *turned;  // null: not made
+    int64_t ld, ld_copy, ld_turned;
+    int rows, cols;
+    const int64_t* target;  // null: rows are not tokens
     int64_t target_stride, ignore;
 
+    __host__ __device__ int64_t tiles() const
+    {
+        return copy || turned ? ((int64_t)rows + relayout::kTile - 1) / relayout::kTile * (((int64_t)cols + relayout::kTile - 1) / relayout::kTile) : 0;
+    }
     __device__ __forceinline__ void run(int id, E* tile) const
     {
         using namespace relayout;
-        const int tiles_c = (turn.cols + kTile - 1) / kTile;
+        const int tiles_c = (cols + kTile - 1) / kTile;
         const int r0 = id / tiles_c * kTile, c0 = id % tiles_c * kTile;
-        const int x = threadIdx.x & 15, y = threadIdx.x >> 4;
+        const int x = threadIdx.x & 15, y = threadIdx.x >> 4, c = c0 + x * 4;
 #pragma unroll
         for (int it = 0; it < 4; ++it) {
             const int r = it * 16 + y;
-            typename Elem<E>::x4 v = {};
-            if (r0 + r < turn.rows && target[(r0 + r) * target_stride] != ignore)
-                v = load4(turn.src + (int64_t)(r0 + r) * turn.lds_, c0 + x * 4, turn.cols, turn.vec);
-            *(typename Elem<E>::x4*)(tile + r * kPitch + x * 4) = v;
+            Four<E> v = {};
+            if (r0 + r < rows && c < cols) v = ::rows::load<E, 4>(src + (r0 + r) * ld + c, cols - c);
+            if (copy && r0 + r < rows) *(Four<E>*)(copy + (r0 + r) * ld_copy + c) = v;
+            if (target && r0 + r < rows && target[(r0 + r) * target_stride] == ignore) v = Four<E>{};
+            *(Four<E>*)(tile + r * kPitch + x * 4) = v;
         }
+        if (!turned) return;
         __syncthreads();
-        store_transposed(tile, turn.dst, turn.ldd, r0, c0, turn.padded, turn.cols);
+        store_transposed(tile, turned, ld_turned, r0, c0, (int)ld_turned, cols);
     }
 };
 
-// What the products read, in one launch: the rows' numbers and X^T (for the
-// first piece), and W^T of a piece.
+// What the products read, in one launch: the rows' numbers (with the first piece), X and
+// a piece of W.
 template <class E>
 struct Prepare {
-    RowNumbers<E> rows;
-    TurnX<E> x;
-    relayout::Transpose<E> w;
-    int first, second;  // the transposes' first workgroups
+    RowNumbers<E> numbers;
+    LayOut<E> x, w;
+    int first, second;  // the layouts' first workgroups
 };
 
 template <class E>
@@ -364,11 +376,22 @@ __global__ void __launch_bounds__(relayout::kThreads) loss_prepare(const Prepare
     __shared__ E tile[relayout::kTile * relayout::kPitch];
     const int id = blockIdx.x;
     if (id < p.first)
-        p.rows.run();
+        p.numbers.run();
     else if (id < p.second)
         p.x.run(id - p.first, tile);
     else
         p.w.run(id - p.second, tile);
+}
+
+template <class E>
+int enqueue(Prepare<E>& p, bool numbers, hipStream_t stream)
+{
+    p.first = numbers ? 1 : 0;
+    p.second = p.first + (int)p.x.tiles();
+    const int64_t groups = p.second + p.w.tiles();
+    if (groups == 0) return hipSuccess;
+    hipLaunchKernelGGL(loss_prepare<E>, dim3((unsigned)groups), dim3(relayout::kThreads), 0, stream, p);
+    return (int)hipGetLastError();
 }
 
 // dl of a piece of the vocabulary: row-major to dl (pitch ldd), times dloss and
@@ -585,7 +608,6 @@ struct DxOp : AddOp<E> {
 
 // ------------------------------------------------------------------ host --
 
-bool vec4(const void* p, int64_t ld) { return (uintptr_t)p % 8 == 0 && ld % 4 == 0; }
 bool vec8(const void* p, int64_t ld) { return (uintptr_t)p % 16 == 0 && ld % 8 == 0; }
 
 // Rows of what is copied, transposed or kept start on 128 bytes, and are written
@@ -597,60 +619,67 @@ constexpr int64_t kLine = 64;
 constexpr int64_t kSmall = (int64_t)1 << 26;
 int64_t part_width(int64_t T, int64_t V) { return T <= kSmall / V ? 32 : 64; }
 
-// Rows of X or W copied to where they can be read 16 bytes at a time.
-template <class E>
-struct Copied {
-    const E* at;
-    int ld;
-    int enqueue(E* to, int64_t rows, int64_t D, hipStream_t stream)
-    {
-        relayout::Copies<E> c = {};
-        c.job[c.jobs++] = {at, to, ld, rows};
-        at = to;
-        ld = (int)abi::up(D, kLine);
-        if (!rows || !ld) return hipSuccess;
-        const int64_t work = rows * (ld / 4);
-        hipLaunchKernelGGL(relayout::copy_rows<E>, dim3((unsigned)std::min<int64_t>((work + 255) / 256, 16384)),
-                           dim3(relayout::kThreads), 0, stream, c, (int)D, ld);
-        return (int)hipGetLastError();
-    }
-};
+bool in_place(const void* p, int64_t D, int64_t ld) { return D % 8 == 0 && vec8(p, ld); }
 
 template <class E>
 struct ForwardSpace {
-    E *x, *w;
-    float *tl, *partial;
+    E *x = nullptr, *w = nullptr;  // null: read in place
+    float *tl, *partial = nullptr;
     f32x2* parts;
     int64_t Mp, bytes;
-    bool copy_x, copy_w;
     ForwardSpace(void* base, const void* X, const void* W, int64_t T, int64_t D, int64_t V, int64_t ldx, int64_t ldw)
     {
         abi::Carve c(base);
-        copy_x = D % 8 || !vec8(X, ldx);
-        copy_w = D % 8 || !vec8(W, ldw);
-        const int64_t ld = abi::up(D, kLine), width = part_width(T, V);
-        Mp = abi::up(T, 16);
-        x = copy_x ? c.take<E>(T * ld) : nullptr;
-        w = copy_w ? c.take<E>(V * ld) : nullptr;
         tl = c.take<float>(T);
-        parts = c.take<f32x2>((V + width - 1) / width * Mp);
-        partial = abi::up(D, 8) >= kSplitK ? c.take<float>(kSplitFloats) : nullptr;
+        if (T <= few::kTokens) {
+            Mp = few::kTokens;
+            parts = c.take<f32x2>((V + few::kRows - 1) / few::kRows * Mp);
+        } else {
+            const int64_t ld = abi::up(D, kLine), width = part_width(T, V);
+            Mp = abi::up(T, 16);
+            if (!in_place(X, D, ldx)) x = c.take<E>(T * ld);
+            if (!in_place(W, D, ldw)) w = c.take<E>(V * ld);
+            parts = c.take<f32x2>((V + width - 1) / width * Mp);
+            if (abi::up(D, 8) >= kSplitK) partial = c.take<float>(kSplitFloats);
+        }
         bytes = T ? c.used() : 0;
     }
 };
+
+int join(const Join& j, hipStream_t stream)
+{
+    auto with = [&](auto kernel, int64_t rows) {
+        hipLaunchKernelGGL(kernel, dim3((unsigned)((j.M + rows - 1) / rows)), dim3(kJoin), 0, stream, j);
+        return (int)hipGetLastError();
+    };
+    if (j.M <= few::kTokens) return with(lse_join<1>, 1);
+    return j.M <= 8 * 2048 ? with(lse_join<8>, 8) : with(lse_join<32>, 32);
+}
 
 template <class E>
 int forward(const E* X, const E* W, const int64_t* target, float* loss, float* saved, int64_t T, int64_t D, int64_t V, int64_t ldx,
             int64_t ldw, int64_t target_stride, int64_t ignore, void* workspace, hipStream_t stream)
 {
     const ForwardSpace<E> w(workspace, X, W, T, D, V, ldx, ldw);
+    Join j = {w.parts, target, w.tl, loss, saved, target_stride, ignore, w.Mp, (int)T, (int)V, 0};
     int rc;
-    Copied<E> cx{X, (int)ldx}, cw{W, (int)ldw};
-    if (w.copy_x && (rc = cx.enqueue(w.x, T, D, stream))) return rc;
-    if (w.copy_w && (rc = cw.enqueue(w.w, V, D, stream))) return rc;
+    if (T <= few::kTokens) {
+        const few::Lse<E> f = {X, W, target, w.tl, w.parts, target_stride, ldx, ldw, (int)T, (int)D, (int)V};
+        const int64_t n = 16 * few::blocks_of(V);
+        j.segments = (int)((V + n - 1) / n);
+        hipLaunchKernelGGL((n > few::kRows ? few::few_lse<E, 4> : few::few_lse<E, 2>), dim3((unsigned)std::min(j.segments, 1 << 20)),
+                           dim3(few::kWaves * kWave), 0, stream, f);
+        if ((rc = (int)hipGetLastError())) return rc;
+        return join(j, stream);
+    }
+    const int64_t ld = abi::up(D, kLine);
+    Prepare<E> p = {};
+    if (w.x) p.x = {X, w.x, nullptr, ldx, ld, 0, (int)T, (int)D};
+    if (w.w) p.w = {W, w.w, nullptr, ldw, ld, 0, (int)V, (int)D};
+    if ((rc = enqueue(p, false, stream))) return rc;
     LseOp<E> op = {};
-    op.X = cx.at;
-    op.W = cw.at;
+    op.X = w.x ? w.x : X;
+    op.W = w.w ? w.w : W;
     op.target = target;
     op.tl = w.tl;
     op.parts = w.parts;
@@ -659,9 +688,8 @@ int forward(const E* X, const E* W, const int64_t* target, float* loss, float* s
     op.M = (int)T;
     op.N = (int)V;
     op.K = (int)abi::up(D, 8);
-    op.lda = cx.ld;
-    op.ldb = cw.ld;
-    int wtn = 0;
+    op.lda = (int)(w.x ? ld : ldx);
+    op.ldb = (int)(w.w ? ld : ldw);
     rc = launch<E>(
         op, op.K, w.partial,
         [&](const Kind& k) {
@@ -672,16 +700,11 @@ int forward(const E* X, const E* W, const int64_t* target, float* loss, float* s
         [&](LseOp<E>& o, const Kind& k) {
             o.tiles_m = (int)((T + k.bm - 1) / k.bm);
             o.tiles_n = (int)((V + k.bn - 1) / k.bn);
-            wtn = k.bn == 256 ? 128 : k.bm == 256 ? 64 : 32;
+            const int wtn = k.bn == 256 ? 128 : k.bm == 256 ? 64 : 32;
+            j.segments = (int)((V + wtn - 1) / wtn);
         },
         stream);
-    if (rc) return rc;
-    const Join j = {w.parts, target, w.tl, loss, saved, target_stride, ignore, w.Mp, (int)T, (int)V, (int)((V + wtn - 1) / wtn)};
-    if (T <= 8 * 2048)
-        hipLaunchKernelGGL(lse_join<8>, dim3((unsigned)((T + 7) / 8)), dim3(kJoin), 0, stream, j);
-    else
-        hipLaunchKernelGGL(lse_join<32>, dim3((unsigned)((T + 31) / 32)), dim3(kJoin), 0, stream, j);
-    return (int)hipGetLastError();
+    return rc ? rc : join(j, stream);
 }
 
 // Columns of the vocabulary to a piece: dl of 2^27 elements, 256 MB, twice, in
@@ -693,26 +716,45 @@ int64_t piece_of(int64_t T, int64_t V)
     return std::min(V, abi::up((V + pieces - 1) / pieces, 256));
 }
 
+// Shares of W's rows for few tokens, whose gradients' sums cross memory twice: as
+// many workgroups as run at once (32000 x 2048 in 256, 512 and 1024: 1 token by 1024 columns
+// 86, 68 and 63 us, 8 tokens 142, 123 and 139).
+struct Shares {
+    int64_t per, count, chunks;  // rows to a share, shares, pieces of D
+    Shares(int64_t T, int64_t D, int64_t V)
+    {
+        const int64_t columns = few::kGradThreads * (T <= 8 ? 8 : 4);
+        chunks = std::max<int64_t>((D + columns - 1) / columns, 1);
+        const int64_t most = std::max<int64_t>((T <= 4 ? 4 : 2) * num_cus() / chunks, 1);
+        per = std::max<int64_t>(abi::up((V + most - 1) / most, 8), 16);
+        count = (V + per - 1) / per;
+    }
+};
+
 template <class E>
 struct BackwardSpace {
-    E *x, *w, *xt, *wt, *dl, *dlt;
+    E *x = nullptr, *w = nullptr;  // null: read in place
+    E *xt, *wt, *dl, *dlt;
     RowInfo* info;
     int* column;
     float *back, *sums, *factor, *partial;
     int64_t Tp, Vp, piece, rows, bytes;
-    bool copy_x, copy_w;
     BackwardSpace(void* base, const void* X, const void* W, int64_t T, int64_t D, int64_t V, int64_t ldx, int64_t ldw)
     {
         abi::Carve c(base);
-        copy_x = D % 8 || !vec8(X, ldx);
-        copy_w = D % 8 || !vec8(W, ldw);
+        if (T > 0 && T <= few::kTokens) {
+            sums = c.take<float>(V * few::kTokens);  // dl
+            partial = c.take<float>(Shares(T, D, V).count * T * D);
+            bytes = c.used();
+            return;
+        }
         const int64_t ld = abi::up(D, kLine);
         piece = piece_of(T, V);
         Tp = abi::up(T, kLine);
         Vp = abi::up(piece, kLine);
         rows = abi::up(T, 256);
-        x = copy_x ? c.take<E>(T * ld) : nullptr;
-        w = copy_w ? c.take<E>(piece * ld) : nullptr;
+        if (!in_place(X, D, ldx)) x = c.take<E>(T * ld);
+        if (!in_place(W, D, ldw)) w = c.take<E>(piece * ld);
         xt = c.take<E>(D * Tp);
         wt = c.take<E>(D * Vp);
         dl = c.take<E>(T * Vp);
@@ -728,36 +770,60 @@ struct BackwardSpace {
 };
 
 template <class E>
+int backward_few(const float* dloss, const E* X, const E* W, const int64_t* target, const float* saved, E* dX, E* dW, int64_t T, int64_t D,
+                 int64_t V, int64_t dloss_stride, int64_t ldx, int64_t ldw, int64_t target_stride, int64_t lddx, int64_t lddw, int64_t ignore,
+                 const BackwardSpace<E>& w, hipStream_t stream)
+{
+    if (D == 0) return hipSuccess;
+    const few::Dl<E> d = {X, W, target, dloss, saved, w.sums, target_stride, dloss_stride, ignore, ldx, ldw, (int)T, (int)D, (int)V};
+    const int64_t n = 16 * few::blocks_of(V), blocks = (V + n - 1) / n;
+    hipLaunchKernelGGL((n > few::kRows ? few::few_dl<E, 4> : few::few_dl<E, 2>), dim3((unsigned)std::min<int64_t>(blocks, 1 << 20)),
+                       dim3(few::kWaves * kWave), 0, stream, d);
+    int rc = (int)hipGetLastError();
+    if (rc) return rc;
+    const Shares s(T, D, V);
+    const few::Grads<E> g = {X, W, target, w.sums, dW, w.partial, target_stride, ignore, ldx, ldw, lddw, (int)T, (int)D, (int)V, (int)s.per};
+    auto with = [&](auto kernel) {
+        hipLaunchKernelGGL(kernel, dim3((unsigned)s.count, (unsigned)s.chunks), dim3(few::kGradThreads), 0, stream, g);
+        return (int)hipGetLastError();
+    };
+    if (T == 1) rc = with(few::few_grads<E, 1, 8>);
+    else if (T <= 4) rc = with(few::few_grads<E, 4, 8>);
+    else if (T <= 8) rc = with(few::few_grads<E, 8, 8>);
+    else rc = with(few::few_grads<E, 16, 4>);
+    if (rc) return rc;
+    const few::Sum<E> sum = {w.partial, target, dX, target_stride, ignore, lddx, (int)T, (int)D, (int)s.count};
+    const bool wide = rows::wide_sums(D, T, num_cus());
+    const int64_t columns = wide ? 64 : 16;
+    hipLaunchKernelGGL((wide ? few::few_sum<E, 64> : few::few_sum<E, 16>), dim3((unsigned)((D + columns - 1) / columns), (unsigned)T),
+                       dim3(rows::kSumThreads), 0, stream, sum);
+    return (int)hipGetLastError();
+}
+
+template <class E>
 int backward(const float* dloss, const E* X, const E* W, const int64_t* target, const float* saved, E* dX, E* dW, int64_t T, int64_t D,
              int64_t V, int64_t dloss_stride, int64_t ldx, int64_t ldw, int64_t target_stride, int64_t lddx, int64_t lddw, int64_t ignore,
              void* workspace, hipStream_t stream)
 {
     const BackwardSpace<E> w(workspace, X, W, T, D, V, ldx, ldw);
+    if (T > 0 && T <= few::kTokens)
+        return backward_few<E>(dloss, X, W, target, saved, dX, dW, T, D, V, dloss_stride, ldx, ldw, target_stride, lddx, lddw, ignore, w, stream);
     int rc;
-    Copied<E> cx{X, (int)ldx};
-    if (w.copy_x && (rc = cx.enqueue(w.x, T, D, stream))) return rc;
+    const int64_t ld = abi::up(D, kLine);
     for (int64_t v0 = 0; v0 < V; v0 += w.piece) {
         const int64_t n = std::min(w.piece, V - v0);
         const E* const W0 = W + v0 * ldw;
         Prepare<E> p = {};
         if (v0 == 0) {
-            p.rows = {dloss, saved, target, dloss_stride, target_stride, ignore, (int)T, (int)w.rows, (int)V, w.info, w.column, w.back, w.factor};
-            p.x = {{X, w.xt, ldx, w.Tp, (int)T, (int)D, (int)w.Tp, (int)vec4(X, ldx)}, target, target_stride, ignore};
-            p.first = 1;
+            p.numbers = {dloss, saved, target, dloss_stride, target_stride, ignore, (int)T, (int)w.rows, (int)V, w.info, w.column, w.back, w.factor};
+            p.x = {X, w.x, w.xt, ldx, ld, w.Tp, (int)T, (int)D, target, target_stride, ignore};
         }
-        p.w = {W0, w.wt, ldw, w.Vp, (int)n, (int)D, (int)abi::up(n, kLine), (int)vec4(W0, ldw)};
-        p.second = p.first + (int)p.x.turn.tiles();
-        const int64_t groups = p.second + (T > 0 ? p.w.tiles() : 0);
-        if (groups > 0) {
-            hipLaunchKernelGGL(loss_prepare<E>, dim3((unsigned)groups), dim3(relayout::kThreads), 0, stream, p);
-            if ((rc = (int)hipGetLastError())) return rc;
-        }
+        if (T > 0) p.w = {W0, w.w, w.wt, ldw, ld, w.Vp, (int)n, (int)D};
+        if ((rc = enqueue(p, v0 == 0, stream))) return rc;
         if (T > 0) {
-            Copied<E> cw{W0, (int)ldw};
-            if (w.copy_w && (rc = cw.enqueue(w.w, n, D, stream))) return rc;
             DlOp<E> op = {};
-            op.X = cx.at;
-            op.W = cw.at;
+            op.X = w.x ? w.x : X;
+            op.W = w.w ? w.w : W0;
             op.dl = w.dl;
             op.dlt = w.dlt;
             op.info = w.info;
@@ -765,8 +831,8 @@ int backward(const float* dloss, const E* X, const E* W, const int64_t* target, 
             op.M = (int)T;
             op.N = (int)n;
             op.K = (int)abi::up(D, 8);
-            op.lda = cx.ld;
-            op.ldb = cw.ld;
+            op.lda = (int)(w.x ? ld : ldx);
+            op.ldb = (int)(w.w ? ld : ldw);
             op.ldd = (int)w.Vp;
             op.ldt = (int)w.Tp;
             op.first = (int)v0;
@@ -825,6 +891,8 @@ bool good_sizes(int64_t T, int64_t D, int64_t V)
     return T >= 0 && T <= abi::kMaxDim - 256 && D >= 0 && D <= abi::kMaxPitch - 63 && V > 0 && V <= abi::kMaxDim - 256;
 }
 bool good_backward_sizes(int64_t T, int64_t D, int64_t V) { return good_sizes(T, D, V) && T <= abi::kMaxPitch - 63; }
+// Workgroups that lay out X and V rows of W, and the one beside them.
+int64_t layout_tiles(int64_t T, int64_t D, int64_t V) { return ((T + 63) / 64 + (V + 63) / 64) * ((D + 63) / 64) + 1; }
 bool good_stride(int64_t s) { return s >= 0 && s <= (int64_t)1 << 31; }
 
 }  // namespace
@@ -853,7 +921,7 @@ int linear_cross_entropy(const void* X, const void* W, const int64_t* target, fl
     if (!good_sizes(T, D, V) || !good_pitch(ldx, D) || !good_pitch(ldw, D) || !good_stride(target_stride)) return hipErrorInvalidValue;
     if (type != LINEAR_CROSS_ENTROPY_F16 && type != LINEAR_CROSS_ENTROPY_BF16) return hipErrorInvalidValue;
     if (T == 0) return hipSuccess;
-    if (!nt::fits(T, V, 1)) return hipErrorInvalidValue;
+    if (!nt::fits(T, V, 1) || !good_grid(layout_tiles(T, D, V), relayout::kThreads)) return hipErrorInvalidValue;
     if (!good_pointer(X, T, D, 2) || !good_pointer(W, V, D, 2) || !good_pointer(target, T, 1, 8) || !good_pointer(loss, T, 1, 4) ||
         (uintptr_t)saved % 4 || (uintptr_t)workspace % 16)
         return hipErrorInvalidValue;
@@ -884,9 +952,7 @@ int linear_cross_entropy_backward(const float* dloss, const void* X, const void*
         return hipErrorInvalidValue;
     if (type != LINEAR_CROSS_ENTROPY_F16 && type != LINEAR_CROSS_ENTROPY_BF16) return hipErrorInvalidValue;
     if (!nt::fits(T, piece_of(T, V), 1) || !nt::fits(T, D, 1) || !nt::fits(piece_of(T, V), D, 1)) return hipErrorInvalidValue;
-    // (the transposes' tiles, and the one workgroup beside them)
-    const int64_t tiles = (up(piece_of(T, V), kLine) / 64 + up(T, kLine) / 64) * ((D + 63) / 64);
-    if (!good_grid(tiles + 1, relayout::kThreads)) return hipErrorInvalidValue;
+    if (!good_grid(layout_tiles(T, D, piece_of(T, V)), relayout::kThreads)) return hipErrorInvalidValue;
     if (!good_pointer(dloss, T, 1, 4) || !good_pointer(X, T, D, 2) || !good_pointer(W, V, D, 2) || !good_pointer(target, T, 1, 8) ||
         !good_pointer(saved, T, 1, 4) || !good_pointer(dX, T, D, 2) || !good_pointer(dW, V, D, 2) || (uintptr_t)workspace % 16)
         return hipErrorInvalidValue;

@@ -102,6 +102,40 @@ __device__ __forceinline__ void sums(float (&v)[K], Parts<G, K>& parts, int turn
     }
 }
 
+// Sums of columns over `parts` rows `step` apart, C columns to a workgroup of 1024
+// threads, which take every (1024 / C)th row each and meet in LDS.  `at`: the
+// thread's column in the first row; null: it has none.  The first C threads get
+// their columns' sums.
+constexpr int kSumThreads = 1024;
+template <int C>
+__device__ __forceinline__ float columns_sum(const float* at, int64_t step, int parts)
+{
+    constexpr int S = kSumThreads / C;
+    __shared__ float meet[S][C];
+    const int c = threadIdx.x % C, share = threadIdx.x / C;
+    float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    if (at) {
+        int p = share;
+        for (; p + 3 * S < parts; p += 4 * S)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) s[k] += at[(p + k * S) * step];
+#pragma unroll
+        for (int k = 0; k < 3; ++k)
+            if (p + k * S < parts) s[k] += at[(p + k * S) * step];
+    }
+    meet[share][c] = (s[0] + s[1]) + (s[2] + s[3]);
+#pragma unroll
+    for (int half = S / 2; half > 0; half /= 2) {
+        __syncthreads();
+        if (share < half) meet[share][c] += meet[share + half][c];
+    }
+    return meet[0][c];
+}
+// 64 columns are whole cache lines, 16 four times the workgroups: where 64 are too
+// few for half the chip.  (1 row of 1024 columns from 1000 parts: 7.4 us by 64 and
+// 4.6 by 16; 8 of 2048 from 500 11.7 and 12.9.)
+inline bool wide_sums(int64_t columns, int64_t rows, int cus) { return columns * rows >= 32 * (int64_t)cus; }
+
 // Bytes [first, last] of a matrix stay far from where 64 bits end.
 inline bool good_span(int64_t rows, int64_t cols, int64_t ld)
 {

@@ -223,7 +223,7 @@ def loss_args(**kw):
     dict(ldw=15), dict(ldx=1 << 21), dict(stride=-1), dict(stride=(1 << 31) + 1), dict(type=2), dict(type=-1), dict(X=None), dict(W=None),
     dict(target=None), dict(loss=None), dict(X=A + 1), dict(W=B + 1), dict(target=C + 4), dict(loss=D + 2), dict(saved=E + 2),
     dict(ws=None), dict(ws_bytes=64), dict(ws=W + 8), dict(loss=A), dict(loss=B), dict(loss=C), dict(saved=A), dict(saved=D), dict(ws=A),
-    dict(ws=D), dict(D=512, ldx=512, ldw=512, ws_bytes=1 << 20), dict(T=1 << 28, V=1 << 28, ws_bytes=1 << 60),
+    dict(ws=D), dict(T=1 << 28, V=1 << 28, ws_bytes=1 << 60), dict(T=64, D=512, ldx=512, ldw=512, ws_bytes=1 << 20),
 ])
 def test_loss_refuses(kw):
     assert operators.load("linear_cross_entropy").linear_cross_entropy(*loss_args(**kw)) == INVALID
