@@ -71,7 +71,7 @@ struct LseOp {
     float* tl;     // [M]: the target's output
     f32x2* parts;  // [segments][Mp]: (largest, sum) of WTN columns of a row
     int64_t target_stride, Mp;
-    int M, N, K, lda, ldb, tiles, tiles_m, tiles_n;
+    int M, N, K, lda, ldb, first, tiles, tiles_m, tiles_n;  // first: the column that W's first row is
 
     template <int BM, int BN>
     __device__ __forceinline__ void tile(int id, Tile& t) const
@@ -144,7 +144,7 @@ struct LseOp {
             const int row = m0 + i * 16 + (ln & 15);
             const f32x2 part = {top[i], sum_over_groups(sum[i])};
             __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(u32x2, part), to, ln < 16 ? (i * 16 + ln) * 8 : kOob, 0, 0);
-            const int64_t c = target[min(row, M - 1) * target_stride] - n0;
+            const int64_t c = target[min(row, M - 1) * target_stride] - first - n0;
             at[i] = row < M && c >= 0 && c < min(T::WTN, N - n0) ? (int)c - 4 * (ln >> 4) : -1;
             any |= at[i] >= 0;
         }
@@ -570,6 +570,37 @@ struct AddOp {
     }
 };
 
+// write_rows for rows on any boundary: eight columns to a lane at any address but at
+// a row's end, and branches around what is not there, which is why the values
+// come by read().  (dW of 181 x 333 x 109366: 95 us with each element stored alone, and 73.)
+template <class T, class E, class Value>
+__device__ __forceinline__ void write_any(Value value, E* out, int64_t ld, int m0, int rows, int n0, int cols, int lane, int wave,
+                                          unsigned char* s0, unsigned char* s1)
+{
+    constexpr int COLS = T::BN, ROUNDS = T::BM * COLS * 2 > T::STAGE_MAX ? 2 : 1, RW = T::WTM / ROUNDS, IR = T::FM / ROUNDS;
+    constexpr int CH = COLS / 8, RPI = 64 / CH, ITERS = T::WAVES_M * RW / RPI / T::WAVES;
+    static_assert(ITERS * RPI * T::WAVES == T::WAVES_M * RW, "rows split evenly over the waves");
+    const Image<COLS> image{s0, s1};
+    const int wm = wave / T::WAVES_N, wn = wave % T::WAVES_N;
+#pragma unroll
+    for (int h = 0; h < ROUNDS; ++h) {
+        const int ln = pinned(lane);
+#pragma unroll
+        for (int i = 0; i < IR; ++i)
+#pragma unroll
+            for (int j = 0; j < T::FN; ++j)
+                image.put(wm * RW + i * 16 + (ln & 15), wn * T::WTN + j * 16 + 4 * (ln >> 4), value(h * IR + i, j));
+        lds_barrier<63>();
+        const int ch = ln % CH, n = n0 + ch * 8;
+        for (int it = 0; it < ITERS; ++it) {
+            const int x = (wave * ITERS + it) * RPI + ln / CH, row = m0 + x / RW * T::WTM + h * RW + x % RW;
+            if (row < rows && n < cols)
+                ::rows::store<E, 8>(out + row * ld + n, cols - n, __builtin_bit_cast(::rows::Vec<E, 8>, image.get(x, ch)));
+        }
+        lds_barrier<63>();
+    }
+}
+
 // The last piece's: dX[t] = back[t] (A B^T and, MORE, the sums of the pieces before),
 // rounded.  EIGHTS: dX's rows take 16-byte pieces and hold a multiple of eight.
 template <class E, bool EIGHTS, bool MORE>
@@ -590,19 +621,36 @@ struct DxOp : AddOp<E> {
 #pragma unroll
         for (int i = 0; i < T::FM; ++i) g[i] = back[(bm + i) * 16 + (ln & 15)];
         f32x4 old[T::FN];
-        write_rows<T, T::FN, EIGHTS>(
-            [&](int i, int j) __attribute__((always_inline)) {
-                if constexpr (MORE)
-                    if (j == 0) {
-                        const float* const at = Base::sums + ((int64_t)(bm + i) * cols + bn) * kBlockFloats;
-                        const __amdgpu_buffer_rsrc_t from = make_rsrc(at, i < rows ? (uint32_t)left * (kBlockFloats * 4u) : 0u);
+        auto value = [&](int i, int j) __attribute__((always_inline)) {
+            if constexpr (MORE)
+                if (j == 0) {
+                    const float* const at = Base::sums + ((int64_t)(bm + i) * cols + bn) * kBlockFloats;
+                    const __amdgpu_buffer_rsrc_t from = make_rsrc(at, i < rows ? (uint32_t)left * (kBlockFloats * 4u) : 0u);
 #pragma unroll
-                        for (int k = 0; k < T::FN; ++k)
-                            old[k] = __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(from, ln * 16 + k * (kBlockFloats * 4), 0, 0));
-                    }
-                return round4<E>((MORE ? acc[i][j] + old[j] : acc[i][j]) * g[i]);
-            },
-            rows_at(dX, t.m0, M, T::BM, ldx, t.n0, N), lane, wave, s0, s1);
+                    for (int k = 0; k < T::FN; ++k)
+                        old[k] = __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(from, ln * 16 + k * (kBlockFloats * 4), 0, 0));
+                }
+            const f32x4 v = EIGHTS ? acc[i][j] : read<T>(acc[i][j]);
+            return round4<E>((MORE ? v + old[j] : v) * g[i]);
+        };
+        if constexpr (EIGHTS)
+            write_rows<T, T::FN, true>(value, rows_at(dX, t.m0, M, T::BM, ldx, t.n0, N), lane, wave, s0, s1);
+        else
+            write_any<T>(value, dX, ldx, t.m0, M, t.n0, N, lane, wave, s0, s1);
+    }
+};
+
+// A piece's rows of dW where StoreOp would store each element alone.
+template <class E>
+struct DwOp : StoreOp<E, false, true> {
+    using Base = StoreOp<E, false, true>;
+    template <class T>
+    __device__ __forceinline__ void epilogue(const Tile& t, const f32x4 (&acc)[T::FM][T::FN], int lane, int wave, unsigned char* s0,
+                                             unsigned char* s1) const
+    {
+        const float f = *Base::factor;
+        write_any<T>([&](int i, int j) __attribute__((always_inline)) { return round4<E>(read<T>(acc[i][j]) * f); }, Base::C[0], Base::ldc[0],
+                     t.m0, Base::M, t.n0, Base::N, lane, wave, s0, s1);
     }
 };
 
@@ -613,6 +661,22 @@ bool vec8(const void* p, int64_t ld) { return (uintptr_t)p % 16 == 0 && ld % 8 =
 // Rows of what is copied, transposed or kept start on 128 bytes, and are written
 // in whole cache lines.
 constexpr int64_t kLine = 64;
+
+// A product over n columns of the vocabulary (by `other` rows, sums of K) may be
+// made in two: whole waves of 256 x 256 tiles first, the rest in tiles that leave
+// fewer CUs idle.  Returns the first one's columns, n if one is better: the
+// model's times and 4 us for the launch.  (Steps of 2048 x 2048 x 50001, 1568
+// tiles for 256 CUs: 1593 us in one and 1555 in two; 1000 x 768 x 50001 471 and 448.)
+template <class OP>
+int64_t first_of_two(int64_t other, int64_t n, int64_t K, bool partial)
+{
+    auto tiles = [=](int64_t m) { return [=](const Kind& k) { return (other + k.bm - 1) / k.bm * ((m + k.bn - 1) / k.bn); }; };
+    const int cus = num_cus();
+    const int64_t strip = (other + 255) / 256, waves = strip * ((n + 255) / 256) / cus, first = waves * cus / strip * 256;
+    if (K <= 128 || first == 0 || first >= n) return n;
+    const Choice one = choose<OP>(K, partial, tiles(n)), rest = choose<OP>(K, partial, tiles(n - first));
+    return model_us(kKinds[0], waves * cus, K, cus) + rest.us + 4.0 < one.us ? first : n;
+}
 
 // The parts of up to this many outputs may be of 32 columns, of more 64 at least
 // (which leaves out the smaller tiles): 8 bytes each.
@@ -639,7 +703,7 @@ struct ForwardSpace {
             Mp = abi::up(T, 16);
             if (!in_place(X, D, ldx)) x = c.take<E>(T * ld);
             if (!in_place(W, D, ldw)) w = c.take<E>(V * ld);
-            parts = c.take<f32x2>((V + width - 1) / width * Mp);
+            parts = c.take<f32x2>(((V + width - 1) / width + 1) * Mp);
             if (abi::up(D, 8) >= kSplitK) partial = c.take<float>(kSplitFloats);
         }
         bytes = T ? c.used() : 0;
@@ -679,32 +743,38 @@ int forward(const E* X, const E* W, const int64_t* target, float* loss, float* s
     if ((rc = enqueue(p, false, stream))) return rc;
     LseOp<E> op = {};
     op.X = w.x ? w.x : X;
-    op.W = w.w ? w.w : W;
     op.target = target;
     op.tl = w.tl;
-    op.parts = w.parts;
     op.target_stride = target_stride;
     op.Mp = w.Mp;
     op.M = (int)T;
-    op.N = (int)V;
     op.K = (int)abi::up(D, 8);
     op.lda = (int)(w.x ? ld : ldx);
     op.ldb = (int)(w.w ? ld : ldw);
-    rc = launch<E>(
-        op, op.K, w.partial,
-        [&](const Kind& k) {
-            const bool wide = k.bn == 256 || k.bm == 256;  // (sub-tiles of 64 columns or more)
-            if (!wide && part_width(T, V) > 32) return INT64_MAX;
-            return (T + k.bm - 1) / k.bm * ((V + k.bn - 1) / k.bn);
-        },
-        [&](LseOp<E>& o, const Kind& k) {
-            o.tiles_m = (int)((T + k.bm - 1) / k.bm);
-            o.tiles_n = (int)((V + k.bn - 1) / k.bn);
-            const int wtn = k.bn == 256 ? 128 : k.bm == 256 ? 64 : 32;
-            j.segments = (int)((V + wtn - 1) / wtn);
-        },
-        stream);
-    return rc ? rc : join(j, stream);
+    const int64_t split = first_of_two<LseOp<E>>(T, V, op.K, w.partial);
+    for (int64_t v0 = 0; v0 < V; v0 = v0 ? V : split) {
+        const int64_t n = v0 ? V - split : split;
+        op.W = (w.w ? w.w : W) + v0 * op.ldb;
+        op.N = (int)n;
+        op.first = (int)v0;
+        op.parts = w.parts + j.segments * w.Mp;
+        rc = launch<E>(
+            op, op.K, w.partial,
+            [&](const Kind& k) {
+                const bool wide = k.bn == 256 || k.bm == 256;  // (sub-tiles of 64 columns or more)
+                if (!wide && part_width(T, V) > 32) return INT64_MAX;
+                return (T + k.bm - 1) / k.bm * ((n + k.bn - 1) / k.bn);
+            },
+            [&](LseOp<E>& o, const Kind& k) {
+                o.tiles_m = (int)((T + k.bm - 1) / k.bm);
+                o.tiles_n = (int)((n + k.bn - 1) / k.bn);
+                const int wtn = k.bn == 256 ? 128 : k.bm == 256 ? 64 : 32;
+                j.segments += (int)((n + wtn - 1) / wtn);
+            },
+            stream);
+        if (rc) return rc;
+    }
+    return join(j, stream);
 }
 
 // Columns of the vocabulary to a piece: dl of 2^27 elements, 256 MB, twice, in
@@ -823,20 +893,23 @@ int backward(const float* dloss, const E* X, const E* W, const int64_t* target, 
         if (T > 0) {
             DlOp<E> op = {};
             op.X = w.x ? w.x : X;
-            op.W = w.w ? w.w : W0;
-            op.dl = w.dl;
-            op.dlt = w.dlt;
             op.info = w.info;
             op.column = w.column;
             op.M = (int)T;
-            op.N = (int)n;
             op.K = (int)abi::up(D, 8);
             op.lda = (int)(w.x ? ld : ldx);
             op.ldb = (int)(w.w ? ld : ldw);
             op.ldd = (int)w.Vp;
             op.ldt = (int)w.Tp;
-            op.first = (int)v0;
-            if ((rc = launch_grid<E>(op, T, n, 1, 1, op.K, nullptr, stream))) return rc;
+            const int64_t split = first_of_two<DlOp<E>>(T, n, op.K, false);
+            for (int64_t c = 0; c < n; c = c ? n : split) {
+                op.W = (w.w ? w.w : W0) + c * op.ldb;
+                op.dl = w.dl + c;
+                op.dlt = w.dlt + c * w.Tp;
+                op.first = (int)(v0 + c);
+                op.N = (int)(c ? n - split : split);
+                if ((rc = launch_grid<E>(op, T, op.N, 1, 1, op.K, nullptr, stream))) return rc;
+            }
             if (D > 0) {
                 auto product = [&](auto op) {
                     op.A = w.dl;
@@ -868,18 +941,23 @@ int backward(const float* dloss, const E* X, const E* W, const int64_t* target, 
         if (D > 0) {
             auto product = [&](auto op) {
                 op.factor = w.factor;
-                op.A[0] = w.dlt;
                 op.B = w.xt;
-                op.C[0] = dW + v0 * lddw;
-                op.M = (int)n;
                 op.N = (int)D;
                 op.K = (int)abi::up(T, 8);
                 op.lda = op.ldb = (int)w.Tp;
                 op.ldc[0] = (int)lddw;
-                return launch_grid<E>(op, n, D, 1, 1, op.K, op.K >= kSplitK ? w.partial : nullptr, stream);
+                float* const partial = op.K >= kSplitK ? w.partial : nullptr;
+                const int64_t split = first_of_two<decltype(op)>(D, n, op.K, partial);
+                for (int64_t c = 0; c < n; c = c ? n : split) {
+                    op.A[0] = w.dlt + c * w.Tp;
+                    op.C[0] = dW + (v0 + c) * lddw;
+                    op.M = (int)(c ? n - split : split);
+                    if ((rc = launch_grid<E>(op, op.M, D, 1, 1, op.K, partial, stream))) return rc;
+                }
+                return (int)hipSuccess;
             };
             const bool eights = vec8(dW, lddw) && D % 8 == 0;
-            rc = eights ? product(StoreOp<E, true, true>{}) : product(StoreOp<E, false, true>{});
+            rc = eights ? product(StoreOp<E, true, true>{}) : product(DwOp<E>{});
             if (rc) return rc;
         }
     }

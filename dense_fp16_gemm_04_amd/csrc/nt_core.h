@@ -240,7 +240,9 @@ __device__ __forceinline__ void mfma_agpr(f32x4& acc, const Elem<__bf16>::x8& b,
 // equal shares of K's steps; each leaves its accumulators, in the lanes'
 // order, in `partial`, and nt_join adds them (in a fixed order) and writes
 // the tile out.  This fills the CUs that a last wave of few tiles would
-// leave idle.
+// leave idle.  Units run part by part, an XCD's one after another: its tiles
+// then read the same share of K, which its L2 holds once.  (1000 x 1032 over
+// 32008, 36 tiles in 7 parts: 94 us with a tile's parts one after another, and 81.)
 struct Split {
     int full, parts;
     float* partial;
@@ -262,9 +264,9 @@ __global__ void __launch_bounds__(T::THREADS, 1) nt_ordered(const OP op, const S
     const int nk = (K + T::BK - 1) / T::BK, nfull = K / T::BK;
     int id = blockIdx.x, part = -1, begin = 0, end = nk;  // the steps to add up
     if (id >= split.full) {
-        const int n = id - split.full;
-        id = split.full + n / split.parts;
-        part = n % split.parts;
+        const int units = (int)gridDim.x - split.full, rest = units / split.parts, n = xcd_order(id - split.full, units);
+        id = split.full + n % rest;
+        part = n / rest;
         begin = (int)((int64_t)nk * part / split.parts);
         end = (int)((int64_t)nk * (part + 1) / split.parts);
     }

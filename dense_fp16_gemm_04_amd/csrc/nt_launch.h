@@ -75,54 +75,57 @@ int launch_ordered(const OP& op, int tiles, int rest, int parts, float* partial,
     return rc;
 }
 
-// Runs OP over `count(kind)` tiles with the kernel that the model finds
-// fastest.  256 x 256 tiles need three K steps and an OP that offers them
-// (kPersist); a split needs `partial` (kSplitFloats floats) and one that offers
-// it (kSplit).
-template <class E, class OP, class Count, class Prepare>
-int launch(OP op, int64_t K, float* partial, Count count, Prepare prepare, hipStream_t stream)
+// Which kernel the model finds fastest over `count(kind)` tiles, and its time.
+// 256 x 256 tiles need three K steps and an OP that offers them (kPersist); a split
+// needs an OP that offers it (kSplit, by the caller who gives `partial`).
+struct Choice {
+    int kind = -1, parts = 1;
+    int64_t tiles = 0;
+    double us = 0;
+};
+template <class OP, class Count>
+Choice choose(int64_t K, bool partial, Count count)
 {
     const int cus = num_cus();
-    int best = -1, parts = 1;
-    int64_t tiles = 0;
-    double best_us = 0;
+    Choice best;
     for (int i = 0; i < kNumKinds; ++i) {
         if (i == 0 && (!OP::kPersist || K <= 128)) continue;
         const int64_t n = count(kKinds[i]);
         if (!abi::good_grid(n, i == 1 || i == 2 ? 512 : 256)) continue;
         const double us = model_us(kKinds[i], n, K, cus);
-        if (best < 0 || us < best_us) {
-            best = i;
-            best_us = us;
-            tiles = n;
-            parts = 1;
-        }
+        if (best.kind < 0 || us < best.us) best = {i, 1, n, us};
         int p = 1;
         const double split = (i == 1 || i == 2) && partial ? split_us(kKinds[i], n, K, cus, p) : -1;
-        if (split > 0 && split < best_us) {
-            best = i;
-            best_us = split;
-            tiles = n;
-            parts = p;
-        }
+        if (split > 0 && split < best.us) best = {i, p, n, split};
     }
-    if (best < 0) return hipErrorInvalidValue;
+    return best;
+}
+
+// Runs OP over `count(kind)` tiles with the kernel that the model finds
+// fastest; a split needs `partial` (kSplitFloats floats).
+template <class E, class OP, class Count, class Prepare>
+int launch(OP op, int64_t K, float* partial, Count count, Prepare prepare, hipStream_t stream)
+{
+    const int cus = num_cus();
+    const Choice best = choose<OP>(K, partial != nullptr, count);
+    if (best.kind < 0) return hipErrorInvalidValue;
+    const int64_t tiles = best.tiles;
     if (tiles == 0) return hipSuccess;
     op.tiles = (int)tiles;
-    prepare(op, kKinds[best]);
+    prepare(op, kKinds[best.kind]);
     if constexpr (OP::kPersist)
-        if (best == 0)
+        if (best.kind == 0)
             hipLaunchKernelGGL((nt_persist<Shape256<E>, OP>), dim3((unsigned)std::min<int64_t>(tiles, cus)), dim3(256),
                                0, stream, op);
-    if (best == 1)
-        return launch_ordered<Shape<E, 256, 128, 4, 2, 3, 1, 4>>(op, (int)tiles, (int)(tiles % cus), parts, partial,
+    if (best.kind == 1)
+        return launch_ordered<Shape<E, 256, 128, 4, 2, 3, 1, 4>>(op, (int)tiles, (int)(tiles % cus), best.parts, partial,
                                                                  stream);
-    if (best == 2)
-        return launch_ordered<Shape<E, 128, 128, 2, 4, 3, 1, 4>>(op, (int)tiles, (int)(tiles % cus), parts, partial,
+    if (best.kind == 2)
+        return launch_ordered<Shape<E, 128, 128, 2, 4, 3, 1, 4>>(op, (int)tiles, (int)(tiles % cus), best.parts, partial,
                                                                  stream);
     // (four stages, two workgroups to a CU: 30.8 us with three for one row and
     // 4096 x 8192 twice, 29.7 with four, 29.5 with five, which take all of LDS)
-    if (best == 3)
+    if (best.kind == 3)
         hipLaunchKernelGGL((nt_tile<Shape<E, 64, 64, 2, 2, 4, 2, 4>, OP>), dim3((unsigned)tiles), dim3(256), 0, stream, op);
     return (int)hipGetLastError();
 }
