@@ -175,7 +175,8 @@ struct Backward {
     const P* weight;
     const float* saved;
     E* dX;
-    float* partial;  // [workgroups][2][cols]: sums of dY h and of dY; null: neither
+    float* partial;  // [workgroups][2][cols]: sums of dY h and of dY; null: none
+    P *dweight, *dbias;  // one workgroup's (null: not wanted)
     int64_t lddy, ldx, lddx;
     int rows, cols;
 };
@@ -264,8 +265,13 @@ __global__ void __launch_bounds__(G > 256 ? G : 256) norm_back_rows(const Backwa
             if (row < f.rows && c < cols) store<E, N>(to + c, cols - c, o);
         }
     }
-    if (!f.partial) return;
-    float* const out = f.partial + (int64_t)blockIdx.x * 2 * cols;
+    float* const out = f.partial ? f.partial + (int64_t)blockIdx.x * 2 * cols : nullptr;
+    auto put = [&](int c, int k, float sum) __attribute__((always_inline)) {
+        if (out) out[k * cols + c] = sum;
+        P* const to = k ? f.dbias : f.dweight;
+        if (to) to[c] = (P)sum;
+    };
+    if (!out && !f.dweight && !f.dbias) return;
     if constexpr (R == 1) {
 #pragma unroll
         for (int i = 0; i < C; ++i) {
@@ -273,8 +279,8 @@ __global__ void __launch_bounds__(G > 256 ? G : 256) norm_back_rows(const Backwa
 #pragma unroll
             for (int e = 0; e < N; ++e)
                 if (c + e < cols) {
-                    out[c + e] = aw[i][e];
-                    out[cols + c + e] = ab[i][e];
+                    put(c + e, 0, aw[i][e]);
+                    put(c + e, 1, ab[i][e]);
                 }
         }
     } else {
@@ -292,7 +298,7 @@ __global__ void __launch_bounds__(G > 256 ? G : 256) norm_back_rows(const Backwa
                 float sum = 0.0f;
 #pragma unroll
                 for (int g = 0; g < R; ++g) sum += meet[g * W + c];
-                out[k * cols + c] = sum;
+                put(c, k, sum);
             }
         }
     }
@@ -408,7 +414,10 @@ int64_t back_groups(int64_t rows, int64_t cols, int32_t type)
     // and 3 for each CU 8192 x 4096 in bfloat16 takes 49, 42 and 46 us, 2048 x 8192 (whose
     // lanes hold more) 32, 32 and 48, 1000 x 2731 16, 18 and 20 (four rows to a
     // workgroup, or two), 20000 x 300 34, 21 and 17.
+    // Few enough rows are one workgroup's, which needs no second launch (4 x 1024: 4.4
+    // us, and 4.4 and 3.5 in two; four turns of rows take longer than that).
     const int64_t per = w.g > 256 ? 1 : 256 / w.g;
+    if (rows > 0 && rows <= 2 * per) return 1;
     if (w.c == 1 && w.g <= 64) return sharers(rows, per, 4 * cus);
     return sharers(rows, per, w.c >= 4 || rows <= 4 * cus * per ? cus : 2 * cus);
 }
@@ -439,7 +448,13 @@ int forward(const Forward<E, P>& f, hipStream_t stream)
 template <class E, class P>
 int backward(Backward<E, P> f, P* dweight, P* dbias, float* partial, float* means, int64_t groups, hipStream_t stream)
 {
-    f.partial = dweight || dbias ? partial : nullptr;
+    const bool alone = groups == 1 && f.rows > 0 && way_of((f.cols + kChunk<E> - 1) / kChunk<E>).g > 0;
+    if (alone) {
+        f.dweight = dweight;
+        f.dbias = dbias;
+    } else if (dweight || dbias) {
+        f.partial = partial;
+    }
     const int64_t chunks = (f.cols + kChunk<E> - 1) / kChunk<E>;
     const Way w = way_of(chunks);
     int rc = hipSuccess;
@@ -468,7 +483,7 @@ int backward(Backward<E, P> f, P* dweight, P* dbias, float* partial, float* mean
         }
         if (rc) return rc;
     }
-    if (dweight || dbias) {
+    if (!alone && (dweight || dbias)) {  // (of no rows: zeros)
         const bool wide = wide_sums(f.cols, 2, cus::num_cus());
         const int64_t columns = wide ? 64 : 16;
         hipLaunchKernelGGL((wide ? norm_columns<P, 64> : norm_columns<P, 16>), dim3((unsigned)((f.cols + columns - 1) / columns), 2),
@@ -569,8 +584,8 @@ int layer_norm_backward(const void* dY, const void* X, const void* weight, const
     }
     const BackwardSpace w(workspace, rows, cols, type);
 #define BACKWARD(E, P)                                                                                                         \
-    backward<E, P>({(const E*)dY, (const E*)X, (const P*)weight, (const float*)saved, (E*)dX, nullptr, lddy, ldx, lddx, (int)rows, \
-                    (int)cols},                                                                                                \
+    backward<E, P>({(const E*)dY, (const E*)X, (const P*)weight, (const float*)saved, (E*)dX, nullptr, nullptr, nullptr, lddy, ldx, \
+                    lddx, (int)rows, (int)cols},                                                                                                \
                    (P*)dweight, (P*)dbias, w.partial, w.means, w.groups, stream)
     return FOR_TYPES(BACKWARD);
 #undef BACKWARD

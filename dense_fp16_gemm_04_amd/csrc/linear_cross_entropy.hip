@@ -796,7 +796,7 @@ struct Shares {
         const int64_t columns = few::kGradThreads * (T <= 8 ? 8 : 4);
         chunks = std::max<int64_t>((D + columns - 1) / columns, 1);
         const int64_t most = std::max<int64_t>((T <= 4 ? 4 : 2) * num_cus() / chunks, 1);
-        per = std::max<int64_t>(abi::up((V + most - 1) / most, 8), 16);
+        per = abi::up((V + most - 1) / most, 4);
         count = (V + per - 1) / per;
     }
 };

@@ -41,38 +41,32 @@ __device__ __forceinline__ f32x4 outputs(const E* X, const E* W, int64_t ldx, in
         w[b] = W + min(first + b * 16 + r, (int64_t)V - 1) * ldw;
         acc[b] = f32x4{0, 0, 0, 0};
     }
-    auto load8 = [&](const E* p, int k) __attribute__((always_inline)) {
-        rows::Vec<E, 8> v = {};
-        if (k < D) v = rows::load<E, 8>(p + k, D - k);
-        return __builtin_bit_cast(x8, v);
-    };
-    // eight steps' loads in flight
+    // eight steps' loads in flight; in the last round, of steps that may reach past
+    // K or not be there (zeros)
     constexpr int AHEAD = 8;
-    const int whole = D / 32;
-    int s = wave;
-    for (; s + (AHEAD - 1) * kWaves < whole; s += AHEAD * kWaves) {
+    auto round = [&](int s, auto all) __attribute__((always_inline)) {
+        constexpr bool ALL = decltype(all)::value;
+        auto load8 = [&](const E* p, int k) __attribute__((always_inline)) {
+            rows::Vec<E, 8> v = {};
+            if (ALL || k < D) v = rows::load<E, 8>(p + k, ALL ? 8 : D - k);
+            return __builtin_bit_cast(x8, v);
+        };
         x8 fx[AHEAD], fw[AHEAD][B];
 #pragma unroll
         for (int a = 0; a < AHEAD; ++a) {
             const int k = (s + a * kWaves) * 32 + q * 8;
-            fx[a] = __builtin_bit_cast(x8, rows::load<E, 8>(x + k, 8));
+            fx[a] = load8(x, k);
 #pragma unroll
-            for (int b = 0; b < B; ++b) fw[a][b] = __builtin_bit_cast(x8, rows::load<E, 8>(w[b] + k, 8));
+            for (int b = 0; b < B; ++b) fw[a][b] = load8(w[b], k);
         }
 #pragma unroll
         for (int a = 0; a < AHEAD; ++a)
 #pragma unroll
             for (int b = 0; b < B; ++b) acc[b] = Elem<E>::mfma(fw[a][b], fx[a], acc[b]);
-    }
-    for (; s * 32 < D; s += kWaves) {
-        const int k = s * 32 + q * 8;
-        const x8 fx = load8(x, k);
-        x8 fw[B];
-#pragma unroll
-        for (int b = 0; b < B; ++b) fw[b] = load8(w[b], k);
-#pragma unroll
-        for (int b = 0; b < B; ++b) acc[b] = Elem<E>::mfma(fw[b], fx, acc[b]);
-    }
+    };
+    int s = wave;
+    for (; s + (AHEAD - 1) * kWaves < D / 32; s += AHEAD * kWaves) round(s, nt::Flag<true>{});
+    if (s * 32 < D) round(s, nt::Flag<false>{});
 #pragma unroll
     for (int b = 0; b < B; ++b) part[wave][b][lane] = acc[b];
     __syncthreads();
@@ -193,14 +187,16 @@ __global__ void __launch_bounds__(kGradThreads) few_grads(const Grads<E> f)
     if (c >= f.D) return;
     const int left = (int)std::min<int64_t>(f.D - c, NC);
     float x[TT][NC], sum[TT][NC];
+    V v[TT];
+#pragma unroll
+    for (int t = 0; t < TT; ++t) v[t] = rows::load<E, NC>(f.X + min(t, f.T - 1) * f.ldx + c, left);
 #pragma unroll
     for (int t = 0; t < TT; ++t) {
-        // (of a token that is ignored nothing is read: 0 times what it holds may be NaN)
-        V v = {};
-        if (t < f.T && f.target[t * f.target_stride] != f.ignore) v = rows::load<E, NC>(f.X + t * f.ldx + c, left);
+        // (of a token that is ignored nothing counts: 0 times what it holds may be NaN)
+        const bool counts = t < f.T && f.target[min(t, f.T - 1) * f.target_stride] != f.ignore;
 #pragma unroll
         for (int k = 0; k < NC; ++k) {
-            x[t][k] = (float)v[k];
+            x[t][k] = counts ? (float)v[t][k] : 0.0f;
             sum[t][k] = 0.0f;
         }
     }
