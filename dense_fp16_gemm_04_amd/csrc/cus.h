@@ -1,10 +1,13 @@
-// How many CUs the current device has.
+// How many CUs the current device has, and an MI355X (for what sizes a workspace or
+// orders a sum, and so may not depend on the device that is current).
 #ifndef DENSE_FP16_GEMM_CUS_H
 #define DENSE_FP16_GEMM_CUS_H
 
 #include <hip/hip_runtime.h>
 
 namespace cus {
+
+constexpr int kCus = 256;
 
 inline int num_cus()
 {

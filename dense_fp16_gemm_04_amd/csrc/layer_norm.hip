@@ -408,7 +408,7 @@ Way way_of(int64_t chunks)
 int64_t back_groups(int64_t rows, int64_t cols, int32_t type)
 {
     const Way w = way_of(chunks_of(cols, type));
-    const int cus = cus::num_cus();
+    constexpr int cus = cus::kCus;
     if (w.g == 0) return sharers(rows, 1, 64);
     // Each workgroup's sums cross memory twice, and fewer workgroups hide less: with 1, 2
     // and 3 for each CU 8192 x 4096 in bfloat16 takes 49, 42 and 46 us, 2048 x 8192 (whose
@@ -426,7 +426,7 @@ template <class E, class P>
 int forward(const Forward<E, P>& f, hipStream_t stream)
 {
     const int64_t chunks = (f.cols + kChunk<E> - 1) / kChunk<E>;
-    const int64_t most = (int64_t)cus::num_cus() * 8;
+    const int64_t most = cus::kCus * 8;
     auto with = [&](auto kernel, int threads, int per) {
         const int64_t n = std::min((f.rows + (int64_t)per - 1) / per, most);
         hipLaunchKernelGGL(kernel, dim3((unsigned)n), dim3(threads), 0, stream, f);
@@ -473,7 +473,7 @@ int backward(Backward<E, P> f, P* dweight, P* dbias, float* partial, float* mean
         else if (w.g == 256 && w.c == 4) rc = with(norm_back_rows<E, P, 256, 4>);
         else if (w.g == 512) rc = with(norm_back_rows<E, P, 512, 4>);
         else {
-            hipLaunchKernelGGL((norm_back_means<E, P>), dim3((unsigned)std::min<int64_t>(f.rows, 2 * cus::num_cus())), dim3(kWide), 0,
+            hipLaunchKernelGGL((norm_back_means<E, P>), dim3((unsigned)std::min<int64_t>(f.rows, 2 * cus::kCus)), dim3(kWide), 0,
                                stream, f, means);
             if ((rc = (int)hipGetLastError())) return rc;
             const int64_t tiles = (chunks + kTileThreads - 1) / kTileThreads;
@@ -484,7 +484,7 @@ int backward(Backward<E, P> f, P* dweight, P* dbias, float* partial, float* mean
         if (rc) return rc;
     }
     if (!alone && (dweight || dbias)) {  // (of no rows: zeros)
-        const bool wide = wide_sums(f.cols, 2, cus::num_cus());
+        const bool wide = wide_sums(f.cols, 2);
         const int64_t columns = wide ? 64 : 16;
         hipLaunchKernelGGL((wide ? norm_columns<P, 64> : norm_columns<P, 16>), dim3((unsigned)((f.cols + columns - 1) / columns), 2),
                            dim3(kSumThreads), 0, stream, (const float*)partial, (int)groups, f.cols, dweight, dbias);

@@ -795,7 +795,7 @@ struct Shares {
     {
         const int64_t columns = few::kGradThreads * (T <= 8 ? 8 : 4);
         chunks = std::max<int64_t>((D + columns - 1) / columns, 1);
-        const int64_t most = std::max<int64_t>((T <= 4 ? 4 : 2) * num_cus() / chunks, 1);
+        const int64_t most = std::max<int64_t>((T <= 4 ? 4 : 2) * cus::kCus / chunks, 1);
         per = abi::up((V + most - 1) / most, 4);
         count = (V + per - 1) / per;
     }
@@ -863,7 +863,7 @@ int backward_few(const float* dloss, const E* X, const E* W, const int64_t* targ
     else rc = with(few::few_grads<E, 16, 4>);
     if (rc) return rc;
     const few::Sum<E> sum = {w.partial, target, dX, target_stride, ignore, lddx, (int)T, (int)D, (int)s.count};
-    const bool wide = rows::wide_sums(D, T, num_cus());
+    const bool wide = rows::wide_sums(D, T);
     const int64_t columns = wide ? 64 : 16;
     hipLaunchKernelGGL((wide ? few::few_sum<E, 64> : few::few_sum<E, 16>), dim3((unsigned)((D + columns - 1) / columns), (unsigned)T),
                        dim3(rows::kSumThreads), 0, stream, sum);
@@ -966,7 +966,7 @@ int backward(const float* dloss, const E* X, const E* W, const int64_t* target, 
 
 bool good_sizes(int64_t T, int64_t D, int64_t V)
 {
-    return T >= 0 && T <= abi::kMaxDim - 256 && D >= 0 && D <= abi::kMaxPitch - 63 && V > 0 && V <= abi::kMaxDim - 256;
+    return T >= 0 && T <= (int64_t)1 << 27 && D >= 0 && D <= abi::kMaxPitch - 63 && V > 0 && V <= abi::kMaxDim - 256;
 }
 bool good_backward_sizes(int64_t T, int64_t D, int64_t V) { return good_sizes(T, D, V) && T <= abi::kMaxPitch - 63; }
 // Workgroups that lay out X and V rows of W, and the one beside them.

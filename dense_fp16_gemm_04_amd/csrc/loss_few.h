@@ -14,7 +14,6 @@
 namespace few {
 
 using namespace cdna4;
-using cus::num_cus;
 
 constexpr int kTokens = 16;   // the most
 constexpr int kWaves = 4;     // of a workgroup, which take K's steps of 32 in turn
@@ -23,7 +22,7 @@ constexpr int kRows = 32;     // of W to a part at least
 // B blocks of 16 rows of W to a workgroup at a time: four, with half the loads of X,
 // where they are enough for the chip (8 tokens by 32000 x 2048, a graph's replay: 34.0 us with
 // two, 30.3 with four; 3 by 13991 x 640 15.0 and 15.9).
-inline int blocks_of(int64_t V) { return V >= 96 * num_cus() ? 4 : 2; }
+inline int blocks_of(int64_t V) { return V >= 96 * cus::kCus ? 4 : 2; }
 
 // The outputs of 16 B rows of W from `first` on: wave b has block b, lane l token l % 16
 // and rows 4 (l / 16) .. + 3 of it, once all waves' shares have met in `part`.

@@ -39,17 +39,22 @@
  * or freed by work enqueued later on the same stream.
  *
  * hipErrorInvalidValue before anything is enqueued: a negative size, V == 0, T
- * or V above 2^31 - 257 (T above 2^21 - 64 in the backward pass, whose sums run
- * over T), D above 2^21 - 64, a result of more tiles than a launch can hold, a
- * row pitch below the row or of 2^21 or more, a negative stride or one above 2^31, an unknown type,
- * a null or misaligned pointer with a non-zero extent (elements on their size),
- * an output whose first-to-last-element range meets an input's, another
- * output's or the workspace's, a workspace that is too small.
+ * above 2^27 (2^21 - 64 in the backward pass, whose sums run over T), V above
+ * 2^31 - 257, D above 2^21 - 64, a result or operands of more tiles than a launch
+ * can hold, a row pitch below the row or of 2^21 or more, a negative stride or
+ * one above 2^31, an unknown type, a null or misaligned pointer with a non-zero
+ * extent (elements on their size), an output whose first-to-last-element range
+ * meets an input's, another output's or the workspace's, a workspace that is
+ * too small.
  *
  * T == 0 writes no loss and zeros to dW; D == 0 makes every l zero.  Any 2-byte
  * aligned X, W, dX and dW and any sizes are accepted.  The kernels read 16 bytes at
- * a time: an X or W whose pointer is not 16-byte aligned or whose pitch or D is
- * no multiple of 8 is first copied into the workspace.
+ * a time: of more than 16 tokens an X or W whose pointer is not 16-byte aligned or
+ * whose pitch or D is no multiple of 8 is first copied into the workspace (181
+ * tokens by 109366 x 333: 43 us of a step's 340).
+ *
+ * Up to 16 tokens have kernels of their own, which read W where it lies, hold dl
+ * in 32 bits and never round it (the gradients' only rounding is their own).
  */
 #ifndef LINEAR_CROSS_ENTROPY_H
 #define LINEAR_CROSS_ENTROPY_H

@@ -163,8 +163,9 @@ def loss(x, w, target, ignore=-100):
     return torch.where(valid, y, zero), torch.where(valid, bound, zero), (x, w, valid, at, p, l, top, s, s_rel, l_off)
 
 
-def loss_gradients(dloss, t, parts):
-    """((dx, dw), their bounds); t: the operands' type."""
+def loss_gradients(dloss, t, parts, rounded=True):
+    """((dx, dw), their bounds); t: the operands' type; rounded: dl is rounded to
+    it (as of more than 16 tokens)."""
     x, w, valid, at, p, l, top, s, s_rel, l_off = parts
     T, D = x.shape
     V = w.shape[0]
@@ -178,6 +179,8 @@ def loss_gradients(dloss, t, parts):
     most = float(g.abs().max()) if T else 0.0
     rounding = rel * dl.abs() + small
     rounding.scatter_(1, at, torch.full_like(s, 4 * EPS))  # (what it takes there is put back)
+    if not rounded:
+        rounding = EPS * dl.abs()
 
     def sums(a, off, rnd, b, n, factor):
         y = a @ b
@@ -189,7 +192,8 @@ def loss_gradients(dloss, t, parts):
     one = torch.ones((), dtype=torch.float64, device=x.device)
     dx = sums(dl, p_off, rounding, w, V, g)
     gd = g * dl
-    dw = sums(gd.T, (g.abs() * p_off).T + 4 * EPS * gd.abs().T, (rel * gd.abs() + most * small).T, x, T, one)
+    of_dw = rel * gd.abs() + most * small if rounded else EPS * gd.abs()
+    dw = sums(gd.T, (g.abs() * p_off).T + 4 * EPS * gd.abs().T, of_dw.T, x, T, one)
     return (dx[0], dw[0]), (dx[1], dw[1])
 
 

@@ -42,7 +42,7 @@ def inputs(T, D, V, t, seed=0, ignored=0.2, sure=4.0):
 def check(x, w, target, dloss, loss, got, ignore=-100):
     want, bound, parts = plain.loss(x, w, target, ignore)
     plain.assert_near(loss, want, bound, "loss")
-    want, bounds = plain.loss_gradients(dloss, x.dtype, parts)
+    want, bounds = plain.loss_gradients(dloss, x.dtype, parts, rounded=len(x) > 16)
     for name, g, v, b in zip(("dx", "dw"), got, want, bounds):
         plain.assert_near(g, v, b, name)
 
@@ -65,6 +65,23 @@ def test_loss_and_gradients(shape, t):
     loss, got = step(x, w, target, dloss)
     assert torch.equal(loss, fw.linear_cross_entropy(x, w, target))
     check(x, w, target, dloss, loss, got)
+
+
+# up to 16 tokens: with 1, 4, 8 and 16 rows of registers; one and several pieces
+# of D; vocabularies below and above where more rows of w go to a workgroup, and
+# that no share or block divides; odd widths and D below a step
+@pytest.mark.parametrize("t", ["fp16", "bf16"])
+@pytest.mark.parametrize("shape", [(1, 1030, 33), (2, 7, 4097), (3, 4100, 70), (4, 31, 25000), (5, 2049, 515), (8, 333, 30001), (9, 1025, 66),
+                                   (12, 65, 24577), (13, 3491, 1001), (16, 2056, 131), (16, 520, 40000), (15, 4096, 3)], ids=str)
+def test_few_tokens(shape, t):
+    x, w, target, dloss = inputs(*shape, plain.TYPES[t], seed=sum(shape))
+    loss, got = step(x, w, target, dloss)
+    assert torch.equal(loss, fw.linear_cross_entropy(x, w, target))
+    check(x, w, target, dloss, loss, got)
+    # (the same in views at other addresses, bit for bit)
+    vx, vw = framed(x, cols=3, offset=1)[0], framed(w, cols=5)[0]
+    l2, (dx, dw) = step(vx, vw, target, dloss)
+    assert torch.equal(l2, loss) and torch.equal(dx, got[0]) and torch.equal(dw, got[1])
 
 
 # the largest tiles, more of them than CUs, with tails; and K loops of 3 to 17

@@ -219,11 +219,11 @@ def loss_args(**kw):
 
 
 @pytest.mark.parametrize("kw", [
-    dict(T=-1), dict(D=-1), dict(V=-1), dict(V=0), dict(T=1 << 31), dict(V=1 << 31), dict(D=1 << 21, ldx=1 << 21, ldw=1 << 21), dict(ldx=15),
+    dict(T=-1), dict(D=-1), dict(V=-1), dict(V=0), dict(T=(1 << 27) + 1), dict(V=1 << 31), dict(D=1 << 21, ldx=1 << 21, ldw=1 << 21), dict(ldx=15),
     dict(ldw=15), dict(ldx=1 << 21), dict(stride=-1), dict(stride=(1 << 31) + 1), dict(type=2), dict(type=-1), dict(X=None), dict(W=None),
     dict(target=None), dict(loss=None), dict(X=A + 1), dict(W=B + 1), dict(target=C + 4), dict(loss=D + 2), dict(saved=E + 2),
     dict(ws=None), dict(ws_bytes=64), dict(ws=W + 8), dict(loss=A), dict(loss=B), dict(loss=C), dict(saved=A), dict(saved=D), dict(ws=A),
-    dict(ws=D), dict(T=1 << 28, V=1 << 28, ws_bytes=1 << 60), dict(T=64, D=512, ldx=512, ldw=512, ws_bytes=1 << 20),
+    dict(ws=D), dict(T=1 << 27, V=1 << 28, ws_bytes=1 << 60), dict(T=64, D=512, ldx=512, ldw=512, ws_bytes=1 << 20),
 ])
 def test_loss_refuses(kw):
     assert operators.load("linear_cross_entropy").linear_cross_entropy(*loss_args(**kw)) == INVALID
