@@ -108,8 +108,12 @@ struct LseOp {
         // -infinity is added to columns that are not there, 0 to the others
         const int there = N - n0 - 4 * (ln >> 4);  // of the lane's columns, from its first on
         float top[T::FM], sum[T::FM];
+        int64_t c[T::FM];  // (loaded while the sums are made)
 #pragma unroll
-        for (int i = 0; i < T::FM; ++i) top[i] = -INFINITY;
+        for (int i = 0; i < T::FM; ++i) {
+            top[i] = -INFINITY;
+            c[i] = target[min(m0 + i * 16 + (ln & 15), M - 1) * target_stride];
+        }
 #pragma unroll
         for (int j = 0; j < T::FN; ++j) {
             const f32x4 bias = absent(j, there);
@@ -144,8 +148,8 @@ struct LseOp {
             const int row = m0 + i * 16 + (ln & 15);
             const f32x2 part = {top[i], sum_over_groups(sum[i])};
             __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(u32x2, part), to, ln < 16 ? (i * 16 + ln) * 8 : kOob, 0, 0);
-            const int64_t c = target[min(row, M - 1) * target_stride] - first - n0;
-            at[i] = row < M && c >= 0 && c < min(T::WTN, N - n0) ? (int)c - 4 * (ln >> 4) : -1;
+            const int64_t place = c[i] - first - n0;
+            at[i] = row < M && place >= 0 && place < min(T::WTN, N - n0) ? (int)place - 4 * (ln >> 4) : -1;
             any |= at[i] >= 0;
         }
         if (!__any(any)) return;

@@ -49,10 +49,12 @@ def _check_norm(x, weight, bias):
     ldx = _pitch("x", x, _TYPES_AND_F32)
     device = x.get_device()
     types = (x.dtype, torch.float32)
-    for name, t in (("weight", weight), ("bias", bias)):
-        if t is not None:
-            _vector(name, t, types, device, x.shape[1])
-            types = (t.dtype,)  # one type for both
+    if weight is not None:
+        _vector("weight", weight, types, device, x.shape[1])
+        types = (weight.dtype,)  # one type for both
+    if bias is not None:
+        _vector("bias", bias, types, device, x.shape[1])
+        types = (bias.dtype,)
     return device, ldx, types[0]
 
 
@@ -84,7 +86,7 @@ def layer_norm(x, weight=None, bias=None, eps: float = 1e-5, out=None):
     ``layer_norm_backward`` are its training form.
     """
     y = _norm(x, weight, bias, eps, out, False)[0]
-    if out is None and any(t is not None and t.requires_grad for t in (x, weight, bias)):
+    if out is None and (x.requires_grad or (weight is not None and weight.requires_grad) or (bias is not None and bias.requires_grad)):
         return _without_gradients(
             y, "layer_norm has no gradients in autograd: use layer_norm_train and layer_norm_backward", x, weight, bias)
     return y
