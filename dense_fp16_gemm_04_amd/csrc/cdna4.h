@@ -61,6 +61,12 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t make_rsrc(const void* base, ui
     return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), (short)0, (int)bytes, kRsrcWord3);
 }
 
+// 16 bytes to each lane's place in LDS, `to` plus 16 times the lane.
+__device__ __forceinline__ void load_lds(__amdgpu_buffer_rsrc_t from, lds_void* __restrict to, uint32_t off, uint32_t soff)
+{
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(from, to, 16, off, soff, 0, 0);
+}
+
 // Wait until at most VM of this wave's vector memory accesses are in flight
 // and its LDS accesses are done, then meet the workgroup's other waves.  One
 // asm statement, so that no access moves across it; __syncthreads() would
@@ -70,6 +76,20 @@ __device__ __forceinline__ void lds_barrier()
 {
     static_assert(VM >= 0 && VM <= 63, "vmcnt holds 0 .. 63");
     asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"i"(VM) : "memory");
+}
+
+// Four 16-bit values of each lane's from LDS, turned among 16 lanes: lane l gets
+// value l % 4 of lanes 4 e + l / 4, e = 0 .. 3.  (Lanes 4 e .. 4 e + 3 read 16
+// columns of row e, and lane l gets column l of four rows.)  `__restrict`, here and in
+// load_lds: else the compiler waits before each such read for all loads into LDS that
+// are in flight, where the barriers have waited for those that matter.
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
+__device__ __forceinline__ s16x4 read_turned(lds_s16x4* __restrict p) { return __builtin_amdgcn_ds_read_tr16_b64_v4i16(p); }
+template <class E>
+__device__ __forceinline__ typename Elem<E>::x4 read_turned(const unsigned char* p)
+{
+    return __builtin_bit_cast(typename Elem<E>::x4, read_turned((lds_s16x4*)p));
 }
 
 // LDS tiles hold 128-byte rows (64 elements) as eight 16-byte chunks; chunk

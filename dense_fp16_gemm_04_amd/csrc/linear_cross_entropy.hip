@@ -8,8 +8,8 @@
 // Backward, a piece of the vocabulary at a time: the product again, whose
 // epilogue turns outputs to dl = softmax - onehot and writes it row-major, and
 // times dloss transposed; dX += dl W, with sums kept in 32 bits from piece to
-// piece, and dW = (dloss dl)^T X, both in NT form on transposed copies of W's piece
-// and of X.
+// piece, and dW = (dloss dl)^T X in NT form on a transposed copy of X.  dX takes W
+// as it lies, or (in the largest tiles) from a transposed copy of the piece.
 #include "linear_cross_entropy.h"
 
 #include <algorithm>
@@ -261,16 +261,17 @@ constexpr float kShift<_Float16> = 15.0f;
 // that times `weight`, dloss over its largest magnitude, which dW's product puts
 // back: where all tokens have one dloss, as of a mean, its digits then are in no
 // rounding (8192 x 4096 x 131072 in bfloat16: dW 3.0e-3 off with dloss itself in
-// them, twice what its own rounding leaves).  A row that is ignored or not there has 0, -infinity, 0, 0: then
-// the minimum, which takes the number of a number and NaN, makes dl zero whatever
-// l is.  So it does where l is of a column that is not there, and of columns that
-// are l is no larger than top but by another order of summation.
+// them, twice what its own rounding leaves).  A row that is ignored or not there
+// has 0, -infinity, 0, 0: then the minimum, which takes the number of a number and
+// NaN, makes dl zero whatever l is.  Of columns that are not there it keeps dl
+// finite, and of those that are l is no larger than top but by another order of
+// summation.
 //
 // The target's dl is most of a row's size, and its rounding most of dX's error
 // where few terms are large.  Each row of dl is therefore held times what makes
-// `hit` a number of the type (1 and half a step at most), which `back`, the factor to the row's
-// sums, and `weight` take out again: dX (300 x 200 x 513, binary16) 2.28e-4 off,
-// its own rounding, and 2.73e-4 without.
+// `hit` a number of the type (1 and half a step at most), which `back`, the factor
+// to the row's sums, and `weight` take out again: dX (300 x 200 x 513, binary16)
+// 2.28e-4 off, its own rounding, and 2.73e-4 without.
 struct RowInfo {
     float top, bias, weight, hit;
 };
@@ -342,7 +343,8 @@ struct LayOut {
 
     __host__ __device__ int64_t tiles() const
     {
-        return copy || turned ? ((int64_t)rows + relayout::kTile - 1) / relayout::kTile * (((int64_t)cols + relayout::kTile - 1) / relayout::kTile) : 0;
+        constexpr int64_t N = relayout::kTile;
+        return copy || turned ? (rows + N - 1) / N * ((cols + N - 1) / N) : 0;
     }
     __device__ __forceinline__ void run(int id, E* tile) const
     {
@@ -503,8 +505,8 @@ struct DlOp {
 #pragma unroll
             for (int it = 0; it < ITERS; ++it) {
                 const int x = x0 + it * RPI;
-                __builtin_amdgcn_raw_buffer_store_b128(turned.get(x, ch), to_t.rs, m < to_t.cols ? (uint32_t)x * to_t.pitch + (uint32_t)m * 2u : kOob,
-                                                       0, 0);
+                const uint32_t at = m < to_t.cols ? (uint32_t)x * to_t.pitch + (uint32_t)m * 2u : kOob;
+                __builtin_amdgcn_raw_buffer_store_b128(turned.get(x, ch), to_t.rs, at, 0, 0);
             }
             lds_barrier<63>();
         }
@@ -515,12 +517,13 @@ struct DlOp {
 // which a wave's lanes hold them (lane l: row l % 16, columns 4 (l / 16) .. + 3).
 constexpr int kBlockFloats = 256;
 
-template <class E>
+// TURNED: B is W where it lies, `there` rows.
+template <class E, bool TURNED>
 struct AddOp {
-    static constexpr bool kPersist = true, kSplit = true;
+    static constexpr bool kPersist = !TURNED, kSplit = true, kTurned = TURNED;
     const E *A, *B;
     float* sums;
-    int M, N, K, lda, ldb, fresh, tiles, tiles_m, tiles_n;  // fresh: sums hold nothing yet
+    int M, N, K, lda, ldb, there, fresh, tiles, tiles_m, tiles_n;  // fresh: sums hold nothing yet
 
     template <int BM, int BN>
     __device__ __forceinline__ void tile(int id, Tile& t) const
@@ -540,6 +543,12 @@ struct AddOp {
     __device__ __forceinline__ const E* b_rows(const Tile& t, int row, int& n) const
     {
         return rows_from(B, t.n0 + row, N, ldb, n);
+    }
+    __device__ __forceinline__ const E* b_turned(const Tile& t, int& steps, int& cols) const
+    {
+        steps = there;
+        cols = ((N + 7) & ~7) - t.n0;
+        return B + t.n0;
     }
     template <int WTN>
     __device__ __forceinline__ int b_pitch(int) const
@@ -607,9 +616,9 @@ __device__ __forceinline__ void write_any(Value value, E* out, int64_t ld, int m
 
 // The last piece's: dX[t] = back[t] (A B^T and, MORE, the sums of the pieces before),
 // rounded.  EIGHTS: dX's rows take 16-byte pieces and hold a multiple of eight.
-template <class E, bool EIGHTS, bool MORE>
-struct DxOp : AddOp<E> {
-    using Base = AddOp<E>;
+template <class E, bool TURNED, bool EIGHTS, bool MORE>
+struct DxOp : AddOp<E, TURNED> {
+    using Base = AddOp<E, TURNED>;
     E* dX;
     const float* back;
     int ldx, pad;
@@ -632,7 +641,8 @@ struct DxOp : AddOp<E> {
                     const __amdgpu_buffer_rsrc_t from = make_rsrc(at, i < rows ? (uint32_t)left * (kBlockFloats * 4u) : 0u);
 #pragma unroll
                     for (int k = 0; k < T::FN; ++k)
-                        old[k] = __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(from, ln * 16 + k * (kBlockFloats * 4), 0, 0));
+                        old[k] = __builtin_bit_cast(
+                            f32x4, __builtin_amdgcn_raw_buffer_load_b128(from, ln * 16 + k * (kBlockFloats * 4), 0, 0));
                 }
             const f32x4 v = EIGHTS ? acc[i][j] : read<T>(acc[i][j]);
             return round4<E>((MORE ? v + old[j] : v) * g[i]);
@@ -653,8 +663,8 @@ struct DwOp : StoreOp<E, false, true> {
                                              unsigned char* s1) const
     {
         const float f = *Base::factor;
-        write_any<T>([&](int i, int j) __attribute__((always_inline)) { return round4<E>(read<T>(acc[i][j]) * f); }, Base::C[0], Base::ldc[0],
-                     t.m0, Base::M, t.n0, Base::N, lane, wave, s0, s1);
+        auto value = [&](int i, int j) __attribute__((always_inline)) { return round4<E>(read<T>(acc[i][j]) * f); };
+        write_any<T>(value, Base::C[0], Base::ldc[0], t.m0, Base::M, t.n0, Base::N, lane, wave, s0, s1);
     }
 };
 
@@ -680,6 +690,22 @@ int64_t first_of_two(int64_t other, int64_t n, int64_t K, bool partial)
     if (K <= 128 || first == 0 || first >= n) return n;
     const Choice one = choose<OP>(K, partial, tiles(n)), rest = choose<OP>(K, partial, tiles(n - first));
     return model_us(kKinds[0], waves * cus, K, cus) + rest.us + 4.0 < one.us ? first : n;
+}
+
+// Whether dX's product over n rows of W reads them as they lie: not in 256 x 256 tiles,
+// which are faster, but without the transpose, whose bytes cross memory twice (once
+// where W is copied anyway).  (Steps with it and without: 17 x 4096 x 20000 256 us and
+// 163, 200 x 1024 x 32000 127 and 108, 1000 x 1032 x 32001 394 and 340, 2048 x 2048 x
+// 32000 975 and 909, 8192 x 1024 x 50000 3410 and 3290; 8192 x 4096 x 32768, in 256 x 256
+// tiles, 6000 and 6330.)
+template <class E>
+bool turned_for(int64_t T, int64_t n, int64_t D, bool copied)
+{
+    auto tiles = [=](const Kind& k) { return (T + k.bm - 1) / k.bm * ((D + k.bn - 1) / k.bn); };
+    const int64_t K = abi::up(n, 8);
+    const bool split = K >= kSplitK;
+    const double transpose = 2.0 * n * D * (copied ? 1 : 2) / 4.9e6;
+    return choose<AddOp<E, true>>(K, split, tiles).us < choose<AddOp<E, false>>(K, split, tiles).us + transpose;
 }
 
 // The parts of up to this many outputs may be of 32 columns, of more 64 at least
@@ -844,9 +870,9 @@ struct BackwardSpace {
 };
 
 template <class E>
-int backward_few(const float* dloss, const E* X, const E* W, const int64_t* target, const float* saved, E* dX, E* dW, int64_t T, int64_t D,
-                 int64_t V, int64_t dloss_stride, int64_t ldx, int64_t ldw, int64_t target_stride, int64_t lddx, int64_t lddw, int64_t ignore,
-                 const BackwardSpace<E>& w, hipStream_t stream)
+int backward_few(const float* dloss, const E* X, const E* W, const int64_t* target, const float* saved, E* dX, E* dW, int64_t T,
+                 int64_t D, int64_t V, int64_t dloss_stride, int64_t ldx, int64_t ldw, int64_t target_stride, int64_t lddx,
+                 int64_t lddw, int64_t ignore, const BackwardSpace<E>& w, hipStream_t stream)
 {
     if (D == 0) return hipSuccess;
     const few::Dl<E> d = {X, W, target, dloss, saved, w.sums, target_stride, dloss_stride, ignore, ldx, ldw, (int)T, (int)D, (int)V};
@@ -856,7 +882,8 @@ int backward_few(const float* dloss, const E* X, const E* W, const int64_t* targ
     int rc = (int)hipGetLastError();
     if (rc) return rc;
     const Shares s(T, D, V);
-    const few::Grads<E> g = {X, W, target, w.sums, dW, w.partial, target_stride, ignore, ldx, ldw, lddw, (int)T, (int)D, (int)V, (int)s.per};
+    const few::Grads<E> g = {X,      W,   target, w.sums, dW,     w.partial, target_stride, ignore,
+                             ldx,    ldw, lddw,   (int)T, (int)D, (int)V,    (int)s.per};
     auto with = [&](auto kernel) {
         hipLaunchKernelGGL(kernel, dim3((unsigned)s.count, (unsigned)s.chunks), dim3(few::kGradThreads), 0, stream, g);
         return (int)hipGetLastError();
@@ -875,13 +902,14 @@ int backward_few(const float* dloss, const E* X, const E* W, const int64_t* targ
 }
 
 template <class E>
-int backward(const float* dloss, const E* X, const E* W, const int64_t* target, const float* saved, E* dX, E* dW, int64_t T, int64_t D,
-             int64_t V, int64_t dloss_stride, int64_t ldx, int64_t ldw, int64_t target_stride, int64_t lddx, int64_t lddw, int64_t ignore,
-             void* workspace, hipStream_t stream)
+int backward(const float* dloss, const E* X, const E* W, const int64_t* target, const float* saved, E* dX, E* dW, int64_t T,
+             int64_t D, int64_t V, int64_t dloss_stride, int64_t ldx, int64_t ldw, int64_t target_stride, int64_t lddx,
+             int64_t lddw, int64_t ignore, void* workspace, hipStream_t stream)
 {
     const BackwardSpace<E> w(workspace, X, W, T, D, V, ldx, ldw);
     if (T > 0 && T <= few::kTokens)
-        return backward_few<E>(dloss, X, W, target, saved, dX, dW, T, D, V, dloss_stride, ldx, ldw, target_stride, lddx, lddw, ignore, w, stream);
+        return backward_few<E>(dloss, X, W, target, saved, dX, dW, T, D, V, dloss_stride, ldx, ldw, target_stride, lddx, lddw,
+                               ignore, w, stream);
     int rc;
     const int64_t ld = abi::up(D, kLine);
     for (int64_t v0 = 0; v0 < V; v0 += w.piece) {
@@ -889,10 +917,12 @@ int backward(const float* dloss, const E* X, const E* W, const int64_t* target, 
         const E* const W0 = W + v0 * ldw;
         Prepare<E> p = {};
         if (v0 == 0) {
-            p.numbers = {dloss, saved, target, dloss_stride, target_stride, ignore, (int)T, (int)w.rows, (int)V, w.info, w.column, w.back, w.factor};
+            p.numbers = {dloss,  saved,       target, dloss_stride, target_stride, ignore,  (int)T,
+                         (int)w.rows, (int)V, w.info, w.column,     w.back,        w.factor};
             p.x = {X, w.x, w.xt, ldx, ld, w.Tp, (int)T, (int)D, target, target_stride, ignore};
         }
-        if (T > 0) p.w = {W0, w.w, w.wt, ldw, ld, w.Vp, (int)n, (int)D};
+        const bool turned = D > 0 && turned_for<E>(T, n, D, w.w != nullptr);
+        if (T > 0) p.w = {W0, w.w, turned ? nullptr : w.wt, ldw, ld, w.Vp, (int)n, (int)D};
         if ((rc = enqueue(p, v0 == 0, stream))) return rc;
         if (T > 0) {
             DlOp<E> op = {};
@@ -917,12 +947,14 @@ int backward(const float* dloss, const E* X, const E* W, const int64_t* target, 
             if (D > 0) {
                 auto product = [&](auto op) {
                     op.A = w.dl;
-                    op.B = w.wt;
+                    op.B = !turned ? w.wt : w.w ? w.w : W0;
                     op.sums = w.sums;
                     op.M = (int)T;
                     op.N = (int)D;
                     op.K = (int)abi::up(n, 8);
-                    op.lda = op.ldb = (int)w.Vp;
+                    op.lda = (int)w.Vp;
+                    op.ldb = (int)(!turned ? w.Vp : w.w ? ld : ldw);
+                    op.there = (int)n;
                     op.fresh = v0 == 0;
                     return launch_grid<E>(op, T, D, 1, 1, op.K, op.K >= kSplitK ? w.partial : nullptr, stream);
                 };
@@ -933,12 +965,13 @@ int backward(const float* dloss, const E* X, const E* W, const int64_t* target, 
                     return product(op);
                 };
                 const bool eights = vec8(dX, lddx) && D % 8 == 0;
-                if (v0 + n < V)
-                    rc = product(AddOp<E>{});
-                else if (v0 == 0)
-                    rc = eights ? last(DxOp<E, true, false>{}) : last(DxOp<E, false, false>{});
-                else
-                    rc = eights ? last(DxOp<E, true, true>{}) : last(DxOp<E, false, true>{});
+                auto either = [&](auto t) {
+                    constexpr bool TURNED = decltype(t)::value;
+                    if (v0 + n < V) return product(AddOp<E, TURNED>{});
+                    if (v0 == 0) return eights ? last(DxOp<E, TURNED, true, false>{}) : last(DxOp<E, TURNED, false, false>{});
+                    return eights ? last(DxOp<E, TURNED, true, true>{}) : last(DxOp<E, TURNED, false, true>{});
+                };
+                rc = turned ? either(Flag<true>{}) : either(Flag<false>{});
                 if (rc) return rc;
             }
         }

@@ -28,11 +28,18 @@
 //                                  makes them free, and another follows
 //   bool outside(t)                (kSplit) nothing of the result is in a
 //                                  sub-tile that starts there
+//   const E* b_turned(t, &steps, &cols)  (kTurned, nt_ordered alone) B lies the
+//                                  other way, k by k, in rows ldb apart: its
+//                                  first row from the tile's first column on,
+//                                  how many rows exist and how many columns
+//                                  (a multiple of 8) from there
 // and the fields K (elements, a multiple of 8), lda (A's row pitch in
 // elements; pitches are multiples of 8 and below 2^21), tiles.  Every row
 // starts on 16 bytes.
 #ifndef DENSE_FP16_GEMM_NT_CORE_H
 #define DENSE_FP16_GEMM_NT_CORE_H
+
+#include <type_traits>
 
 #include "cdna4.h"
 
@@ -87,12 +94,23 @@ struct Int {
     static constexpr int value = V;
 };
 
+// Whether OP has B k by k.
+template <class OP, class = void>
+struct Turned : std::false_type {};
+template <class OP>
+struct Turned<OP, std::enable_if_t<OP::kTurned>> : std::true_type {};
+
+// LDS of such a B: a step's 64 rows of 128 columns, 16 chunks of 16 bytes.  A
+// turning read takes 32 bytes of four rows in each 16 lanes, whose places differ
+// in four rows' chunks and every other eight rows': 256 bytes apart, on all banks.
+__device__ __forceinline__ int turned_swizzle(int k, int chunk) { return chunk ^ ((k & 3) << 1) ^ (((k >> 3) & 1) << 3); }
+
 // The loads of one wave: load l of an operand fills rows 8 l .. 8 l + 7 of
 // the wave's quarter of its tile; lane -> row lane / 8, position lane % 8,
 // which the swizzle fills with chunk pos ^ ((row / 2) % 8).  (A quarter starts
 // at a multiple of 16 rows, so the row's place within it decides.)  B's
 // quarter is two operands of BN / 8 rows, which the gated layer needs.
-template <class T>
+template <class T, bool TURNED = false>
 struct Loader {
     __amdgpu_buffer_rsrc_t ra, rb0, rb1;
     uint32_t va[T::A_LOADS], vb[T::B_LOADS];
@@ -214,6 +232,60 @@ __global__ void __launch_bounds__(T::THREADS, T::OCC) nt_tile(const OP op)
     op.template epilogue<T>(t, acc, lane, wave, smem, smem + 32768);
 }
 
+// The same with B k by k: a wave's quarter of B is 16 rows, four to a load, lane ->
+// row lane / 16, position lane % 16.  A step's rows are a buffer of their own, as
+// all of them may span more than its 32 bits.
+template <class T>
+struct Loader<T, true> {
+    __amdgpu_buffer_rsrc_t ra;
+    const typename T::E* b;
+    uint32_t va[T::A_LOADS], vb[T::B_LOADS], pitch_b;
+    int c01[2], wave, steps, cols;
+    // B's rows of step ks
+    __device__ __forceinline__ __amdgpu_buffer_rsrc_t rows(int ks) const
+    {
+        const int left = min(steps - ks * T::BK, T::BK);
+        return make_rsrc((const unsigned char*)b + (int64_t)ks * T::BK * pitch_b,
+                         left > 0 ? (uint32_t)(left - 1) * pitch_b + (uint32_t)cols * 2u : 0u);
+    }
+    template <class OP>
+    __device__ __forceinline__ Loader(const OP& op, const Tile& t, int lane, int w) : wave(w)
+    {
+        static_assert(T::BN == 128 && T::B_LOADS == 4, "four rows of B to a load");
+        const uint32_t pitch_a = (uint32_t)op.lda * 2u;
+        int na = 0;
+        const void* pa = op.a_rows(t, w * (T::BM / 4), na);
+        ra = make_rsrc(pa, (uint32_t)min(na, T::BM / 4) * pitch_a);
+        b = op.b_turned(t, steps, cols);
+        pitch_b = (uint32_t)op.ldb * 2u;
+        const int lr = lane >> 3, lp = lane & 7;
+        c01[0] = swizzle(lr, lp);
+        c01[1] = swizzle(8 + lr, lp);
+#pragma unroll
+        for (int l = 0; l < T::A_LOADS; ++l) va[l] = (uint32_t)(l * 8 + lr) * pitch_a + (uint32_t)c01[l & 1] * 16u;
+#pragma unroll
+        for (int l = 0; l < T::B_LOADS; ++l) {
+            const int k = w * 16 + l * 4 + (lane >> 4);
+            vb[l] = (uint32_t)k * pitch_b + (uint32_t)turned_swizzle(k, lane & 15) * 16u;
+        }
+    }
+    template <class Masked>
+    __device__ __forceinline__ void load(unsigned char* base, int l, int ks, int K, Masked) const
+    {
+        if (l < T::A_LOADS) {
+            uint32_t off = va[l < T::A_LOADS ? l : 0], soff = (uint32_t)ks * (T::BK * 2);
+            if constexpr (Masked::value) {
+                off = c01[l & 1] * 8 < K - ks * T::BK ? off + soff : kOob;
+                soff = 0;
+            }
+            load_lds(ra, (lds_void*)(base + (wave * T::A_LOADS + l) * 1024), off, soff);
+        } else {
+            const int lb = l < T::A_LOADS ? 0 : l - T::A_LOADS;
+            load_lds(rows(ks), (lds_void*)(base + T::A_BYTES + (wave * T::B_LOADS + lb) * 1024), vb[lb], 0);
+        }
+    }
+};
+
 // acc += b * a with the accumulator in AGPRs; the memory clobber keeps every
 // LDS and global access on its side, so the source order of a loop built from
 // these is its issue order.
@@ -252,7 +324,8 @@ template <class T, class OP>
 __global__ void __launch_bounds__(T::THREADS, 1) nt_ordered(const OP op, const Split split)
 {
     using x8 = typename T::x8;
-    constexpr int S = T::STAGES, G = T::FM * T::FN, R = T::FM + T::FN;
+    constexpr bool TURNED = Turned<OP>::value;
+    constexpr int S = T::STAGES, G = T::FM * T::FN, BR = TURNED ? 2 * T::FN : T::FN, R = T::FM + BR;
     static_assert(T::WAVES == 8, "two waves per SIMD, one of which loads");
     static_assert(T::RS * (R - 1) < G && T::LS * (T::LOADS - 1) + T::LS / 2 < G, "reads and loads fit in a sub-step");
     __shared__ __attribute__((aligned(1024))) unsigned char smem[T::LDS_BYTES];
@@ -272,12 +345,21 @@ __global__ void __launch_bounds__(T::THREADS, 1) nt_ordered(const OP op, const S
     }
     Tile t;
     op.template tile<T::BM, T::BN>(id, t);
-    const Loader<T> loader(op, t, lane, wave & 3);
+    const Loader<T, TURNED> loader(op, t, lane, wave & 3);
 
     const int fr = lane & 15, fh = lane >> 4;
     const int pos[2] = {swizzle(fr, fh) * 16, swizzle(fr, 4 + fh) * 16};
     const int arow = (wm * T::WTM + fr) * T::ROW_BYTES;
     const int brow = T::A_BYTES + (wn * T::WTN + fr) * T::ROW_BYTES;
+    // (turned: the lane reads columns 4 (l % 4) .. + 3 of row l / 4 of four, l of 16
+    // lanes, and gets column l of all four)
+    int bturn[T::FN];
+    if constexpr (TURNED)
+#pragma unroll
+        for (int j = 0; j < T::FN; ++j) {
+            const int k = fh * 8 + (fr >> 2), chunk = (wn * T::WTN + j * 16) / 8 + ((fr & 3) >> 1);
+            bturn[j] = T::A_BYTES + k * (T::BN * 2) + turned_swizzle(k, chunk) * 16 + (fr & 1) * 8;
+        }
 
     x8 fa[2][T::FM], fb[2][T::FN];
     f32x4 acc[T::FM][T::FN];
@@ -286,14 +368,24 @@ __global__ void __launch_bounds__(T::THREADS, 1) nt_ordered(const OP op, const S
 #pragma unroll
         for (int j = 0; j < T::FN; ++j) acc[i][j] = f32x4{0, 0, 0, 0};
 
+    typename Elem<typename T::E>::x4 half[2][TURNED ? T::FN : 1][2];
     // fragment read idx of set `set`, in the order the MFMAs need them
     auto read_one = [&](int set, const unsigned char* base, int idx) __attribute__((always_inline)) {
         if (idx == 0)
             fa[set][0] = *(const x8*)(base + arow + pos[set]);
-        else if (idx <= T::FN)
+        else if (TURNED && idx <= BR)
+            half[set][(idx - 1) / 2][(idx - 1) % 2] =
+                read_turned<typename T::E>(base + bturn[(idx - 1) / 2] + (set * 32 + (idx - 1) % 2 * 4) * (T::BN * 2));
+        else if (idx <= BR)
             fb[set][idx - 1] = *(const x8*)(base + brow + pos[set] + (idx - 1) * 16 * T::ROW_BYTES);
         else
-            fa[set][idx - T::FN] = *(const x8*)(base + arow + pos[set] + (idx - T::FN) * 16 * T::ROW_BYTES);
+            fa[set][idx - BR] = *(const x8*)(base + arow + pos[set] + (idx - BR) * 16 * T::ROW_BYTES);
+    };
+    auto fragment = [&](int set, int j) __attribute__((always_inline)) {
+        if constexpr (TURNED)
+            return (x8)__builtin_shufflevector(half[set][j][0], half[set][j][1], 0, 1, 2, 3, 4, 5, 6, 7);
+        else
+            return fb[set][j];
     };
     // MFMAs along the rows of blocks and back, so that neighbours share a fragment
     auto substep = [&](int set, const unsigned char* reads, auto ld, unsigned char* into, int lstep, auto masked)
@@ -301,7 +393,7 @@ __global__ void __launch_bounds__(T::THREADS, 1) nt_ordered(const OP op, const S
 #pragma unroll
         for (int n = 0; n < G; ++n) {
             const int i = n / T::FN, j = (i & 1) ? T::FN - 1 - n % T::FN : n % T::FN;
-            mfma_agpr(acc[i][j], fb[set][j], fa[set][i]);
+            mfma_agpr(acc[i][j], fragment(set, j), fa[set][i]);
             if (n % T::RS == 0 && n / T::RS < R) read_one(1 - set, reads, n / T::RS);
             if constexpr (decltype(ld)::value)
                 if (n % T::LS == T::LS / 2 && n / T::LS < T::LOADS) loader.load(into, n / T::LS, lstep, K, masked);

@@ -89,7 +89,7 @@ Choice choose(int64_t K, bool partial, Count count)
     const int cus = num_cus();
     Choice best;
     for (int i = 0; i < kNumKinds; ++i) {
-        if (i == 0 && (!OP::kPersist || K <= 128)) continue;
+        if ((i == 0 && (!OP::kPersist || K <= 128)) || (i == 3 && Turned<OP>::value)) continue;
         const int64_t n = count(kKinds[i]);
         if (!abi::good_grid(n, i == 1 || i == 2 ? 512 : 256)) continue;
         const double us = model_us(kKinds[i], n, K, cus);
@@ -125,8 +125,9 @@ int launch(OP op, int64_t K, float* partial, Count count, Prepare prepare, hipSt
                                                                  stream);
     // (four stages, two workgroups to a CU: 30.8 us with three for one row and
     // 4096 x 8192 twice, 29.7 with four, 29.5 with five, which take all of LDS)
-    if (best.kind == 3)
-        hipLaunchKernelGGL((nt_tile<Shape<E, 64, 64, 2, 2, 4, 2, 4>, OP>), dim3((unsigned)tiles), dim3(256), 0, stream, op);
+    if constexpr (!Turned<OP>::value)
+        if (best.kind == 3)
+            hipLaunchKernelGGL((nt_tile<Shape<E, 64, 64, 2, 2, 4, 2, 4>, OP>), dim3((unsigned)tiles), dim3(256), 0, stream, op);
     return (int)hipGetLastError();
 }
 

@@ -112,6 +112,38 @@ def test_pieces_of_the_vocabulary(shape, t):
     check(x, w, target, dloss, loss, got)
 
 
+# long sums over the vocabulary, which dx's product takes from w as it lies: in place
+# and copied, over vocabularies and to widths that no step, tile or part divides,
+# rows that span more than 32 bits, and two pieces of the vocabulary
+@pytest.mark.parametrize("t", ["fp16", "bf16"])
+@pytest.mark.parametrize("shape", [(17, 4096, 20001), (200, 1000, 9001), (129, 520, 20007), (600, 1160, 30002), (200, 333, 30001)], ids=str)
+def test_w_as_it_lies(shape, t):
+    x, w, target, dloss = inputs(*shape, plain.TYPES[t], seed=sum(shape))
+    loss, got = step(x, w, target, dloss)
+    check(x, w, target, dloss, loss, got)
+    # (between its rows and behind them there may be anything)
+    vw = framed(w, cols=24, offset=8)[0]
+    l2, (dx, dw) = step(x, vw, target, dloss)
+    assert torch.equal(l2, loss) and torch.equal(dx, got[0]) and torch.equal(dw, got[1])
+
+
+def test_w_far_apart():
+    T, D, V = 200, 1000, 20000
+    x, w, target, dloss = inputs(T, D, V, torch.float16, seed=20)
+    far = torch.empty(V, 1 << 17, dtype=torch.float16, device=DEV)[:, :D]
+    far.copy_(w)
+    loss, got = step(x, w, target, dloss)
+    l2, (dx, dw) = step(x, far, target, dloss)
+    assert torch.equal(l2, loss) and torch.equal(dx, got[0]) and torch.equal(dw, got[1])
+
+
+@pytest.mark.parametrize("shape", [(40, 776, 2 ** 20 + 5003)], ids=str)
+def test_w_as_it_lies_in_pieces(shape):
+    x, w, target, dloss = inputs(*shape, torch.bfloat16, seed=21)
+    loss, got = step(x, w, target, dloss)
+    check(x, w, target, dloss, loss, got)
+
+
 @pytest.mark.parametrize("shape", [(1, 24, 2 ** 20 + 70), (3, 8, 2 ** 21 + 5)], ids=str)
 def test_vocabularies_past_a_pitch(shape):
     x, w, target, dloss = inputs(*shape, torch.bfloat16, seed=6, ignored=0.0)

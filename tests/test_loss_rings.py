@@ -4,7 +4,8 @@ Its products run on the rings of ``test_operator_rings``; what is its own:
 * the persistent kernel's epilogue with no results through LDS (the loss, sums
   kept in 32 bits), and with four rounds of two images (dl both ways round);
 * in the built code the persistent loops issue the model's schedule, and the
-  ordered kernels wait as theirs.
+  ordered kernels wait as theirs, those that read W as it lies too;
+* W's rows as they lie in LDS.
 """
 from __future__ import annotations
 
@@ -50,7 +51,11 @@ def test_persistent_loops_issue_the_model_schedule(code, monkeypatch, tmp_path):
 
 def test_ordered_kernels_wait_as_the_model(code):
     found = {s: lines for s, lines in code[1].items() if "nt_ordered" in s}
-    assert len(found) == 36
+    # each as two tiles in two types: the loss, dl, the sums and dX in four forms, both
+    # on a transposed W and on W as it lies, dW in two
+    assert len(found) == 56
+    turned = [s for s, lines in found.items() if any(l.startswith("ds_read_b64_tr_b16") for l in lines)]
+    assert len(turned) == 20 and all("AddOp" in s or "DxOp" in s for s in turned)
     for s, lines in found.items():
         size = re.search(r"Li(\d+)ELi(\d+)E", s)
         loads = rings.ORDERED["ILi%sELi%sE" % size.groups()]
@@ -78,3 +83,32 @@ def test_accumulators_are_read_after_their_products(code):
                 checked += 1
                 last = None
     assert checked >= 18
+
+
+def turned_swizzle(k, chunk):
+    return chunk ^ ((k & 3) << 1) ^ (((k >> 3) & 1) << 3)
+
+
+def test_rows_of_w_in_lds():
+    """Rows of 128 columns, 64 of them: each of the loads' 16-byte pieces has a place of its
+    own, a fragment's reads find their columns, and those of a wave, 512 bytes, fall
+    on all 64 banks evenly."""
+    places = {}
+    for wave in range(4):
+        for load in range(4):
+            for lane in range(64):
+                k = wave * 16 + load * 4 + lane // 16
+                places[(wave * 4 + load) * 1024 + lane * 16] = (k, turned_swizzle(k, lane % 16))
+    assert sorted(places) == list(range(0, 64 * 256, 16)) and len(set(places.values())) == 64 * 16
+    for first in range(0, 128, 16):  # of a block's 16 columns
+        for step in (0, 32):
+            for half in (0, 4):
+                banks = [0] * 64
+                for lane in range(64):
+                    r, k = lane % 16, lane // 16 * 8 + lane % 16 // 4
+                    at = k * 256 + turned_swizzle(k, first // 8 + r % 4 // 2) * 16 + r % 2 * 8 + (step + half) * 256
+                    k += step + half
+                    assert places[at // 16 * 16] == (k, (first + r % 4 * 4) // 8) and at % 16 == (first + r % 4 * 4) % 8 * 2
+                    for b in range(2):
+                        banks[at // 4 % 64 + b] += 1
+                assert banks == [2] * 64
