@@ -6,6 +6,7 @@
 #include "layer_norm.h"
 
 #include <algorithm>
+#include <type_traits>
 
 #include "abi.h"
 #include "cus.h"
@@ -54,24 +55,38 @@ __device__ __forceinline__ float squares(const Vec<E, N>& v, float mean, int lef
     return sum;
 }
 
-// A chunk of a row, loaded and used.  16-bit rows of one chunk to a lane load their
-// ends early; with more the registers that takes cost more than it gives (backward,
-// 20000 x 300 17.2 us and early 14.1, 150000 x 33 14.2 and 12.3; 8192 x 4096 41 and 52).
-template <class E, int C>
-constexpr bool kEarly = C == 1 && sizeof(E) == 2;
-template <class E, int C>
-__device__ __forceinline__ Vec<E, kChunk<E>> first_load(const E* p, int left, int cols)
-{
-    if constexpr (kEarly<E, C>) return load_early<E, kChunk<E>>(p, left, cols);
-    return load<E, kChunk<E>>(p, left);
-}
-template <class E, int C>
-__device__ __forceinline__ Vec<E, kChunk<E>> first_use(const Vec<E, kChunk<E>>& v, int left, int cols)
-{
-    if constexpr (kEarly<E, C>)
-        if (left > 0) return settled<E, kChunk<E>>(v, left, cols);
-    return v;
-}
+// Where a lane's chunk `n` of a row lies.  The last one, where a row is no whole
+// number of chunks, moves back to end with the row: it holds some elements that
+// the chunk before holds too, which count once in the row's sums; whatever is
+// computed of each is computed twice alike and stored twice.  (Loaded and stored one
+// by one the row's last elements make their wave wait, and all others for it: steps
+// of 1000 x 2731 in binary16 take 30 us and so 26, 20000 x 3003 212 and 161, 20000 x
+// 301 in binary32 41 and 33.)  A row shorter than a chunk is loaded one by one: G of
+// 8 and C of 1 alone (SHORT).  WHOLE: rows are whole chunks, and nothing else is
+// there (steps of 2048 x 8192 in bfloat16 50.3 us and 48.5).
+// (`twice` is new to the compiler each time: it would keep the comparisons through
+// the rows, in more scalar registers than there are.)
+template <int N, int G, int C, bool WHOLE>
+struct Place {
+    static constexpr bool SHORT = !WHOLE && G == 8 && C == 1;
+    int c, twice, cols;  // the first element, how many the chunk before has too
+    bool ends;           // a row may end here: in the second half of a lane's chunks
+    __device__ __forceinline__ Place(int i, int lane, int cols_)
+        : c((i * G + lane) * N), twice(0), cols(cols_), ends(!WHOLE && 2 * i + 1 >= C)
+    {
+        if (ends) {
+            if (c < cols && c + N > cols && (!SHORT || cols >= N)) {
+                twice = c + N - cols;
+                c = cols - N;
+            }
+            asm volatile("" : "+v"(twice));
+        }
+    }
+    __device__ __forceinline__ bool there() const { return c < cols; }
+    __device__ __forceinline__ int left() const { return SHORT ? cols - c : N; }
+    // whether element e counts in the row's sums
+    __device__ __forceinline__ bool counts(int e) const { return !ends || (e >= twice && (!SHORT || e < cols - c)); }
+};
 
 // weight and bias of a chunk.
 template <class P, int N>
@@ -85,19 +100,20 @@ __device__ __forceinline__ void load_params(const P* weight, const P* bias, int 
 
 // Rows of up to G * C chunks, G lanes to a row; G below 64: several rows to a wave.
 // Lanes with few chunks keep weight and bias for all their rows.
-template <class E, class P, int G, int C>
+template <class E, class P, int G, int C, bool WHOLE>
 __global__ void __launch_bounds__(G > 256 ? G : 256) norm_rows(const Forward<E, P> f)
 {
     constexpr int N = kChunk<E>, R = (G > 256 ? G : 256) / G;
     constexpr bool KEEP = C <= 2;
+    using At = Place<N, G, C, WHOLE>;
     __shared__ Parts<G, 1> parts;
     const int lane = threadIdx.x % G, mine = threadIdx.x / G, cols = f.cols;
     Vec<P, N> kw[KEEP ? C : 1], kb[KEEP ? C : 1];
     if constexpr (KEEP)
 #pragma unroll
         for (int i = 0; i < C; ++i) {
-            const int c = (i * G + lane) * N;
-            load_params<P, N>(f.weight, f.bias, c, cols - c, kw[i], kb[i]);
+            const At at(i, lane, cols);
+            load_params<P, N>(f.weight, f.bias, at.c, at.there() ? at.left() : 0, kw[i], kb[i]);
         }
     for (int64_t first = (int64_t)blockIdx.x * R; first < f.rows; first += (int64_t)gridDim.x * R) {
         const int64_t row = first + mine;
@@ -105,22 +121,30 @@ __global__ void __launch_bounds__(G > 256 ? G : 256) norm_rows(const Forward<E, 
         Vec<E, N> v[C];
 #pragma unroll
         for (int i = 0; i < C; ++i) {
-            const int c = (i * G + lane) * N;
+            const At at(i, lane, cols);
             v[i] = Vec<E, N>{};
-            if (there && c < cols) v[i] = first_load<E, C>(f.X + row * f.ldx + c, cols - c, cols);
+            if (there && at.there()) v[i] = load<E, N>(f.X + row * f.ldx + at.c, at.left());
         }
-#pragma unroll
-        for (int i = 0; i < C; ++i) v[i] = first_use<E, C>(v[i], cols - (i * G + lane) * N, cols);
         float s[1] = {0.0f};
 #pragma unroll
-        for (int i = 0; i < C; ++i)
+        for (int i = 0; i < C; ++i) {
+            const At at(i, lane, cols);
 #pragma unroll
-            for (int e = 0; e < N; ++e) s[0] += (float)v[i][e];
+            for (int e = 0; e < N; ++e) s[0] += at.counts(e) ? (float)v[i][e] : 0.0f;
+        }
         sums<G, 1>(s, parts, 0);
         const float mean = s[0] / (float)cols;
         s[0] = 0.0f;
 #pragma unroll
-        for (int i = 0; i < C; ++i) s[0] = squares<E, N>(v[i], mean, cols - (i * G + lane) * N, s[0]);
+        for (int i = 0; i < C; ++i) {
+            const At at(i, lane, cols);
+            if (!at.there()) continue;
+#pragma unroll
+            for (int e = 0; e < N; ++e) {
+                const float d = at.counts(e) ? (float)v[i][e] - mean : 0.0f;
+                s[0] = __builtin_fmaf(d, d, s[0]);
+            }
+        }
         sums<G, 1>(s, parts, 1);
         const float r = deviation(s[0], cols, f.eps);
         if (there && f.saved && lane == 0) {
@@ -130,18 +154,18 @@ __global__ void __launch_bounds__(G > 256 ? G : 256) norm_rows(const Forward<E, 
         E* y = f.Y + row * f.ldy;
 #pragma unroll
         for (int i = 0; i < C; ++i) {
-            const int c = (i * G + lane) * N;
+            const At at(i, lane, cols);
             Vec<P, N> w, b;
             if constexpr (KEEP) {
                 w = kw[i];
                 b = kb[i];
             } else {
-                load_params<P, N>(f.weight, f.bias, c, cols - c, w, b);
+                load_params<P, N>(f.weight, f.bias, at.c, at.there() ? at.left() : 0, w, b);
             }
             Vec<E, N> o;
 #pragma unroll
             for (int e = 0; e < N; ++e) o[e] = (E)__builtin_fmaf(((float)v[i][e] - mean) * r, (float)w[e], (float)b[e]);
-            if (there && c < cols) store<E, N>(y + c, cols - c, o);
+            if (there && at.there()) store<E, N>(y + at.c, at.left(), o);
         }
     }
 }
@@ -204,11 +228,12 @@ struct Backward {
 
 // Rows of up to G * C chunks: dX, and each workgroup's sums over its rows.  The
 // next row's loads are in flight while a row is worked on, where registers allow.
-template <class E, class P, int G, int C>
+template <class E, class P, int G, int C, bool WHOLE>
 __global__ void __launch_bounds__(G > 256 ? G : 256) norm_back_rows(const Backward<E, P> f)
 {
     constexpr int N = kChunk<E>, T = G > 256 ? G : 256, R = T / G;
     constexpr bool AHEAD = C * N < 32;
+    using At = Place<N, G, C, WHOLE>;
     __shared__ Parts<G, 2> parts;
     __shared__ float meet[R > 1 ? R * G * C * N : 1];
     const int lane = threadIdx.x % G, mine = threadIdx.x / G, cols = f.cols;
@@ -216,9 +241,9 @@ __global__ void __launch_bounds__(G > 256 ? G : 256) norm_back_rows(const Backwa
     Vec<P, N> w[C];
 #pragma unroll
     for (int i = 0; i < C; ++i) {
-        const int c = (i * G + lane) * N;
+        const At at(i, lane, cols);
         w[i] = (P)1.0f;
-        if (c < cols && f.weight) w[i] = load<P, N>(f.weight + c, cols - c);
+        if (at.there() && f.weight) w[i] = load<P, N>(f.weight + at.c, at.left());
     }
     float aw[C][N], ab[C][N];
 #pragma unroll
@@ -237,12 +262,12 @@ __global__ void __launch_bounds__(G > 256 ? G : 256) norm_back_rows(const Backwa
         v.r = there ? f.saved[2 * row + 1] : 0.0f;
 #pragma unroll
         for (int i = 0; i < C; ++i) {
-            const int c = (i * G + lane) * N;
+            const At at(i, lane, cols);
             v.x[i] = Vec<E, N>{};
             v.d[i] = Vec<E, N>{};
-            if (there && c < cols) {
-                v.x[i] = first_load<E, C>(f.X + row * f.ldx + c, cols - c, cols);
-                v.d[i] = first_load<E, C>(f.dY + row * f.lddy + c, cols - c, cols);
+            if (there && at.there()) {
+                v.x[i] = load<E, N>(f.X + row * f.ldx + at.c, at.left());
+                v.d[i] = load<E, N>(f.dY + row * f.lddy + at.c, at.left());
             }
         }
         return v;
@@ -260,54 +285,57 @@ __global__ void __launch_bounds__(G > 256 ? G : 256) norm_back_rows(const Backwa
         } else {
             v = fetch(row);
         }
-#pragma unroll
-        for (int i = 0; i < C; ++i) {
-            v.x[i] = first_use<E, C>(v.x[i], cols - (i * G + lane) * N, cols);
-            v.d[i] = first_use<E, C>(v.d[i], cols - (i * G + lane) * N, cols);
-        }
         float s[2] = {0.0f, 0.0f};
 #pragma unroll
-        for (int i = 0; i < C; ++i)
+        for (int i = 0; i < C; ++i) {
+            const At at(i, lane, cols);
 #pragma unroll
             for (int e = 0; e < N; ++e) {
-                const float h = ((float)v.x[i][e] - v.mean) * v.r, dy = (float)v.d[i][e], g = dy * (float)w[i][e];
+                const float h = ((float)v.x[i][e] - v.mean) * v.r, dy = (float)v.d[i][e];
+                const float g = at.counts(e) ? dy * (float)w[i][e] : 0.0f;
                 s[0] += g;
                 s[1] = __builtin_fmaf(g, h, s[1]);
                 aw[i][e] = __builtin_fmaf(dy, h, aw[i][e]);
                 ab[i][e] += dy;
             }
+        }
         sums<G, 2>(s, parts, turn++);
         const float mg = s[0] / (float)cols, mgh = s[1] / (float)cols;
         E* to = f.dX + row * f.lddx;
 #pragma unroll
         for (int i = 0; i < C; ++i) {
-            const int c = (i * G + lane) * N;
+            const At at(i, lane, cols);
             Vec<E, N> o;
 #pragma unroll
             for (int e = 0; e < N; ++e) {
                 const float h = ((float)v.x[i][e] - v.mean) * v.r, g = (float)v.d[i][e] * (float)w[i][e];
                 o[e] = (E)(v.r * (g - mg - h * mgh));
             }
-            if (row < f.rows && c < cols) store<E, N>(to + c, cols - c, o);
+            if (row < f.rows && at.there()) store<E, N>(to + at.c, at.left(), o);
         }
     }
     float* const out = f.partial ? f.partial + (int64_t)blockIdx.x * 2 * cols : nullptr;
-    auto put = [&](int c, int k, float sum) __attribute__((always_inline)) {
-        if (out) out[k * cols + c] = sum;
-        P* const to = k ? f.dbias : f.dweight;
-        if (to) to[c] = (P)sum;
-    };
     if (!out && !f.dweight && !f.dbias) return;
     if constexpr (R == 1) {
+        // (a lane's chunks whole: one element at a time, which lie apart from lane to
+        // lane, 1000 x 2728 takes 13.9 us, and 11.5)
 #pragma unroll
         for (int i = 0; i < C; ++i) {
-            const int c = (i * G + lane) * N;
+            const At at(i, lane, cols);
+            if (!at.there()) continue;
 #pragma unroll
-            for (int e = 0; e < N; ++e)
-                if (c + e < cols) {
-                    put(c + e, 0, aw[i][e]);
-                    put(c + e, 1, ab[i][e]);
+            for (int k = 0; k < 2; ++k) {
+                Vec<float, N> sum;
+                Vec<P, N> rounded;
+#pragma unroll
+                for (int e = 0; e < N; ++e) {
+                    sum[e] = k ? ab[i][e] : aw[i][e];
+                    rounded[e] = (P)sum[e];
                 }
+                if (out) store<float, N>(out + k * cols + at.c, at.left(), sum);
+                P* const to = k ? f.dbias : f.dweight;
+                if (to) store<P, N>(to + at.c, at.left(), rounded);
+            }
         }
     } else {
         // the groups' sums meet in LDS, first those of dY h
@@ -316,15 +344,19 @@ __global__ void __launch_bounds__(G > 256 ? G : 256) norm_back_rows(const Backwa
         for (int k = 0; k < 2; ++k) {
             __syncthreads();
 #pragma unroll
-            for (int i = 0; i < C; ++i)
+            for (int i = 0; i < C; ++i) {
+                const At at(i, lane, cols);
 #pragma unroll
-                for (int e = 0; e < N; ++e) meet[mine * W + (i * G + lane) * N + e] = k ? ab[i][e] : aw[i][e];
+                for (int e = 0; e < N; ++e) meet[mine * W + at.c + e] = k ? ab[i][e] : aw[i][e];
+            }
             __syncthreads();
             for (int c = threadIdx.x; c < cols; c += T) {
                 float sum = 0.0f;
 #pragma unroll
                 for (int g = 0; g < R; ++g) sum += meet[g * W + c];
-                put(c, k, sum);
+                if (out) out[k * cols + c] = sum;
+                P* const to = k ? f.dbias : f.dweight;
+                if (to) to[c] = (P)sum;
             }
         }
     }
@@ -393,12 +425,14 @@ __global__ void __launch_bounds__(kTileThreads) norm_back_tiles(const Backward<E
     }
     if (!f.partial) return;
     float* const out = f.partial + (int64_t)blockIdx.x * 2 * cols + c;
+    Vec<float, N> sw, sb;
 #pragma unroll
-    for (int e = 0; e < N; ++e)
-        if (e < left) {
-            out[e] = aw[e];
-            out[cols + e] = ab[e];
-        }
+    for (int e = 0; e < N; ++e) {
+        sw[e] = aw[e];
+        sb[e] = ab[e];
+    }
+    store<float, N>(out, left, sw);
+    store<float, N>(out + cols, left, sb);
 }
 
 // Adds the workgroups' sums.  blockIdx.y: dweight, dbias.
@@ -436,10 +470,11 @@ int64_t back_groups(int64_t rows, int64_t cols, int32_t type)
     const Way w = way_of(chunks_of(cols, type));
     constexpr int cus = cus::kCus;
     if (w.g == 0) return sharers(rows, 1, 64);
-    // Each workgroup's sums cross memory twice, and fewer workgroups hide less: with 1, 2
-    // and 3 for each CU 8192 x 4096 in bfloat16 takes 49, 42 and 46 us, 2048 x 8192 (whose
-    // lanes hold more) 32, 32 and 48, 1000 x 2731 16, 18 and 20 (four rows to a
-    // workgroup, or two), 20000 x 300 34, 21 and 17.
+    // Each workgroup's sums cross memory twice, and fewer workgroups hide less: steps with
+    // 1, 2 and 3 for each CU take, of 500 x 16384 in bfloat16 (whose lanes hold more) 38, 50
+    // and 50 us, of 1000 x 2048 (four rows to a workgroup, or two) 22.5, 24.5 and 28.4, and
+    // with 2, 3 and 4 of 8192 x 4096 70, 73 and 81; the backward pass alone of 20000 x 300
+    // with 1, 2 and 3 34, 21 and 17.
     // Few enough rows are one workgroup's, which needs no second launch (4 x 1024: 4.4
     // us, and 4.4 and 3.5 in two; four turns of rows take longer than that).
     const int64_t per = w.g > 256 ? 1 : 256 / w.g;
@@ -458,16 +493,20 @@ int forward(const Forward<E, P>& f, hipStream_t stream)
         hipLaunchKernelGGL(kernel, dim3((unsigned)n), dim3(threads), 0, stream, f);
         return (int)hipGetLastError();
     };
-    if (chunks <= 8) return with(norm_rows<E, P, 8, 1>, 256, 32);
-    if (chunks <= 16) return with(norm_rows<E, P, 16, 1>, 256, 16);
-    if (chunks <= 32) return with(norm_rows<E, P, 32, 1>, 256, 8);
-    if (chunks <= 64) return with(norm_rows<E, P, 64, 1>, 256, 4);
-    if (chunks <= 128) return with(norm_rows<E, P, 64, 2>, 256, 4);
-    if (chunks <= 256) return with(norm_rows<E, P, 256, 1>, 256, 1);
-    if (chunks <= 512) return with(norm_rows<E, P, 256, 2>, 256, 1);
-    if (chunks <= 1024) return with(norm_rows<E, P, 256, 4>, 256, 1);
-    if (chunks <= 2048) return with(norm_rows<E, P, 512, 4>, 512, 1);
-    if (chunks <= 4096) return with(norm_rows<E, P, 1024, 4>, 1024, 1);
+    auto rows = [&](auto whole) {
+        constexpr bool W = decltype(whole)::value;
+        if (chunks <= 8) return with(norm_rows<E, P, 8, 1, W>, 256, 32);
+        if (chunks <= 16) return with(norm_rows<E, P, 16, 1, W>, 256, 16);
+        if (chunks <= 32) return with(norm_rows<E, P, 32, 1, W>, 256, 8);
+        if (chunks <= 64) return with(norm_rows<E, P, 64, 1, W>, 256, 4);
+        if (chunks <= 128) return with(norm_rows<E, P, 64, 2, W>, 256, 4);
+        if (chunks <= 256) return with(norm_rows<E, P, 256, 1, W>, 256, 1);
+        if (chunks <= 512) return with(norm_rows<E, P, 256, 2, W>, 256, 1);
+        if (chunks <= 1024) return with(norm_rows<E, P, 256, 4, W>, 256, 1);
+        if (chunks <= 2048) return with(norm_rows<E, P, 512, 4, W>, 512, 1);
+        return with(norm_rows<E, P, 1024, 4, W>, 1024, 1);
+    };
+    if (chunks <= 4096) return f.cols % kChunk<E> ? rows(std::false_type{}) : rows(std::true_type{});
     return with(norm_wide<E, P>, kWide, 1);
 }
 
@@ -489,15 +528,18 @@ int backward(Backward<E, P> f, P* dweight, P* dbias, float* partial, float* mean
             hipLaunchKernelGGL(kernel, dim3((unsigned)groups), dim3(std::max(256, w.g)), 0, stream, f);
             return (int)hipGetLastError();
         };
-        if (w.g == 8) rc = with(norm_back_rows<E, P, 8, 1>);
-        else if (w.g == 16) rc = with(norm_back_rows<E, P, 16, 1>);
-        else if (w.g == 32) rc = with(norm_back_rows<E, P, 32, 1>);
-        else if (w.g == 64 && w.c == 1) rc = with(norm_back_rows<E, P, 64, 1>);
-        else if (w.g == 64) rc = with(norm_back_rows<E, P, 64, 2>);
-        else if (w.g == 256 && w.c == 1) rc = with(norm_back_rows<E, P, 256, 1>);
-        else if (w.g == 256 && w.c == 2) rc = with(norm_back_rows<E, P, 256, 2>);
-        else if (w.g == 256 && w.c == 4) rc = with(norm_back_rows<E, P, 256, 4>);
-        else if (w.g == 512) rc = with(norm_back_rows<E, P, 512, 4>);
+        auto rows = [&](auto whole) {
+            constexpr bool W = decltype(whole)::value;
+            if (w.g == 8) return with(norm_back_rows<E, P, 8, 1, W>);
+            if (w.g == 16) return with(norm_back_rows<E, P, 16, 1, W>);
+            if (w.g == 32) return with(norm_back_rows<E, P, 32, 1, W>);
+            if (w.g == 64) return w.c == 1 ? with(norm_back_rows<E, P, 64, 1, W>) : with(norm_back_rows<E, P, 64, 2, W>);
+            if (w.g == 512) return with(norm_back_rows<E, P, 512, 4, W>);
+            if (w.c == 1) return with(norm_back_rows<E, P, 256, 1, W>);
+            return w.c == 2 ? with(norm_back_rows<E, P, 256, 2, W>) : with(norm_back_rows<E, P, 256, 4, W>);
+        };
+        if (w.g)
+            rc = f.cols % kChunk<E> ? rows(std::false_type{}) : rows(std::true_type{});
         else {
             hipLaunchKernelGGL((norm_back_means<E, P>), dim3((unsigned)std::min<int64_t>(f.rows, 2 * cus::kCus)), dim3(kWide), 0,
                                stream, f, means);

@@ -41,24 +41,6 @@ __device__ __forceinline__ Vec<T, N> load(const T* p, int left)
     return v;
 }
 
-// The same in two steps, so that loads may be in flight meanwhile: a chunk at a
-// row's end is loaded whole from where it ends (`row`: the elements from the row's
-// start to its end), and what it does not own shifted out when it is used.
-template <class T, int N>
-__device__ __forceinline__ Vec<T, N> load_early(const T* p, int left, int row)
-{
-    typedef Vec<T, N> Any __attribute__((aligned(sizeof(T))));
-    if (row >= N) return *(const Any*)(p + min(left - N, 0));
-    return load<T, N>(p, left);
-}
-template <class T, int N>
-__device__ __forceinline__ Vec<T, N> settled(const Vec<T, N>& v, int left, int row)
-{
-    static_assert(sizeof(v) == 16, "a chunk");
-    if (left >= N || row < N) return v;
-    return __builtin_bit_cast(Vec<T, N>, __builtin_bit_cast(unsigned __int128, v) >> ((N - left) * (int)sizeof(T) * 8));
-}
-
 template <class T, int N>
 __device__ __forceinline__ void store(T* p, int left, const Vec<T, N>& v)
 {
