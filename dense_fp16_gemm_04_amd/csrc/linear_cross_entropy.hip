@@ -356,7 +356,12 @@ struct LayOut {
         for (int it = 0; it < 4; ++it) {
             const int r = it * 16 + y;
             Four<E> v = {};
-            if (r0 + r < rows && c < cols) v = ::rows::load<E, 4>(src + (r0 + r) * ld + c, cols - c);
+            if (r0 + r < rows && c < cols) {
+                // (a row's end is loaded from four elements before it, and shifted)
+                const int past = cols < 4 ? 0 : max(c + 4 - cols, 0);
+                v = ::rows::load<E, 4>(src + (r0 + r) * ld + c - past, cols < 4 ? cols - c : 4);
+                v = __builtin_bit_cast(Four<E>, __builtin_bit_cast(uint64_t, v) >> past * 16);
+            }
             if (copy && r0 + r < rows) *(Four<E>*)(copy + (r0 + r) * ld_copy + c) = v;
             if (target && r0 + r < rows && target[(r0 + r) * target_stride] == ignore) v = Four<E>{};
             *(Four<E>*)(tile + r * kPitch + x * 4) = v;
@@ -672,8 +677,9 @@ struct DwOp : StoreOp<E, false, true> {
 
 bool vec8(const void* p, int64_t ld) { return (uintptr_t)p % 16 == 0 && ld % 8 == 0; }
 
-// Rows of what is copied, transposed or kept start on 128 bytes, and are written
-// in whole cache lines.
+// Rows of what is copied, transposed or kept start on 128 bytes, and are written and
+// read in whole cache lines.  (Copies of rows that start on 16 bytes: steps of 4000 x
+// 4001 x 32001 3520 us, and 3217; 181 x 333 x 109366 332 and 322.)
 constexpr int64_t kLine = 64;
 
 // A product over n columns of the vocabulary (by `other` rows, sums of K) may be
@@ -714,6 +720,16 @@ constexpr int64_t kSmall = (int64_t)1 << 26;
 int64_t part_width(int64_t T, int64_t V) { return T <= kSmall / V ? 32 : 64; }
 
 bool in_place(const void* p, int64_t D, int64_t ld) { return D % 8 == 0 && vec8(p, ld); }
+// X, which every tile of the vocabulary reads anew, is copied to whole lines too where
+// the products are large.  (Steps of 2000 x 1496 x 32001 848 us in place and 827,
+// 8192 x 1000 x 50000 3520 and 3405; forward alone 6000 x 2632 x 4000 148 and 138, but
+// 1000 x 520 x 60001 97 and 102.  W's copy costs more than it gives: 2000 x 1496 x 32001
+// forward 185 and 220.)
+bool in_place(const void* X, int64_t T, int64_t D, int64_t V, int64_t ldx)
+{
+    const bool lines = (uintptr_t)X % 128 == 0 && ldx % kLine == 0;
+    return in_place(X, D, ldx) && (lines || (double)T * (double)D * (double)V < 6e10);
+}
 
 template <class E>
 struct ForwardSpace {
@@ -731,7 +747,7 @@ struct ForwardSpace {
         } else {
             const int64_t ld = abi::up(D, kLine), width = part_width(T, V);
             Mp = abi::up(T, 16);
-            if (!in_place(X, D, ldx)) x = c.take<E>(T * ld);
+            if (!in_place(X, T, D, V, ldx)) x = c.take<E>(T * ld);
             if (!in_place(W, D, ldw)) w = c.take<E>(V * ld);
             parts = c.take<f32x2>(((V + width - 1) / width + 1) * Mp);
             if (abi::up(D, 8) >= kSplitK) partial = c.take<float>(kSplitFloats);
@@ -853,7 +869,7 @@ struct BackwardSpace {
         Tp = abi::up(T, kLine);
         Vp = abi::up(piece, kLine);
         rows = abi::up(T, 256);
-        if (!in_place(X, D, ldx)) x = c.take<E>(T * ld);
+        if (!in_place(X, T, D, V, ldx)) x = c.take<E>(T * ld);
         if (!in_place(W, D, ldw)) w = c.take<E>(piece * ld);
         xt = c.take<E>(D * Tp);
         wt = c.take<E>(D * Vp);

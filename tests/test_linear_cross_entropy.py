@@ -127,6 +127,17 @@ def test_w_as_it_lies(shape, t):
     assert torch.equal(l2, loss) and torch.equal(dx, got[0]) and torch.equal(dw, got[1])
 
 
+def test_large_products():
+    """X is copied to whole lines, or lies in them: the same bits."""
+    x, w, target, dloss = inputs(4100, 1000, 16001, torch.bfloat16, seed=22)
+    loss, got = step(x, w, target, dloss)
+    check(x, w, target, dloss, loss, got)
+    lines = torch.full((4100, 1024), float("nan"), dtype=torch.bfloat16, device=DEV)[:, :1000]
+    lines.copy_(x)
+    l2, (dx, dw) = step(lines, w, target, dloss)
+    assert torch.equal(l2, loss) and torch.equal(dx, got[0]) and torch.equal(dw, got[1])
+
+
 def test_w_far_apart():
     T, D, V = 200, 1000, 20000
     x, w, target, dloss = inputs(T, D, V, torch.float16, seed=20)
