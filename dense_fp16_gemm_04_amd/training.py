@@ -216,8 +216,16 @@ def _check_loss(x, w, target):
     return device, T, D, V, ldx, ldw, _strided("target", target, torch.int64, device, T)
 
 
+def _ignored(index):
+    index = int(index)
+    if not -_WORDS // 2 <= index < _WORDS // 2:
+        raise ValueError("ignore_index must fit 64 bits, got %d" % index)
+    return index
+
+
 def _loss(x, w, target, ignore_index, out, train):
     device, T, D, V, ldx, ldw, stride = _check_loss(x, w, target)
+    ignored = _ignored(ignore_index)
     if out is None:
         out = x.new_empty(T, dtype=torch.float32)
     else:
@@ -229,7 +237,7 @@ def _loss(x, w, target, ignore_index, out, train):
         raise GemmError("linear_cross_entropy", 1)
     keep, workspace = _workspace(x, nbytes)
     _call("linear_cross_entropy", "linear_cross_entropy", device, px, pw, target.data_ptr(), out.data_ptr(),
-          saved.data_ptr() if train else None, T, D, V, ldx, ldw, stride, _TYPES[x.dtype], int(ignore_index), workspace, nbytes)
+          saved.data_ptr() if train else None, T, D, V, ldx, ldw, stride, _TYPES[x.dtype], ignored, workspace, nbytes)
     return out, saved
 
 
@@ -268,6 +276,7 @@ def linear_cross_entropy_backward(dloss, x, w, target, saved, ignore_index: int 
     """
     device, T, D, V, ldx, ldw, stride = _check_loss(x, w, target)
     types = (x.dtype,)
+    ignored = _ignored(ignore_index)
     sg = _strided("dloss", dloss, torch.float32, device, T)
     if not isinstance(saved, torch.Tensor) or saved.dtype != torch.float32 or tuple(saved.shape) != (T, 3) \
             or not saved.is_contiguous() or saved.get_device() != device:
@@ -288,5 +297,5 @@ def linear_cross_entropy_backward(dloss, x, w, target, saved, ignore_index: int 
     keep, workspace = _workspace(x, nbytes)
     _call("linear_cross_entropy", "linear_cross_entropy_backward", device, dloss.data_ptr(), px, pw, target.data_ptr(),
           saved.data_ptr(), dx.data_ptr(), dw.data_ptr(), T, D, V, sg, ldx, ldw, stride, lddx, lddw, _TYPES[x.dtype],
-          int(ignore_index), workspace, nbytes)
+          ignored, workspace, nbytes)
     return dx, dw

@@ -368,6 +368,11 @@ def test_refusals_on_gpu_tensors():
         fw.linear_cross_entropy(x, w[:0], target)
     with pytest.raises(TypeError):
         fw.linear_cross_entropy(x, w, target, out=loss.half())
+    for bad in (1 << 63, -(1 << 63) - 1):
+        with pytest.raises(ValueError, match="ignore_index"):
+            fw.linear_cross_entropy(x, w, target, ignore_index=bad)
+        with pytest.raises(ValueError, match="ignore_index"):
+            fw.linear_cross_entropy_backward(dloss, x, w, target, saved, ignore_index=bad)
     with pytest.raises(ValueError, match="saved"):
         fw.linear_cross_entropy_backward(dloss, x, w, target, saved[:3])
     with pytest.raises(ValueError, match="dloss"):
