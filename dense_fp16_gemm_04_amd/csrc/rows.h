@@ -136,7 +136,7 @@ __device__ __forceinline__ float columns_sum(const float* at, int64_t step, int 
 // 64 columns are whole cache lines, 16 four times the workgroups: where 64 are too
 // few for half the chip.  (1 row of 1024 columns from 1000 parts: 7.4 us by 64 and
 // 4.6 by 16; 8 of 2048 from 500 11.7 and 12.9.)
-inline bool wide_sums(int64_t columns, int64_t rows) { return columns * rows >= 32 * cus::kCus; }
+inline bool wide_sums(int64_t columns, int64_t rows) { return (columns + 63) / 64 * rows >= cus::kCus / 2; }
 
 // Bytes [first, last] of a matrix stay far from where 64 bits end.
 inline bool good_span(int64_t rows, int64_t cols, int64_t ld)
