@@ -60,7 +60,8 @@ def test_forward_and_gradients(shape, t):
 
 
 @pytest.mark.parametrize("t", ["fp16", "fp32"])
-@pytest.mark.parametrize("shape", [(20000, 64), (70000, 24), (9001, 200), (5000, 1000), (4100, 4096), (3000, 10000), (900, 40000)], ids=str)
+@pytest.mark.parametrize("shape", [(20000, 64), (70000, 24), (9001, 200), (5000, 1000), (4100, 4096), (3000, 10000), (900, 40000), (70000, 13),
+                                   (30000, 5), (9001, 201), (4100, 4095), (900, 16381)], ids=str)
 def test_many_rows(shape, t):
     """More rows than the workgroups take at once."""
     x, w, b, dy = inputs(*shape, plain.TYPES[t], torch.float32, seed=3)
