@@ -45,25 +45,28 @@ __device__ __forceinline__ f32x4 outputs(const E* X, const E* W, int64_t ldx, in
     // eight steps' loads in flight; in the last round, of steps that may reach past
     // K or not be there (zeros)
     constexpr int AHEAD = 8;
+    // The last eight of a K that is no multiple end with it.  What the eight before
+    // hold too is then zeros in both operands: zero times an infinity is NaN.
+    const int twice = D < 8 ? 0 : -D & 7, last = twice ? D & ~7 : -1;
+    u32x4 keep;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) keep[i] = twice <= 2 * i ? ~0u : twice == 2 * i + 1 ? 0xffff0000u : 0u;
     auto round = [&](int s, auto all) __attribute__((always_inline)) {
         constexpr bool ALL = decltype(all)::value;
-        // (the last eight of a K that is no multiple end with it: X's elements that
-        // the eight before hold too are zeros then)
         auto load8 = [&](const E* p, int k) __attribute__((always_inline)) {
             rows::Vec<E, 8> v = {};
             if (ALL || k < D) v = rows::load<E, 8>(p + (ALL || D < 8 ? k : min(k, D - 8)), ALL || D >= 8 ? 8 : D - k);
-            return __builtin_bit_cast(x8, v);
+            u32x4 words = __builtin_bit_cast(u32x4, v);
+            if constexpr (!ALL)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) words[i] &= k == last ? keep[i] : ~0u;
+            return __builtin_bit_cast(x8, words);
         };
         x8 fx[AHEAD], fw[AHEAD][B];
 #pragma unroll
         for (int a = 0; a < AHEAD; ++a) {
             const int k = (s + a * kWaves) * 32 + q * 8;
             fx[a] = load8(x, k);
-            if constexpr (!ALL) {
-                const int twice = D < 8 ? 0 : k + 8 - D;
-#pragma unroll
-                for (int e = 0; e < 8; ++e) fx[a][e] = e < twice ? (E)0.0f : fx[a][e];
-            }
 #pragma unroll
             for (int b = 0; b < B; ++b) fw[a][b] = load8(w[b], k);
         }

@@ -340,6 +340,31 @@ def test_special_values_stay_in_their_rows(shape):
     assert torch.allclose(l2, want, rtol=1e-5, atol=1e-5) and (dw2[V - 1] == 0).all()
 
 
+# up to 16 tokens (D with and without a last chunk that ends with it, in the first round
+# of loads and behind whole ones) and more
+@pytest.mark.parametrize("t", ["fp16", "bf16"])
+@pytest.mark.parametrize("shape", [(2, 7, 50), (3, 12, 70), (16, 33, 100), (5, 1033, 130), (8, 1033, 25000), (1, 1040, 66), (17, 33, 100),
+                                   (40, 1033, 130)], ids=str)
+def test_one_infinite_weight(shape, t):
+    """Minus infinity in each of the last sixteen columns of a row of w, which leaves that row no
+    probability: losses and gradients are those of the rows without it."""
+    T, D, V = shape
+    x, w, target, dloss = inputs(*shape, plain.TYPES[t], seed=24)
+    target = torch.where(target == V - 1, torch.zeros_like(target), target)
+    for c in range(max(0, D - 16), D):
+        pos, low = x.clone(), w.clone()
+        pos[:, c] = pos[:, c].abs() + 0.5
+        low[V - 1, c] = float("-inf")
+        loss, (dx, dw) = step(pos, low, target, dloss)
+        want, bound, parts = plain.loss(pos, w[:V - 1], target)
+        plain.assert_near(loss, want, bound, "loss, column %d" % c)
+        want, bounds = plain.loss_gradients(dloss, x.dtype, parts, rounded=T > 16)
+        rest = torch.arange(D, device=DEV) != c  # (column c of dx is 0 times the infinity)
+        plain.assert_near(dx[:, rest], want[0][:, rest], bounds[0][:, rest], "dx, column %d" % c)
+        plain.assert_near(dw[:V - 1], want[1], bounds[1], "dw, column %d" % c)
+        assert (dw[V - 1] == 0).all()
+
+
 @pytest.mark.parametrize("shape", [(0, 16, 8), (4, 0, 8), (0, 0, 5), (0, 16, 3000)], ids=str)
 def test_empty(shape):
     T, D, V = shape
