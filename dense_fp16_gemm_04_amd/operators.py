@@ -8,7 +8,8 @@ libraries' HIP kernels, a missing library raises ``RuntimeError`` and a
 refused call ``TypeError``, ``ValueError`` or ``GemmError``.  Nothing here
 takes part in autograd: a training step calls the backward function itself.
 A new result of inputs that require gradients raises when they are asked of it
-(results in ``out`` and those of the training pair are the caller's affair).
+(results in ``out`` and those of the training pair are the caller's affair), and
+an operand with a tangent of forward-mode differentiation is refused.
 
 Matrices may be views: the elements of a row are adjacent, rows may lie any
 distance apart that does not make them overlap.
@@ -20,6 +21,7 @@ import os
 import threading
 
 import torch
+from torch.autograd import forward_ad
 
 from .binding import GemmError, _stream
 
@@ -102,8 +104,16 @@ def load(name: str):
     return _libs[name]
 
 
+def _refuse_tangent(name, t):
+    """Refuse a dual tensor, whose tangent a call would leave out (asked only inside a dual level)."""
+    if isinstance(t, torch.Tensor) and forward_ad.unpack_dual(t).tangent is not None:
+        raise RuntimeError("%s has a tangent: this operator has no derivatives in forward mode" % name)
+
+
 def _pitch(name, t, types, device=None, shape=None):
     """The row pitch of t, a GPU matrix of one of `types` whose rows do not overlap."""
+    if forward_ad._current_level >= 0:
+        _refuse_tangent(name, t)
     # (what holds is found out first and told apart only where it does not:
     # these checks are half of a short call's time on the host)
     if isinstance(t, torch.Tensor) and t.dtype in types and t.dim() == 2:

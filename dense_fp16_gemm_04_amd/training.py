@@ -8,15 +8,19 @@ the C ABIs of ``include/layer_norm.h``, ``include/dropout.h`` and
 memory and the current stream, a missing library raises ``RuntimeError`` and a
 refused call ``TypeError``, ``ValueError`` or ``GemmError``, matrices may be
 views whose rows' elements are adjacent, and nothing takes part in autograd: a
-training step calls the backward functions itself, and a new result of inputs
-that require gradients raises when they are asked of it.
+training step calls the backward functions itself.  A new result raises when
+gradients are asked of it that it has none for: those of the inputs of
+``layer_norm``, ``dropout`` and ``linear_cross_entropy``, and those of a backward
+function's dy or dloss (a second derivative).  An operand with a tangent of
+forward-mode differentiation is refused.
 """
 from __future__ import annotations
 
 import torch
+from torch.autograd import forward_ad
 
 from .binding import GemmError
-from .operators import _TYPES, _TYPES_AND_F32, _call, _pitch, _without_gradients, _workspace, load
+from .operators import _TYPES, _TYPES_AND_F32, _call, _pitch, _refuse_tangent, _without_gradients, _workspace, load
 
 _WORDS = 1 << 64
 
@@ -28,6 +32,8 @@ def _new(x, pitch):
 
 def _vector(name, t, types, device, size):
     """Check t, `size` adjacent elements of one of `types` on `device`."""
+    if forward_ad._current_level >= 0:
+        _refuse_tangent(name, t)
     # (what holds is found out first and told apart only where it does not)
     if isinstance(t, torch.Tensor) and t.dtype in types and t.shape == (size,) and t.get_device() == device and t.is_contiguous():
         return
@@ -135,6 +141,9 @@ def layer_norm_backward(dy, x, weight, bias, saved, out=None):
     _call("layer_norm", "layer_norm_backward", device, dy.data_ptr(), x.data_ptr(), None if weight is None else weight.data_ptr(),
           saved.data_ptr(), dx.data_ptr(), None if dw is None else dw.data_ptr(), None if db is None else db.data_ptr(), rows, cols,
           lddy, ldx, lddx, _TYPES_AND_F32[x.dtype], _TYPES_AND_F32[params], workspace, nbytes)
+    if out is None and dy.requires_grad:
+        return tuple(None if t is None else _without_gradients(t, "layer_norm_backward has no gradients in autograd", dy)
+                     for t in (dx, dw, db))
     return dx, dw, db
 
 
@@ -186,13 +195,18 @@ def dropout(x, p: float, seed, offset: int = 0, residual=None, out=None):
 
 def dropout_backward(dy, p: float, seed, offset: int = 0, out=None):
     """x's gradient for the gradient dy of ``dropout``'s result with the same p, seed and offset; ``out`` may be dy."""
-    return _dropout(dy, p, seed, offset, None, out)
+    dx = _dropout(dy, p, seed, offset, None, out)
+    if out is None and dy.requires_grad:
+        return _without_gradients(dx, "dropout_backward has no gradients in autograd", dy)
+    return dx
 
 
 # ------------------------------------------------- linear_cross_entropy --
 
 def _strided(name, t, dtype, device, size):
     """The stride of t, `size` elements of `dtype` on `device`, any distance apart."""
+    if forward_ad._current_level >= 0:
+        _refuse_tangent(name, t)
     if not isinstance(t, torch.Tensor):
         raise TypeError("%s must be a torch tensor" % name)
     if t.dtype != dtype:
@@ -298,4 +312,6 @@ def linear_cross_entropy_backward(dloss, x, w, target, saved, ignore_index: int 
     _call("linear_cross_entropy", "linear_cross_entropy_backward", device, dloss.data_ptr(), px, pw, target.data_ptr(),
           saved.data_ptr(), dx.data_ptr(), dw.data_ptr(), T, D, V, sg, ldx, ldw, stride, lddx, lddw, _TYPES[x.dtype],
           ignored, workspace, nbytes)
+    if out is None and dloss.requires_grad:
+        return tuple(_without_gradients(t, "linear_cross_entropy_backward has no gradients in autograd", dloss) for t in (dx, dw))
     return dx, dw

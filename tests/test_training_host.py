@@ -9,10 +9,11 @@ import re
 
 import pytest
 import torch
+from torch.autograd import forward_ad
 
 import _training as plain
 import dense_fp16_gemm_04_amd as fw
-from dense_fp16_gemm_04_amd import build, operators
+from dense_fp16_gemm_04_amd import build, operators, training
 
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 INVALID = 1  # hipErrorInvalidValue
@@ -155,6 +156,29 @@ def test_bindings_refuse_host_tensors_and_wrong_types():
     for call in (lambda: fw.layer_norm(x.double()), lambda: fw.layer_norm([1.0]), lambda: fw.dropout(x.long(), 0.1, 1)):
         with pytest.raises(TypeError):
             call()
+
+
+def test_tangents_are_refused():
+    """A dual tensor of forward-mode differentiation, whose tangent a call would lose."""
+    x, v, w = torch.zeros(4, 16), torch.ones(16), torch.zeros(8, 16)
+    target, saved = torch.zeros(4, dtype=torch.int64), torch.zeros(4, 3)
+    with forward_ad.dual_level():
+        dual = [forward_ad.make_dual(t, torch.ones_like(t)) for t in (x, v, x.half())]
+        for call in (lambda: fw.layer_norm(dual[0]), lambda: fw.layer_norm_train(dual[0], v, v), lambda: fw.dropout(dual[0], 0.1, 1),
+                     lambda: fw.layer_norm_backward(x, dual[0], None, None, saved[:, :2]), lambda: fw.dropout_backward(dual[0], 0.1, 1),
+                     lambda: fw.linear_cross_entropy(dual[2], w.half(), target), lambda: fw.linear_cross_entropy_train(dual[2], w.half(), target),
+                     lambda: fw.linear_cross_entropy_backward(saved[:, 0], dual[2], w.half(), target, saved),
+                     lambda: training._vector("weight", dual[1], (torch.float32,), -1, 16),
+                     lambda: training._strided("dloss", dual[1], torch.float32, -1, 16),
+                     lambda: fw.gated_nt(dual[2], w.half(), w.half()), lambda: fw.orthogonalize_ns(dual[0])):
+            with pytest.raises(RuntimeError, match="tangent"):
+                call()
+        # others are looked at as ever
+        training._vector("weight", v, (torch.float32,), -1, 16)
+        with pytest.raises(ValueError, match="GPU"):
+            fw.layer_norm(x)
+        with pytest.raises(TypeError):
+            fw.layer_norm([1.0])
 
 
 # ------------------------------------------------- the plain forms here --

@@ -7,6 +7,7 @@ import os
 
 import pytest
 import torch
+from torch.autograd import forward_ad
 
 import _training as plain
 import dense_fp16_gemm_04_amd as fw
@@ -226,3 +227,40 @@ def test_inputs_that_require_gradients():
     # the training forms give their gradients themselves
     got = many(x, w, b, dy.detach(), xl, wl, target, g)
     assert all(torch.equal(a, c) and not a.requires_grad for a, c in zip(got, want))
+
+
+def test_derivatives_that_a_call_does_not_have():
+    """Tangents are refused; a second derivative raises when it is asked for."""
+    x, w, b, dy, xl, wl, target, g = many_inputs(20, 64, 30, 64, 100, seed=180)
+    want = many(x, w, b, dy, xl, wl, target, g)
+    y, saved = fw.layer_norm_train(x, w, b)
+    _, l_saved = fw.linear_cross_entropy_train(xl, wl, target)
+    with forward_ad.dual_level():
+        assert all(torch.equal(a, c) for a, c in zip(want, many(x, w, b, dy, xl, wl, target, g)))
+        wd, xd, dd, gd = (forward_ad.make_dual(v, torch.ones_like(v)) for v in (w, xl, dy, g))
+        for call in (lambda: fw.layer_norm(x, wd, b), lambda: fw.layer_norm_train(x, w, wd), lambda: fw.dropout(x, 0.5, 3, residual=dd),
+                     lambda: fw.layer_norm_backward(dd, x, w, b, saved), lambda: fw.dropout_backward(dd, 0.5, 3),
+                     lambda: fw.layer_norm(x, w, b, out=dd),
+                     lambda: fw.linear_cross_entropy(xd, wl, target), lambda: fw.linear_cross_entropy_train(xl, wl, target, out=gd),
+                     lambda: fw.linear_cross_entropy_backward(gd, xl, wl, target, l_saved)):
+            with pytest.raises(RuntimeError, match="tangent"):
+                call()
+        assert all(torch.equal(a, c) for a, c in zip(want, many(x, w, b, dy, xl, wl, target, g)))
+    plain_grads = [*fw.layer_norm_backward(dy, x, w, b, saved), fw.dropout_backward(dy, 0.5, 3),
+                   *fw.linear_cross_entropy_backward(g, xl, wl, target, l_saved)]
+    for v in (dy, g):
+        v.requires_grad_()
+    grads = [*fw.layer_norm_backward(dy, x, w, b, saved), fw.dropout_backward(dy, 0.5, 3),
+             *fw.linear_cross_entropy_backward(g, xl, wl, target, l_saved)]
+    for a, c in zip(grads, plain_grads):
+        assert torch.equal(a, c)
+        with pytest.raises(RuntimeError, match="_backward has no gradients"):
+            a.float().sum().backward()
+    out = [torch.zeros_like(c) for c in plain_grads]
+    fw.layer_norm_backward(dy, x, w, b, saved, out=out[:3])
+    fw.dropout_backward(dy, 0.5, 3, out=out[3])
+    fw.linear_cross_entropy_backward(g, xl, wl, target, l_saved, out=out[4:])
+    with torch.no_grad():
+        grads = [*fw.layer_norm_backward(dy, x, w, b, saved), fw.dropout_backward(dy, 0.5, 3),
+                 *fw.linear_cross_entropy_backward(g, xl, wl, target, l_saved)]
+    assert all(torch.equal(a, c) and not a.requires_grad for a, c in zip(grads + out, 2 * plain_grads))
