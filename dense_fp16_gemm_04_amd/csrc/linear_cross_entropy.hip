@@ -708,7 +708,8 @@ int64_t first_of_two(int64_t other, int64_t n, int64_t K, bool partial)
 // where W is copied anyway).  (Steps with it and without: 17 x 4096 x 20000 256 us and
 // 163, 200 x 1024 x 32000 127 and 108, 1000 x 1032 x 32001 394 and 340, 2048 x 2048 x
 // 32000 975 and 909, 8192 x 1024 x 50000 3410 and 3290; 8192 x 4096 x 32768, in 256 x 256
-// tiles, 6000 and 6330.)
+// tiles, 6000 and 6330.)  Which of the two a workspace has to hold too, and so by an
+// MI355X's CUs, whatever device is current.
 template <class E>
 bool turned_for(int64_t T, int64_t n, int64_t D, bool copied)
 {
@@ -716,7 +717,7 @@ bool turned_for(int64_t T, int64_t n, int64_t D, bool copied)
     const int64_t K = abi::up(n, 8);
     const bool split = K >= kSplitK;
     const double transpose = 2.0 * n * D * (copied ? 1 : 2) / 4.9e6;
-    return choose<AddOp<E, true>>(K, split, tiles).us < choose<AddOp<E, false>>(K, split, tiles).us + transpose;
+    return choose<AddOp<E, true>>(K, split, tiles, cus::kCus).us < choose<AddOp<E, false>>(K, split, tiles, cus::kCus).us + transpose;
 }
 
 // The parts of up to this many outputs may be of 32 columns, of more 64 at least
@@ -855,7 +856,7 @@ struct Shares {
 template <class E>
 struct BackwardSpace {
     E *x = nullptr, *w = nullptr;  // null: read in place
-    E *xt, *wt, *dl, *dlt;
+    E *xt, *wt = nullptr, *dl, *dlt;
     RowInfo* info;
     int* column;
     float *back, *sums, *factor, *partial;
@@ -875,9 +876,13 @@ struct BackwardSpace {
         Vp = abi::up(piece, kLine);
         rows = abi::up(T, 256);
         if (!in_place(X, T, D, V, ldx)) x = c.take<E>(T * ld);
-        if (!in_place(W, D, ldw)) w = c.take<E>(piece * ld);
+        const bool products = T > 0 && D > 0, copied = products && !in_place(W, D, ldw);  // W is read, copied first
+        if (copied) w = c.take<E>(piece * ld);
         xt = c.take<E>(D * Tp);
-        wt = c.take<E>(D * Vp);
+        // (the last piece's rows of W may be fewer, and read the other way)
+        const int64_t last = V - (V - 1) / piece * piece;
+        if (products && !(turned_for<E>(T, piece, D, copied) && (last == piece || turned_for<E>(T, last, D, copied))))
+            wt = c.take<E>(D * Vp);
         dl = c.take<E>(T * Vp);
         dlt = c.take<E>(piece * Tp);
         info = c.take<RowInfo>(rows);
@@ -885,7 +890,7 @@ struct BackwardSpace {
         back = c.take<float>(rows);
         sums = piece < V ? c.take<float>((T + 15) / 16 * ((D + 15) / 16) * kBlockFloats) : nullptr;
         factor = c.take<float>(1);
-        partial = c.take<float>(kSplitFloats);
+        partial = T ? c.take<float>(kSplitFloats) : nullptr;
         bytes = c.used();
     }
 };

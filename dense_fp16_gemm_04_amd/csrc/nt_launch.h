@@ -84,9 +84,8 @@ struct Choice {
     double us = 0;
 };
 template <class OP, class Count>
-Choice choose(int64_t K, bool partial, Count count)
+Choice choose(int64_t K, bool partial, Count count, int cus = num_cus())
 {
-    const int cus = num_cus();
     Choice best;
     for (int i = 0; i < kNumKinds; ++i) {
         if ((i == 0 && (!OP::kPersist || K <= 128)) || (i == 3 && Turned<OP>::value)) continue;

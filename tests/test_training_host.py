@@ -289,6 +289,19 @@ def test_loss_empty_and_workspace():
     assert lib.linear_cross_entropy_backward_workspace(A, B, T, D, V, D, D) < T * V
 
 
+@pytest.mark.parametrize("T", [0, 17, 64, 1000, 4096])
+@pytest.mark.parametrize("D", [1032, 4096])
+def test_loss_backward_workspace_holds_what_is_read(T, D):
+    """Both images of dl and X transposed; W, which is read as it lies at these sizes, neither copied
+    nor transposed (1 GB at 4096 x 131072); the parts of split sums, 32 MB."""
+    V = 131072
+    need = operators.load("linear_cross_entropy").linear_cross_entropy_backward_workspace(A, B, T, D, V, D, D)
+    rows = (T + 63) // 64 * 64
+    images = 2 * 2 * max(min(rows * V, 1 << 27), 1024 * rows) * 1.1  # (pieces are whole tiles)
+    x = 2 * 2 * rows * (D + 64) + 4 * rows * (D + 64)  # whole lines, transposed; dX's sums
+    assert need <= images + x + (36 << 20 if T else 4096)
+
+
 def test_loss_bindings_refuse_host_tensors():
     x, w = torch.zeros(4, 16, dtype=torch.float16), torch.zeros(8, 16, dtype=torch.float16)
     target = torch.zeros(4, dtype=torch.int64)

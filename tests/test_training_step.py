@@ -11,7 +11,7 @@ from torch.autograd import forward_ad
 
 import _training as plain
 import dense_fp16_gemm_04_amd as fw
-from dense_fp16_gemm_04_amd import build, operators
+from dense_fp16_gemm_04_amd import build, operators, training
 from test_operators import normal
 
 pytestmark = pytest.mark.gpu
@@ -180,6 +180,26 @@ def test_large_calls_on_streams_and_in_graphs():
             torch.cuda.synchronize()
             kept = [o.clone() for o in out]
             assert all(torch.equal(a, b) for a, b in zip(kept, many(*args)))
+
+
+@pytest.mark.parametrize("shape", [(300, 40000, 4101, 200, 4093), (9000, 24, 300, 8200, 1001), (500, 2731, 1, 64, 9000), (3, 8, 17, 4096, 20001),
+                                   (3, 8, 200, 333, 30001), (3, 8, 4101, 1080, 4093), (3, 8, 9000, 136, 33001), (3, 8, 0, 16, 300),
+                                   (0, 24, 40, 776, 2 ** 20 + 5003)], ids=str)
+def test_nothing_is_written_past_a_workspace(shape, monkeypatch):
+    args = many_inputs(*shape, seed=190)
+    want = many(*args)
+    given = []
+
+    def framed(like, nbytes):
+        given.append(torch.full((max(nbytes, 0) + 8192,), 0x5A, dtype=torch.uint8, device=like.device))
+        return given[-1], given[-1].data_ptr() + 4096 if nbytes > 0 else None
+
+    monkeypatch.setattr(training, "_workspace", framed)
+    got = many(*args)
+    assert all(torch.equal(a, b) for a, b in zip(want, got))
+    assert len(given) == 3
+    for w in given:
+        assert (w[:4096] == 0x5A).all() and (w[-4096:] == 0x5A).all()
 
 
 def test_on_another_current_device(monkeypatch):
