@@ -476,7 +476,9 @@ int64_t back_groups(int64_t rows, int64_t cols, int32_t type)
 {
     const Way w = way_of(chunks_of(cols, type));
     constexpr int cus = cus::kCus;
-    if (w.g == 0) return sharers(rows, 1, 64);
+    // (of rows of any length the sums are 256 MB at most; 2^19 columns, where this
+    // begins, are 256 workgroups to a share)
+    if (w.g == 0) return sharers(rows, 1, std::min<int64_t>(64, ((int64_t)1 << 25) / cols));
     // Each workgroup's sums cross memory twice, and fewer workgroups hide less: steps with
     // 1, 2 and 3 for each CU take, of 500 x 16384 in bfloat16 (whose lanes hold more) 38, 50
     // and 50 us, of 1000 x 2048 (four rows to a workgroup, or two) 22.5, 24.5 and 28.4, and

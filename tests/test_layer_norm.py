@@ -69,6 +69,14 @@ def test_many_rows(shape, t):
     check(x, w, b, dy, y, saved, fw.layer_norm_backward(dy, x, w, b, saved))
 
 
+@pytest.mark.parametrize("shape", [(70, 600001), (5, 2 ** 22 + 4)], ids=str)
+def test_columns_with_fewer_shares(shape):
+    """Rows so long that fewer workgroups share them."""
+    x, w, b, dy = inputs(*shape, torch.bfloat16, torch.float32, seed=4)
+    y, saved = fw.layer_norm_train(x, w, b)
+    check(x, w, b, dy, y, saved, fw.layer_norm_backward(dy, x, w, b, saved))
+
+
 @pytest.mark.parametrize("cols", [40, 1000, 70000])
 def test_without_parameters(cols):
     x, w, b, dy = inputs(30, cols, torch.bfloat16, torch.bfloat16)

@@ -99,6 +99,12 @@ def test_layer_norm_empty_and_workspace():
     assert lib.layer_norm_backward_workspace(4, 16) > 0
 
 
+@pytest.mark.parametrize("cols", [20000, 1 << 19, (1 << 19) + 1, 1 << 22, 1 << 24])
+def test_layer_norm_backward_workspace_of_wide_rows(cols):
+    """Sums of columns of 256 MB at most (64 shares of 2^24 columns would be 8.6 GB beside rows of 2), two means a row."""
+    assert 0 < operators.load("layer_norm").layer_norm_backward_workspace(64, cols) <= (1 << 28) + (1 << 14)
+
+
 # -------------------------------------------------------------- dropout --
 
 def dropout_args(**kw):
