@@ -171,9 +171,9 @@ _entries = {}
 
 def _call(library, name, device, *args):
     """Call an entry point on `device` and its current stream (the last argument)."""
-    fn = _entries.get(name)
+    fn = _entries.get((library, name))
     if fn is None:
-        fn = _entries[name] = getattr(load(library), name)
+        fn = _entries[library, name] = getattr(load(library), name)
     if device == torch.cuda.current_device():
         rc = fn(*args, _stream(device))
     else:

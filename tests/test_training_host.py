@@ -164,6 +164,22 @@ def test_bindings_refuse_host_tensors_and_wrong_types():
             call()
 
 
+def test_entry_points_are_kept_by_library(monkeypatch):
+    """Two libraries that export one name: each call reaches its own."""
+    class Library:
+        def __init__(self, code):
+            self.entry = lambda *args: code
+
+    libraries = {"first": Library(0), "second": Library(7)}
+    monkeypatch.setattr(operators, "load", libraries.__getitem__)
+    monkeypatch.setattr(operators, "_stream", lambda device: None)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    for _ in range(2):
+        operators._call("first", "entry", 0)
+        with pytest.raises(fw.GemmError):
+            operators._call("second", "entry", 0)
+
+
 def test_tangents_are_refused():
     """A dual tensor of forward-mode differentiation, whose tangent a call would lose."""
     x, v, w = torch.zeros(4, 16), torch.ones(16), torch.zeros(8, 16)
