@@ -206,6 +206,29 @@ def test_past_32_bits():
     plain.assert_within(fw.layer_norm(tall), want, bound)
 
 
+@pytest.mark.parametrize("shape", [(70000, 32768), (180000, 12000)], ids=str)
+def test_sums_of_columns_past_32_bits(shape):
+    """dweight and dbias of more than 2^31 elements, column by column: rows of any length, and held in registers."""
+    rows, cols = shape
+    x, w, b, dy = (torch.empty(*s, dtype=t, device=DEV).normal_(generator=torch.Generator(DEV).manual_seed(i)) for i, (s, t) in enumerate(
+        ((shape, torch.float16), ((cols,), torch.float32), ((cols,), torch.float32), (shape, torch.float16))))
+    _, saved = fw.layer_norm_train(x, w, b)
+    _, dw, db = fw.layer_norm_backward(dy, x, w, b, saved)
+    at = torch.tensor([0, 1, 7, 8, 2047, 2048, 4095, 8191, cols // 2 + 3, cols - 9, cols - 1], device=DEV)
+    h, off = [], []
+    for i in range(0, rows, 1000):
+        parts = plain._norm_parts(x[i:i + 1000].double(), 1e-5)
+        h.append(parts[0][:, at])
+        off.append(parts[2][:, at])
+    h, off, d = torch.cat(h), torch.cat(off), dy[:, at].double()
+    # (the sums' additions as in plain.norm_gradients)
+    adds = rows // 64 + 1 + 32 + 32 + 16 + 2
+    want, bound = (d * h).sum(0), adds * plain.EPS * (d * h).abs().sum(0) + (d.abs() * off).sum(0)
+    plain.assert_near(dw[at], want, bound + plain.rounded(want, torch.float32), "dweight")
+    want, bound = d.sum(0), adds * plain.EPS * d.abs().sum(0)
+    plain.assert_near(db[at], want, bound + plain.rounded(want, torch.float32), "dbias")
+
+
 def test_refusals_on_gpu_tensors():
     x, w, b, dy = inputs(4, 16, torch.float16, torch.float16)
     y, saved = fw.layer_norm_train(x, w, b)

@@ -374,6 +374,64 @@ def test_empty(shape):
     assert ((loss - math.log(V)).abs() < 1e-6).all()
 
 
+@pytest.mark.parametrize("t", ["fp16", "bf16"])
+@pytest.mark.parametrize("shape", [(17, 0, 8), (300, 0, 513), (5000, 0, 40)], ids=str)
+def test_no_columns(shape, t):
+    """D of 0 above 16 tokens: every output is zero."""
+    T, D, V = shape
+    x, w, target, dloss = inputs(*shape, plain.TYPES[t])
+    loss, saved = fw.linear_cross_entropy_train(x, w, target)
+    dx, dw = fw.linear_cross_entropy_backward(dloss, x, w, target, saved)
+    valid = target != -100
+    assert ((loss - math.log(V))[valid].abs() < 1e-6 * math.log(V)).all() and (loss[~valid] == 0).all()
+    assert dx.shape == (T, 0) and dw.shape == (V, 0)
+    assert torch.equal(saved[valid], torch.tensor([0.0, V, 0.0], device=DEV).expand(int(valid.sum()), 3))
+
+
+def some_rows_of_dw(x, w, target, dloss, rows, chunk):
+    """(dw[rows], bound) by plain.loss_gradients, the tokens `chunk` at a time."""
+    kept = []
+    for i in range(0, len(x), chunk):
+        part = slice(i, i + chunk)
+        xc, w64, valid, at, p, l, top, s, s_rel, l_off = plain.loss(x[part], w, target[part])[2]
+        here = at == rows
+        # (a column more, for the targets that are not among `rows`)
+        at = torch.where(here.any(1, keepdim=True), here.int().argmax(1, keepdim=True), torch.full_like(at, len(rows)))
+        wide = [torch.cat([v[:, rows], torch.zeros_like(v[:, :1])], 1) for v in (p, l, l_off)]
+        kept.append((xc, valid, at, wide[0], wide[1], top, s, s_rel, wide[2]))
+    xc, valid, at, p, l, top, s, s_rel, l_off = (torch.cat(v) for v in zip(*kept))
+    w64 = torch.cat([w[rows], w[:1]]).double()
+    want, bounds = plain.loss_gradients(dloss, x.dtype, (xc, w64, valid, at, p, l, top, s, s_rel, l_off), rounded=len(x) > 16)
+    return want[1][:-1], bounds[1][:-1]
+
+
+@pytest.mark.parametrize("t", ["fp16", "bf16"])
+@pytest.mark.parametrize("shape, piece", [((40000, 16, 110000), 3584), ((9000, 136, 33001), 11008)], ids=str)
+def test_rows_of_dw_in_pieces_of_the_vocabulary(shape, piece, t):
+    """Outputs past 32 bits and pieces of the vocabulary: dw on both sides of pieces' ends, of targets and of both ends."""
+    T, D, V = shape
+    x, w, target, dloss = inputs(*shape, plain.TYPES[t], seed=25)
+    target[-1], target[0] = V - 1, 0
+    _, (_, dw) = step(x, w, target, dloss)
+    ends = [v for e in range(piece, V, piece) for v in (e - 1, e)]
+    rows = torch.tensor(sorted({0, 1, V - 2, V - 1, *ends, *target[target >= 0][:20].tolist()}), device=DEV)
+    want, bound = some_rows_of_dw(x, w, target, dloss, rows, 2000)
+    plain.assert_near(dw[rows], want, bound, "dw")
+
+
+@pytest.mark.parametrize("shape", [(2100, 136, 2100), (2100, 133, 2100), (9, 136, 2100)], ids=str)
+def test_gradients_that_lie_far_apart(shape):
+    """dx and dw whose last rows lie past 2^32 bytes."""
+    T, D, V = shape
+    x, w, target, dloss = inputs(*shape, torch.bfloat16, seed=26)
+    _, saved = fw.linear_cross_entropy_train(x, w, target)
+    want = fw.linear_cross_entropy_backward(dloss, x, w, target, saved)
+    far = [torch.full((n, 1 << 20), 7.0, dtype=x.dtype, device=DEV) for n in (T, V)]
+    got = fw.linear_cross_entropy_backward(dloss, x, w, target, saved, out=[f[:, 8:8 + D] for f in far])
+    for g, f, v in zip(got, far, want):
+        assert torch.equal(g, v) and (f[:, :8] == 7).all() and (f[:, 8 + D:] == 7).all()
+
+
 def test_refusals_on_gpu_tensors():
     x, w, target, dloss = inputs(4, 16, 8, torch.float16)
     loss, saved = fw.linear_cross_entropy_train(x, w, target)
