@@ -762,6 +762,9 @@ struct ForwardSpace {
     }
 };
 
+// Rows to a workgroup: 8, or from 2048 on 32, whose parts lie in two whole cache lines,
+// not in half of one.  (The loss of D 64 by 131072 words: 1000 tokens 94.7 us with 8 and 98.6
+// with 32, 1500 136 and 137, 2048 178 and 176, 6000 506 and 492; 8192 by 50000 273 and 264.)
 int join(const Join& j, hipStream_t stream)
 {
     auto with = [&](auto kernel, int64_t rows) {
@@ -769,7 +772,7 @@ int join(const Join& j, hipStream_t stream)
         return (int)hipGetLastError();
     };
     if (j.M <= few::kTokens) return with(lse_join<1>, 1);
-    return j.M <= 8 * 2048 ? with(lse_join<8>, 8) : with(lse_join<32>, 32);
+    return j.M < 2048 ? with(lse_join<8>, 8) : with(lse_join<32>, 32);
 }
 
 template <class E>
@@ -830,7 +833,8 @@ int forward(const E* X, const E* W, const int64_t* target, float* loss, float* s
 }
 
 // Columns of the vocabulary to a piece: dl of 2^27 elements, 256 MB, twice, in
-// rows of 2^20 at most (a pitch is below 2^21); the pieces alike, of whole tiles.
+// rows of 2^20 at most (a pitch is below 2^21) and 1024 at least, for which more than
+// 131072 tokens take more; the pieces alike, of whole tiles.
 int64_t piece_of(int64_t T, int64_t V)
 {
     const int64_t most = std::min<int64_t>(std::max<int64_t>(((int64_t)1 << 27) / std::max<int64_t>(T, 1), 1024), 1 << 20);
