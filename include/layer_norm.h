@@ -63,7 +63,8 @@ int layer_norm_backward(const void* dY, const void* X, const void* weight, const
                         void* dbias, int64_t rows, int64_t cols, int64_t lddy, int64_t ldx, int64_t lddx, int32_t type,
                         int32_t param_type, void* workspace, int64_t workspace_bytes, hipStream_t stream);
 
-/* Bytes of the backward call's workspace; -1 for invalid sizes.  Host-only. */
+/* Bytes of the backward call's workspace (sums of the columns, 256 MB at most, and 8 bytes
+ * to a row of more than 8192 elements); -1 for invalid sizes.  Host-only. */
 int64_t layer_norm_backward_workspace(int64_t rows, int64_t cols);
 
 /* LAYER_NORM_VERSION of the built library. */

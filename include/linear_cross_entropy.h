@@ -27,11 +27,14 @@
  * with sums in 32 bits.  It reads what the forward pass kept in `saved` ([T, 3]
  * binary32: the largest l, the sum, the target's l) and computes l again, a piece
  * of the vocabulary at a time.  dl is rounded once to the type for dX, and once,
- * times dloss over dloss' largest finite magnitude, for dW, as operands of matrix
- * products have to be; for dX what rounding takes from the target's dl is put
+ * times dloss over dloss' largest finite magnitude, for dW, to be the operand of
+ * one matrix product each; for dX what rounding takes from the target's dl is put
  * back.  This adds at most about as much to a gradient's error as its own
- * rounding (sqrt 2 of it in all).  In binary16 both are held times 2^15:
- * probabilities down to 2^-29 keep all bits, and dloss may have any size.
+ * rounding (sqrt 2 of it in all: 2.4e-4 off for 1000 x 1032 x 32001 in binary16, 2.1e-4
+ * with dl in 32 bits; 1.8e-3 and 1.7e-3 for 8192 x 4096 x 131072 in bfloat16).  A high
+ * and a low part of dl would keep its bits for both products a second time, about 47%
+ * of that large step.  In binary16 both are held times 2^15: probabilities down to
+ * 2^-29 keep all bits, and dloss may have any size.
  *
  * Ownership, concurrency, errors and capture are those of gemm_nt_f16.h: the
  * caller owns every buffer, calls enqueue on `stream` and return a hipError_t
@@ -84,7 +87,15 @@ int linear_cross_entropy_backward(const float* dloss, const void* X, const void*
                                   int64_t lddw, int32_t type, int64_t ignore_index, void* workspace,
                                   int64_t workspace_bytes, hipStream_t stream);
 
-/* Bytes of the calls' workspaces for these operands; -1 for invalid sizes.  Host-only. */
+/* Bytes of the calls' workspaces for these operands; -1 for invalid sizes.  Host-only.
+ *
+ * Above 16 tokens, forward: 8 bytes for each token and 32 words (64, of more than 2^26
+ * outputs), what is copied of X and W, and 32 MB from D 505 on.  Backward: dl of a piece of the vocabulary
+ * twice, each of 2^27 elements of 2 bytes or 1024 to a token, whichever is more; X
+ * transposed, what is copied of X and of a piece of W, a transpose of the piece where
+ * the products run faster on one (some thousand tokens of long rows), 4 D bytes to a
+ * token where there are several pieces, and 32 MB.  (1000 x 4096 x 131072: 48 MB and
+ * 546 MB.) */
 int64_t linear_cross_entropy_workspace(const void* X, const void* W, int64_t T, int64_t D, int64_t V, int64_t ldx,
                                        int64_t ldw);
 int64_t linear_cross_entropy_backward_workspace(const void* X, const void* W, int64_t T, int64_t D, int64_t V,
