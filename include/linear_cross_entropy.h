@@ -90,12 +90,12 @@ int linear_cross_entropy_backward(const float* dloss, const void* X, const void*
 /* Bytes of the calls' workspaces for these operands; -1 for invalid sizes.  Host-only.
  *
  * Above 16 tokens, forward: 8 bytes for each token and 32 words (64, of more than 2^26
- * outputs), what is copied of X and W, and 32 MB from D 505 on.  Backward: dl of a piece of the vocabulary
- * twice, each of 2^27 elements of 2 bytes or 1024 to a token, whichever is more; X
- * transposed, what is copied of X and of a piece of W, a transpose of the piece where
- * the products run faster on one (some thousand tokens of long rows), 4 D bytes to a
- * token where there are several pieces, and 32 MB.  (1000 x 4096 x 131072: 48 MB and
- * 546 MB.) */
+ * outputs), what is copied of X and W, and 32 MB from D 505 on.  Backward: dl of a piece
+ * of the vocabulary twice, each of up to 2^27 elements of 2 bytes, or 1024 to a token if
+ * that is more; X transposed, what is copied of X and of a piece of W, a transpose of the
+ * piece where the products run faster on one (some thousand tokens of long rows), 4 D
+ * bytes to a token where there are several pieces, and 32 MB.  (1000 x 4096 x 131072:
+ * 48 MB and 546 MB.) */
 int64_t linear_cross_entropy_workspace(const void* X, const void* W, int64_t T, int64_t D, int64_t V, int64_t ldx,
                                        int64_t ldw);
 int64_t linear_cross_entropy_backward_workspace(const void* X, const void* W, int64_t T, int64_t D, int64_t V,
